@@ -377,6 +377,45 @@ int tw_gemm_i8(const int8_t *At, const int8_t *vals, const int32_t *offset_k,
  * variant of the tile-wise slides.  M % 8 == 0, K % 8 == 0. */
 int ssg_transpose_f16(const void *A, void *At, int64_t M, int64_t K, void *stream);
 
+/* ---- Tuning and serving pruned layers --------------------------------
+ * A packed 2:4 or tile-wise weight is fixed; what is trained after pruning
+ * (GPUSQ-ViT and the tile-wise slides both fine-tune the pruned model) is what
+ * sits beside it: the norms, low-rank adapters next to the projection, and the
+ * loss that drives them.  Rows (x, y and their gradients) are row-major with a
+ * row stride ld* in elements; device buffers, caller-owned, asynchronous on
+ * `stream`. */
+
+/* Element types of the calls below. */
+enum { SSG_DT_F16 = 0, SSG_DT_BF16 = 1, SSG_DT_F32 = 2 };
+
+/* Layer norm over the last axis of x [M][N] (M >= 0, N >= 1; any width, row
+ * stride and element-aligned address):
+ *   s = x, or x + residual rounded to the rows' type (then stored to sum, the
+ *       residual stream of the block; residual and sum are both given or NULL)
+ *   y = (s - mean) * rstd * weight + bias
+ * with mean and 1 / sqrt(variance + eps) in fp32 over s, stored to mean and
+ * rstd [M] unless both are NULL.  weight and bias [N] are of type wtype
+ * (dtype or SSG_DT_F32), either may be NULL (ones / zeros).  y may be x or
+ * residual, sum may be x or residual (not the same one as y). */
+int layer_norm_forward(int32_t dtype, const void *x, int64_t ldx, const void *residual, int64_t ldr,
+                       const void *weight, const void *bias, int32_t wtype, float eps, void *y, int64_t ldy,
+                       void *sum, int64_t lds, float *mean, float *rstd, int64_t M, int64_t N, void *stream);
+
+/* Backward pass of layer_norm_forward: x is the normalised input (the sum, if
+ * there was a residual), mean and rstd its saved statistics.  dx [M][N] gets
+ * the input's gradient, plus dres when that is given (the gradient arriving on
+ * the residual stream; dx may be dres, but not dy or x).  dweight and dbias,
+ * both or neither: fp32 [N], the sums over all rows of dy * xhat and of dy
+ * (zeros when M = 0), summed through the workspace in a fixed order. */
+int layer_norm_backward(int32_t dtype, const void *dy, int64_t lddy, const void *x, int64_t ldx, const float *mean,
+                        const float *rstd, const void *weight, int32_t wtype, const void *dres, int64_t ldres,
+                        void *dx, int64_t lddx, float *dweight, float *dbias, int64_t M, int64_t N, void *ws,
+                        int64_t ws_bytes, void *stream);
+
+/* Device bytes layer_norm_backward needs when dweight and dbias are asked for
+ * (0 for M <= 0 or arguments it would refuse); ws 16-byte aligned. */
+int64_t layer_norm_workspace_bytes(int32_t dtype, int64_t M, int64_t N);
+
 #ifdef __cplusplus
 }
 #endif

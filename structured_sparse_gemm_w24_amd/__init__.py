@@ -62,4 +62,11 @@ from ._lib import (  # noqa: F401
     ssg_device_arch,
     TwPacked,
 )
+from ._tune import (  # noqa: F401
+    SSG_DT_F16,
+    SSG_DT_BF16,
+    SSG_DT_F32,
+    layer_norm,
+    layer_norm_backward,
+)
 from . import perf  # noqa: F401

@@ -39,8 +39,9 @@ class TwSizes(ct.Structure):
 _P = ct.c_void_p
 _I64 = ct.c_int64
 _I32 = ct.c_int32
+_F32 = ct.c_float
 
-# name -> argument types (every function returns int, but ssg_splitk_workspace_bytes: int64)
+# name -> argument types (every function returns int, but the *_workspace_bytes: int64)
 SIGNATURES = {
     "w24_pack_f16": [_P, _I64, _I64, _P, _P],
     "w24_pack_i8": [_P, _I64, _I64, _P, _P],
@@ -70,6 +71,10 @@ SIGNATURES = {
     "w24_gemm_f16_splitk_static": [_P, _P, _P, _P, _I64, _I64, _I64, _I32, _P],
     "ssg_splitk_suggest": [_I32, _I64, _I64, _I64],
     "ssg_tile_choice": [_I32, _I64, _I64, _I64],
+    "layer_norm_forward": [_I32, _P, _I64, _P, _I64, _P, _P, _I32, _F32, _P, _I64, _P, _I64, _P, _P, _I64, _I64, _P],
+    "layer_norm_backward": [_I32, _P, _I64, _P, _I64, _P, _P, _P, _I32, _P, _I64, _P, _I64, _P, _P, _I64, _I64, _P,
+                            _I64, _P],
+    "layer_norm_workspace_bytes": [_I32, _I64, _I64],
 }
 
 
@@ -102,7 +107,7 @@ def load():
             for name, argtypes in SIGNATURES.items():
                 fn = getattr(lib, name)
                 fn.argtypes = argtypes
-                fn.restype = ct.c_int
+                fn.restype = ct.c_int64 if name.endswith("_workspace_bytes") else ct.c_int
             lib.ssg_last_error.argtypes = []
             lib.ssg_last_error.restype = ct.c_char_p
             lib.ssg_version.argtypes = []

@@ -1,0 +1,165 @@
+"""Binding of the calls that tune and serve pruned layers: layer norm, low-rank
+adapters, the cross entropy of a linear head.
+
+Same manner as ``_lib``: torch device tensors in and out, one library call on
+torch's current stream, ``SsgError`` on a nonzero status, no fallback.  Rows may
+be strided (a 2-D tensor whose last axis is contiguous); workspaces come from
+torch's caching allocator, whose reuse is ordered by the stream.
+"""
+
+from __future__ import annotations
+
+import contextlib
+
+from ._lib import _check, _ptr, _stream, _torch, load
+
+SSG_DT_F16, SSG_DT_BF16, SSG_DT_F32 = 0, 1, 2
+_CODES = None
+
+
+def _codes():
+    global _CODES
+    if _CODES is None:
+        torch = _torch()
+        _CODES = {torch.float16: SSG_DT_F16, torch.bfloat16: SSG_DT_BF16, torch.float32: SSG_DT_F32}
+    return _CODES
+
+
+_SAME = contextlib.nullcontext()
+
+
+def _on(device):
+    """Makes the tensors' device current for the launch."""
+    torch = _torch()
+    return _SAME if device.index == torch.cuda.current_device() else torch.cuda.device(device)
+
+
+def _code(t, name, allowed=(SSG_DT_F16, SSG_DT_BF16, SSG_DT_F32)):
+    torch = _torch()
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a torch tensor on a HIP device")
+    code = _codes().get(t.dtype)
+    if code is None or code not in allowed:
+        raise TypeError(f"{name} has type {t.dtype}, which this call does not take")
+    return code
+
+
+def _rows(t, like, shape, name):
+    """A [M, N] matrix of like's type and device with contiguous rows; returns its row stride."""
+    torch = _torch()
+    if not isinstance(t, torch.Tensor) or t.device != like.device:
+        raise TypeError(f"{name} must be a torch tensor on {like.device}")
+    if t.dtype != like.dtype:
+        raise TypeError(f"{name} must be {like.dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    ld, last = t.stride()
+    if last != 1 and shape[1] > 1:
+        raise ValueError(f"{name} must have contiguous rows")
+    if shape[0] <= 1:
+        return max(shape[1], 1)
+    if ld < shape[1]:
+        raise ValueError(f"{name} has overlapping rows")
+    return ld
+
+
+def _flat(t, dtype, shape, device, name):
+    """A contiguous tensor of the given type, shape and device."""
+    torch = _torch()
+    if not isinstance(t, torch.Tensor) or t.device != device:
+        raise TypeError(f"{name} must be a torch tensor on {device}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t
+
+
+def _matrix(t, name):
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be a matrix, got shape {tuple(t.shape)}")
+    return t.shape
+
+
+def _out(out, like, shape, name="out"):
+    """The caller's output (rows may be strided) or a new one; returns it and its row stride."""
+    if out is None:
+        return _torch().empty(shape, dtype=like.dtype, device=like.device), max(shape[1], 1)
+    return out, _rows(out, like, shape, name)
+
+
+def _workspace(n, like, ws=None):
+    torch = _torch()
+    if ws is not None:
+        return _flat(ws, torch.uint8, ws.shape, like.device, "workspace")
+    return torch.empty(n if n > 16 else 16, dtype=torch.uint8, device=like.device)
+
+
+# ------------------------------------------------------------------ layer norm
+def _norm_params(x, n, weight, bias):
+    torch = _torch()
+    wt = None
+    for p, name in ((weight, "weight"), (bias, "bias")):
+        if p is None:
+            continue
+        if wt is None:
+            wt = p.dtype
+            if wt not in (x.dtype, torch.float32):
+                raise TypeError(f"{name} must be {x.dtype} or torch.float32, got {wt}")
+        _flat(p, wt, (n,), x.device, name)
+    return _codes()[wt if wt is not None else x.dtype]
+
+
+def layer_norm(x, weight=None, bias=None, eps=1e-5, residual=None, out=None, sum_out=None):
+    """y = (s - mean) * rstd * weight + bias over the last axis of x [M, N], where s = x, or
+    x + residual rounded to x's type.  Returns (y, mean, rstd), with a residual
+    (y, mean, rstd, s); mean and rstd are fp32 [M].  x: float16, bfloat16 or float32;
+    weight and bias [N]: x's type or float32."""
+    torch = _torch()
+    dt = _code(x, "x")
+    shape = _matrix(x, "x")
+    m, n = shape
+    ldx = _rows(x, x, shape, "x")
+    wt = _norm_params(x, n, weight, bias)
+    y, ldy = _out(out, x, shape)
+    ldr = lds = n
+    s = None
+    if residual is not None:
+        ldr = _rows(residual, x, shape, "residual")
+        s, lds = _out(sum_out, x, shape, "sum_out")
+    elif sum_out is not None:
+        raise ValueError("sum_out needs a residual")
+    mean, rstd = torch.empty((2, m), dtype=torch.float32, device=x.device)
+    with _on(x.device):
+        _check(load().layer_norm_forward(dt, _ptr(x), ldx, _ptr(residual), ldr, _ptr(weight), _ptr(bias), wt, eps,
+                                         _ptr(y), ldy, _ptr(s), lds, _ptr(mean), _ptr(rstd), m, n, _stream(x)))
+    return (y, mean, rstd) if residual is None else (y, mean, rstd, s)
+
+
+def layer_norm_backward(dy, x, mean, rstd, weight=None, dres=None, out=None, param_grads=True, workspace=None):
+    """Gradients of layer_norm: x is its normalised input (the sum s, if there was a residual),
+    mean and rstd what it returned.  Returns (dx, dweight, dbias); dx has dres added when that is
+    given, dweight and dbias are fp32 [N] (None with param_grads=False: frozen norms)."""
+    torch = _torch()
+    dt = _code(x, "x")
+    shape = _matrix(x, "x")
+    m, n = shape
+    ldx = _rows(x, x, shape, "x")
+    lddy = _rows(dy, x, shape, "dy")
+    _flat(mean, torch.float32, (m,), x.device, "mean")
+    _flat(rstd, torch.float32, (m,), x.device, "rstd")
+    wt = _norm_params(x, n, weight, None)
+    ldres = _rows(dres, x, shape, "dres") if dres is not None else n
+    dx, lddx = _out(out, x, shape)
+    dw = db = ws = None
+    lib = load()
+    if param_grads:
+        dw, db = torch.empty((2, n), dtype=torch.float32, device=x.device)
+        ws = _workspace(lib.layer_norm_workspace_bytes(dt, m, n), x, workspace)
+    with _on(x.device):
+        _check(lib.layer_norm_backward(dt, _ptr(dy), lddy, _ptr(x), ldx, _ptr(mean), _ptr(rstd), _ptr(weight), wt,
+                                       _ptr(dres), ldres, _ptr(dx), lddx, _ptr(dw), _ptr(db), m, n, _ptr(ws),
+                                       ws.numel() if ws is not None else 0, _stream(x)))
+    return dx, dw, db

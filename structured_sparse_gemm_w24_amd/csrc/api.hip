@@ -6,6 +6,7 @@
 #include <cstring>
 #include <mutex>
 
+#include "device.h"
 #include "kernels/launch.h"
 #include "status.h"
 
@@ -16,8 +17,9 @@ constexpr int kMaxDevices = 64;
 int g_arch_state[kMaxDevices] = {0};
 std::mutex g_arch_mu;
 
-// SSG_OK if a gfx950 device is current; SSG_ENODEV / SSG_EARCH / SSG_EHIP otherwise.
-int check_device() {
+}  // namespace
+
+int ssg::check_device() {
     int count = 0;
     hipError_t e = hipGetDeviceCount(&count);
     if (e != hipSuccess || count <= 0) return ssg::fail(SSG_ENODEV, "no HIP device visible");
@@ -38,13 +40,17 @@ int check_device() {
     return SSG_OK;
 }
 
-int launched(hipError_t e, const char *what) {
+int ssg::launched(hipError_t e, const char *what) {
     if (e != hipSuccess) return ssg::fail(SSG_EHIP, "%s launch failed: %s", what, hipGetErrorString(e));
     ssg::clear_error();
     return SSG_OK;
 }
 
-bool fits_int(int64_t v) { return v >= 0 && v < (int64_t(1) << 31); }
+namespace {
+
+using ssg::check_device;
+using ssg::fits_int;
+using ssg::launched;
 
 // Common shape / pointer checks for the row-major GEMMs.
 int check_gemm(const char *fn, const void *A, const void *W, const void *C, int64_t M, int64_t N, int64_t K,

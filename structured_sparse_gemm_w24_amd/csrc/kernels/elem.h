@@ -1,0 +1,88 @@
+// Element types of the kernels that take fp16, bf16 or fp32 rows: 16-byte
+// vector access at any element alignment, conversion to fp32 and back (one
+// rounding to nearest even), and wave / workgroup sums in a fixed order.
+#pragma once
+
+#include "common.h"
+
+namespace ssg {
+
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+
+// V elements of T make one 16-byte access.
+template <class T>
+struct Elem {
+    static constexpr int V = 16 / int(sizeof(T));
+    typedef T Vec __attribute__((ext_vector_type(16 / sizeof(T))));
+};
+
+// Loads elements [c, c + V) of a row of n elements as fp32, zeros past the
+// row's end.  Rows of an odd width start at any element, so the access is not
+// assumed to be 16-byte aligned (gfx950 takes unaligned global vectors).
+template <class T>
+__device__ __forceinline__ void load_vec(const T *row, int64_t c, int64_t n, float (&f)[Elem<T>::V]) {
+    constexpr int V = Elem<T>::V;
+    if (c + V <= n) {
+        typename Elem<T>::Vec v;
+        __builtin_memcpy(&v, row + c, 16);
+#pragma unroll
+        for (int i = 0; i < V; ++i) f[i] = float(v[i]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) f[i] = c + i < n ? float(row[c + i]) : 0.0f;
+    }
+}
+
+template <class T>
+__device__ __forceinline__ void store_vec(T *row, int64_t c, int64_t n, const float (&f)[Elem<T>::V]) {
+    constexpr int V = Elem<T>::V;
+    if (c + V <= n) {
+        typename Elem<T>::Vec v;
+#pragma unroll
+        for (int i = 0; i < V; ++i) v[i] = T(f[i]);
+        __builtin_memcpy(row + c, &v, 16);
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            if (c + i < n) row[c + i] = T(f[i]);
+    }
+}
+
+// V elements of an fp32 or T parameter vector.
+template <int V, class T>
+__device__ __forceinline__ void load_param(const T *p, int64_t c, int64_t n, float (&f)[V]) {
+    if (c + V <= n) {
+        T v[V];
+        __builtin_memcpy(v, p + c, sizeof(v));
+#pragma unroll
+        for (int i = 0; i < V; ++i) f[i] = float(v[i]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) f[i] = c + i < n ? float(p[c + i]) : 0.0f;
+    }
+}
+
+__device__ __forceinline__ float wave_sum(float v) {
+#pragma unroll
+    for (int d = 32; d > 0; d >>= 1) v += __shfl_xor(v, d, 64);
+    return v;
+}
+
+// Sum over the T threads (a multiple of 64) that share a row; every thread
+// gets it.  One wave needs no LDS; more exchange through red[T / 64], which
+// the caller does not touch between calls (a barrier precedes its reuse).
+template <int T>
+__device__ __forceinline__ float row_sum(float v, float *red) {
+    v = wave_sum(v);
+    if constexpr (T > 64) {
+        __syncthreads();
+        if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
+        __syncthreads();
+        v = 0.0f;
+#pragma unroll
+        for (int i = 0; i < T / 64; ++i) v += red[i];
+    }
+    return v;
+}
+
+}  // namespace ssg

@@ -47,6 +47,37 @@ hipError_t launch_splitk_reduce(const void *ws, int splits, bool i8, const float
 int suggest_splits(int kind, int M, int N, int K);
 // tile rows x columns the GEMM launchers pick for a kind (0-3) and shape
 void tile_choice(int kind, int M, int N, int K, int *bm, int *bn);
+// ---- layer norm, low-rank adapters, linear cross entropy.
+// element types (the values of the C-ABI's SSG_DT_* constants)
+enum DType { DT_F16 = 0, DT_BF16 = 1, DT_F32 = 2 };
+
+// Rows of x and y (and of the residual and the kept sum) are ld* elements
+// apart; w and b are of type wtype (the rows' type or fp32) or null.
+struct LnFwd {
+    int dtype, wtype;
+    const void *x, *res, *w, *b;
+    int64_t ldx, ldr, ldy, lds;
+    float eps;
+    void *y, *sum;
+    float *mean, *rstd;
+    int64_t M, N;
+};
+// dw, db: fp32 [N] or both null; part: layer_norm_slices() slices of [2][N]
+// fp32 when they are not.
+struct LnBwd {
+    int dtype, wtype;
+    const void *dy, *x;
+    const float *mean, *rstd;
+    const void *w, *dres;
+    int64_t lddy, ldx, ldres, lddx;
+    void *dx;
+    float *dw, *db, *part;
+    int64_t M, N;
+};
+hipError_t launch_layer_norm_fwd(const LnFwd &a, hipStream_t st);
+hipError_t launch_layer_norm_bwd(const LnBwd &a, hipStream_t st);
+int64_t layer_norm_slices(int dtype, int64_t M, int64_t N);
+
 // K stages (one per 128 bytes of an A row) for a kind and K.
 inline int gemm_k_stages(int kind, int K) { return (kind == 2 || kind == 3) ? K / 128 : K / 64; }
 
