@@ -16,36 +16,57 @@ struct Elem {
     typedef T Vec __attribute__((ext_vector_type(16 / sizeof(T))));
 };
 
-// Loads elements [c, c + V) of a row of n elements as fp32, zeros past the
-// row's end.  Rows of an odd width start at any element, so the access is not
-// assumed to be 16-byte aligned (gfx950 takes unaligned global vectors).
+// Loads elements [c, c + V) of a row of n elements, zeros past the row's end.
+// Rows of an odd width start at any element, so the access is not assumed to
+// be 16-byte aligned (gfx950 takes unaligned global vectors).
 template <class T>
-__device__ __forceinline__ void load_vec(const T *row, int64_t c, int64_t n, float (&f)[Elem<T>::V]) {
+__device__ __forceinline__ typename Elem<T>::Vec load_raw(const T *row, int64_t c, int64_t n) {
     constexpr int V = Elem<T>::V;
+    typename Elem<T>::Vec v = {};
     if (c + V <= n) {
-        typename Elem<T>::Vec v;
         __builtin_memcpy(&v, row + c, 16);
-#pragma unroll
-        for (int i = 0; i < V; ++i) f[i] = float(v[i]);
     } else {
 #pragma unroll
-        for (int i = 0; i < V; ++i) f[i] = c + i < n ? float(row[c + i]) : 0.0f;
+        for (int i = 0; i < V; ++i)
+            if (c + i < n) v[i] = row[c + i];
     }
+    return v;
 }
 
 template <class T>
+__device__ __forceinline__ void to_float(typename Elem<T>::Vec v, float (&f)[Elem<T>::V]) {
+#pragma unroll
+    for (int i = 0; i < Elem<T>::V; ++i) f[i] = float(v[i]);
+}
+
+template <class T>
+__device__ __forceinline__ void load_vec(const T *row, int64_t c, int64_t n, float (&f)[Elem<T>::V]) {
+    to_float<T>(load_raw(row, c, n), f);
+}
+
+// Stores elements [c, c + V) of a row, rounded to T; NTS: past the L2.
+template <class T, bool NTS = false>
 __device__ __forceinline__ void store_vec(T *row, int64_t c, int64_t n, const float (&f)[Elem<T>::V]) {
     constexpr int V = Elem<T>::V;
     if (c + V <= n) {
         typename Elem<T>::Vec v;
 #pragma unroll
         for (int i = 0; i < V; ++i) v[i] = T(f[i]);
-        __builtin_memcpy(row + c, &v, 16);
+        if constexpr (NTS) {
+            typedef u32x4 Any __attribute__((aligned(2)));
+            __builtin_nontemporal_store(__builtin_bit_cast(u32x4, v), reinterpret_cast<Any *>(row + c));
+        } else {
+            __builtin_memcpy(row + c, &v, 16);
+        }
     } else {
 #pragma unroll
         for (int i = 0; i < V; ++i)
             if (c + i < n) row[c + i] = T(f[i]);
     }
+}
+template <class T>
+__device__ __forceinline__ void store_stream(T *row, int64_t c, int64_t n, const float (&f)[Elem<T>::V]) {
+    store_vec<T, true>(row, c, n, f);
 }
 
 // V elements of an fp32 or T parameter vector.

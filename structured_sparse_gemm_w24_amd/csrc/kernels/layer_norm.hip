@@ -9,16 +9,27 @@
 //             dw = sum over rows of dy * xh,  db = sum over rows of dy
 //
 // Bound by memory: forward reads and writes every row once, backward reads dy
-// and x once and writes dx once.  A row therefore stays in registers as fp32
-// between the statistics and the output, held by TPR threads with C 16-byte
-// chunks each (one wave per row up to 2048 16-bit elements, 256 threads up to
-// 8192, 1024 up to 16384); only longer rows are read again.  The variance is
-// the sum of squared distances from the finished mean, so an offset that is
-// large against the spread costs no digits.  Workgroups are persistent over
-// rows: w and b are loaded once, and the backward pass keeps its column sums
-// for dw and db in registers, adds the rows' partial sums of a workgroup
-// through LDS and writes one slice a workgroup; a second launch sums the
-// slices in order.  No atomics: results repeat bit for bit.
+// and x (and dres) once and writes dx once.  A row therefore stays in registers
+// as fp32 between the statistics and the output, held by TPR threads with C
+// 16-byte chunks each; only rows past 16384 16-bit elements (backward 8192) are
+// read again.  The variance is the sum of squared distances from the finished
+// mean, so an offset that is large against the spread costs no digits.
+// Workgroups are persistent over rows: w and b are loaded once, the next turn's
+// rows are fetched while this turn's are reduced, and outputs are streaming
+// stores (without the last two, forward ran 18.7 instead of 16.8 us at
+// 12608 x 768 fp16 with a residual).  The backward pass keeps its column sums
+// for dw and db in registers, adds those of a workgroup's rows through LDS and
+// writes one slice a workgroup; a second launch sums the slices in order.  No
+// atomics: results repeat bit for bit.  Its registers (w, dw, db, x, dy and the
+// fetched row) set the split: one chunk a thread and 1024 threads keep 16 waves
+// a CU and one slice a CU, where two to four chunks a thread ran at 1-3 waves a
+// SIMD (12608 x 768 fp16: 21.4 us, 25.3 with two chunks and 768 slices;
+// 4099 x 1537 bf16: 19.7 us, 37 with four chunks).
+// Measured on MI355X in rotating buffers (233 MB): forward 12608 x 768 fp16 with
+// residual 16.4 us = 4.7 TB/s, 4096 x 4096 24.7 us = 5.4 TB/s (a 1 GiB copy
+// reaches 5.1); backward 21.4 us = 3.6 TB/s and 30.8 us = 4.4 TB/s, both
+// launches.  Rows of an odd width pay for unaligned access: 4099 x 1537 bf16
+// forward 12.8 us = 2.0 TB/s.
 #include "elem.h"
 #include "launch.h"
 
@@ -35,38 +46,49 @@ ln_fwd_kernel(const T *x, int64_t ldx, const T *res, int64_t ldr, const W *__res
     constexpr int V = Elem<T>::V, NT = TPR < 256 ? 256 : TPR, RPB = NT / TPR;
     __shared__ float red[NT / 64];
     const int t = threadIdx.x % TPR;
+    // The rows of the next turn are fetched while this turn's are reduced; the
+    // first turn's, before the parameters are waited for.
+    typename Elem<T>::Vec xr[C], rr[C];
+    auto fetch = [&](int64_t m) {
+        if (m >= M) return;
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            const int at = (c * TPR + t) * V;
+            if (at < N) xr[c] = load_raw(x + m * ldx, at, N);
+            if (res && at < N) rr[c] = load_raw(res + m * ldr, at, N);
+        }
+    };
+    const int64_t step = int64_t(gridDim.x) * RPB;
+    int64_t m = int64_t(blockIdx.x) * RPB + threadIdx.x / TPR;
+#pragma unroll
+    for (int c = 0; c < C; ++c) xr[c] = rr[c] = typename Elem<T>::Vec{};
+    fetch(m);
     float wv[C][V], bv[C][V];
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-        const int64_t at = int64_t(c * TPR + t) * V;
+        const int at = (c * TPR + t) * V;
 #pragma unroll
         for (int i = 0; i < V; ++i) wv[c][i] = 1.0f, bv[c][i] = 0.0f;
         if (w && at < N) load_param<V>(w, at, N, wv[c]);
         if (b && at < N) load_param<V>(b, at, N, bv[c]);
     }
     const float inv_n = 1.0f / float(N);
-    for (int64_t m = int64_t(blockIdx.x) * RPB + threadIdx.x / TPR; m < M; m += int64_t(gridDim.x) * RPB) {
+    for (; m < M; m += step) {
         float f[C][V];
         float acc = 0.0f;
 #pragma unroll
         for (int c = 0; c < C; ++c) {
-            const int64_t at = int64_t(c * TPR + t) * V;
-#pragma unroll
-            for (int i = 0; i < V; ++i) f[c][i] = 0.0f;
-            if (at < N) load_vec(x + m * ldx, at, N, f[c]);
-        }
-        if (res) {
-#pragma unroll
-            for (int c = 0; c < C; ++c) {
-                const int64_t at = int64_t(c * TPR + t) * V;
-                if (at >= N) continue;
+            const int at = (c * TPR + t) * V;
+            to_float<T>(xr[c], f[c]);
+            if (res) {
                 float g[V];
-                load_vec(res + m * ldr, at, N, g);
+                to_float<T>(rr[c], g);
 #pragma unroll
                 for (int i = 0; i < V; ++i) f[c][i] = float(T(f[c][i] + g[i]));
-                store_vec(sum + m * lds, at, N, f[c]);
+                if (at < N) store_stream(sum + m * lds, at, N, f[c]);
             }
         }
+        fetch(m + step);
 #pragma unroll
         for (int c = 0; c < C; ++c)
 #pragma unroll
@@ -75,7 +97,7 @@ ln_fwd_kernel(const T *x, int64_t ldx, const T *res, int64_t ldr, const W *__res
         acc = 0.0f;
 #pragma unroll
         for (int c = 0; c < C; ++c) {
-            const int64_t at = int64_t(c * TPR + t) * V;
+            const int at = (c * TPR + t) * V;
 #pragma unroll
             for (int i = 0; i < V; ++i) {
                 f[c][i] = at + i < N ? f[c][i] - mean : 0.0f;
@@ -86,11 +108,11 @@ ln_fwd_kernel(const T *x, int64_t ldx, const T *res, int64_t ldr, const W *__res
         const float rstd = 1.0f / sqrtf(var + eps);
 #pragma unroll
         for (int c = 0; c < C; ++c) {
-            const int64_t at = int64_t(c * TPR + t) * V;
+            const int at = (c * TPR + t) * V;
             if (at >= N) continue;
 #pragma unroll
             for (int i = 0; i < V; ++i) f[c][i] = fmaf(f[c][i] * rstd, wv[c][i], bv[c][i]);
-            store_vec(y + m * ldy, at, N, f[c]);
+            store_stream(y + m * ldy, at, N, f[c]);
         }
         if (mean_out && t == 0) mean_out[m] = mean, rstd_out[m] = rstd;
     }
@@ -152,44 +174,68 @@ ln_fwd_long_kernel(const T *x, int64_t ldx, const T *res, int64_t ldr, const W *
 }
 
 // PARAM: also sum dw and db over this workgroup's rows into part[block][2][N].
-template <class T, class W, int TPR, int C, bool PARAM>
-__global__ void __launch_bounds__(TPR < 256 ? 256 : TPR)
+// NT threads a workgroup, NT / TPR rows at a time.
+template <class T, class W, int TPR, int C, int NT, bool PARAM>
+__global__ void __launch_bounds__(NT)
 ln_bwd_kernel(const T *dy, int64_t lddy, const T *x, int64_t ldx, const float *__restrict__ mean,
               const float *__restrict__ rstd, const W *__restrict__ w, const T *dres, int64_t ldres, T *dx,
               int64_t lddx, float *__restrict__ part, int64_t M, int N) {
-    constexpr int V = Elem<T>::V, NT = TPR < 256 ? 256 : TPR, RPB = NT / TPR;
-    __shared__ float red[2 * NT / 64];
-    __shared__ float cols[PARAM && RPB > 1 ? 2 * C * TPR * V : 1];
-    const int t = threadIdx.x % TPR;
+    constexpr int V = Elem<T>::V, RPB = NT / TPR, WPR = TPR / 64;
+    __shared__ float red[2][RPB][WPR][2];
+    __shared__ float cols[PARAM && RPB > 1 ? RPB * 2 * C * TPR * V : 1];
+    const int t = threadIdx.x % TPR, sub = threadIdx.x / TPR;
+    typename Elem<T>::Vec xr[C], gr[C], rr[C];
+    float mu = 0.0f, rs = 0.0f;
+    auto fetch = [&](int64_t m) {
+        if (m >= M) return;
+        mu = mean[m], rs = rstd[m];
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            const int at = (c * TPR + t) * V;
+            if (at < N) xr[c] = load_raw(x + m * ldx, at, N), gr[c] = load_raw(dy + m * lddy, at, N);
+            if (dres && at < N) rr[c] = load_raw(dres + m * ldres, at, N);
+        }
+    };
+    const int64_t step = int64_t(gridDim.x) * RPB;
+#pragma unroll
+    for (int c = 0; c < C; ++c) xr[c] = gr[c] = rr[c] = typename Elem<T>::Vec{};
+    fetch(int64_t(blockIdx.x) * RPB + sub);
     float wv[C][V], dw[C][V], db[C][V];
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-        const int64_t at = int64_t(c * TPR + t) * V;
+        const int at = (c * TPR + t) * V;
 #pragma unroll
         for (int i = 0; i < V; ++i) wv[c][i] = 1.0f, dw[c][i] = 0.0f, db[c][i] = 0.0f;
         if (w && at < N) load_param<V>(w, at, N, wv[c]);
     }
     const float inv_n = 1.0f / float(N);
-    for (int64_t m = int64_t(blockIdx.x) * RPB + threadIdx.x / TPR; m < M; m += int64_t(gridDim.x) * RPB) {
+    int turn = 0;
+    // (the turns of a workgroup are the same for all its threads: past the last
+    // row they only meet the barriers)
+    for (int64_t base = int64_t(blockIdx.x) * RPB; base < M; base += step, turn ^= 1) {
+        const int64_t m = base + sub;
+        const bool live = m < M;
         float xh[C][V], g[C][V];
+        typename Elem<T>::Vec rc[C];
         float a1 = 0.0f, a2 = 0.0f;
-        const float mu = mean[m], rs = rstd[m];
+        const float rs_m = rs;
 #pragma unroll
         for (int c = 0; c < C; ++c) {
-            const int64_t at = int64_t(c * TPR + t) * V;
-#pragma unroll
-            for (int i = 0; i < V; ++i) xh[c][i] = 0.0f, g[c][i] = 0.0f;
-            if (at < N) {
-                load_vec(x + m * ldx, at, N, xh[c]);
-                load_vec(dy + m * lddy, at, N, g[c]);
-            }
-        }
-#pragma unroll
-        for (int c = 0; c < C; ++c) {
-            const int64_t at = int64_t(c * TPR + t) * V;
+            const int at = (c * TPR + t) * V;
+            to_float<T>(xr[c], xh[c]);
+            to_float<T>(gr[c], g[c]);
+            rc[c] = rr[c];
 #pragma unroll
             for (int i = 0; i < V; ++i) {
-                xh[c][i] = at + i < N ? (xh[c][i] - mu) * rs : 0.0f;
+                xh[c][i] = live && at + i < N ? (xh[c][i] - mu) * rs : 0.0f;
+                g[c][i] = live ? g[c][i] : 0.0f;
+            }
+        }
+        fetch(m + step);
+#pragma unroll
+        for (int c = 0; c < C; ++c)
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
                 if constexpr (PARAM) {
                     dw[c][i] = fmaf(g[c][i], xh[c][i], dw[c][i]);
                     db[c][i] += g[c][i];
@@ -198,49 +244,54 @@ ln_bwd_kernel(const T *dy, int64_t lddy, const T *x, int64_t ldx, const float *_
                 a1 += g[c][i];
                 a2 = fmaf(g[c][i], xh[c][i], a2);
             }
+        a1 = wave_sum(a1);
+        a2 = wave_sum(a2);
+        if constexpr (WPR > 1) {
+            // one exchange a row; the buffers alternate, so that the next row's
+            // sums meet only readers that have passed its barrier
+            if ((threadIdx.x & 63) == 0) red[turn][sub][t >> 6][0] = a1, red[turn][sub][t >> 6][1] = a2;
+            __syncthreads();
+            a1 = a2 = 0.0f;
+#pragma unroll
+            for (int i = 0; i < WPR; ++i) a1 += red[turn][sub][i][0], a2 += red[turn][sub][i][1];
         }
-        const float c1 = row_sum<TPR>(a1, red) * inv_n;
-        const float c2 = row_sum<TPR>(a2, red + NT / 64) * inv_n;
+        const float c1 = a1 * inv_n, c2 = a2 * inv_n;
 #pragma unroll
         for (int c = 0; c < C; ++c) {
-            const int64_t at = int64_t(c * TPR + t) * V;
-            if (at >= N) continue;
+            const int at = (c * TPR + t) * V;
+            if (at >= N || !live) continue;
             float r[V];
+            to_float<T>(rc[c], r);
 #pragma unroll
-            for (int i = 0; i < V; ++i) r[i] = 0.0f;
-            if (dres) load_vec(dres + m * ldres, at, N, r);
-#pragma unroll
-            for (int i = 0; i < V; ++i) r[i] = fmaf(rs, fmaf(-xh[c][i], c2, g[c][i] - c1), r[i]);
-            store_vec(dx + m * lddx, at, N, r);
+            for (int i = 0; i < V; ++i) r[i] = fmaf(rs_m, fmaf(-xh[c][i], c2, g[c][i] - c1), r[i]);
+            store_stream(dx + m * lddx, at, N, r);
         }
     }
     if constexpr (PARAM) {
         float *pw = part + int64_t(blockIdx.x) * 2 * N, *pb = pw + N;
         if constexpr (RPB > 1) {
-            // the workgroup's waves add their column sums one after another
-            for (int q = 0; q < RPB; ++q) {
-                if (int(threadIdx.x) / TPR == q) {
+            // the rows' partial sums of the workgroup, added in order
+            constexpr int NC = C * TPR * V;
 #pragma unroll
-                    for (int c = 0; c < C; ++c)
+            for (int c = 0; c < C; ++c)
 #pragma unroll
-                        for (int i = 0; i < V; ++i) {
-                            float *s = cols + ((c * V + i) * TPR + t) * 2;
-                            s[0] = q ? s[0] + dw[c][i] : dw[c][i];
-                            s[1] = q ? s[1] + db[c][i] : db[c][i];
-                        }
+                for (int i = 0; i < V; ++i) {
+                    cols[(sub * 2 + 0) * NC + (c * V + i) * TPR + t] = dw[c][i];
+                    cols[(sub * 2 + 1) * NC + (c * V + i) * TPR + t] = db[c][i];
                 }
-                __syncthreads();
-            }
+            __syncthreads();
             for (int j = threadIdx.x; j < N; j += NT) {
                 const int chunk = j / V, i = j % V;
-                const float *s = cols + (((chunk / TPR) * V + i) * TPR + chunk % TPR) * 2;
-                pw[j] = s[0];
-                pb[j] = s[1];
+                const float *s = cols + ((chunk / TPR) * V + i) * TPR + chunk % TPR;
+                float sw = 0.0f, sb = 0.0f;
+                for (int q = 0; q < RPB; ++q) sw += s[(q * 2) * NC], sb += s[(q * 2 + 1) * NC];
+                pw[j] = sw;
+                pb[j] = sb;
             }
         } else {
 #pragma unroll
             for (int c = 0; c < C; ++c) {
-                const int64_t at = int64_t(c * TPR + t) * V;
+                const int at = (c * TPR + t) * V;
 #pragma unroll
                 for (int i = 0; i < V; ++i)
                     if (at + i < N) pw[at + i] = dw[c][i], pb[at + i] = db[c][i];
@@ -341,50 +392,62 @@ ln_param_kernel(const float *__restrict__ part, int G, int64_t N, float *__restr
     }
 }
 
-// Threads a row and chunks a thread of the register form; tpr = 0: long rows.
+// Threads a row and chunks a thread of the register forms; tpr = 0: long rows.
 struct LnShape {
     int tpr, c;
 };
-LnShape ln_shape(int64_t N, int v) {
+LnShape ln_fwd_shape(int64_t N, int v) {
     const int64_t chunks = (N + v - 1) / v;
     if (chunks <= 64) return {64, 1};
     if (chunks <= 128) return {64, 2};
-    if (chunks <= 256) return {64, 4};
+    if (chunks <= 256) return {256, 1};
     if (chunks <= 512) return {256, 2};
     if (chunks <= 1024) return {256, 4};
     if (chunks <= 2048) return {1024, 2};
     return {0, 0};
 }
+LnShape ln_bwd_shape(int64_t N, int v) {
+    const int64_t chunks = (N + v - 1) / v;
+    if (chunks <= 64) return {64, 1};
+    if (chunks <= 128) return {128, 1};
+    if (chunks <= 256) return {256, 1};
+    if (chunks <= 512) return {512, 1};
+    if (chunks <= 1024) return {1024, 1};
+    return {0, 0};
+}
 
-// Workgroups of the register form's persistent grids.
-int ln_blocks(int64_t M, const LnShape &sh, int most) {
-    const int rpb = sh.tpr < 256 ? 256 / sh.tpr : 1;
-    const int64_t groups = (M + rpb - 1) / rpb;
+// Workgroups of a persistent grid over `groups` turns, at most `most`, the
+// turns dealt evenly.
+int even_blocks(int64_t groups, int most) {
     const int64_t turns = (groups + most - 1) / most;
     return int((groups + turns - 1) / turns);
 }
 
+constexpr int kBwdThreads = 1024, kBwdBlocks = 256;
+
 int ln_bwd_blocks(int64_t M, int64_t N, int v) {
-    const LnShape sh = ln_shape(N, v);
+    const LnShape sh = ln_bwd_shape(N, v);
     if (M == 0) return 0;
     if (sh.tpr == 0) return int(M < 64 ? M : 64);
-    return ln_blocks(M, sh, sh.tpr == 1024 ? 256 : 512);
+    const int nt = sh.tpr > kBwdThreads ? sh.tpr : kBwdThreads, rpb = nt / sh.tpr;
+    return even_blocks((M + rpb - 1) / rpb, kBwdBlocks);
 }
 
 template <class T, class W>
 hipError_t fwd(const LnFwd &a, hipStream_t st) {
-    const LnShape sh = ln_shape(a.N, Elem<T>::V);
+    const LnShape sh = ln_fwd_shape(a.N, Elem<T>::V);
     const T *x = static_cast<const T *>(a.x), *res = static_cast<const T *>(a.res);
     const W *w = static_cast<const W *>(a.w), *b = static_cast<const W *>(a.b);
     T *y = static_cast<T *>(a.y), *sum = static_cast<T *>(a.sum);
 #define SSG_LN(TPR, C)                                                                                             \
     if (sh.tpr == TPR && sh.c == C) {                                                                              \
-        hipLaunchKernelGGL((ln_fwd_kernel<T, W, TPR, C>), dim3(ln_blocks(a.M, sh, 2048)),                          \
+        constexpr int RPB = TPR < 256 ? 256 / TPR : 1;                                                             \
+        hipLaunchKernelGGL((ln_fwd_kernel<T, W, TPR, C>), dim3(even_blocks((a.M + RPB - 1) / RPB, 768)),           \
                            dim3(TPR < 256 ? 256 : TPR), 0, st, x, a.ldx, res, a.ldr, w, b, a.eps, y, a.ldy, sum,   \
                            a.lds, a.mean, a.rstd, a.M, int(a.N));                                                  \
         return hipGetLastError();                                                                                  \
     }
-    SSG_LN(64, 1) SSG_LN(64, 2) SSG_LN(64, 4) SSG_LN(256, 2) SSG_LN(256, 4) SSG_LN(1024, 2)
+    SSG_LN(64, 1) SSG_LN(64, 2) SSG_LN(256, 1) SSG_LN(256, 2) SSG_LN(256, 4) SSG_LN(1024, 2)
 #undef SSG_LN
     hipLaunchKernelGGL((ln_fwd_long_kernel<T, W>), dim3(int(a.M < 2048 ? a.M : 2048)), dim3(256), 0, st, x, a.ldx, res,
                        a.ldr, w, b, a.eps, y, a.ldy, sum, a.lds, a.mean, a.rstd, a.M, a.N);
@@ -393,7 +456,7 @@ hipError_t fwd(const LnFwd &a, hipStream_t st) {
 
 template <class T, class W, bool PARAM>
 hipError_t bwd(const LnBwd &a, hipStream_t st) {
-    const LnShape sh = ln_shape(a.N, Elem<T>::V);
+    const LnShape sh = ln_bwd_shape(a.N, Elem<T>::V);
     const T *dy = static_cast<const T *>(a.dy), *x = static_cast<const T *>(a.x);
     const T *dres = static_cast<const T *>(a.dres);
     const W *w = static_cast<const W *>(a.w);
@@ -403,12 +466,13 @@ hipError_t bwd(const LnBwd &a, hipStream_t st) {
     bool done = G == 0;
 #define SSG_LN(TPR, C)                                                                                               \
     if (!done && sh.tpr == TPR && sh.c == C) {                                                                       \
-        hipLaunchKernelGGL((ln_bwd_kernel<T, W, TPR, C, PARAM>), dim3(G), dim3(TPR < 256 ? 256 : TPR), 0, st, dy,    \
-                           a.lddy, x, a.ldx, a.mean, a.rstd, w, dres, a.ldres, dx, a.lddx, a.part, a.M, int(a.N));   \
+        constexpr int NT = TPR > kBwdThreads ? TPR : kBwdThreads;                                                    \
+        hipLaunchKernelGGL((ln_bwd_kernel<T, W, TPR, C, NT, PARAM>), dim3(G), dim3(NT), 0, st, dy, a.lddy, x, a.ldx,     \
+                           a.mean, a.rstd, w, dres, a.ldres, dx, a.lddx, a.part, a.M, int(a.N));                     \
         e = hipGetLastError();                                                                                       \
         done = true;                                                                                                 \
     }
-    SSG_LN(64, 1) SSG_LN(64, 2) SSG_LN(64, 4) SSG_LN(256, 2) SSG_LN(256, 4) SSG_LN(1024, 2)
+    SSG_LN(64, 1) SSG_LN(128, 1) SSG_LN(256, 1) SSG_LN(512, 1) SSG_LN(1024, 1)
 #undef SSG_LN
     int slices = G;
     if (!done) {
