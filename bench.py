@@ -60,10 +60,10 @@ def _code_only(text):
 
 
 def kernel_hash(main="gemm.hip"):
-    """Hash of a kernel source and the shared header, code only (traffic
-    counters are only reused while this matches)."""
+    """Hash of a kernel source and the headers it is built from, code only
+    (traffic counters are only reused while this matches)."""
     h = hashlib.sha256()
-    for f in (main, "common.h"):
+    for f in (main, "common.h") + (("gemm_core.h", "gemm_tiles.h") if main == "gemm.hip" else ()):
         src = open(os.path.join(ROOT, "structured_sparse_gemm_w24_amd", "csrc", "kernels", f)).read()
         h.update(_code_only(src).encode())
     return h.hexdigest()[:16]
