@@ -416,6 +416,58 @@ int layer_norm_backward(int32_t dtype, const void *dy, int64_t lddy, const void 
  * (0 for M <= 0 or arguments it would refuse); ws 16-byte aligned. */
 int64_t layer_norm_workspace_bytes(int32_t dtype, int64_t M, int64_t N);
 
+/* Low-rank adapters of many requests beside a shared projection: token m with
+ * adapter a = index[m] gets, in addition to the projection's output,
+ *   delta[m] = scale[a] * up[a] . (down[a] . x[m]).
+ * One pool holds every adapter: down [adapters][R][K] and up [adapters][N][R],
+ * both of `dtype` (SSG_DT_F16 or SSG_DT_BF16), contiguous and 16-byte aligned.
+ * R, a multiple of 8 up to 128, is the pool's slots of rank; adapter a uses
+ * its first ranks[a] of them (clamped to 0..R; ranks NULL: all R) and what
+ * lies in the others is not used.  scale: fp32 [adapters], NULL for ones.
+ * index: int32 [M] on the device, in any order, one entry a token; -1 is no
+ * adapter, and a token whose index is otherwise outside [0, adapters) gets
+ * NaN in its output rows (the device cannot refuse the call).
+ * Products accumulate in fp32.  The low-rank values scale * down . x pass
+ * between the kernels as a pair of dtype values that keeps 16 (bf16) to 21
+ * (fp16) bits of them; with fp16 they must stay below 65504 in size. */
+typedef struct {
+    const void *down, *up;
+    const float *scale;
+    const int32_t *ranks, *index;
+    int32_t dtype, adapters, R;
+} ssg_low_rank;
+
+/* out = base + delta, rounded once; x [M][K], base and out [M][N], rows of
+ * lr->dtype with strides ldx, ldb, ldo (multiples of 8 elements; pointers
+ * 16-byte aligned).  base may be NULL (zeros) and out may be base.  K and N are
+ * multiples of 8, M >= 0.  ws: low_rank_workspace_bytes(M, R) device bytes,
+ * 16-byte aligned (0 for few tokens). */
+int low_rank_add(const ssg_low_rank *lr, const void *x, int64_t ldx, const void *base, int64_t ldb, void *out,
+                 int64_t ldo, int64_t M, int64_t N, int64_t K, void *ws, int64_t ws_bytes, void *stream);
+int64_t low_rank_workspace_bytes(int64_t M, int32_t R);
+
+/* C = A . W + delta with a 2:4 fp16 weight: w24_gemm_f16 (its layouts and shape
+ * limits) with lr's adapters added to the fp32 accumulators, so C is rounded
+ * and written once.  lr->dtype must be SSG_DT_F16.  ws:
+ * w24_low_rank_workspace_bytes(M, N, K, R) device bytes, 16-byte aligned. */
+int w24_low_rank_gemm_f16(const void *A, const void *vals, const uint32_t *meta, const ssg_low_rank *lr, void *C,
+                          int64_t M, int64_t N, int64_t K, void *ws, int64_t ws_bytes, void *stream);
+int64_t w24_low_rank_workspace_bytes(int64_t M, int64_t N, int64_t K, int32_t R);
+
+/* Gradients of delta: with dlow[m] = scale[a] * up[a]^T . dy[m],
+ *   dx[m] = base[m] + down[a]^T . dlow[m]   (base [M][K]: the shared
+ *           projection's part of the input gradient, may be NULL; dx may be base)
+ *   ddown[a][r][k] = sum over a's tokens of dlow[m][r] x[m][k]
+ *   dup[a][n][r]   = scale[a] * sum over a's tokens of dy[m][n] (down[a] . x[m])[r]
+ * ddown and dup are of lr->dtype, shaped as the pools and rounded once; slots
+ * past an adapter's rank and adapters without tokens get zeros.  Sums run in a
+ * fixed order.  Layouts and limits as for low_rank_add (dy [M][N], x and dx
+ * [M][K]); ws: low_rank_backward_workspace_bytes device bytes. */
+int low_rank_backward(const ssg_low_rank *lr, const void *dy, int64_t lddy, const void *x, int64_t ldx,
+                      const void *base, int64_t ldb, void *dx, int64_t lddx, void *ddown, void *dup, int64_t M,
+                      int64_t N, int64_t K, void *ws, int64_t ws_bytes, void *stream);
+int64_t low_rank_backward_workspace_bytes(int32_t adapters, int32_t R, int64_t M, int64_t N, int64_t K);
+
 #ifdef __cplusplus
 }
 #endif

@@ -75,6 +75,12 @@ SIGNATURES = {
     "layer_norm_backward": [_I32, _P, _I64, _P, _I64, _P, _P, _P, _I32, _P, _I64, _P, _I64, _P, _P, _I64, _I64, _P,
                             _I64, _P],
     "layer_norm_workspace_bytes": [_I32, _I64, _I64],
+    "low_rank_add": [_P, _P, _I64, _P, _I64, _P, _I64, _I64, _I64, _I64, _P, _I64, _P],
+    "low_rank_workspace_bytes": [_I64, _I32],
+    "w24_low_rank_gemm_f16": [_P, _P, _P, _P, _P, _I64, _I64, _I64, _P, _I64, _P],
+    "w24_low_rank_workspace_bytes": [_I64, _I64, _I64, _I32],
+    "low_rank_backward": [_P, _P, _I64, _P, _I64, _P, _I64, _P, _I64, _P, _P, _I64, _I64, _I64, _P, _I64, _P],
+    "low_rank_backward_workspace_bytes": [_I32, _I32, _I64, _I64, _I64],
 }
 
 

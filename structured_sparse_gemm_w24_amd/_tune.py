@@ -10,6 +10,7 @@ torch's caching allocator, whose reuse is ordered by the stream.
 from __future__ import annotations
 
 import contextlib
+import ctypes as ct
 
 from ._lib import _check, _ptr, _stream, _torch, load
 
@@ -163,3 +164,100 @@ def layer_norm_backward(dy, x, mean, rstd, weight=None, dres=None, out=None, par
                                        _ptr(dres), ldres, _ptr(dx), lddx, _ptr(dw), _ptr(db), m, n, _ptr(ws),
                                        ws.numel() if ws is not None else 0, _stream(x)))
     return dx, dw, db
+
+
+# -------------------------------------------------------------------- adapters
+class _LowRank(ct.Structure):
+    _fields_ = [("down", ct.c_void_p), ("up", ct.c_void_p), ("scale", ct.c_void_p), ("ranks", ct.c_void_p),
+                ("index", ct.c_void_p), ("dtype", ct.c_int32), ("adapters", ct.c_int32), ("R", ct.c_int32)]
+
+
+def _pool(x, n, down, up, index, scale, ranks):
+    """The C description of an adapter pool for rows x [M, K] and N = n output channels."""
+    torch = _torch()
+    dt = _code(x, "x", (SSG_DT_F16, SSG_DT_BF16))
+    m, k = _matrix(x, "x")
+    if not isinstance(down, torch.Tensor) or down.dim() != 3:
+        raise ValueError("down must be a tensor of shape [adapters, R, K]")
+    a, r, _ = down.shape
+    _flat(down, x.dtype, (a, r, k), x.device, "down")
+    _flat(up, x.dtype, (a, n, r), x.device, "up")
+    _flat(index, torch.int32, (m,), x.device, "index")
+    if scale is not None:
+        _flat(scale, torch.float32, (a,), x.device, "scale")
+    if ranks is not None:
+        _flat(ranks, torch.int32, (a,), x.device, "ranks")
+    return _LowRank(down.data_ptr(), up.data_ptr(), scale.data_ptr() if scale is not None else None,
+                    ranks.data_ptr() if ranks is not None else None, index.data_ptr(), dt, a, r)
+
+
+def _channels(up):
+    if not isinstance(up, _torch().Tensor) or up.dim() != 3:
+        raise ValueError("up must be a tensor of shape [adapters, N, R]")
+    return up.shape[1]
+
+
+def low_rank_add(base, x, down, up, index, scale=None, ranks=None, out=None, workspace=None):
+    """out[m] = base[m] + scale[a] * up[a] . (down[a] . x[m]) with a = index[m] (-1: base alone).
+
+    x [M, K], base [M, N] (None: zeros) and out (may be base): float16 or bfloat16, row strides in
+    multiples of 8.  down [adapters, R, K] and up [adapters, N, R] hold the pool, R a multiple of 8
+    up to 128; ranks int32 [adapters] are the slots in use (None: all R), scale float32 [adapters].
+    index int32 [M], any order; a token with another index outside the pool gets NaN."""
+    n = _channels(up)
+    lr = _pool(x, n, down, up, index, scale, ranks)
+    m, k = x.shape
+    ldx = _rows(x, x, x.shape, "x")
+    ldb = _rows(base, x, (m, n), "base") if base is not None else n
+    out, ldo = _out(out, x, (m, n))
+    lib = load()
+    need = lib.low_rank_workspace_bytes(m, lr.R)
+    ws = _workspace(need, x, workspace) if need > 0 else None
+    with _on(x.device):
+        _check(lib.low_rank_add(ct.byref(lr), _ptr(x), ldx, _ptr(base), ldb, _ptr(out), ldo, m, n, k, _ptr(ws),
+                                ws.numel() if ws is not None else 0, _stream(x)))
+    return out
+
+
+def w24_low_rank_gemm_f16(A, vals, meta, down, up, index, scale=None, ranks=None, out=None, workspace=None):
+    """C = A . W + the adapters' part in one pass: w24_gemm_f16 with a pool of adapters beside its 2:4
+    weight (arguments as there and as in low_rank_add; everything float16, A contiguous)."""
+    torch = _torch()
+    _code(A, "A", (SSG_DT_F16,))
+    m, k = _matrix(A, "A")
+    _flat(A, torch.float16, A.shape, A.device, "A")
+    n = vals.shape[0]
+    _flat(vals, torch.float16, (n, k // 2), A.device, "vals")
+    _flat(meta, torch.int32, (n, -(-k // 32)), A.device, "meta")
+    lr = _pool(A, n, down, up, index, scale, ranks)
+    if out is None:
+        out = torch.empty((m, n), dtype=torch.float16, device=A.device)
+    else:
+        _flat(out, torch.float16, (m, n), A.device, "out")
+    lib = load()
+    ws = _workspace(lib.w24_low_rank_workspace_bytes(m, n, k, lr.R), A, workspace)
+    with _on(A.device):
+        _check(lib.w24_low_rank_gemm_f16(_ptr(A), _ptr(vals), _ptr(meta), ct.byref(lr), _ptr(out), m, n, k, _ptr(ws),
+                                         ws.numel(), _stream(A)))
+    return out
+
+
+def low_rank_backward(dy, x, down, up, index, scale=None, ranks=None, base=None, out=None, workspace=None):
+    """Gradients of the adapters' part for dy [M, N] and the forward pass's x [M, K]: returns
+    (dx, ddown, dup).  dx [M, K] has base (the shared projection's input gradient) added when that is
+    given; ddown and dup are shaped and typed as the pool, zero where a slot or an adapter has no use."""
+    torch = _torch()
+    n = _channels(up)
+    lr = _pool(x, n, down, up, index, scale, ranks)
+    m, k = x.shape
+    ldx = _rows(x, x, x.shape, "x")
+    lddy = _rows(dy, x, (m, n), "dy")
+    ldb = _rows(base, x, x.shape, "base") if base is not None else k
+    dx, lddx = _out(out, x, x.shape)
+    ddown, dup = torch.empty_like(down), torch.empty_like(up)
+    lib = load()
+    ws = _workspace(lib.low_rank_backward_workspace_bytes(lr.adapters, lr.R, m, n, k), x, workspace)
+    with _on(x.device):
+        _check(lib.low_rank_backward(ct.byref(lr), _ptr(dy), lddy, _ptr(x), ldx, _ptr(base), ldb, _ptr(dx), lddx,
+                                     _ptr(ddown), _ptr(dup), m, n, k, _ptr(ws), ws.numel(), _stream(x)))
+    return dx, ddown, dup

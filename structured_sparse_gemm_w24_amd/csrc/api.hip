@@ -46,14 +46,7 @@ int ssg::launched(hipError_t e, const char *what) {
     return SSG_OK;
 }
 
-namespace {
-
-using ssg::check_device;
-using ssg::fits_int;
-using ssg::launched;
-
-// Common shape / pointer checks for the row-major GEMMs.
-int check_gemm(const char *fn, const void *A, const void *W, const void *C, int64_t M, int64_t N, int64_t K,
+int ssg::check_gemm(const char *fn, const void *A, const void *W, const void *C, int64_t M, int64_t N, int64_t K,
                int k_mult, int n_mult) {
     if (M < 0 || N <= 0 || K <= 0)
         return ssg::fail(SSG_EINVAL, "%s: M=%lld N=%lld K=%lld (need M >= 0, N > 0, K > 0)", fn, (long long)M,
@@ -71,6 +64,13 @@ int check_gemm(const char *fn, const void *A, const void *W, const void *C, int6
         return ssg::fail(SSG_EINVAL, "%s: pointers must be 16-byte aligned", fn);
     return SSG_OK;
 }
+
+namespace {
+
+using ssg::check_device;
+using ssg::check_gemm;
+using ssg::fits_int;
+using ssg::launched;
 
 }  // namespace
 

@@ -98,3 +98,142 @@ SSG_API int layer_norm_backward(int32_t dtype, const void *dy, int64_t lddy, con
                        ldx,   ldres, lddx, dx,    dweight, dbias, static_cast<float *>(ws), M, N};
     return launched(ssg::launch_layer_norm_bwd(a, hipStream_t(stream)), fn);
 }
+
+// ---------------------------------------------------------------- adapters
+namespace {
+
+constexpr int64_t kMaxTokens = int64_t(65535) * 2048;  // token ranges of the gradient launch
+
+int check_low_rank(const char *fn, const ssg_low_rank *lr, int64_t M, int64_t N, int64_t K) {
+    if (!lr) return ssg::fail(SSG_EINVAL, "%s: null adapter description", fn);
+    if (lr->dtype != SSG_DT_F16 && lr->dtype != SSG_DT_BF16)
+        return ssg::fail(SSG_EINVAL, "%s: adapter dtype %d must be fp16 or bf16", fn, lr->dtype);
+    if (lr->R < 8 || lr->R > 128 || lr->R % 8)
+        return ssg::fail(SSG_EINVAL, "%s: R=%d must be a multiple of 8, at most 128", fn, lr->R);
+    if (lr->adapters < 1 || lr->adapters > 65535)
+        return ssg::fail(SSG_EINVAL, "%s: adapters=%d must be in 1..65535", fn, lr->adapters);
+    if (M < 0 || M > kMaxTokens || N < 8 || K < 8 || N % 8 || K % 8 || !fits_int(N) || !fits_int(K))
+        return ssg::fail(SSG_EINVAL, "%s: M=%lld N=%lld K=%lld (need 0 <= M < 2^27, N and K positive multiples of 8)",
+                         fn, (long long)M, (long long)N, (long long)K);
+    // launch grids: tiles of 64 x 256 outputs, 64 x 64 pieces of the pools
+    if (!fits_int((M + 63) / 64 * ((N + 255) / 256)) || !fits_int((M + 63) / 64 * ((K + 255) / 256)) ||
+        !fits_int(int64_t(lr->adapters) * 2 * ((N + 63) / 64 + (K + 63) / 64)))
+        return ssg::fail(SSG_EINVAL, "%s: dimensions too large", fn);
+    return SSG_OK;
+}
+
+int check_pool(const char *fn, const ssg_low_rank *lr) {
+    if (!lr->down || !lr->up || !lr->index) return ssg::fail(SSG_EINVAL, "%s: null pointer", fn);
+    if (!ssg::aligned16(lr->down) || !ssg::aligned16(lr->up))
+        return ssg::fail(SSG_EINVAL, "%s: down and up must be 16-byte aligned", fn);
+    if (!aligned_to(lr->index, 4) || !aligned_to(lr->ranks, 4) || !aligned_to(lr->scale, 4))
+        return ssg::fail(SSG_EINVAL, "%s: index, ranks or scale misaligned", fn);
+    return SSG_OK;
+}
+
+// A matrix of 16-bit rows read and written 16 bytes at a time.
+int check_rows(const char *fn, const char *name, const void *p, int64_t ld, int64_t M, int64_t N) {
+    if (bad_ld(ld, M, N) || ld % 8)
+        return ssg::fail(SSG_EINVAL, "%s: row stride %lld of %s must be a multiple of 8, at least %lld", fn,
+                         (long long)ld, name, (long long)N);
+    if (!p) return ssg::fail(SSG_EINVAL, "%s: %s is null", fn, name);
+    if (!ssg::aligned16(p)) return ssg::fail(SSG_EINVAL, "%s: %s must be 16-byte aligned", fn, name);
+    return SSG_OK;
+}
+
+int check_ws(const char *fn, const void *ws, int64_t ws_bytes, int64_t need) {
+    if (need <= 0) return SSG_OK;
+    if (!ws || !ssg::aligned16(ws)) return ssg::fail(SSG_EINVAL, "%s: workspace null or not 16-byte aligned", fn);
+    if (ws_bytes < need)
+        return ssg::fail(SSG_EINVAL, "%s: workspace of %lld bytes, %lld needed", fn, (long long)ws_bytes,
+                         (long long)need);
+    return SSG_OK;
+}
+
+ssg::LowRank internal(const ssg_low_rank *lr) {
+    return {lr->dtype, lr->down, lr->up, lr->scale, lr->ranks, lr->index, lr->adapters, lr->R};
+}
+
+bool plain_rank(int32_t R) { return R >= 8 && R <= 128 && R % 8 == 0; }
+
+}  // namespace
+
+SSG_API int64_t low_rank_workspace_bytes(int64_t M, int32_t R) {
+    if (M <= 0 || M > kMaxTokens || !plain_rank(R) || ssg::low_rank_few(int(M))) return 0;
+    return M * R * 4;
+}
+
+SSG_API int low_rank_add(const ssg_low_rank *lr, const void *x, int64_t ldx, const void *base, int64_t ldb, void *out,
+                         int64_t ldo, int64_t M, int64_t N, int64_t K, void *ws, int64_t ws_bytes, void *stream) {
+    const char *fn = "low_rank_add";
+    int rc = check_low_rank(fn, lr, M, N, K);
+    if (rc) return rc;
+    if (M == 0) return ok();
+    if ((rc = check_pool(fn, lr))) return rc;
+    if ((rc = check_rows(fn, "x", x, ldx, M, K)) || (base && (rc = check_rows(fn, "base", base, ldb, M, N))) ||
+        (rc = check_rows(fn, "out", out, ldo, M, N)))
+        return rc;
+    if ((rc = check_ws(fn, ws, ws_bytes, low_rank_workspace_bytes(M, lr->R)))) return rc;
+    if ((rc = check_device())) return rc;
+    return launched(ssg::launch_low_rank_add(internal(lr), x, ldx, base, ldb, out, ldo, int(M), int(N), int(K), ws,
+                                             hipStream_t(stream)),
+                    fn);
+}
+
+SSG_API int64_t w24_low_rank_workspace_bytes(int64_t M, int64_t N, int64_t K, int32_t R) {
+    if (M <= 0 || N <= 0 || K <= 0 || !fits_int(M) || !fits_int(N) || !fits_int(K) || !plain_rank(R)) return 0;
+    if (!ssg::low_rank_few(int(M))) return M * R * 4;
+    return int64_t(ssg::low_rank_splits(int(M), int(N), int(K))) * M * N * 4;
+}
+
+SSG_API int w24_low_rank_gemm_f16(const void *A, const void *vals, const uint32_t *meta, const ssg_low_rank *lr,
+                                  void *C, int64_t M, int64_t N, int64_t K, void *ws, int64_t ws_bytes, void *stream) {
+    const char *fn = "w24_low_rank_gemm_f16";
+    int rc = check_low_rank(fn, lr, M, N, K);
+    if (rc) return rc;
+    if (lr->dtype != SSG_DT_F16) return ssg::fail(SSG_EINVAL, "%s: the adapters must be fp16", fn);
+    if ((rc = ssg::check_gemm(fn, A, vals, C, M, N, K, 64, 64))) return rc;
+    if (M == 0) return ok();
+    if (!meta || !ssg::aligned16(meta)) return ssg::fail(SSG_EINVAL, "%s: meta null or misaligned", fn);
+    if ((rc = check_pool(fn, lr))) return rc;
+    if ((rc = check_ws(fn, ws, ws_bytes, w24_low_rank_workspace_bytes(M, N, K, lr->R)))) return rc;
+    if ((rc = check_device())) return rc;
+    const hipStream_t st = hipStream_t(stream);
+    const ssg::LowRank in = internal(lr);
+    const int m = int(M), n = int(N), k = int(K);
+    if (ssg::low_rank_few(m)) {
+        // the 2:4 product's fp32 sums first, then adapters and rounding in one launch
+        const int splits = ssg::low_rank_splits(m, n, k);
+        if ((rc = launched(ssg::launch_gemm_partials(1, A, vals, meta, ws, m, n, k, splits, st), fn))) return rc;
+        return launched(ssg::launch_low_rank_tokens(in, A, K, ws, N, splits, C, N, m, n, k, st), fn);
+    }
+    if ((rc = launched(ssg::launch_low_rank_shrink(in, A, K, ws, m, k, st), fn))) return rc;
+    return launched(ssg::launch_w24_low_rank_f16(A, vals, meta, in, ws, C, m, n, k, st), fn);
+}
+
+SSG_API int64_t low_rank_backward_workspace_bytes(int32_t adapters, int32_t R, int64_t M, int64_t N, int64_t K) {
+    if (adapters < 1 || adapters > 65535 || !plain_rank(R) || M < 0 || M > kMaxTokens || N < 8 || K < 8 || N % 8 ||
+        K % 8 || !fits_int(N) || !fits_int(K))
+        return 0;
+    return ssg::low_rank_plan(adapters, R, M, N, K).total;
+}
+
+SSG_API int low_rank_backward(const ssg_low_rank *lr, const void *dy, int64_t lddy, const void *x, int64_t ldx,
+                              const void *base, int64_t ldb, void *dx, int64_t lddx, void *ddown, void *dup, int64_t M,
+                              int64_t N, int64_t K, void *ws, int64_t ws_bytes, void *stream) {
+    const char *fn = "low_rank_backward";
+    int rc = check_low_rank(fn, lr, M, N, K);
+    if (rc) return rc;
+    if (!ddown || !dup || !ssg::aligned16(ddown) || !ssg::aligned16(dup))
+        return ssg::fail(SSG_EINVAL, "%s: ddown or dup null or not 16-byte aligned", fn);
+    if (M > 0) {
+        if ((rc = check_pool(fn, lr))) return rc;
+        if ((rc = check_rows(fn, "dy", dy, lddy, M, N)) || (rc = check_rows(fn, "x", x, ldx, M, K)) ||
+            (base && (rc = check_rows(fn, "base", base, ldb, M, K))) || (rc = check_rows(fn, "dx", dx, lddx, M, K)))
+            return rc;
+    }
+    if ((rc = check_ws(fn, ws, ws_bytes, low_rank_backward_workspace_bytes(lr->adapters, lr->R, M, N, K)))) return rc;
+    if ((rc = check_device())) return rc;
+    const ssg::LowRankBwd b{internal(lr), dy, x, base, lddy, ldx, ldb, lddx, dx, ddown, dup, ws, int(M), int(N), int(K)};
+    return launched(ssg::launch_low_rank_bwd(b, hipStream_t(stream)), fn);
+}

@@ -78,6 +78,61 @@ hipError_t launch_layer_norm_fwd(const LnFwd &a, hipStream_t st);
 hipError_t launch_layer_norm_bwd(const LnBwd &a, hipStream_t st);
 int64_t layer_norm_slices(int dtype, int64_t M, int64_t N);
 
+// Low-rank adapters (formulas in low_rank.h).  dtype: DT_F16 or DT_BF16.
+struct LowRank {
+    int dtype;
+    const void *down, *up;  // [adapters][R][K], [adapters][N][R]
+    const float *scale;     // [adapters] or null (ones)
+    const int32_t *ranks;   // [adapters] or null (all R)
+    const int32_t *index;   // [M]
+    int adapters, R;
+};
+template <class T>
+struct ShrinkTask {
+    const T *x;
+    int64_t ldx;
+    const T *down;  // [adapters][R][K]
+    T *low;         // two planes [M][R]
+    int K;
+};
+template <class T>
+struct WgradTask {
+    const T *z;
+    int64_t ldz;
+    const T *low;
+    float *part;  // fp32 slices, or null: out is written
+    T *out;
+    int C, tiles;
+    bool rows_c;  // the result's rows are z's columns ([C][R]), else [R][C]
+};
+struct LowRankBwd {
+    LowRank lr;
+    const void *dy, *x, *base;
+    int64_t lddy, ldx, ldb, lddx;
+    void *dx, *ddown, *dup, *ws;
+    int M, N, K;
+};
+// Byte offsets in the backward pass's workspace, and its split of the tokens.
+struct LowRankPlan {
+    int64_t up_t, down_t, low, dlow, part, total;
+    int range, slices;
+};
+bool low_rank_few(int M);
+// K splits of the 2:4 product under low_rank_few()
+int low_rank_splits(int M, int N, int K);
+LowRankPlan low_rank_plan(int adapters, int R, int64_t M, int64_t N, int64_t K);
+// base: rows of T (or null: zeros); splits > 0: `splits` fp32 slices [M][N].
+hipError_t launch_low_rank_tokens(const LowRank &lr, const void *x, int64_t ldx, const void *base, int64_t ldb,
+                                  int splits, void *out, int64_t ldo, int M, int N, int K, hipStream_t st);
+hipError_t launch_low_rank_shrink(const LowRank &lr, const void *x, int64_t ldx, void *low, int M, int K,
+                                  hipStream_t st);
+// ws: two planes [M][R] of the rows' type (unused with few tokens).
+hipError_t launch_low_rank_add(const LowRank &lr, const void *x, int64_t ldx, const void *base, int64_t ldb, void *out,
+                               int64_t ldo, int M, int N, int K, void *ws, hipStream_t st);
+hipError_t launch_low_rank_bwd(const LowRankBwd &b, hipStream_t st);
+hipError_t launch_w24_low_rank_f16(const void *A, const void *vals, const uint32_t *meta, const LowRank &lr,
+                                   const void *low, void *C, int M, int N, int K, hipStream_t st);
+
 // K stages (one per 128 bytes of an A row) for a kind and K.
 inline int gemm_k_stages(int kind, int K) { return (kind == 2 || kind == 3) ? K / 128 : K / 64; }
 

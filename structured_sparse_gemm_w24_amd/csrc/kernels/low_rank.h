@@ -1,0 +1,147 @@
+// Low-rank adapters: what the kernels share.
+//
+// Token m with adapter a = index[m] gets, beside its shared projection,
+//   delta[m] = scale[a] * up[a] . (down[a] . x[m])
+// down [n][R][K] and up [n][N][R] are pools of n adapters, R slots of rank
+// each; adapter a uses the first ranks[a] slots (all R without ranks), and
+// what lies in the others is not used.  index -1: no adapter.  Any other index
+// outside [0, n) makes the token's output NaN: no pool row is read for it.
+//
+// The low-rank activations low[m][r] = scale[a] * (down[a] . x[m])[r] are
+// handed from one kernel to the next as two values of the rows' type, hi =
+// round(low) and lo = round((low - hi) * kLoScale), two planes [M][R].  Both
+// feed the matrix instructions, so that the split costs one more small product
+// instead of the digits that a single 16-bit value would lose (16 bits of
+// mantissa for bf16, 21 for fp16, against the 8 and 11 of the outputs).
+#pragma once
+
+#include "elem.h"
+
+namespace ssg {
+
+// fp16 keeps its low part scaled by 2^11, out of the subnormal range.
+template <class T>
+struct LowSplit;
+template <>
+struct LowSplit<_Float16> {
+    static constexpr float kLoScale = 2048.0f;
+};
+template <>
+struct LowSplit<__bf16> {
+    static constexpr float kLoScale = 1.0f;
+};
+
+template <class T>
+__device__ __forceinline__ floatx16 mfma32(u32x4 a, u32x4 b, floatx16 c) {
+    if constexpr (sizeof(T) == 2 && __is_same(T, _Float16))
+        return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(half8, a), __builtin_bit_cast(half8, b), c, 0,
+                                                      0, 0);
+    else
+        return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c,
+                                                       0, 0, 0);
+}
+template <class T>
+__device__ __forceinline__ floatx4 mfma16(u32x4 a, u32x4 b, floatx4 c) {
+    if constexpr (sizeof(T) == 2 && __is_same(T, _Float16))
+        return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(half8, a), __builtin_bit_cast(half8, b), c, 0,
+                                                      0, 0);
+    else
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c,
+                                                       0, 0, 0);
+}
+
+// The first `n` of eight 16-bit elements, zeros after them.
+__device__ __forceinline__ u32x4 keep16(u32x4 v, int n) {
+    if (n >= 8) return v;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = 2 * i + 1 < n ? v[i] : 2 * i < n ? v[i] & 0xffffu : 0u;
+    return v;
+}
+
+// The low part of the fp16 split back at its own scale.
+template <class T>
+__device__ __forceinline__ u32x4 lo_unscaled(u32x4 v) {
+    if constexpr (LowSplit<T>::kLoScale == 1.0f) return v;
+    typename Elem<T>::Vec h = __builtin_bit_cast(typename Elem<T>::Vec, v);
+    h *= T(1.0f / LowSplit<T>::kLoScale);
+    return __builtin_bit_cast(u32x4, h);
+}
+
+__device__ __forceinline__ int low_rank_of(const int32_t *ranks, int a, int R) {
+    if (!ranks) return R;
+    const int r = ranks[a];
+    return r < 0 ? 0 : r > R ? R : r;
+}
+
+// Adds up[a] . low to accumulators of 32x32 blocks: acc[tn][tm] holds, for the
+// 32 tokens from mw + 32 tm, the channels nw + 32 tn + 8 (i/4) + 4 h + i%4 of
+// token lane%32.  Up rows hold `upn` channels; channels past the last repeat
+// it (their results are not stored).
+// The wave visits the distinct adapters of its tokens one after another, each
+// with the other tokens' low values zeroed.
+template <class T, int TN, int TM>
+__device__ __forceinline__ void low_rank_expand(floatx16 (&acc)[TN][TM], const T *__restrict__ up,
+                                                const T *__restrict__ low, const int32_t *__restrict__ index,
+                                                const int32_t *__restrict__ ranks, int adapters, int R, int mw, int nw,
+                                                int M, int N) {
+    const int lane = threadIdx.x & 63, h = lane >> 5, r = lane & 31;
+    const int64_t plane = int64_t(M) * R;
+    int mine[TM];
+    bool todo[TM];
+#pragma unroll
+    for (int tm = 0; tm < TM; ++tm) {
+        const int m = mw + tm * 32 + r;
+        mine[tm] = m < M ? index[m] : -1;
+        todo[tm] = mine[tm] >= 0 && mine[tm] < adapters;
+        if (mine[tm] != -1 && !todo[tm]) {
+#pragma unroll
+            for (int tn = 0; tn < TN; ++tn)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) acc[tn][tm][i] = __builtin_nanf("");
+        }
+    }
+#pragma unroll
+    for (int first = 0; first < TM; ++first) {
+        for (uint64_t left = __ballot(todo[first]); left; left = __ballot(todo[first])) {
+            const int a = __builtin_amdgcn_readlane(mine[first], __builtin_ctzll(left));
+            bool sel[TM];
+#pragma unroll
+            for (int tm = 0; tm < TM; ++tm) {
+                sel[tm] = todo[tm] && mine[tm] == a;
+                todo[tm] = todo[tm] && !sel[tm];
+            }
+            const int rank = low_rank_of(ranks, a, R);
+            const T *pool = up + int64_t(a) * N * R;
+            for (int k0 = 0; k0 < rank; k0 += 16) {
+                const int k = k0 + 8 * h;
+                u32x4 w[TN], hi[TM], lo[TM];
+#pragma unroll
+                for (int tn = 0; tn < TN; ++tn) {
+                    const int n = min(nw + tn * 32 + r, N - 1);
+                    w[tn] = u32x4{0, 0, 0, 0};
+                    if (k < rank) w[tn] = keep16(ld16(pool + int64_t(n) * R + k), rank - k);
+                }
+#pragma unroll
+                for (int tm = 0; tm < TM; ++tm) {
+                    hi[tm] = lo[tm] = u32x4{0, 0, 0, 0};
+                    if (sel[tm] && k < rank) {
+                        const T *row = low + int64_t(mw + tm * 32 + r) * R + k;
+                        hi[tm] = ld16(row);
+                        lo[tm] = ld16(row + plane);
+                    }
+                }
+#pragma unroll
+                for (int tm = 0; tm < TM; ++tm) {
+                    const u32x4 l = lo_unscaled<T>(lo[tm]);
+#pragma unroll
+                    for (int tn = 0; tn < TN; ++tn) {
+                        acc[tn][tm] = mfma32<T>(w[tn], hi[tm], acc[tn][tm]);
+                        acc[tn][tm] = mfma32<T>(w[tn], l, acc[tn][tm]);
+                    }
+                }
+            }
+        }
+    }
+}
+
+}  // namespace ssg

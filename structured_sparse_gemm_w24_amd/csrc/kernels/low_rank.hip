@@ -1,0 +1,597 @@
+// Low-rank adapters of many requests beside a shared projection, for gfx950
+// (formulas and formats in low_rank.h).
+//
+//   shrink   low[m] = scale[a] * (down[a] . x[m])          a = index[m]
+//   expand   out[m] = base[m] + up[a] . low[m]
+//   tokens   both in one launch on the vector units, for few tokens
+//   wgrad    ddown[a][r][k] = sum over a's tokens of (scale up[a]^T dy)[r] x[k]
+//            dup[a][n][r]   = sum over a's tokens of dy[n] low[r]
+// The input gradient is the same pair of kernels with the roles exchanged:
+// dlow = shrink(dy, up^T), dx = expand(base, dlow, down^T), on transposed
+// copies of the pools.
+//
+// Memory bound: shrink reads x once, expand reads base and writes out once,
+// wgrad reads x and dy once; the pools are small beside them, and the products
+// (2 M R (K + N) operations) far below the matrix units' rate.
+#include "launch.h"
+#include "low_rank.h"
+#include "tw_common.h"
+
+namespace ssg {
+
+namespace {
+
+using namespace tw_detail;
+
+// Source of padding in direct-to-LDS loads.
+__device__ __attribute__((aligned(256))) uint16_t g_low_zero[128];
+
+// ---- shrink.  A workgroup takes 16 * TT tokens, its four waves every fourth
+// 64-wide slice of K; v_mfma 16x16x32 with the rank slots as rows and the
+// tokens as columns (lane: row / column lane%16, k = 8 (lane/16)..; results:
+// rows 4 (lane/16) + i of column lane%16).  The waves' sums are added in order
+// through LDS.  RB: blocks of 16 rank slots.
+template <class T, int TT, int RB>
+__device__ __forceinline__ void shrink_tile(const T *__restrict__ x, int64_t ldx, const T *__restrict__ down,
+                                            const float *__restrict__ scale, const int32_t *__restrict__ ranks,
+                                            const int32_t *__restrict__ index, int adapters, int R,
+                                            T *__restrict__ low, int M, int K, int tile, floatx4 *part) {
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int g = lane >> 4, c = lane & 15;
+    const int m0 = tile * 16 * TT;
+    // every wave finds the distinct adapters of the same tokens, in the same order
+    int mine = -1;
+    if (lane < 16 * TT && m0 + lane < M) mine = index[m0 + lane];
+    bool todo = mine >= 0 && mine < adapters;
+    int tok_a[TT];
+#pragma unroll
+    for (int t = 0; t < TT; ++t) tok_a[t] = __shfl(mine, t * 16 + c, 64);
+    for (uint64_t left = __ballot(todo); left; left = __ballot(todo)) {
+        const int a = __builtin_amdgcn_readlane(mine, __builtin_ctzll(left));
+        todo = todo && mine != a;
+        const int rank = low_rank_of(ranks, a, R);
+        const T *pool = down + int64_t(a) * R * K;
+        floatx4 acc[TT][RB];
+#pragma unroll
+        for (int t = 0; t < TT; ++t)
+#pragma unroll
+            for (int b = 0; b < RB; ++b) acc[t][b] = floatx4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll 2
+        for (int k0 = wave * 64; k0 < K; k0 += 256) {
+            u32x4 xv[2][TT], dv[2][RB];
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+                const int k = k0 + 32 * s + 8 * g;
+#pragma unroll
+                for (int t = 0; t < TT; ++t) {
+                    xv[s][t] = u32x4{0, 0, 0, 0};
+                    if (k < K && tok_a[t] == a) xv[s][t] = ld16(x + int64_t(m0 + t * 16 + c) * ldx + k);
+                }
+#pragma unroll
+                for (int b = 0; b < RB; ++b) {
+                    dv[s][b] = u32x4{0, 0, 0, 0};
+                    if (k < K && b * 16 + c < rank) dv[s][b] = ld16(pool + int64_t(b * 16 + c) * K + k);
+                }
+            }
+#pragma unroll
+            for (int s = 0; s < 2; ++s)
+#pragma unroll
+                for (int b = 0; b < RB; ++b)
+#pragma unroll
+                    for (int t = 0; t < TT; ++t) acc[t][b] = mfma16<T>(dv[s][b], xv[s][t], acc[t][b]);
+        }
+        __syncthreads();  // (the previous adapter's sums have been read)
+#pragma unroll
+        for (int t = 0; t < TT; ++t)
+#pragma unroll
+            for (int b = 0; b < RB; ++b) part[((t * RB + b) * 4 + wave) * 64 + lane] = acc[t][b];
+        __syncthreads();
+        const float s = scale ? scale[a] : 1.0f;
+        for (int q = wave; q < TT * RB; q += 4) {
+            const int t = q / RB, b = q % RB;
+            floatx4 v = part[(q * 4) * 64 + lane];
+#pragma unroll
+            for (int w = 1; w < 4; ++w) {
+                const floatx4 u = part[(q * 4 + w) * 64 + lane];
+                v.x += u.x, v.y += u.y, v.z += u.z, v.w += u.w;
+            }
+            const int m = m0 + t * 16 + c, r = b * 16 + 4 * g;
+            const int am = __shfl(mine, t * 16 + c, 64);
+            if (am == a && r < R) {
+                T hi[4], lo[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    // The product is made opaque: the compiler otherwise forms hi a
+                    // second time with a multiply that rounds to fp16 directly, and
+                    // next to a tie the stored hi is then not the one lo was taken from.
+                    float f = v[i] * s;
+                    asm("" : "+v"(f));
+                    hi[i] = T(f);
+                    lo[i] = T((f - float(hi[i])) * LowSplit<T>::kLoScale);
+                }
+                __builtin_memcpy(low + int64_t(m) * R + r, hi, 8);
+                __builtin_memcpy(low + int64_t(M) * R + int64_t(m) * R + r, lo, 8);
+            }
+        }
+    }
+}
+
+template <class T, int TT, int RB>
+__global__ void __launch_bounds__(256)
+shrink_kernel(ShrinkTask<T> p, ShrinkTask<T> q, const float *__restrict__ scale, const int32_t *__restrict__ ranks,
+              const int32_t *__restrict__ index, int adapters, int R, int M) {
+    __shared__ floatx4 part[TT * RB * 4 * 64];
+    const ShrinkTask<T> &w = blockIdx.y ? q : p;
+    shrink_tile<T, TT, RB>(w.x, w.ldx, w.down, scale, ranks, index, adapters, R, w.low, M, w.K, blockIdx.x, part);
+}
+
+// ---- expand: a workgroup takes 64 tokens x 256 channels, a wave 32 x 128.
+// The sums go through LDS as fp32 rows, so that base is read and out written
+// 16 bytes a lane; out may be base.
+template <class T>
+__global__ void __launch_bounds__(256, 2)
+expand_kernel(const T *__restrict__ up, const T *__restrict__ low, const int32_t *__restrict__ index,
+              const int32_t *__restrict__ ranks, int adapters, int R, const T *base, int64_t ldb, T *out, int64_t ldo,
+              int M, int N) {
+    constexpr int TN = 4, ROW = TN * 32 + 4;
+    __shared__ float slab[4][32 * ROW];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int h = lane >> 5, r = lane & 31;
+    const int tiles_n = (N + 255) / 256;
+    const int b = xcd_remap(blockIdx.x, gridDim.x);
+    const int mw = (b / tiles_n) * 64 + (wave & 1) * 32, nw = (b % tiles_n) * 256 + (wave >> 1) * 128;
+    const int ch = (lane & 15) * 8, row0 = lane >> 4;
+    u32x4 old[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int m = mw + i * 4 + row0, n = nw + ch;
+        old[i] = u32x4{0, 0, 0, 0};
+        if (base && m < M && n < N) old[i] = ld16(base + int64_t(m) * ldb + n);
+    }
+    floatx16 acc[TN][1];
+#pragma unroll
+    for (int tn = 0; tn < TN; ++tn) acc[tn][0] = floatx16{};
+    if (nw < N) low_rank_expand<T, TN, 1>(acc, up, low, index, ranks, adapters, R, mw, nw, M, N);
+#pragma unroll
+    for (int tn = 0; tn < TN; ++tn)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const floatx4 v = {acc[tn][0][4 * q], acc[tn][0][4 * q + 1], acc[tn][0][4 * q + 2], acc[tn][0][4 * q + 3]};
+            *reinterpret_cast<floatx4 *>(&slab[wave][r * ROW + tn * 32 + q * 8 + h * 4]) = v;
+        }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int m = mw + i * 4 + row0, n = nw + ch;
+        if (m >= M || n >= N) continue;
+        const float *s = &slab[wave][(i * 4 + row0) * ROW + ch];
+        const typename Elem<T>::Vec o = __builtin_bit_cast(typename Elem<T>::Vec, old[i]);
+        typename Elem<T>::Vec v;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = T(float(o[j]) + s[j]);
+        __builtin_nontemporal_store(__builtin_bit_cast(u32x4, v),
+                                    reinterpret_cast<u32x4 *>(out + int64_t(m) * ldo + n));
+    }
+}
+
+// ---- few tokens: one launch on the vector units.  A workgroup takes one token
+// and 512 channels and computes the token's low values by itself (the pool row
+// comes from L2 for every workgroup but the first), in fp32 throughout.
+// base: T rows, or `splits` fp32 slices [M][N] of a split product, summed here.
+template <class T, bool PARTS>
+__global__ void __launch_bounds__(512)
+tokens_kernel(const T *__restrict__ x, int64_t ldx, const T *__restrict__ down, const T *__restrict__ up,
+              const float *__restrict__ scale, const int32_t *__restrict__ ranks, const int32_t *__restrict__ index,
+              int adapters, int R, const void *base, int64_t ldb, int splits, T *out, int64_t ldo, int M, int N,
+              int K) {
+    __shared__ float low[128];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int m = blockIdx.y, n = blockIdx.x * 512 + threadIdx.x;
+    const int a = index[m];
+    const bool live = a >= 0 && a < adapters;
+    const int rank = live ? low_rank_of(ranks, a, R) : 0;
+    float sum = 0.0f;
+    if (n < N) {
+        if constexpr (PARTS) {
+            for (int s = 0; s < splits; ++s)
+                sum += static_cast<const float *>(base)[(int64_t(s) * M + m) * N + n];
+        } else if (base) {
+            sum = float(static_cast<const T *>(base)[int64_t(m) * ldb + n]);
+        }
+    }
+    const T *xr = x + int64_t(m) * ldx;
+    for (int r0 = wave * 2; r0 < rank; r0 += 16) {
+        const T *d0 = down + (int64_t(a) * R + r0) * K, *d1 = d0 + (r0 + 1 < rank ? K : 0);
+        float s0 = 0.0f, s1 = 0.0f;
+#pragma unroll 2
+        for (int k = lane * 8; k < K; k += 512) {
+            float xv[8], v0[8], v1[8];
+            to_float<T>(__builtin_bit_cast(typename Elem<T>::Vec, ld16(xr + k)), xv);
+            to_float<T>(__builtin_bit_cast(typename Elem<T>::Vec, ld16(d0 + k)), v0);
+            to_float<T>(__builtin_bit_cast(typename Elem<T>::Vec, ld16(d1 + k)), v1);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) s0 = fmaf(xv[i], v0[i], s0), s1 = fmaf(xv[i], v1[i], s1);
+        }
+        s0 = wave_sum(s0);
+        s1 = wave_sum(s1);
+        if (lane == 0) {
+            const float c = scale ? scale[a] : 1.0f;
+            low[r0] = s0 * c;
+            if (r0 + 1 < rank) low[r0 + 1] = s1 * c;
+        }
+    }
+    __syncthreads();
+    if (n >= N) return;
+    if (live) {
+        const T *u = up + (int64_t(a) * N + n) * R;
+#pragma unroll 2
+        for (int r = 0; r < rank; r += 8) {
+            float v[8];
+            to_float<T>(__builtin_bit_cast(typename Elem<T>::Vec, ld16(u + r)), v);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (r + i < rank) sum = fmaf(v[i], low[r + i], sum);
+        }
+    } else if (a != -1) {
+        sum = __builtin_nanf("");
+    }
+    out[int64_t(m) * ldo + n] = T(sum);
+}
+
+// ---- transposed copies of the pools: [n][P][Q] -> [n][Q][P], 64 x 64 tiles
+// through LDS (P and Q multiples of 8).
+template <class T>
+__global__ void __launch_bounds__(256)
+pool_transpose_kernel(const T *__restrict__ src0, T *__restrict__ dst0, int P0, int Q0, int tiles0,
+                      const T *__restrict__ src1, T *__restrict__ dst1, int P1, int Q1) {
+    __shared__ uint16_t s[64][72];
+    const bool second = int(blockIdx.x) >= tiles0;
+    const int P = second ? P1 : P0, Q = second ? Q1 : Q0;
+    const uint16_t *src = reinterpret_cast<const uint16_t *>(second ? src1 : src0);
+    uint16_t *dst = reinterpret_cast<uint16_t *>(second ? dst1 : dst0);
+    const int tile = int(blockIdx.x) - (second ? tiles0 : 0);
+    const int tq = (Q + 63) / 64, tp = (P + 63) / 64;
+    const int64_t a = tile / (tq * tp);
+    const int p0 = (tile / tq) % tp * 64, q0 = tile % tq * 64;
+    src += a * P * Q;
+    dst += a * P * Q;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int row = i * 32 + threadIdx.x / 8, c = threadIdx.x % 8 * 8;
+        if (p0 + row < P && q0 + c < Q)
+            *reinterpret_cast<u32x4 *>(&s[row][c]) = ld16(src + int64_t(p0 + row) * Q + q0 + c);
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int col = i * 32 + threadIdx.x / 8, r = threadIdx.x % 8 * 8;
+        if (q0 + col < Q && p0 + r < P) {
+            u32x4 v;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) v[j] = uint32_t(s[r + 2 * j][col]) | (uint32_t(s[r + 2 * j + 1][col]) << 16);
+            st16(dst + int64_t(q0 + col) * P + p0 + r, v);
+        }
+    }
+}
+
+// ---- wgrad: out[r][c] = sum over adapter a's tokens of low[m][r] z[m][c], z
+// [M][C] one of x (out = ddown [R][K]) and dy (out = dup [N][R]).
+// A workgroup takes one adapter, 128 columns of z and one range of tokens: it
+// lists the range's tokens of its adapter in LDS, then works through the list
+// 32 tokens at a time, their z rows and low rows copied to LDS as they lie in
+// memory ([token][column]) and read by transposing LDS reads, which give each
+// lane 8 consecutive tokens of one column (lane i of a 16-lane group receives
+// element i%4 of the 8-byte run read by lane 4e + i/4, e = 0..3).  The high and
+// the low part of `low` have accumulators of their own.  Ranges write fp32
+// slices [range][adapter][R][C] that a second launch sums in order.
+constexpr int kListCap = 2048;  // tokens of a range, at most
+
+template <class T, int RB>
+__global__ void __launch_bounds__(256)
+wgrad_kernel(WgradTask<T> p, WgradTask<T> q, const int32_t *__restrict__ index, int adapters, int R, int M,
+             int range) {
+    constexpr int RT = RB * 16;                  // rank slots of a stage row
+    constexpr int Z_STAGE = 32 * 128 * 2;        // [32][128]
+    constexpr int L_STAGE = 32 * RT * 2;         // [32][RT], one part
+    constexpr int STAGE = Z_STAGE + 2 * L_STAGE;
+    constexpr int NB = 2;
+    __shared__ __attribute__((aligned(1024))) uint8_t smem[NB * STAGE];
+    __shared__ int32_t list[kListCap];
+    __shared__ int counts[4][kListCap / 256];
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const bool second = int(blockIdx.x) >= p.tiles;
+    const WgradTask<T> &w = second ? q : p;
+    const int c0 = (int(blockIdx.x) - (second ? p.tiles : 0)) * 128;
+    const int a = blockIdx.y, C = w.C;
+    const int first = blockIdx.z * range, last = min(first + range, M);
+
+    // the tokens of adapter a in [first, last), in order
+    int total = 0;
+    {
+        constexpr int TURNS = kListCap / 256;
+        bool hit[TURNS];
+        uint64_t votes[TURNS];
+#pragma unroll
+        for (int i = 0; i < TURNS; ++i) {
+            const int m = first + i * 256 + tid;
+            hit[i] = m < last && index[m] == a;
+            votes[i] = __ballot(hit[i]);
+            if (lane == 0) counts[wave][i] = __builtin_popcountll(votes[i]);
+        }
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < TURNS; ++i)
+#pragma unroll
+            for (int v = 0; v < 4; ++v) {
+                if (v == wave && hit[i])
+                    list[total + __builtin_popcountll(votes[i] & ((uint64_t(1) << lane) - 1))] = first + i * 256 + tid;
+                total += counts[v][i];
+            }
+        __syncthreads();
+    }
+    total = __builtin_amdgcn_readfirstlane(total);
+
+    const int g = lane >> 4, j16 = lane & 15;
+    floatx4 acc[2][RB][2];
+#pragma unroll
+    for (int s = 0; s < 2; ++s)
+#pragma unroll
+        for (int b = 0; b < RB; ++b) acc[s][b][0] = acc[s][b][1] = floatx4{0.f, 0.f, 0.f, 0.f};
+
+    // Direct-to-LDS loads of a stage: 8 KiB of z (row = 4 q + lane/16, 16-byte
+    // chunk lane%16, swizzled), then 2 * RB KiB of low.
+    const int64_t plane = int64_t(M) * R;
+    auto issue = [&](int s) {
+        uint8_t *base = smem + (s % NB) * STAGE;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const int qq = j * 4 + wave, row = 4 * qq + g;
+            const int at = s * 32 + row, col = c0 + (j16 ^ (2 * (row & 3))) * 8;
+            const void *src = g_low_zero;
+            if (at < total && col < C) src = w.z + int64_t(list[at]) * w.ldz + col;
+            tw_dma16(src, base + qq * 1024);
+        }
+        for (int qq = wave; qq < 2 * RB; qq += 4) {
+            const int part = qq / RB, byte = (qq % RB) * 1024 + lane * 16;
+            const int row = byte / (RT * 2), r = byte % (RT * 2) / 2;
+            const int at = s * 32 + row;
+            const void *src = g_low_zero;
+            if (at < total && r < R) src = w.low + part * plane + int64_t(list[at]) * R + r;
+            tw_dma16(src, base + Z_STAGE + qq * 1024);
+        }
+    };
+    const int S = (total + 31) / 32;
+    typedef short s16x4 __attribute__((ext_vector_type(4)));
+    typedef __attribute__((address_space(3))) s16x4 *lds_s4;
+    // two transposing reads: rows 8 g + j16/4 and four rows on, elements from `at`
+    auto tr = [&](const uint8_t *at, int row_bytes) -> u32x4 {
+        const s16x4 lo4 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4)(at));
+        const s16x4 hi4 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4)(at + 4 * row_bytes));
+        const u32x2 u = __builtin_bit_cast(u32x2, lo4), v = __builtin_bit_cast(u32x2, hi4);
+        return u32x4{u.x, u.y, v.x, v.y};
+    };
+    if (S > 0) issue(0);
+    for (int s = 0; s < S; ++s) {
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        __syncthreads();  // stage s has landed, and everyone is done with stage s - 1
+        if (s + 1 < S) issue(s + 1);
+        const uint8_t *base = smem + (s % NB) * STAGE;
+        const int row = 8 * g + (j16 >> 2);
+        u32x4 zv[2], lv[2][RB];
+#pragma unroll
+        for (int cb = 0; cb < 2; ++cb) {
+            const int col = wave * 32 + cb * 16 + 4 * (j16 & 3);
+            zv[cb] = tr(base + row * 256 + ((col >> 3) ^ (2 * (row & 3))) * 16 + (col & 7) * 2, 256);
+        }
+#pragma unroll
+        for (int part = 0; part < 2; ++part)
+#pragma unroll
+            for (int b = 0; b < RB; ++b)
+                lv[part][b] = tr(base + Z_STAGE + part * L_STAGE + row * (RT * 2) + (b * 16 + 4 * (j16 & 3)) * 2, RT * 2);
+#pragma unroll
+        for (int part = 0; part < 2; ++part)
+#pragma unroll
+            for (int b = 0; b < RB; ++b)
+#pragma unroll
+                for (int cb = 0; cb < 2; ++cb) acc[part][b][cb] = mfma16<T>(lv[part][b], zv[cb], acc[part][b][cb]);
+    }
+
+    // lane: rank slots 16 b + 4 g + i of column c0 + 32 wave + 16 cb + j16
+    const int slice = blockIdx.z;
+#pragma unroll
+    for (int b = 0; b < RB; ++b)
+#pragma unroll
+        for (int cb = 0; cb < 2; ++cb) {
+            const int c = c0 + wave * 32 + cb * 16 + j16, r = b * 16 + 4 * g;
+            if (c >= C || r >= R) continue;
+            float v[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] = fmaf(acc[1][b][cb][i], 1.0f / LowSplit<T>::kLoScale, acc[0][b][cb][i]);
+            const int64_t mat = int64_t(R) * C;
+            if (w.part) {
+                float *o = w.part + (int64_t(slice) * adapters + a) * mat;
+                if (w.rows_c) {
+                    __builtin_memcpy(o + int64_t(c) * R + r, v, 16);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) o[int64_t(r + i) * C + c] = v[i];
+                }
+            } else {
+                T *o = w.out + int64_t(a) * mat;
+                if (w.rows_c) {
+                    T t[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) t[i] = T(v[i]);
+                    __builtin_memcpy(o + int64_t(c) * R + r, t, 8);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) o[int64_t(r + i) * C + c] = T(v[i]);
+                }
+            }
+        }
+}
+
+// Sums the ranges' slices in order and rounds once: 4 values a thread.
+template <class T>
+__global__ void __launch_bounds__(256)
+wgrad_sum_kernel(const float *__restrict__ part0, T *__restrict__ out0, int64_t n0, const float *__restrict__ part1,
+                 T *__restrict__ out1, int64_t n1, int slices) {
+    int64_t i = (int64_t(blockIdx.x) * 256 + threadIdx.x) * 4;
+    const float *part = part0;
+    T *out = out0;
+    int64_t n = n0;
+    if (i >= n0) i -= n0, part = part1, out = out1, n = n1;
+    if (i >= n) return;
+    floatx4 s = *reinterpret_cast<const floatx4 *>(part + i);
+#pragma unroll 4
+    for (int q = 1; q < slices; ++q) {
+        const floatx4 v = *reinterpret_cast<const floatx4 *>(part + q * n + i);
+        s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
+    }
+    T t[4] = {T(s.x), T(s.y), T(s.z), T(s.w)};
+    __builtin_memcpy(out + i, t, 8);
+}
+
+template <class T>
+hipError_t shrink(const ShrinkTask<T> &p, const ShrinkTask<T> *q, const LowRank &lr, int M, hipStream_t st) {
+    const dim3 grid((M + 15) / 16, q ? 2 : 1);
+#define SSG_SHRINK(RB)                                                                                              \
+    hipLaunchKernelGGL((shrink_kernel<T, 1, RB>), grid, dim3(256), 0, st, p, q ? *q : p, lr.scale, lr.ranks,        \
+                       lr.index, lr.adapters, lr.R, M)
+    if (lr.R <= 16) SSG_SHRINK(1);
+    else if (lr.R <= 32) SSG_SHRINK(2);
+    else if (lr.R <= 64) SSG_SHRINK(4);
+    else SSG_SHRINK(8);
+#undef SSG_SHRINK
+    return hipGetLastError();
+}
+
+template <class T>
+hipError_t expand(const T *up, const T *low, const LowRank &lr, const void *base, int64_t ldb, void *out, int64_t ldo,
+                  int M, int N, hipStream_t st) {
+    const int nb = (M + 63) / 64 * ((N + 255) / 256);
+    hipLaunchKernelGGL((expand_kernel<T>), dim3(nb), dim3(256), 0, st, up, low, lr.index, lr.ranks, lr.adapters, lr.R,
+                       static_cast<const T *>(base), ldb, static_cast<T *>(out), ldo, M, N);
+    return hipGetLastError();
+}
+
+template <class T>
+hipError_t add(const LowRank &lr, const void *x, int64_t ldx, const void *base, int64_t ldb, void *out, int64_t ldo,
+               int M, int N, int K, void *ws, hipStream_t st) {
+    T *low = static_cast<T *>(ws);
+    if (low_rank_few(M)) return launch_low_rank_tokens(lr, x, ldx, base, ldb, 0, out, ldo, M, N, K, st);
+    const ShrinkTask<T> p{static_cast<const T *>(x), ldx, static_cast<const T *>(lr.down), low, K};
+    const hipError_t e = shrink<T>(p, nullptr, lr, M, st);
+    if (e != hipSuccess) return e;
+    return expand<T>(static_cast<const T *>(lr.up), low, lr, base, ldb, out, ldo, M, N, st);
+}
+
+template <class T>
+hipError_t bwd(const LowRankBwd &b, hipStream_t st) {
+    const LowRank &lr = b.lr;
+    const int M = b.M, N = b.N, K = b.K, R = lr.R;
+    const LowRankPlan pl = low_rank_plan(lr.adapters, R, M, N, K);
+    uint8_t *ws = static_cast<uint8_t *>(b.ws);
+    T *up_t = reinterpret_cast<T *>(ws + pl.up_t), *down_t = reinterpret_cast<T *>(ws + pl.down_t);
+    T *low = reinterpret_cast<T *>(ws + pl.low), *dlow = reinterpret_cast<T *>(ws + pl.dlow);
+    hipError_t e;
+    const int64_t t0 = int64_t(lr.adapters) * ((R + 63) / 64) * ((N + 63) / 64);
+    const int64_t t1 = int64_t(lr.adapters) * ((R + 63) / 64) * ((K + 63) / 64);
+    if (M > 0) {
+        hipLaunchKernelGGL((pool_transpose_kernel<T>), dim3(int(t0 + t1)), dim3(256), 0, st,
+                           static_cast<const T *>(lr.up), up_t, N, R, int(t0), static_cast<const T *>(lr.down), down_t,
+                           R, K);
+        if ((e = hipGetLastError()) != hipSuccess) return e;
+        const ShrinkTask<T> p{static_cast<const T *>(b.dy), b.lddy, up_t, dlow, N};
+        const ShrinkTask<T> q{static_cast<const T *>(b.x), b.ldx, static_cast<const T *>(lr.down), low, K};
+        if ((e = shrink<T>(p, &q, lr, M, st)) != hipSuccess) return e;
+        if ((e = expand<T>(down_t, dlow, lr, b.base, b.ldb, b.dx, b.lddx, M, K, st)) != hipSuccess) return e;
+    }
+    const int64_t n0 = int64_t(lr.adapters) * R * K, n1 = int64_t(lr.adapters) * R * N;
+    float *part0 = pl.slices > 1 ? reinterpret_cast<float *>(ws + pl.part) : nullptr;
+    float *part1 = part0 ? part0 + pl.slices * n0 : nullptr;
+    const WgradTask<T> p{static_cast<const T *>(b.x), b.ldx, dlow, part0, static_cast<T *>(b.ddown), K, (K + 127) / 128,
+                         false};
+    const WgradTask<T> q{static_cast<const T *>(b.dy), b.lddy, low, part1, static_cast<T *>(b.dup), N, (N + 127) / 128,
+                         true};
+    const dim3 grid(p.tiles + q.tiles, lr.adapters, pl.slices);
+#define SSG_WGRAD(RB) \
+    hipLaunchKernelGGL((wgrad_kernel<T, RB>), grid, dim3(256), 0, st, p, q, lr.index, lr.adapters, R, M, pl.range)
+    if (R <= 16) SSG_WGRAD(1);
+    else if (R <= 32) SSG_WGRAD(2);
+    else if (R <= 64) SSG_WGRAD(4);
+    else SSG_WGRAD(8);
+#undef SSG_WGRAD
+    if ((e = hipGetLastError()) != hipSuccess || pl.slices == 1) return e;
+    hipLaunchKernelGGL((wgrad_sum_kernel<T>), dim3(int(((n0 + n1) / 4 + 255) / 256)), dim3(256), 0, st, part0,
+                       static_cast<T *>(b.ddown), n0, part1, static_cast<T *>(b.dup), n1, pl.slices);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+// Few tokens: one launch on the vector units.
+bool low_rank_few(int M) { return M <= 128; }
+
+LowRankPlan low_rank_plan(int adapters, int R, int64_t M, int64_t N, int64_t K) {
+    auto up256 = [](int64_t v) { return (v + 255) / 256 * 256; };
+    LowRankPlan p;
+    p.up_t = 0;
+    p.down_t = p.up_t + up256(int64_t(adapters) * R * N * 2);
+    p.low = p.down_t + up256(int64_t(adapters) * R * K * 2);
+    p.dlow = p.low + up256(M * R * 4);
+    p.part = p.dlow + up256(M * R * 4);
+    // token ranges: enough workgroups to fill the chip, at least 256 tokens each, at most what the list holds
+    const int64_t per = int64_t(adapters) * ((N + 127) / 128 + (K + 127) / 128);
+    int64_t want = (1024 + per - 1) / per;
+    const int64_t most = M > 256 ? M / 256 : 1;
+    if (want > most) want = most;
+    int64_t range = want > 0 ? (M + want - 1) / want : M;
+    range = (range + 31) / 32 * 32;
+    if (range > kListCap) range = kListCap;
+    if (range < 32) range = 32;
+    p.range = int(range);
+    p.slices = int(M > 0 ? (M + range - 1) / range : 1);
+    p.total = p.part + (p.slices > 1 ? p.slices * int64_t(adapters) * R * (N + K) * 4 : 0);
+    return p;
+}
+
+hipError_t launch_low_rank_tokens(const LowRank &lr, const void *x, int64_t ldx, const void *base, int64_t ldb,
+                                  int splits, void *out, int64_t ldo, int M, int N, int K, hipStream_t st) {
+    const dim3 grid((N + 511) / 512, M);
+#define SSG_TOK(T, PARTS)                                                                                            \
+    hipLaunchKernelGGL((tokens_kernel<T, PARTS>), grid, dim3(512), 0, st, static_cast<const T *>(x), ldx,            \
+                       static_cast<const T *>(lr.down), static_cast<const T *>(lr.up), lr.scale, lr.ranks, lr.index, \
+                       lr.adapters, lr.R, base, ldb, splits, static_cast<T *>(out), ldo, M, N, K)
+    if (lr.dtype == DT_F16) {
+        if (splits > 0) SSG_TOK(_Float16, true);
+        else SSG_TOK(_Float16, false);
+    } else {
+        SSG_TOK(__bf16, false);
+    }
+#undef SSG_TOK
+    return hipGetLastError();
+}
+
+hipError_t launch_low_rank_shrink(const LowRank &lr, const void *x, int64_t ldx, void *low, int M, int K,
+                                  hipStream_t st) {
+    if (lr.dtype == DT_F16)
+        return shrink<_Float16>({static_cast<const _Float16 *>(x), ldx, static_cast<const _Float16 *>(lr.down),
+                                 static_cast<_Float16 *>(low), K},
+                                nullptr, lr, M, st);
+    return shrink<__bf16>({static_cast<const __bf16 *>(x), ldx, static_cast<const __bf16 *>(lr.down),
+                           static_cast<__bf16 *>(low), K},
+                          nullptr, lr, M, st);
+}
+
+hipError_t launch_low_rank_add(const LowRank &lr, const void *x, int64_t ldx, const void *base, int64_t ldb, void *out,
+                               int64_t ldo, int M, int N, int K, void *ws, hipStream_t st) {
+    return lr.dtype == DT_F16 ? add<_Float16>(lr, x, ldx, base, ldb, out, ldo, M, N, K, ws, st)
+                              : add<__bf16>(lr, x, ldx, base, ldb, out, ldo, M, N, K, ws, st);
+}
+
+hipError_t launch_low_rank_bwd(const LowRankBwd &b, hipStream_t st) {
+    return b.lr.dtype == DT_F16 ? bwd<_Float16>(b, st) : bwd<__bf16>(b, st);
+}
+
+}  // namespace ssg

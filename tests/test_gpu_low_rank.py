@@ -1,0 +1,262 @@
+"""Low-rank adapters (added to a base, beside the 2:4 product, and their
+gradients) against a plain 64-bit implementation.
+
+Tolerance of every output, set before the first run: one rounding to the output
+type, u |ref|, plus (split + 2^-24 L) S, where S is the same sum taken over
+absolute values, L the length of the longest fp32 chain (K, N or the tokens)
+plus 64, and split what the pair of 16-bit values that carries the low-rank
+values can lose: twice 2^-21 for fp16 (11 + 11 bits), twice 2^-16 for bf16; plus
+the type's smallest step (and for fp16 the low-rank values' own, 2^-24, times
+the pool's size)."""
+
+import numpy as np
+import pytest
+
+import workloads as wl
+
+pytestmark = pytest.mark.gpu
+
+
+def _kind(dtype):
+    import torch
+    return {"f16": (torch.float16, 2.0 ** -11, 2.0 ** -20, 2.0 ** -24),
+            "bf16": (torch.bfloat16, 2.0 ** -8, 2.0 ** -15, 1e-37)}[dtype]
+
+
+def make(seed, dtype, m, n, k, r, adapters, index="runs", ranks=True, scale=True, strided=False):
+    import torch
+    dt = _kind(dtype)[0]
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    rnd = lambda *s: torch.randn(*s, generator=g, device="cuda")
+    ints = lambda lo, hi, s: torch.randint(lo, hi, s, generator=g, device="cuda").to(torch.int32)
+
+    def rows(c):
+        if strided:
+            return rnd(m, c + 24).to(dt)[:, 8:8 + c]
+        return rnd(m, c).to(dt)
+    c = dict(x=rows(k), base=rows(n), dy=rows(n), xbase=rows(k),
+             down=(rnd(adapters, r, k) / k ** 0.5).to(dt), up=(rnd(adapters, n, r) / r ** 0.5).to(dt),
+             scale=(rnd(adapters).abs() + 0.25) if scale else None,
+             ranks=ints(0, r + 1, (adapters,)) if ranks else None)
+    if index == "runs":
+        i = torch.arange(m, device="cuda") * 5 // max(m, 1)
+        c["index"] = (ints(-1, adapters, (8,))[i.long()]).to(torch.int32)
+    elif index == "mixed":
+        c["index"] = ints(-1, adapters, (m,))
+    else:
+        c["index"] = torch.full((m,), index, dtype=torch.int32, device="cuda")
+    return c
+
+
+def reference(c, backward=False):
+    """(value, sum of absolute values) of delta, or of dx, ddown and dup without the base."""
+    import torch
+    x, dy, down, up = (c[q].double() for q in ("x", "dy", "down", "up"))
+    a, r, k = down.shape
+    n, m = up.shape[1], x.shape[0]
+    z = lambda *s: torch.zeros(*s, dtype=torch.float64, device="cuda")
+    delta, dx, ddown, dup = (z(m, n), z(m, n)), (z(m, k), z(m, k)), (z(a, r, k), z(a, r, k)), (z(a, n, r), z(a, n, r))
+    for i in range(a):
+        t = (c["index"] == i).nonzero()[:, 0]
+        q = r if c["ranks"] is None else int(c["ranks"][i])
+        s = 1.0 if c["scale"] is None else c["scale"][i].double()
+        d, u = down[i, :q], up[i, :, :q]
+        for v, f in ((0, lambda w: w), (1, torch.abs)):
+            low, dlow = s * f(x[t]) @ f(d).t(), s * f(dy[t]) @ f(u)
+            delta[v][t] = low @ f(u).t()
+            if backward:
+                dx[v][t] = dlow @ f(d)
+                ddown[v][i, :q] = dlow.t() @ f(x[t])
+                dup[v][i, :, :q] = f(dy[t]).t() @ low
+    return (dx, ddown, dup) if backward else delta
+
+
+def close(got, ref, size, dtype, chain, pool=1.0):
+    _, u, split, tiny = _kind(dtype)
+    bound = u * ref.abs() + (split + 2.0 ** -24 * (chain + 64)) * size + tiny * (1 + pool)
+    off = (got.double() - ref).abs()
+    assert (off <= bound).all(), ((off / bound).max().item(), (off > bound).sum().item())
+
+
+SHAPES = [
+    # m, n, k, R, adapters, index
+    (1, 8, 8, 8, 1, 0), (1, 1024, 768, 16, 4, "mixed"), (7, 264, 72, 8, 3, "mixed"), (32, 4096, 1024, 16, 24, "mixed"),
+    (128, 520, 200, 128, 5, "mixed"), (129, 520, 200, 128, 5, "runs"), (130, 256, 64, 24, 9, "mixed"),
+    (257, 776, 392, 40, 300, "mixed"), (640, 1024, 1000, 64, 6, "runs"), (1531, 2312, 768, 32, 8, "runs"),
+    (2500, 136, 2056, 16, 2, "runs"), (300, 768, 768, 8, 1, 0), (200, 128, 128, 16, 3, -1),
+]
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("m,n,k,r,a,index", SHAPES)
+def test_add(lib, gpu, dtype, m, n, k, r, a, index):
+    c = make(m + n + k, dtype, m, n, k, r, a, index)
+    out = lib.low_rank_add(c["base"], c["x"], c["down"], c["up"], c["index"], c["scale"], c["ranks"])
+    delta, size = reference(c)
+    base = c["base"].double()
+    close(out, base + delta, base.abs() + size, dtype, k + r, r)
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("m,n,k,r,a,index", SHAPES + [(6200, 256, 136, 16, 2, "runs"), (4100, 64, 64, 8, 1, 0)])
+def test_backward(lib, gpu, dtype, m, n, k, r, a, index):
+    c = make(m * 3 + n + k, dtype, m, n, k, r, a, index)
+    got = lib.low_rank_backward(c["dy"], c["x"], c["down"], c["up"], c["index"], c["scale"], c["ranks"],
+                                base=c["xbase"])
+    dx, ddown, dup = reference(c, backward=True)
+    base = c["xbase"].double()
+    close(got[0], base + dx[0], base.abs() + dx[1], dtype, n + r, r)
+    # (the low values' own smallest step, fp16: 2^-24 of a value that is then multiplied by up to M tokens)
+    close(got[1], ddown[0], ddown[1], dtype, n + m, m ** 0.5)
+    close(got[2], dup[0], dup[1], dtype, k + m, m ** 0.5)
+
+
+@pytest.mark.parametrize("m,n,k,r,a,index", [
+    (1, 64, 64, 8, 1, 0), (3, 192, 128, 16, 2, "mixed"), (32, 4096, 1024, 16, 24, "mixed"), (64, 1024, 4096, 8, 70, "mixed"),
+    (128, 256, 512, 32, 3, "runs"), (129, 256, 512, 32, 3, "mixed"), (200, 512, 256, 64, 2, "runs"),
+    (520, 1024, 1024, 16, 4, "runs"), (512, 4096, 1024, 24, 4, "runs"), (1024, 1024, 4096, 128, 3, "runs"),
+    (4096, 3072, 768, 40, 7, "runs"), (700, 320, 320, 16, 90, "mixed")])
+def test_beside_the_sparse_product(lib, gpu, m, n, k, r, a, index):
+    import torch
+    c = make(m * 7 + n, "f16", m, n, k, r, a, index)
+    w = wl.random_24_f16(np.random.default_rng(m + n), 1, k, n)["Wp"]
+    vals, meta = lib.w24_pack_f16(w)
+    vals, meta = torch.from_numpy(vals).cuda(), torch.from_numpy(meta.view(np.int32)).cuda()
+    x = c["x"]
+    out = lib.w24_low_rank_gemm_f16(x, vals, meta, c["down"], c["up"], c["index"], c["scale"], c["ranks"])
+    wd = torch.from_numpy(w).cuda().double()
+    delta, size = reference(c)
+    close(out, x.double() @ wd + delta, x.double().abs() @ wd.abs() + size, "f16", k + r, r)
+    if index == -1 or m == 520:  # without adapters: the plain product, bit for bit
+        none = torch.full_like(c["index"], -1)
+        plain = lib.w24_gemm_f16(x, vals, meta, splits=1)
+        assert torch.equal(lib.w24_low_rank_gemm_f16(x, vals, meta, c["down"], c["up"], none), plain)
+
+
+@pytest.mark.parametrize("m", [20, 300])
+def test_pool_slots_past_the_rank_are_not_used(lib, gpu, m):
+    """NaN in every unused slot of the pool, and in every adapter nobody has, changes nothing."""
+    import torch
+    c = make(5, "f16", m, 256, 128, 24, 6, "mixed")
+    c["index"][c["index"] == 4] = -1
+    args = lambda d, u: (c["base"], c["x"], d, u, c["index"], c["scale"], c["ranks"])
+    down, up = c["down"].clone(), c["up"].clone()
+    for i in range(6):
+        q = 0 if i == 4 else int(c["ranks"][i])
+        down[i, q:], up[i, :, q:] = float("nan"), float("nan")
+    assert torch.equal(lib.low_rank_add(*args(down, up)), lib.low_rank_add(*args(c["down"], c["up"])))
+    bwd = lambda d, u: lib.low_rank_backward(c["dy"], c["x"], d, u, c["index"], c["scale"], c["ranks"], c["xbase"])
+    for p, q in zip(bwd(down, up), bwd(c["down"], c["up"])):
+        assert torch.equal(p, q) and torch.isfinite(p).all()
+
+
+@pytest.mark.parametrize("m", [40, 260])
+def test_index_outside_the_pool_gives_nan_rows(lib, gpu, m):
+    import torch
+    c = make(6, "f16", m, 192, 64, 8, 3, "mixed")
+    bad = torch.zeros(m, dtype=torch.bool, device="cuda")
+    good = c["index"].clone()
+    for i, v in ((0, 3), (17, -2), (m - 1, 2 ** 31 - 1), (33, -2 ** 31)):
+        c["index"][i] = v
+        bad[i] = True
+        good[i] = -1
+    out = lib.low_rank_add(c["base"], c["x"], c["down"], c["up"], c["index"], c["scale"], c["ranks"])
+    ref = lib.low_rank_add(c["base"], c["x"], c["down"], c["up"], good, c["scale"], c["ranks"])
+    assert torch.isnan(out[bad]).all() and torch.equal(out[~bad], ref[~bad])
+    got = lib.low_rank_backward(c["dy"], c["x"], c["down"], c["up"], c["index"], c["scale"], c["ranks"], c["xbase"])
+    ref = lib.low_rank_backward(c["dy"], c["x"], c["down"], c["up"], good, c["scale"], c["ranks"], c["xbase"])
+    assert torch.isnan(got[0][bad]).all() and torch.equal(got[0][~bad], ref[0][~bad])
+    assert torch.equal(got[1], ref[1]) and torch.equal(got[2], ref[2])
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("m", [9, 211])
+def test_strides_in_place_and_without_base(lib, gpu, dtype, m):
+    import torch
+    c = make(8, dtype, m, 328, 136, 16, 3, "mixed", strided=True)
+    pool = (c["down"], c["up"], c["index"], c["scale"], c["ranks"])
+    flat = {q: c[q].contiguous() for q in ("x", "base", "dy", "xbase")}
+    out = lib.low_rank_add(c["base"], c["x"], *pool)
+    assert torch.equal(out, lib.low_rank_add(flat["base"], flat["x"], *pool))
+    for p, q in zip(lib.low_rank_backward(c["dy"], c["x"], *pool, base=c["xbase"]),
+                    lib.low_rank_backward(flat["dy"], flat["x"], *pool, base=flat["xbase"])):
+        assert torch.equal(p, q)
+    alone = lib.low_rank_add(None, c["x"], *pool)
+    assert torch.equal(alone, lib.low_rank_add(torch.zeros_like(flat["base"]), c["x"], *pool))
+    lib.low_rank_add(c["base"], c["x"], *pool, out=c["base"])
+    assert torch.equal(c["base"], out)
+    dx = lib.low_rank_backward(c["dy"], c["x"], *pool, base=c["xbase"])[0]
+    lib.low_rank_backward(c["dy"], c["x"], *pool, base=c["xbase"], out=c["xbase"])
+    assert torch.equal(c["xbase"], dx)
+
+
+def test_no_tokens(lib, gpu):
+    import torch
+    c = make(9, "bf16", 0, 64, 64, 8, 2, -1)
+    assert lib.low_rank_add(c["base"], c["x"], c["down"], c["up"], c["index"]).shape == (0, 64)
+    dx, ddown, dup = lib.low_rank_backward(c["dy"], c["x"], c["down"], c["up"], c["index"])
+    assert dx.shape == (0, 64) and (ddown == 0).all() and (dup == 0).all()
+
+
+def test_gradients_against_differences(lib, gpu):
+    """Central differences of the 64-bit forward formula through the returned gradients: the loss
+    sum(dy * delta) is linear in x, in down and in up, so a difference along one of them is exact."""
+    import torch
+    c = make(10, "f16", 150, 64, 48, 8, 2, "mixed", ranks=False)
+    got = lib.low_rank_backward(c["dy"], c["x"], c["down"], c["up"], c["index"], c["scale"], None)
+    g = torch.Generator(device="cuda").manual_seed(1)
+    for key, grad in (("x", got[0]), ("down", got[1]), ("up", got[2])):
+        way = torch.randn(c[key].shape, generator=g, device="cuda").double()
+        loss = []
+        for sign in (1, -1):
+            d = dict(c, **{key: c[key].double() + sign * way})
+            loss.append((d["dy"].double() * reference(d)[0]).sum())
+        diff = (loss[0] - loss[1]) / 2
+        # every entry of the gradient was rounded once to fp16 (2^-11) from sums good to 2^-19
+        bound = (2.0 ** -11 + 2.0 ** -19) * (grad.double() * way).abs().sum() + 1e-6
+        assert (diff - (grad.double() * way).sum()).abs() <= bound
+
+
+def test_repeatable_and_on_another_stream(lib, gpu):
+    import torch
+    c = make(11, "f16", 3000, 512, 256, 16, 5, "runs")
+    call = lambda: (lib.low_rank_add(c["base"], c["x"], c["down"], c["up"], c["index"], c["scale"]),
+                    *lib.low_rank_backward(c["dy"], c["x"], c["down"], c["up"], c["index"], c["scale"], None, c["xbase"]))
+    first = call()
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(st):
+        again = call()
+    torch.cuda.current_stream().wait_stream(st)
+    for p, q in zip(first, again):
+        assert torch.equal(p, q)
+
+
+def test_refusals(lib, gpu):
+    import torch
+    c = make(12, "f16", 200, 64, 64, 16, 2, "mixed")
+    pool = (c["down"], c["up"], c["index"])
+    with pytest.raises(TypeError):
+        lib.low_rank_add(c["base"], c["x"].float(), *pool)
+    with pytest.raises(TypeError):
+        lib.low_rank_add(c["base"], c["x"], c["down"], c["up"], c["index"].long())
+    with pytest.raises(ValueError):
+        lib.low_rank_add(c["base"], c["x"], c["down"], c["up"], c["index"][:-1].contiguous())
+    with pytest.raises(TypeError):
+        lib.low_rank_add(c["base"], c["x"], c["down"].bfloat16(), c["up"], c["index"])
+    with pytest.raises(lib.SsgError, match="multiple of 8"):
+        lib.low_rank_add(c["base"], c["x"], c["down"][:, :12].contiguous(), c["up"][:, :, :12].contiguous(), c["index"])
+    with pytest.raises(lib.SsgError, match="row stride"):
+        wide = torch.zeros((200, 68), device="cuda").half()
+        lib.low_rank_add(c["base"], wide[:, :64], *pool)
+    with pytest.raises(lib.SsgError, match="aligned"):
+        wide = torch.zeros((200, 72), device="cuda").half()
+        lib.low_rank_add(c["base"], wide[:, 4:68], *pool)
+    with pytest.raises(lib.SsgError, match="workspace"):
+        lib.low_rank_add(c["base"], c["x"], *pool, workspace=torch.empty(32, dtype=torch.uint8, device="cuda"))
+    with pytest.raises(lib.SsgError, match="multiples of 8"):
+        lib.low_rank_add(c["base"][:, :60], c["x"], c["down"], c["up"][:, :60].contiguous(), c["index"])
+    with pytest.raises(lib.SsgError, match="multiple of 64"):
+        y = torch.zeros((96, 32), device="cuda").half()
+        lib.w24_low_rank_gemm_f16(c["x"], y, torch.zeros((96, 2), dtype=torch.int32, device="cuda"), c["down"],
+                                  torch.zeros((2, 96, 16), device="cuda").half(), c["index"])
