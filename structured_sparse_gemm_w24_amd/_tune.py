@@ -11,22 +11,51 @@ from __future__ import annotations
 
 import contextlib
 import ctypes as ct
+import functools
 
-from ._lib import _check, _ptr, _stream, _torch, load
+from . import _lib
+from ._lib import SSG_OK, SsgError
 
 SSG_DT_F16, SSG_DT_BF16, SSG_DT_F32 = 0, 1, 2
-_CODES = None
-
-
-def _codes():
-    global _CODES
-    if _CODES is None:
-        torch = _torch()
-        _CODES = {torch.float16: SSG_DT_F16, torch.bfloat16: SSG_DT_BF16, torch.float32: SSG_DT_F32}
-    return _CODES
-
-
 _SAME = contextlib.nullcontext()
+
+
+@functools.lru_cache(maxsize=None)
+def _torch():
+    import torch
+    return torch
+
+
+def load():
+    return _lib._LIB or _lib.load()
+
+
+def _check(rc):
+    if rc != SSG_OK:
+        raise SsgError(rc, load().ssg_last_error().decode())
+
+
+@functools.lru_cache(maxsize=None)
+def _codes():
+    torch = _torch()
+    return {torch.float16: SSG_DT_F16, torch.bfloat16: SSG_DT_BF16, torch.float32: SSG_DT_F32}
+
+
+@functools.lru_cache(maxsize=None)
+def _raw_stream():
+    """device index -> its current stream's handle (torch's own lookup where it has one: it
+    builds no Stream object, 0.1 instead of 1.8 us a call)."""
+    torch = _torch()
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return raw or (lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+def _stream(t):
+    return _raw_stream()(t.device.index)
+
+
+def _ptr(t):
+    return t.data_ptr() if t is not None else None
 
 
 def _on(device):
@@ -36,8 +65,7 @@ def _on(device):
 
 
 def _code(t, name, allowed=(SSG_DT_F16, SSG_DT_BF16, SSG_DT_F32)):
-    torch = _torch()
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+    if not isinstance(t, _torch().Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a torch tensor on a HIP device")
     code = _codes().get(t.dtype)
     if code is None or code not in allowed:
@@ -45,20 +73,25 @@ def _code(t, name, allowed=(SSG_DT_F16, SSG_DT_BF16, SSG_DT_F32)):
     return code
 
 
-def _rows(t, like, shape, name):
-    """A [M, N] matrix of like's type and device with contiguous rows; returns its row stride."""
-    torch = _torch()
-    if not isinstance(t, torch.Tensor) or t.device != like.device:
-        raise TypeError(f"{name} must be a torch tensor on {like.device}")
-    if t.dtype != like.dtype:
-        raise TypeError(f"{name} must be {like.dtype}, got {t.dtype}")
+def _tensor(t, dtype, shape, device, name):
+    if not isinstance(t, _torch().Tensor) or t.device != device:
+        raise TypeError(f"{name} must be a torch tensor on {device}")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+
+
+def _rows(t, like, shape, name):
+    """A [M, N] matrix of like's type and device with contiguous rows; returns its row stride."""
+    _tensor(t, like.dtype, shape, like.device, name)
+    if t.is_contiguous():
+        return shape[1] or 1
     ld, last = t.stride()
     if last != 1 and shape[1] > 1:
         raise ValueError(f"{name} must have contiguous rows")
     if shape[0] <= 1:
-        return max(shape[1], 1)
+        return shape[1] or 1
     if ld < shape[1]:
         raise ValueError(f"{name} has overlapping rows")
     return ld
@@ -66,13 +99,7 @@ def _rows(t, like, shape, name):
 
 def _flat(t, dtype, shape, device, name):
     """A contiguous tensor of the given type, shape and device."""
-    torch = _torch()
-    if not isinstance(t, torch.Tensor) or t.device != device:
-        raise TypeError(f"{name} must be a torch tensor on {device}")
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.shape != shape:
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    _tensor(t, dtype, shape, device, name)
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     return t
@@ -87,7 +114,8 @@ def _matrix(t, name):
 def _out(out, like, shape, name="out"):
     """The caller's output (rows may be strided) or a new one; returns it and its row stride."""
     if out is None:
-        return _torch().empty(shape, dtype=like.dtype, device=like.device), max(shape[1], 1)
+        return (_torch().empty_like(like) if like.is_contiguous() and like.shape == shape else like.new_empty(shape),
+                shape[1] or 1)
     return out, _rows(out, like, shape, name)
 
 
@@ -95,7 +123,7 @@ def _workspace(n, like, ws=None):
     torch = _torch()
     if ws is not None:
         return _flat(ws, torch.uint8, ws.shape, like.device, "workspace")
-    return torch.empty(n if n > 16 else 16, dtype=torch.uint8, device=like.device)
+    return like.new_empty(n if n > 16 else 16, dtype=torch.uint8)
 
 
 # ------------------------------------------------------------------ layer norm
@@ -132,7 +160,7 @@ def layer_norm(x, weight=None, bias=None, eps=1e-5, residual=None, out=None, sum
         s, lds = _out(sum_out, x, shape, "sum_out")
     elif sum_out is not None:
         raise ValueError("sum_out needs a residual")
-    mean, rstd = torch.empty((2, m), dtype=torch.float32, device=x.device)
+    mean, rstd = x.new_empty(m, dtype=torch.float32), x.new_empty(m, dtype=torch.float32)
     with _on(x.device):
         _check(load().layer_norm_forward(dt, _ptr(x), ldx, _ptr(residual), ldr, _ptr(weight), _ptr(bias), wt, eps,
                                          _ptr(y), ldy, _ptr(s), lds, _ptr(mean), _ptr(rstd), m, n, _stream(x)))
@@ -157,7 +185,7 @@ def layer_norm_backward(dy, x, mean, rstd, weight=None, dres=None, out=None, par
     dw = db = ws = None
     lib = load()
     if param_grads:
-        dw, db = torch.empty((2, n), dtype=torch.float32, device=x.device)
+        dw, db = x.new_empty(n, dtype=torch.float32), x.new_empty(n, dtype=torch.float32)
         ws = _workspace(lib.layer_norm_workspace_bytes(dt, m, n), x, workspace)
     with _on(x.device):
         _check(lib.layer_norm_backward(dt, _ptr(dy), lddy, _ptr(x), ldx, _ptr(mean), _ptr(rstd), _ptr(weight), wt,
@@ -231,7 +259,7 @@ def w24_low_rank_gemm_f16(A, vals, meta, down, up, index, scale=None, ranks=None
     _flat(meta, torch.int32, (n, -(-k // 32)), A.device, "meta")
     lr = _pool(A, n, down, up, index, scale, ranks)
     if out is None:
-        out = torch.empty((m, n), dtype=torch.float16, device=A.device)
+        out = A.new_empty((m, n))
     else:
         _flat(out, torch.float16, (m, n), A.device, "out")
     lib = load()

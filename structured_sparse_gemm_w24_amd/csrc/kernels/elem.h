@@ -69,6 +69,16 @@ __device__ __forceinline__ void store_stream(T *row, int64_t c, int64_t n, const
     store_vec<T, true>(row, c, n, f);
 }
 
+// a + b rounded to T by way of fp32.  The fp32 sum is made opaque, so that every
+// use sees this one rounding (the compiler may otherwise round some uses to
+// fp16 directly, which differs next to a tie).
+template <class T>
+__device__ __forceinline__ float rounded_sum(float a, float b) {
+    float s = a + b;
+    asm("" : "+v"(s));
+    return float(T(s));
+}
+
 // V elements of an fp32 or T parameter vector.
 template <int V, class T>
 __device__ __forceinline__ void load_param(const T *p, int64_t c, int64_t n, float (&f)[V]) {

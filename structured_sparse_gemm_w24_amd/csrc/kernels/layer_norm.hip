@@ -84,7 +84,7 @@ ln_fwd_kernel(const T *x, int64_t ldx, const T *res, int64_t ldr, const W *__res
                 float g[V];
                 to_float<T>(rr[c], g);
 #pragma unroll
-                for (int i = 0; i < V; ++i) f[c][i] = float(T(f[c][i] + g[i]));
+                for (int i = 0; i < V; ++i) f[c][i] = rounded_sum<T>(f[c][i], g[i]);
                 if (at < N) store_stream(sum + m * lds, at, N, f[c]);
             }
         }
@@ -134,7 +134,7 @@ ln_fwd_long_kernel(const T *x, int64_t ldx, const T *res, int64_t ldr, const W *
                 float g[V];
                 load_vec(res + m * ldr, c, N, g);
 #pragma unroll
-                for (int i = 0; i < V; ++i) f[i] = float(T(f[i] + g[i]));
+                for (int i = 0; i < V; ++i) f[i] = rounded_sum<T>(f[i], g[i]);
             }
         };
         float acc = 0.0f;
