@@ -468,6 +468,36 @@ int low_rank_backward(const ssg_low_rank *lr, const void *dy, int64_t lddy, cons
                       int64_t N, int64_t K, void *ws, int64_t ws_bytes, void *stream);
 int64_t low_rank_backward_workspace_bytes(int32_t adapters, int32_t R, int64_t M, int64_t N, int64_t K);
 
+/* Softmax cross entropy of a linear head, without keeping the logits
+ * z[m][v] = x[m] . w[v] of x [M][D] and w [V][D] (dtype SSG_DT_F16 or
+ * SSG_DT_BF16, fp32 accumulation, row strides ldx and ldw):
+ *   lse[m]  = log(sum_v exp z[m][v])
+ *   loss[m] = lse[m] - z[m][target[m]],  0 where target[m] == ignore_index
+ * both fp32 [M], any reduction left to the caller.  A target that is neither
+ * ignore_index nor in [0, V) makes its row's loss NaN (the device cannot refuse
+ * the call).  M >= 0, V >= 1, 1 <= D < 2^20, x below 4 GiB.  Contiguous x and w
+ * (ld == D, D a multiple of 64) are read where they lie and must be 16-byte
+ * aligned; others are first copied into the workspace
+ * (linear_cross_entropy_workspace_bytes(.., backward = 0), 16-byte aligned). */
+int linear_cross_entropy_forward(int32_t dtype, const void *x, int64_t ldx, const void *w, int64_t ldw,
+                                 const int64_t *target, int64_t ignore_index, float *loss, float *lse, int64_t M,
+                                 int64_t V, int64_t D, void *ws, int64_t ws_bytes, void *stream);
+
+/* Its gradient for dloss fp32 [M] (the derivative by each row's loss), with the
+ * forward pass's lse: for G[m][v] = dloss[m] (exp(z[m][v] - lse[m]) - [v ==
+ * target[m]]), zero in ignored rows,
+ *   dx = G . w  [M][D]  and  dw = G^T . x  [V][D]  (row strides lddx, lddw)
+ * in dtype, rounded once from fp32 sums.  The logits are computed again in
+ * pieces of the vocabulary; the workspace holds one piece's G (at most 256 MiB,
+ * or 2048 entries) and copies of the operands.  A target outside [0, V) makes its
+ * row of dx, and dw, NaN.  dw is all zeros when M = 0. */
+int linear_cross_entropy_backward(int32_t dtype, const float *dloss, const void *x, int64_t ldx, const void *w,
+                                  int64_t ldw, const int64_t *target, int64_t ignore_index, const float *lse, void *dx,
+                                  int64_t lddx, void *dw, int64_t lddw, int64_t M, int64_t V, int64_t D, void *ws,
+                                  int64_t ws_bytes, void *stream);
+int64_t linear_cross_entropy_workspace_bytes(int32_t dtype, int64_t M, int64_t V, int64_t D, int64_t ldx, int64_t ldw,
+                                             int32_t backward);
+
 #ifdef __cplusplus
 }
 #endif

@@ -68,6 +68,8 @@ from ._tune import (  # noqa: F401
     SSG_DT_F32,
     layer_norm,
     layer_norm_backward,
+    linear_cross_entropy,
+    linear_cross_entropy_backward,
     low_rank_add,
     low_rank_backward,
     w24_low_rank_gemm_f16,

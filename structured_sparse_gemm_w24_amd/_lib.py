@@ -81,6 +81,10 @@ SIGNATURES = {
     "w24_low_rank_workspace_bytes": [_I64, _I64, _I64, _I32],
     "low_rank_backward": [_P, _P, _I64, _P, _I64, _P, _I64, _P, _I64, _P, _P, _I64, _I64, _I64, _P, _I64, _P],
     "low_rank_backward_workspace_bytes": [_I32, _I32, _I64, _I64, _I64],
+    "linear_cross_entropy_forward": [_I32, _P, _I64, _P, _I64, _P, _I64, _P, _P, _I64, _I64, _I64, _P, _I64, _P],
+    "linear_cross_entropy_backward": [_I32, _P, _P, _I64, _P, _I64, _P, _I64, _P, _P, _I64, _P, _I64, _I64, _I64,
+                                      _I64, _P, _I64, _P],
+    "linear_cross_entropy_workspace_bytes": [_I32, _I64, _I64, _I64, _I64, _I64, _I32],
 }
 
 

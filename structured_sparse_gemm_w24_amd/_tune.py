@@ -289,3 +289,52 @@ def low_rank_backward(dy, x, down, up, index, scale=None, ranks=None, base=None,
         _check(lib.low_rank_backward(ct.byref(lr), _ptr(dy), lddy, _ptr(x), ldx, _ptr(base), ldb, _ptr(dx), lddx,
                                      _ptr(ddown), _ptr(dup), m, n, k, _ptr(ws), ws.numel(), _stream(x)))
     return dx, ddown, dup
+
+
+# ------------------------------------------------------------------------ loss
+def _head(x, w, target):
+    torch = _torch()
+    dt = _code(x, "x", (SSG_DT_F16, SSG_DT_BF16))
+    m, d = _matrix(x, "x")
+    if not isinstance(w, torch.Tensor) or w.dim() != 2:
+        raise ValueError("w must be a matrix [V, D]")
+    v = w.shape[0]
+    ldx = _rows(x, x, x.shape, "x")
+    ldw = _rows(w, x, (v, d), "w")
+    _flat(target, torch.int64, (m,), x.device, "target")
+    return dt, m, v, d, ldx, ldw
+
+
+def linear_cross_entropy(x, w, target, ignore_index=-100, workspace=None):
+    """Softmax cross entropy of the logits x . w^T, which are never stored: x [M, D] and w [V, D] float16
+    or bfloat16 (rows may be strided), target int64 [M].  Returns (loss, lse), float32 [M]: a row's loss (0
+    where its target is ignore_index, NaN for a target outside the vocabulary) and its log-sum-exp, which
+    the backward pass takes."""
+    torch = _torch()
+    dt, m, v, d, ldx, ldw = _head(x, w, target)
+    loss, lse = x.new_empty(m, dtype=torch.float32), x.new_empty(m, dtype=torch.float32)
+    lib = load()
+    ws = _workspace(lib.linear_cross_entropy_workspace_bytes(dt, m, v, d, ldx, ldw, 0), x, workspace)
+    with _on(x.device):
+        _check(lib.linear_cross_entropy_forward(dt, _ptr(x), ldx, _ptr(w), ldw, _ptr(target), ignore_index, _ptr(loss),
+                                                _ptr(lse), m, v, d, _ptr(ws), ws.numel(), _stream(x)))
+    return loss, lse
+
+
+def linear_cross_entropy_backward(dloss, x, w, target, lse, ignore_index=-100, out=None, dw_out=None, workspace=None):
+    """Gradient of linear_cross_entropy for dloss float32 [M] (the derivative by each row's loss: 1 / rows for
+    their mean) and its lse.  Returns (dx, dw) in x's type; the logits are computed again in pieces of the
+    vocabulary."""
+    torch = _torch()
+    dt, m, v, d, ldx, ldw = _head(x, w, target)
+    _flat(dloss, torch.float32, (m,), x.device, "dloss")
+    _flat(lse, torch.float32, (m,), x.device, "lse")
+    dx, lddx = _out(out, x, x.shape)
+    dw, lddw = _out(dw_out, w, w.shape, "dw_out")
+    lib = load()
+    ws = _workspace(lib.linear_cross_entropy_workspace_bytes(dt, m, v, d, ldx, ldw, 1), x, workspace)
+    with _on(x.device):
+        _check(lib.linear_cross_entropy_backward(dt, _ptr(dloss), _ptr(x), ldx, _ptr(w), ldw, _ptr(target),
+                                                 ignore_index, _ptr(lse), _ptr(dx), lddx, _ptr(dw), lddw, m, v, d,
+                                                 _ptr(ws), ws.numel(), _stream(x)))
+    return dx, dw

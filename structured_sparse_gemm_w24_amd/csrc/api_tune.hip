@@ -237,3 +237,80 @@ SSG_API int low_rank_backward(const ssg_low_rank *lr, const void *dy, int64_t ld
     const ssg::LowRankBwd b{internal(lr), dy, x, base, lddy, ldx, ldb, lddx, dx, ddown, dup, ws, int(M), int(N), int(K)};
     return launched(ssg::launch_low_rank_bwd(b, hipStream_t(stream)), fn);
 }
+
+// -------------------------------------------------------------------- loss
+namespace {
+
+// Operands the products cannot read where they lie get a packed copy.
+bool packs(int64_t ld, int64_t D) { return ld != D || D % 64 != 0; }
+
+bool plain_loss(int32_t dtype, int64_t M, int64_t V, int64_t D) {
+    return (dtype == SSG_DT_F16 || dtype == SSG_DT_BF16) && M >= 0 && V >= 1 && D >= 1 && fits_int(M) && fits_int(V) &&
+           fits_int(D) && M * ((D + 63) / 64 * 128) < (int64_t(1) << 32) && D < (1 << 20) &&
+           (M + 63) / 64 * ((V + 63) / 64) < (int64_t(1) << 31);
+}
+
+int check_loss(const char *fn, int32_t dtype, const void *x, int64_t ldx, const void *w, int64_t ldw,
+               const int64_t *target, int64_t M, int64_t V, int64_t D) {
+    if (dtype != SSG_DT_F16 && dtype != SSG_DT_BF16)
+        return ssg::fail(SSG_EINVAL, "%s: dtype %d must be fp16 or bf16", fn, dtype);
+    if (!plain_loss(dtype, M, V, D))
+        return ssg::fail(SSG_EINVAL, "%s: M=%lld V=%lld D=%lld (need 0 <= M, 1 <= V, 1 <= D < 2^20, x below 4 GiB)", fn,
+                         (long long)M, (long long)V, (long long)D);
+    if (bad_ld(ldx, M, D) || bad_ld(ldw, V, D))
+        return ssg::fail(SSG_EINVAL, "%s: a row stride is shorter than D=%lld", fn, (long long)D);
+    if (M == 0) return SSG_OK;
+    if (!x || !w || !target) return ssg::fail(SSG_EINVAL, "%s: null pointer", fn);
+    if (!aligned_to(x, packs(ldx, D) ? 2 : 16) || !aligned_to(w, packs(ldw, D) ? 2 : 16) || !aligned_to(target, 8))
+        return ssg::fail(SSG_EINVAL, "%s: x and w must be 16-byte aligned, target 8-byte", fn);
+    return SSG_OK;
+}
+
+}  // namespace
+
+SSG_API int64_t linear_cross_entropy_workspace_bytes(int32_t dtype, int64_t M, int64_t V, int64_t D, int64_t ldx,
+                                                     int64_t ldw, int32_t backward) {
+    if (!plain_loss(dtype, M, V, D) || M == 0) return 0;
+    return ssg::loss_plan(M, V, D, packs(ldx, D), packs(ldw, D), backward != 0).total;
+}
+
+SSG_API int linear_cross_entropy_forward(int32_t dtype, const void *x, int64_t ldx, const void *w, int64_t ldw,
+                                         const int64_t *target, int64_t ignore_index, float *loss, float *lse,
+                                         int64_t M, int64_t V, int64_t D, void *ws, int64_t ws_bytes, void *stream) {
+    const char *fn = "linear_cross_entropy_forward";
+    int rc = check_loss(fn, dtype, x, ldx, w, ldw, target, M, V, D);
+    if (rc) return rc;
+    if (M == 0) return ok();
+    if (!loss || !lse || !aligned_to(loss, 4) || !aligned_to(lse, 4))
+        return ssg::fail(SSG_EINVAL, "%s: loss or lse null or misaligned", fn);
+    const ssg::LossPlan pl = ssg::loss_plan(M, V, D, packs(ldx, D), packs(ldw, D), false);
+    if ((rc = check_ws(fn, ws, ws_bytes, pl.total))) return rc;
+    if ((rc = check_device())) return rc;
+    ssg::Loss a{};
+    a.dtype = dtype, a.x = x, a.w = w, a.ldx = ldx, a.ldw = ldw, a.target = target, a.ignore = ignore_index;
+    a.loss = loss, a.lse = lse, a.M = M, a.V = V, a.D = D, a.ws = ws;
+    return launched(ssg::launch_loss_fwd(a, pl, hipStream_t(stream)), fn);
+}
+
+SSG_API int linear_cross_entropy_backward(int32_t dtype, const float *dloss, const void *x, int64_t ldx, const void *w,
+                                          int64_t ldw, const int64_t *target, int64_t ignore_index, const float *lse,
+                                          void *dx, int64_t lddx, void *dw, int64_t lddw, int64_t M, int64_t V,
+                                          int64_t D, void *ws, int64_t ws_bytes, void *stream) {
+    const char *fn = "linear_cross_entropy_backward";
+    int rc = check_loss(fn, dtype, x, ldx, w, ldw, target, M, V, D);
+    if (rc) return rc;
+    if (bad_ld(lddx, M, D) || bad_ld(lddw, V, D))
+        return ssg::fail(SSG_EINVAL, "%s: a row stride is shorter than D=%lld", fn, (long long)D);
+    if (!dw || !aligned_to(dw, 2) || (M > 0 && (!dx || !aligned_to(dx, 2))))
+        return ssg::fail(SSG_EINVAL, "%s: dx or dw null or misaligned", fn);
+    if (M > 0 && (!dloss || !lse || !aligned_to(dloss, 4) || !aligned_to(lse, 4)))
+        return ssg::fail(SSG_EINVAL, "%s: dloss or lse null or misaligned", fn);
+    const ssg::LossPlan pl = ssg::loss_plan(M, V, D, packs(ldx, D), packs(ldw, D), true);
+    if (M > 0 && (rc = check_ws(fn, ws, ws_bytes, pl.total))) return rc;
+    if ((rc = check_device())) return rc;
+    ssg::Loss a{};
+    a.dtype = dtype, a.x = x, a.w = w, a.ldx = ldx, a.ldw = ldw, a.target = target, a.ignore = ignore_index;
+    a.dloss = dloss, a.lse = const_cast<float *>(lse), a.dx = dx, a.dw = dw, a.lddx = lddx, a.lddw = lddw;
+    a.M = M, a.V = V, a.D = D, a.ws = ws;
+    return launched(ssg::launch_loss_bwd(a, pl, hipStream_t(stream)), fn);
+}

@@ -7,8 +7,6 @@
 
 namespace ssg {
 
-typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
-
 // V elements of T make one 16-byte access.
 template <class T>
 struct Elem {

@@ -77,7 +77,8 @@
 
 namespace ssg {
 
-enum Kind { DENSE_F16 = 0, W24_F16 = 1, DENSE_I8 = 2, W24_I8 = 3 };
+// (DENSE_BF16 is used by the linear cross entropy alone.)
+enum Kind { DENSE_F16 = 0, W24_F16 = 1, DENSE_I8 = 2, W24_I8 = 3, DENSE_BF16 = 4 };
 // EPI_F16: fp16 kinds.  int8 kinds: EPI_I32 raw accumulators; the others
 // compute y = float(acc) * scale[n] (+ bias[n]), each step rounded to nearest
 // even, then store y as fp32, fp16 or saturated int8.  EPI_PART (split K, any
@@ -95,6 +96,8 @@ struct KindTraits<DENSE_F16> {
     static constexpr int kMW = 0;    // meta words per row per stage
     static constexpr int kNI = 4;    // instructions per stage
 };
+template <>
+struct KindTraits<DENSE_BF16> : KindTraits<DENSE_F16> {};
 template <>
 struct KindTraits<W24_F16> {
     static constexpr bool kSparse = true, kI8 = false;
@@ -180,6 +183,10 @@ __device__ __forceinline__ void mma(typename AccOf<KIND>::T &acc, u32x4 w, u32x8
         const u32x4 lo = __builtin_shufflevector(a, a, 0, 1, 2, 3);
         acc = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(half8, w), __builtin_bit_cast(half8, lo), acc,
                                                       0, 0, 0);
+    } else if constexpr (KIND == DENSE_BF16) {
+        const u32x4 lo = __builtin_shufflevector(a, a, 0, 1, 2, 3);
+        acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, w), __builtin_bit_cast(bf16x8, lo),
+                                                       acc, 0, 0, 0);
     } else {
         const u32x4 lo = __builtin_shufflevector(a, a, 0, 1, 2, 3);
         acc = __builtin_amdgcn_mfma_i32_32x32x32_i8(__builtin_bit_cast(intx4, w), __builtin_bit_cast(intx4, lo), acc,

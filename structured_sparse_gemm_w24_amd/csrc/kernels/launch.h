@@ -133,6 +133,33 @@ hipError_t launch_low_rank_bwd(const LowRankBwd &b, hipStream_t st);
 hipError_t launch_w24_low_rank_f16(const void *A, const void *vals, const uint32_t *meta, const LowRank &lr,
                                    const void *low, void *C, int M, int N, int K, hipStream_t st);
 
+// Linear cross entropy (formulas in loss.hip).
+struct Loss {
+    int dtype;  // DT_F16 or DT_BF16
+    const void *x, *w;
+    int64_t ldx, ldw;
+    const int64_t *target;
+    int64_t ignore;
+    float *loss, *lse;  // forward: written; backward: lse read
+    const float *dloss;
+    void *dx, *dw;
+    int64_t lddx, lddw;
+    int64_t M, V, D;
+    void *ws;
+};
+// Pieces of the vocabulary and byte offsets in the workspace.
+struct LossPlan {
+    int64_t dp;      // D rounded up to the products' step of 64
+    int64_t mp;      // M likewise
+    bool pack_x, pack_w;
+    int64_t piece;   // vocabulary entries of a piece
+    int64_t tiles;   // forward: tiles of the vocabulary
+    int64_t x, w, part, logit, xt, wt, g, gt, acc, scale, total;
+};
+LossPlan loss_plan(int64_t M, int64_t V, int64_t D, bool pack_x, bool pack_w, bool backward);
+hipError_t launch_loss_fwd(const Loss &a, const LossPlan &pl, hipStream_t st);
+hipError_t launch_loss_bwd(const Loss &a, const LossPlan &pl, hipStream_t st);
+
 // K stages (one per 128 bytes of an A row) for a kind and K.
 inline int gemm_k_stages(int kind, int K) { return (kind == 2 || kind == 3) ? K / 128 : K / 64; }
 

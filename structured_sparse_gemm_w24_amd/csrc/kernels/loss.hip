@@ -1,0 +1,552 @@
+// Softmax cross entropy of a linear head over a large vocabulary, and its
+// gradient, without keeping the logits, for gfx950.
+//
+//   z[m][v]  = x[m] . w[v]
+//   lse[m]   = log sum_v exp z[m][v],   loss[m] = lse[m] - z[m][target[m]]
+//   G[m][v]  = dloss[m] (exp(z[m][v] - lse[m]) - [v = target[m]])
+//   dx = G w,   dw = G^T x                    (G = 0 in ignored rows)
+//
+// Bound by the matrix units: 2 M V D operations forward, 6 M V D backward (the
+// logits once more, and the two products).  All products run on the GEMM
+// skeleton (gemm_core.h), whose operands are both contiguous along the summed
+// axis, with epilogues of their own:
+//   * forward, each tile reduces its logits to a maximum and a sum of
+//     exponentials per row in registers and writes those 8 bytes a row; a second
+//     launch merges a row's tiles in order;
+//   * backward works through the vocabulary in pieces.  For a piece, the first
+//     product's epilogue turns the logits into G, and writes it both ways
+//     round, [M][piece] and [piece][M]: the operands of dx += G w and of
+//     dw[piece] = G^T x.  w's piece and x are transposed once for the same reason
+//     (reading w or x against its grain inside the products would cost them their
+//     direct-to-LDS loads).  dx is summed over the pieces in fp32.
+// G is rounded to the operands' 16 bits, as the products need it; its rows are
+// divided by the largest |dloss| first (and, fp16, multiplied by 2^12, so that a
+// probability of 2^-26 is still a normal number), which the products' outputs
+// are multiplied by again in fp32.
+#include "elem.h"
+#include "gemm_core.h"
+#include "gemm_tiles.h"
+#include "launch.h"
+
+namespace ssg {
+
+namespace {
+
+constexpr float kLog2e = 1.44269504088896340736f;
+__device__ __forceinline__ float exp_of(float x) { return __builtin_amdgcn_exp2f(x * kLog2e); }
+
+template <class T>
+constexpr float kGradScale = __is_same(T, _Float16) ? 4096.0f : 1.0f;
+
+// (max, sum of exp(z - max)) of two sets of logits; an empty or all -inf set
+// has max -inf and sum 0.
+__device__ __forceinline__ void merge(float &m, float &s, float m2, float s2) {
+    const float top = fmaxf(m, m2);
+    const float at = top == -INFINITY ? 0.0f : top;
+    s = s * exp_of(m - at) + s2 * exp_of(m2 - at);
+    m = top;
+}
+
+// ---- forward epilogue: a tile's statistics and the targets' logits.
+struct LossStats {
+    static constexpr bool kAfter = false, kEpilogue = true;
+    const int64_t *target;
+    float *part;   // [tiles][M][2]
+    float *logit;  // [M]
+    int64_t v0;    // first vocabulary entry of this launch
+    int tile0;     // its first tile
+
+    template <class CF, int SMEM>
+    __device__ __forceinline__ void epilogue(floatx16 (&acc)[CF::TN][CF::TM], uint8_t *smem, bool loader, int m0,
+                                             int n0, int wave, int M, int N, int, int tile_n) const {
+        constexpr int TN = CF::TN, TM = CF::TM, BM = CF::WM * TM * 32;
+        static_assert(CF::WN * BM * 8 <= SMEM, "statistics must fit in the stage ring");
+        const int lane = threadIdx.x & 63, h = lane >> 5, r = lane & 31;
+        const int wm = wave % CF::WM, wn = wave / CF::WM;
+        const int nw = n0 + wn * TN * 32;
+        float *s_max = reinterpret_cast<float *>(smem), *s_sum = s_max + CF::WN * BM;
+        __syncthreads();  // every wave is done reading the stage buffers
+        if (!loader) {
+#pragma unroll
+            for (int tm = 0; tm < TM; ++tm) {
+                const int room = N - nw - 4 * h;  // channels c < room exist
+                const int row = wm * TM * 32 + tm * 32 + r, m = m0 + row;
+                const int64_t t = m < M ? target[m] - v0 : -1;
+                // the target's place among this lane's channels (those with bit 2 clear, from 4 h)
+                const int at = t >= nw && t < nw + TN * 32 && t < N ? int(t) - nw - 4 * h : -1;
+                float zt = 0.0f, top = -INFINITY;
+#pragma unroll
+                for (int tn = 0; tn < TN; ++tn)
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        const int c = tn * 32 + 8 * (i / 4) + i % 4;
+                        const float z = c < room ? acc[tn][tm][i] : -INFINITY;
+                        zt = c == at ? z : zt;
+                        top = fmaxf(top, z);
+                    }
+                if (at >= 0 && (at & 4) == 0) logit[m] = zt;
+                top = fmaxf(top, __shfl_xor(top, 32, 64));
+                const float ref = top == -INFINITY ? 0.0f : top;
+                float sum = 0.0f;
+#pragma unroll
+                for (int tn = 0; tn < TN; ++tn)
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                    sum += tn * 32 + 8 * (i / 4) + i % 4 < room ? exp_of(acc[tn][tm][i] - ref) : 0.0f;
+                sum += __shfl_xor(sum, 32, 64);
+                if (h == 0) s_max[wn * BM + row] = top, s_sum[wn * BM + row] = sum;
+            }
+        }
+        __syncthreads();
+        if (int(threadIdx.x) < BM && m0 + int(threadIdx.x) < M) {
+            float m = s_max[threadIdx.x], s = s_sum[threadIdx.x];
+#pragma unroll
+            for (int q = 1; q < CF::WN; ++q) merge(m, s, s_max[q * BM + threadIdx.x], s_sum[q * BM + threadIdx.x]);
+            float *o = part + (int64_t(tile0 + tile_n) * M + m0 + threadIdx.x) * 2;
+            o[0] = m;
+            o[1] = s;
+        }
+    }
+};
+
+// Merges a row's tiles: 64 rows a workgroup, 16 threads a row.
+__global__ void __launch_bounds__(1024)
+loss_rows_kernel(const float *__restrict__ part, const float *__restrict__ logit, const int64_t *__restrict__ target,
+                 int64_t ignore, int tiles, int64_t V, int M, float *__restrict__ loss, float *__restrict__ lse) {
+    __shared__ float sm[16][64], ss[16][64];
+    const int row = threadIdx.x & 63, q = threadIdx.x >> 6;
+    const int m = blockIdx.x * 64 + row;
+    float top = -INFINITY, sum = 0.0f;
+    if (m < M) {
+        // the maximum first, so that the sums are independent of one another
+#pragma unroll 4
+        for (int t = q; t < tiles; t += 16) top = fmaxf(top, part[(int64_t(t) * M + m) * 2]);
+        const float ref = top == -INFINITY ? 0.0f : top;
+#pragma unroll 4
+        for (int t = q; t < tiles; t += 16) {
+            const float *p = part + (int64_t(t) * M + m) * 2;
+            sum += p[1] * exp_of(p[0] - ref);
+        }
+    }
+    sm[q][row] = top;
+    ss[q][row] = sum;
+    __syncthreads();
+    if (q == 0 && m < M) {
+        for (int i = 1; i < 16; ++i) merge(top, sum, sm[i][row], ss[i][row]);
+        const float l = top + logf(sum);
+        const int64_t t = target[m];
+        lse[m] = l;
+        loss[m] = t == ignore ? 0.0f : t < 0 || t >= V ? __builtin_nanf("") : l - logit[m];
+    }
+}
+
+// ---- backward epilogue: logits to G, written [M][ldg] and transposed [N][mp],
+// zeros in the padding of both.
+template <class T>
+struct LossGrad {
+    static constexpr bool kAfter = false, kEpilogue = true;
+    const int64_t *target;
+    int64_t ignore, V, v0;
+    const float *dloss, *lse, *scale;  // scale[0] = largest |dloss|
+    T *g, *gt;
+    int ldg, mp;
+
+    template <class CF, int SMEM>
+    __device__ __forceinline__ void epilogue(floatx16 (&acc)[CF::TN][CF::TM], uint8_t *smem, bool loader, int m0,
+                                             int n0, int wave, int M, int N, int, int) const {
+        constexpr int TN = CF::TN, TM = CF::TM, NWV = CF::WM * CF::WN;
+        constexpr int GROW = TN * 64 + 16;  // slab row of G: TN * 32 channels
+        constexpr int TROW = 64 + 16;       // slab row of G^T: 32 tokens
+        constexpr int SLAB = (32 * GROW > TN * 32 * TROW) ? 32 * GROW : TN * 32 * TROW;
+        static_assert(SLAB * NWV <= SMEM, "slabs must fit in the stage ring");
+        const int lane = threadIdx.x & 63, h = lane >> 5, r = lane & 31;
+        const int wm = wave % CF::WM, wn = wave / CF::WM;
+        const int mw = m0 + wm * TM * 32, nw = n0 + wn * TN * 32;
+        uint8_t *slab = smem + wave * SLAB;
+        const float most = scale[0];
+#pragma unroll
+        for (int tm = 0; tm < TM; ++tm) {
+            __syncthreads();  // the stage buffers, or the slab of the block before, have been read
+            uint64_t v[TN][4];
+            if (!loader) {
+                const int m = mw + tm * 32 + r;
+                int at = -1;  // the target's place among this lane's channels
+                float s = 0.0f, ref = 0.0f;
+                if (m < M) {
+                    const int64_t t = target[m];
+                    if (t != ignore) {
+                        s = most > 0.0f ? dloss[m] / most * kGradScale<T> : dloss[m] * 0.0f;
+                        if (t < 0 || t >= V) s = __builtin_nanf("");
+                        ref = lse[m];
+                        const int64_t u = t - v0 - nw;
+                        if (u >= 0 && u < TN * 32) at = int(u) - 4 * h;
+                    }
+                }
+                const bool live = m < M && (s != 0.0f);
+#pragma unroll
+                for (int tn = 0; tn < TN; ++tn)
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        T e[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const int c = tn * 32 + 8 * q + i;
+                            const float p = exp_of(acc[tn][tm][4 * q + i] - ref) - (c == at ? 1.0f : 0.0f);
+                            e[i] = T(live && nw + c + 4 * h < N ? p * s : 0.0f);
+                        }
+                        __builtin_memcpy(&v[tn][q], e, 8);
+                        *reinterpret_cast<uint64_t *>(slab + r * GROW + (tn * 32 + q * 8 + h * 4) * 2) = v[tn][q];
+                    }
+            }
+            __syncthreads();
+            if (!loader) {
+                constexpr int CPR = TN * 4, RPI = 64 / CPR;  // 16-byte pieces a row, rows an instruction
+#pragma unroll
+                for (int i = 0; i < 32 / RPI; ++i) {
+                    const int row = i * RPI + lane / CPR, ch = lane % CPR;
+                    const int m = mw + tm * 32 + row, n = nw + ch * 8;
+                    const u32x4 o = *reinterpret_cast<const u32x4 *>(slab + row * GROW + ch * 16);
+                    if (m < M && n < ldg) st16(g + int64_t(m) * ldg + n, o);
+                }
+            }
+            __syncthreads();
+            if (!loader) {
+#pragma unroll
+                for (int tn = 0; tn < TN; ++tn)
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            *reinterpret_cast<uint16_t *>(slab + (tn * 32 + q * 8 + h * 4 + i) * TROW + r * 2) =
+                                uint16_t(v[tn][q] >> (16 * i));
+            }
+            __syncthreads();
+            if (!loader) {
+#pragma unroll
+                for (int i = 0; i < TN * 2; ++i) {
+                    const int row = i * 16 + lane / 4, ch = lane % 4;
+                    const int n = nw + row, m = mw + tm * 32 + ch * 8;
+                    const u32x4 o = *reinterpret_cast<const u32x4 *>(slab + row * TROW + ch * 16);
+                    if (n < N && m < mp) st16(gt + int64_t(n) * mp + m, o);
+                }
+            }
+        }
+    }
+};
+
+// ---- epilogue of the two gradient products: out = T((acc + sum so far) * scale),
+// or, between the pieces, the fp32 sum alone.
+template <class T>
+struct LossOut {
+    static constexpr bool kAfter = false, kEpilogue = true;
+    const float *scale;  // [1]: largest |dloss| / kGradScale
+    const float *prev;   // fp32 [M][lda] or null
+    float *next;         // fp32 [M][lda] (may be prev), or null: out is written
+    T *out;
+    int64_t ldo;
+    int lda;
+    bool wide;  // out's rows take 16-byte stores
+
+    template <class CF, int SMEM>
+    __device__ __forceinline__ void epilogue(floatx16 (&acc)[CF::TN][CF::TM], uint8_t *smem, bool loader, int m0,
+                                             int n0, int wave, int M, int N, int, int) const {
+        constexpr int TN = CF::TN, TM = CF::TM, NWV = CF::WM * CF::WN;
+        constexpr int TP = TN > 2 ? 2 : TN;  // channel blocks a pass
+        constexpr int ROW = TP * 32 + 4;
+        static_assert(32 * ROW * 4 * NWV <= SMEM && TN % TP == 0, "slabs must fit in the stage ring");
+        const int lane = threadIdx.x & 63, h = lane >> 5, r = lane & 31;
+        const int wm = wave % CF::WM, wn = wave / CF::WM;
+        const int mw = m0 + wm * TM * 32, nw = n0 + wn * TN * 32;
+        float *slab = reinterpret_cast<float *>(smem) + wave * 32 * ROW;
+        const float f = scale[1];
+#pragma unroll
+        for (int tm = 0; tm < TM; ++tm)
+#pragma unroll
+            for (int tp = 0; tp < TN; tp += TP) {
+                __syncthreads();
+                if (!loader) {
+#pragma unroll
+                    for (int tn = 0; tn < TP; ++tn)
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            const floatx16 &a = acc[tp + tn][tm];
+                            *reinterpret_cast<floatx4 *>(slab + r * ROW + tn * 32 + q * 8 + h * 4) =
+                                floatx4{a[4 * q], a[4 * q + 1], a[4 * q + 2], a[4 * q + 3]};
+                        }
+                }
+                __syncthreads();
+                if (loader) continue;
+                constexpr int CPR = TP * 4, RPI = 64 / CPR;  // pieces of 8 values a row
+#pragma unroll
+                for (int i = 0; i < 32 / RPI; ++i) {
+                    const int row = i * RPI + lane / CPR, ch = lane % CPR * 8;
+                    const int m = mw + tm * 32 + row, n = nw + tp * 32 + ch;
+                    if (m >= M || n >= N) continue;
+                    float v[8];
+                    __builtin_memcpy(v, slab + row * ROW + ch, 32);
+                    if (prev) {  // (padded to a multiple of 64 columns)
+                        float p[8];
+                        __builtin_memcpy(p, prev + int64_t(m) * lda + n, 32);
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) v[j] += p[j];
+                    }
+                    if (next) {
+                        __builtin_memcpy(next + int64_t(m) * lda + n, v, 32);
+                        continue;
+                    }
+                    T *o = out + int64_t(m) * ldo + n;
+                    if (wide && n + 8 <= N) {
+                        typename Elem<T>::Vec t;
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) t[j] = T(v[j] * f);
+                        __builtin_nontemporal_store(__builtin_bit_cast(u32x4, t), reinterpret_cast<u32x4 *>(o));
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 8; ++j)
+                            if (n + j < N) o[j] = T(v[j] * f);
+                    }
+                }
+            }
+    }
+};
+
+// ---- copies.  Rows to a contiguous copy of dp columns, zeros past D.
+__global__ void __launch_bounds__(256)
+loss_pack_kernel(const uint16_t *__restrict__ src, int64_t ld, uint16_t *__restrict__ dst, int64_t rows, int D,
+                 int dp) {
+    const int64_t pieces = rows * (dp / 8);
+    for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < pieces; i += int64_t(gridDim.x) * 256) {
+        const int64_t m = i / (dp / 8);
+        const int c = int(i % (dp / 8)) * 8;
+        typename Elem<_Float16>::Vec v = {};
+        if (c < D) v = load_raw(reinterpret_cast<const _Float16 *>(src) + m * ld, c, D);
+        st16(dst + m * dp + c, __builtin_bit_cast(u32x4, v));
+    }
+}
+
+// src [P][ld] (Q columns) -> dst [Q][pp], zeros for rows P..pp; 64 x 64 tiles
+// through LDS.  ld and pp are multiples of 8 and src is 16-byte aligned.
+__global__ void __launch_bounds__(256)
+loss_transpose_kernel(const uint16_t *__restrict__ src, int64_t ld, uint16_t *__restrict__ dst, int P, int Q, int pp) {
+    __shared__ uint16_t s[64][72];
+    const int tq = (Q + 63) / 64;
+    const int p0 = int(blockIdx.x) / tq * 64, q0 = int(blockIdx.x) % tq * 64;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int row = i * 32 + threadIdx.x / 8, c = threadIdx.x % 8 * 8;
+        u32x4 v = {0, 0, 0, 0};
+        if (p0 + row < P && q0 + c < Q) v = ld16(src + int64_t(p0 + row) * ld + q0 + c);
+        *reinterpret_cast<u32x4 *>(&s[row][c]) = v;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int col = i * 32 + threadIdx.x / 8, r = threadIdx.x % 8 * 8;
+        if (q0 + col >= Q || p0 + r >= pp) continue;
+        u32x4 v;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[j] = uint32_t(s[r + 2 * j][col]) | (uint32_t(s[r + 2 * j + 1][col]) << 16);
+        st16(dst + int64_t(q0 + col) * pp + p0 + r, v);
+    }
+}
+
+__global__ void __launch_bounds__(256)
+loss_zero_kernel(uint16_t *__restrict__ dst, int64_t ld, int64_t rows, int D) {
+    for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < rows * D; i += int64_t(gridDim.x) * 256)
+        dst[i / D * ld + i % D] = 0;
+}
+
+// out[0] = largest |dloss| of the rows that count, out[1] = out[0] / div.
+__global__ void __launch_bounds__(1024)
+loss_scale_kernel(const float *__restrict__ dloss, const int64_t *__restrict__ target, int64_t ignore, int M,
+                  float div, float *__restrict__ out) {
+    __shared__ float red[16];
+    float top = 0.0f;
+#pragma unroll 4
+    for (int m = threadIdx.x; m < M; m += 1024)
+        if (target[m] != ignore) top = fmaxf(top, fabsf(dloss[m]));
+#pragma unroll
+    for (int d = 32; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor(top, d, 64));
+    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = top;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        for (int i = 1; i < 16; ++i) top = fmaxf(top, red[i]);
+        out[0] = top;
+        out[1] = top / div;
+    }
+}
+
+template <int KIND, class CF, class Extra>
+hipError_t product_cfg(const void *A, const void *W, const Extra &ex, int64_t M, int64_t N, int64_t K,
+                       hipStream_t st) {
+    using LY = Layout<KIND, CF>;
+    const int nb = int((M + LY::BM - 1) / LY::BM * ((N + LY::BN - 1) / LY::BN));
+    hipLaunchKernelGGL((gemm_kernel<KIND, EPI_F16, CF, Extra>), dim3(nb), dim3(LY::NT), 0, st,
+                       static_cast<const uint8_t *>(A), static_cast<const uint8_t *>(W), nullptr, nullptr, nullptr,
+                       nullptr, int(M), int(N), int(K), int(K / (64 * CF::DK)), ex);
+    return hipGetLastError();
+}
+
+// A [M][K] . W [N][K]^T with an epilogue; K a multiple of 64.  Tiles of
+// 256 x 256 once they give three quarters of the CUs one each, else 128 x 128,
+// else 64 x 64.
+template <class T, class Extra>
+hipError_t product(const void *A, const void *W, const Extra &ex, int64_t M, int64_t N, int64_t K, hipStream_t st) {
+    constexpr int KIND = __is_same(T, _Float16) ? DENSE_F16 : DENSE_BF16;
+    if (tiles(int(M), int(N), 256, 256) >= 192) return product_cfg<KIND, CfgBigDense<true>>(A, W, ex, M, N, K, st);
+    if (tiles(int(M), int(N), 128, 128) >= 96)
+        return product_cfg<KIND, CfgSmallP<true, false, 0>>(A, W, ex, M, N, K, st);
+    return product_cfg<KIND, CfgT64<true, false>>(A, W, ex, M, N, K, st);
+}
+
+int64_t loss_tile_n(int64_t M, int64_t N) {
+    if (tiles(int(M), int(N), 256, 256) >= 192) return 256;
+    return tiles(int(M), int(N), 128, 128) >= 96 ? 128 : 64;
+}
+
+// The operands as the products take them: contiguous rows of dp columns.
+hipError_t operands(const Loss &a, const LossPlan &pl, const void **x, const void **w, hipStream_t st) {
+    *x = a.x;
+    *w = a.w;
+    uint8_t *ws = static_cast<uint8_t *>(a.ws);
+    auto pack = [&](const void *src, int64_t ld, int64_t at, int64_t rows) {
+        const int64_t blocks = (rows * (pl.dp / 8) + 255) / 256;
+        hipLaunchKernelGGL(loss_pack_kernel, dim3(int(blocks < 4096 ? blocks : 4096)), dim3(256), 0, st,
+                           static_cast<const uint16_t *>(src), ld, reinterpret_cast<uint16_t *>(ws + at), rows,
+                           int(a.D), int(pl.dp));
+        return hipGetLastError();
+    };
+    hipError_t e = hipSuccess;
+    if (pl.pack_x) {
+        if ((e = pack(a.x, a.ldx, pl.x, a.M)) != hipSuccess) return e;
+        *x = ws + pl.x;
+    }
+    if (pl.pack_w) {
+        if ((e = pack(a.w, a.ldw, pl.w, a.V)) != hipSuccess) return e;
+        *w = ws + pl.w;
+    }
+    return e;
+}
+
+template <class T>
+hipError_t fwd(const Loss &a, const LossPlan &pl, hipStream_t st) {
+    const void *x, *w;
+    hipError_t e = operands(a, pl, &x, &w, st);
+    if (e != hipSuccess) return e;
+    uint8_t *ws = static_cast<uint8_t *>(a.ws);
+    float *part = reinterpret_cast<float *>(ws + pl.part), *logit = reinterpret_cast<float *>(ws + pl.logit);
+    int tile0 = 0;
+    for (int64_t v0 = 0; v0 < a.V; v0 += pl.piece) {
+        const int64_t n = a.V - v0 < pl.piece ? a.V - v0 : pl.piece;
+        const LossStats ex{a.target, part, logit, v0, tile0};
+        e = product<T>(x, static_cast<const T *>(w) + v0 * pl.dp, ex, a.M, n, pl.dp, st);
+        if (e != hipSuccess) return e;
+        const int64_t bn = loss_tile_n(a.M, n);
+        tile0 += int((n + bn - 1) / bn);
+    }
+    hipLaunchKernelGGL(loss_rows_kernel, dim3(int((a.M + 63) / 64)), dim3(1024), 0, st, part, logit, a.target, a.ignore,
+                       tile0, a.V, int(a.M), a.loss, a.lse);
+    return hipGetLastError();
+}
+
+template <class T>
+hipError_t bwd(const Loss &a, const LossPlan &pl, hipStream_t st) {
+    uint8_t *ws = static_cast<uint8_t *>(a.ws);
+    T *xt = reinterpret_cast<T *>(ws + pl.xt), *wt = reinterpret_cast<T *>(ws + pl.wt);
+    T *g = reinterpret_cast<T *>(ws + pl.g), *gt = reinterpret_cast<T *>(ws + pl.gt);
+    float *acc = reinterpret_cast<float *>(ws + pl.acc), *scale = reinterpret_cast<float *>(ws + pl.scale);
+    const int M = int(a.M), D = int(a.D), mp = int(pl.mp), dp = int(pl.dp);
+    if (M == 0) {  // no rows: no gradient
+        hipLaunchKernelGGL(loss_zero_kernel, dim3(2048), dim3(256), 0, st, static_cast<uint16_t *>(a.dw), a.lddw, a.V, D);
+        return hipGetLastError();
+    }
+    const void *x, *w;
+    hipError_t e = operands(a, pl, &x, &w, st);
+    if (e != hipSuccess) return e;
+    auto transpose = [&](const void *src, int64_t ld, T *dst, int P, int Q, int pp) {
+        hipLaunchKernelGGL(loss_transpose_kernel, dim3((pp + 63) / 64 * ((Q + 63) / 64)), dim3(256), 0, st,
+                           static_cast<const uint16_t *>(src), ld, reinterpret_cast<uint16_t *>(dst), P, Q, pp);
+        return hipGetLastError();
+    };
+    hipLaunchKernelGGL(loss_scale_kernel, dim3(1), dim3(1024), 0, st, a.dloss, a.target, a.ignore, M, kGradScale<T>,
+                       scale);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+    if ((e = transpose(x, dp, xt, M, D, mp)) != hipSuccess) return e;
+    const bool wide_x = a.lddx % 8 == 0 && (reinterpret_cast<uintptr_t>(a.dx) & 15) == 0;
+    const bool wide_w = a.lddw % 8 == 0 && (reinterpret_cast<uintptr_t>(a.dw) & 15) == 0;
+    for (int64_t v0 = 0; v0 < a.V; v0 += pl.piece) {
+        const int64_t n = a.V - v0 < pl.piece ? a.V - v0 : pl.piece;
+        const int ldg = int((n + 63) / 64 * 64);
+        const bool first = v0 == 0, last = v0 + n == a.V;
+        const T *wv = static_cast<const T *>(w) + v0 * dp;
+        const LossGrad<T> grad{a.target, a.ignore, a.V, v0, a.dloss, a.lse, scale, g, gt, ldg, mp};
+        if ((e = product<T>(x, wv, grad, M, n, dp, st)) != hipSuccess) return e;
+        if ((e = transpose(wv, dp, wt, int(n), D, ldg)) != hipSuccess) return e;
+        const LossOut<T> to_x{scale, first ? nullptr : acc, last ? nullptr : acc, static_cast<T *>(a.dx), a.lddx, dp,
+                              wide_x};
+        if ((e = product<T>(g, wt, to_x, M, D, ldg, st)) != hipSuccess) return e;
+        const LossOut<T> to_w{scale, nullptr, nullptr, static_cast<T *>(a.dw) + v0 * a.lddw, a.lddw, dp, wide_w};
+        if ((e = product<T>(gt, xt, to_w, n, D, mp, st)) != hipSuccess) return e;
+    }
+    return hipSuccess;
+}
+
+}  // namespace
+
+LossPlan loss_plan(int64_t M, int64_t V, int64_t D, bool pack_x, bool pack_w, bool backward) {
+    auto up = [](int64_t v, int64_t to) { return (v + to - 1) / to * to; };
+    LossPlan p{};
+    p.dp = up(D, 64);
+    p.mp = up(M > 0 ? M : 1, 64);
+    p.pack_x = pack_x;
+    p.pack_w = pack_w;
+    int64_t at = 0;
+    auto take = [&](int64_t bytes) {
+        const int64_t o = at;
+        at += up(bytes, 256);
+        return o;
+    };
+    if (pack_x) p.x = take(M * p.dp * 2);
+    if (pack_w) p.w = take(V * p.dp * 2);
+    if (!backward) {
+        // pieces only where w passes the products' 4 GiB
+        p.piece = (int64_t(4000) << 20) / (p.dp * 2) / 256 * 256;
+        if (p.piece > V) p.piece = V;
+        p.tiles = 0;
+        for (int64_t v0 = 0; v0 < V; v0 += p.piece) {
+            const int64_t n = V - v0 < p.piece ? V - v0 : p.piece;
+            const int64_t bn = loss_tile_n(M, n);
+            p.tiles += (n + bn - 1) / bn;
+        }
+        p.part = take(p.tiles * M * 8);
+        p.logit = take(M * 4);
+    } else {
+        // pieces of equal size whose G, both ways round, takes at most 256 MiB
+        // (but at least 2048 entries)
+        int64_t most = (int64_t(256) << 20) / (4 * p.mp) / 256 * 256;
+        if (most < 2048) most = 2048;
+        const int64_t reach = (int64_t(4000) << 20) / (p.dp * 2) / 256 * 256;  // the products' 4 GiB
+        if (most > reach) most = reach;
+        const int64_t pieces = (V + most - 1) / most;
+        p.piece = up((V + pieces - 1) / pieces, 256);
+        if (p.piece > V) p.piece = V;
+        const int64_t ldg = up(p.piece, 64);
+        p.xt = take(D * p.mp * 2);
+        p.wt = take(D * ldg * 2);
+        p.g = take(M * ldg * 2);
+        p.gt = take(p.piece * p.mp * 2);
+        p.acc = p.piece < V ? take(M * p.dp * 4) : at;
+        p.scale = take(8);
+    }
+    p.total = at;
+    return p;
+}
+
+hipError_t launch_loss_fwd(const Loss &a, const LossPlan &pl, hipStream_t st) {
+    return a.dtype == DT_F16 ? fwd<_Float16>(a, pl, st) : fwd<__bf16>(a, pl, st);
+}
+hipError_t launch_loss_bwd(const Loss &a, const LossPlan &pl, hipStream_t st) {
+    return a.dtype == DT_F16 ? bwd<_Float16>(a, pl, st) : bwd<__bf16>(a, pl, st);
+}
+
+}  // namespace ssg
