@@ -387,21 +387,46 @@ hipError_t product_cfg(const void *A, const void *W, const Extra &ex, int64_t M,
     return hipGetLastError();
 }
 
-// A [M][K] . W [N][K]^T with an epilogue; K a multiple of 64.  Tiles of
-// 256 x 256 once they give three quarters of the CUs one each, else 128 x 128,
-// else 64 x 64.
-template <class T, class Extra>
-hipError_t product(const void *A, const void *W, const Extra &ex, int64_t M, int64_t N, int64_t K, hipStream_t st) {
-    constexpr int KIND = __is_same(T, _Float16) ? DENSE_F16 : DENSE_BF16;
-    if (tiles(int(M), int(N), 256, 256) >= 192) return product_cfg<KIND, CfgBigDense<true>>(A, W, ex, M, N, K, st);
-    if (tiles(int(M), int(N), 128, 128) >= 96)
-        return product_cfg<KIND, CfgSmallP<true, false, 0>>(A, W, ex, M, N, K, st);
-    return product_cfg<KIND, CfgT64<true, false>>(A, W, ex, M, N, K, st);
+// Tiles of the products.  One workgroup of any but the smallest fills a CU, so a
+// product takes ceil(tiles / 256) rounds, and the tile is the one with the least
+// rounds * cost of a round.  Costs relative to 256 x 256, from bf16 products of
+// M x N x K (MI355X, us for 256 x 256 / 256 x 128 / 128 x 128):
+// 8192 x 32000 x 1024 492 / 635 / 693 (16, 32 and 63 rounds), 6144 x 1024 x 10240
+// 169 / 120 / 145 (1, 1, 2), 10240 x 1024 x 6144 121 / 149 / 140 (1, 2, 3).
+// 256 x 128 has four compute waves of 128 x 64, which read less from LDS per
+// product than 128 x 128's 64 x 64, and four loader waves; without loaders it
+// ran 145-178 in the last two, as eight waves of 64 x 64 127-160; 256 x 256 as
+// four waves of 128 x 128 ran 555 in the first.
+enum LossTile { LT_256, LT_256X128, LT_128, LT_64 };
+using CfgWideP = Cfg<2, 2, 4, 2, 3, 8, true, false, 0, true>;
+
+LossTile loss_tile(int64_t M, int64_t N) {
+    constexpr long kCUs = 256;
+    if (tiles(int(M), int(N), 128, 128) < 96) return LT_64;
+    auto cost = [&](int bm, int bn, long unit) { return (tiles(int(M), int(N), bm, bn) + kCUs - 1) / kCUs * unit; };
+    const long c256 = cost(256, 256, 100), c2128 = cost(256, 128, 68), c128 = cost(128, 128, 41);
+    if (c256 <= c2128 && c256 <= c128) return LT_256;
+    return c2128 <= c128 ? LT_256X128 : LT_128;
 }
 
 int64_t loss_tile_n(int64_t M, int64_t N) {
-    if (tiles(int(M), int(N), 256, 256) >= 192) return 256;
-    return tiles(int(M), int(N), 128, 128) >= 96 ? 128 : 64;
+    switch (loss_tile(M, N)) {
+        case LT_256: return 256;
+        case LT_64: return 64;
+        default: return 128;
+    }
+}
+
+// A [M][K] . W [N][K]^T with an epilogue; K a multiple of 64.
+template <class T, class Extra>
+hipError_t product(const void *A, const void *W, const Extra &ex, int64_t M, int64_t N, int64_t K, hipStream_t st) {
+    constexpr int KIND = __is_same(T, _Float16) ? DENSE_F16 : DENSE_BF16;
+    switch (loss_tile(M, N)) {
+        case LT_256: return product_cfg<KIND, CfgBigDense<true>>(A, W, ex, M, N, K, st);
+        case LT_256X128: return product_cfg<KIND, CfgWideP>(A, W, ex, M, N, K, st);
+        case LT_128: return product_cfg<KIND, CfgSmallP<true, false, 0>>(A, W, ex, M, N, K, st);
+        default: return product_cfg<KIND, CfgT64<true, false>>(A, W, ex, M, N, K, st);
+    }
 }
 
 // The operands as the products take them: contiguous rows of dp columns.
@@ -521,9 +546,9 @@ LossPlan loss_plan(int64_t M, int64_t V, int64_t D, bool pack_x, bool pack_w, bo
         p.part = take(p.tiles * M * 8);
         p.logit = take(M * 4);
     } else {
-        // pieces of equal size whose G, both ways round, takes at most 256 MiB
+        // pieces of equal size whose G, both ways round, takes at most 512 MiB
         // (but at least 2048 entries)
-        int64_t most = (int64_t(256) << 20) / (4 * p.mp) / 256 * 256;
+        int64_t most = (int64_t(512) << 20) / (4 * p.mp) / 256 * 256;
         if (most < 2048) most = 2048;
         const int64_t reach = (int64_t(4000) << 20) / (p.dp * 2) / 256 * 256;  // the products' 4 GiB
         if (most > reach) most = reach;
