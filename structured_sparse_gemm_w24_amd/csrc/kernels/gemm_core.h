@@ -283,11 +283,51 @@ struct Layout {
 
 // What a kernel adds to the plain product: Extra::kAfter -- after() runs on the
 // compute waves between the main loop and the epilogue, with the accumulators;
-// Extra::kEpilogue -- epilogue() takes the place of the store to C.  Plain
-// GEMMs have neither.
+// Extra::kEpilogue -- epilogue() takes the place of the store to C; kTransA /
+// kTransW (dense 16-bit kinds) -- the operand lies the other way round, A as
+// [rows_a][lda] and W as [rows_w][ldw] with k along the rows (zeros past the
+// last one), and is read through transposing LDS reads.  Plain GEMMs have none
+// of them.
 struct NoExtra {
-    static constexpr bool kAfter = false, kEpilogue = false;
+    static constexpr bool kAfter = false, kEpilogue = false, kTransA = false, kTransW = false;
 };
+
+template <class Extra>
+__device__ __forceinline__ int lda_of(const Extra &e) {
+    if constexpr (Extra::kTransA) return e.lda;
+    else return 0;
+}
+template <class Extra>
+__device__ __forceinline__ int ldw_of(const Extra &e) {
+    if constexpr (Extra::kTransW) return e.ldw;
+    else return 0;
+}
+template <class Extra>
+__device__ __forceinline__ uint32_t bytes_a_of(const Extra &e) {
+    if constexpr (Extra::kTransA) return uint32_t(int64_t(e.rows_a) * e.lda * 2);
+    else return 0;
+}
+template <class Extra>
+__device__ __forceinline__ uint32_t bytes_w_of(const Extra &e) {
+    if constexpr (Extra::kTransW) return uint32_t(int64_t(e.rows_w) * e.ldw * 2);
+    else return 0;
+}
+
+// Transposed operand in LDS: 16-byte chunk of a row of `chunks` chunks.  One
+// transposing fragment read takes 64 bytes of rows k..k+3 and k+8..k+11: the
+// first four fall into distinct quarters of the banks.
+__device__ __forceinline__ int swzk(int row, int col, int chunks) { return col ^ ((4 * (row & 3)) & (chunks - 1)); }
+
+// Eight consecutive k of one column from a [k][column] image: lane j of a
+// 16-lane group points at row j/4 and columns 4 (j%4).., and receives column j
+// of rows 0..3; the second read takes the four rows after them.
+__device__ __forceinline__ u32x4 lds_tr8(const uint8_t *p, int row_bytes) {
+    typedef short s16x4 __attribute__((ext_vector_type(4)));
+    typedef __attribute__((address_space(3))) s16x4 *lds_s4;
+    const u32x2 lo = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4)(p)));
+    const u32x2 hi = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4)(p + 4 * row_bytes)));
+    return u32x4{lo.x, lo.y, hi.x, hi.y};
+}
 
 template <int KIND, int EPI, class CF, class Extra>
 __global__ void __launch_bounds__(CF::WM *CF::WN * 64 * (CF::PROD ? 2 : 1))
@@ -354,15 +394,25 @@ gemm_kernel(const uint8_t *__restrict__ A, const uint8_t *__restrict__ Wv, const
 #pragma unroll
     for (int j = 0; j < LY::LA; ++j) {
         const int byte = (j * LY::NL + wave) * 1024 + lane * 16;
-        const int row = byte / LY::AB, pos = (byte / 16) % (LY::AB / 16);
-        oa[j] = uint32_t(min(m0 + row, M - 1)) * uint32_t(a_row) + swzw<LY::AB>(row, pos) * 16;
+        if constexpr (Extra::kTransA) {  // (columns past M: finite or not, they stay in rows that are not stored)
+            const int row = byte / (BM * 2), pos = (byte / 16) % (BM / 8);
+            oa[j] = uint32_t(row) * uint32_t(extra.lda * 2) + uint32_t(m0 * 2) + swzk(row, pos, BM / 8) * 16;
+        } else {
+            const int row = byte / LY::AB, pos = (byte / 16) % (LY::AB / 16);
+            oa[j] = uint32_t(min(m0 + row, M - 1)) * uint32_t(a_row) + swzw<LY::AB>(row, pos) * 16;
+        }
     }
     uint32_t ow[LY::LW];
 #pragma unroll
     for (int j = 0; j < LY::LW; ++j) {
         const int byte = (j * LY::NL + wave) * 1024 + lane * 16;
-        const int row = byte / WB, pos = (byte / 16) % (WB / 16);
-        ow[j] = uint32_t(min(n0 + row, N - 1)) * uint32_t(w_row) + swzw<WB>(row, pos) * 16;
+        if constexpr (Extra::kTransW) {
+            const int row = byte / (BN * 2), pos = (byte / 16) % (BN / 8);
+            ow[j] = uint32_t(row) * uint32_t(extra.ldw * 2) + uint32_t(n0 * 2) + swzk(row, pos, BN / 8) * 16;
+        } else {
+            const int row = byte / WB, pos = (byte / 16) % (WB / 16);
+            ow[j] = uint32_t(min(n0 + row, N - 1)) * uint32_t(w_row) + swzw<WB>(row, pos) * 16;
+        }
     }
     uint32_t om[LY::LM > 0 ? LY::LM : 1];
 #pragma unroll
@@ -384,8 +434,11 @@ gemm_kernel(const uint8_t *__restrict__ A, const uint8_t *__restrict__ Wv, const
     // (ROT in the tile configurations below).
     const int rot = CF::ROT ? b % S : 0;
     // (the host caps A and W below 4 GiB, so every byte count fits 32 bits)
-    const __amdgpu_buffer_rsrc_t bufA = buffer_of(A, uint32_t(int64_t(M) * a_row));
-    const __amdgpu_buffer_rsrc_t bufW = buffer_of(Wv, uint32_t(int64_t(N) * w_row));
+    // (transposed operands end with their last row: a partial last stage reads zeros past it)
+    const __amdgpu_buffer_rsrc_t bufA =
+        buffer_of(A, Extra::kTransA ? bytes_a_of(extra) : uint32_t(int64_t(M) * a_row));
+    const __amdgpu_buffer_rsrc_t bufW =
+        buffer_of(Wv, Extra::kTransW ? bytes_w_of(extra) : uint32_t(int64_t(N) * w_row));
     const __amdgpu_buffer_rsrc_t bufM = buffer_of(meta_b, KT::kSparse ? uint32_t(int64_t(N) * m_row * 4) : 0u);
     // Part t - (c - 1) * MP - 1 of metadata block c = ceil(t / MP), loaded
     // with the loads of stage t (t < 0: the prologue's parts of block 0).
@@ -418,10 +471,10 @@ gemm_kernel(const uint8_t *__restrict__ A, const uint8_t *__restrict__ Wv, const
         const int sg = ks0 + ((s + rot < S) ? s + rot : s + rot - S);  // global K stage
 #pragma unroll
         for (int j = 0; j < LY::LA; ++j)
-            dma16(bufA, oa[j] + uint32_t(sg * LY::AB), base + (j * LY::NL + wave) * 1024);
+            dma16(bufA, oa[j] + (Extra::kTransA ? uint32_t(sg) * uint32_t(lda_of(extra) * 128) : uint32_t(sg * LY::AB)), base + (j * LY::NL + wave) * 1024);
 #pragma unroll
         for (int j = 0; j < LY::LW; ++j)
-            dma16(bufW, ow[j] + uint32_t(sg * WB), base + A_STAGE + (j * LY::NL + wave) * 1024);
+            dma16(bufW, ow[j] + (Extra::kTransW ? uint32_t(sg) * uint32_t(ldw_of(extra) * 128) : uint32_t(sg * WB)), base + A_STAGE + (j * LY::NL + wave) * 1024);
         if constexpr (LY::MP == 0) {
 #pragma unroll
             for (int j = 0; j < LY::LM; ++j)
@@ -438,6 +491,11 @@ gemm_kernel(const uint8_t *__restrict__ A, const uint8_t *__restrict__ Wv, const
         uint32_t idx[TN];
         u32x8 a[TM];
     };
+    // byte of a [k][column] stage that this lane points at for k-step kk, block column `row`
+    [[maybe_unused]] auto tr_at = [&](int row, int kk, int columns) {
+        const int k = 16 * kk + 8 * h + ((lane & 15) >> 2), col = row - (r & 15) + 4 * (lane & 3);
+        return k * (columns * 2) + swzk(k, col >> 3, columns / 8) * 16 + (col & 7) * 2;
+    };
     auto load_frag = [&](int s, int kk, Frag &F) {
         const uint8_t *bA = smem + (s % NB) * STAGE;
         const uint8_t *bW = bA + A_STAGE;
@@ -449,7 +507,8 @@ gemm_kernel(const uint8_t *__restrict__ A, const uint8_t *__restrict__ Wv, const
 #pragma unroll
         for (int tn = 0; tn < TN; ++tn) {
             const int row = wn * TN * 32 + tn * 32 + r;
-            F.w[tn] = lds16(bW + row * WB + swzw<WB>(row, 2 * kk + h) * 16);
+            if constexpr (!Extra::kTransW) F.w[tn] = lds16(bW + row * WB + swzw<WB>(row, 2 * kk + h) * 16);
+            else F.w[tn] = lds_tr8(bW + tr_at(row, kk, BN), BN * 2);
             if constexpr (LY::MP > 0 && KIND == W24_F16) F.idx[tn] = bB[LY::mword(row, q + kk)] >> (16 * h);
             else if constexpr (LY::MP > 0 && KIND == W24_I8) F.idx[tn] = bB[LY::mword(row, q + 2 * kk + h)];
             else if constexpr (KIND == W24_F16) F.idx[tn] = bM[row * MW + kk] >> (16 * h);
@@ -464,6 +523,9 @@ gemm_kernel(const uint8_t *__restrict__ A, const uint8_t *__restrict__ Wv, const
                 const u32x4 lo = lds16(bA + row * LY::AB + swzw<LY::AB>(row, 4 * kk + h) * 16);
                 const u32x4 hi = lds16(bA + row * LY::AB + swzw<LY::AB>(row, 4 * kk + 2 + h) * 16);
                 F.a[tm] = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+            } else if constexpr (Extra::kTransA) {
+                const u32x4 lo = lds_tr8(bA + tr_at(row, kk, BM), BM * 2);
+                F.a[tm] = __builtin_shufflevector(lo, lo, 0, 1, 2, 3, 0, 1, 2, 3);
             } else {
                 const u32x4 lo = lds16(bA + row * LY::AB + swzw<LY::AB>(row, 2 * kk + h) * 16);
                 F.a[tm] = __builtin_shufflevector(lo, lo, 0, 1, 2, 3, 0, 1, 2, 3);
@@ -485,7 +547,7 @@ gemm_kernel(const uint8_t *__restrict__ A, const uint8_t *__restrict__ Wv, const
     };
     // Interleave hint: one matrix instruction, then its share of LDS reads.
     constexpr int NMMA = TN * TM;
-    constexpr int NRD = TN * (KT::kSparse ? 2 : 1) + TM * (KT::kSparse ? 2 : 1);
+    constexpr int NRD = TN * (KT::kSparse || Extra::kTransW ? 2 : 1) + TM * (KT::kSparse || Extra::kTransA ? 2 : 1);
     constexpr int RPM = (NRD + NMMA - 1) / NMMA;
     auto interleave = [&]() {
 #pragma unroll

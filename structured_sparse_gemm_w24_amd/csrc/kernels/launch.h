@@ -150,11 +150,10 @@ struct Loss {
 // Pieces of the vocabulary and byte offsets in the workspace.
 struct LossPlan {
     int64_t dp;      // D rounded up to the products' step of 64
-    int64_t mp;      // M likewise
     bool pack_x, pack_w;
     int64_t piece;   // vocabulary entries of a piece
     int64_t tiles;   // forward: tiles of the vocabulary
-    int64_t x, w, part, logit, xt, wt, g, gt, acc, scale, total;
+    int64_t x, w, part, logit, g, acc, scale, total;
 };
 LossPlan loss_plan(int64_t M, int64_t V, int64_t D, bool pack_x, bool pack_w, bool backward);
 hipError_t launch_loss_fwd(const Loss &a, const LossPlan &pl, hipStream_t st);

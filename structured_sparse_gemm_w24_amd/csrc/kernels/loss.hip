@@ -8,17 +8,18 @@
 //
 // Bound by the matrix units: 2 M V D operations forward, 6 M V D backward (the
 // logits once more, and the two products).  All products run on the GEMM
-// skeleton (gemm_core.h), whose operands are both contiguous along the summed
-// axis, with epilogues of their own:
+// skeleton (gemm_core.h) with epilogues of their own:
 //   * forward, each tile reduces its logits to a maximum and a sum of
 //     exponentials per row in registers and writes those 8 bytes a row; a second
 //     launch merges a row's tiles in order;
 //   * backward works through the vocabulary in pieces.  For a piece, the first
-//     product's epilogue turns the logits into G, and writes it both ways
-//     round, [M][piece] and [piece][M]: the operands of dx += G w and of
-//     dw[piece] = G^T x.  w's piece and x are transposed once for the same reason
-//     (reading w or x against its grain inside the products would cost them their
-//     direct-to-LDS loads).  dx is summed over the pieces in fp32.
+//     product's epilogue turns the logits into G [M][piece]; then dx += G w and
+//     dw[piece] = G^T x.  What these sum over runs along the rows of w, of G and
+//     of x, so they read those operands through transposing LDS reads as they
+//     lie (with 256 x 128 tiles that is as fast as reading along the rows:
+//     6144 x 1024 x 10240 bf16 126 us either way, both operands so 130;
+//     transposed copies, and G written both ways round, cost 250 of 1365 us at
+//     6144 x 30001 x 1024).  dx is summed over the pieces in fp32.
 // G is rounded to the operands' 16 bits, as the products need it; its rows are
 // divided by the largest |dloss| first (and, fp16, multiplied by 2^12, so that a
 // probability of 2^-26 is still a normal number), which the products' outputs
@@ -49,7 +50,7 @@ __device__ __forceinline__ void merge(float &m, float &s, float m2, float s2) {
 
 // ---- forward epilogue: a tile's statistics and the targets' logits.
 struct LossStats {
-    static constexpr bool kAfter = false, kEpilogue = true;
+    static constexpr bool kAfter = false, kEpilogue = true, kTransA = false, kTransW = false;
     const int64_t *target;
     float *part;   // [tiles][M][2]
     float *logit;  // [M]
@@ -140,24 +141,22 @@ loss_rows_kernel(const float *__restrict__ part, const float *__restrict__ logit
     }
 }
 
-// ---- backward epilogue: logits to G, written [M][ldg] and transposed [N][mp],
-// zeros in the padding of both.
+// ---- backward epilogue: logits to G [M][ldg], zeros past the last channel.
 template <class T>
 struct LossGrad {
-    static constexpr bool kAfter = false, kEpilogue = true;
+    static constexpr bool kAfter = false, kEpilogue = true, kTransA = false, kTransW = false;
     const int64_t *target;
     int64_t ignore, V, v0;
     const float *dloss, *lse, *scale;  // scale[0] = largest |dloss|
-    T *g, *gt;
-    int ldg, mp;
+    T *g;
+    int ldg;
 
     template <class CF, int SMEM>
     __device__ __forceinline__ void epilogue(floatx16 (&acc)[CF::TN][CF::TM], uint8_t *smem, bool loader, int m0,
                                              int n0, int wave, int M, int N, int, int) const {
         constexpr int TN = CF::TN, TM = CF::TM, NWV = CF::WM * CF::WN;
-        constexpr int GROW = TN * 64 + 16;  // slab row of G: TN * 32 channels
-        constexpr int TROW = 64 + 16;       // slab row of G^T: 32 tokens
-        constexpr int SLAB = (32 * GROW > TN * 32 * TROW) ? 32 * GROW : TN * 32 * TROW;
+        constexpr int GROW = TN * 64 + 16;  // slab row: TN * 32 channels
+        constexpr int SLAB = 32 * GROW;
         static_assert(SLAB * NWV <= SMEM, "slabs must fit in the stage ring");
         const int lane = threadIdx.x & 63, h = lane >> 5, r = lane & 31;
         const int wm = wave % CF::WM, wn = wave / CF::WM;
@@ -167,7 +166,6 @@ struct LossGrad {
 #pragma unroll
         for (int tm = 0; tm < TM; ++tm) {
             __syncthreads();  // the stage buffers, or the slab of the block before, have been read
-            uint64_t v[TN][4];
             if (!loader) {
                 const int m = mw + tm * 32 + r;
                 int at = -1;  // the target's place among this lane's channels
@@ -194,41 +192,18 @@ struct LossGrad {
                             const float p = exp_of(acc[tn][tm][4 * q + i] - ref) - (c == at ? 1.0f : 0.0f);
                             e[i] = T(live && nw + c + 4 * h < N ? p * s : 0.0f);
                         }
-                        __builtin_memcpy(&v[tn][q], e, 8);
-                        *reinterpret_cast<uint64_t *>(slab + r * GROW + (tn * 32 + q * 8 + h * 4) * 2) = v[tn][q];
+                        __builtin_memcpy(slab + r * GROW + (tn * 32 + q * 8 + h * 4) * 2, e, 8);
                     }
             }
             __syncthreads();
-            if (!loader) {
-                constexpr int CPR = TN * 4, RPI = 64 / CPR;  // 16-byte pieces a row, rows an instruction
+            if (loader) continue;
+            constexpr int CPR = TN * 4, RPI = 64 / CPR;  // 16-byte pieces a row, rows an instruction
 #pragma unroll
-                for (int i = 0; i < 32 / RPI; ++i) {
-                    const int row = i * RPI + lane / CPR, ch = lane % CPR;
-                    const int m = mw + tm * 32 + row, n = nw + ch * 8;
-                    const u32x4 o = *reinterpret_cast<const u32x4 *>(slab + row * GROW + ch * 16);
-                    if (m < M && n < ldg) st16(g + int64_t(m) * ldg + n, o);
-                }
-            }
-            __syncthreads();
-            if (!loader) {
-#pragma unroll
-                for (int tn = 0; tn < TN; ++tn)
-#pragma unroll
-                    for (int q = 0; q < 4; ++q)
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            *reinterpret_cast<uint16_t *>(slab + (tn * 32 + q * 8 + h * 4 + i) * TROW + r * 2) =
-                                uint16_t(v[tn][q] >> (16 * i));
-            }
-            __syncthreads();
-            if (!loader) {
-#pragma unroll
-                for (int i = 0; i < TN * 2; ++i) {
-                    const int row = i * 16 + lane / 4, ch = lane % 4;
-                    const int n = nw + row, m = mw + tm * 32 + ch * 8;
-                    const u32x4 o = *reinterpret_cast<const u32x4 *>(slab + row * TROW + ch * 16);
-                    if (n < N && m < mp) st16(gt + int64_t(n) * mp + m, o);
-                }
+            for (int i = 0; i < 32 / RPI; ++i) {
+                const int row = i * RPI + lane / CPR, ch = lane % CPR;
+                const int m = mw + tm * 32 + row, n = nw + ch * 8;
+                const u32x4 o = *reinterpret_cast<const u32x4 *>(slab + row * GROW + ch * 16);
+                if (m < M && n < ldg) st16(g + int64_t(m) * ldg + n, o);
             }
         }
     }
@@ -236,15 +211,18 @@ struct LossGrad {
 
 // ---- epilogue of the two gradient products: out = T((acc + sum so far) * scale),
 // or, between the pieces, the fp32 sum alone.
-template <class T>
+// w (and, TA, the first operand too) has k along its rows.
+template <class T, bool TA>
 struct LossOut {
-    static constexpr bool kAfter = false, kEpilogue = true;
+    static constexpr bool kAfter = false, kEpilogue = true, kTransA = TA, kTransW = true;
+    int lda, rows_a;  // (TA)
+    int ldw, rows_w;
     const float *scale;  // [1]: largest |dloss| / kGradScale
-    const float *prev;   // fp32 [M][lda] or null
-    float *next;         // fp32 [M][lda] (may be prev), or null: out is written
+    const float *prev;   // fp32 [M][ldp] or null
+    float *next;         // fp32 [M][ldp] (may be prev), or null: out is written
     T *out;
     int64_t ldo;
-    int lda;
+    int ldp;
     bool wide;  // out's rows take 16-byte stores
 
     template <class CF, int SMEM>
@@ -286,12 +264,12 @@ struct LossOut {
                     __builtin_memcpy(v, slab + row * ROW + ch, 32);
                     if (prev) {  // (padded to a multiple of 64 columns)
                         float p[8];
-                        __builtin_memcpy(p, prev + int64_t(m) * lda + n, 32);
+                        __builtin_memcpy(p, prev + int64_t(m) * ldp + n, 32);
 #pragma unroll
                         for (int j = 0; j < 8; ++j) v[j] += p[j];
                     }
                     if (next) {
-                        __builtin_memcpy(next + int64_t(m) * lda + n, v, 32);
+                        __builtin_memcpy(next + int64_t(m) * ldp + n, v, 32);
                         continue;
                     }
                     T *o = out + int64_t(m) * ldo + n;
@@ -321,32 +299,6 @@ loss_pack_kernel(const uint16_t *__restrict__ src, int64_t ld, uint16_t *__restr
         typename Elem<_Float16>::Vec v = {};
         if (c < D) v = load_raw(reinterpret_cast<const _Float16 *>(src) + m * ld, c, D);
         st16(dst + m * dp + c, __builtin_bit_cast(u32x4, v));
-    }
-}
-
-// src [P][ld] (Q columns) -> dst [Q][pp], zeros for rows P..pp; 64 x 64 tiles
-// through LDS.  ld and pp are multiples of 8 and src is 16-byte aligned.
-__global__ void __launch_bounds__(256)
-loss_transpose_kernel(const uint16_t *__restrict__ src, int64_t ld, uint16_t *__restrict__ dst, int P, int Q, int pp) {
-    __shared__ uint16_t s[64][72];
-    const int tq = (Q + 63) / 64;
-    const int p0 = int(blockIdx.x) / tq * 64, q0 = int(blockIdx.x) % tq * 64;
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const int row = i * 32 + threadIdx.x / 8, c = threadIdx.x % 8 * 8;
-        u32x4 v = {0, 0, 0, 0};
-        if (p0 + row < P && q0 + c < Q) v = ld16(src + int64_t(p0 + row) * ld + q0 + c);
-        *reinterpret_cast<u32x4 *>(&s[row][c]) = v;
-    }
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const int col = i * 32 + threadIdx.x / 8, r = threadIdx.x % 8 * 8;
-        if (q0 + col >= Q || p0 + r >= pp) continue;
-        u32x4 v;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) v[j] = uint32_t(s[r + 2 * j][col]) | (uint32_t(s[r + 2 * j + 1][col]) << 16);
-        st16(dst + int64_t(q0 + col) * pp + p0 + r, v);
     }
 }
 
@@ -383,7 +335,7 @@ hipError_t product_cfg(const void *A, const void *W, const Extra &ex, int64_t M,
     const int nb = int((M + LY::BM - 1) / LY::BM * ((N + LY::BN - 1) / LY::BN));
     hipLaunchKernelGGL((gemm_kernel<KIND, EPI_F16, CF, Extra>), dim3(nb), dim3(LY::NT), 0, st,
                        static_cast<const uint8_t *>(A), static_cast<const uint8_t *>(W), nullptr, nullptr, nullptr,
-                       nullptr, int(M), int(N), int(K), int(K / (64 * CF::DK)), ex);
+                       nullptr, int(M), int(N), int(K), int((K + 63) / 64), ex);
     return hipGetLastError();
 }
 
@@ -397,31 +349,40 @@ hipError_t product_cfg(const void *A, const void *W, const Extra &ex, int64_t M,
 // product than 128 x 128's 64 x 64, and four loader waves; without loaders it
 // ran 145-178 in the last two, as eight waves of 64 x 64 127-160; 256 x 256 as
 // four waves of 128 x 128 ran 555 in the first.
+// The transposing reads cost 256 x 256 more (10240 x 1024 x 6144 121 -> 141, 15104 x
+// 1024 x 6144 147 -> 160, where 256 x 128 takes 149 -> 158 and 165 -> 176).
 enum LossTile { LT_256, LT_256X128, LT_128, LT_64 };
 using CfgWideP = Cfg<2, 2, 4, 2, 3, 8, true, false, 0, true>;
 
-LossTile loss_tile(int64_t M, int64_t N) {
+// Rounds times cost of the best tile, and the tile.
+long loss_cost(int64_t M, int64_t N, bool trans, LossTile *tile) {
     constexpr long kCUs = 256;
-    if (tiles(int(M), int(N), 128, 128) < 96) return LT_64;
     auto cost = [&](int bm, int bn, long unit) { return (tiles(int(M), int(N), bm, bn) + kCUs - 1) / kCUs * unit; };
-    const long c256 = cost(256, 256, 100), c2128 = cost(256, 128, 68), c128 = cost(128, 128, 41);
-    if (c256 <= c2128 && c256 <= c128) return LT_256;
-    return c2128 <= c128 ? LT_256X128 : LT_128;
+    const long c256 = cost(256, 256, trans ? 115 : 100), c2128 = cost(256, 128, 68), c128 = cost(128, 128, 41);
+    if (tiles(int(M), int(N), 128, 128) < 96) *tile = LT_64;
+    else if (c256 <= c2128 && c256 <= c128) *tile = LT_256;
+    else *tile = c2128 <= c128 ? LT_256X128 : LT_128;
+    return c256 < c2128 ? (c256 < c128 ? c256 : c128) : (c2128 < c128 ? c2128 : c128);
+}
+LossTile loss_tile(int64_t M, int64_t N, bool trans) {
+    LossTile t;
+    loss_cost(M, N, trans, &t);
+    return t;
 }
 
 int64_t loss_tile_n(int64_t M, int64_t N) {
-    switch (loss_tile(M, N)) {
+    switch (loss_tile(M, N, false)) {
         case LT_256: return 256;
         case LT_64: return 64;
         default: return 128;
     }
 }
 
-// A [M][K] . W [N][K]^T with an epilogue; K a multiple of 64.
+// A [M][K] . W [N][K]^T with an epilogue; K a multiple of 64 unless both are transposed.
 template <class T, class Extra>
 hipError_t product(const void *A, const void *W, const Extra &ex, int64_t M, int64_t N, int64_t K, hipStream_t st) {
     constexpr int KIND = __is_same(T, _Float16) ? DENSE_F16 : DENSE_BF16;
-    switch (loss_tile(M, N)) {
+    switch (loss_tile(M, N, Extra::kTransW)) {
         case LT_256: return product_cfg<KIND, CfgBigDense<true>>(A, W, ex, M, N, K, st);
         case LT_256X128: return product_cfg<KIND, CfgWideP>(A, W, ex, M, N, K, st);
         case LT_128: return product_cfg<KIND, CfgSmallP<true, false, 0>>(A, W, ex, M, N, K, st);
@@ -477,10 +438,9 @@ hipError_t fwd(const Loss &a, const LossPlan &pl, hipStream_t st) {
 template <class T>
 hipError_t bwd(const Loss &a, const LossPlan &pl, hipStream_t st) {
     uint8_t *ws = static_cast<uint8_t *>(a.ws);
-    T *xt = reinterpret_cast<T *>(ws + pl.xt), *wt = reinterpret_cast<T *>(ws + pl.wt);
-    T *g = reinterpret_cast<T *>(ws + pl.g), *gt = reinterpret_cast<T *>(ws + pl.gt);
+    T *g = reinterpret_cast<T *>(ws + pl.g);
     float *acc = reinterpret_cast<float *>(ws + pl.acc), *scale = reinterpret_cast<float *>(ws + pl.scale);
-    const int M = int(a.M), D = int(a.D), mp = int(pl.mp), dp = int(pl.dp);
+    const int M = int(a.M), D = int(a.D), dp = int(pl.dp);
     if (M == 0) {  // no rows: no gradient
         hipLaunchKernelGGL(loss_zero_kernel, dim3(2048), dim3(256), 0, st, static_cast<uint16_t *>(a.dw), a.lddw, a.V, D);
         return hipGetLastError();
@@ -488,15 +448,9 @@ hipError_t bwd(const Loss &a, const LossPlan &pl, hipStream_t st) {
     const void *x, *w;
     hipError_t e = operands(a, pl, &x, &w, st);
     if (e != hipSuccess) return e;
-    auto transpose = [&](const void *src, int64_t ld, T *dst, int P, int Q, int pp) {
-        hipLaunchKernelGGL(loss_transpose_kernel, dim3((pp + 63) / 64 * ((Q + 63) / 64)), dim3(256), 0, st,
-                           static_cast<const uint16_t *>(src), ld, reinterpret_cast<uint16_t *>(dst), P, Q, pp);
-        return hipGetLastError();
-    };
     hipLaunchKernelGGL(loss_scale_kernel, dim3(1), dim3(1024), 0, st, a.dloss, a.target, a.ignore, M, kGradScale<T>,
                        scale);
     if ((e = hipGetLastError()) != hipSuccess) return e;
-    if ((e = transpose(x, dp, xt, M, D, mp)) != hipSuccess) return e;
     const bool wide_x = a.lddx % 8 == 0 && (reinterpret_cast<uintptr_t>(a.dx) & 15) == 0;
     const bool wide_w = a.lddw % 8 == 0 && (reinterpret_cast<uintptr_t>(a.dw) & 15) == 0;
     for (int64_t v0 = 0; v0 < a.V; v0 += pl.piece) {
@@ -504,14 +458,14 @@ hipError_t bwd(const Loss &a, const LossPlan &pl, hipStream_t st) {
         const int ldg = int((n + 63) / 64 * 64);
         const bool first = v0 == 0, last = v0 + n == a.V;
         const T *wv = static_cast<const T *>(w) + v0 * dp;
-        const LossGrad<T> grad{a.target, a.ignore, a.V, v0, a.dloss, a.lse, scale, g, gt, ldg, mp};
+        const LossGrad<T> grad{a.target, a.ignore, a.V, v0, a.dloss, a.lse, scale, g, ldg};
         if ((e = product<T>(x, wv, grad, M, n, dp, st)) != hipSuccess) return e;
-        if ((e = transpose(wv, dp, wt, int(n), D, ldg)) != hipSuccess) return e;
-        const LossOut<T> to_x{scale, first ? nullptr : acc, last ? nullptr : acc, static_cast<T *>(a.dx), a.lddx, dp,
-                              wide_x};
-        if ((e = product<T>(g, wt, to_x, M, D, ldg, st)) != hipSuccess) return e;
-        const LossOut<T> to_w{scale, nullptr, nullptr, static_cast<T *>(a.dw) + v0 * a.lddw, a.lddw, dp, wide_w};
-        if ((e = product<T>(gt, xt, to_w, n, D, mp, st)) != hipSuccess) return e;
+        const LossOut<T, false> to_x{0, 0, dp, int(n), scale, first ? nullptr : acc, last ? nullptr : acc,
+                                     static_cast<T *>(a.dx), a.lddx, dp, wide_x};
+        if ((e = product<T>(g, wv, to_x, M, D, ldg, st)) != hipSuccess) return e;
+        const LossOut<T, true> to_w{ldg, M, dp, M, scale, nullptr, nullptr,
+                                    static_cast<T *>(a.dw) + v0 * a.lddw, a.lddw, dp, wide_w};
+        if ((e = product<T>(g, x, to_w, n, D, M, st)) != hipSuccess) return e;
     }
     return hipSuccess;
 }
@@ -522,7 +476,6 @@ LossPlan loss_plan(int64_t M, int64_t V, int64_t D, bool pack_x, bool pack_w, bo
     auto up = [](int64_t v, int64_t to) { return (v + to - 1) / to * to; };
     LossPlan p{};
     p.dp = up(D, 64);
-    p.mp = up(M > 0 ? M : 1, 64);
     p.pack_x = pack_x;
     p.pack_w = pack_w;
     int64_t at = 0;
@@ -546,20 +499,34 @@ LossPlan loss_plan(int64_t M, int64_t V, int64_t D, bool pack_x, bool pack_w, bo
         p.part = take(p.tiles * M * 8);
         p.logit = take(M * 4);
     } else {
-        // pieces of equal size whose G, both ways round, takes at most 512 MiB
-        // (but at least 2048 entries)
-        int64_t most = (int64_t(512) << 20) / (4 * p.mp) / 256 * 256;
+        // pieces of about equal size whose G takes at most 256 MiB (but at least
+        // 2048 entries): of the counts from the least one on, the one whose products
+        // fill their rounds best
+        int64_t most = (int64_t(256) << 20) / (2 * (M > 0 ? M : 1)) / 256 * 256;
         if (most < 2048) most = 2048;
         const int64_t reach = (int64_t(4000) << 20) / (p.dp * 2) / 256 * 256;  // the products' 4 GiB
         if (most > reach) most = reach;
-        const int64_t pieces = (V + most - 1) / most;
-        p.piece = up((V + pieces - 1) / pieces, 256);
+        const int64_t least = (V + most - 1) / most;
+        double best = 0.0;
+        for (int64_t pieces = least; pieces < least + 6; ++pieces) {
+            const int64_t n = up((V + pieces - 1) / pieces, 256);
+            double cost = 0.0;
+            LossTile t;
+            for (int64_t v0 = 0; v0 < V; v0 += n) {
+                const int64_t q = V - v0 < n ? V - v0 : n;
+                cost += double(loss_cost(M, q, false, &t)) * p.dp + double(loss_cost(M, D, true, &t)) * q +
+                        double(loss_cost(q, D, true, &t)) * M;
+                cost += 32768.0;  // three launches, about 10 us
+                if (q == n && v0 + 2 * n < V) {  // the other full pieces cost the same
+                    const int64_t more = (V - v0) / n - 1;
+                    cost *= double(more + 1);
+                    v0 += more * n;
+                }
+            }
+            if (pieces == least || cost < best) best = cost, p.piece = n;
+        }
         if (p.piece > V) p.piece = V;
-        const int64_t ldg = up(p.piece, 64);
-        p.xt = take(D * p.mp * 2);
-        p.wt = take(D * ldg * 2);
-        p.g = take(M * ldg * 2);
-        p.gt = take(p.piece * p.mp * 2);
+        p.g = take(M * up(p.piece, 64) * 2);
         p.acc = p.piece < V ? take(M * p.dp * 4) : at;
         p.scale = take(8);
     }

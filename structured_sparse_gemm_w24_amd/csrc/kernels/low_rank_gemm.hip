@@ -11,7 +11,7 @@
 namespace ssg {
 
 struct LowRankAfter {
-    static constexpr bool kAfter = true, kEpilogue = false;
+    static constexpr bool kAfter = true, kEpilogue = false, kTransA = false, kTransW = false;
     const _Float16 *up, *low;
     const int32_t *index, *ranks;
     int adapters, R;
