@@ -281,8 +281,9 @@ struct Layout {
     }
 };
 
-// What a kernel adds to the plain product: Extra::kAfter -- after() runs on the
-// compute waves between the main loop and the epilogue, with the accumulators;
+// What a kernel adds to the plain product: Extra::kAfter -- index[M] is fetched
+// to LDS ahead of the first stage, and after() runs on the compute waves between
+// the main loop and the epilogue, with the accumulators and the tile's indices;
 // Extra::kEpilogue -- epilogue() takes the place of the store to C; kTransA /
 // kTransW (dense 16-bit kinds) -- the operand lies the other way round, A as
 // [rows_a][lda] and W as [rows_w][ldw] with k along the rows (zeros past the
@@ -352,6 +353,7 @@ gemm_kernel(const uint8_t *__restrict__ A, const uint8_t *__restrict__ Wv, const
     constexpr int SMEM = (SMEM_MAIN > SMEM_EPI) ? SMEM_MAIN : SMEM_EPI;
 
     __shared__ __attribute__((aligned(1024))) uint8_t smem[SMEM];
+    __shared__ int32_t s_index[Extra::kAfter ? BM < 64 ? 64 : BM : 1];
 
     const int tid = threadIdx.x;
     const int lane = tid & 63;
@@ -563,6 +565,13 @@ gemm_kernel(const uint8_t *__restrict__ A, const uint8_t *__restrict__ Wv, const
     // instructions; the stage hand-off (wait + barrier) sits before the last
     // k-step's instructions so that the next stage's first fragments overlap
     // them too.
+    if constexpr (Extra::kAfter) {
+        // (the oldest loads of their waves, so the first stage's wait covers them; zeros past M)
+        const __amdgpu_buffer_rsrc_t bufI = buffer_of(extra.index, uint32_t(M) * 4u);
+        if ((!PROD || loader) && wave < (BM + 63) / 64)
+            for (int j = wave; j < (BM + 63) / 64; j += LY::NW)
+                dma4(bufI, uint32_t(m0 + j * 64 + lane) * 4u, reinterpret_cast<uint8_t *>(s_index + j * 64));
+    }
     if (!PROD || loader) {
         if constexpr (LY::MP > 1)
             for (int t = 1 - LY::MP; t < 0; ++t) issue_meta(t);
@@ -615,7 +624,7 @@ gemm_kernel(const uint8_t *__restrict__ A, const uint8_t *__restrict__ Wv, const
     }
 
     if constexpr (Extra::kAfter) {
-        if (!loader) extra.template after<CF>(acc, m0 + wm * TM * 32, n0 + wn * TN * 32, M, N);
+        if (!loader) extra.template after<CF>(acc, s_index + wm * TM * 32, m0 + wm * TM * 32, n0 + wn * TN * 32, M, N);
     }
     if constexpr (Extra::kEpilogue) {
         extra.template epilogue<CF, SMEM>(acc, smem, loader, m0, n0, wave, M, N, tile_m, tile_n);

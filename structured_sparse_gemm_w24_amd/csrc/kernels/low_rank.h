@@ -75,13 +75,14 @@ __device__ __forceinline__ int low_rank_of(const int32_t *ranks, int a, int R) {
 
 // Adds up[a] . low to accumulators of 32x32 blocks: acc[tn][tm] holds, for the
 // 32 tokens from mw + 32 tm, the channels nw + 32 tn + 8 (i/4) + 4 h + i%4 of
-// token lane%32.  Up rows hold `upn` channels; channels past the last repeat
-// it (their results are not stored).
+// token lane%32.  at[i]: index of token mw + i (anything past M).  Channels past
+// the last repeat it (their results are not stored).
 // The wave visits the distinct adapters of its tokens one after another, each
-// with the other tokens' low values zeroed.
+// with the other tokens' low values zeroed, 32 rank slots at a time: the loads
+// of a turn wait for one another only, not for the adapter's rank.
 template <class T, int TN, int TM>
 __device__ __forceinline__ void low_rank_expand(floatx16 (&acc)[TN][TM], const T *__restrict__ up,
-                                                const T *__restrict__ low, const int32_t *__restrict__ index,
+                                                const T *__restrict__ low, const int32_t *at,
                                                 const int32_t *__restrict__ ranks, int adapters, int R, int mw, int nw,
                                                 int M, int N) {
     const int lane = threadIdx.x & 63, h = lane >> 5, r = lane & 31;
@@ -90,8 +91,8 @@ __device__ __forceinline__ void low_rank_expand(floatx16 (&acc)[TN][TM], const T
     bool todo[TM];
 #pragma unroll
     for (int tm = 0; tm < TM; ++tm) {
-        const int m = mw + tm * 32 + r;
-        mine[tm] = m < M ? index[m] : -1;
+        mine[tm] = at[tm * 32 + r];
+        if (mw + tm * 32 + r >= M) mine[tm] = -1;
         todo[tm] = mine[tm] >= 0 && mine[tm] < adapters;
         if (mine[tm] != -1 && !todo[tm]) {
 #pragma unroll
@@ -112,31 +113,42 @@ __device__ __forceinline__ void low_rank_expand(floatx16 (&acc)[TN][TM], const T
             }
             const int rank = low_rank_of(ranks, a, R);
             const T *pool = up + int64_t(a) * N * R;
-            for (int k0 = 0; k0 < rank; k0 += 16) {
-                const int k = k0 + 8 * h;
-                u32x4 w[TN], hi[TM], lo[TM];
+            for (int k0 = 0; k0 < R; k0 += 32) {
+                u32x4 w[2][TN], hi[2][TM], lo[2][TM];
 #pragma unroll
-                for (int tn = 0; tn < TN; ++tn) {
-                    const int n = min(nw + tn * 32 + r, N - 1);
-                    w[tn] = u32x4{0, 0, 0, 0};
-                    if (k < rank) w[tn] = keep16(ld16(pool + int64_t(n) * R + k), rank - k);
-                }
-#pragma unroll
-                for (int tm = 0; tm < TM; ++tm) {
-                    hi[tm] = lo[tm] = u32x4{0, 0, 0, 0};
-                    if (sel[tm] && k < rank) {
-                        const T *row = low + int64_t(mw + tm * 32 + r) * R + k;
-                        hi[tm] = ld16(row);
-                        lo[tm] = ld16(row + plane);
-                    }
-                }
-#pragma unroll
-                for (int tm = 0; tm < TM; ++tm) {
-                    const u32x4 l = lo_unscaled<T>(lo[tm]);
+                for (int s = 0; s < 2; ++s) {
+                    const int k = k0 + 16 * s + 8 * h;
 #pragma unroll
                     for (int tn = 0; tn < TN; ++tn) {
-                        acc[tn][tm] = mfma32<T>(w[tn], hi[tm], acc[tn][tm]);
-                        acc[tn][tm] = mfma32<T>(w[tn], l, acc[tn][tm]);
+                        const int n = min(nw + tn * 32 + r, N - 1);
+                        w[s][tn] = u32x4{0, 0, 0, 0};
+                        if (k < R) w[s][tn] = ld16(pool + int64_t(n) * R + k);
+                    }
+#pragma unroll
+                    for (int tm = 0; tm < TM; ++tm) {
+                        hi[s][tm] = lo[s][tm] = u32x4{0, 0, 0, 0};
+                        if (sel[tm] && k < R) {
+                            const T *row = low + int64_t(mw + tm * 32 + r) * R + k;
+                            hi[s][tm] = ld16(row);
+                            lo[s][tm] = ld16(row + plane);
+                        }
+                    }
+                }
+                if (k0 >= rank) break;  // (after the loads: the rank itself comes from memory)
+#pragma unroll
+                for (int s = 0; s < 2; ++s) {
+                    const int k = k0 + 16 * s;
+                    if (k >= rank) break;
+#pragma unroll
+                    for (int tn = 0; tn < TN; ++tn) w[s][tn] = keep16(w[s][tn], rank - k - 8 * h);
+#pragma unroll
+                    for (int tm = 0; tm < TM; ++tm) {
+                        const u32x4 l = lo_unscaled<T>(lo[s][tm]);
+#pragma unroll
+                        for (int tn = 0; tn < TN; ++tn) {
+                            acc[tn][tm] = mfma32<T>(w[s][tn], hi[s][tm], acc[tn][tm]);
+                            acc[tn][tm] = mfma32<T>(w[s][tn], l, acc[tn][tm]);
+                        }
                     }
                 }
             }

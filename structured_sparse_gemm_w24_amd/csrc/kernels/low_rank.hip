@@ -26,103 +26,121 @@ using namespace tw_detail;
 // Source of padding in direct-to-LDS loads.
 __device__ __attribute__((aligned(256))) uint16_t g_low_zero[128];
 
-// ---- shrink.  A workgroup takes 16 * TT tokens, its four waves every fourth
+// ---- shrink.  A workgroup takes 16 tokens, its NW waves every NW-th
 // 64-wide slice of K; v_mfma 16x16x32 with the rank slots as rows and the
 // tokens as columns (lane: row / column lane%16, k = 8 (lane/16)..; results:
 // rows 4 (lane/16) + i of column lane%16).  The waves' sums are added in order
 // through LDS.  RB: blocks of 16 rank slots.
-template <class T, int TT, int RB>
+// Two of a tile's adapters are taken at a time, on the same x values, so that a
+// tile where one request ends and the next begins costs no second pass; the
+// first x values are fetched before the indices are known.
+template <class T, int RB, int NW>
 __device__ __forceinline__ void shrink_tile(const T *__restrict__ x, int64_t ldx, const T *__restrict__ down,
                                             const float *__restrict__ scale, const int32_t *__restrict__ ranks,
                                             const int32_t *__restrict__ index, int adapters, int R,
                                             T *__restrict__ low, int M, int K, int tile, floatx4 *part) {
+    constexpr int UNROLL = RB <= 2 ? 4 : RB == 4 ? 2 : 1;  // 64-wide slices of K in flight
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int g = lane >> 4, c = lane & 15;
-    const int m0 = tile * 16 * TT;
-    // every wave finds the distinct adapters of the same tokens, in the same order
-    int mine = -1;
-    if (lane < 16 * TT && m0 + lane < M) mine = index[m0 + lane];
-    bool todo = mine >= 0 && mine < adapters;
-    int tok_a[TT];
+    const int m = tile * 16 + c;
+    const int step = NW * 64 * UNROLL;
+    const T *row = x + int64_t(m) * ldx;
+    u32x4 xv[UNROLL][2];
+    auto fetch_x = [&](int k0) {
 #pragma unroll
-    for (int t = 0; t < TT; ++t) tok_a[t] = __shfl(mine, t * 16 + c, 64);
-    for (uint64_t left = __ballot(todo); left; left = __ballot(todo)) {
-        const int a = __builtin_amdgcn_readlane(mine, __builtin_ctzll(left));
-        todo = todo && mine != a;
-        const int rank = low_rank_of(ranks, a, R);
-        const T *pool = down + int64_t(a) * R * K;
-        floatx4 acc[TT][RB];
-#pragma unroll
-        for (int t = 0; t < TT; ++t)
-#pragma unroll
-            for (int b = 0; b < RB; ++b) acc[t][b] = floatx4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll 2
-        for (int k0 = wave * 64; k0 < K; k0 += 256) {
-            u32x4 xv[2][TT], dv[2][RB];
+        for (int u = 0; u < UNROLL; ++u)
 #pragma unroll
             for (int s = 0; s < 2; ++s) {
-                const int k = k0 + 32 * s + 8 * g;
-#pragma unroll
-                for (int t = 0; t < TT; ++t) {
-                    xv[s][t] = u32x4{0, 0, 0, 0};
-                    if (k < K && tok_a[t] == a) xv[s][t] = ld16(x + int64_t(m0 + t * 16 + c) * ldx + k);
-                }
-#pragma unroll
-                for (int b = 0; b < RB; ++b) {
-                    dv[s][b] = u32x4{0, 0, 0, 0};
-                    if (k < K && b * 16 + c < rank) dv[s][b] = ld16(pool + int64_t(b * 16 + c) * K + k);
-                }
+                const int k = k0 + u * NW * 64 + 32 * s + 8 * g;
+                xv[u][s] = u32x4{0, 0, 0, 0};
+                if (k < K && m < M) xv[u][s] = ld16(row + k);
             }
+    };
+    fetch_x(wave * 64);
+    // every wave finds the distinct adapters of the same tokens, in the same order
+    const int mine = m < M ? index[m] : -1;  // (each token in four lanes)
+    bool todo = mine >= 0 && mine < adapters;
+    bool held = true;  // xv holds the first slices
+    for (uint64_t left = __ballot(todo); left; left = __ballot(todo)) {
+        const int a0 = __builtin_amdgcn_readlane(mine, __builtin_ctzll(left));
+        todo = todo && mine != a0;
+        left = __ballot(todo);
+        const int a1 = left ? __builtin_amdgcn_readlane(mine, __builtin_ctzll(left)) : -1;
+        todo = todo && mine != a1;
+        const int rank0 = low_rank_of(ranks, a0, R), rank1 = a1 >= 0 ? low_rank_of(ranks, a1, R) : 0;
+        const float s0 = scale ? scale[a0] : 1.0f, s1 = scale && a1 >= 0 ? scale[a1] : 1.0f;
+        const T *pool0 = down + int64_t(a0) * R * K, *pool1 = down + int64_t(a1 < 0 ? 0 : a1) * R * K;
+        floatx4 acc[2][RB];
 #pragma unroll
-            for (int s = 0; s < 2; ++s)
+        for (int b = 0; b < RB; ++b) acc[0][b] = acc[1][b] = floatx4{0.f, 0.f, 0.f, 0.f};
+        auto product = [&](const T *pool, int rank, int a, floatx4 (&to)[RB], int k0) {
+            u32x4 dv[UNROLL][2][RB];
 #pragma unroll
-                for (int b = 0; b < RB; ++b)
+            for (int u = 0; u < UNROLL; ++u)
 #pragma unroll
-                    for (int t = 0; t < TT; ++t) acc[t][b] = mfma16<T>(dv[s][b], xv[s][t], acc[t][b]);
+                for (int s = 0; s < 2; ++s)
+#pragma unroll
+                    for (int b = 0; b < RB; ++b) {
+                        const int k = k0 + u * NW * 64 + 32 * s + 8 * g;
+                        dv[u][s][b] = u32x4{0, 0, 0, 0};
+                        if (k < K && b * 16 + c < rank) dv[u][s][b] = ld16(pool + int64_t(b * 16 + c) * K + k);
+                    }
+#pragma unroll
+            for (int u = 0; u < UNROLL; ++u)
+#pragma unroll
+                for (int s = 0; s < 2; ++s) {
+                    const u32x4 v = mine == a ? xv[u][s] : u32x4{0, 0, 0, 0};
+#pragma unroll
+                    for (int b = 0; b < RB; ++b) to[b] = mfma16<T>(dv[u][s][b], v, to[b]);
+                }
+        };
+        for (int k0 = wave * 64; k0 < K; k0 += step) {
+            if (!held) fetch_x(k0);
+            held = K <= step;
+            product(pool0, rank0, a0, acc[0], k0);
+            if (a1 >= 0) product(pool1, rank1, a1, acc[1], k0);
         }
-        __syncthreads();  // (the previous adapter's sums have been read)
+        __syncthreads();  // (the previous adapters' sums have been read)
 #pragma unroll
-        for (int t = 0; t < TT; ++t)
-#pragma unroll
-            for (int b = 0; b < RB; ++b) part[((t * RB + b) * 4 + wave) * 64 + lane] = acc[t][b];
+        for (int b = 0; b < RB; ++b) {
+            part[(b * NW + wave) * 64 + lane] = acc[0][b];
+            if (a1 >= 0) part[((RB + b) * NW + wave) * 64 + lane] = acc[1][b];
+        }
         __syncthreads();
-        const float s = scale ? scale[a] : 1.0f;
-        for (int q = wave; q < TT * RB; q += 4) {
-            const int t = q / RB, b = q % RB;
-            floatx4 v = part[(q * 4) * 64 + lane];
+        for (int q = wave; q < (a1 >= 0 ? 2 : 1) * RB; q += NW) {
+            const int b = q % RB, r = b * 16 + 4 * g;
+            const float s = q < RB ? s0 : s1;
+            if (mine != (q < RB ? a0 : a1) || r >= R) continue;
+            floatx4 v = part[(q * NW) * 64 + lane];
 #pragma unroll
-            for (int w = 1; w < 4; ++w) {
-                const floatx4 u = part[(q * 4 + w) * 64 + lane];
+            for (int w = 1; w < NW; ++w) {
+                const floatx4 u = part[(q * NW + w) * 64 + lane];
                 v.x += u.x, v.y += u.y, v.z += u.z, v.w += u.w;
             }
-            const int m = m0 + t * 16 + c, r = b * 16 + 4 * g;
-            const int am = __shfl(mine, t * 16 + c, 64);
-            if (am == a && r < R) {
-                T hi[4], lo[4];
+            T hi[4], lo[4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    // The product is made opaque: the compiler otherwise forms hi a
-                    // second time with a multiply that rounds to fp16 directly, and
-                    // next to a tie the stored hi is then not the one lo was taken from.
-                    float f = v[i] * s;
-                    asm("" : "+v"(f));
-                    hi[i] = T(f);
-                    lo[i] = T((f - float(hi[i])) * LowSplit<T>::kLoScale);
-                }
-                __builtin_memcpy(low + int64_t(m) * R + r, hi, 8);
-                __builtin_memcpy(low + int64_t(M) * R + int64_t(m) * R + r, lo, 8);
+            for (int i = 0; i < 4; ++i) {
+                // The product is made opaque: the compiler otherwise forms hi a
+                // second time with a multiply that rounds to fp16 directly, and
+                // next to a tie the stored hi is then not the one lo was taken from.
+                float f = v[i] * s;
+                asm("" : "+v"(f));
+                hi[i] = T(f);
+                lo[i] = T((f - float(hi[i])) * LowSplit<T>::kLoScale);
             }
+            __builtin_memcpy(low + int64_t(m) * R + r, hi, 8);
+            __builtin_memcpy(low + int64_t(M) * R + int64_t(m) * R + r, lo, 8);
         }
     }
 }
 
-template <class T, int TT, int RB>
-__global__ void __launch_bounds__(256)
+template <class T, int RB, int NW>
+__global__ void __launch_bounds__(NW * 64)
 shrink_kernel(ShrinkTask<T> p, ShrinkTask<T> q, const float *__restrict__ scale, const int32_t *__restrict__ ranks,
               const int32_t *__restrict__ index, int adapters, int R, int M) {
-    __shared__ floatx4 part[TT * RB * 4 * 64];
+    __shared__ floatx4 part[2 * RB * NW * 64];
     const ShrinkTask<T> &w = blockIdx.y ? q : p;
-    shrink_tile<T, TT, RB>(w.x, w.ldx, w.down, scale, ranks, index, adapters, R, w.low, M, w.K, blockIdx.x, part);
+    shrink_tile<T, RB, NW>(w.x, w.ldx, w.down, scale, ranks, index, adapters, R, w.low, M, w.K, blockIdx.x, part);
 }
 
 // ---- expand: a workgroup takes 64 tokens x 256 channels, a wave 32 x 128.
@@ -151,7 +169,10 @@ expand_kernel(const T *__restrict__ up, const T *__restrict__ low, const int32_t
     floatx16 acc[TN][1];
 #pragma unroll
     for (int tn = 0; tn < TN; ++tn) acc[tn][0] = floatx16{};
-    if (nw < N) low_rank_expand<T, TN, 1>(acc, up, low, index, ranks, adapters, R, mw, nw, M, N);
+    __shared__ int32_t at[64];
+    if (threadIdx.x < 64) at[threadIdx.x] = int(mw - (wave & 1) * 32 + threadIdx.x) < M ? index[mw - (wave & 1) * 32 + threadIdx.x] : -1;
+    __syncthreads();
+    if (nw < N) low_rank_expand<T, TN, 1>(acc, up, low, at + (wave & 1) * 32, ranks, adapters, R, mw, nw, M, N);
 #pragma unroll
     for (int tn = 0; tn < TN; ++tn)
 #pragma unroll
@@ -281,24 +302,47 @@ pool_transpose_kernel(const T *__restrict__ src0, T *__restrict__ dst0, int P0, 
 // 32 tokens at a time, their z rows and low rows copied to LDS as they lie in
 // memory ([token][column]) and read by transposing LDS reads, which give each
 // lane 8 consecutive tokens of one column (lane i of a 16-lane group receives
-// element i%4 of the 8-byte run read by lane 4e + i/4, e = 0..3).  The high and
-// the low part of `low` have accumulators of their own.  Ranges write fp32
-// slices [range][adapter][R][C] that a second launch sums in order.
+// element i%4 of the 8-byte run read by lane 4e + i/4, e = 0..3).  Three stages
+// are in flight beside the one in use.  The high and the low part of `low` have
+// accumulators of their own.  Ranges write fp32 slices [range][adapter][R][C]
+// that a second launch sums in order; an adapter without tokens in a range
+// writes nothing but its count.
 constexpr int kListCap = 2048;  // tokens of a range, at most
+
+// Two fragments of 8 consecutive tokens a lane: transposing reads of the rows at
+// p (q) and of the rows four below, FOUR bytes on.  Waited for in the same
+// statement: the compiler would place a wait for every load in flight before
+// the builtin form, which it cannot tell apart from the direct-to-LDS loads'
+// stores.
+template <int FOUR>
+__device__ __forceinline__ void read_tr(uint32_t p, uint32_t q, u32x4 &u, u32x4 &v) {
+    u32x2 u0, u1, v0, v1;
+    asm volatile(
+        "ds_read_b64_tr_b16 %0, %4\n\t"
+        "ds_read_b64_tr_b16 %1, %4 offset:%6\n\t"
+        "ds_read_b64_tr_b16 %2, %5\n\t"
+        "ds_read_b64_tr_b16 %3, %5 offset:%6\n\t"
+        "s_waitcnt lgkmcnt(0)"
+        : "=&v"(u0), "=&v"(u1), "=&v"(v0), "=&v"(v1)
+        : "v"(p), "v"(q), "n"(FOUR)
+        : "memory");
+    u = u32x4{u0.x, u0.y, u1.x, u1.y};
+    v = u32x4{v0.x, v0.y, v1.x, v1.y};
+}
 
 template <class T, int RB>
 __global__ void __launch_bounds__(256)
 wgrad_kernel(WgradTask<T> p, WgradTask<T> q, const int32_t *__restrict__ index, int adapters, int R, int M,
-             int range) {
+             int range, int32_t *__restrict__ counts_out) {
     constexpr int RT = RB * 16;                  // rank slots of a stage row
     constexpr int Z_STAGE = 32 * 128 * 2;        // [32][128]
     constexpr int L_STAGE = 32 * RT * 2;         // [32][RT], one part
     constexpr int STAGE = Z_STAGE + 2 * L_STAGE;
-    constexpr int NB = 2;
+    constexpr int NB = 4;
     __shared__ __attribute__((aligned(1024))) uint8_t smem[NB * STAGE];
     __shared__ int32_t list[kListCap];
     __shared__ int counts[4][kListCap / 256];
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const bool second = int(blockIdx.x) >= p.tiles;
     const WgradTask<T> &w = second ? q : p;
     const int c0 = (int(blockIdx.x) - (second ? p.tiles : 0)) * 128;
@@ -330,6 +374,10 @@ wgrad_kernel(WgradTask<T> p, WgradTask<T> q, const int32_t *__restrict__ index, 
         __syncthreads();
     }
     total = __builtin_amdgcn_readfirstlane(total);
+    if (w.part) {
+        if (blockIdx.x == 0 && tid == 0) counts_out[int64_t(blockIdx.z) * adapters + a] = total;
+        if (total == 0) return;
+    }
 
     const int g = lane >> 4, j16 = lane & 15;
     floatx4 acc[2][RB][2];
@@ -361,33 +409,26 @@ wgrad_kernel(WgradTask<T> p, WgradTask<T> q, const int32_t *__restrict__ index, 
         }
     };
     const int S = (total + 31) / 32;
-    typedef short s16x4 __attribute__((ext_vector_type(4)));
-    typedef __attribute__((address_space(3))) s16x4 *lds_s4;
-    // two transposing reads: rows 8 g + j16/4 and four rows on, elements from `at`
-    auto tr = [&](const uint8_t *at, int row_bytes) -> u32x4 {
-        const s16x4 lo4 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4)(at));
-        const s16x4 hi4 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4)(at + 4 * row_bytes));
-        const u32x2 u = __builtin_bit_cast(u32x2, lo4), v = __builtin_bit_cast(u32x2, hi4);
-        return u32x4{u.x, u.y, v.x, v.y};
-    };
-    if (S > 0) issue(0);
+    const uint32_t smem_addr = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(smem));
+    const int per_stage = 2 + (2 * RB - wave + 3) / 4;  // loads of this wave
+    for (int s = 0; s < NB - 1 && s < S; ++s) issue(s);
     for (int s = 0; s < S; ++s) {
-        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-        __syncthreads();  // stage s has landed, and everyone is done with stage s - 1
-        if (s + 1 < S) issue(s + 1);
-        const uint8_t *base = smem + (s % NB) * STAGE;
+        // stage s has landed (younger ones may be in flight), and everyone is done with stage s - 1
+        tw_wait_barrier(min(NB - 2, S - 1 - s) * per_stage);
+        if (s + NB - 1 < S) issue(s + NB - 1);
+        const uint32_t base = smem_addr + (s % NB) * STAGE;
         const int row = 8 * g + (j16 >> 2);
-        u32x4 zv[2], lv[2][RB];
+        uint32_t z_at[2];
 #pragma unroll
         for (int cb = 0; cb < 2; ++cb) {
             const int col = wave * 32 + cb * 16 + 4 * (j16 & 3);
-            zv[cb] = tr(base + row * 256 + ((col >> 3) ^ (2 * (row & 3))) * 16 + (col & 7) * 2, 256);
+            z_at[cb] = base + row * 256 + ((col >> 3) ^ (2 * (row & 3))) * 16 + (col & 7) * 2;
         }
+        const uint32_t l_at = base + Z_STAGE + row * (RT * 2) + 4 * (j16 & 3) * 2;
+        u32x4 zv[2], lv[2][RB];
+        read_tr<1024>(z_at[0], z_at[1], zv[0], zv[1]);
 #pragma unroll
-        for (int part = 0; part < 2; ++part)
-#pragma unroll
-            for (int b = 0; b < RB; ++b)
-                lv[part][b] = tr(base + Z_STAGE + part * L_STAGE + row * (RT * 2) + (b * 16 + 4 * (j16 & 3)) * 2, RT * 2);
+        for (int b = 0; b < RB; ++b) read_tr<RT * 8>(l_at + b * 32, l_at + L_STAGE + b * 32, lv[0][b], lv[1][b]);
 #pragma unroll
         for (int part = 0; part < 2; ++part)
 #pragma unroll
@@ -435,16 +476,18 @@ wgrad_kernel(WgradTask<T> p, WgradTask<T> q, const int32_t *__restrict__ index, 
 template <class T>
 __global__ void __launch_bounds__(256)
 wgrad_sum_kernel(const float *__restrict__ part0, T *__restrict__ out0, int64_t n0, const float *__restrict__ part1,
-                 T *__restrict__ out1, int64_t n1, int slices) {
+                 T *__restrict__ out1, int64_t n1, int slices, const int32_t *__restrict__ counts, int adapters) {
     int64_t i = (int64_t(blockIdx.x) * 256 + threadIdx.x) * 4;
     const float *part = part0;
     T *out = out0;
     int64_t n = n0;
     if (i >= n0) i -= n0, part = part1, out = out1, n = n1;
     if (i >= n) return;
-    floatx4 s = *reinterpret_cast<const floatx4 *>(part + i);
+    const int a = int(i / (n / adapters));
+    floatx4 s = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll 4
-    for (int q = 1; q < slices; ++q) {
+    for (int q = 0; q < slices; ++q) {
+        if (counts[int64_t(q) * adapters + a] == 0) continue;
         const floatx4 v = *reinterpret_cast<const floatx4 *>(part + q * n + i);
         s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
     }
@@ -454,9 +497,10 @@ wgrad_sum_kernel(const float *__restrict__ part0, T *__restrict__ out0, int64_t 
 
 template <class T>
 hipError_t shrink(const ShrinkTask<T> &p, const ShrinkTask<T> *q, const LowRank &lr, int M, hipStream_t st) {
+    constexpr int NW = 8;
     const dim3 grid((M + 15) / 16, q ? 2 : 1);
 #define SSG_SHRINK(RB)                                                                                              \
-    hipLaunchKernelGGL((shrink_kernel<T, 1, RB>), grid, dim3(256), 0, st, p, q ? *q : p, lr.scale, lr.ranks,        \
+    hipLaunchKernelGGL((shrink_kernel<T, RB, NW>), grid, dim3(NW * 64), 0, st, p, q ? *q : p, lr.scale, lr.ranks, \
                        lr.index, lr.adapters, lr.R, M)
     if (lr.R <= 16) SSG_SHRINK(1);
     else if (lr.R <= 32) SSG_SHRINK(2);
@@ -510,13 +554,14 @@ hipError_t bwd(const LowRankBwd &b, hipStream_t st) {
     const int64_t n0 = int64_t(lr.adapters) * R * K, n1 = int64_t(lr.adapters) * R * N;
     float *part0 = pl.slices > 1 ? reinterpret_cast<float *>(ws + pl.part) : nullptr;
     float *part1 = part0 ? part0 + pl.slices * n0 : nullptr;
+    int32_t *counts = reinterpret_cast<int32_t *>(ws + pl.counts);
     const WgradTask<T> p{static_cast<const T *>(b.x), b.ldx, dlow, part0, static_cast<T *>(b.ddown), K, (K + 127) / 128,
                          false};
     const WgradTask<T> q{static_cast<const T *>(b.dy), b.lddy, low, part1, static_cast<T *>(b.dup), N, (N + 127) / 128,
                          true};
     const dim3 grid(p.tiles + q.tiles, lr.adapters, pl.slices);
 #define SSG_WGRAD(RB) \
-    hipLaunchKernelGGL((wgrad_kernel<T, RB>), grid, dim3(256), 0, st, p, q, lr.index, lr.adapters, R, M, pl.range)
+    hipLaunchKernelGGL((wgrad_kernel<T, RB>), grid, dim3(256), 0, st, p, q, lr.index, lr.adapters, R, M, pl.range, counts)
     if (R <= 16) SSG_WGRAD(1);
     else if (R <= 32) SSG_WGRAD(2);
     else if (R <= 64) SSG_WGRAD(4);
@@ -524,7 +569,7 @@ hipError_t bwd(const LowRankBwd &b, hipStream_t st) {
 #undef SSG_WGRAD
     if ((e = hipGetLastError()) != hipSuccess || pl.slices == 1) return e;
     hipLaunchKernelGGL((wgrad_sum_kernel<T>), dim3(int(((n0 + n1) / 4 + 255) / 256)), dim3(256), 0, st, part0,
-                       static_cast<T *>(b.ddown), n0, part1, static_cast<T *>(b.dup), n1, pl.slices);
+                       static_cast<T *>(b.ddown), n0, part1, static_cast<T *>(b.dup), n1, pl.slices, counts, lr.adapters);
     return hipGetLastError();
 }
 
@@ -541,18 +586,24 @@ LowRankPlan low_rank_plan(int adapters, int R, int64_t M, int64_t N, int64_t K) 
     p.low = p.down_t + up256(int64_t(adapters) * R * K * 2);
     p.dlow = p.low + up256(M * R * 4);
     p.part = p.dlow + up256(M * R * 4);
-    // token ranges: enough workgroups to fill the chip, at least 256 tokens each, at most what the list holds
-    const int64_t per = int64_t(adapters) * ((N + 127) / 128 + (K + 127) / 128);
-    int64_t want = (1024 + per - 1) / per;
+    // Token ranges: about 512 workgroups (an adapter's workgroups of a range hold
+    // its tokens only, so the adapters do not add to them), of at least 256 tokens
+    // and at most what the list holds, in at most 256 MiB of slices.
+    const int64_t cols = (N + 127) / 128 + (K + 127) / 128;
+    const int64_t slice = int64_t(adapters) * R * (N + K) * 4;
+    int64_t want = (512 + cols - 1) / cols;
     const int64_t most = M > 256 ? M / 256 : 1;
     if (want > most) want = most;
+    if (want > (int64_t(256) << 20) / slice) want = (int64_t(256) << 20) / slice;
     int64_t range = want > 0 ? (M + want - 1) / want : M;
     range = (range + 31) / 32 * 32;
     if (range > kListCap) range = kListCap;
     if (range < 32) range = 32;
     p.range = int(range);
     p.slices = int(M > 0 ? (M + range - 1) / range : 1);
-    p.total = p.part + (p.slices > 1 ? p.slices * int64_t(adapters) * R * (N + K) * 4 : 0);
+    p.counts = p.part;
+    p.part += up256(int64_t(p.slices) * adapters * 4);
+    p.total = p.part + (p.slices > 1 ? p.slices * slice : 0);
     return p;
 }
 

@@ -17,8 +17,9 @@ struct LowRankAfter {
     int adapters, R;
 
     template <class CF>
-    __device__ __forceinline__ void after(floatx16 (&acc)[CF::TN][CF::TM], int mw, int nw, int M, int N) const {
-        low_rank_expand<_Float16, CF::TN, CF::TM>(acc, up, low, index, ranks, adapters, R, mw, nw, M, N);
+    __device__ __forceinline__ void after(floatx16 (&acc)[CF::TN][CF::TM], const int32_t *at, int mw, int nw, int M,
+                                          int N) const {
+        low_rank_expand<_Float16, CF::TN, CF::TM>(acc, up, low, at, ranks, adapters, R, mw, nw, M, N);
     }
 };
 
