@@ -160,7 +160,7 @@ bool plain_rank(int32_t R) { return R >= 8 && R <= 128 && R % 8 == 0; }
 
 SSG_API int64_t low_rank_workspace_bytes(int64_t M, int32_t R) {
     if (M <= 0 || M > kMaxTokens || !plain_rank(R) || ssg::low_rank_few(int(M))) return 0;
-    return M * R * 4;
+    return ssg::low_rank_bytes(M, R);
 }
 
 SSG_API int low_rank_add(const ssg_low_rank *lr, const void *x, int64_t ldx, const void *base, int64_t ldb, void *out,
@@ -182,7 +182,7 @@ SSG_API int low_rank_add(const ssg_low_rank *lr, const void *x, int64_t ldx, con
 
 SSG_API int64_t w24_low_rank_workspace_bytes(int64_t M, int64_t N, int64_t K, int32_t R) {
     if (M <= 0 || N <= 0 || K <= 0 || !fits_int(M) || !fits_int(N) || !fits_int(K) || !plain_rank(R)) return 0;
-    if (!ssg::low_rank_few(int(M))) return M * R * 4;
+    if (!ssg::low_rank_few(int(M))) return ssg::low_rank_bytes(M, R);
     return int64_t(ssg::low_rank_splits(int(M), int(N), int(K))) * M * N * 4;
 }
 

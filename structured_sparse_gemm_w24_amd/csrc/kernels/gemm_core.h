@@ -282,8 +282,8 @@ struct Layout {
 };
 
 // What a kernel adds to the plain product: Extra::kAfter -- index[M] is fetched
-// to LDS ahead of the first stage, and after() runs on the compute waves between
-// the main loop and the epilogue, with the accumulators and the tile's indices;
+// to LDS ahead of the first stage, and after() runs between the main loop and
+// the epilogue, with the accumulators and the tile's indices;
 // Extra::kEpilogue -- epilogue() takes the place of the store to C; kTransA /
 // kTransW (dense 16-bit kinds) -- the operand lies the other way round, A as
 // [rows_a][lda] and W as [rows_w][ldw] with k along the rows (zeros past the
@@ -624,7 +624,8 @@ gemm_kernel(const uint8_t *__restrict__ A, const uint8_t *__restrict__ Wv, const
     }
 
     if constexpr (Extra::kAfter) {
-        if (!loader) extra.template after<CF>(acc, s_index + wm * TM * 32, m0 + wm * TM * 32, n0 + wn * TN * 32, M, N);
+        __syncthreads();  // (the stage ring is its scratch: every wave is done reading it)
+        extra.template after<CF, SMEM>(acc, s_index, smem, loader, m0, n0, M, N);
     }
     if constexpr (Extra::kEpilogue) {
         extra.template epilogue<CF, SMEM>(acc, smem, loader, m0, n0, wave, M, N, tile_m, tile_n);
@@ -689,6 +690,16 @@ gemm_kernel(const uint8_t *__restrict__ A, const uint8_t *__restrict__ Wv, const
     static_assert(RPI * CPR == kWave, "row segment must tile a wave");
     __syncthreads();  // every wave is done reading the stage buffers
     uint8_t *const Cb = reinterpret_cast<uint8_t *>(C) + (EPI == EPI_PART ? int64_t(blockIdx.y) * M * N * OB : 0);
+    // (with after(), recomputed: the main loop has no register to keep it in)
+    const int row_of_wave = [&]() {
+        if constexpr (Extra::kAfter) {
+            int t = threadIdx.x;
+            asm volatile("" : "+v"(t));
+            return ((t >> 6) % LY::NW) % WM * (TM * 32);
+        } else {
+            return wm * TM * 32;
+        }
+    }();
     uint8_t *ew = smem + wave * EPASS * EWAVE;  // (compute waves)
     const int nw = n0 + wn * TN * 32;  // first channel of the wave
 #pragma unroll
@@ -716,7 +727,7 @@ gemm_kernel(const uint8_t *__restrict__ A, const uint8_t *__restrict__ Wv, const
 #pragma unroll
                 for (int i = 0; i < 32 / RPI; ++i) {
                     const int row = i * RPI + lane / CPR, ch = lane % CPR;
-                    const int m = m0 + wm * TM * 32 + (tp + e) * 32 + row;
+                    const int m = m0 + row_of_wave + (tp + e) * 32 + row;
                     const int n = nw + ch * (16 / OB);
                     const u32x4 v = *reinterpret_cast<const u32x4 *>(ew + e * EWAVE + row * EROW + ch * 16);
                     if (m < M && n < N) store16<CF::NTS>(Cb + (int64_t(m) * N + n) * OB, v);

@@ -92,7 +92,7 @@ struct ShrinkTask {
     const T *x;
     int64_t ldx;
     const T *down;  // [adapters][R][K]
-    T *low;         // two planes [M][R]
+    T *low;         // two planes
     int K;
 };
 template <class T>
@@ -118,6 +118,7 @@ struct LowRankPlan {
     int range, slices;
 };
 bool low_rank_few(int M);
+int64_t low_rank_bytes(int64_t M, int R);  // both planes of the low-rank values
 // K splits of the 2:4 product under low_rank_few()
 int low_rank_splits(int M, int N, int K);
 LowRankPlan low_rank_plan(int adapters, int R, int64_t M, int64_t N, int64_t K);
@@ -126,7 +127,7 @@ hipError_t launch_low_rank_tokens(const LowRank &lr, const void *x, int64_t ldx,
                                   int splits, void *out, int64_t ldo, int M, int N, int K, hipStream_t st);
 hipError_t launch_low_rank_shrink(const LowRank &lr, const void *x, int64_t ldx, void *low, int M, int K,
                                   hipStream_t st);
-// ws: two planes [M][R] of the rows' type (unused with few tokens).
+// ws: low_rank_bytes() (unused with few tokens).
 hipError_t launch_low_rank_add(const LowRank &lr, const void *x, int64_t ldx, const void *base, int64_t ldb, void *out,
                                int64_t ldo, int M, int N, int K, void *ws, hipStream_t st);
 hipError_t launch_low_rank_bwd(const LowRankBwd &b, hipStream_t st);

@@ -9,13 +9,18 @@
 //
 // The low-rank activations low[m][r] = scale[a] * (down[a] . x[m])[r] are
 // handed from one kernel to the next as two values of the rows' type, hi =
-// round(low) and lo = round((low - hi) * kLoScale), two planes [M][R].  Both
-// feed the matrix instructions, so that the split costs one more small product
-// instead of the digits that a single 16-bit value would lose (16 bits of
-// mantissa for bf16, 21 for fp16, against the 8 and 11 of the outputs).
+// round(low) and lo = round((low - hi) * kLoScale), two planes.  Both feed the
+// matrix instructions, so that the split costs one more small product instead of
+// the digits that a single 16-bit value would lose (16 bits of mantissa for
+// bf16, 21 for fp16, against the 8 and 11 of the outputs).  A plane is laid out
+// as the 32x32x16 instruction's operand: blocks of 32 tokens x 16 slots, in each
+// the 16 bytes of lane (slot / 8 % 2) * 32 + token % 32 hold slots 8 (slot / 8)
+// .. + 7, so that a wave reads a block as one contiguous KiB (read row by row,
+// 32 rows an instruction, the loads took 4 times as many cache lines).
 #pragma once
 
 #include "elem.h"
+#include "tw_common.h"
 
 namespace ssg {
 
@@ -73,20 +78,32 @@ __device__ __forceinline__ int low_rank_of(const int32_t *ranks, int a, int R) {
     return r < 0 ? 0 : r > R ? R : r;
 }
 
+// Elements of one plane, and the place of 8 slots from r (a multiple of 8) of token m.
+__host__ __device__ inline int64_t low_plane(int64_t M, int R) { return (M + 31) / 32 * 32 * ((R + 15) / 16 * 16); }
+__device__ __forceinline__ int64_t low_at(int64_t m, int r, int R) {
+    return ((m / 32 * ((R + 15) / 16) + r / 16) * 64 + (r / 8 % 2) * 32 + m % 32) * 8;
+}
+
+// Source of padding in direct-to-LDS loads.
+static __device__ __attribute__((aligned(256))) uint16_t g_low_zero[128];
+
 // Adds up[a] . low to accumulators of 32x32 blocks: acc[tn][tm] holds, for the
-// 32 tokens from mw + 32 tm, the channels nw + 32 tn + 8 (i/4) + 4 h + i%4 of
-// token lane%32.  at[i]: index of token mw + i (anything past M).  Channels past
-// the last repeat it (their results are not stored).
+// 32 tokens from mw + 32 tm (mw a multiple of 32), the channels nw + 32 tn +
+// 8 (i/4) + 4 h + i%4 of token lane%32.  at[i]: index of token mw + i (anything
+// past M).  Channels past the last repeat it (their results are not stored).
 // The wave visits the distinct adapters of its tokens one after another, each
-// with the other tokens' low values zeroed, 32 rank slots at a time: the loads
-// of a turn wait for one another only, not for the adapter's rank.
+// with the other tokens' low values zeroed, up to 64 rank slots at a time: it
+// copies its channels' rows of the pool to `lds` (TN * 4 KiB of its own) with
+// whole-line direct-to-LDS loads and reads its operand from there.
 template <class T, int TN, int TM>
 __device__ __forceinline__ void low_rank_expand(floatx16 (&acc)[TN][TM], const T *__restrict__ up,
                                                 const T *__restrict__ low, const int32_t *at,
                                                 const int32_t *__restrict__ ranks, int adapters, int R, int mw, int nw,
-                                                int M, int N) {
+                                                int M, int N, uint8_t *lds) {
     const int lane = threadIdx.x & 63, h = lane >> 5, r = lane & 31;
-    const int64_t plane = int64_t(M) * R;
+    const int64_t plane = low_plane(M, R);
+    // 16-byte pieces of a pool row held at a time, as a shift
+    const int ws = R <= 16 ? 1 : R <= 32 ? 2 : 3;
     int mine[TM];
     bool todo[TM];
 #pragma unroll
@@ -101,10 +118,15 @@ __device__ __forceinline__ void low_rank_expand(floatx16 (&acc)[TN][TM], const T
                 for (int i = 0; i < 16; ++i) acc[tn][tm][i] = __builtin_nanf("");
         }
     }
+    for (;;) {
+        int a = -1;
 #pragma unroll
-    for (int first = 0; first < TM; ++first) {
-        for (uint64_t left = __ballot(todo[first]); left; left = __ballot(todo[first])) {
-            const int a = __builtin_amdgcn_readlane(mine[first], __builtin_ctzll(left));
+        for (int tm = TM - 1; tm >= 0; --tm) {
+            const uint64_t left = __ballot(todo[tm]);
+            if (left) a = __builtin_amdgcn_readlane(mine[tm], __builtin_ctzll(left));
+        }
+        if (a < 0) return;
+        {
             bool sel[TM];
 #pragma unroll
             for (int tm = 0; tm < TM; ++tm) {
@@ -113,41 +135,50 @@ __device__ __forceinline__ void low_rank_expand(floatx16 (&acc)[TN][TM], const T
             }
             const int rank = low_rank_of(ranks, a, R);
             const T *pool = up + int64_t(a) * N * R;
-            for (int k0 = 0; k0 < R; k0 += 32) {
-                u32x4 w[2][TN], hi[2][TM], lo[2][TM];
+            for (int k0 = 0; k0 < R; k0 += 64) {
+                // (the previous turn's reads are done before its bytes are replaced)
+                asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+                for (int j = 0; j < TN << (ws - 1); ++j) {
+                    const int row = (j << (6 - ws)) + (lane >> ws);
+                    const int k = k0 + ((lane & ((1 << ws) - 1)) ^ (row & ((1 << ws) - 1))) * 8;
+                    const void *src = g_low_zero;
+                    if (k < R) src = pool + int64_t(min(nw + row, N - 1)) * R + k;
+                    tw_detail::tw_dma16(src, lds + j * 1024);
+                }
+                u32x4 hi[4][TM], lo[4][TM];
 #pragma unroll
-                for (int s = 0; s < 2; ++s) {
-                    const int k = k0 + 16 * s + 8 * h;
-#pragma unroll
-                    for (int tn = 0; tn < TN; ++tn) {
-                        const int n = min(nw + tn * 32 + r, N - 1);
-                        w[s][tn] = u32x4{0, 0, 0, 0};
-                        if (k < R) w[s][tn] = ld16(pool + int64_t(n) * R + k);
-                    }
+                for (int s = 0; s < 4; ++s)
 #pragma unroll
                     for (int tm = 0; tm < TM; ++tm) {
+                        const int k = k0 + 16 * s + 8 * h;
                         hi[s][tm] = lo[s][tm] = u32x4{0, 0, 0, 0};
                         if (sel[tm] && k < R) {
-                            const T *row = low + int64_t(mw + tm * 32 + r) * R + k;
-                            hi[s][tm] = ld16(row);
-                            lo[s][tm] = ld16(row + plane);
+                            const T *p = low + low_at(mw + tm * 32 + r, k, R);
+                            hi[s][tm] = ld16(p);
+                            lo[s][tm] = ld16(p + plane);
                         }
                     }
-                }
-                if (k0 >= rank) break;  // (after the loads: the rank itself comes from memory)
+                asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+                if (k0 >= rank) break;
 #pragma unroll
-                for (int s = 0; s < 2; ++s) {
+                for (int s = 0; s < 4; ++s) {
                     const int k = k0 + 16 * s;
                     if (k >= rank) break;
+                    u32x4 w[TN];
 #pragma unroll
-                    for (int tn = 0; tn < TN; ++tn) w[s][tn] = keep16(w[s][tn], rank - k - 8 * h);
+                    for (int tn = 0; tn < TN; ++tn) {
+                        const int row = tn * 32 + r;
+                        const int piece = (2 * s + h) ^ (row & ((1 << ws) - 1));
+                        w[tn] = keep16(*reinterpret_cast<const u32x4 *>(lds + (row << (ws + 4)) + piece * 16),
+                                       rank - k - 8 * h);
+                    }
 #pragma unroll
                     for (int tm = 0; tm < TM; ++tm) {
                         const u32x4 l = lo_unscaled<T>(lo[s][tm]);
 #pragma unroll
                         for (int tn = 0; tn < TN; ++tn) {
-                            acc[tn][tm] = mfma32<T>(w[s][tn], hi[s][tm], acc[tn][tm]);
-                            acc[tn][tm] = mfma32<T>(w[s][tn], l, acc[tn][tm]);
+                            acc[tn][tm] = mfma32<T>(w[tn], hi[s][tm], acc[tn][tm]);
+                            acc[tn][tm] = mfma32<T>(w[tn], l, acc[tn][tm]);
                         }
                     }
                 }

@@ -23,9 +23,6 @@ namespace {
 
 using namespace tw_detail;
 
-// Source of padding in direct-to-LDS loads.
-__device__ __attribute__((aligned(256))) uint16_t g_low_zero[128];
-
 // ---- shrink.  A workgroup takes 16 tokens, its NW waves every NW-th
 // 64-wide slice of K; v_mfma 16x16x32 with the rank slots as rows and the
 // tokens as columns (lane: row / column lane%16, k = 8 (lane/16)..; results:
@@ -39,7 +36,8 @@ __device__ __forceinline__ void shrink_tile(const T *__restrict__ x, int64_t ldx
                                             const float *__restrict__ scale, const int32_t *__restrict__ ranks,
                                             const int32_t *__restrict__ index, int adapters, int R,
                                             T *__restrict__ low, int M, int K, int tile, floatx4 *part) {
-    constexpr int UNROLL = RB <= 2 ? 4 : RB == 4 ? 2 : 1;  // 64-wide slices of K in flight
+    constexpr int UNROLL = RB == 1 ? 4 : RB <= 4 ? 2 : 1;  // 64-wide slices of K in flight
+    constexpr bool AHEAD = RB <= 2;  // both pools' values in registers at once
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int g = lane >> 4, c = lane & 15;
     const int m = tile * 16 + c;
@@ -73,8 +71,7 @@ __device__ __forceinline__ void shrink_tile(const T *__restrict__ x, int64_t ldx
         floatx4 acc[2][RB];
 #pragma unroll
         for (int b = 0; b < RB; ++b) acc[0][b] = acc[1][b] = floatx4{0.f, 0.f, 0.f, 0.f};
-        auto product = [&](const T *pool, int rank, int a, floatx4 (&to)[RB], int k0) {
-            u32x4 dv[UNROLL][2][RB];
+        auto fetch_pool = [&](const T *pool, int rank, u32x4 (&dv)[UNROLL][2][RB], int k0) {
 #pragma unroll
             for (int u = 0; u < UNROLL; ++u)
 #pragma unroll
@@ -85,6 +82,8 @@ __device__ __forceinline__ void shrink_tile(const T *__restrict__ x, int64_t ldx
                         dv[u][s][b] = u32x4{0, 0, 0, 0};
                         if (k < K && b * 16 + c < rank) dv[u][s][b] = ld16(pool + int64_t(b * 16 + c) * K + k);
                     }
+        };
+        auto product = [&](const u32x4 (&dv)[UNROLL][2][RB], int a, floatx4 (&to)[RB]) {
 #pragma unroll
             for (int u = 0; u < UNROLL; ++u)
 #pragma unroll
@@ -97,8 +96,20 @@ __device__ __forceinline__ void shrink_tile(const T *__restrict__ x, int64_t ldx
         for (int k0 = wave * 64; k0 < K; k0 += step) {
             if (!held) fetch_x(k0);
             held = K <= step;
-            product(pool0, rank0, a0, acc[0], k0);
-            if (a1 >= 0) product(pool1, rank1, a1, acc[1], k0);
+            u32x4 d0[UNROLL][2][RB];
+            fetch_pool(pool0, rank0, d0, k0);
+            if (AHEAD && a1 >= 0) {
+                u32x4 d1[UNROLL][2][RB];
+                fetch_pool(pool1, rank1, d1, k0);
+                product(d0, a0, acc[0]);
+                product(d1, a1, acc[1]);
+            } else {
+                product(d0, a0, acc[0]);
+                if (!AHEAD && a1 >= 0) {
+                    fetch_pool(pool1, rank1, d0, k0);
+                    product(d0, a1, acc[1]);
+                }
+            }
         }
         __syncthreads();  // (the previous adapters' sums have been read)
 #pragma unroll
@@ -128,8 +139,9 @@ __device__ __forceinline__ void shrink_tile(const T *__restrict__ x, int64_t ldx
                 hi[i] = T(f);
                 lo[i] = T((f - float(hi[i])) * LowSplit<T>::kLoScale);
             }
-            __builtin_memcpy(low + int64_t(m) * R + r, hi, 8);
-            __builtin_memcpy(low + int64_t(M) * R + int64_t(m) * R + r, lo, 8);
+            T *to = low + low_at(m, r & ~7, R) + (r & 4);
+            __builtin_memcpy(to, hi, 8);
+            __builtin_memcpy(to + low_plane(M, R), lo, 8);
         }
     }
 }
@@ -152,7 +164,8 @@ expand_kernel(const T *__restrict__ up, const T *__restrict__ low, const int32_t
               const int32_t *__restrict__ ranks, int adapters, int R, const T *base, int64_t ldb, T *out, int64_t ldo,
               int M, int N) {
     constexpr int TN = 4, ROW = TN * 32 + 4;
-    __shared__ float slab[4][32 * ROW];
+    __shared__ __attribute__((aligned(16))) float slab[4][32 * ROW];
+    static_assert(32 * ROW * 4 >= TN * 4096, "the slab is low_rank_expand's scratch first");
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int h = lane >> 5, r = lane & 31;
     const int tiles_n = (N + 255) / 256;
@@ -172,7 +185,8 @@ expand_kernel(const T *__restrict__ up, const T *__restrict__ low, const int32_t
     __shared__ int32_t at[64];
     if (threadIdx.x < 64) at[threadIdx.x] = int(mw - (wave & 1) * 32 + threadIdx.x) < M ? index[mw - (wave & 1) * 32 + threadIdx.x] : -1;
     __syncthreads();
-    if (nw < N) low_rank_expand<T, TN, 1>(acc, up, low, at + (wave & 1) * 32, ranks, adapters, R, mw, nw, M, N);
+    if (nw < N) low_rank_expand<T, TN, 1>(acc, up, low, at + (wave & 1) * 32, ranks, adapters, R, mw, nw, M, N,
+                                            reinterpret_cast<uint8_t *>(slab[wave]));
 #pragma unroll
     for (int tn = 0; tn < TN; ++tn)
 #pragma unroll
@@ -297,16 +311,17 @@ pool_transpose_kernel(const T *__restrict__ src0, T *__restrict__ dst0, int P0, 
 
 // ---- wgrad: out[r][c] = sum over adapter a's tokens of low[m][r] z[m][c], z
 // [M][C] one of x (out = ddown [R][K]) and dy (out = dup [N][R]).
-// A workgroup takes one adapter, 128 columns of z and one range of tokens: it
-// lists the range's tokens of its adapter in LDS, then works through the list
-// 32 tokens at a time, their z rows and low rows copied to LDS as they lie in
-// memory ([token][column]) and read by transposing LDS reads, which give each
-// lane 8 consecutive tokens of one column (lane i of a 16-lane group receives
-// element i%4 of the 8-byte run read by lane 4e + i/4, e = 0..3).  Three stages
-// are in flight beside the one in use.  The high and the low part of `low` have
-// accumulators of their own.  Ranges write fp32 slices [range][adapter][R][C]
-// that a second launch sums in order; an adapter without tokens in a range
-// writes nothing but its count.
+// A workgroup takes 128 columns of z and one range of tokens, and the range's
+// distinct adapters one after another (so every workgroup has the same number of
+// tokens, however they fall to adapters): it lists the adapter's tokens in LDS,
+// then works through the list 32 tokens at a time, their z rows and low values
+// copied to LDS as they lie in memory ([token][column]) and read by transposing
+// LDS reads, which give each lane 8 consecutive tokens of one column (lane i of a
+// 16-lane group receives element i%4 of the 8-byte run read by lane 4e + i/4, e =
+// 0..3).  Three stages are in flight beside the one in use.  The high and the low
+// part of `low` have accumulators of their own.  Ranges write fp32 slices
+// [range][adapter][R][C] that a second launch sums in order, of the adapters
+// only that the range has.
 constexpr int kListCap = 2048;  // tokens of a range, at most
 
 // Two fragments of 8 consecutive tokens a lane: transposing reads of the rows at
@@ -330,10 +345,20 @@ __device__ __forceinline__ void read_tr(uint32_t p, uint32_t q, u32x4 &u, u32x4 
     v = u32x4{v0.x, v0.y, v1.x, v1.y};
 }
 
+// Zeros for a workgroup's tile of one adapter's gradient: 128 columns from c0.
+template <class T>
+__device__ __forceinline__ void zero_tile(T *o, bool rows_c, int c0, int C, int R) {
+    const int n = min(128, C - c0);
+    for (int i = threadIdx.x; i < n * R; i += 256) {
+        if (rows_c) o[int64_t(c0) * R + i] = T(0.0f);
+        else o[int64_t(i / n) * C + c0 + i % n] = T(0.0f);
+    }
+}
+
 template <class T, int RB>
 __global__ void __launch_bounds__(256)
 wgrad_kernel(WgradTask<T> p, WgradTask<T> q, const int32_t *__restrict__ index, int adapters, int R, int M,
-             int range, int32_t *__restrict__ counts_out) {
+             int range, int32_t *__restrict__ present) {
     constexpr int RT = RB * 16;                  // rank slots of a stage row
     constexpr int Z_STAGE = 32 * 128 * 2;        // [32][128]
     constexpr int L_STAGE = 32 * RT * 2;         // [32][RT], one part
@@ -342,24 +367,54 @@ wgrad_kernel(WgradTask<T> p, WgradTask<T> q, const int32_t *__restrict__ index, 
     __shared__ __attribute__((aligned(1024))) uint8_t smem[NB * STAGE];
     __shared__ int32_t list[kListCap];
     __shared__ int counts[4][kListCap / 256];
+    __shared__ int least[2][4];
+    constexpr int TURNS = kListCap / 256;
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const bool second = int(blockIdx.x) >= p.tiles;
     const WgradTask<T> &w = second ? q : p;
     const int c0 = (int(blockIdx.x) - (second ? p.tiles : 0)) * 128;
-    const int a = blockIdx.y, C = w.C;
-    const int first = blockIdx.z * range, last = min(first + range, M);
+    const int C = w.C, slice = blockIdx.y;
+    const int first = slice * range, last = min(first + range, M);
+    const bool marks = w.part && blockIdx.x == 0;
+    if (marks)
+        for (int a = tid; a < adapters; a += 256) present[int64_t(slice) * adapters + a] = 0;
 
-    // the tokens of adapter a in [first, last), in order
+    // this thread's tokens of the range
+    int mine[TURNS];
+#pragma unroll
+    for (int i = 0; i < TURNS; ++i) {
+        const int m = first + i * 256 + tid;
+        mine[i] = m < last ? index[m] : -1;
+        if (mine[i] >= adapters) mine[i] = -1;
+    }
+    constexpr int kNone = 0x7fffffff;
+    int turn = 0, next = 0;  // adapters below `next` are done
+    for (;; turn ^= 1) {
+    // the least adapter that is not done, and its tokens in order
+    int a = kNone;
+#pragma unroll
+    for (int i = 0; i < TURNS; ++i)
+        if (mine[i] >= next) a = min(a, mine[i]);
+#pragma unroll
+    for (int d = 32; d > 0; d >>= 1) a = min(a, __shfl_xor(a, d, 64));
+    if (lane == 0) least[turn][wave] = a;
+    __syncthreads();
+    a = min(min(least[turn][0], least[turn][1]), min(least[turn][2], least[turn][3]));
+    a = __builtin_amdgcn_readfirstlane(a);
+    if (!w.part) {
+        // the one range writes every adapter: zeros for those without tokens
+        const int upto = a == kNone ? adapters : a;
+        for (int z = next; z < upto; ++z) zero_tile(w.out + int64_t(z) * R * C, w.rows_c, c0, C, R);
+    }
+    if (a == kNone) return;
+    next = a + 1;
+    if (marks && tid == 0) present[int64_t(slice) * adapters + a] = 1;
     int total = 0;
     {
-        constexpr int TURNS = kListCap / 256;
-        bool hit[TURNS];
         uint64_t votes[TURNS];
 #pragma unroll
         for (int i = 0; i < TURNS; ++i) {
-            const int m = first + i * 256 + tid;
-            hit[i] = m < last && index[m] == a;
-            votes[i] = __ballot(hit[i]);
+            votes[i] = __ballot(mine[i] == a);
             if (lane == 0) counts[wave][i] = __builtin_popcountll(votes[i]);
         }
         __syncthreads();
@@ -367,17 +422,13 @@ wgrad_kernel(WgradTask<T> p, WgradTask<T> q, const int32_t *__restrict__ index, 
         for (int i = 0; i < TURNS; ++i)
 #pragma unroll
             for (int v = 0; v < 4; ++v) {
-                if (v == wave && hit[i])
+                if (v == wave && mine[i] == a)
                     list[total + __builtin_popcountll(votes[i] & ((uint64_t(1) << lane) - 1))] = first + i * 256 + tid;
                 total += counts[v][i];
             }
         __syncthreads();
     }
     total = __builtin_amdgcn_readfirstlane(total);
-    if (w.part) {
-        if (blockIdx.x == 0 && tid == 0) counts_out[int64_t(blockIdx.z) * adapters + a] = total;
-        if (total == 0) return;
-    }
 
     const int g = lane >> 4, j16 = lane & 15;
     floatx4 acc[2][RB][2];
@@ -388,7 +439,7 @@ wgrad_kernel(WgradTask<T> p, WgradTask<T> q, const int32_t *__restrict__ index, 
 
     // Direct-to-LDS loads of a stage: 8 KiB of z (row = 4 q + lane/16, 16-byte
     // chunk lane%16, swizzled), then 2 * RB KiB of low.
-    const int64_t plane = int64_t(M) * R;
+    const int64_t plane = low_plane(M, R);
     auto issue = [&](int s) {
         uint8_t *base = smem + (s % NB) * STAGE;
 #pragma unroll
@@ -404,7 +455,7 @@ wgrad_kernel(WgradTask<T> p, WgradTask<T> q, const int32_t *__restrict__ index, 
             const int row = byte / (RT * 2), r = byte % (RT * 2) / 2;
             const int at = s * 32 + row;
             const void *src = g_low_zero;
-            if (at < total && r < R) src = w.low + part * plane + int64_t(list[at]) * R + r;
+            if (at < total && r < R) src = w.low + part * plane + low_at(list[at], r, R);
             tw_dma16(src, base + Z_STAGE + qq * 1024);
         }
     };
@@ -438,7 +489,6 @@ wgrad_kernel(WgradTask<T> p, WgradTask<T> q, const int32_t *__restrict__ index, 
     }
 
     // lane: rank slots 16 b + 4 g + i of column c0 + 32 wave + 16 cb + j16
-    const int slice = blockIdx.z;
 #pragma unroll
     for (int b = 0; b < RB; ++b)
 #pragma unroll
@@ -470,29 +520,47 @@ wgrad_kernel(WgradTask<T> p, WgradTask<T> q, const int32_t *__restrict__ index, 
                 }
             }
         }
+    }
 }
 
-// Sums the ranges' slices in order and rounds once: 4 values a thread.
+// Sums the ranges' slices of the adapters that the ranges have, in order, and
+// rounds once: one adapter a grid row, 4 values a thread.
 template <class T>
 __global__ void __launch_bounds__(256)
 wgrad_sum_kernel(const float *__restrict__ part0, T *__restrict__ out0, int64_t n0, const float *__restrict__ part1,
-                 T *__restrict__ out1, int64_t n1, int slices, const int32_t *__restrict__ counts, int adapters) {
-    int64_t i = (int64_t(blockIdx.x) * 256 + threadIdx.x) * 4;
-    const float *part = part0;
-    T *out = out0;
-    int64_t n = n0;
-    if (i >= n0) i -= n0, part = part1, out = out1, n = n1;
-    if (i >= n) return;
-    const int a = int(i / (n / adapters));
+                 T *__restrict__ out1, int64_t n1, int slices, const int32_t *__restrict__ present, int adapters) {
+    const int a = blockIdx.y, lane = threadIdx.x & 63;
+    int64_t i = (int64_t(blockIdx.x) * 256 + threadIdx.x) * 4;  // in the adapter's n0, then n1 values
+    const bool second = i >= n0;
+    const int64_t n = second ? n1 : n0;
+    const float *part = second ? part1 : part0;
+    T *out = second ? out1 : out0;
+    if (second) i -= n0;
+    const bool live = i < n;
     floatx4 s = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll 4
-    for (int q = 0; q < slices; ++q) {
-        if (counts[int64_t(q) * adapters + a] == 0) continue;
-        const floatx4 v = *reinterpret_cast<const floatx4 *>(part + q * n + i);
-        s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
+    for (int q0 = 0; q0 < slices; q0 += 64) {
+        uint64_t has = __ballot(q0 + lane < slices && present[int64_t(q0 + lane) * adapters + a] != 0);
+        while (has) {
+            // four slices' loads at a time
+            floatx4 v[4];
+            int got = 0;
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                v[u] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
+                if (!has) continue;
+                const int q = q0 + __builtin_ctzll(has);
+                has &= has - 1;
+                got = u + 1;
+                if (live) v[u] = *reinterpret_cast<const floatx4 *>(part + (int64_t(q) * adapters + a) * n + i);
+            }
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+                if (u < got) s.x += v[u].x, s.y += v[u].y, s.z += v[u].z, s.w += v[u].w;
+        }
     }
+    if (!live) return;
     T t[4] = {T(s.x), T(s.y), T(s.z), T(s.w)};
-    __builtin_memcpy(out + i, t, 8);
+    __builtin_memcpy(out + int64_t(a) * n + i, t, 8);
 }
 
 template <class T>
@@ -559,7 +627,7 @@ hipError_t bwd(const LowRankBwd &b, hipStream_t st) {
                          false};
     const WgradTask<T> q{static_cast<const T *>(b.dy), b.lddy, low, part1, static_cast<T *>(b.dup), N, (N + 127) / 128,
                          true};
-    const dim3 grid(p.tiles + q.tiles, lr.adapters, pl.slices);
+    const dim3 grid(p.tiles + q.tiles, pl.slices);
 #define SSG_WGRAD(RB) \
     hipLaunchKernelGGL((wgrad_kernel<T, RB>), grid, dim3(256), 0, st, p, q, lr.index, lr.adapters, R, M, pl.range, counts)
     if (R <= 16) SSG_WGRAD(1);
@@ -568,12 +636,16 @@ hipError_t bwd(const LowRankBwd &b, hipStream_t st) {
     else SSG_WGRAD(8);
 #undef SSG_WGRAD
     if ((e = hipGetLastError()) != hipSuccess || pl.slices == 1) return e;
-    hipLaunchKernelGGL((wgrad_sum_kernel<T>), dim3(int(((n0 + n1) / 4 + 255) / 256)), dim3(256), 0, st, part0,
-                       static_cast<T *>(b.ddown), n0, part1, static_cast<T *>(b.dup), n1, pl.slices, counts, lr.adapters);
+    const int64_t m0 = int64_t(R) * K, m1 = int64_t(R) * N;  // values of one adapter
+    hipLaunchKernelGGL((wgrad_sum_kernel<T>), dim3(int(((m0 + m1) / 4 + 255) / 256), lr.adapters), dim3(256), 0, st,
+                       part0, static_cast<T *>(b.ddown), m0, part1, static_cast<T *>(b.dup), m1, pl.slices, counts,
+                       lr.adapters);
     return hipGetLastError();
 }
 
 }  // namespace
+
+int64_t low_rank_bytes(int64_t M, int R) { return low_plane(M, R) * 4; }
 
 // Few tokens: one launch on the vector units.
 bool low_rank_few(int M) { return M <= 128; }
@@ -584,14 +656,13 @@ LowRankPlan low_rank_plan(int adapters, int R, int64_t M, int64_t N, int64_t K) 
     p.up_t = 0;
     p.down_t = p.up_t + up256(int64_t(adapters) * R * N * 2);
     p.low = p.down_t + up256(int64_t(adapters) * R * K * 2);
-    p.dlow = p.low + up256(M * R * 4);
-    p.part = p.dlow + up256(M * R * 4);
-    // Token ranges: about 512 workgroups (an adapter's workgroups of a range hold
-    // its tokens only, so the adapters do not add to them), of at least 256 tokens
-    // and at most what the list holds, in at most 256 MiB of slices.
+    p.dlow = p.low + up256(low_plane(M, R) * 4);
+    p.part = p.dlow + up256(low_plane(M, R) * 4);
+    // Token ranges: about 1024 workgroups, of at least 256 tokens and at most what
+    // the list holds, in at most 256 MiB of slices.
     const int64_t cols = (N + 127) / 128 + (K + 127) / 128;
     const int64_t slice = int64_t(adapters) * R * (N + K) * 4;
-    int64_t want = (512 + cols - 1) / cols;
+    int64_t want = (1024 + cols - 1) / cols;
     const int64_t most = M > 256 ? M / 256 : 1;
     if (want > most) want = most;
     if (want > (int64_t(256) << 20) / slice) want = (int64_t(256) << 20) / slice;

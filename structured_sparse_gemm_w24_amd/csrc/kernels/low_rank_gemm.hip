@@ -16,10 +16,127 @@ struct LowRankAfter {
     const int32_t *index, *ranks;
     int adapters, R;
 
-    template <class CF>
-    __device__ __forceinline__ void after(floatx16 (&acc)[CF::TN][CF::TM], const int32_t *at, int mw, int nw, int M,
-                                          int N) const {
-        low_rank_expand<_Float16, CF::TN, CF::TM>(acc, up, low, at, ranks, adapters, R, mw, nw, M, N);
+    // The tile's low values go to LDS once for all waves, 64 slots at a time, and
+    // of its distinct adapters, two at a time, the channels' rows of the pool.  These
+    // copies leave and arrive together at the end of a tile, so their bytes set
+    // their time: read by every wave for itself they were 256 KiB a 256 x 256 tile
+    // and 64 slots, instead of 96.
+    template <class CF, int SMEM>
+    __device__ __forceinline__ void after(floatx16 (&acc)[CF::TN][CF::TM], const int32_t *at, uint8_t *smem,
+                                          bool loader, int m0, int n0, int M, int N) const {
+        constexpr int TN = CF::TN, TM = CF::TM, NW = CF::WM * CF::WN, WAVES = CF::PROD ? 2 * NW : NW;
+        constexpr int BM = CF::WM * TM * 32, BN = CF::WN * TN * 32, SEEN = (BM + 63) / 64;
+        constexpr int LOW = BM * 256, UP = BN * 128;  // 64 slots: both planes; one adapter's rows
+        static_assert(LOW + 2 * UP <= SMEM, "scratch must fit in the stage ring");
+        // (opaque, so that nothing derived from it is kept in registers across the main loop)
+        int tid = threadIdx.x;
+        asm volatile("" : "+v"(tid));
+        const int lane = tid & 63, h = lane >> 5, r = lane & 31;
+        const int all = __builtin_amdgcn_readfirstlane(tid >> 6);  // wave of the workgroup
+        const int wave = all % NW, wm = wave % CF::WM, wn = wave / CF::WM;
+        const int ks = (R + 15) / 16, blocks = (M + 31) / 32;
+        const int ws = R <= 16 ? 1 : R <= 32 ? 2 : 3;  // 16-byte pieces of a pool row, as a shift
+        int mine[TM];
+#pragma unroll
+        for (int tm = 0; tm < TM; ++tm) {
+            const int i = (wm * TM + tm) * 32 + r;
+            mine[tm] = m0 + i < M ? at[i] : -1;
+            if (mine[tm] != -1 && (mine[tm] < 0 || mine[tm] >= adapters)) {
+#pragma unroll
+                for (int tn = 0; tn < TN; ++tn)
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) acc[tn][tm][i] = __builtin_nanf("");
+            }
+        }
+#pragma unroll 1
+        for (int k0 = 0; k0 < R; k0 += 64) {
+            const int steps = min(4, ks - k0 / 16);
+            int seen[SEEN];
+#pragma unroll
+            for (int j = 0; j < SEEN; ++j) {
+                const int i = j * 64 + lane;
+                seen[j] = i < BM && m0 + i < M ? at[i] : -1;
+                if (seen[j] >= adapters) seen[j] = -1;
+            }
+            // the next distinct adapter of the tile (every wave finds the same ones), -1: none
+            auto next = [&]() {
+                int a = -1;
+#pragma unroll
+                for (int j = SEEN - 1; j >= 0; --j) {
+                    const uint64_t left = __ballot(seen[j] >= 0);
+                    if (left) a = __builtin_amdgcn_readlane(seen[j], __builtin_ctzll(left));
+                }
+#pragma unroll
+                for (int j = 0; j < SEEN; ++j)
+                    if (seen[j] == a) seen[j] = -1;
+                return a;
+            };
+            bool first = true;
+#pragma unroll 1
+            for (int a0 = next(); a0 >= 0; a0 = next()) {
+                const int a1 = next();
+                if (!first || k0 > 0) __syncthreads();  // the last pair has been used
+                if (first)
+                    for (int j = all; j < BM / 32 * steps * 2; j += WAVES) {
+                        const int plane = j / (BM / 32 * steps), tb = j / steps % (BM / 32), s = j % steps;
+                        const void *src = g_low_zero;
+                        if (m0 / 32 + tb < blocks)
+                            src = low + plane * low_plane(M, R) +
+                                  ((int64_t(m0 / 32 + tb) * ks + k0 / 16 + s) * 64 + lane) * 8;
+                        tw_detail::tw_dma16(src, smem + ((plane * (BM / 32) + tb) * 4 + s) * 1024);
+                    }
+                first = false;
+                const int pieces = BN >> (6 - ws);
+                for (int j = all; j < (a1 >= 0 ? 2 * pieces : pieces); j += WAVES) {
+                    const int u = j >= pieces, i = j - (u ? pieces : 0);
+                    const int row = (i << (6 - ws)) + (lane >> ws);
+                    const int k = k0 + ((lane & ((1 << ws) - 1)) ^ (row & ((1 << ws) - 1))) * 8;
+                    const void *src = g_low_zero;
+                    if (k < R) src = up + (int64_t(u ? a1 : a0) * N + min(n0 + row, N - 1)) * R + k;
+                    tw_detail::tw_dma16(src, smem + LOW + u * UP + i * 1024);
+                }
+                asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+                __syncthreads();
+                if (loader) continue;
+#pragma unroll 1
+                for (int u = 0; u < 2; ++u) {
+                    const int a = u ? a1 : a0;
+                    bool any = false;
+#pragma unroll
+                    for (int tm = 0; tm < TM; ++tm) any = any || __ballot(a >= 0 && mine[tm] == a) != 0;
+                    if (!any) continue;
+                    const int rank = low_rank_of(ranks, a, R);
+#pragma unroll 1
+                    for (int s = 0; s < 4 && k0 + 16 * s < rank; ++s) {
+                        const int k = k0 + 16 * s;
+                        u32x4 w[TN];
+#pragma unroll
+                        for (int tn = 0; tn < TN; ++tn) {
+                            const int row = (wn * TN + tn) * 32 + r;
+                            const int piece = (2 * s + h) ^ (row & ((1 << ws) - 1));
+                            w[tn] = keep16(
+                                *reinterpret_cast<const u32x4 *>(smem + LOW + u * UP + (row << (ws + 4)) + piece * 16),
+                                rank - k - 8 * h);
+                        }
+#pragma unroll
+                        for (int tm = 0; tm < TM; ++tm) {
+                            if (__ballot(mine[tm] == a) == 0) continue;
+                            const uint8_t *p = smem + ((wm * TM + tm) * 4 + s) * 1024 + lane * 16;
+                            u32x4 hi = *reinterpret_cast<const u32x4 *>(p);
+                            u32x4 lo = *reinterpret_cast<const u32x4 *>(p + BM / 32 * 4096);
+                            const bool use = mine[tm] == a && k + 8 * h < R;
+                            hi = use ? hi : u32x4{0, 0, 0, 0};
+                            lo = use ? lo_unscaled<_Float16>(lo) : u32x4{0, 0, 0, 0};
+#pragma unroll
+                            for (int tn = 0; tn < TN; ++tn) {
+                                acc[tn][tm] = mfma32<_Float16>(w[tn], hi, acc[tn][tm]);
+                                acc[tn][tm] = mfma32<_Float16>(w[tn], lo, acc[tn][tm]);
+                            }
+                        }
+                    }
+                }
+            }
+        }
     }
 };
 
