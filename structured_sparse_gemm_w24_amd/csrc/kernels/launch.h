@@ -91,7 +91,7 @@ template <class T>
 struct ShrinkTask {
     const T *x;
     int64_t ldx;
-    const T *down;  // [adapters][R][K]
+    const T *down;  // [adapters][R][K] (or [adapters][K][R])
     T *low;         // two planes
     int K;
 };
@@ -114,7 +114,7 @@ struct LowRankBwd {
 };
 // Byte offsets in the backward pass's workspace, and its split of the tokens.
 struct LowRankPlan {
-    int64_t up_t, down_t, low, dlow, counts, part, total;
+    int64_t low, dlow, counts, part, total;
     int range, slices;
 };
 bool low_rank_few(int M);

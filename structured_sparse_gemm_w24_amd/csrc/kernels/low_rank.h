@@ -84,6 +84,29 @@ __device__ __forceinline__ int64_t low_at(int64_t m, int r, int R) {
     return ((m / 32 * ((R + 15) / 16) + r / 16) * 64 + (r / 8 % 2) * 32 + m % 32) * 8;
 }
 
+// Two operands of 8 consecutive rows a lane: transposing reads of the four rows
+// at p (q) and of the four below them, at p4 (q4).  Waited for in the same
+// statement: the compiler would place a wait for every load in flight before
+// the builtin form, which it cannot tell apart from the direct-to-LDS loads'
+// stores.
+__device__ __forceinline__ void read_tr(uint32_t p, uint32_t p4, uint32_t q, uint32_t q4, u32x4 &u, u32x4 &v) {
+    u32x2 u0, u1, v0, v1;
+    asm volatile(
+        "ds_read_b64_tr_b16 %0, %4\n\t"
+        "ds_read_b64_tr_b16 %1, %5\n\t"
+        "ds_read_b64_tr_b16 %2, %6\n\t"
+        "ds_read_b64_tr_b16 %3, %7\n\t"
+        "s_waitcnt lgkmcnt(0)"
+        : "=&v"(u0), "=&v"(u1), "=&v"(v0), "=&v"(v1)
+        : "v"(p), "v"(p4), "v"(q), "v"(q4)
+        : "memory");
+    u = u32x4{u0.x, u0.y, u1.x, u1.y};
+    v = u32x4{v0.x, v0.y, v1.x, v1.y};
+}
+__device__ __forceinline__ uint32_t lds_address(const void *p) {
+    return static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p));
+}
+
 // Source of padding in direct-to-LDS loads.
 static __device__ __attribute__((aligned(256))) uint16_t g_low_zero[128];
 
@@ -95,7 +118,9 @@ static __device__ __attribute__((aligned(256))) uint16_t g_low_zero[128];
 // with the other tokens' low values zeroed, up to 64 rank slots at a time: it
 // copies its channels' rows of the pool to `lds` (TN * 4 KiB of its own) with
 // whole-line direct-to-LDS loads and reads its operand from there.
-template <class T, int TN, int TM>
+// TRANS (TN = 4): the pool is [adapters][R][N], slots along the rows, and the
+// operand comes through transposing LDS reads.
+template <class T, int TN, int TM, bool TRANS>
 __device__ __forceinline__ void low_rank_expand(floatx16 (&acc)[TN][TM], const T *__restrict__ up,
                                                 const T *__restrict__ low, const int32_t *at,
                                                 const int32_t *__restrict__ ranks, int adapters, int R, int mw, int nw,
@@ -138,7 +163,13 @@ __device__ __forceinline__ void low_rank_expand(floatx16 (&acc)[TN][TM], const T
             for (int k0 = 0; k0 < R; k0 += 64) {
                 // (the previous turn's reads are done before its bytes are replaced)
                 asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-                for (int j = 0; j < TN << (ws - 1); ++j) {
+                for (int j = 0; TRANS && j < 16; ++j) {
+                    const int row = 4 * j + (lane >> 4), n = nw + ((lane & 15) ^ (4 * (row & 3))) * 8;
+                    const void *src = g_low_zero;
+                    if (k0 + row < rank && n < N) src = pool + int64_t(k0 + row) * N + n;
+                    tw_detail::tw_dma16(src, lds + j * 1024);
+                }
+                for (int j = 0; !TRANS && j < TN << (ws - 1); ++j) {
                     const int row = (j << (6 - ws)) + (lane >> ws);
                     const int k = k0 + ((lane & ((1 << ws) - 1)) ^ (row & ((1 << ws) - 1))) * 8;
                     const void *src = g_low_zero;
@@ -165,12 +196,25 @@ __device__ __forceinline__ void low_rank_expand(floatx16 (&acc)[TN][TM], const T
                     const int k = k0 + 16 * s;
                     if (k >= rank) break;
                     u32x4 w[TN];
+                    if constexpr (TRANS) {
+                        static_assert(!TRANS || TN == 4, "rows of 128 channels");
+                        const int row = 16 * s + 8 * h + ((lane & 15) >> 2), c = (lane & 16) + 4 * (lane & 3);
+                        auto at_block = [&](int tn) {
+                            const int col = tn * 32 + c;
+                            return lds_address(lds) + row * 256 + ((col >> 3) ^ (4 * (row & 3))) * 16 + (col & 7) * 2;
+                        };
 #pragma unroll
-                    for (int tn = 0; tn < TN; ++tn) {
-                        const int row = tn * 32 + r;
-                        const int piece = (2 * s + h) ^ (row & ((1 << ws) - 1));
-                        w[tn] = keep16(*reinterpret_cast<const u32x4 *>(lds + (row << (ws + 4)) + piece * 16),
-                                       rank - k - 8 * h);
+                        for (int tn = 0; tn < TN; tn += 2)
+                            read_tr(at_block(tn), at_block(tn) + 1024, at_block(tn + 1), at_block(tn + 1) + 1024, w[tn],
+                                    w[tn + 1]);
+                    } else {
+#pragma unroll
+                        for (int tn = 0; tn < TN; ++tn) {
+                            const int row = tn * 32 + r;
+                            const int piece = (2 * s + h) ^ (row & ((1 << ws) - 1));
+                            w[tn] = keep16(*reinterpret_cast<const u32x4 *>(lds + (row << (ws + 4)) + piece * 16),
+                                           rank - k - 8 * h);
+                        }
                     }
 #pragma unroll
                     for (int tm = 0; tm < TM; ++tm) {

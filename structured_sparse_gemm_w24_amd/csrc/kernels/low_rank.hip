@@ -7,8 +7,8 @@
 //   wgrad    ddown[a][r][k] = sum over a's tokens of (scale up[a]^T dy)[r] x[k]
 //            dup[a][n][r]   = sum over a's tokens of dy[n] low[r]
 // The input gradient is the same pair of kernels with the roles exchanged:
-// dlow = shrink(dy, up^T), dx = expand(base, dlow, down^T), on transposed
-// copies of the pools.
+// dlow = shrink(dy, up^T), dx = expand(base, dlow, down^T), which take the pools
+// as they lie through transposing LDS reads.
 //
 // Memory bound: shrink reads x once, expand reads base and writes out once,
 // wgrad reads x and dy once; the pools are small beside them, and the products
@@ -31,13 +31,19 @@ using namespace tw_detail;
 // Two of a tile's adapters are taken at a time, on the same x values, so that a
 // tile where one request ends and the next begins costs no second pass; the
 // first x values are fetched before the indices are known.
-template <class T, int RB, int NW>
+// TRANS: the pool is [adapters][K][R] (the gradient's use of `up`): a slice's
+// rows are copied to LDS as they lie, for each wave its own, and read by
+// transposing reads.
+template <bool TRANS, int RB>
+constexpr int kShrinkUnroll = RB <= 2 || (!TRANS && RB == 4) ? 2 : 1;  // 64-wide slices of K in flight
+template <class T, int RB, int NW, bool TRANS>
 __device__ __forceinline__ void shrink_tile(const T *__restrict__ x, int64_t ldx, const T *__restrict__ down,
                                             const float *__restrict__ scale, const int32_t *__restrict__ ranks,
                                             const int32_t *__restrict__ index, int adapters, int R,
                                             T *__restrict__ low, int M, int K, int tile, floatx4 *part) {
-    constexpr int UNROLL = RB == 1 ? 4 : RB <= 4 ? 2 : 1;  // 64-wide slices of K in flight
-    constexpr bool AHEAD = RB <= 2;  // both pools' values in registers at once
+    constexpr int UNROLL = kShrinkUnroll<TRANS, RB>;
+    constexpr bool AHEAD = RB <= 2 && !TRANS;  // both pools' values in registers at once
+    constexpr int SLICE = RB * 2048;           // bytes of a slice in LDS (TRANS)
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int g = lane >> 4, c = lane & 15;
     const int m = tile * 16 + c;
@@ -67,11 +73,34 @@ __device__ __forceinline__ void shrink_tile(const T *__restrict__ x, int64_t ldx
         todo = todo && mine != a1;
         const int rank0 = low_rank_of(ranks, a0, R), rank1 = a1 >= 0 ? low_rank_of(ranks, a1, R) : 0;
         const float s0 = scale ? scale[a0] : 1.0f, s1 = scale && a1 >= 0 ? scale[a1] : 1.0f;
+        if constexpr (TRANS) __syncthreads();  // (the previous adapters' sums, in the same LDS, have been read)
         const T *pool0 = down + int64_t(a0) * R * K, *pool1 = down + int64_t(a1 < 0 ? 0 : a1) * R * K;
         floatx4 acc[2][RB];
 #pragma unroll
         for (int b = 0; b < RB; ++b) acc[0][b] = acc[1][b] = floatx4{0.f, 0.f, 0.f, 0.f};
         auto fetch_pool = [&](const T *pool, int rank, u32x4 (&dv)[UNROLL][2][RB], int k0) {
+            if constexpr (TRANS) {
+                uint8_t *own = reinterpret_cast<uint8_t *>(part) + wave * UNROLL * SLICE;
+#pragma unroll
+                for (int u = 0; u < UNROLL; ++u)
+                    for (int j = 0; j < R / 8; ++j) {
+                        const int64_t e = int64_t(k0 + u * NW * 64) * R + (j * 64 + lane) * 8;
+                        const void *src = g_low_zero;
+                        if (e < int64_t(K) * R) src = pool + e;
+                        tw_dma16(src, own + u * SLICE + j * 1024);
+                    }
+                asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+                // (slots past R read what follows: their sums are not used)
+#pragma unroll
+                for (int u = 0; u < UNROLL; ++u)
+#pragma unroll
+                    for (int b = 0; b < RB; ++b) {
+                        const uint32_t p = lds_address(own) + u * SLICE + (8 * g + (c >> 2)) * (R * 2) +
+                                           (b * 16 + 4 * (c & 3)) * 2;
+                        read_tr(p, p + 8 * R, p + 64 * R, p + 72 * R, dv[u][0][b], dv[u][1][b]);
+                    }
+                return;
+            }
 #pragma unroll
             for (int u = 0; u < UNROLL; ++u)
 #pragma unroll
@@ -131,6 +160,7 @@ __device__ __forceinline__ void shrink_tile(const T *__restrict__ x, int64_t ldx
             T hi[4], lo[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
+                if (TRANS && r + i >= (q < RB ? rank0 : rank1)) v[i] = 0.0f;
                 // The product is made opaque: the compiler otherwise forms hi a
                 // second time with a multiply that rounds to fp16 directly, and
                 // next to a tie the stored hi is then not the one lo was taken from.
@@ -146,19 +176,26 @@ __device__ __forceinline__ void shrink_tile(const T *__restrict__ x, int64_t ldx
     }
 }
 
-template <class T, int RB, int NW>
+// TRANS: of the first task's pool.
+template <class T, int RB, int NW, bool TRANS>
 __global__ void __launch_bounds__(NW * 64)
 shrink_kernel(ShrinkTask<T> p, ShrinkTask<T> q, const float *__restrict__ scale, const int32_t *__restrict__ ranks,
               const int32_t *__restrict__ index, int adapters, int R, int M) {
-    __shared__ floatx4 part[2 * RB * NW * 64];
-    const ShrinkTask<T> &w = blockIdx.y ? q : p;
-    shrink_tile<T, RB, NW>(w.x, w.ldx, w.down, scale, ranks, index, adapters, R, w.low, M, w.K, blockIdx.x, part);
+    constexpr int SUMS = 2 * RB * NW * 64, SLICES = TRANS ? NW * kShrinkUnroll<TRANS, RB> * RB * 2048 / 16 : 0;
+    __shared__ floatx4 part[SUMS > SLICES ? SUMS : SLICES];
+    if (blockIdx.y)
+        shrink_tile<T, RB, NW, false>(q.x, q.ldx, q.down, scale, ranks, index, adapters, R, q.low, M, q.K, blockIdx.x,
+                                      part);
+    else
+        shrink_tile<T, RB, NW, TRANS>(p.x, p.ldx, p.down, scale, ranks, index, adapters, R, p.low, M, p.K, blockIdx.x,
+                                      part);
 }
 
 // ---- expand: a workgroup takes 64 tokens x 256 channels, a wave 32 x 128.
 // The sums go through LDS as fp32 rows, so that base is read and out written
 // 16 bytes a lane; out may be base.
-template <class T>
+// TRANS: the pool is [adapters][R][N] (the gradient's use of `down`).
+template <class T, bool TRANS>
 __global__ void __launch_bounds__(256, 2)
 expand_kernel(const T *__restrict__ up, const T *__restrict__ low, const int32_t *__restrict__ index,
               const int32_t *__restrict__ ranks, int adapters, int R, const T *base, int64_t ldb, T *out, int64_t ldo,
@@ -185,7 +222,7 @@ expand_kernel(const T *__restrict__ up, const T *__restrict__ low, const int32_t
     __shared__ int32_t at[64];
     if (threadIdx.x < 64) at[threadIdx.x] = int(mw - (wave & 1) * 32 + threadIdx.x) < M ? index[mw - (wave & 1) * 32 + threadIdx.x] : -1;
     __syncthreads();
-    if (nw < N) low_rank_expand<T, TN, 1>(acc, up, low, at + (wave & 1) * 32, ranks, adapters, R, mw, nw, M, N,
+    if (nw < N) low_rank_expand<T, TN, 1, TRANS>(acc, up, low, at + (wave & 1) * 32, ranks, adapters, R, mw, nw, M, N,
                                             reinterpret_cast<uint8_t *>(slab[wave]));
 #pragma unroll
     for (int tn = 0; tn < TN; ++tn)
@@ -273,42 +310,6 @@ tokens_kernel(const T *__restrict__ x, int64_t ldx, const T *__restrict__ down, 
     out[int64_t(m) * ldo + n] = T(sum);
 }
 
-// ---- transposed copies of the pools: [n][P][Q] -> [n][Q][P], 64 x 64 tiles
-// through LDS (P and Q multiples of 8).
-template <class T>
-__global__ void __launch_bounds__(256)
-pool_transpose_kernel(const T *__restrict__ src0, T *__restrict__ dst0, int P0, int Q0, int tiles0,
-                      const T *__restrict__ src1, T *__restrict__ dst1, int P1, int Q1) {
-    __shared__ uint16_t s[64][72];
-    const bool second = int(blockIdx.x) >= tiles0;
-    const int P = second ? P1 : P0, Q = second ? Q1 : Q0;
-    const uint16_t *src = reinterpret_cast<const uint16_t *>(second ? src1 : src0);
-    uint16_t *dst = reinterpret_cast<uint16_t *>(second ? dst1 : dst0);
-    const int tile = int(blockIdx.x) - (second ? tiles0 : 0);
-    const int tq = (Q + 63) / 64, tp = (P + 63) / 64;
-    const int64_t a = tile / (tq * tp);
-    const int p0 = (tile / tq) % tp * 64, q0 = tile % tq * 64;
-    src += a * P * Q;
-    dst += a * P * Q;
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const int row = i * 32 + threadIdx.x / 8, c = threadIdx.x % 8 * 8;
-        if (p0 + row < P && q0 + c < Q)
-            *reinterpret_cast<u32x4 *>(&s[row][c]) = ld16(src + int64_t(p0 + row) * Q + q0 + c);
-    }
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const int col = i * 32 + threadIdx.x / 8, r = threadIdx.x % 8 * 8;
-        if (q0 + col < Q && p0 + r < P) {
-            u32x4 v;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) v[j] = uint32_t(s[r + 2 * j][col]) | (uint32_t(s[r + 2 * j + 1][col]) << 16);
-            st16(dst + int64_t(q0 + col) * P + p0 + r, v);
-        }
-    }
-}
-
 // ---- wgrad: out[r][c] = sum over adapter a's tokens of low[m][r] z[m][c], z
 // [M][C] one of x (out = ddown [R][K]) and dy (out = dup [N][R]).
 // A workgroup takes 128 columns of z and one range of tokens, and the range's
@@ -323,27 +324,6 @@ pool_transpose_kernel(const T *__restrict__ src0, T *__restrict__ dst0, int P0, 
 // [range][adapter][R][C] that a second launch sums in order, of the adapters
 // only that the range has.
 constexpr int kListCap = 2048;  // tokens of a range, at most
-
-// Two fragments of 8 consecutive tokens a lane: transposing reads of the rows at
-// p (q) and of the rows four below, FOUR bytes on.  Waited for in the same
-// statement: the compiler would place a wait for every load in flight before
-// the builtin form, which it cannot tell apart from the direct-to-LDS loads'
-// stores.
-template <int FOUR>
-__device__ __forceinline__ void read_tr(uint32_t p, uint32_t q, u32x4 &u, u32x4 &v) {
-    u32x2 u0, u1, v0, v1;
-    asm volatile(
-        "ds_read_b64_tr_b16 %0, %4\n\t"
-        "ds_read_b64_tr_b16 %1, %4 offset:%6\n\t"
-        "ds_read_b64_tr_b16 %2, %5\n\t"
-        "ds_read_b64_tr_b16 %3, %5 offset:%6\n\t"
-        "s_waitcnt lgkmcnt(0)"
-        : "=&v"(u0), "=&v"(u1), "=&v"(v0), "=&v"(v1)
-        : "v"(p), "v"(q), "n"(FOUR)
-        : "memory");
-    u = u32x4{u0.x, u0.y, u1.x, u1.y};
-    v = u32x4{v0.x, v0.y, v1.x, v1.y};
-}
 
 // Zeros for a workgroup's tile of one adapter's gradient: 128 columns from c0.
 template <class T>
@@ -460,7 +440,7 @@ wgrad_kernel(WgradTask<T> p, WgradTask<T> q, const int32_t *__restrict__ index, 
         }
     };
     const int S = (total + 31) / 32;
-    const uint32_t smem_addr = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(smem));
+    const uint32_t smem_addr = lds_address(smem);
     const int per_stage = 2 + (2 * RB - wave + 3) / 4;  // loads of this wave
     for (int s = 0; s < NB - 1 && s < S; ++s) issue(s);
     for (int s = 0; s < S; ++s) {
@@ -477,9 +457,12 @@ wgrad_kernel(WgradTask<T> p, WgradTask<T> q, const int32_t *__restrict__ index, 
         }
         const uint32_t l_at = base + Z_STAGE + row * (RT * 2) + 4 * (j16 & 3) * 2;
         u32x4 zv[2], lv[2][RB];
-        read_tr<1024>(z_at[0], z_at[1], zv[0], zv[1]);
+        read_tr(z_at[0], z_at[0] + 1024, z_at[1], z_at[1] + 1024, zv[0], zv[1]);
 #pragma unroll
-        for (int b = 0; b < RB; ++b) read_tr<RT * 8>(l_at + b * 32, l_at + L_STAGE + b * 32, lv[0][b], lv[1][b]);
+        for (int b = 0; b < RB; ++b) {
+            const uint32_t hi = l_at + b * 32, lo = hi + L_STAGE;
+            read_tr(hi, hi + RT * 8, lo, lo + RT * 8, lv[0][b], lv[1][b]);
+        }
 #pragma unroll
         for (int part = 0; part < 2; ++part)
 #pragma unroll
@@ -563,12 +546,13 @@ wgrad_sum_kernel(const float *__restrict__ part0, T *__restrict__ out0, int64_t 
     __builtin_memcpy(out + int64_t(a) * n + i, t, 8);
 }
 
-template <class T>
-hipError_t shrink(const ShrinkTask<T> &p, const ShrinkTask<T> *q, const LowRank &lr, int M, hipStream_t st) {
+// One task, or the gradient's two (the first on the pool's other side).
+template <class T, bool BOTH>
+hipError_t shrink(const ShrinkTask<T> &p, const ShrinkTask<T> &q, const LowRank &lr, int M, hipStream_t st) {
     constexpr int NW = 8;
-    const dim3 grid((M + 15) / 16, q ? 2 : 1);
+    const dim3 grid((M + 15) / 16, BOTH ? 2 : 1);
 #define SSG_SHRINK(RB)                                                                                              \
-    hipLaunchKernelGGL((shrink_kernel<T, RB, NW>), grid, dim3(NW * 64), 0, st, p, q ? *q : p, lr.scale, lr.ranks, \
+    hipLaunchKernelGGL((shrink_kernel<T, RB, NW, BOTH>), grid, dim3(NW * 64), 0, st, p, q, lr.scale, lr.ranks,      \
                        lr.index, lr.adapters, lr.R, M)
     if (lr.R <= 16) SSG_SHRINK(1);
     else if (lr.R <= 32) SSG_SHRINK(2);
@@ -578,11 +562,11 @@ hipError_t shrink(const ShrinkTask<T> &p, const ShrinkTask<T> *q, const LowRank 
     return hipGetLastError();
 }
 
-template <class T>
+template <class T, bool TRANS>
 hipError_t expand(const T *up, const T *low, const LowRank &lr, const void *base, int64_t ldb, void *out, int64_t ldo,
                   int M, int N, hipStream_t st) {
     const int nb = (M + 63) / 64 * ((N + 255) / 256);
-    hipLaunchKernelGGL((expand_kernel<T>), dim3(nb), dim3(256), 0, st, up, low, lr.index, lr.ranks, lr.adapters, lr.R,
+    hipLaunchKernelGGL((expand_kernel<T, TRANS>), dim3(nb), dim3(256), 0, st, up, low, lr.index, lr.ranks, lr.adapters, lr.R,
                        static_cast<const T *>(base), ldb, static_cast<T *>(out), ldo, M, N);
     return hipGetLastError();
 }
@@ -593,9 +577,9 @@ hipError_t add(const LowRank &lr, const void *x, int64_t ldx, const void *base, 
     T *low = static_cast<T *>(ws);
     if (low_rank_few(M)) return launch_low_rank_tokens(lr, x, ldx, base, ldb, 0, out, ldo, M, N, K, st);
     const ShrinkTask<T> p{static_cast<const T *>(x), ldx, static_cast<const T *>(lr.down), low, K};
-    const hipError_t e = shrink<T>(p, nullptr, lr, M, st);
+    const hipError_t e = shrink<T, false>(p, p, lr, M, st);
     if (e != hipSuccess) return e;
-    return expand<T>(static_cast<const T *>(lr.up), low, lr, base, ldb, out, ldo, M, N, st);
+    return expand<T, false>(static_cast<const T *>(lr.up), low, lr, base, ldb, out, ldo, M, N, st);
 }
 
 template <class T>
@@ -604,20 +588,15 @@ hipError_t bwd(const LowRankBwd &b, hipStream_t st) {
     const int M = b.M, N = b.N, K = b.K, R = lr.R;
     const LowRankPlan pl = low_rank_plan(lr.adapters, R, M, N, K);
     uint8_t *ws = static_cast<uint8_t *>(b.ws);
-    T *up_t = reinterpret_cast<T *>(ws + pl.up_t), *down_t = reinterpret_cast<T *>(ws + pl.down_t);
     T *low = reinterpret_cast<T *>(ws + pl.low), *dlow = reinterpret_cast<T *>(ws + pl.dlow);
     hipError_t e;
-    const int64_t t0 = int64_t(lr.adapters) * ((R + 63) / 64) * ((N + 63) / 64);
-    const int64_t t1 = int64_t(lr.adapters) * ((R + 63) / 64) * ((K + 63) / 64);
     if (M > 0) {
-        hipLaunchKernelGGL((pool_transpose_kernel<T>), dim3(int(t0 + t1)), dim3(256), 0, st,
-                           static_cast<const T *>(lr.up), up_t, N, R, int(t0), static_cast<const T *>(lr.down), down_t,
-                           R, K);
-        if ((e = hipGetLastError()) != hipSuccess) return e;
-        const ShrinkTask<T> p{static_cast<const T *>(b.dy), b.lddy, up_t, dlow, N};
+        const ShrinkTask<T> p{static_cast<const T *>(b.dy), b.lddy, static_cast<const T *>(lr.up), dlow, N};
         const ShrinkTask<T> q{static_cast<const T *>(b.x), b.ldx, static_cast<const T *>(lr.down), low, K};
-        if ((e = shrink<T>(p, &q, lr, M, st)) != hipSuccess) return e;
-        if ((e = expand<T>(down_t, dlow, lr, b.base, b.ldb, b.dx, b.lddx, M, K, st)) != hipSuccess) return e;
+        if ((e = shrink<T, true>(p, q, lr, M, st)) != hipSuccess) return e;
+        if ((e = expand<T, true>(static_cast<const T *>(lr.down), dlow, lr, b.base, b.ldb, b.dx, b.lddx, M, K, st)) !=
+            hipSuccess)
+            return e;
     }
     const int64_t n0 = int64_t(lr.adapters) * R * K, n1 = int64_t(lr.adapters) * R * N;
     float *part0 = pl.slices > 1 ? reinterpret_cast<float *>(ws + pl.part) : nullptr;
@@ -653,9 +632,7 @@ bool low_rank_few(int M) { return M <= 128; }
 LowRankPlan low_rank_plan(int adapters, int R, int64_t M, int64_t N, int64_t K) {
     auto up256 = [](int64_t v) { return (v + 255) / 256 * 256; };
     LowRankPlan p;
-    p.up_t = 0;
-    p.down_t = p.up_t + up256(int64_t(adapters) * R * N * 2);
-    p.low = p.down_t + up256(int64_t(adapters) * R * K * 2);
+    p.low = 0;
     p.dlow = p.low + up256(low_plane(M, R) * 4);
     p.part = p.dlow + up256(low_plane(M, R) * 4);
     // Token ranges: about 1024 workgroups, of at least 256 tokens and at most what
@@ -697,13 +674,14 @@ hipError_t launch_low_rank_tokens(const LowRank &lr, const void *x, int64_t ldx,
 
 hipError_t launch_low_rank_shrink(const LowRank &lr, const void *x, int64_t ldx, void *low, int M, int K,
                                   hipStream_t st) {
-    if (lr.dtype == DT_F16)
-        return shrink<_Float16>({static_cast<const _Float16 *>(x), ldx, static_cast<const _Float16 *>(lr.down),
-                                 static_cast<_Float16 *>(low), K},
-                                nullptr, lr, M, st);
-    return shrink<__bf16>({static_cast<const __bf16 *>(x), ldx, static_cast<const __bf16 *>(lr.down),
-                           static_cast<__bf16 *>(low), K},
-                          nullptr, lr, M, st);
+    if (lr.dtype == DT_F16) {
+        using T = _Float16;
+        const ShrinkTask<T> p{static_cast<const T *>(x), ldx, static_cast<const T *>(lr.down), static_cast<T *>(low), K};
+        return shrink<T, false>(p, p, lr, M, st);
+    }
+    using T = __bf16;
+    const ShrinkTask<T> p{static_cast<const T *>(x), ldx, static_cast<const T *>(lr.down), static_cast<T *>(low), K};
+    return shrink<T, false>(p, p, lr, M, st);
 }
 
 hipError_t launch_low_rank_add(const LowRank &lr, const void *x, int64_t ldx, const void *base, int64_t ldb, void *out,
