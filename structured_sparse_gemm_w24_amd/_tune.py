@@ -51,17 +51,18 @@ def _raw_stream():
 
 
 def _stream(t):
-    return _raw_stream()(t.device.index)
+    return _raw_stream()(t.get_device())
 
 
 def _ptr(t):
     return t.data_ptr() if t is not None else None
 
 
-def _on(device):
+def _on(t):
     """Makes the tensors' device current for the launch."""
     torch = _torch()
-    return _SAME if device.index == torch.cuda.current_device() else torch.cuda.device(device)
+    index = t.get_device()
+    return _SAME if index == torch.cuda.current_device() else torch.cuda.device(index)
 
 
 def _code(t, name, allowed=(SSG_DT_F16, SSG_DT_BF16, SSG_DT_F32)):
@@ -73,18 +74,25 @@ def _code(t, name, allowed=(SSG_DT_F16, SSG_DT_BF16, SSG_DT_F32)):
     return code
 
 
-def _tensor(t, dtype, shape, device, name):
-    if not isinstance(t, _torch().Tensor) or t.device != device:
-        raise TypeError(f"{name} must be a torch tensor on {device}")
+def _refuse(t, dtype, shape, like, name):
+    """Says what is wrong with a tensor that failed the checks of its caller."""
+    if not isinstance(t, _torch().Tensor) or t.device != like.device:
+        raise TypeError(f"{name} must be a torch tensor on {like.device}")
     if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    raise ValueError(f"{name} must be contiguous")
 
 
+# (the checks below are one expression each: they run eight times in a call of
+# 12 us, most of whose time is the host's)
 def _rows(t, like, shape, name):
     """A [M, N] matrix of like's type and device with contiguous rows; returns its row stride."""
-    _tensor(t, like.dtype, shape, like.device, name)
+    dtype = like.dtype
+    if not (isinstance(t, _torch().Tensor) and t.dtype is dtype and t.shape == shape
+            and t.get_device() == like.get_device()):
+        _refuse(t, dtype, shape, like, name)
     if t.is_contiguous():
         return shape[1] or 1
     ld, last = t.stride()
@@ -97,11 +105,11 @@ def _rows(t, like, shape, name):
     return ld
 
 
-def _flat(t, dtype, shape, device, name):
-    """A contiguous tensor of the given type, shape and device."""
-    _tensor(t, dtype, shape, device, name)
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
+def _flat(t, dtype, shape, like, name):
+    """A contiguous tensor of the given type and shape on like's device."""
+    if not (isinstance(t, _torch().Tensor) and t.dtype is dtype and t.shape == shape
+            and t.get_device() == like.get_device() and t.is_contiguous()):
+        _refuse(t, dtype, shape, like, name)
     return t
 
 
@@ -114,15 +122,16 @@ def _matrix(t, name):
 def _out(out, like, shape, name="out"):
     """The caller's output (rows may be strided) or a new one; returns it and its row stride."""
     if out is None:
-        return (_torch().empty_like(like) if like.is_contiguous() and like.shape == shape else like.new_empty(shape),
-                shape[1] or 1)
+        if like.shape == shape and like.is_contiguous():
+            return _torch().empty_like(like), shape[1] or 1
+        return like.new_empty(shape), shape[1] or 1
     return out, _rows(out, like, shape, name)
 
 
 def _workspace(n, like, ws=None):
     torch = _torch()
     if ws is not None:
-        return _flat(ws, torch.uint8, ws.shape, like.device, "workspace")
+        return _flat(ws, torch.uint8, ws.shape, like, "workspace")
     return like.new_empty(n if n > 16 else 16, dtype=torch.uint8)
 
 
@@ -137,7 +146,7 @@ def _norm_params(x, n, weight, bias):
             wt = p.dtype
             if wt not in (x.dtype, torch.float32):
                 raise TypeError(f"{name} must be {x.dtype} or torch.float32, got {wt}")
-        _flat(p, wt, (n,), x.device, name)
+        _flat(p, wt, (n,), x, name)
     return _codes()[wt if wt is not None else x.dtype]
 
 
@@ -160,8 +169,9 @@ def layer_norm(x, weight=None, bias=None, eps=1e-5, residual=None, out=None, sum
         s, lds = _out(sum_out, x, shape, "sum_out")
     elif sum_out is not None:
         raise ValueError("sum_out needs a residual")
-    mean, rstd = x.new_empty(m, dtype=torch.float32), x.new_empty(m, dtype=torch.float32)
-    with _on(x.device):
+    mean = x.new_empty(m, dtype=torch.float32)
+    rstd = torch.empty_like(mean)
+    with _on(x):
         _check(load().layer_norm_forward(dt, _ptr(x), ldx, _ptr(residual), ldr, _ptr(weight), _ptr(bias), wt, eps,
                                          _ptr(y), ldy, _ptr(s), lds, _ptr(mean), _ptr(rstd), m, n, _stream(x)))
     return (y, mean, rstd) if residual is None else (y, mean, rstd, s)
@@ -177,17 +187,18 @@ def layer_norm_backward(dy, x, mean, rstd, weight=None, dres=None, out=None, par
     m, n = shape
     ldx = _rows(x, x, shape, "x")
     lddy = _rows(dy, x, shape, "dy")
-    _flat(mean, torch.float32, (m,), x.device, "mean")
-    _flat(rstd, torch.float32, (m,), x.device, "rstd")
+    _flat(mean, torch.float32, (m,), x, "mean")
+    _flat(rstd, torch.float32, (m,), x, "rstd")
     wt = _norm_params(x, n, weight, None)
     ldres = _rows(dres, x, shape, "dres") if dres is not None else n
     dx, lddx = _out(out, x, shape)
     dw = db = ws = None
     lib = load()
     if param_grads:
-        dw, db = x.new_empty(n, dtype=torch.float32), x.new_empty(n, dtype=torch.float32)
+        dw = x.new_empty(n, dtype=torch.float32)
+        db = torch.empty_like(dw)
         ws = _workspace(lib.layer_norm_workspace_bytes(dt, m, n), x, workspace)
-    with _on(x.device):
+    with _on(x):
         _check(lib.layer_norm_backward(dt, _ptr(dy), lddy, _ptr(x), ldx, _ptr(mean), _ptr(rstd), _ptr(weight), wt,
                                        _ptr(dres), ldres, _ptr(dx), lddx, _ptr(dw), _ptr(db), m, n, _ptr(ws),
                                        ws.numel() if ws is not None else 0, _stream(x)))
@@ -208,13 +219,13 @@ def _pool(x, n, down, up, index, scale, ranks):
     if not isinstance(down, torch.Tensor) or down.dim() != 3:
         raise ValueError("down must be a tensor of shape [adapters, R, K]")
     a, r, _ = down.shape
-    _flat(down, x.dtype, (a, r, k), x.device, "down")
-    _flat(up, x.dtype, (a, n, r), x.device, "up")
-    _flat(index, torch.int32, (m,), x.device, "index")
+    _flat(down, x.dtype, (a, r, k), x, "down")
+    _flat(up, x.dtype, (a, n, r), x, "up")
+    _flat(index, torch.int32, (m,), x, "index")
     if scale is not None:
-        _flat(scale, torch.float32, (a,), x.device, "scale")
+        _flat(scale, torch.float32, (a,), x, "scale")
     if ranks is not None:
-        _flat(ranks, torch.int32, (a,), x.device, "ranks")
+        _flat(ranks, torch.int32, (a,), x, "ranks")
     return _LowRank(down.data_ptr(), up.data_ptr(), scale.data_ptr() if scale is not None else None,
                     ranks.data_ptr() if ranks is not None else None, index.data_ptr(), dt, a, r)
 
@@ -241,7 +252,7 @@ def low_rank_add(base, x, down, up, index, scale=None, ranks=None, out=None, wor
     lib = load()
     need = lib.low_rank_workspace_bytes(m, lr.R)
     ws = _workspace(need, x, workspace) if need > 0 else None
-    with _on(x.device):
+    with _on(x):
         _check(lib.low_rank_add(ct.byref(lr), _ptr(x), ldx, _ptr(base), ldb, _ptr(out), ldo, m, n, k, _ptr(ws),
                                 ws.numel() if ws is not None else 0, _stream(x)))
     return out
@@ -253,18 +264,18 @@ def w24_low_rank_gemm_f16(A, vals, meta, down, up, index, scale=None, ranks=None
     torch = _torch()
     _code(A, "A", (SSG_DT_F16,))
     m, k = _matrix(A, "A")
-    _flat(A, torch.float16, A.shape, A.device, "A")
+    _flat(A, torch.float16, A.shape, A, "A")
     n = vals.shape[0]
-    _flat(vals, torch.float16, (n, k // 2), A.device, "vals")
-    _flat(meta, torch.int32, (n, -(-k // 32)), A.device, "meta")
+    _flat(vals, torch.float16, (n, k // 2), A, "vals")
+    _flat(meta, torch.int32, (n, -(-k // 32)), A, "meta")
     lr = _pool(A, n, down, up, index, scale, ranks)
     if out is None:
         out = A.new_empty((m, n))
     else:
-        _flat(out, torch.float16, (m, n), A.device, "out")
+        _flat(out, torch.float16, (m, n), A, "out")
     lib = load()
     ws = _workspace(lib.w24_low_rank_workspace_bytes(m, n, k, lr.R), A, workspace)
-    with _on(A.device):
+    with _on(A):
         _check(lib.w24_low_rank_gemm_f16(_ptr(A), _ptr(vals), _ptr(meta), ct.byref(lr), _ptr(out), m, n, k, _ptr(ws),
                                          ws.numel(), _stream(A)))
     return out
@@ -285,7 +296,7 @@ def low_rank_backward(dy, x, down, up, index, scale=None, ranks=None, base=None,
     ddown, dup = torch.empty_like(down), torch.empty_like(up)
     lib = load()
     ws = _workspace(lib.low_rank_backward_workspace_bytes(lr.adapters, lr.R, m, n, k), x, workspace)
-    with _on(x.device):
+    with _on(x):
         _check(lib.low_rank_backward(ct.byref(lr), _ptr(dy), lddy, _ptr(x), ldx, _ptr(base), ldb, _ptr(dx), lddx,
                                      _ptr(ddown), _ptr(dup), m, n, k, _ptr(ws), ws.numel(), _stream(x)))
     return dx, ddown, dup
@@ -301,7 +312,7 @@ def _head(x, w, target):
     v = w.shape[0]
     ldx = _rows(x, x, x.shape, "x")
     ldw = _rows(w, x, (v, d), "w")
-    _flat(target, torch.int64, (m,), x.device, "target")
+    _flat(target, torch.int64, (m,), x, "target")
     return dt, m, v, d, ldx, ldw
 
 
@@ -312,10 +323,11 @@ def linear_cross_entropy(x, w, target, ignore_index=-100, workspace=None):
     the backward pass takes."""
     torch = _torch()
     dt, m, v, d, ldx, ldw = _head(x, w, target)
-    loss, lse = x.new_empty(m, dtype=torch.float32), x.new_empty(m, dtype=torch.float32)
+    loss = x.new_empty(m, dtype=torch.float32)
+    lse = torch.empty_like(loss)
     lib = load()
     ws = _workspace(lib.linear_cross_entropy_workspace_bytes(dt, m, v, d, ldx, ldw, 0), x, workspace)
-    with _on(x.device):
+    with _on(x):
         _check(lib.linear_cross_entropy_forward(dt, _ptr(x), ldx, _ptr(w), ldw, _ptr(target), ignore_index, _ptr(loss),
                                                 _ptr(lse), m, v, d, _ptr(ws), ws.numel(), _stream(x)))
     return loss, lse
@@ -327,13 +339,13 @@ def linear_cross_entropy_backward(dloss, x, w, target, lse, ignore_index=-100, o
     vocabulary."""
     torch = _torch()
     dt, m, v, d, ldx, ldw = _head(x, w, target)
-    _flat(dloss, torch.float32, (m,), x.device, "dloss")
-    _flat(lse, torch.float32, (m,), x.device, "lse")
+    _flat(dloss, torch.float32, (m,), x, "dloss")
+    _flat(lse, torch.float32, (m,), x, "lse")
     dx, lddx = _out(out, x, x.shape)
     dw, lddw = _out(dw_out, w, w.shape, "dw_out")
     lib = load()
     ws = _workspace(lib.linear_cross_entropy_workspace_bytes(dt, m, v, d, ldx, ldw, 1), x, workspace)
-    with _on(x.device):
+    with _on(x):
         _check(lib.linear_cross_entropy_backward(dt, _ptr(dloss), _ptr(x), ldx, _ptr(w), ldw, _ptr(target),
                                                  ignore_index, _ptr(lse), _ptr(dx), lddx, _ptr(dw), lddw, m, v, d,
                                                  _ptr(ws), ws.numel(), _stream(x)))

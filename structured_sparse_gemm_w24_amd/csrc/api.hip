@@ -3,6 +3,7 @@
 // caller's stream.  Nothing is allocated and nothing is synchronised.
 #include <hip/hip_runtime.h>
 
+#include <atomic>
 #include <cstring>
 #include <mutex>
 
@@ -14,16 +15,19 @@ namespace {
 
 constexpr int kMaxDevices = 64;
 // 0 = unknown, 1 = gfx950, 2 = other architecture
-int g_arch_state[kMaxDevices] = {0};
+std::atomic<int> g_arch_state[kMaxDevices] = {};
 std::mutex g_arch_mu;
 
 }  // namespace
 
 int ssg::check_device() {
-    int count = 0;
-    hipError_t e = hipGetDeviceCount(&count);
-    if (e != hipSuccess || count <= 0) return ssg::fail(SSG_ENODEV, "no HIP device visible");
     int dev = 0;
+    hipError_t e = hipGetDevice(&dev);
+    if (e == hipSuccess && dev >= 0 && dev < kMaxDevices && g_arch_state[dev].load(std::memory_order_acquire) == 1)
+        return SSG_OK;  // (a device that has been looked at before)
+    int count = 0;
+    e = hipGetDeviceCount(&count);
+    if (e != hipSuccess || count <= 0) return ssg::fail(SSG_ENODEV, "no HIP device visible");
     e = hipGetDevice(&dev);
     if (e != hipSuccess) return ssg::fail(SSG_EHIP, "hipGetDevice: %s", hipGetErrorString(e));
     if (dev < 0 || dev >= kMaxDevices) return ssg::fail(SSG_ENODEV, "device id %d out of range", dev);

@@ -115,9 +115,8 @@ int check_low_rank(const char *fn, const ssg_low_rank *lr, int64_t M, int64_t N,
     if (M < 0 || M > kMaxTokens || N < 8 || K < 8 || N % 8 || K % 8 || !fits_int(N) || !fits_int(K))
         return ssg::fail(SSG_EINVAL, "%s: M=%lld N=%lld K=%lld (need 0 <= M < 2^27, N and K positive multiples of 8)",
                          fn, (long long)M, (long long)N, (long long)K);
-    // launch grids: tiles of 64 x 256 outputs, 64 x 64 pieces of the pools
-    if (!fits_int((M + 63) / 64 * ((N + 255) / 256)) || !fits_int((M + 63) / 64 * ((K + 255) / 256)) ||
-        !fits_int(int64_t(lr->adapters) * 2 * ((N + 63) / 64 + (K + 63) / 64)))
+    // launch grids: tiles of 64 x 128 outputs
+    if (!fits_int((M + 63) / 64 * ((N + 127) / 128)) || !fits_int((M + 63) / 64 * ((K + 127) / 128)))
         return ssg::fail(SSG_EINVAL, "%s: dimensions too large", fn);
     return SSG_OK;
 }

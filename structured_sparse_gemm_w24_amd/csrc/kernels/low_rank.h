@@ -118,7 +118,7 @@ static __device__ __attribute__((aligned(256))) uint16_t g_low_zero[128];
 // with the other tokens' low values zeroed, up to 64 rank slots at a time: it
 // copies its channels' rows of the pool to `lds` (TN * 4 KiB of its own) with
 // whole-line direct-to-LDS loads and reads its operand from there.
-// TRANS (TN = 4): the pool is [adapters][R][N], slots along the rows, and the
+// TRANS (TN even): the pool is [adapters][R][N], slots along the rows, and the
 // operand comes through transposing LDS reads.
 template <class T, int TN, int TM, bool TRANS>
 __device__ __forceinline__ void low_rank_expand(floatx16 (&acc)[TN][TM], const T *__restrict__ up,
@@ -163,8 +163,10 @@ __device__ __forceinline__ void low_rank_expand(floatx16 (&acc)[TN][TM], const T
             for (int k0 = 0; k0 < R; k0 += 64) {
                 // (the previous turn's reads are done before its bytes are replaced)
                 asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-                for (int j = 0; TRANS && j < 16; ++j) {
-                    const int row = 4 * j + (lane >> 4), n = nw + ((lane & 15) ^ (4 * (row & 3))) * 8;
+                constexpr int PIECES = TN * 4;  // of a row of TN * 32 channels
+                for (int j = 0; TRANS && j < TN * 4; ++j) {
+                    const int row = (j * 64 + lane) / PIECES;
+                    const int n = nw + (lane % PIECES ^ (4 * (row & 3) & (PIECES - 1))) * 8;
                     const void *src = g_low_zero;
                     if (k0 + row < rank && n < N) src = pool + int64_t(k0 + row) * N + n;
                     tw_detail::tw_dma16(src, lds + j * 1024);
@@ -197,16 +199,17 @@ __device__ __forceinline__ void low_rank_expand(floatx16 (&acc)[TN][TM], const T
                     if (k >= rank) break;
                     u32x4 w[TN];
                     if constexpr (TRANS) {
-                        static_assert(!TRANS || TN == 4, "rows of 128 channels");
+                        static_assert(TN % 2 == 0, "channel blocks in pairs");
                         const int row = 16 * s + 8 * h + ((lane & 15) >> 2), c = (lane & 16) + 4 * (lane & 3);
                         auto at_block = [&](int tn) {
                             const int col = tn * 32 + c;
-                            return lds_address(lds) + row * 256 + ((col >> 3) ^ (4 * (row & 3))) * 16 + (col & 7) * 2;
+                            return lds_address(lds) + row * (PIECES * 16) +
+                                   ((col >> 3) ^ (4 * (row & 3) & (PIECES - 1))) * 16 + (col & 7) * 2;
                         };
 #pragma unroll
                         for (int tn = 0; tn < TN; tn += 2)
-                            read_tr(at_block(tn), at_block(tn) + 1024, at_block(tn + 1), at_block(tn + 1) + 1024, w[tn],
-                                    w[tn + 1]);
+                            read_tr(at_block(tn), at_block(tn) + PIECES * 64, at_block(tn + 1),
+                                    at_block(tn + 1) + PIECES * 64, w[tn], w[tn + 1]);
                     } else {
 #pragma unroll
                         for (int tn = 0; tn < TN; ++tn) {

@@ -31,19 +31,20 @@ using namespace tw_detail;
 // Two of a tile's adapters are taken at a time, on the same x values, so that a
 // tile where one request ends and the next begins costs no second pass; the
 // first x values are fetched before the indices are known.
-// TRANS: the pool is [adapters][K][R] (the gradient's use of `up`): a slice's
-// rows are copied to LDS as they lie, for each wave its own, and read by
-// transposing reads.
-template <bool TRANS, int RB>
-constexpr int kShrinkUnroll = RB <= 2 || (!TRANS && RB == 4) ? 2 : 1;  // 64-wide slices of K in flight
+// The pool's part of a slice is copied to LDS, for each wave its own, with
+// whole-line direct-to-LDS loads (read as operands straight from memory, 16 rows
+// of 64 bytes an instruction, the same pass took 18.0 us instead of 14.2 at
+// 6144 x 4096 and 1024, rank 16).  TRANS: the pool is [adapters][K][R] (the gradient's use
+// of `up`) and is read by transposing reads.
+template <int RB>
+constexpr int kShrinkUnroll = RB <= 2 ? 2 : 1;  // 64-wide slices of K in flight
 template <class T, int RB, int NW, bool TRANS>
 __device__ __forceinline__ void shrink_tile(const T *__restrict__ x, int64_t ldx, const T *__restrict__ down,
                                             const float *__restrict__ scale, const int32_t *__restrict__ ranks,
                                             const int32_t *__restrict__ index, int adapters, int R,
                                             T *__restrict__ low, int M, int K, int tile, floatx4 *part) {
-    constexpr int UNROLL = kShrinkUnroll<TRANS, RB>;
-    constexpr bool AHEAD = RB <= 2 && !TRANS;  // both pools' values in registers at once
-    constexpr int SLICE = RB * 2048;           // bytes of a slice in LDS (TRANS)
+    constexpr int UNROLL = kShrinkUnroll<RB>;
+    constexpr int SLICE = RB * 2048;  // bytes of a slice in LDS
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int g = lane >> 4, c = lane & 15;
     const int m = tile * 16 + c;
@@ -73,44 +74,46 @@ __device__ __forceinline__ void shrink_tile(const T *__restrict__ x, int64_t ldx
         todo = todo && mine != a1;
         const int rank0 = low_rank_of(ranks, a0, R), rank1 = a1 >= 0 ? low_rank_of(ranks, a1, R) : 0;
         const float s0 = scale ? scale[a0] : 1.0f, s1 = scale && a1 >= 0 ? scale[a1] : 1.0f;
-        if constexpr (TRANS) __syncthreads();  // (the previous adapters' sums, in the same LDS, have been read)
+        __syncthreads();  // (the previous adapters' sums, in the same LDS, have been read)
         const T *pool0 = down + int64_t(a0) * R * K, *pool1 = down + int64_t(a1 < 0 ? 0 : a1) * R * K;
         floatx4 acc[2][RB];
 #pragma unroll
         for (int b = 0; b < RB; ++b) acc[0][b] = acc[1][b] = floatx4{0.f, 0.f, 0.f, 0.f};
+        // one adapter's operand of the slices from k0
+        uint8_t *own = reinterpret_cast<uint8_t *>(part) + wave * UNROLL * SLICE;
         auto fetch_pool = [&](const T *pool, int rank, u32x4 (&dv)[UNROLL][2][RB], int k0) {
-            if constexpr (TRANS) {
-                uint8_t *own = reinterpret_cast<uint8_t *>(part) + wave * UNROLL * SLICE;
 #pragma unroll
-                for (int u = 0; u < UNROLL; ++u)
-                    for (int j = 0; j < R / 8; ++j) {
-                        const int64_t e = int64_t(k0 + u * NW * 64) * R + (j * 64 + lane) * 8;
-                        const void *src = g_low_zero;
+            for (int u = 0; u < UNROLL; ++u) {
+                const int ku = k0 + u * NW * 64;
+                for (int j = 0; j < (TRANS ? R / 8 : RB * 2); ++j) {
+                    const void *src = g_low_zero;
+                    if constexpr (TRANS) {
+                        const int64_t e = int64_t(ku) * R + (j * 64 + lane) * 8;
                         if (e < int64_t(K) * R) src = pool + e;
-                        tw_dma16(src, own + u * SLICE + j * 1024);
+                    } else {  // rows of 128 bytes, 16-byte pieces swizzled by row
+                        const int row = j * 8 + (lane >> 3), k = ku + ((lane & 7) ^ (row & 7)) * 8;
+                        if (row < rank && k < K) src = pool + int64_t(row) * K + k;
                     }
-                asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-                // (slots past R read what follows: their sums are not used)
-#pragma unroll
-                for (int u = 0; u < UNROLL; ++u)
-#pragma unroll
-                    for (int b = 0; b < RB; ++b) {
-                        const uint32_t p = lds_address(own) + u * SLICE + (8 * g + (c >> 2)) * (R * 2) +
-                                           (b * 16 + 4 * (c & 3)) * 2;
-                        read_tr(p, p + 8 * R, p + 64 * R, p + 72 * R, dv[u][0][b], dv[u][1][b]);
-                    }
-                return;
+                    tw_dma16(src, own + u * SLICE + j * 1024);
+                }
             }
+            asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
 #pragma unroll
             for (int u = 0; u < UNROLL; ++u)
 #pragma unroll
-                for (int s = 0; s < 2; ++s)
-#pragma unroll
-                    for (int b = 0; b < RB; ++b) {
-                        const int k = k0 + u * NW * 64 + 32 * s + 8 * g;
-                        dv[u][s][b] = u32x4{0, 0, 0, 0};
-                        if (k < K && b * 16 + c < rank) dv[u][s][b] = ld16(pool + int64_t(b * 16 + c) * K + k);
+                for (int b = 0; b < RB; ++b) {
+                    if constexpr (TRANS) {  // (slots past R read what follows: their sums are not used)
+                        const uint32_t p = lds_address(own) + u * SLICE + (8 * g + (c >> 2)) * (R * 2) +
+                                           (b * 16 + 4 * (c & 3)) * 2;
+                        read_tr(p, p + 8 * R, p + 64 * R, p + 72 * R, dv[u][0][b], dv[u][1][b]);
+                    } else {
+                        const uint8_t *p = own + u * SLICE + (b * 16 + c) * 128;
+                        dv[u][0][b] = *reinterpret_cast<const u32x4 *>(p + (g ^ (c & 7)) * 16);
+                        dv[u][1][b] = *reinterpret_cast<const u32x4 *>(p + ((4 + g) ^ (c & 7)) * 16);
                     }
+                }
+            // (the bytes are replaced only after these reads)
+            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
         };
         auto product = [&](const u32x4 (&dv)[UNROLL][2][RB], int a, floatx4 (&to)[RB]) {
 #pragma unroll
@@ -125,22 +128,15 @@ __device__ __forceinline__ void shrink_tile(const T *__restrict__ x, int64_t ldx
         for (int k0 = wave * 64; k0 < K; k0 += step) {
             if (!held) fetch_x(k0);
             held = K <= step;
-            u32x4 d0[UNROLL][2][RB];
-            fetch_pool(pool0, rank0, d0, k0);
-            if (AHEAD && a1 >= 0) {
-                u32x4 d1[UNROLL][2][RB];
-                fetch_pool(pool1, rank1, d1, k0);
-                product(d0, a0, acc[0]);
-                product(d1, a1, acc[1]);
-            } else {
-                product(d0, a0, acc[0]);
-                if (!AHEAD && a1 >= 0) {
-                    fetch_pool(pool1, rank1, d0, k0);
-                    product(d0, a1, acc[1]);
-                }
+            u32x4 d[UNROLL][2][RB];
+            fetch_pool(pool0, rank0, d, k0);
+            product(d, a0, acc[0]);
+            if (a1 >= 0) {
+                fetch_pool(pool1, rank1, d, k0);
+                product(d, a1, acc[1]);
             }
         }
-        __syncthreads();  // (the previous adapters' sums have been read)
+        __syncthreads();  // (every wave has read its slices, which the sums replace)
 #pragma unroll
         for (int b = 0; b < RB; ++b) {
             part[(b * NW + wave) * 64 + lane] = acc[0][b];
@@ -181,7 +177,7 @@ template <class T, int RB, int NW, bool TRANS>
 __global__ void __launch_bounds__(NW * 64)
 shrink_kernel(ShrinkTask<T> p, ShrinkTask<T> q, const float *__restrict__ scale, const int32_t *__restrict__ ranks,
               const int32_t *__restrict__ index, int adapters, int R, int M) {
-    constexpr int SUMS = 2 * RB * NW * 64, SLICES = TRANS ? NW * kShrinkUnroll<TRANS, RB> * RB * 2048 / 16 : 0;
+    constexpr int SUMS = 2 * RB * NW * 64, SLICES = NW * kShrinkUnroll<RB> * RB * 2048 / 16;
     __shared__ floatx4 part[SUMS > SLICES ? SUMS : SLICES];
     if (blockIdx.y)
         shrink_tile<T, RB, NW, false>(q.x, q.ldx, q.down, scale, ranks, index, adapters, R, q.low, M, q.K, blockIdx.x,
@@ -191,28 +187,29 @@ shrink_kernel(ShrinkTask<T> p, ShrinkTask<T> q, const float *__restrict__ scale,
                                       part);
 }
 
-// ---- expand: a workgroup takes 64 tokens x 256 channels, a wave 32 x 128.
+// ---- expand: a workgroup takes 64 tokens x 128 channels, a wave 32 x 64.
 // The sums go through LDS as fp32 rows, so that base is read and out written
 // 16 bytes a lane; out may be base.
 // TRANS: the pool is [adapters][R][N] (the gradient's use of `down`).
+constexpr int kExpandTN = 2;
 template <class T, bool TRANS>
-__global__ void __launch_bounds__(256, 2)
+__global__ void __launch_bounds__(256, 3)
 expand_kernel(const T *__restrict__ up, const T *__restrict__ low, const int32_t *__restrict__ index,
               const int32_t *__restrict__ ranks, int adapters, int R, const T *base, int64_t ldb, T *out, int64_t ldo,
               int M, int N) {
-    constexpr int TN = 4, ROW = TN * 32 + 4;
+    constexpr int TN = kExpandTN, ROW = TN * 32 + 4, CPR = TN * 4, RPI = 64 / CPR, TURNS = 32 / RPI;
     __shared__ __attribute__((aligned(16))) float slab[4][32 * ROW];
     static_assert(32 * ROW * 4 >= TN * 4096, "the slab is low_rank_expand's scratch first");
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int h = lane >> 5, r = lane & 31;
-    const int tiles_n = (N + 255) / 256;
+    const int tiles_n = (N + TN * 64 - 1) / (TN * 64);
     const int b = xcd_remap(blockIdx.x, gridDim.x);
-    const int mw = (b / tiles_n) * 64 + (wave & 1) * 32, nw = (b % tiles_n) * 256 + (wave >> 1) * 128;
-    const int ch = (lane & 15) * 8, row0 = lane >> 4;
-    u32x4 old[8];
+    const int mw = (b / tiles_n) * 64 + (wave & 1) * 32, nw = (b % tiles_n) * TN * 64 + (wave >> 1) * TN * 32;
+    const int ch = lane % CPR * 8, row0 = lane / CPR;
+    u32x4 old[TURNS];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const int m = mw + i * 4 + row0, n = nw + ch;
+    for (int i = 0; i < TURNS; ++i) {
+        const int m = mw + i * RPI + row0, n = nw + ch;
         old[i] = u32x4{0, 0, 0, 0};
         if (base && m < M && n < N) old[i] = ld16(base + int64_t(m) * ldb + n);
     }
@@ -233,10 +230,10 @@ expand_kernel(const T *__restrict__ up, const T *__restrict__ low, const int32_t
         }
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const int m = mw + i * 4 + row0, n = nw + ch;
+    for (int i = 0; i < TURNS; ++i) {
+        const int m = mw + i * RPI + row0, n = nw + ch;
         if (m >= M || n >= N) continue;
-        const float *s = &slab[wave][(i * 4 + row0) * ROW + ch];
+        const float *s = &slab[wave][(i * RPI + row0) * ROW + ch];
         const typename Elem<T>::Vec o = __builtin_bit_cast(typename Elem<T>::Vec, old[i]);
         typename Elem<T>::Vec v;
 #pragma unroll
@@ -565,7 +562,7 @@ hipError_t shrink(const ShrinkTask<T> &p, const ShrinkTask<T> &q, const LowRank 
 template <class T, bool TRANS>
 hipError_t expand(const T *up, const T *low, const LowRank &lr, const void *base, int64_t ldb, void *out, int64_t ldo,
                   int M, int N, hipStream_t st) {
-    const int nb = (M + 63) / 64 * ((N + 255) / 256);
+    const int nb = (M + 63) / 64 * ((N + kExpandTN * 64 - 1) / (kExpandTN * 64));
     hipLaunchKernelGGL((expand_kernel<T, TRANS>), dim3(nb), dim3(256), 0, st, up, low, lr.index, lr.ranks, lr.adapters, lr.R,
                        static_cast<const T *>(base), ldb, static_cast<T *>(out), ldo, M, N);
     return hipGetLastError();
@@ -635,11 +632,12 @@ LowRankPlan low_rank_plan(int adapters, int R, int64_t M, int64_t N, int64_t K) 
     p.low = 0;
     p.dlow = p.low + up256(low_plane(M, R) * 4);
     p.part = p.dlow + up256(low_plane(M, R) * 4);
-    // Token ranges: about 1024 workgroups, of at least 256 tokens and at most what
-    // the list holds, in at most 256 MiB of slices.
+    // Token ranges: the workgroups that the CUs hold at once (by LDS), of at least
+    // 256 tokens and at most what the list holds, in at most 256 MiB of slices.
     const int64_t cols = (N + 127) / 128 + (K + 127) / 128;
+    const int64_t slots = 256 * (R <= 16 ? 3 : R <= 64 ? 2 : 1);
     const int64_t slice = int64_t(adapters) * R * (N + K) * 4;
-    int64_t want = (1024 + cols - 1) / cols;
+    int64_t want = slots / cols > 0 ? slots / cols : 1;
     const int64_t most = M > 256 ? M / 256 : 1;
     if (want > most) want = most;
     if (want > (int64_t(256) << 20) / slice) want = (int64_t(256) << 20) / slice;
