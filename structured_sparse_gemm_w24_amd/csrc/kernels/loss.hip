@@ -342,27 +342,39 @@ hipError_t product_cfg(const void *A, const void *W, const Extra &ex, int64_t M,
 // Tiles of the products.  One workgroup of any but the smallest fills a CU, so a
 // product takes ceil(tiles / 256) rounds, and the tile is the one with the least
 // rounds * cost of a round.  Costs relative to 256 x 256, from bf16 products of
-// M x N x K (MI355X, us for 256 x 256 / 256 x 128 / 128 x 128):
-// 8192 x 32000 x 1024 492 / 635 / 693 (16, 32 and 63 rounds), 6144 x 1024 x 10240
-// 169 / 120 / 145 (1, 1, 2), 10240 x 1024 x 6144 121 / 149 / 140 (1, 2, 3).
-// 256 x 128 has four compute waves of 128 x 64, which read less from LDS per
-// product than 128 x 128's 64 x 64, and four loader waves; without loaders it
-// ran 145-178 in the last two, as eight waves of 64 x 64 127-160; 256 x 256 as
-// four waves of 128 x 128 ran 555 in the first.
-// The transposing reads cost 256 x 256 more (10240 x 1024 x 6144 121 -> 141, 15104 x
-// 1024 x 6144 147 -> 160, where 256 x 128 takes 149 -> 158 and 165 -> 176).
-enum LossTile { LT_256, LT_256X128, LT_128, LT_64 };
-using CfgWideP = Cfg<2, 2, 4, 2, 3, 8, true, false, 0, true>;
+// M x N x K on MI355X (us; rounds in brackets):
+//                        256 x 256   256 x 128   192 x 128   128 x 128
+//   8192 x 32000 x 1024  492 (16)    635 (32)                693 (63)
+//   read by transposing reads:
+//   6144 x 1024 x 15104  322 (1)     187 (1)     163 (1)     205 (2)
+//   15104 x 1024 x 6144  161 (1)     181 (2)     194 (3)     191 (4)
+//   12608 x 768 x 8192   189 (1)     200 (2)     161 (2)     178 (3)
+// The narrower tiles have four compute waves of half the tile's rows and columns
+// (which read less from LDS per product than more, smaller ones: eight waves of
+// 64 x 64 ran 127 where four of 128 x 64 ran 120) and four loader waves, which the
+// transposing reads need: without them they cost 256 x 256 a tenth to a fifth.
+enum LossTile { LT_256, LT_256X128, LT_192X128, LT_128, LT_64, LT_TILES };
+struct LossTileShape {
+    int bm, bn, cost, cost_trans;
+};
+constexpr LossTileShape kLossTiles[LT_TILES] = {
+    {256, 256, 100, 115}, {256, 128, 68, 68}, {192, 128, 56, 56}, {128, 128, 40, 40}, {64, 64, 0, 0}};
+using Cfg256x128 = Cfg<2, 2, 4, 2, 3, 8, true, false, 0, true>;
+using Cfg192x128 = Cfg<2, 2, 3, 2, 4, 8, true, false, 0, true>;
+using Cfg128x128 = Cfg<2, 2, 2, 2, 4, 8, true, false, 0, true>;
 
 // Rounds times cost of the best tile, and the tile.
 long loss_cost(int64_t M, int64_t N, bool trans, LossTile *tile) {
     constexpr long kCUs = 256;
-    auto cost = [&](int bm, int bn, long unit) { return (tiles(int(M), int(N), bm, bn) + kCUs - 1) / kCUs * unit; };
-    const long c256 = cost(256, 256, trans ? 115 : 100), c2128 = cost(256, 128, 68), c128 = cost(128, 128, 41);
+    long best = 0;
+    for (int t = LT_256; t < LT_64; ++t) {
+        const LossTileShape &s = kLossTiles[t];
+        const long rounds = (tiles(int(M), int(N), s.bm, s.bn) + kCUs - 1) / kCUs;
+        const long c = rounds * (trans ? s.cost_trans : s.cost);
+        if (t == LT_256 || c < best) best = c, *tile = LossTile(t);
+    }
     if (tiles(int(M), int(N), 128, 128) < 96) *tile = LT_64;
-    else if (c256 <= c2128 && c256 <= c128) *tile = LT_256;
-    else *tile = c2128 <= c128 ? LT_256X128 : LT_128;
-    return c256 < c2128 ? (c256 < c128 ? c256 : c128) : (c2128 < c128 ? c2128 : c128);
+    return best;
 }
 LossTile loss_tile(int64_t M, int64_t N, bool trans) {
     LossTile t;
@@ -370,13 +382,7 @@ LossTile loss_tile(int64_t M, int64_t N, bool trans) {
     return t;
 }
 
-int64_t loss_tile_n(int64_t M, int64_t N) {
-    switch (loss_tile(M, N, false)) {
-        case LT_256: return 256;
-        case LT_64: return 64;
-        default: return 128;
-    }
-}
+int64_t loss_tile_n(int64_t M, int64_t N) { return kLossTiles[loss_tile(M, N, false)].bn; }
 
 // A [M][K] . W [N][K]^T with an epilogue; K a multiple of 64 unless both are transposed.
 template <class T, class Extra>
@@ -384,8 +390,9 @@ hipError_t product(const void *A, const void *W, const Extra &ex, int64_t M, int
     constexpr int KIND = __is_same(T, _Float16) ? DENSE_F16 : DENSE_BF16;
     switch (loss_tile(M, N, Extra::kTransW)) {
         case LT_256: return product_cfg<KIND, CfgBigDense<true>>(A, W, ex, M, N, K, st);
-        case LT_256X128: return product_cfg<KIND, CfgWideP>(A, W, ex, M, N, K, st);
-        case LT_128: return product_cfg<KIND, CfgSmallP<true, false, 0>>(A, W, ex, M, N, K, st);
+        case LT_256X128: return product_cfg<KIND, Cfg256x128>(A, W, ex, M, N, K, st);
+        case LT_192X128: return product_cfg<KIND, Cfg192x128>(A, W, ex, M, N, K, st);
+        case LT_128: return product_cfg<KIND, Cfg128x128>(A, W, ex, M, N, K, st);
         default: return product_cfg<KIND, CfgT64<true, false>>(A, W, ex, M, N, K, st);
     }
 }
