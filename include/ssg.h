@@ -475,7 +475,7 @@ int64_t low_rank_backward_workspace_bytes(int32_t adapters, int32_t R, int64_t M
  *   loss[m] = lse[m] - z[m][target[m]],  0 where target[m] == ignore_index
  * both fp32 [M], any reduction left to the caller.  A target that is neither
  * ignore_index nor in [0, V) makes its row's loss NaN (the device cannot refuse
- * the call).  M >= 0, V >= 1, 1 <= D < 2^20, x below 4 GiB.  Contiguous x and w
+ * the call).  0 <= M < 8000000, V >= 1, 1 <= D < 2^20, x below 4 GiB.  Contiguous x and w
  * (ld == D, D a multiple of 64) are read where they lie and must be 16-byte
  * aligned; others are first copied into the workspace
  * (linear_cross_entropy_workspace_bytes(.., backward = 0), 16-byte aligned). */

@@ -245,7 +245,7 @@ bool packs(int64_t ld, int64_t D) { return ld != D || D % 64 != 0; }
 
 bool plain_loss(int32_t dtype, int64_t M, int64_t V, int64_t D) {
     return (dtype == SSG_DT_F16 || dtype == SSG_DT_BF16) && M >= 0 && V >= 1 && D >= 1 && fits_int(M) && fits_int(V) &&
-           fits_int(D) && M * ((D + 63) / 64 * 128) < (int64_t(1) << 32) && D < (1 << 20) &&
+           fits_int(D) && M * ((D + 63) / 64 * 128) < (int64_t(1) << 32) && D < (1 << 20) && M < 8000000 &&
            (M + 63) / 64 * ((V + 63) / 64) < (int64_t(1) << 31);
 }
 
@@ -254,7 +254,7 @@ int check_loss(const char *fn, int32_t dtype, const void *x, int64_t ldx, const 
     if (dtype != SSG_DT_F16 && dtype != SSG_DT_BF16)
         return ssg::fail(SSG_EINVAL, "%s: dtype %d must be fp16 or bf16", fn, dtype);
     if (!plain_loss(dtype, M, V, D))
-        return ssg::fail(SSG_EINVAL, "%s: M=%lld V=%lld D=%lld (need 0 <= M, 1 <= V, 1 <= D < 2^20, x below 4 GiB)", fn,
+        return ssg::fail(SSG_EINVAL, "%s: M=%lld V=%lld D=%lld (need 0 <= M < 8000000, 1 <= V, 1 <= D < 2^20, x below 4 GiB)", fn,
                          (long long)M, (long long)V, (long long)D);
     if (bad_ld(ldx, M, D) || bad_ld(ldw, V, D))
         return ssg::fail(SSG_EINVAL, "%s: a row stride is shorter than D=%lld", fn, (long long)D);

@@ -690,18 +690,15 @@ gemm_kernel(const uint8_t *__restrict__ A, const uint8_t *__restrict__ Wv, const
     static_assert(RPI * CPR == kWave, "row segment must tile a wave");
     __syncthreads();  // every wave is done reading the stage buffers
     uint8_t *const Cb = reinterpret_cast<uint8_t *>(C) + (EPI == EPI_PART ? int64_t(blockIdx.y) * M * N * OB : 0);
-    // (with after(), recomputed: the main loop has no register to keep it in)
-    const int row_of_wave = [&]() {
-        if constexpr (Extra::kAfter) {
-            int t = threadIdx.x;
-            asm volatile("" : "+v"(t));
-            return ((t >> 6) % LY::NW) % WM * (TM * 32);
-        } else {
-            return wm * TM * 32;
-        }
-    }();
+    // (with after(), recomputed: the main loop has no registers to keep them in)
+    [[maybe_unused]] auto late = [](int waves, int each) {
+        int t = threadIdx.x;
+        asm volatile("" : "+v"(t));
+        return (waves ? (t >> 6) % LY::NW % waves : (t >> 6) % LY::NW / WM) * each;
+    };
+    const int row_of_wave = Extra::kAfter ? late(WM, TM * 32) : wm * TM * 32;
     uint8_t *ew = smem + wave * EPASS * EWAVE;  // (compute waves)
-    const int nw = n0 + wn * TN * 32;  // first channel of the wave
+    const int nw = n0 + (Extra::kAfter ? late(0, TN * 32) : wn * TN * 32);  // first channel of the wave
 #pragma unroll
     for (int tp = 0; tp < TM; tp += EPASS) {
         if (!loader) {

@@ -511,7 +511,9 @@ LossPlan loss_plan(int64_t M, int64_t V, int64_t D, bool pack_x, bool pack_w, bo
         // fill their rounds best
         int64_t most = (int64_t(256) << 20) / (2 * (M > 0 ? M : 1)) / 256 * 256;
         if (most < 2048) most = 2048;
-        const int64_t reach = (int64_t(4000) << 20) / (p.dp * 2) / 256 * 256;  // the products' 4 GiB
+        // (w's piece and G inside the products' 4 GiB)
+        const int64_t widest = p.dp > M ? p.dp : M;
+        const int64_t reach = (int64_t(4000) << 20) / (widest * 2) / 256 * 256;
         if (most > reach) most = reach;
         const int64_t least = (V + most - 1) / most;
         double best = 0.0;

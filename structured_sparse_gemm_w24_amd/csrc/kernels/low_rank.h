@@ -78,6 +78,47 @@ __device__ __forceinline__ int low_rank_of(const int32_t *ranks, int a, int R) {
     return r < 0 ? 0 : r > R ? R : r;
 }
 
+// Whether one of eight 16-bit elements is an infinity or NaN.
+template <class T>
+__device__ __forceinline__ bool not_finite(u32x4 v) {
+    constexpr uint32_t kExp = __is_same(T, _Float16) ? 0x7c00u : 0x7f80u;
+    bool bad = false;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        bad = bad || (v[i] & kExp) == kExp || ((v[i] >> 16) & kExp) == kExp;
+    return bad;
+}
+
+// acc += w . (hi + lo), with hi and lo zero for the tokens (lanes) without `use`.
+// An adapter whose weights are not finite must not reach the tokens of other
+// requests through 0 * inf: such channels (rows of w) are taken out of the
+// product, and the adapter's own tokens get NaN in them.
+template <class T, int TN, int TM>
+__device__ __forceinline__ void add_low(floatx16 (&acc)[TN][TM], int tm, u32x4 (&w)[TN], u32x4 hi, u32x4 lo,
+                                        const uint32_t (&broken)[TN], bool use) {
+    const int h = (threadIdx.x & 63) >> 5;
+#pragma unroll
+    for (int tn = 0; tn < TN; ++tn) {
+        acc[tn][tm] = mfma32<T>(w[tn], hi, acc[tn][tm]);
+        acc[tn][tm] = mfma32<T>(w[tn], lo, acc[tn][tm]);
+        if (broken[tn]) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                if (use && (broken[tn] >> (8 * (i / 4) + 4 * h + i % 4) & 1)) acc[tn][tm][i] = __builtin_nanf("");
+        }
+    }
+}
+template <class T, int TN>
+__device__ __forceinline__ void take_out(u32x4 (&w)[TN], uint32_t (&broken)[TN]) {
+#pragma unroll
+    for (int tn = 0; tn < TN; ++tn) {
+        const bool bad = not_finite<T>(w[tn]);
+        const uint64_t b = __ballot(bad);
+        broken[tn] = __builtin_amdgcn_readfirstlane(uint32_t(b) | uint32_t(b >> 32));
+        if (b) w[tn] = bad ? u32x4{0, 0, 0, 0} : w[tn];
+    }
+}
+
 // Elements of one plane, and the place of 8 slots from r (a multiple of 8) of token m.
 __host__ __device__ inline int64_t low_plane(int64_t M, int R) { return (M + 31) / 32 * 32 * ((R + 15) / 16 * 16); }
 __device__ __forceinline__ int64_t low_at(int64_t m, int r, int R) {
@@ -219,15 +260,11 @@ __device__ __forceinline__ void low_rank_expand(floatx16 (&acc)[TN][TM], const T
                                            rank - k - 8 * h);
                         }
                     }
+                    uint32_t broken[TN];
+                    take_out<T>(w, broken);
 #pragma unroll
-                    for (int tm = 0; tm < TM; ++tm) {
-                        const u32x4 l = lo_unscaled<T>(lo[s][tm]);
-#pragma unroll
-                        for (int tn = 0; tn < TN; ++tn) {
-                            acc[tn][tm] = mfma32<T>(w[tn], hi[s][tm], acc[tn][tm]);
-                            acc[tn][tm] = mfma32<T>(w[tn], l, acc[tn][tm]);
-                        }
-                    }
+                    for (int tm = 0; tm < TM; ++tm)
+                        add_low<T>(acc, tm, w, hi[s][tm], lo_unscaled<T>(lo[s][tm]), broken, sel[tm]);
                 }
             }
         }

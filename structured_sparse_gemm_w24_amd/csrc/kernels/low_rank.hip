@@ -320,7 +320,7 @@ tokens_kernel(const T *__restrict__ x, int64_t ldx, const T *__restrict__ down, 
 // part of `low` have accumulators of their own.  Ranges write fp32 slices
 // [range][adapter][R][C] that a second launch sums in order, of the adapters
 // only that the range has.
-constexpr int kListCap = 2048;  // tokens of a range, at most
+constexpr int kListCap = 2048;  // tokens listed at a time
 
 // Zeros for a workgroup's tile of one adapter's gradient: 128 columns from c0.
 template <class T>
@@ -356,150 +356,163 @@ wgrad_kernel(WgradTask<T> p, WgradTask<T> q, const int32_t *__restrict__ index, 
     if (marks)
         for (int a = tid; a < adapters; a += 256) present[int64_t(slice) * adapters + a] = 0;
 
-    // this thread's tokens of the range
+    // this thread's tokens of the range's piece c (only a large pool's single range,
+    // kept that long for its slices' size, has more than one)
+    const int pieces = (last - first + kListCap - 1) / kListCap;
     int mine[TURNS];
+    auto fetch = [&](int c) {
 #pragma unroll
-    for (int i = 0; i < TURNS; ++i) {
-        const int m = first + i * 256 + tid;
-        mine[i] = m < last ? index[m] : -1;
-        if (mine[i] >= adapters) mine[i] = -1;
-    }
+        for (int i = 0; i < TURNS; ++i) {
+            const int m = first + c * kListCap + i * 256 + tid;
+            mine[i] = m < last ? index[m] : -1;
+            if (mine[i] >= adapters) mine[i] = -1;
+        }
+    };
+    fetch(0);
+    const int g = lane >> 4, j16 = lane & 15;
+    const int64_t plane = low_plane(M, R);
+    const uint32_t smem_addr = lds_address(smem);
+    const int per_stage = 2 + (2 * RB - wave + 3) / 4;  // loads of this wave
     constexpr int kNone = 0x7fffffff;
     int turn = 0, next = 0;  // adapters below `next` are done
     for (;; turn ^= 1) {
-    // the least adapter that is not done, and its tokens in order
-    int a = kNone;
+        // the least adapter that is not done
+        int a = kNone;
+        for (int c = 0; c < max(pieces, 1); ++c) {
+            if (pieces > 1) fetch(c);
 #pragma unroll
-    for (int i = 0; i < TURNS; ++i)
-        if (mine[i] >= next) a = min(a, mine[i]);
-#pragma unroll
-    for (int d = 32; d > 0; d >>= 1) a = min(a, __shfl_xor(a, d, 64));
-    if (lane == 0) least[turn][wave] = a;
-    __syncthreads();
-    a = min(min(least[turn][0], least[turn][1]), min(least[turn][2], least[turn][3]));
-    a = __builtin_amdgcn_readfirstlane(a);
-    if (!w.part) {
-        // the one range writes every adapter: zeros for those without tokens
-        const int upto = a == kNone ? adapters : a;
-        for (int z = next; z < upto; ++z) zero_tile(w.out + int64_t(z) * R * C, w.rows_c, c0, C, R);
-    }
-    if (a == kNone) return;
-    next = a + 1;
-    if (marks && tid == 0) present[int64_t(slice) * adapters + a] = 1;
-    int total = 0;
-    {
-        uint64_t votes[TURNS];
-#pragma unroll
-        for (int i = 0; i < TURNS; ++i) {
-            votes[i] = __ballot(mine[i] == a);
-            if (lane == 0) counts[wave][i] = __builtin_popcountll(votes[i]);
+            for (int i = 0; i < TURNS; ++i)
+                if (mine[i] >= next) a = min(a, mine[i]);
         }
+#pragma unroll
+        for (int d = 32; d > 0; d >>= 1) a = min(a, __shfl_xor(a, d, 64));
+        if (lane == 0) least[turn][wave] = a;
         __syncthreads();
+        a = min(min(least[turn][0], least[turn][1]), min(least[turn][2], least[turn][3]));
+        a = __builtin_amdgcn_readfirstlane(a);
+        if (!w.part) {
+            // the one range writes every adapter: zeros for those without tokens
+            const int upto = a == kNone ? adapters : a;
+            for (int z = next; z < upto; ++z) zero_tile(w.out + int64_t(z) * R * C, w.rows_c, c0, C, R);
+        }
+        if (a == kNone) return;
+        next = a + 1;
+        if (marks && tid == 0) present[int64_t(slice) * adapters + a] = 1;
+        floatx4 acc[2][RB][2];
 #pragma unroll
-        for (int i = 0; i < TURNS; ++i)
+        for (int s = 0; s < 2; ++s)
 #pragma unroll
-            for (int v = 0; v < 4; ++v) {
-                if (v == wave && mine[i] == a)
-                    list[total + __builtin_popcountll(votes[i] & ((uint64_t(1) << lane) - 1))] = first + i * 256 + tid;
-                total += counts[v][i];
+            for (int b = 0; b < RB; ++b) acc[s][b][0] = acc[s][b][1] = floatx4{0.f, 0.f, 0.f, 0.f};
+
+        for (int c = 0; c < pieces; ++c) {
+            // its tokens of the piece, in order
+            if (pieces > 1) fetch(c);
+            int total = 0;
+            {
+                uint64_t votes[TURNS];
+#pragma unroll
+                for (int i = 0; i < TURNS; ++i) {
+                    votes[i] = __ballot(mine[i] == a);
+                    if (lane == 0) counts[wave][i] = __builtin_popcountll(votes[i]);
+                }
+                __syncthreads();
+#pragma unroll
+                for (int i = 0; i < TURNS; ++i)
+#pragma unroll
+                    for (int v = 0; v < 4; ++v) {
+                        if (v == wave && mine[i] == a)
+                            list[total + __builtin_popcountll(votes[i] & ((uint64_t(1) << lane) - 1))] =
+                                first + c * kListCap + i * 256 + tid;
+                        total += counts[v][i];
+                    }
+                __syncthreads();
             }
-        __syncthreads();
-    }
-    total = __builtin_amdgcn_readfirstlane(total);
+            total = __builtin_amdgcn_readfirstlane(total);
 
-    const int g = lane >> 4, j16 = lane & 15;
-    floatx4 acc[2][RB][2];
+            // Direct-to-LDS loads of a stage: 8 KiB of z (row = 4 q + lane/16, 16-byte
+            // chunk lane%16, swizzled), then 2 * RB KiB of low.
+            auto issue = [&](int s) {
+                uint8_t *base = smem + (s % NB) * STAGE;
 #pragma unroll
-    for (int s = 0; s < 2; ++s)
-#pragma unroll
-        for (int b = 0; b < RB; ++b) acc[s][b][0] = acc[s][b][1] = floatx4{0.f, 0.f, 0.f, 0.f};
-
-    // Direct-to-LDS loads of a stage: 8 KiB of z (row = 4 q + lane/16, 16-byte
-    // chunk lane%16, swizzled), then 2 * RB KiB of low.
-    const int64_t plane = low_plane(M, R);
-    auto issue = [&](int s) {
-        uint8_t *base = smem + (s % NB) * STAGE;
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const int qq = j * 4 + wave, row = 4 * qq + g;
-            const int at = s * 32 + row, col = c0 + (j16 ^ (2 * (row & 3))) * 8;
-            const void *src = g_low_zero;
-            if (at < total && col < C) src = w.z + int64_t(list[at]) * w.ldz + col;
-            tw_dma16(src, base + qq * 1024);
-        }
-        for (int qq = wave; qq < 2 * RB; qq += 4) {
-            const int part = qq / RB, byte = (qq % RB) * 1024 + lane * 16;
-            const int row = byte / (RT * 2), r = byte % (RT * 2) / 2;
-            const int at = s * 32 + row;
-            const void *src = g_low_zero;
-            if (at < total && r < R) src = w.low + part * plane + low_at(list[at], r, R);
-            tw_dma16(src, base + Z_STAGE + qq * 1024);
-        }
-    };
-    const int S = (total + 31) / 32;
-    const uint32_t smem_addr = lds_address(smem);
-    const int per_stage = 2 + (2 * RB - wave + 3) / 4;  // loads of this wave
-    for (int s = 0; s < NB - 1 && s < S; ++s) issue(s);
-    for (int s = 0; s < S; ++s) {
-        // stage s has landed (younger ones may be in flight), and everyone is done with stage s - 1
-        tw_wait_barrier(min(NB - 2, S - 1 - s) * per_stage);
-        if (s + NB - 1 < S) issue(s + NB - 1);
-        const uint32_t base = smem_addr + (s % NB) * STAGE;
-        const int row = 8 * g + (j16 >> 2);
-        uint32_t z_at[2];
-#pragma unroll
-        for (int cb = 0; cb < 2; ++cb) {
-            const int col = wave * 32 + cb * 16 + 4 * (j16 & 3);
-            z_at[cb] = base + row * 256 + ((col >> 3) ^ (2 * (row & 3))) * 16 + (col & 7) * 2;
-        }
-        const uint32_t l_at = base + Z_STAGE + row * (RT * 2) + 4 * (j16 & 3) * 2;
-        u32x4 zv[2], lv[2][RB];
-        read_tr(z_at[0], z_at[0] + 1024, z_at[1], z_at[1] + 1024, zv[0], zv[1]);
-#pragma unroll
-        for (int b = 0; b < RB; ++b) {
-            const uint32_t hi = l_at + b * 32, lo = hi + L_STAGE;
-            read_tr(hi, hi + RT * 8, lo, lo + RT * 8, lv[0][b], lv[1][b]);
-        }
-#pragma unroll
-        for (int part = 0; part < 2; ++part)
-#pragma unroll
-            for (int b = 0; b < RB; ++b)
-#pragma unroll
-                for (int cb = 0; cb < 2; ++cb) acc[part][b][cb] = mfma16<T>(lv[part][b], zv[cb], acc[part][b][cb]);
-    }
-
-    // lane: rank slots 16 b + 4 g + i of column c0 + 32 wave + 16 cb + j16
-#pragma unroll
-    for (int b = 0; b < RB; ++b)
-#pragma unroll
-        for (int cb = 0; cb < 2; ++cb) {
-            const int c = c0 + wave * 32 + cb * 16 + j16, r = b * 16 + 4 * g;
-            if (c >= C || r >= R) continue;
-            float v[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) v[i] = fmaf(acc[1][b][cb][i], 1.0f / LowSplit<T>::kLoScale, acc[0][b][cb][i]);
-            const int64_t mat = int64_t(R) * C;
-            if (w.part) {
-                float *o = w.part + (int64_t(slice) * adapters + a) * mat;
-                if (w.rows_c) {
-                    __builtin_memcpy(o + int64_t(c) * R + r, v, 16);
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) o[int64_t(r + i) * C + c] = v[i];
+                for (int j = 0; j < 2; ++j) {
+                    const int qq = j * 4 + wave, row = 4 * qq + g;
+                    const int at = s * 32 + row, col = c0 + (j16 ^ (2 * (row & 3))) * 8;
+                    const void *src = g_low_zero;
+                    if (at < total && col < C) src = w.z + int64_t(list[at]) * w.ldz + col;
+                    tw_dma16(src, base + qq * 1024);
                 }
-            } else {
-                T *o = w.out + int64_t(a) * mat;
-                if (w.rows_c) {
-                    T t[4];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) t[i] = T(v[i]);
-                    __builtin_memcpy(o + int64_t(c) * R + r, t, 8);
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) o[int64_t(r + i) * C + c] = T(v[i]);
+                for (int qq = wave; qq < 2 * RB; qq += 4) {
+                    const int part = qq / RB, byte = (qq % RB) * 1024 + lane * 16;
+                    const int row = byte / (RT * 2), r = byte % (RT * 2) / 2;
+                    const int at = s * 32 + row;
+                    const void *src = g_low_zero;
+                    if (at < total && r < R) src = w.low + part * plane + low_at(list[at], r, R);
+                    tw_dma16(src, base + Z_STAGE + qq * 1024);
                 }
+            };
+            const int S = (total + 31) / 32;
+            for (int s = 0; s < NB - 1 && s < S; ++s) issue(s);
+            for (int s = 0; s < S; ++s) {
+                // stage s has landed (younger ones may be in flight), and everyone is done with stage s - 1
+                tw_wait_barrier(min(NB - 2, S - 1 - s) * per_stage);
+                if (s + NB - 1 < S) issue(s + NB - 1);
+                const uint32_t base = smem_addr + (s % NB) * STAGE;
+                const int row = 8 * g + (j16 >> 2);
+                uint32_t z_at[2];
+#pragma unroll
+                for (int cb = 0; cb < 2; ++cb) {
+                    const int col = wave * 32 + cb * 16 + 4 * (j16 & 3);
+                    z_at[cb] = base + row * 256 + ((col >> 3) ^ (2 * (row & 3))) * 16 + (col & 7) * 2;
+                }
+                const uint32_t l_at = base + Z_STAGE + row * (RT * 2) + 4 * (j16 & 3) * 2;
+                u32x4 zv[2], lv[2][RB];
+                read_tr(z_at[0], z_at[0] + 1024, z_at[1], z_at[1] + 1024, zv[0], zv[1]);
+#pragma unroll
+                for (int b = 0; b < RB; ++b) {
+                    const uint32_t hi = l_at + b * 32, lo = hi + L_STAGE;
+                    read_tr(hi, hi + RT * 8, lo, lo + RT * 8, lv[0][b], lv[1][b]);
+                }
+#pragma unroll
+                for (int part = 0; part < 2; ++part)
+#pragma unroll
+                    for (int b = 0; b < RB; ++b)
+#pragma unroll
+                        for (int cb = 0; cb < 2; ++cb) acc[part][b][cb] = mfma16<T>(lv[part][b], zv[cb], acc[part][b][cb]);
             }
         }
+
+        // lane: rank slots 16 b + 4 g + i of column c0 + 32 wave + 16 cb + j16
+#pragma unroll
+        for (int b = 0; b < RB; ++b)
+#pragma unroll
+            for (int cb = 0; cb < 2; ++cb) {
+                const int c = c0 + wave * 32 + cb * 16 + j16, r = b * 16 + 4 * g;
+                if (c >= C || r >= R) continue;
+                float v[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) v[i] = fmaf(acc[1][b][cb][i], 1.0f / LowSplit<T>::kLoScale, acc[0][b][cb][i]);
+                const int64_t mat = int64_t(R) * C;
+                if (w.part) {
+                    float *o = w.part + (int64_t(slice) * adapters + a) * mat;
+                    if (w.rows_c) {
+                        __builtin_memcpy(o + int64_t(c) * R + r, v, 16);
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) o[int64_t(r + i) * C + c] = v[i];
+                    }
+                } else {
+                    T *o = w.out + int64_t(a) * mat;
+                    if (w.rows_c) {
+                        T t[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) t[i] = T(v[i]);
+                        __builtin_memcpy(o + int64_t(c) * R + r, t, 8);
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) o[int64_t(r + i) * C + c] = T(v[i]);
+                    }
+                }
+            }
     }
 }
 
@@ -633,17 +646,20 @@ LowRankPlan low_rank_plan(int adapters, int R, int64_t M, int64_t N, int64_t K) 
     p.dlow = p.low + up256(low_plane(M, R) * 4);
     p.part = p.dlow + up256(low_plane(M, R) * 4);
     // Token ranges: the workgroups that the CUs hold at once (by LDS), of at least
-    // 256 tokens and at most what the list holds, in at most 256 MiB of slices.
+    // 256 tokens and at most what the list holds, in at most 256 MiB of slices;
+    // one range if a large pool's slices do not fit.
     const int64_t cols = (N + 127) / 128 + (K + 127) / 128;
     const int64_t slots = 256 * (R <= 16 ? 3 : R <= 64 ? 2 : 1);
     const int64_t slice = int64_t(adapters) * R * (N + K) * 4;
     int64_t want = slots / cols > 0 ? slots / cols : 1;
     const int64_t most = M > 256 ? M / 256 : 1;
     if (want > most) want = most;
-    if (want > (int64_t(256) << 20) / slice) want = (int64_t(256) << 20) / slice;
+    const int64_t fit = (int64_t(256) << 20) / slice, cap = (M + kListCap - 1) / kListCap;
+    if (want < cap) want = cap;
+    if (want > fit) want = fit < cap ? 1 : fit;  // (one range if those of the list's length do not fit)
     int64_t range = want > 0 ? (M + want - 1) / want : M;
     range = (range + 31) / 32 * 32;
-    if (range > kListCap) range = kListCap;
+    if (want > 1 && range > kListCap) range = kListCap;
     if (range < 32) range = 32;
     p.range = int(range);
     p.slices = int(M > 0 ? (M + range - 1) / range : 1);

@@ -118,20 +118,18 @@ struct LowRankAfter {
                                 *reinterpret_cast<const u32x4 *>(smem + LOW + u * UP + (row << (ws + 4)) + piece * 16),
                                 rank - k - 8 * h);
                         }
+                        uint32_t broken[TN];
+                        take_out<_Float16>(w, broken);
 #pragma unroll
                         for (int tm = 0; tm < TM; ++tm) {
                             if (__ballot(mine[tm] == a) == 0) continue;
                             const uint8_t *p = smem + ((wm * TM + tm) * 4 + s) * 1024 + lane * 16;
                             u32x4 hi = *reinterpret_cast<const u32x4 *>(p);
                             u32x4 lo = *reinterpret_cast<const u32x4 *>(p + BM / 32 * 4096);
-                            const bool use = mine[tm] == a && k + 8 * h < R;
-                            hi = use ? hi : u32x4{0, 0, 0, 0};
-                            lo = use ? lo_unscaled<_Float16>(lo) : u32x4{0, 0, 0, 0};
-#pragma unroll
-                            for (int tn = 0; tn < TN; ++tn) {
-                                acc[tn][tm] = mfma32<_Float16>(w[tn], hi, acc[tn][tm]);
-                                acc[tn][tm] = mfma32<_Float16>(w[tn], lo, acc[tn][tm]);
-                            }
+                            const bool use = mine[tm] == a, held = use && k + 8 * h < R;
+                            hi = held ? hi : u32x4{0, 0, 0, 0};
+                            lo = held ? lo_unscaled<_Float16>(lo) : u32x4{0, 0, 0, 0};
+                            add_low<_Float16>(acc, tm, w, hi, lo, broken, use);
                         }
                     }
                 }

@@ -98,7 +98,9 @@ def test_add(lib, gpu, dtype, m, n, k, r, a, index):
 
 
 @pytest.mark.parametrize("dtype", ["f16", "bf16"])
-@pytest.mark.parametrize("m,n,k,r,a,index", SHAPES + [(6200, 256, 136, 16, 2, "runs"), (4100, 64, 64, 8, 1, 0)])
+@pytest.mark.parametrize("m,n,k,r,a,index", SHAPES + [
+    (6200, 256, 136, 16, 2, "runs"), (4100, 64, 64, 8, 1, 0), (5000, 1024, 512, 128, 400, "runs"),
+    (4500, 2048, 1024, 64, 500, "mixed")])
 def test_backward(lib, gpu, dtype, m, n, k, r, a, index):
     c = make(m * 3 + n + k, dtype, m, n, k, r, a, index)
     got = lib.low_rank_backward(c["dy"], c["x"], c["down"], c["up"], c["index"], c["scale"], c["ranks"],
@@ -148,6 +150,35 @@ def test_pool_slots_past_the_rank_are_not_used(lib, gpu, m):
     bwd = lambda d, u: lib.low_rank_backward(c["dy"], c["x"], d, u, c["index"], c["scale"], c["ranks"], c["xbase"])
     for p, q in zip(bwd(down, up), bwd(c["down"], c["up"])):
         assert torch.equal(p, q) and torch.isfinite(p).all()
+
+
+@pytest.mark.parametrize("m", [30, 150, 700])
+def test_a_broken_adapter_stays_with_its_tokens(lib, gpu, m):
+    """One request's adapter holds NaN and infinities: no other token changes, in any form."""
+    import torch
+    c = make(15, "f16", m, 256, 128, 16, 5, "mixed")
+    w = wl.random_24_f16(np.random.default_rng(3), 1, 128, 256)["Wp"]
+    vals, meta = lib.w24_pack_f16(w)
+    vals, meta = torch.from_numpy(vals).cuda(), torch.from_numpy(meta.view(np.int32)).cuda()
+    c["ranks"][2] = 16
+    others = c["index"] != 2
+    x = c["x"].clone()
+    x[~others, 7] = float("inf")  # and inputs of its own that are not finite
+    down, up = c["down"].clone(), c["up"].clone()
+    down[2, 3] = float("nan")
+    up[2, 5:9] = float("inf")
+    rest = (c["index"], c["scale"], c["ranks"])
+
+    def outputs(x, down, up):
+        return (lib.low_rank_add(c["base"], x, down, up, *rest), lib.w24_low_rank_gemm_f16(x, vals, meta, down, up, *rest),
+                *lib.low_rank_backward(c["dy"], x, down, up, *rest, base=c["xbase"]))
+    good, bad = outputs(c["x"], c["down"], c["up"]), outputs(x, down, up)
+    for p, q in zip(good[:3], bad[:3]):
+        assert torch.equal(p[others], q[others])
+        assert not torch.isfinite(q[~others].float()).all()
+    for p, q in zip(good[3:], bad[3:]):
+        keep = [0, 1, 3, 4]
+        assert torch.equal(p[keep], q[keep])
 
 
 @pytest.mark.parametrize("m", [40, 260])
