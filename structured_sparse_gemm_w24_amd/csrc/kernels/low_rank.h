@@ -89,33 +89,33 @@ __device__ __forceinline__ bool not_finite(u32x4 v) {
     return bad;
 }
 
-// acc += w . (hi + lo), with hi and lo zero for the tokens (lanes) without `use`.
 // An adapter whose weights are not finite must not reach the tokens of other
-// requests through 0 * inf: such channels (rows of w) are taken out of the
-// product, and the adapter's own tokens get NaN in them.
-template <class T, int TN, int TM>
-__device__ __forceinline__ void add_low(floatx16 (&acc)[TN][TM], int tm, u32x4 (&w)[TN], u32x4 hi, u32x4 lo,
-                                        const uint32_t (&broken)[TN], bool use) {
+// requests through 0 * inf: its broken channels (rows of w) are taken out of the
+// product, and its own tokens get NaN in them afterwards.  take_out() says whether
+// the wave has such channels; the products between the two calls stay one block
+// of independent matrix instructions.
+template <class T, int TN>
+__device__ __forceinline__ bool take_out(u32x4 (&w)[TN], bool (&bad)[TN]) {
+    bool any = false;
+#pragma unroll
+    for (int tn = 0; tn < TN; ++tn) bad[tn] = not_finite<T>(w[tn]), any = any || bad[tn];
+    if (__ballot(any) == 0) return false;
+#pragma unroll
+    for (int tn = 0; tn < TN; ++tn) w[tn] = bad[tn] ? u32x4{0, 0, 0, 0} : w[tn];
+    return true;
+}
+template <int TN, int TM>
+__device__ __forceinline__ void poison(floatx16 (&acc)[TN][TM], const bool (&bad)[TN], const bool (&use)[TM]) {
     const int h = (threadIdx.x & 63) >> 5;
 #pragma unroll
     for (int tn = 0; tn < TN; ++tn) {
-        acc[tn][tm] = mfma32<T>(w[tn], hi, acc[tn][tm]);
-        acc[tn][tm] = mfma32<T>(w[tn], lo, acc[tn][tm]);
-        if (broken[tn]) {
+        const uint64_t b = __ballot(bad[tn]);
+        const uint32_t rows = uint32_t(b) | uint32_t(b >> 32);
+#pragma unroll
+        for (int tm = 0; tm < TM; ++tm)
 #pragma unroll
             for (int i = 0; i < 16; ++i)
-                if (use && (broken[tn] >> (8 * (i / 4) + 4 * h + i % 4) & 1)) acc[tn][tm][i] = __builtin_nanf("");
-        }
-    }
-}
-template <class T, int TN>
-__device__ __forceinline__ void take_out(u32x4 (&w)[TN], uint32_t (&broken)[TN]) {
-#pragma unroll
-    for (int tn = 0; tn < TN; ++tn) {
-        const bool bad = not_finite<T>(w[tn]);
-        const uint64_t b = __ballot(bad);
-        broken[tn] = __builtin_amdgcn_readfirstlane(uint32_t(b) | uint32_t(b >> 32));
-        if (b) w[tn] = bad ? u32x4{0, 0, 0, 0} : w[tn];
+                if (use[tm] && (rows >> (8 * (i / 4) + 4 * h + i % 4) & 1)) acc[tn][tm][i] = __builtin_nanf("");
     }
 }
 
@@ -260,11 +260,18 @@ __device__ __forceinline__ void low_rank_expand(floatx16 (&acc)[TN][TM], const T
                                            rank - k - 8 * h);
                         }
                     }
-                    uint32_t broken[TN];
-                    take_out<T>(w, broken);
+                    bool bad[TN];
+                    const bool some = take_out<T>(w, bad);
 #pragma unroll
-                    for (int tm = 0; tm < TM; ++tm)
-                        add_low<T>(acc, tm, w, hi[s][tm], lo_unscaled<T>(lo[s][tm]), broken, sel[tm]);
+                    for (int tm = 0; tm < TM; ++tm) {
+                        const u32x4 l = lo_unscaled<T>(lo[s][tm]);
+#pragma unroll
+                        for (int tn = 0; tn < TN; ++tn) {
+                            acc[tn][tm] = mfma32<T>(w[tn], hi[s][tm], acc[tn][tm]);
+                            acc[tn][tm] = mfma32<T>(w[tn], l, acc[tn][tm]);
+                        }
+                    }
+                    if (some) poison(acc, bad, sel);
                 }
             }
         }

@@ -21,13 +21,19 @@ struct LowRankAfter {
     // copies leave and arrive together at the end of a tile, so their bytes set
     // their time: read by every wave for itself they were 256 KiB a 256 x 256 tile
     // and 64 slots, instead of 96.
+    // An adapter whose weights are not finite must not reach the tokens of other
+    // requests through 0 * inf: such pieces are zeroed in LDS before use, and the
+    // adapter's own tokens get NaN in those channels at the end (noted in `hit`, so
+    // that the accumulators meet nothing but matrix instructions inside the loops:
+    // a check there cost 6 to 17 of 45 us at 4096 x 1024 x 4096).
     template <class CF, int SMEM>
     __device__ __forceinline__ void after(floatx16 (&acc)[CF::TN][CF::TM], const int32_t *at, uint8_t *smem,
                                           bool loader, int m0, int n0, int M, int N) const {
         constexpr int TN = CF::TN, TM = CF::TM, NW = CF::WM * CF::WN, WAVES = CF::PROD ? 2 * NW : NW;
         constexpr int BM = CF::WM * TM * 32, BN = CF::WN * TN * 32, SEEN = (BM + 63) / 64;
         constexpr int LOW = BM * 256, UP = BN * 128;  // 64 slots: both planes; one adapter's rows
-        static_assert(LOW + 2 * UP <= SMEM, "scratch must fit in the stage ring");
+        static_assert(LOW + 2 * UP + BN / 4 <= SMEM, "scratch must fit in the stage ring");
+        uint32_t *broken = reinterpret_cast<uint32_t *>(smem + LOW + 2 * UP);  // [2][BN / 32] channel bits
         // (opaque, so that nothing derived from it is kept in registers across the main loop)
         int tid = threadIdx.x;
         asm volatile("" : "+v"(tid));
@@ -48,6 +54,11 @@ struct LowRankAfter {
                     for (int i = 0; i < 16; ++i) acc[tn][tm][i] = __builtin_nanf("");
             }
         }
+        uint32_t hit[TN][TM];  // channels whose weights of this token's adapter are broken
+#pragma unroll
+        for (int tn = 0; tn < TN; ++tn)
+#pragma unroll
+            for (int tm = 0; tm < TM; ++tm) hit[tn][tm] = 0;
 #pragma unroll 1
         for (int k0 = 0; k0 < R; k0 += 64) {
             const int steps = min(4, ks - k0 / 16);
@@ -75,6 +86,7 @@ struct LowRankAfter {
 #pragma unroll 1
             for (int a0 = next(); a0 >= 0; a0 = next()) {
                 const int a1 = next();
+                const int rank0 = low_rank_of(ranks, a0, R), rank1 = a1 >= 0 ? low_rank_of(ranks, a1, R) : 0;
                 if (!first || k0 > 0) __syncthreads();  // the last pair has been used
                 if (first)
                     for (int j = all; j < BM / 32 * steps * 2; j += WAVES) {
@@ -95,7 +107,41 @@ struct LowRankAfter {
                     if (k < R) src = up + (int64_t(u ? a1 : a0) * N + min(n0 + row, N - 1)) * R + k;
                     tw_detail::tw_dma16(src, smem + LOW + u * UP + i * 1024);
                 }
+                if (tid < BN / 16) broken[tid] = 0;
                 asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+                __syncthreads();
+                const int staged = a1 >= 0 ? 2 * pieces : pieces;
+                for (int j0 = all; j0 < staged; j0 += 4 * WAVES) {
+                    u32x4 v[4];
+                    bool bad[4], any = false;
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const int j = j0 + q * WAVES, u = j >= pieces;
+                        const int at_byte = LOW + (u ? UP - pieces * 1024 : 0) + j * 1024 + lane * 16;
+                        v[q] = u32x4{0, 0, 0, 0};
+                        if (j < staged) v[q] = *reinterpret_cast<const u32x4 *>(smem + at_byte);
+                    }
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        // (x * 0 has exponent bits only where x is not finite; slots past the rank do not count)
+                        const int j = j0 + q * WAVES, u = j >= pieces, i = j - (u ? pieces : 0);
+                        const int row = (i << (6 - ws)) + (lane >> ws);
+                        const int k = k0 + ((lane & ((1 << ws) - 1)) ^ (row & ((1 << ws) - 1))) * 8;
+                        const u32x4 z = __builtin_bit_cast(u32x4, __builtin_bit_cast(half8, v[q]) * half8{});
+                        bad[q] = ((z.x | z.y | z.z | z.w) & 0x7c007c00u) != 0 &&
+                                 not_finite<_Float16>(keep16(v[q], (u ? rank1 : rank0) - k));
+                        any = any || bad[q];
+                    }
+                    if (__ballot(any) == 0) continue;
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const int j = j0 + q * WAVES, u = j >= pieces, i = j - (u ? pieces : 0);
+                        const int row = (i << (6 - ws)) + (lane >> ws);
+                        if (!bad[q]) continue;
+                        *reinterpret_cast<u32x4 *>(smem + LOW + u * UP + i * 1024 + lane * 16) = u32x4{0, 0, 0, 0};
+                        atomicOr(broken + u * (BN / 32) + row / 32, 1u << (row % 32));
+                    }
+                }
                 __syncthreads();
                 if (loader) continue;
 #pragma unroll 1
@@ -105,7 +151,7 @@ struct LowRankAfter {
 #pragma unroll
                     for (int tm = 0; tm < TM; ++tm) any = any || __ballot(a >= 0 && mine[tm] == a) != 0;
                     if (!any) continue;
-                    const int rank = low_rank_of(ranks, a, R);
+                    const int rank = u ? rank1 : rank0;
 #pragma unroll 1
                     for (int s = 0; s < 4 && k0 + 16 * s < rank; ++s) {
                         const int k = k0 + 16 * s;
@@ -118,22 +164,44 @@ struct LowRankAfter {
                                 *reinterpret_cast<const u32x4 *>(smem + LOW + u * UP + (row << (ws + 4)) + piece * 16),
                                 rank - k - 8 * h);
                         }
-                        uint32_t broken[TN];
-                        take_out<_Float16>(w, broken);
 #pragma unroll
                         for (int tm = 0; tm < TM; ++tm) {
                             if (__ballot(mine[tm] == a) == 0) continue;
                             const uint8_t *p = smem + ((wm * TM + tm) * 4 + s) * 1024 + lane * 16;
                             u32x4 hi = *reinterpret_cast<const u32x4 *>(p);
                             u32x4 lo = *reinterpret_cast<const u32x4 *>(p + BM / 32 * 4096);
-                            const bool use = mine[tm] == a, held = use && k + 8 * h < R;
-                            hi = held ? hi : u32x4{0, 0, 0, 0};
-                            lo = held ? lo_unscaled<_Float16>(lo) : u32x4{0, 0, 0, 0};
-                            add_low<_Float16>(acc, tm, w, hi, lo, broken, use);
+                            const bool use = mine[tm] == a && k + 8 * h < R;
+                            hi = use ? hi : u32x4{0, 0, 0, 0};
+                            lo = use ? lo_unscaled<_Float16>(lo) : u32x4{0, 0, 0, 0};
+#pragma unroll
+                            for (int tn = 0; tn < TN; ++tn) {
+                                acc[tn][tm] = mfma32<_Float16>(w[tn], hi, acc[tn][tm]);
+                                acc[tn][tm] = mfma32<_Float16>(w[tn], lo, acc[tn][tm]);
+                            }
                         }
+                    }
+#pragma unroll
+                    for (int tn = 0; tn < TN; ++tn) {
+                        const uint32_t rows = broken[u * (BN / 32) + wn * TN + tn];
+#pragma unroll
+                        for (int tm = 0; tm < TM; ++tm) hit[tn][tm] |= mine[tm] == a ? rows : 0u;
                     }
                 }
             }
+        }
+        uint32_t any = 0;
+#pragma unroll
+        for (int tn = 0; tn < TN; ++tn)
+#pragma unroll
+            for (int tm = 0; tm < TM; ++tm) any |= hit[tn][tm];
+        if (__ballot(any != 0) != 0) {
+#pragma unroll
+            for (int tn = 0; tn < TN; ++tn)
+#pragma unroll
+                for (int tm = 0; tm < TM; ++tm)
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        if (hit[tn][tm] >> (8 * (i / 4) + 4 * h + i % 4) & 1) acc[tn][tm][i] = __builtin_nanf("");
         }
     }
 };
