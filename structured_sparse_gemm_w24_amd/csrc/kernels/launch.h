@@ -115,7 +115,7 @@ struct LowRankBwd {
 // Byte offsets in the backward pass's workspace, and its split of the tokens.
 struct LowRankPlan {
     int64_t low, dlow, counts, part, total;
-    int range, slices;
+    int range, slices, deals;
 };
 bool low_rank_few(int M);
 int64_t low_rank_bytes(int64_t M, int R);  // both planes of the low-rank values
@@ -154,6 +154,7 @@ struct LossPlan {
     bool pack_x, pack_w;
     int64_t piece;   // vocabulary entries of a piece
     int64_t tiles;   // forward: tiles of the vocabulary
+    int splits;      // backward: K splits of dx's product
     int64_t x, w, part, logit, g, acc, scale, total;
 };
 LossPlan loss_plan(int64_t M, int64_t V, int64_t D, bool pack_x, bool pack_w, bool backward);

@@ -206,6 +206,13 @@ struct LossGrad {
                 if (m < M && n < ldg) st16(g + int64_t(m) * ldg + n, o);
             }
         }
+        // the last tile of a row fills the padding that lies past it
+        const int done = n0 + CF::WN * TN * 32, pad = (ldg - done) / 8;
+        if (done >= N && pad > 0)
+            for (int i = threadIdx.x; i < CF::WM * TM * 32 * pad; i += blockDim.x) {
+                const int m = m0 + i / pad;
+                if (m < M) st16(g + int64_t(m) * ldg + done + i % pad * 8, u32x4{0, 0, 0, 0});
+            }
     }
 };
 
@@ -219,7 +226,7 @@ struct LossOut {
     int ldw, rows_w;
     const float *scale;  // [1]: largest |dloss| / kGradScale
     const float *prev;   // fp32 [M][ldp] or null
-    float *next;         // fp32 [M][ldp] (may be prev), or null: out is written
+    float *next;         // fp32 [M][ldp] (may be prev; K split: a slice each), or null: out is written
     T *out;
     int64_t ldo;
     int ldp;
@@ -269,7 +276,7 @@ struct LossOut {
                         for (int j = 0; j < 8; ++j) v[j] += p[j];
                     }
                     if (next) {
-                        __builtin_memcpy(next + int64_t(m) * ldp + n, v, 32);
+                        __builtin_memcpy(next + (int64_t(blockIdx.y) * M + m) * ldp + n, v, 32);
                         continue;
                     }
                     T *o = out + int64_t(m) * ldo + n;
@@ -328,14 +335,40 @@ loss_scale_kernel(const float *__restrict__ dloss, const int64_t *__restrict__ t
     }
 }
 
+// Sums the K splits' slices in order onto the pieces' sum so far (acc, null: none
+// yet); last: out is written, else acc2.  4 columns a thread.
+template <class T>
+__global__ void __launch_bounds__(256)
+loss_splits_kernel(const float *__restrict__ part, int splits, const float *acc, float *acc2, bool last,
+                   const float *__restrict__ scale, T *__restrict__ out, int64_t ldo, int64_t M, int N, int ldp) {
+    const int64_t i = (int64_t(blockIdx.x) * 256 + threadIdx.x) * 4;
+    const int64_t m = i / ldp;
+    const int n = int(i % ldp);
+    if (m >= M || n >= N) return;
+    floatx4 v = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (acc) v = *reinterpret_cast<const floatx4 *>(acc + i);
+#pragma unroll 4
+    for (int s = 0; s < splits; ++s) {
+        const floatx4 u = *reinterpret_cast<const floatx4 *>(part + s * M * ldp + i);
+        v.x += u.x, v.y += u.y, v.z += u.z, v.w += u.w;
+    }
+    if (!last) {
+        *reinterpret_cast<floatx4 *>(acc2 + i) = v;
+        return;
+    }
+    const float f = scale[1];
+    for (int j = 0; j < 4; ++j)
+        if (n + j < N) out[m * ldo + n + j] = T(v[j] * f);
+}
+
 template <int KIND, class CF, class Extra>
 hipError_t product_cfg(const void *A, const void *W, const Extra &ex, int64_t M, int64_t N, int64_t K,
-                       hipStream_t st) {
+                       hipStream_t st, int splits = 1) {
     using LY = Layout<KIND, CF>;
     const int nb = int((M + LY::BM - 1) / LY::BM * ((N + LY::BN - 1) / LY::BN));
-    hipLaunchKernelGGL((gemm_kernel<KIND, EPI_F16, CF, Extra>), dim3(nb), dim3(LY::NT), 0, st,
+    hipLaunchKernelGGL((gemm_kernel<KIND, EPI_F16, CF, Extra>), dim3(nb, splits), dim3(LY::NT), 0, st,
                        static_cast<const uint8_t *>(A), static_cast<const uint8_t *>(W), nullptr, nullptr, nullptr,
-                       nullptr, int(M), int(N), int(K), int((K + 63) / 64), ex);
+                       nullptr, int(M), int(N), int(K), int((K + 63) / 64 / splits), ex);
     return hipGetLastError();
 }
 
@@ -384,16 +417,30 @@ LossTile loss_tile(int64_t M, int64_t N, bool trans) {
 
 int64_t loss_tile_n(int64_t M, int64_t N) { return kLossTiles[loss_tile(M, N, false)].bn; }
 
+// K splits for dx [M][D]: with few tiles of a long sum (a small batch against the
+// vocabulary) each tile's sum is a chain of K / 64 dependent stages that leaves
+// most CUs idle; split, about two workgroups a CU share it, eight stages at
+// least each (the whole backward call: bf16 187 x 264 x 5382 75 -> 35 us, fp16
+// 38 x 1210 x 4306 83 -> 50 us).
+int loss_splits(int64_t M, int64_t D, int64_t piece) {
+    if (loss_tile(M, D, true) != LT_64) return 1;
+    const long t = tiles(int(M), int(D), 64, 64), stages = long((piece + 63) / 64);
+    long p = 512 / t;
+    if (p > stages / 8) p = stages / 8;
+    return int(p < 1 ? 1 : p > 64 ? 64 : p);
+}
+
 // A [M][K] . W [N][K]^T with an epilogue; K a multiple of 64 unless both are transposed.
 template <class T, class Extra>
-hipError_t product(const void *A, const void *W, const Extra &ex, int64_t M, int64_t N, int64_t K, hipStream_t st) {
+hipError_t product(const void *A, const void *W, const Extra &ex, int64_t M, int64_t N, int64_t K, hipStream_t st,
+                   int splits = 1) {
     constexpr int KIND = __is_same(T, _Float16) ? DENSE_F16 : DENSE_BF16;
     switch (loss_tile(M, N, Extra::kTransW)) {
         case LT_256: return product_cfg<KIND, CfgBigDense<true>>(A, W, ex, M, N, K, st);
         case LT_256X128: return product_cfg<KIND, Cfg256x128>(A, W, ex, M, N, K, st);
         case LT_192X128: return product_cfg<KIND, Cfg192x128>(A, W, ex, M, N, K, st);
         case LT_128: return product_cfg<KIND, Cfg128x128>(A, W, ex, M, N, K, st);
-        default: return product_cfg<KIND, CfgT64<true, false>>(A, W, ex, M, N, K, st);
+        default: return product_cfg<KIND, CfgT64<true, false>>(A, W, ex, M, N, K, st, splits);
     }
 }
 
@@ -462,14 +509,25 @@ hipError_t bwd(const Loss &a, const LossPlan &pl, hipStream_t st) {
     const bool wide_w = a.lddw % 8 == 0 && (reinterpret_cast<uintptr_t>(a.dw) & 15) == 0;
     for (int64_t v0 = 0; v0 < a.V; v0 += pl.piece) {
         const int64_t n = a.V - v0 < pl.piece ? a.V - v0 : pl.piece;
-        const int ldg = int((n + 63) / 64 * 64);
+        const int step = 64 * pl.splits, ldg = int((n + step - 1) / step * step);
         const bool first = v0 == 0, last = v0 + n == a.V;
         const T *wv = static_cast<const T *>(w) + v0 * dp;
         const LossGrad<T> grad{a.target, a.ignore, a.V, v0, a.dloss, a.lse, scale, g, ldg};
         if ((e = product<T>(x, wv, grad, M, n, dp, st)) != hipSuccess) return e;
-        const LossOut<T, false> to_x{0, 0, dp, int(n), scale, first ? nullptr : acc, last ? nullptr : acc,
-                                     static_cast<T *>(a.dx), a.lddx, dp, wide_x};
-        if ((e = product<T>(g, wv, to_x, M, D, ldg, st)) != hipSuccess) return e;
+        float *const so_far = first ? nullptr : acc;
+        if (pl.splits > 1) {
+            float *part = reinterpret_cast<float *>(ws + pl.part);
+            const LossOut<T, false> to_part{0, 0, dp, int(n), scale, nullptr, part, nullptr, 0, dp, false};
+            if ((e = product<T>(g, wv, to_part, M, D, ldg, st, pl.splits)) != hipSuccess) return e;
+            const int64_t blocks = (a.M * dp / 4 + 255) / 256;
+            hipLaunchKernelGGL((loss_splits_kernel<T>), dim3(int(blocks)), dim3(256), 0, st, part, pl.splits, so_far,
+                               acc, last, scale, static_cast<T *>(a.dx), a.lddx, a.M, D, dp);
+            if ((e = hipGetLastError()) != hipSuccess) return e;
+        } else {
+            const LossOut<T, false> to_x{0,  0,       dp, int(n), scale, so_far, last ? nullptr : acc,
+                                         static_cast<T *>(a.dx), a.lddx, dp, wide_x};
+            if ((e = product<T>(g, wv, to_x, M, D, ldg, st)) != hipSuccess) return e;
+        }
         const LossOut<T, true> to_w{ldg, M, dp, M, scale, nullptr, nullptr,
                                     static_cast<T *>(a.dw) + v0 * a.lddw, a.lddw, dp, wide_w};
         if ((e = product<T>(g, x, to_w, n, D, M, st)) != hipSuccess) return e;
@@ -535,7 +593,9 @@ LossPlan loss_plan(int64_t M, int64_t V, int64_t D, bool pack_x, bool pack_w, bo
             if (pieces == least || cost < best) best = cost, p.piece = n;
         }
         if (p.piece > V) p.piece = V;
-        p.g = take(M * up(p.piece, 64) * 2);
+        p.splits = loss_splits(M > 0 ? M : 1, D, p.piece);
+        p.g = take(M * up(p.piece, 64 * p.splits) * 2);
+        p.part = p.splits > 1 ? take(p.splits * M * p.dp * 4) : at;
         p.acc = p.piece < V ? take(M * p.dp * 4) : at;
         p.scale = take(8);
     }

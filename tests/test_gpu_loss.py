@@ -94,6 +94,22 @@ def test_several_pieces_of_the_vocabulary(lib, gpu, m, v, d):
     check_backward(lib.linear_cross_entropy_backward(dloss, x, w, t, got[1]), x, w, t, dloss, got[1], "f16")
 
 
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("m,v,d", [(1, 2049, 64), (38, 4306, 1210), (187, 5382, 264), (9000, 20001, 64)])
+def test_split_sum_over_the_vocabulary(lib, gpu, dtype, m, v, d):
+    """Few tiles of dx against a long vocabulary (the last with two pieces): its sum is split, the
+    same way in every call, and a row without weight holds zeros whatever its input is."""
+    x, w, t, dloss = make(m + v, dtype, m, v, d, ignore=0.0)
+    _, lse = lib.linear_cross_entropy(x, w, t)
+    got = lib.linear_cross_entropy_backward(dloss, x, w, t, lse)
+    check_backward(got, x, w, t, dloss, lse, dtype)
+    again = lib.linear_cross_entropy_backward(dloss, x, w, t, lse)
+    assert got[0].equal(again[0]) and got[1].equal(again[1])
+    t[m // 2] = -100
+    dx, _ = lib.linear_cross_entropy_backward(dloss, x, w, t, lse)
+    assert (dx[m // 2] == 0).all()
+
+
 def test_strides(lib, gpu):
     import torch
     x, w, t, dloss = make(1, "f16", 77, 300, 3 * 128)

@@ -221,6 +221,23 @@ def test_strides_in_place_and_without_base(lib, gpu, dtype, m):
     assert torch.equal(c["xbase"], dx)
 
 
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("m,n,k,r,a,index", [
+    (1, 64, 64, 8, 1, 0), (32, 136, 512, 24, 26, "mixed"), (7, 64, 64, 8, 900, "mixed"), (600, 128, 128, 16, 60, "mixed"),
+    (5000, 64, 64, 8, 40, "runs")])
+def test_backward_with_adapters_dealt_over_workgroups(lib, gpu, dtype, m, n, k, r, a, index):
+    """Narrow matrices, where one range of tokens is worked through by several workgroups: every
+    adapter's gradient is written once, zeros for those without a token."""
+    c = make(m * 5 + a, dtype, m, n, k, r, a, index)
+    got = lib.low_rank_backward(c["dy"], c["x"], c["down"], c["up"], c["index"], c["scale"], c["ranks"],
+                                base=c["xbase"])
+    _, ddown, dup = reference(c, backward=True)
+    close(got[1], ddown[0], ddown[1], dtype, n + m, m ** 0.5)
+    close(got[2], dup[0], dup[1], dtype, k + m, m ** 0.5)
+    unused = [i for i in range(a) if not (c["index"] == i).any()]
+    assert (got[1][unused] == 0).all() and (got[2][unused] == 0).all()
+
+
 def test_no_tokens(lib, gpu):
     import torch
     c = make(9, "bf16", 0, 64, 64, 8, 2, -1)
