@@ -42,7 +42,8 @@ template <class T, int RB, int NW, bool TRANS>
 __device__ __forceinline__ void shrink_tile(const T *__restrict__ x, int64_t ldx, const T *__restrict__ down,
                                             const float *__restrict__ scale, const int32_t *__restrict__ ranks,
                                             const int32_t *__restrict__ index, int adapters, int R,
-                                            T *__restrict__ low, int M, int K, int tile, floatx4 *part) {
+                                            T *__restrict__ low, int M, int K, int tile, int deal, int deals,
+                                            floatx4 *part) {
     constexpr int UNROLL = kShrinkUnroll<RB>;
     constexpr int SLICE = RB * 2048;  // bytes of a slice in LDS
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -66,12 +67,14 @@ __device__ __forceinline__ void shrink_tile(const T *__restrict__ x, int64_t ldx
     const int mine = m < M ? index[m] : -1;  // (each token in four lanes)
     bool todo = mine >= 0 && mine < adapters;
     bool held = true;  // xv holds the first slices
-    for (uint64_t left = __ballot(todo); left; left = __ballot(todo)) {
+    int pair = 0;
+    for (uint64_t left = __ballot(todo); left; left = __ballot(todo), ++pair) {
         const int a0 = __builtin_amdgcn_readlane(mine, __builtin_ctzll(left));
         todo = todo && mine != a0;
         left = __ballot(todo);
         const int a1 = left ? __builtin_amdgcn_readlane(mine, __builtin_ctzll(left)) : -1;
         todo = todo && mine != a1;
+        if (pair % deals != deal) continue;
         const int rank0 = low_rank_of(ranks, a0, R), rank1 = a1 >= 0 ? low_rank_of(ranks, a1, R) : 0;
         const float s0 = scale ? scale[a0] : 1.0f, s1 = scale && a1 >= 0 ? scale[a1] : 1.0f;
         __syncthreads();  // (the previous adapters' sums, in the same LDS, have been read)
@@ -181,10 +184,10 @@ shrink_kernel(ShrinkTask<T> p, ShrinkTask<T> q, const float *__restrict__ scale,
     __shared__ floatx4 part[SUMS > SLICES ? SUMS : SLICES];
     if (blockIdx.y)
         shrink_tile<T, RB, NW, false>(q.x, q.ldx, q.down, scale, ranks, index, adapters, R, q.low, M, q.K, blockIdx.x,
-                                      part);
+                                      blockIdx.z, gridDim.z, part);
     else
         shrink_tile<T, RB, NW, TRANS>(p.x, p.ldx, p.down, scale, ranks, index, adapters, R, p.low, M, p.K, blockIdx.x,
-                                      part);
+                                      blockIdx.z, gridDim.z, part);
 }
 
 // ---- expand: a workgroup takes 64 tokens x 128 channels, a wave 32 x 64.
@@ -305,6 +308,49 @@ tokens_kernel(const T *__restrict__ x, int64_t ldx, const T *__restrict__ down, 
         sum = __builtin_nanf("");
     }
     out[int64_t(m) * ldo + n] = T(sum);
+}
+
+// ---- few tokens' input gradient, dx[m] = base[m] + down[a]^T . dlow[m]: expand
+// takes a tile's adapters one after another, which for a tile of many requests is
+// a chain of pool loads (32 tokens of 26 adapters, 512 wide: 29 us).  Here a
+// workgroup takes one token and 512 columns, its waves every fourth rank slot.
+template <class T>
+__global__ void __launch_bounds__(256)
+tokens_dx_kernel(const T *__restrict__ down, const T *__restrict__ dlow, const int32_t *__restrict__ index,
+                 const int32_t *__restrict__ ranks, int adapters, int R, const T *base, int64_t ldb, T *out,
+                 int64_t ldo, int M, int K) {
+    __shared__ __attribute__((aligned(16))) float part[3][512];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int m = blockIdx.y, k = blockIdx.x * 512 + lane * 8;
+    const int a = index[m];
+    const bool live = a >= 0 && a < adapters;
+    const int rank = live ? low_rank_of(ranks, a, R) : 0;
+    using Vec = typename Elem<T>::Vec;
+    float sum[8] = {};
+    if (k < K) {
+        const int64_t plane = low_plane(M, R);
+#pragma unroll 4
+        for (int r = wave; r < rank; r += 4) {
+            const T *l = dlow + low_at(m, r & ~7, R) + (r & 7);
+            const float f = fmaf(float(l[plane]), 1.0f / LowSplit<T>::kLoScale, float(l[0]));
+            float v[8];
+            to_float<T>(__builtin_bit_cast(Vec, ld16(down + (int64_t(a) * R + r) * K + k)), v);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) sum[i] = fmaf(f, v[i], sum[i]);
+        }
+    }
+    if (wave > 0) __builtin_memcpy(&part[wave - 1][lane * 8], sum, 32);
+    __syncthreads();
+    if (wave > 0 || k >= K) return;
+    float b[8] = {};
+    if (base) to_float<T>(__builtin_bit_cast(Vec, ld16(base + int64_t(m) * ldb + k)), b);
+    Vec o;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float s = ((sum[i] + part[0][lane * 8 + i]) + part[1][lane * 8 + i]) + part[2][lane * 8 + i];
+        o[i] = T(live || a == -1 ? b[i] + s : __builtin_nanf(""));
+    }
+    st16(out + int64_t(m) * ldo + k, __builtin_bit_cast(u32x4, o));
 }
 
 // ---- wgrad: out[r][c] = sum over adapter a's tokens of low[m][r] z[m][c], z
@@ -563,7 +609,9 @@ wgrad_sum_kernel(const float *__restrict__ part0, T *__restrict__ out0, int64_t 
 template <class T, bool BOTH>
 hipError_t shrink(const ShrinkTask<T> &p, const ShrinkTask<T> &q, const LowRank &lr, int M, hipStream_t st) {
     constexpr int NW = 8;
-    const dim3 grid((M + 15) / 16, BOTH ? 2 : 1);
+    // with few tiles, a tile's pairs of adapters (eight at most) are dealt over workgroups
+    const int nb = (M + 15) / 16 * (BOTH ? 2 : 1);
+    const dim3 grid((M + 15) / 16, BOTH ? 2 : 1, nb <= 32 ? 8 : nb <= 128 ? 256 / nb : 1);
 #define SSG_SHRINK(RB)                                                                                              \
     hipLaunchKernelGGL((shrink_kernel<T, RB, NW, BOTH>), grid, dim3(NW * 64), 0, st, p, q, lr.scale, lr.ranks,      \
                        lr.index, lr.adapters, lr.R, M)
@@ -607,9 +655,15 @@ hipError_t bwd(const LowRankBwd &b, hipStream_t st) {
         const ShrinkTask<T> p{static_cast<const T *>(b.dy), b.lddy, static_cast<const T *>(lr.up), dlow, N};
         const ShrinkTask<T> q{static_cast<const T *>(b.x), b.ldx, static_cast<const T *>(lr.down), low, K};
         if ((e = shrink<T, true>(p, q, lr, M, st)) != hipSuccess) return e;
-        if ((e = expand<T, true>(static_cast<const T *>(lr.down), dlow, lr, b.base, b.ldb, b.dx, b.lddx, M, K, st)) !=
-            hipSuccess)
-            return e;
+        if (low_rank_few(M)) {
+            hipLaunchKernelGGL((tokens_dx_kernel<T>), dim3((K + 511) / 512, M), dim3(256), 0, st,
+                               static_cast<const T *>(lr.down), dlow, lr.index, lr.ranks, lr.adapters, R,
+                               static_cast<const T *>(b.base), b.ldb, static_cast<T *>(b.dx), b.lddx, M, K);
+            e = hipGetLastError();
+        } else {
+            e = expand<T, true>(static_cast<const T *>(lr.down), dlow, lr, b.base, b.ldb, b.dx, b.lddx, M, K, st);
+        }
+        if (e != hipSuccess) return e;
     }
     const int64_t n0 = int64_t(lr.adapters) * R * K, n1 = int64_t(lr.adapters) * R * N;
     float *part0 = pl.slices > 1 ? reinterpret_cast<float *>(ws + pl.part) : nullptr;
