@@ -26,7 +26,7 @@
 // SIMD (12608 x 768 fp16: 21.4 us, 25.3 with two chunks and 768 slices;
 // 4099 x 1537 bf16: 19.7 us, 37 with four chunks).
 // Measured on MI355X in rotating buffers (233 MB): forward 12608 x 768 fp16 with
-// residual 16.4 us = 4.7 TB/s, 4096 x 4096 24.7 us = 5.4 TB/s (a 1 GiB copy
+// residual 15.8-16.4 us = 4.7 TB/s, 4096 x 4096 24.7 us = 5.4 TB/s (a 1 GiB copy
 // reaches 5.1); backward 21.4 us = 3.6 TB/s and 30.8 us = 4.4 TB/s, both
 // launches.  Rows of an odd width pay for unaligned access: 4099 x 1537 bf16
 // forward 12.8 us = 2.0 TB/s.
