@@ -26,10 +26,14 @@
 // SIMD (12608 x 768 fp16: 21.4 us, 25.3 with two chunks and 768 slices;
 // 4099 x 1537 bf16: 19.7 us, 37 with four chunks).
 // Measured on MI355X in rotating buffers (233 MB): forward 12608 x 768 fp16 with
-// residual 15.8-16.4 us = 4.7 TB/s, 4096 x 4096 24.7 us = 5.4 TB/s (a 1 GiB copy
-// reaches 5.1); backward 21.4 us = 3.6 TB/s and 30.8 us = 4.4 TB/s, both
-// launches.  Rows of an odd width pay for unaligned access: 4099 x 1537 bf16
-// forward 12.8 us = 2.0 TB/s.
+// residual 16.4 us = 4.7 TB/s, 4096 x 4096 23.9 us = 5.6 TB/s (a 1 GiB copy
+// reaches 5.1); backward 21.4-22.3 us = 3.5 TB/s and 31.6 us = 4.2 TB/s, both
+// launches.  Rows that end in part of a 16-byte piece have kernels of their own
+// (TAIL): 3000 x 8191 fp16 forward 49.8 us = 4.0 TB/s, backward 62 us = 3.2 TB/s (8192
+// wide 36.2 and 50.7), 2865 x 4183 bf16 31.5 us = 3.0 TB/s and 32.6 us, 4099 x
+// 1537 bf16 without residual 12.4 us = 2.0 TB/s and 19.5 us.  Pieces cut at 16-byte boundaries
+// instead of the row's start were slower (60 us at 2865 x 4183: two part pieces a row), and a
+// row's sums would then depend on its place in the batch.
 #include "elem.h"
 #include "launch.h"
 
@@ -38,7 +42,8 @@ namespace ssg {
 namespace {
 
 // Rows held in registers: TPR threads a row, C chunks of V elements a thread.
-template <class T, class W, int TPR, int C>
+// TAIL: rows end in part of a chunk.
+template <class T, class W, int TPR, int C, bool TAIL>
 __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR)
 ln_fwd_kernel(const T *x, int64_t ldx, const T *res, int64_t ldr, const W *__restrict__ w,
               const W *__restrict__ b, float eps, T *y, int64_t ldy, T *sum, int64_t lds, float *mean_out,
@@ -54,8 +59,8 @@ ln_fwd_kernel(const T *x, int64_t ldx, const T *res, int64_t ldr, const W *__res
 #pragma unroll
         for (int c = 0; c < C; ++c) {
             const int at = (c * TPR + t) * V;
-            if (at < N) xr[c] = load_raw(x + m * ldx, at, N);
-            if (res && at < N) rr[c] = load_raw(res + m * ldr, at, N);
+            if (at < N) xr[c] = fetch_raw<T, TAIL>(x + m * ldx, at, N);
+            if (res && at < N) rr[c] = fetch_raw<T, TAIL>(res + m * ldr, at, N);
         }
     };
     const int64_t step = int64_t(gridDim.x) * RPB;
@@ -79,13 +84,13 @@ ln_fwd_kernel(const T *x, int64_t ldx, const T *res, int64_t ldr, const W *__res
 #pragma unroll
         for (int c = 0; c < C; ++c) {
             const int at = (c * TPR + t) * V;
-            to_float<T>(xr[c], f[c]);
+            to_float<T>(settle<T, TAIL>(xr[c], at, N), f[c]);
             if (res) {
                 float g[V];
-                to_float<T>(rr[c], g);
+                to_float<T>(settle<T, TAIL>(rr[c], at, N), g);
 #pragma unroll
                 for (int i = 0; i < V; ++i) f[c][i] = rounded_sum<T>(f[c][i], g[i]);
-                if (at < N) store_stream(sum + m * lds, at, N, f[c]);
+                if (at < N) store_stream<T, TAIL>(sum + m * lds, at, N, f[c]);
             }
         }
         fetch(m + step);
@@ -112,7 +117,7 @@ ln_fwd_kernel(const T *x, int64_t ldx, const T *res, int64_t ldr, const W *__res
             if (at >= N) continue;
 #pragma unroll
             for (int i = 0; i < V; ++i) f[c][i] = fmaf(f[c][i] * rstd, wv[c][i], bv[c][i]);
-            store_stream(y + m * ldy, at, N, f[c]);
+            store_stream<T, TAIL>(y + m * ldy, at, N, f[c]);
         }
         if (mean_out && t == 0) mean_out[m] = mean, rstd_out[m] = rstd;
     }
@@ -175,7 +180,7 @@ ln_fwd_long_kernel(const T *x, int64_t ldx, const T *res, int64_t ldr, const W *
 
 // PARAM: also sum dw and db over this workgroup's rows into part[block][2][N].
 // NT threads a workgroup, NT / TPR rows at a time.
-template <class T, class W, int TPR, int C, int NT, bool PARAM>
+template <class T, class W, int TPR, int C, int NT, bool PARAM, bool TAIL>
 __global__ void __launch_bounds__(NT)
 ln_bwd_kernel(const T *dy, int64_t lddy, const T *x, int64_t ldx, const float *__restrict__ mean,
               const float *__restrict__ rstd, const W *__restrict__ w, const T *dres, int64_t ldres, T *dx,
@@ -192,8 +197,8 @@ ln_bwd_kernel(const T *dy, int64_t lddy, const T *x, int64_t ldx, const float *_
 #pragma unroll
         for (int c = 0; c < C; ++c) {
             const int at = (c * TPR + t) * V;
-            if (at < N) xr[c] = load_raw(x + m * ldx, at, N), gr[c] = load_raw(dy + m * lddy, at, N);
-            if (dres && at < N) rr[c] = load_raw(dres + m * ldres, at, N);
+            if (at < N) xr[c] = fetch_raw<T, TAIL>(x + m * ldx, at, N), gr[c] = fetch_raw<T, TAIL>(dy + m * lddy, at, N);
+            if (dres && at < N) rr[c] = fetch_raw<T, TAIL>(dres + m * ldres, at, N);
         }
     };
     const int64_t step = int64_t(gridDim.x) * RPB;
@@ -222,8 +227,8 @@ ln_bwd_kernel(const T *dy, int64_t lddy, const T *x, int64_t ldx, const float *_
 #pragma unroll
         for (int c = 0; c < C; ++c) {
             const int at = (c * TPR + t) * V;
-            to_float<T>(xr[c], xh[c]);
-            to_float<T>(gr[c], g[c]);
+            to_float<T>(settle<T, TAIL>(xr[c], at, N), xh[c]);
+            to_float<T>(settle<T, TAIL>(gr[c], at, N), g[c]);
             rc[c] = rr[c];
 #pragma unroll
             for (int i = 0; i < V; ++i) {
@@ -261,10 +266,10 @@ ln_bwd_kernel(const T *dy, int64_t lddy, const T *x, int64_t ldx, const float *_
             const int at = (c * TPR + t) * V;
             if (at >= N || !live) continue;
             float r[V];
-            to_float<T>(rc[c], r);
+            to_float<T>(settle<T, TAIL>(rc[c], at, N), r);
 #pragma unroll
             for (int i = 0; i < V; ++i) r[i] = fmaf(rs_m, fmaf(-xh[c][i], c2, g[c][i] - c1), r[i]);
-            store_stream(dx + m * lddx, at, N, r);
+            store_stream<T, TAIL>(dx + m * lddx, at, N, r);
         }
     }
     if constexpr (PARAM) {
@@ -436,18 +441,22 @@ int ln_bwd_blocks(int64_t M, int64_t N, int v) {
 template <class T, class W>
 hipError_t fwd(const LnFwd &a, hipStream_t st) {
     const LnShape sh = ln_fwd_shape(a.N, Elem<T>::V);
+    const bool tail = a.N % Elem<T>::V != 0;
     const T *x = static_cast<const T *>(a.x), *res = static_cast<const T *>(a.res);
     const W *w = static_cast<const W *>(a.w), *b = static_cast<const W *>(a.b);
     T *y = static_cast<T *>(a.y), *sum = static_cast<T *>(a.sum);
-#define SSG_LN(TPR, C)                                                                                             \
-    if (sh.tpr == TPR && sh.c == C) {                                                                              \
+#define SSG_LN(TPR, C, TAIL)                                                                                       \
+    if (sh.tpr == TPR && sh.c == C && tail == TAIL) {                                                              \
         constexpr int RPB = TPR < 256 ? 256 / TPR : 1;                                                             \
-        hipLaunchKernelGGL((ln_fwd_kernel<T, W, TPR, C>), dim3(even_blocks((a.M + RPB - 1) / RPB, 768)),           \
+        hipLaunchKernelGGL((ln_fwd_kernel<T, W, TPR, C, TAIL>), dim3(even_blocks((a.M + RPB - 1) / RPB, 768)),           \
                            dim3(TPR < 256 ? 256 : TPR), 0, st, x, a.ldx, res, a.ldr, w, b, a.eps, y, a.ldy, sum,   \
                            a.lds, a.mean, a.rstd, a.M, int(a.N));                                                  \
         return hipGetLastError();                                                                                  \
     }
-    SSG_LN(64, 1) SSG_LN(64, 2) SSG_LN(256, 1) SSG_LN(256, 2) SSG_LN(256, 4) SSG_LN(1024, 2)
+    SSG_LN(64, 1, false) SSG_LN(64, 2, false) SSG_LN(256, 1, false) SSG_LN(256, 2, false) SSG_LN(256, 4, false)
+    SSG_LN(1024, 2, false)
+    SSG_LN(64, 1, true) SSG_LN(64, 2, true) SSG_LN(256, 1, true) SSG_LN(256, 2, true) SSG_LN(256, 4, true)
+    SSG_LN(1024, 2, true)
 #undef SSG_LN
     hipLaunchKernelGGL((ln_fwd_long_kernel<T, W>), dim3(int(a.M < 2048 ? a.M : 2048)), dim3(256), 0, st, x, a.ldx, res,
                        a.ldr, w, b, a.eps, y, a.ldy, sum, a.lds, a.mean, a.rstd, a.M, a.N);
@@ -457,6 +466,7 @@ hipError_t fwd(const LnFwd &a, hipStream_t st) {
 template <class T, class W, bool PARAM>
 hipError_t bwd(const LnBwd &a, hipStream_t st) {
     const LnShape sh = ln_bwd_shape(a.N, Elem<T>::V);
+    const bool tail = a.N % Elem<T>::V != 0;
     const T *dy = static_cast<const T *>(a.dy), *x = static_cast<const T *>(a.x);
     const T *dres = static_cast<const T *>(a.dres);
     const W *w = static_cast<const W *>(a.w);
@@ -464,15 +474,16 @@ hipError_t bwd(const LnBwd &a, hipStream_t st) {
     const int G = ln_bwd_blocks(a.M, a.N, Elem<T>::V);
     hipError_t e = hipSuccess;
     bool done = G == 0;
-#define SSG_LN(TPR, C)                                                                                               \
-    if (!done && sh.tpr == TPR && sh.c == C) {                                                                       \
+#define SSG_LN(TPR, C, TAIL)                                                                                         \
+    if (!done && sh.tpr == TPR && sh.c == C && tail == TAIL) {                                                       \
         constexpr int NT = TPR > kBwdThreads ? TPR : kBwdThreads;                                                    \
-        hipLaunchKernelGGL((ln_bwd_kernel<T, W, TPR, C, NT, PARAM>), dim3(G), dim3(NT), 0, st, dy, a.lddy, x, a.ldx,     \
+        hipLaunchKernelGGL((ln_bwd_kernel<T, W, TPR, C, NT, PARAM, TAIL>), dim3(G), dim3(NT), 0, st, dy, a.lddy, x, a.ldx,     \
                            a.mean, a.rstd, w, dres, a.ldres, dx, a.lddx, a.part, a.M, int(a.N));                     \
         e = hipGetLastError();                                                                                       \
         done = true;                                                                                                 \
     }
-    SSG_LN(64, 1) SSG_LN(128, 1) SSG_LN(256, 1) SSG_LN(512, 1) SSG_LN(1024, 1)
+    SSG_LN(64, 1, false) SSG_LN(128, 1, false) SSG_LN(256, 1, false) SSG_LN(512, 1, false) SSG_LN(1024, 1, false)
+    SSG_LN(64, 1, true) SSG_LN(128, 1, true) SSG_LN(256, 1, true) SSG_LN(512, 1, true) SSG_LN(1024, 1, true)
 #undef SSG_LN
     int slices = G;
     if (!done) {
