@@ -24,9 +24,9 @@
 // fetched row) set the split: one chunk a thread and 1024 threads keep 16 waves
 // a CU and one slice a CU, where two to four chunks a thread ran at 1-3 waves a
 // SIMD (12608 x 768 fp16: 21.4 us, 25.3 with two chunks and 768 slices;
-// 4099 x 1537 bf16: 19.7 us, 37 with four chunks).
+// 4099 x 1537 bf16: 19.1 us, 37 with four chunks).
 // Measured on MI355X in rotating buffers (233 MB): forward 12608 x 768 fp16 with
-// residual 16.4 us = 4.7 TB/s, 4096 x 4096 23.9 us = 5.6 TB/s (a 1 GiB copy
+// residual 15.7-16.4 us = 4.7-4.9 TB/s, 4096 x 4096 23.9 us = 5.6 TB/s (a 1 GiB copy
 // reaches 5.1); backward 21.4-22.3 us = 3.5 TB/s and 31.6 us = 4.2 TB/s, both
 // launches.  Rows that end in part of a 16-byte piece have kernels of their own
 // (TAIL): 3000 x 8191 fp16 forward 49.8 us = 4.0 TB/s, backward 62 us = 3.2 TB/s (8192

@@ -25,8 +25,8 @@
 // probability of 2^-26 is still a normal number), which the products' outputs
 // are multiplied by again in fp32.
 // Measured on MI355X: forward 8192 x 1024 x 32000 fp16 501 us = 1072 TFLOP/s (the
-// library's product alone 431-448 us); backward 6144 x 1024 x 30001 bf16 1091 us =
-// 1038 TFLOP/s, in two pieces, each G 220 us, dx 168, dw 163.  The matrix units are
+// library's product alone 431-448 us); backward 6144 x 1024 x 30001 bf16 1069-1091 us
+// = 1038-1059 TFLOP/s, in two pieces, each G 211-220 us, dx 164, dw 158.  The matrix units are
 // busy 0.57 of the forward and 0.41 / 0.61 / 0.55 of the three: what bounds them is
 // LDS, whose reads and direct writes fill its port, and for G the epilogue (an
 // exponential a logit and 184 MB of G written; a library product of that size, at
