@@ -10,8 +10,8 @@ type (2^-11 fp16, 2^-8 bf16, 2^-24 fp32) and e = 2^-24.
   mean   32 e mean|s|;  rstd 64 e rstd (1 + rstd^2 mean(s^2) ...) -- with the
          two-sweep variance the relative error of rstd is a few e plus the
          error of the mean squared, so 64 e rstd.
-  dx     u |dx| + 256 e rstd (|g| + mean|g| + |xh| mean|g xh|) + u-free dres
-         part 4 e |dres| + smallest step.
+  dx     u |dx| + 256 e rstd (|g| + mean|g| + |xh| mean|g xh|) + 4 e |dres| (added in
+         fp32, before the one rounding) + smallest step.
   dw, db sums of M terms in fp32, a chain of at most ceil(M / slices) + 64
          additions: e (chain + 8) sum |term|, taken with chain <= M.
 """
@@ -248,3 +248,27 @@ def test_refusals(lib, gpu):
         lib.layer_norm_backward(x, x, s[:3], s)
     with pytest.raises(lib.SsgError, match="workspace"):
         lib.layer_norm_backward(x, x, s, s, workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16", "f32"])
+@pytest.mark.parametrize("n", list(range(1, 18)) + [505, 1023, 2051, 4093, 8190, 16383])
+def test_every_tail_of_a_row(lib, gpu, dtype, n):
+    """Rows that end in part of a 16-byte piece: the values, nothing written beside them, and the same
+    bits for a row wherever in the batch it lies."""
+    import torch
+    m = 9
+    c = _case(n, dtype, m, n)
+    dt = c["x"].dtype
+    wide = [torch.full((m, n + 3), 7.0, dtype=dt, device="cuda") for _ in range(3)]
+    y, s, dx = (t[:, 1:n + 1] for t in wide)
+    out = lib.layer_norm(c["x"], c["w"], c["b"], residual=c["res"], out=y, sum_out=s)
+    assert torch.equal(s, (c["x"].float() + c["res"].float()).to(dt))
+    _check_forward(out, s, c["w"], c["b"], dtype)
+    mean, rstd = out[1:3]
+    got = lib.layer_norm_backward(c["dy"], s, mean, rstd, c["w"], dres=c["dres"], out=dx)
+    _check_backward(got, c["dy"], s, mean, rstd, c["w"], c["dres"], dtype)
+    for t in wide:
+        assert (t[:, 0] == 7).all() and (t[:, n + 1:] == 7).all()
+    for i in (0, 5):
+        one = lib.layer_norm(c["x"][i:i + 1], c["w"], c["b"], residual=c["res"][i:i + 1])
+        assert torch.equal(one[0], y[i:i + 1]) and torch.equal(one[2], rstd[i:i + 1])
