@@ -490,7 +490,9 @@ int linear_cross_entropy_forward(int32_t dtype, const void *x, int64_t ldx, cons
  * in dtype, rounded once from fp32 sums.  The logits are computed again in
  * pieces of the vocabulary; the workspace holds one piece's G (at most 256 MiB,
  * or 2048 entries), dx's fp32 sums, and copies of operands not read in place.  A target outside [0, V) makes its
- * row of dx, and dw, NaN.  dw is all zeros when M = 0. */
+ * row of dx, and dw, NaN; a dloss that is not finite, in a row that is not
+ * ignored, leaves that row of dx, and dw, not finite.  dw is all zeros when
+ * M = 0. */
 int linear_cross_entropy_backward(int32_t dtype, const float *dloss, const void *x, int64_t ldx, const void *w,
                                   int64_t ldw, const int64_t *target, int64_t ignore_index, const float *lse, void *dx,
                                   int64_t lddx, void *dw, int64_t lddw, int64_t M, int64_t V, int64_t D, void *ws,

@@ -21,7 +21,7 @@
 //     transposed copies, and G written both ways round, cost 250 of 1365 us at
 //     6144 x 30001 x 1024).  dx is summed over the pieces in fp32.
 // G is rounded to the operands' 16 bits, as the products need it; its rows are
-// divided by the largest |dloss| first (and, fp16, multiplied by 2^12, so that a
+// divided by the largest finite |dloss| first (and, fp16, multiplied by 2^12, so that a
 // probability of 2^-26 is still a normal number), which the products' outputs
 // are multiplied by again in fp32.
 // Measured on MI355X: forward 8192 x 1024 x 32000 fp16 501 us = 1072 TFLOP/s (the
@@ -154,7 +154,7 @@ struct LossGrad {
     static constexpr bool kAfter = false, kEpilogue = true, kTransA = false, kTransW = false;
     const int64_t *target;
     int64_t ignore, V, v0;
-    const float *dloss, *lse, *scale;  // scale[0] = largest |dloss|
+    const float *dloss, *lse, *scale;  // scale[0] = largest finite |dloss|
     T *g;
     int ldg;
 
@@ -231,7 +231,7 @@ struct LossOut {
     static constexpr bool kAfter = false, kEpilogue = true, kTransA = TA, kTransW = true;
     int lda, rows_a;  // (TA)
     int ldw, rows_w;
-    const float *scale;  // [1]: largest |dloss| / kGradScale
+    const float *scale;  // [1]: largest finite |dloss| / kGradScale
     const float *prev;   // fp32 [M][ldp] or null
     float *next;         // fp32 [M][ldp] (may be prev; K split: a slice each), or null: out is written
     T *out;
@@ -322,7 +322,9 @@ loss_zero_kernel(uint16_t *__restrict__ dst, int64_t ld, int64_t rows, int D) {
         dst[i / D * ld + i % D] = 0;
 }
 
-// out[0] = largest |dloss| of the rows that count, out[1] = out[0] / div.
+// out[0] = largest finite |dloss| of the rows that count, out[1] = out[0] / div.
+// (An infinite one as the common factor would make every other row 0 * inf; so
+// such a row, and one that is NaN, is not finite in its own G alone.)
 __global__ void __launch_bounds__(1024)
 loss_scale_kernel(const float *__restrict__ dloss, const int64_t *__restrict__ target, int64_t ignore, int M,
                   float div, float *__restrict__ out) {
@@ -330,7 +332,7 @@ loss_scale_kernel(const float *__restrict__ dloss, const int64_t *__restrict__ t
     float top = 0.0f;
 #pragma unroll 4
     for (int m = threadIdx.x; m < M; m += 1024)
-        if (target[m] != ignore) top = fmaxf(top, fabsf(dloss[m]));
+        if (target[m] != ignore && fabsf(dloss[m]) <= __FLT_MAX__) top = fmaxf(top, fabsf(dloss[m]));
 #pragma unroll
     for (int d = 32; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor(top, d, 64));
     if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = top;

@@ -143,6 +143,36 @@ def test_gradient_scale_spans_its_rows(lib, gpu):
     check_backward(lib.linear_cross_entropy_backward(dloss, x, w, t, lse), x, w, t, dloss, lse, "bf16")
 
 
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("value", [float("inf"), float("-inf"), float("nan")])
+@pytest.mark.parametrize("m,v,d", [(1, 50, 64), (90, 300, 64), (70, 4306, 72), (4100, 9001, 64)])
+def test_a_weight_that_is_not_finite_stays_with_its_row(lib, gpu, dtype, value, m, v, d):
+    """dloss[m] infinite or NaN: dx of that row and dw are not finite, the other rows of dx are what
+    they are beside a zero there (the same bits: the rows' common factor is the largest finite one)."""
+    import torch
+    x, w, t, dloss = make(m + v, dtype, m, v, d)
+    bad = m // 2
+    t[bad] = v // 3
+    lse = lib.linear_cross_entropy(x, w, t)[1]
+    plain, broken = dloss.clone(), dloss.clone()
+    plain[bad], broken[bad] = 0.0, value
+    others = torch.arange(m, device="cuda") != bad
+    ref = lib.linear_cross_entropy_backward(plain, x, w, t, lse)
+    dx, dw = lib.linear_cross_entropy_backward(broken, x, w, t, lse)
+    assert torch.equal(dx[others], ref[0][others])
+    assert not torch.isfinite(dx[bad]).any() and not torch.isfinite(dw).any()
+    # every finite weight zero
+    zero = torch.zeros_like(dloss)
+    zero[bad] = value
+    dx, _ = lib.linear_cross_entropy_backward(zero, x, w, t, lse)
+    assert (dx[others] == 0).all() and not torch.isfinite(dx[bad]).any()
+    # in an ignored row it is not looked at
+    t[bad] = -100
+    for p, q in zip(lib.linear_cross_entropy_backward(broken, x, w, t, lse),
+                    lib.linear_cross_entropy_backward(plain, x, w, t, lse)):
+        assert torch.equal(p, q)
+
+
 def test_ignored_rows_and_zero_weights(lib, gpu):
     import torch
     x, w, t, dloss = make(4, "f16", 70, 200, 64)
