@@ -485,12 +485,13 @@ int linear_cross_entropy_forward(int32_t dtype, const void *x, int64_t ldx, cons
 
 /* Its gradient for dloss fp32 [M] (the derivative by each row's loss), with the
  * forward pass's lse: for G[m][v] = dloss[m] (exp(z[m][v] - lse[m]) - [v ==
- * target[m]]), zero in ignored rows,
+ * target[m]]), zero in ignored rows whatever their x holds,
  *   dx = G . w  [M][D]  and  dw = G^T . x  [V][D]  (row strides lddx, lddw)
  * in dtype, rounded once from fp32 sums.  The logits are computed again in
- * pieces of the vocabulary; the workspace holds one piece's G (at most 256 MiB,
- * or 2048 entries), dx's fp32 sums, and copies of operands not read in place.  A target outside [0, V) makes its
- * row of dx, and dw, NaN; a dloss that is not finite, in a row that is not
+ * pieces of the vocabulary; the workspace holds a copy of x and one piece's G
+ * (together at most 256 MiB, or the copy and 2048 entries' G), dx's fp32 sums,
+ * and a copy of a w that is not read in place.  A target outside [0, V) makes
+ * its row of dx, and dw, NaN; a dloss that is not finite, in a row that is not
  * ignored, leaves that row of dx, and dw, not finite.  dw is all zeros when
  * M = 0. */
 int linear_cross_entropy_backward(int32_t dtype, const float *dloss, const void *x, int64_t ldx, const void *w,

@@ -322,12 +322,29 @@ loss_zero_kernel(uint16_t *__restrict__ dst, int64_t ld, int64_t rows, int D) {
         dst[i / D * ld + i % D] = 0;
 }
 
-// out[0] = largest finite |dloss| of the rows that count, out[1] = out[0] / div.
-// (An infinite one as the common factor would make every other row 0 * inf; so
-// such a row, and one that is NaN, is not finite in its own G alone.)
+// What the backward pass needs first.  Workgroup 0: out[0] = largest finite
+// |dloss| of the rows that count, out[1] = out[0] / div.  (An infinite one as the
+// common factor would make every other row 0 * inf; so such a row, and one that is
+// NaN, is not finite in its own G alone.)  The others: x to contiguous rows of dp
+// columns, zeros past D and in ignored rows, whose G is zero: read as they lie, an
+// infinity or NaN there (padding that nothing has written) would reach all of
+// dw = G^T x as 0 * inf.  The copy costs the call nothing while it takes less
+// than workgroup 0's 8 us (6144 x 1024: 5).
 __global__ void __launch_bounds__(1024)
-loss_scale_kernel(const float *__restrict__ dloss, const int64_t *__restrict__ target, int64_t ignore, int M,
-                  float div, float *__restrict__ out) {
+loss_prepare_kernel(const float *__restrict__ dloss, const int64_t *__restrict__ target, int64_t ignore, int M,
+                    float div, float *__restrict__ out, const uint16_t *__restrict__ x, int64_t ldx,
+                    uint16_t *__restrict__ rows, int D, int dp) {
+    if (blockIdx.x > 0) {
+        const int64_t pieces = int64_t(M) * (dp / 8);
+        for (int64_t i = int64_t(blockIdx.x - 1) * 1024 + threadIdx.x; i < pieces; i += int64_t(gridDim.x - 1) * 1024) {
+            const int64_t m = i / (dp / 8);
+            const int c = int(i % (dp / 8)) * 8;
+            typename Elem<_Float16>::Vec v = {};
+            if (c < D && target[m] != ignore) v = load_raw(reinterpret_cast<const _Float16 *>(x) + m * ldx, c, D);
+            st16(rows + m * dp + c, __builtin_bit_cast(u32x4, v));
+        }
+        return;
+    }
     __shared__ float red[16];
     float top = 0.0f;
 #pragma unroll 4
@@ -453,11 +470,12 @@ hipError_t product(const void *A, const void *W, const Extra &ex, int64_t M, int
     }
 }
 
-// The operands as the products take them: contiguous rows of dp columns.
-hipError_t operands(const Loss &a, const LossPlan &pl, const void **x, const void **w, hipStream_t st) {
-    *x = a.x;
-    *w = a.w;
+// The operands as the products take them: contiguous rows of dp columns (the
+// backward pass's x comes from loss_prepare_kernel).
+hipError_t operands(const Loss &a, const LossPlan &pl, const void **x, const void **w, bool backward, hipStream_t st) {
     uint8_t *ws = static_cast<uint8_t *>(a.ws);
+    *x = backward ? ws + pl.x : a.x;
+    *w = a.w;
     auto pack = [&](const void *src, int64_t ld, int64_t at, int64_t rows) {
         const int64_t blocks = (rows * (pl.dp / 8) + 255) / 256;
         hipLaunchKernelGGL(loss_pack_kernel, dim3(int(blocks < 4096 ? blocks : 4096)), dim3(256), 0, st,
@@ -466,7 +484,7 @@ hipError_t operands(const Loss &a, const LossPlan &pl, const void **x, const voi
         return hipGetLastError();
     };
     hipError_t e = hipSuccess;
-    if (pl.pack_x) {
+    if (pl.pack_x && !backward) {
         if ((e = pack(a.x, a.ldx, pl.x, a.M)) != hipSuccess) return e;
         *x = ws + pl.x;
     }
@@ -480,7 +498,7 @@ hipError_t operands(const Loss &a, const LossPlan &pl, const void **x, const voi
 template <class T>
 hipError_t fwd(const Loss &a, const LossPlan &pl, hipStream_t st) {
     const void *x, *w;
-    hipError_t e = operands(a, pl, &x, &w, st);
+    hipError_t e = operands(a, pl, &x, &w, false, st);
     if (e != hipSuccess) return e;
     uint8_t *ws = static_cast<uint8_t *>(a.ws);
     float *part = reinterpret_cast<float *>(ws + pl.part), *logit = reinterpret_cast<float *>(ws + pl.logit);
@@ -509,10 +527,12 @@ hipError_t bwd(const Loss &a, const LossPlan &pl, hipStream_t st) {
         return hipGetLastError();
     }
     const void *x, *w;
-    hipError_t e = operands(a, pl, &x, &w, st);
+    hipError_t e = operands(a, pl, &x, &w, true, st);
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL(loss_scale_kernel, dim3(1), dim3(1024), 0, st, a.dloss, a.target, a.ignore, M, kGradScale<T>,
-                       scale);
+    const int64_t copies = (a.M * (dp / 8) + 1023) / 1024;
+    hipLaunchKernelGGL(loss_prepare_kernel, dim3(1 + int(copies < 2048 ? copies : 2048)), dim3(1024), 0, st, a.dloss,
+                       a.target, a.ignore, M, kGradScale<T>, scale, static_cast<const uint16_t *>(a.x), a.ldx,
+                       reinterpret_cast<uint16_t *>(ws + pl.x), D, dp);
     if ((e = hipGetLastError()) != hipSuccess) return e;
     const bool wide_x = a.lddx % 8 == 0 && (reinterpret_cast<uintptr_t>(a.dx) & 15) == 0;
     const bool wide_w = a.lddw % 8 == 0 && (reinterpret_cast<uintptr_t>(a.dw) & 15) == 0;
@@ -558,7 +578,7 @@ LossPlan loss_plan(int64_t M, int64_t V, int64_t D, bool pack_x, bool pack_w, bo
         at += up(bytes, 256);
         return o;
     };
-    if (pack_x) p.x = take(M * p.dp * 2);
+    if (pack_x || backward) p.x = take(M * p.dp * 2);
     if (pack_w) p.w = take(V * p.dp * 2);
     if (!backward) {
         // pieces only where w passes the products' 4 GiB
@@ -573,15 +593,19 @@ LossPlan loss_plan(int64_t M, int64_t V, int64_t D, bool pack_x, bool pack_w, bo
         p.part = take(p.tiles * M * 8);
         p.logit = take(M * 4);
     } else {
-        // pieces of about equal size whose G takes at most 256 MiB (but at least
-        // 2048 entries): of the counts from the least one on, the one whose products
-        // fill their rounds best
-        int64_t most = (int64_t(256) << 20) / (2 * (M > 0 ? M : 1)) / 256 * 256;
+        // pieces of about equal size whose G takes, with the copy of x, at most 256 MiB
+        // (but at least 2048 entries): of the counts from the least one on, the one
+        // whose products fill their rounds best
+        const int64_t copy = M * p.dp * 2, row = 2 * (M > 0 ? M : 1);
+        int64_t most = ((int64_t(256) << 20) - copy) / row / 256 * 256;
         if (most < 2048) most = 2048;
-        // (w's piece and G inside the products' 4 GiB)
-        const int64_t widest = p.dp > M ? p.dp : M;
-        const int64_t reach = (int64_t(4000) << 20) / (widest * 2) / 256 * 256;
+        // (w's piece, and G with the copy, inside the products' 4 GiB; G alone of a batch
+        // so tall that 256 entries are more)
+        const int64_t reach_w = (int64_t(4000) << 20) / (p.dp * 2) / 256 * 256;
+        int64_t reach = ((int64_t(4000) << 20) - copy) / row / 256 * 256;
+        if (reach < 256) reach = 256;
         if (most > reach) most = reach;
+        if (most > reach_w) most = reach_w;
         const int64_t least = (V + most - 1) / most;
         double best = 0.0;
         for (int64_t pieces = least; pieces < least + 6; ++pieces) {

@@ -195,6 +195,32 @@ def test_ignored_rows_and_zero_weights(lib, gpu):
     assert (other[0][t == -100] == 0).all()
 
 
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("m,v,d", [(1, 30, 64), (70, 200, 64), (70, 200, 72), (300, 9001, 8), (2050, 515, 128),
+                                   (4100, 9001, 64)])
+def test_ignored_rows_leave_no_trace_in_the_gradients(lib, gpu, dtype, m, v, d):
+    """Whatever an ignored row's input holds, dx of all rows and dw are what they are with zeros there."""
+    import torch
+    x, w, t, dloss = make(m + v + d, dtype, m, v, d, ignore=0.2)
+    t[m // 2] = -100
+    rows = (t == -100).nonzero()[:, 0]
+    clean = x.clone()
+    clean[rows] = 0
+    lse = lib.linear_cross_entropy(clean, w, t)[1]
+    ref = lib.linear_cross_entropy_backward(dloss, clean, w, t, lse)
+    for i, value in enumerate((float("nan"), float("inf"), float("-inf"))):
+        x[rows[i::3], i % d] = value
+    x[rows[0]] = float("nan")
+    loss, lse = lib.linear_cross_entropy(x, w, t)
+    assert (loss[rows] == 0).all()
+    got = lib.linear_cross_entropy_backward(dloss, x, w, t, lse)
+    assert torch.equal(got[0], ref[0]) and torch.equal(got[1], ref[1])
+    wide = torch.full((m, d + 24), float("nan"), device="cuda", dtype=x.dtype)
+    wide[:, 8:d + 8] = x
+    got = lib.linear_cross_entropy_backward(dloss, wide[:, 8:d + 8], w, t, lse)
+    assert torch.equal(got[0], ref[0]) and torch.equal(got[1], ref[1])
+
+
 def test_targets_outside_the_vocabulary_and_non_finite_rows(lib, gpu):
     import torch
     x, w, t, dloss = make(5, "f16", 130, 300, 64, ignore=0.0)
