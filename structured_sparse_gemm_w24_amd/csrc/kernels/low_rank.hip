@@ -390,8 +390,8 @@ __device__ __forceinline__ void zero_tile(T *o, bool rows_c, int c0, int C, int 
 
 template <class T, int RB>
 __global__ void __launch_bounds__(256)
-wgrad_kernel(WgradTask<T> p, WgradTask<T> q, const int32_t *__restrict__ index, int adapters, int R, int M,
-             int range, int32_t *__restrict__ present) {
+wgrad_kernel(WgradTask<T> p, WgradTask<T> q, const int32_t *__restrict__ index, const int32_t *__restrict__ ranks,
+             int adapters, int R, int M, int range, int32_t *__restrict__ present) {
     constexpr int RT = RB * 16;                  // rank slots of a stage row
     constexpr int Z_STAGE = 32 * 128 * 2;        // [32][128]
     constexpr int L_STAGE = 32 * RT * 2;         // [32][RT], one part
@@ -539,6 +539,7 @@ wgrad_kernel(WgradTask<T> p, WgradTask<T> q, const int32_t *__restrict__ index, 
             }
         }
 
+        const int rank = w.part ? R : low_rank_of(ranks, a, R);
         // lane: rank slots 16 b + 4 g + i of column c0 + 32 wave + 16 cb + j16
 #pragma unroll
         for (int b = 0; b < RB; ++b)
@@ -559,6 +560,13 @@ wgrad_kernel(WgradTask<T> p, WgradTask<T> q, const int32_t *__restrict__ index, 
                         for (int i = 0; i < 4; ++i) o[int64_t(r + i) * C + c] = v[i];
                     }
                 } else {
+                    // Slots past the rank hold sums of zeros (NaN where x is not finite) times a z that
+                    // need not be finite.  (Ranges' slices are cleared where they are summed: masks
+                    // among those stores took 1.5 to 4 of 32 us at 4096 x 1024, rank 128.)
+                    int keep = rank - r;
+                    asm volatile("" : "+v"(keep));  // (formed here: ahead, all blocks' masks took registers)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) v[i] = i < keep ? v[i] : 0.0f;
                     T *o = w.out + int64_t(a) * mat;
                     if (w.rows_c) {
                         T t[4];
@@ -575,11 +583,13 @@ wgrad_kernel(WgradTask<T> p, WgradTask<T> q, const int32_t *__restrict__ index, 
 }
 
 // Sums the ranges' slices of the adapters that the ranges have, in order, and
-// rounds once: one adapter a grid row, 4 values a thread.
+// rounds once: one adapter a grid row, 4 values a thread (ddown [R][K], then dup
+// [N][R]).  Slots past the rank get zeros.
 template <class T>
 __global__ void __launch_bounds__(256)
 wgrad_sum_kernel(const float *__restrict__ part0, T *__restrict__ out0, int64_t n0, const float *__restrict__ part1,
-                 T *__restrict__ out1, int64_t n1, int slices, const int32_t *__restrict__ present, int adapters) {
+                 T *__restrict__ out1, int64_t n1, int slices, const int32_t *__restrict__ present, int adapters,
+                 const int32_t *__restrict__ ranks, int R, int K) {
     const int a = blockIdx.y, lane = threadIdx.x & 63;
     int64_t i = (int64_t(blockIdx.x) * 256 + threadIdx.x) * 4;  // in the adapter's n0, then n1 values
     const bool second = i >= n0;
@@ -610,6 +620,12 @@ wgrad_sum_kernel(const float *__restrict__ part0, T *__restrict__ out0, int64_t 
         }
     }
     if (!live) return;
+    const int rank = low_rank_of(ranks, a, R);
+    if (rank < R) {  // ddown's first rank * K values are in use; in dup, 4 values lie in one row of R
+        const int keep = second ? rank - int(i % R) : i < int64_t(rank) * K ? 4 : 0;
+        s.x = keep > 0 ? s.x : 0.0f, s.y = keep > 1 ? s.y : 0.0f;
+        s.z = keep > 2 ? s.z : 0.0f, s.w = keep > 3 ? s.w : 0.0f;
+    }
     T t[4] = {T(s.x), T(s.y), T(s.z), T(s.w)};
     __builtin_memcpy(out + int64_t(a) * n + i, t, 8);
 }
@@ -686,7 +702,8 @@ hipError_t bwd(const LowRankBwd &b, hipStream_t st) {
                          true};
     const dim3 grid(p.tiles + q.tiles, pl.slices, pl.deals);
 #define SSG_WGRAD(RB) \
-    hipLaunchKernelGGL((wgrad_kernel<T, RB>), grid, dim3(256), 0, st, p, q, lr.index, lr.adapters, R, M, pl.range, counts)
+    hipLaunchKernelGGL((wgrad_kernel<T, RB>), grid, dim3(256), 0, st, p, q, lr.index, lr.ranks, lr.adapters, R, M, pl.range, \
+                       counts)
     if (R <= 16) SSG_WGRAD(1);
     else if (R <= 32) SSG_WGRAD(2);
     else if (R <= 64) SSG_WGRAD(4);
@@ -696,7 +713,7 @@ hipError_t bwd(const LowRankBwd &b, hipStream_t st) {
     const int64_t m0 = int64_t(R) * K, m1 = int64_t(R) * N;  // values of one adapter
     hipLaunchKernelGGL((wgrad_sum_kernel<T>), dim3(int(((m0 + m1) / 4 + 255) / 256), lr.adapters), dim3(256), 0, st,
                        part0, static_cast<T *>(b.ddown), m0, part1, static_cast<T *>(b.dup), m1, pl.slices, counts,
-                       lr.adapters);
+                       lr.adapters, lr.ranks, R, K);
     return hipGetLastError();
 }
 

@@ -181,6 +181,31 @@ def test_a_broken_adapter_stays_with_its_tokens(lib, gpu, m):
         assert torch.equal(p[keep], q[keep])
 
 
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("m,n,k,r,a", [(30, 64, 72, 24, 5), (300, 128, 64, 40, 5), (1500, 1024, 128, 8, 3),
+                                       (5000, 256, 512, 128, 5)])
+def test_slots_past_the_rank_get_zeros_beside_inputs_that_are_not_finite(lib, gpu, dtype, m, n, k, r, a):
+    """Infinities and NaN in x and in dy of one adapter's tokens: its gradients' slots past its rank
+    are zeros all the same, and the other adapters and tokens keep their values."""
+    import torch
+    c = make(m + n, dtype, m, n, k, r, a, "mixed")
+    c["ranks"][1] = r - 3
+    pool = (c["down"], c["up"], c["index"], c["scale"], c["ranks"])
+    ref = lib.low_rank_backward(c["dy"], c["x"], *pool, base=c["xbase"])
+    mine = (c["index"] == 1).nonzero()[:, 0]
+    others = c["index"] != 1
+    keep = [i for i in range(a) if i != 1]
+    for key, value in (("x", float("inf")), ("x", float("nan")), ("dy", float("inf")), ("dy", float("nan"))):
+        d = {q: c[q].clone() for q in ("x", "dy")}
+        d[key][mine[0], 5] = value
+        d[key][mine[-1]] = value
+        dx, ddown, dup = lib.low_rank_backward(d["dy"], d["x"], *pool, base=c["xbase"])
+        assert (ddown[1, r - 3:] == 0).all() and (dup[1, :, r - 3:] == 0).all()
+        assert not torch.isfinite(ddown[1, :r - 3]).all() and not torch.isfinite(dup[1, :, :r - 3]).all()
+        assert torch.equal(dx[others], ref[0][others])
+        assert torch.equal(ddown[keep], ref[1][keep]) and torch.equal(dup[keep], ref[2][keep])
+
+
 @pytest.mark.parametrize("m", [40, 260])
 def test_index_outside_the_pool_gives_nan_rows(lib, gpu, m):
     import torch
