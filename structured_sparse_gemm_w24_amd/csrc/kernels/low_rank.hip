@@ -165,16 +165,20 @@ __device__ __forceinline__ void shrink_tile(const T *__restrict__ x, int64_t ldx
                 v.x += u.x, v.y += u.y, v.z += u.z, v.w += u.w;
             }
             T hi[4], lo[4];
+            // Slots past the rank: zeros, also beside an x that is not finite.
+            int keep = (q < RB ? rank0 : rank1) - r;
+            asm volatile("" : "+v"(keep));  // (formed here: ahead, it took registers of the loop)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                if (TRANS && r + i >= (q < RB ? rank0 : rank1)) v[i] = 0.0f;
                 // The product is made opaque: the compiler otherwise forms hi a
                 // second time with a multiply that rounds to fp16 directly, and
                 // next to a tie the stored hi is then not the one lo was taken from.
-                float f = v[i] * s;
+                float f = i < keep ? v[i] * s : 0.0f;
                 asm("" : "+v"(f));
                 hi[i] = T(f);
-                lo[i] = T((f - float(hi[i])) * LowSplit<T>::kLoScale);
+                // (an infinite value has no rest: inf - inf is NaN)
+                const float rest = f - float(hi[i]);
+                lo[i] = T(fabsf(rest) <= __FLT_MAX__ ? rest * LowSplit<T>::kLoScale : 0.0f);
             }
             T *to = low + low_at(m, r & ~7, R) + (r & 4);
             __builtin_memcpy(to, hi, 8);

@@ -226,6 +226,25 @@ def test_index_outside_the_pool_gives_nan_rows(lib, gpu, m):
 
 
 @pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("m,r,rank", [(60, 8, 8), (60, 24, 13), (200, 8, 8), (200, 24, 13), (200, 128, 100)])
+def test_infinite_low_rank_values_follow_the_formula(lib, gpu, dtype, m, r, rank):
+    """A token whose input makes its low-rank values infinite gets the formula's infinities of either sign
+    (no NaN from a difference of infinities, or from the slots that are not used), in both forms."""
+    import torch
+    c = make(2, dtype, m, 64, 64, r, 1, 0)
+    c["ranks"][0] = rank
+    sign = torch.sign(c["up"][0, :, :1])
+    c["down"] = c["down"].abs() + 0.5
+    c["up"][0] = (c["up"][0].abs() + 0.5) * sign
+    c["x"][5] = 1.0
+    c["x"][5, 7] = float("inf")
+    others = torch.arange(m, device="cuda") != 5
+    out = lib.low_rank_add(c["base"], c["x"], c["down"], c["up"], c["index"], c["scale"], c["ranks"])
+    assert torch.isfinite(out[others]).all()
+    assert torch.equal(out[5].double(), sign[:, 0].double() * float("inf"))
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
 @pytest.mark.parametrize("m", [9, 211])
 def test_strides_in_place_and_without_base(lib, gpu, dtype, m):
     import torch
