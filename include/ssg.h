@@ -427,9 +427,10 @@ int64_t layer_norm_workspace_bytes(int32_t dtype, int64_t M, int64_t N);
  * index: int32 [M] on the device, in any order, one entry a token; -1 is no
  * adapter, and a token whose index is otherwise outside [0, adapters) gets
  * NaN in its output rows (the device cannot refuse the call).
- * Products accumulate in fp32.  The low-rank values scale * down . x pass
- * between the kernels as a pair of dtype values that keeps 16 (bf16) to 21
- * (fp16) bits of them; with fp16 they must stay below 65504 in size. */
+ * Products accumulate in fp32.  The low-rank values (scale * down . x, and
+ * in the gradient scale * up^T . dy) pass between the kernels as a pair of
+ * dtype values, with 16 bits of each (bf16), or 15 to 21 bits of a token's largest
+ * (fp16, with a power of two for each token: values of any size up to 2^100). */
 typedef struct {
     const void *down, *up;
     const float *scale;

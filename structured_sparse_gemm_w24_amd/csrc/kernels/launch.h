@@ -94,6 +94,7 @@ struct ShrinkTask {
     const T *down;  // [adapters][R][K] (or [adapters][K][R])
     T *low;         // two planes
     int K;
+    int32_t *key;  // [M], or null: wgrad's list (fp16, low_key in low_rank.h)
 };
 template <class T>
 struct WgradTask {
@@ -104,6 +105,7 @@ struct WgradTask {
     T *out;
     int C, tiles;
     bool rows_c;  // the result's rows are z's columns ([C][R]), else [R][C]
+    const int32_t *key;
 };
 struct LowRankBwd {
     LowRank lr;
@@ -114,7 +116,7 @@ struct LowRankBwd {
 };
 // Byte offsets in the backward pass's workspace, and its split of the tokens.
 struct LowRankPlan {
-    int64_t low, dlow, counts, part, total;
+    int64_t low, dlow, keys, counts, part, total;
     int range, slices, deals;
 };
 bool low_rank_few(int M);

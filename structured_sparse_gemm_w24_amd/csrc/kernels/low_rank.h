@@ -9,14 +9,27 @@
 //
 // The low-rank activations low[m][r] = scale[a] * (down[a] . x[m])[r] are
 // handed from one kernel to the next as two values of the rows' type, hi =
-// round(low) and lo = round((low - hi) * kLoScale), two planes.  Both feed the
+// round(low) and lo = round(low - hi), two planes.  Both feed the
 // matrix instructions, so that the split costs one more small product instead of
 // the digits that a single 16-bit value would lose (16 bits of mantissa for
-// bf16, 21 for fp16, against the 8 and 11 of the outputs).  A plane is laid out
+// bf16, 15 to 21 for fp16, against the 8 and 11 of the outputs).  A plane is laid out
 // as the 32x32x16 instruction's operand: blocks of 32 tokens x 16 slots, in each
 // the 16 bytes of lane (slot / 8 % 2) * 32 + token % 32 hold slots 8 (slot / 8)
 // .. + 7, so that a wave reads a block as one contiguous KiB (read row by row,
 // 32 rows an instruction, the loads took 4 times as many cache lines).
+//
+// fp16 has neither the range nor the small steps for values that are products of
+// two of its numbers, so there a token's pair holds low * 2^-e, which puts the token's
+// largest value into [2^-8, 2^15), where the pair's steps of 2^-23 are 15 bits of it or more
+// (21 from 2^-2 on).  e is a multiple of 23, and 0 for values of ordinary size: narrower
+// steps would hold more bits, but every e of an adapter costs wgrad another pass over its
+// list (with steps of 20, 32 tokens of 26 adapters with values about 2^-5 took 23.4 us instead
+// of 21.7, 6144 tokens about 2^-2, steps of 17, 56 instead of 52.5).  It travels in the last bits
+// of lo, eight bits in every eight slots, which the readers take out; sums over one
+// token's slots are multiplied by 2^e at their end.  Sums over tokens (wgrad) go
+// through an adapter's tokens one e after another, from the least, and are brought to the
+// next one's size between them.  (Multiplying each token's values by its 2^(e - largest)
+// in the product's loop instead took 2 to 6 of 32 us there, with nothing to scale too.)
 #pragma once
 
 #include "elem.h"
@@ -24,17 +37,46 @@
 
 namespace ssg {
 
-// fp16 keeps its low part scaled by 2^11, out of the subnormal range.
+// Whether a token's pair carries a power of two (fp16).
 template <class T>
-struct LowSplit;
-template <>
-struct LowSplit<_Float16> {
-    static constexpr float kLoScale = 2048.0f;
-};
-template <>
-struct LowSplit<__bf16> {
-    static constexpr float kLoScale = 1.0f;
-};
+constexpr bool kLowScaled = __is_same(T, _Float16);
+
+// The power of two for a token whose largest value is `top`: in steps of 23, the
+// width of [2^-8, 2^15), so that tokens of similar size have the same one.  The limits:
+// values below 2^-54 are held to 2^-70, far below what a pool and an output in fp16
+// can show, and 2^92 leaves the product in front of them room for 2^-92.
+__device__ __forceinline__ int low_exponent(float top) {
+    const int e = int(__builtin_bit_cast(uint32_t, top) >> 23) - 127 + 54;  // top = 1.. * 2^(e - 54)
+    if (top == 0.0f) return 0;
+    return min(max(e, 0) / 23 - 2, 4) * 23;
+}
+// Largest value of lanes i, i + 16, i + 32 and i + 48, for each of them (values >= 0).
+__device__ __forceinline__ float max_of_groups(float v) {
+    uint32_t u = __builtin_bit_cast(uint32_t, v);
+    const auto a = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+    u = max(uint32_t(a[0]), uint32_t(a[1]));
+    const auto b = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+    return __builtin_bit_cast(float, max(uint32_t(b[0]), uint32_t(b[1])));
+}
+// A token of wgrad's list: its adapter, and e as the low eight bits.
+__device__ __forceinline__ int low_key(int adapter, int e) { return adapter << 8 | (e + 128); }
+__device__ __forceinline__ int low_key_power(int key) { return (key & 255) - 128; }
+// Eight slots of lo: their last bits to e (the even slots hold bits 0-3, the odd ones
+// 4-7), and the values without them.
+__device__ __forceinline__ int low_exponent_of(u32x4 lo) {
+    constexpr uint32_t kBits = 0x00010001u;
+    const uint32_t t = (lo.x & kBits) | (lo.y & kBits) << 1 | (lo.z & kBits) << 2 | (lo.w & kBits) << 3;
+    return int8_t((t & 15) | t >> 12);
+}
+__device__ __forceinline__ uint32_t low_exponent_bit(int e, int slot) {
+    return uint32_t(e) >> ((slot & 1) * 4 + (slot & 7) / 2) & 1;
+}
+template <class T>
+__device__ __forceinline__ u32x4 lo_value(u32x4 lo) {
+    if constexpr (!kLowScaled<T>) return lo;
+    constexpr uint32_t kValue = 0xfffefffeu;
+    return u32x4{lo.x & kValue, lo.y & kValue, lo.z & kValue, lo.w & kValue};
+}
 
 template <class T>
 __device__ __forceinline__ floatx16 mfma32(u32x4 a, u32x4 b, floatx16 c) {
@@ -61,15 +103,6 @@ __device__ __forceinline__ u32x4 keep16(u32x4 v, int n) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) v[i] = 2 * i + 1 < n ? v[i] : 2 * i < n ? v[i] & 0xffffu : 0u;
     return v;
-}
-
-// The low part of the fp16 split back at its own scale.
-template <class T>
-__device__ __forceinline__ u32x4 lo_unscaled(u32x4 v) {
-    if constexpr (LowSplit<T>::kLoScale == 1.0f) return v;
-    typename Elem<T>::Vec h = __builtin_bit_cast(typename Elem<T>::Vec, v);
-    h *= T(1.0f / LowSplit<T>::kLoScale);
-    return __builtin_bit_cast(u32x4, h);
 }
 
 __device__ __forceinline__ int low_rank_of(const int32_t *ranks, int a, int R) {
@@ -151,7 +184,7 @@ __device__ __forceinline__ uint32_t lds_address(const void *p) {
 // Source of padding in direct-to-LDS loads.
 static __device__ __attribute__((aligned(256))) uint16_t g_low_zero[128];
 
-// Adds up[a] . low to accumulators of 32x32 blocks: acc[tn][tm] holds, for the
+// Adds up[a] . low to accumulators of 32x32 blocks, zeros before: acc[tn][tm] holds, for the
 // 32 tokens from mw + 32 tm (mw a multiple of 32), the channels nw + 32 tn +
 // 8 (i/4) + 4 h + i%4 of token lane%32.  at[i]: index of token mw + i (anything
 // past M).  Channels past the last repeat it (their results are not stored).
@@ -170,10 +203,11 @@ __device__ __forceinline__ void low_rank_expand(floatx16 (&acc)[TN][TM], const T
     const int64_t plane = low_plane(M, R);
     // 16-byte pieces of a pool row held at a time, as a shift
     const int ws = R <= 16 ? 1 : R <= 32 ? 2 : 3;
-    int mine[TM];
+    int mine[TM], power[TM];  // (of its token)
     bool todo[TM];
 #pragma unroll
     for (int tm = 0; tm < TM; ++tm) {
+        power[tm] = 0;
         mine[tm] = at[tm * 32 + r];
         if (mw + tm * 32 + r >= M) mine[tm] = -1;
         todo[tm] = mine[tm] >= 0 && mine[tm] < adapters;
@@ -191,7 +225,7 @@ __device__ __forceinline__ void low_rank_expand(floatx16 (&acc)[TN][TM], const T
             const uint64_t left = __ballot(todo[tm]);
             if (left) a = __builtin_amdgcn_readlane(mine[tm], __builtin_ctzll(left));
         }
-        if (a < 0) return;
+        if (a < 0) break;
         {
             bool sel[TM];
 #pragma unroll
@@ -234,6 +268,19 @@ __device__ __forceinline__ void low_rank_expand(floatx16 (&acc)[TN][TM], const T
                     }
                 asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
                 if (k0 >= rank) break;
+                if constexpr (kLowScaled<T>) {
+                    if (k0 == 0) {
+#pragma unroll
+                        for (int tm = 0; tm < TM; ++tm) {
+                            // (the lower half's piece: the upper one's lies past R = 8)
+                            const int e = low_exponent_of(lo[0][tm]);
+                            if (__ballot(e != 0) != 0) {
+                                const int own = __shfl(e, r, 64);
+                                power[tm] = sel[tm] ? own : power[tm];
+                            }
+                        }
+                    }
+                }
 #pragma unroll
                 for (int s = 0; s < 4; ++s) {
                     const int k = k0 + 16 * s;
@@ -264,7 +311,7 @@ __device__ __forceinline__ void low_rank_expand(floatx16 (&acc)[TN][TM], const T
                     const bool some = take_out<T>(w, bad);
 #pragma unroll
                     for (int tm = 0; tm < TM; ++tm) {
-                        const u32x4 l = lo_unscaled<T>(lo[s][tm]);
+                        const u32x4 l = lo_value<T>(lo[s][tm]);
 #pragma unroll
                         for (int tn = 0; tn < TN; ++tn) {
                             acc[tn][tm] = mfma32<T>(w[tn], hi[s][tm], acc[tn][tm]);
@@ -274,6 +321,16 @@ __device__ __forceinline__ void low_rank_expand(floatx16 (&acc)[TN][TM], const T
                     if (some) poison(acc, bad, sel);
                 }
             }
+        }
+    }
+    if constexpr (kLowScaled<T>) {
+#pragma unroll
+        for (int tm = 0; tm < TM; ++tm) {
+            if (__ballot(power[tm] != 0) == 0) continue;
+#pragma unroll
+            for (int tn = 0; tn < TN; ++tn)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) acc[tn][tm][i] = __builtin_amdgcn_ldexpf(acc[tn][tm][i], power[tm]);
         }
     }
 }

@@ -51,7 +51,7 @@ __device__ __forceinline__ void shrink_tile(const T *__restrict__ x, int64_t ldx
                                             const float *__restrict__ scale, const int32_t *__restrict__ ranks,
                                             const int32_t *__restrict__ index, int adapters, int R,
                                             T *__restrict__ low, int M, int K, int tile, int deal, int deals,
-                                            floatx4 *part) {
+                                            floatx4 *part, float *tops, int32_t *__restrict__ key) {
     constexpr int UNROLL = kShrinkUnroll<RB>;
     constexpr int SLICE = RB * 2048;  // bytes of a slice in LDS
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -74,6 +74,8 @@ __device__ __forceinline__ void shrink_tile(const T *__restrict__ x, int64_t ldx
     // every wave finds the distinct adapters of the same tokens, in the same order
     const int mine = m < M ? index[m] : -1;  // (each token in four lanes)
     bool todo = mine >= 0 && mine < adapters;
+    // (a key for every token: those of an adapter are written with their values)
+    if (kLowScaled<T> && key && deal == 0 && wave == 0 && g == 0 && m < M && !todo) key[m] = -1;
     bool held = true;  // xv holds the first slices
     int pair = 0;
     for (uint64_t left = __ballot(todo); left; left = __ballot(todo), ++pair) {
@@ -154,31 +156,73 @@ __device__ __forceinline__ void shrink_tile(const T *__restrict__ x, int64_t ldx
             if (a1 >= 0) part[((RB + b) * NW + wave) * 64 + lane] = acc[1][b];
         }
         __syncthreads();
-        for (int q = wave; q < (a1 >= 0 ? 2 : 1) * RB; q += NW) {
-            const int b = q % RB, r = b * 16 + 4 * g;
-            const float s = q < RB ? s0 : s1;
-            if (mine != (q < RB ? a0 : a1) || r >= R) continue;
-            floatx4 v = part[(q * NW) * 64 + lane];
+        // A wave finishes the blocks of 16 slots q = wave, wave + NW of the pair's 2 RB.
+        constexpr int QS = (2 * RB + NW - 1) / NW;
+        // (opaque, so that nothing formed from it here is kept in registers across the loop above)
+        int id = threadIdx.x;
+        asm volatile("" : "+v"(id));
+        const int turn = __builtin_amdgcn_readfirstlane(id >> 6);
+        const int at = id & 63, g = at >> 4, c = at & 15, m = tile * 16 + c;
+        const int count = (a1 >= 0 ? 2 : 1) * RB;
+        float f[QS][4];
+        int power = 0;
+#pragma unroll
+        for (int j = 0; j < QS; ++j) {
+            const int q = turn + j * NW, r = q % RB * 16 + 4 * g;
+            if (q >= count) break;
+            floatx4 v = part[(q * NW) * 64 + at];
 #pragma unroll
             for (int w = 1; w < NW; ++w) {
-                const floatx4 u = part[(q * NW + w) * 64 + lane];
+                const floatx4 u = part[(q * NW + w) * 64 + at];
                 v.x += u.x, v.y += u.y, v.z += u.z, v.w += u.w;
             }
-            T hi[4], lo[4];
             // Slots past the rank: zeros, also beside an x that is not finite.
             int keep = (q < RB ? rank0 : rank1) - r;
             asm volatile("" : "+v"(keep));  // (formed here: ahead, it took registers of the loop)
+            float top = 0.0f;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 // The product is made opaque: the compiler otherwise forms hi a
                 // second time with a multiply that rounds to fp16 directly, and
                 // next to a tie the stored hi is then not the one lo was taken from.
-                float f = i < keep ? v[i] * s : 0.0f;
-                asm("" : "+v"(f));
-                hi[i] = T(f);
+                f[j][i] = i < keep ? v[i] * (q < RB ? s0 : s1) : 0.0f;
+                asm("" : "+v"(f[j][i]));
+                if (fabsf(f[j][i]) <= __FLT_MAX__) top = fmaxf(top, fabsf(f[j][i]));
+            }
+            if constexpr (kLowScaled<T>) {
+                top = max_of_groups(top);
+                if (RB == 1) power = low_exponent(top);
+                else if (g == 0) tops[q * 16 + c] = top;
+            }
+        }
+        if constexpr (kLowScaled<T> && RB > 1) __syncthreads();
+#pragma unroll
+        for (int j = 0; j < QS; ++j) {
+            const int q = turn + j * NW, r = q % RB * 16 + 4 * g;
+            if (q >= count) break;
+            if constexpr (kLowScaled<T> && RB > 1) {
+                float top = 0.0f;
+#pragma unroll
+                for (int i = 0; i < RB; ++i) top = fmaxf(top, tops[(q < RB ? i : RB + i) * 16 + c]);
+                power = low_exponent(top);
+            }
+            if (mine != (q < RB ? a0 : a1) || r >= R) continue;
+            if (kLowScaled<T> && key && r == 0) key[m] = low_key(mine, power);
+            T hi[4], lo[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                float v = kLowScaled<T> ? __builtin_amdgcn_ldexpf(f[j][i], -power) : f[j][i];
+                asm("" : "+v"(v));
+                hi[i] = T(v);
                 // (an infinite value has no rest: inf - inf is NaN)
-                const float rest = f - float(hi[i]);
-                lo[i] = T(fabsf(rest) <= __FLT_MAX__ ? rest * LowSplit<T>::kLoScale : 0.0f);
+                const float rest = v - float(hi[i]);
+                lo[i] = T(fabsf(rest) <= __FLT_MAX__ ? rest : 0.0f);
+                if constexpr (kLowScaled<T>) {
+                    const uint16_t u = __builtin_bit_cast(uint16_t, lo[i]);
+                    // (rounded once more, to even, where the last bit goes)
+                    const uint32_t t = ((u + (u >> 1 & 1u)) & 0xfffeu) | low_exponent_bit(power, r + i);
+                    lo[i] = __builtin_bit_cast(T, uint16_t(t));
+                }
             }
             T *to = low + low_at(m, r & ~7, R) + (r & 4);
             __builtin_memcpy(to, hi, 8);
@@ -194,12 +238,13 @@ shrink_kernel(ShrinkTask<T> p, ShrinkTask<T> q, const float *__restrict__ scale,
               const int32_t *__restrict__ index, int adapters, int R, int M) {
     constexpr int SUMS = 2 * RB * NW * 64, SLICES = NW * kShrinkUnroll<RB> * RB * 2048 / 16;
     __shared__ floatx4 part[SUMS > SLICES ? SUMS : SLICES];
+    __shared__ float tops[kLowScaled<T> && RB > 1 ? 2 * RB * 16 : 1];  // a token's largest value in each block
     if (blockIdx.y)
         shrink_tile<T, RB, NW, false>(q.x, q.ldx, q.down, scale, ranks, index, adapters, R, q.low, M, q.K, blockIdx.x,
-                                      blockIdx.z, gridDim.z, part);
+                                      blockIdx.z, gridDim.z, part, tops, q.key);
     else
         shrink_tile<T, RB, NW, TRANS>(p.x, p.ldx, p.down, scale, ranks, index, adapters, R, p.low, M, p.K, blockIdx.x,
-                                      blockIdx.z, gridDim.z, part);
+                                      blockIdx.z, gridDim.z, part, tops, p.key);
 }
 
 // ---- expand: a workgroup takes 64 tokens x 128 channels, a wave 32 x 64.
@@ -340,12 +385,16 @@ tokens_dx_kernel(const T *__restrict__ down, const T *__restrict__ dlow, const i
     const int rank = live ? low_rank_of(ranks, a, R) : 0;
     using Vec = typename Elem<T>::Vec;
     float sum[8] = {};
+    int power = 0;
     if (k < K) {
         const int64_t plane = low_plane(M, R);
+        if (kLowScaled<T> && rank > 0) power = low_exponent_of(ld16(dlow + low_at(m, 0, R) + plane));
 #pragma unroll 4
         for (int r = wave; r < rank; r += 4) {
             const T *l = dlow + low_at(m, r & ~7, R) + (r & 7);
-            const float f = fmaf(float(l[plane]), 1.0f / LowSplit<T>::kLoScale, float(l[0]));
+            uint16_t lo = __builtin_bit_cast(uint16_t, l[plane]);
+            if (kLowScaled<T>) lo &= 0xfffeu;
+            const float f = float(__builtin_bit_cast(T, lo)) + float(l[0]);
             float v[8];
             to_float<T>(__builtin_bit_cast(Vec, ld16(down + (int64_t(a) * R + r) * K + k)), v);
 #pragma unroll
@@ -360,7 +409,8 @@ tokens_dx_kernel(const T *__restrict__ down, const T *__restrict__ dlow, const i
     Vec o;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        const float s = ((sum[i] + part[0][lane * 8 + i]) + part[1][lane * 8 + i]) + part[2][lane * 8 + i];
+        float s = ((sum[i] + part[0][lane * 8 + i]) + part[1][lane * 8 + i]) + part[2][lane * 8 + i];
+        if (kLowScaled<T>) s = __builtin_amdgcn_ldexpf(s, power);
         o[i] = T(live || a == -1 ? b[i] + s : __builtin_nanf(""));
     }
     st16(out + int64_t(m) * ldo + k, __builtin_bit_cast(u32x4, o));
@@ -421,13 +471,21 @@ wgrad_kernel(WgradTask<T> p, WgradTask<T> q, const int32_t *__restrict__ index, 
     // this thread's tokens of the range's piece c (only a large pool's single range,
     // kept that long for its slices' size, has more than one)
     const int pieces = (last - first + kListCap - 1) / kListCap;
+    // (fp16: low_key's adapters and powers of two, which the shrink has written; one after another
+    // by power within an adapter)
     int mine[TURNS];
+    auto adapter = [](int v) { return kLowScaled<T> ? v >> 8 : v; };
     auto fetch = [&](int c) {
 #pragma unroll
         for (int i = 0; i < TURNS; ++i) {
             const int m = first + c * kListCap + i * 256 + tid;
-            mine[i] = m < last ? index[m] : -1;
-            if (mine[i] >= adapters || (deals > 1 && mine[i] >= 0 && mine[i] % deals != deal)) mine[i] = -1;
+            if constexpr (kLowScaled<T>) {
+                mine[i] = m < last ? w.key[m] : -1;
+            } else {
+                mine[i] = m < last ? index[m] : -1;
+                if (mine[i] >= adapters) mine[i] = -1;
+            }
+            if (deals > 1 && mine[i] >= 0 && adapter(mine[i]) % deals != deal) mine[i] = -1;
         }
     };
     fetch(0);
@@ -436,15 +494,29 @@ wgrad_kernel(WgradTask<T> p, WgradTask<T> q, const int32_t *__restrict__ index, 
     const uint32_t smem_addr = lds_address(smem);
     const int per_stage = 2 + (2 * RB - wave + 3) / 4;  // loads of this wave
     constexpr int kNone = 0x7fffffff;
-    int turn = 0, next = deal;  // this workgroup's adapters below `next` are done
+    floatx4 acc[2][RB][2];
+    auto scale = [&](int e) {
+#pragma unroll
+        for (int s = 0; s < 2; ++s)
+#pragma unroll
+            for (int b = 0; b < RB; ++b)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    acc[s][b][0][i] = __builtin_amdgcn_ldexpf(acc[s][b][0][i], e);
+                    acc[s][b][1][i] = __builtin_amdgcn_ldexpf(acc[s][b][1][i], e);
+                }
+    };
+    // this workgroup's adapters below `next`, and entries of `mine` below `from`, are done;
+    // acc: the sums of adapter `now`, times 2^-power
+    int turn = 0, next = deal, from = 0, now = -1, power = 0;
     for (;; turn ^= 1) {
-        // the least adapter that is not done
+        // the least entry that is not done
         int a = kNone;
         for (int c = 0; c < max(pieces, 1); ++c) {
             if (pieces > 1) fetch(c);
 #pragma unroll
             for (int i = 0; i < TURNS; ++i)
-                if (mine[i] >= next) a = min(a, mine[i]);
+                if (mine[i] >= from) a = min(a, mine[i]);
         }
 #pragma unroll
         for (int d = 32; d > 0; d >>= 1) a = min(a, __shfl_xor(a, d, 64));
@@ -452,19 +524,75 @@ wgrad_kernel(WgradTask<T> p, WgradTask<T> q, const int32_t *__restrict__ index, 
         __syncthreads();
         a = min(min(least[turn][0], least[turn][1]), min(least[turn][2], least[turn][3]));
         a = __builtin_amdgcn_readfirstlane(a);
-        if (!w.part) {
-            // the one range writes every adapter: zeros for those without tokens
-            const int upto = a == kNone ? adapters : a;
-            for (int z = next; z < upto; z += deals) zero_tile(w.out + int64_t(z) * R * C, w.rows_c, c0, C, R);
+        const int id = a == kNone ? kNone : adapter(a);
+        if constexpr (kLowScaled<T>) {
+            // to their size at the adapter's end, else to the next tokens' (the sums so far are the smaller ones)
+            const int shift = id != now ? power : power - low_key_power(a);
+            if (now >= 0 && shift != 0) scale(shift);
         }
-        if (a == kNone) return;
-        next = a + deals;
-        if (marks && tid == 0) present[int64_t(slice) * adapters + a] = 1;
-        floatx4 acc[2][RB][2];
+        if (now >= 0 && id != now) {
+            const int rank = w.part ? R : low_rank_of(ranks, now, R);
+            // lane: rank slots 16 b + 4 g + i of column c0 + 32 wave + 16 cb + j16.  (Its place is opaque,
+            // so that the addresses are formed here and not kept through the products.)
+            int place = lane;
+            asm volatile("" : "+v"(place));
+            const int g = place >> 4, j16 = place & 15;
 #pragma unroll
-        for (int s = 0; s < 2; ++s)
+            for (int b = 0; b < RB; ++b)
 #pragma unroll
-            for (int b = 0; b < RB; ++b) acc[s][b][0] = acc[s][b][1] = floatx4{0.f, 0.f, 0.f, 0.f};
+                for (int cb = 0; cb < 2; ++cb) {
+                    const int c = c0 + wave * 32 + cb * 16 + j16, r = b * 16 + 4 * g;
+                    if (c >= C || r >= R) continue;
+                    float v[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) v[i] = acc[0][b][cb][i] + acc[1][b][cb][i];
+                    const int64_t mat = int64_t(R) * C;
+                    if (w.part) {
+                        float *o = w.part + (int64_t(slice) * adapters + now) * mat;
+                        if (w.rows_c) {
+                            __builtin_memcpy(o + int64_t(c) * R + r, v, 16);
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) o[int64_t(r + i) * C + c] = v[i];
+                        }
+                    } else {
+                        // Slots past the rank hold sums of zeros (NaN where x is not finite) times a z that
+                        // need not be finite.  (Ranges' slices are cleared where they are summed: masks
+                        // among those stores took 1.5 to 4 of 32 us at 4096 x 1024, rank 128.)
+                        int keep = rank - r;
+                        asm volatile("" : "+v"(keep));  // (formed here: ahead, all blocks' masks took registers)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) v[i] = i < keep ? v[i] : 0.0f;
+                        T *o = w.out + int64_t(now) * mat;
+                        if (w.rows_c) {
+                            T t[4];
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) t[i] = T(v[i]);
+                            __builtin_memcpy(o + int64_t(c) * R + r, t, 8);
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) o[int64_t(r + i) * C + c] = T(v[i]);
+                        }
+                    }
+                }
+        }
+        if (id != now) {
+            if (!w.part) {
+                // the one range writes every adapter: zeros for those without tokens
+                const int upto = id == kNone ? adapters : id;
+                for (int z = next; z < upto; z += deals) zero_tile(w.out + int64_t(z) * R * C, w.rows_c, c0, C, R);
+            }
+            if (id == kNone) return;
+            next = id + deals;
+            if (marks && tid == 0) present[int64_t(slice) * adapters + id] = 1;
+#pragma unroll
+            for (int s = 0; s < 2; ++s)
+#pragma unroll
+                for (int b = 0; b < RB; ++b) acc[s][b][0] = acc[s][b][1] = floatx4{0.f, 0.f, 0.f, 0.f};
+        }
+        now = id;
+        from = a + 1;
+        if constexpr (kLowScaled<T>) power = low_key_power(a);
 
         for (int c = 0; c < pieces; ++c) {
             // its tokens of the piece, in order
@@ -542,47 +670,6 @@ wgrad_kernel(WgradTask<T> p, WgradTask<T> q, const int32_t *__restrict__ index, 
                         for (int cb = 0; cb < 2; ++cb) acc[part][b][cb] = mfma16<T>(lv[part][b], zv[cb], acc[part][b][cb]);
             }
         }
-
-        const int rank = w.part ? R : low_rank_of(ranks, a, R);
-        // lane: rank slots 16 b + 4 g + i of column c0 + 32 wave + 16 cb + j16
-#pragma unroll
-        for (int b = 0; b < RB; ++b)
-#pragma unroll
-            for (int cb = 0; cb < 2; ++cb) {
-                const int c = c0 + wave * 32 + cb * 16 + j16, r = b * 16 + 4 * g;
-                if (c >= C || r >= R) continue;
-                float v[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) v[i] = fmaf(acc[1][b][cb][i], 1.0f / LowSplit<T>::kLoScale, acc[0][b][cb][i]);
-                const int64_t mat = int64_t(R) * C;
-                if (w.part) {
-                    float *o = w.part + (int64_t(slice) * adapters + a) * mat;
-                    if (w.rows_c) {
-                        __builtin_memcpy(o + int64_t(c) * R + r, v, 16);
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) o[int64_t(r + i) * C + c] = v[i];
-                    }
-                } else {
-                    // Slots past the rank hold sums of zeros (NaN where x is not finite) times a z that
-                    // need not be finite.  (Ranges' slices are cleared where they are summed: masks
-                    // among those stores took 1.5 to 4 of 32 us at 4096 x 1024, rank 128.)
-                    int keep = rank - r;
-                    asm volatile("" : "+v"(keep));  // (formed here: ahead, all blocks' masks took registers)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) v[i] = i < keep ? v[i] : 0.0f;
-                    T *o = w.out + int64_t(a) * mat;
-                    if (w.rows_c) {
-                        T t[4];
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) t[i] = T(v[i]);
-                        __builtin_memcpy(o + int64_t(c) * R + r, t, 8);
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) o[int64_t(r + i) * C + c] = T(v[i]);
-                    }
-                }
-            }
     }
 }
 
@@ -668,7 +755,7 @@ hipError_t add(const LowRank &lr, const void *x, int64_t ldx, const void *base, 
                int M, int N, int K, void *ws, hipStream_t st) {
     T *low = static_cast<T *>(ws);
     if (low_rank_few(M)) return launch_low_rank_tokens(lr, x, ldx, base, ldb, 0, out, ldo, M, N, K, st);
-    const ShrinkTask<T> p{static_cast<const T *>(x), ldx, static_cast<const T *>(lr.down), low, K};
+    const ShrinkTask<T> p{static_cast<const T *>(x), ldx, static_cast<const T *>(lr.down), low, K, nullptr};
     const hipError_t e = shrink<T, false>(p, p, lr, M, st);
     if (e != hipSuccess) return e;
     return expand<T, false>(static_cast<const T *>(lr.up), low, lr, base, ldb, out, ldo, M, N, st);
@@ -681,10 +768,11 @@ hipError_t bwd(const LowRankBwd &b, hipStream_t st) {
     const LowRankPlan pl = low_rank_plan(lr.adapters, R, M, N, K);
     uint8_t *ws = static_cast<uint8_t *>(b.ws);
     T *low = reinterpret_cast<T *>(ws + pl.low), *dlow = reinterpret_cast<T *>(ws + pl.dlow);
+    int32_t *keys = reinterpret_cast<int32_t *>(ws + pl.keys);  // dy's tokens, then x's
     hipError_t e;
     if (M > 0) {
-        const ShrinkTask<T> p{static_cast<const T *>(b.dy), b.lddy, static_cast<const T *>(lr.up), dlow, N};
-        const ShrinkTask<T> q{static_cast<const T *>(b.x), b.ldx, static_cast<const T *>(lr.down), low, K};
+        const ShrinkTask<T> p{static_cast<const T *>(b.dy), b.lddy, static_cast<const T *>(lr.up), dlow, N, keys};
+        const ShrinkTask<T> q{static_cast<const T *>(b.x), b.ldx, static_cast<const T *>(lr.down), low, K, keys + M};
         if ((e = shrink<T, true>(p, q, lr, M, st)) != hipSuccess) return e;
         if (low_rank_few(M)) {
             hipLaunchKernelGGL((tokens_dx_kernel<T>), dim3((K + 511) / 512, M), dim3(256), 0, st,
@@ -701,9 +789,9 @@ hipError_t bwd(const LowRankBwd &b, hipStream_t st) {
     float *part1 = part0 ? part0 + pl.slices * n0 : nullptr;
     int32_t *counts = reinterpret_cast<int32_t *>(ws + pl.counts);
     const WgradTask<T> p{static_cast<const T *>(b.x), b.ldx, dlow, part0, static_cast<T *>(b.ddown), K, (K + 127) / 128,
-                         false};
+                         false, keys};
     const WgradTask<T> q{static_cast<const T *>(b.dy), b.lddy, low, part1, static_cast<T *>(b.dup), N, (N + 127) / 128,
-                         true};
+                         true, keys + M};
     const dim3 grid(p.tiles + q.tiles, pl.slices, pl.deals);
 #define SSG_WGRAD(RB) \
     hipLaunchKernelGGL((wgrad_kernel<T, RB>), grid, dim3(256), 0, st, p, q, lr.index, lr.ranks, lr.adapters, R, M, pl.range, \
@@ -733,7 +821,8 @@ LowRankPlan low_rank_plan(int adapters, int R, int64_t M, int64_t N, int64_t K) 
     LowRankPlan p;
     p.low = 0;
     p.dlow = p.low + up256(low_plane(M, R) * 4);
-    p.part = p.dlow + up256(low_plane(M, R) * 4);
+    p.keys = p.dlow + up256(low_plane(M, R) * 4);
+    p.part = p.keys + up256(2 * M * 4);
     // Token ranges: the workgroups that the CUs hold at once (by LDS), of at least
     // 256 tokens and at most what the list holds, in at most 256 MiB of slices;
     // one range if a large pool's slices do not fit.
@@ -783,11 +872,11 @@ hipError_t launch_low_rank_shrink(const LowRank &lr, const void *x, int64_t ldx,
                                   hipStream_t st) {
     if (lr.dtype == DT_F16) {
         using T = _Float16;
-        const ShrinkTask<T> p{static_cast<const T *>(x), ldx, static_cast<const T *>(lr.down), static_cast<T *>(low), K};
+        const ShrinkTask<T> p{static_cast<const T *>(x), ldx, static_cast<const T *>(lr.down), static_cast<T *>(low), K, nullptr};
         return shrink<T, false>(p, p, lr, M, st);
     }
     using T = __bf16;
-    const ShrinkTask<T> p{static_cast<const T *>(x), ldx, static_cast<const T *>(lr.down), static_cast<T *>(low), K};
+    const ShrinkTask<T> p{static_cast<const T *>(x), ldx, static_cast<const T *>(lr.down), static_cast<T *>(low), K, nullptr};
     return shrink<T, false>(p, p, lr, M, st);
 }
 

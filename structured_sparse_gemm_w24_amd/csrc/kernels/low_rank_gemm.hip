@@ -58,6 +58,18 @@ struct LowRankAfter {
                     for (int i = 0; i < 16; ++i) acc[tn][tm][i] = __builtin_nanf("");
             }
         }
+        // Powers of two of the tokens' low values: the product so far is divided by them
+        // before the first adapter, and everything multiplied at the end.
+        int power[TM] = {};
+        bool scaled = false;
+        auto scale = [&](int sign) {
+#pragma unroll
+            for (int tn = 0; tn < TN; ++tn)
+#pragma unroll
+                for (int tm = 0; tm < TM; ++tm)
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) acc[tn][tm][i] = __builtin_amdgcn_ldexpf(acc[tn][tm][i], sign * power[tm]);
+        };
         uint32_t hit[TN][TM];  // channels whose weights of this token's adapter are broken
 #pragma unroll
         for (int tn = 0; tn < TN; ++tn)
@@ -90,6 +102,7 @@ struct LowRankAfter {
 #pragma unroll 1
             for (int a0 = next(); a0 >= 0; a0 = next()) {
                 const int a1 = next();
+                const bool opening = first && k0 == 0;
                 const int rank0 = low_rank_of(ranks, a0, R), rank1 = a1 >= 0 ? low_rank_of(ranks, a1, R) : 0;
                 if (!first || k0 > 0) __syncthreads();  // the last pair has been used
                 if (first)
@@ -148,6 +161,16 @@ struct LowRankAfter {
                 }
                 __syncthreads();
                 if (loader) continue;
+                if (opening) {
+#pragma unroll
+                    for (int tm = 0; tm < TM; ++tm) {  // (slots 0..7, for both halves of the wave)
+                        const uint8_t *p = smem + BM / 32 * 4096 + (wm * TM + tm) * 4096 + r * 16;
+                        const int e = low_exponent_of(*reinterpret_cast<const u32x4 *>(p));
+                        power[tm] = mine[tm] >= 0 && mine[tm] < adapters ? e : 0;
+                        scaled = scaled || __ballot(power[tm] != 0) != 0;
+                    }
+                    if (scaled) scale(-1);
+                }
 #pragma unroll 1
                 for (int u = 0; u < 2; ++u) {
                     const int a = u ? a1 : a0;
@@ -176,7 +199,7 @@ struct LowRankAfter {
                             u32x4 lo = *reinterpret_cast<const u32x4 *>(p + BM / 32 * 4096);
                             const bool use = mine[tm] == a && k + 8 * h < R;
                             hi = use ? hi : u32x4{0, 0, 0, 0};
-                            lo = use ? lo_unscaled<_Float16>(lo) : u32x4{0, 0, 0, 0};
+                            lo = use ? lo_value<_Float16>(lo) : u32x4{0, 0, 0, 0};
 #pragma unroll
                             for (int tn = 0; tn < TN; ++tn) {
                                 acc[tn][tm] = mfma32<_Float16>(w[tn], hi, acc[tn][tm]);
@@ -193,6 +216,7 @@ struct LowRankAfter {
                 }
             }
         }
+        if (scaled) scale(1);
         uint32_t any = 0;
 #pragma unroll
         for (int tn = 0; tn < TN; ++tn)

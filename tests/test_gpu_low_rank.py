@@ -225,6 +225,47 @@ def test_index_outside_the_pool_gives_nan_rows(lib, gpu, m):
     assert torch.equal(got[1], ref[1]) and torch.equal(got[2], ref[2])
 
 
+@pytest.mark.parametrize("m", [128, 129, 700])
+@pytest.mark.parametrize("size", [18, 5, -9, -13, -20])
+@pytest.mark.parametrize("forward", [True, False])
+def test_low_rank_values_of_any_size(lib, gpu, m, size, forward):
+    """Low-rank values far above fp16's largest number and far below its steps (about 2^size, times 2^-6
+    to 2^6 by token), in pools whose other side brings the result back into range: the tolerance of every
+    other case, in every call, and the same on both sides of the few tokens' form."""
+    import torch
+    n, k, r, a = 320, 192, 24, 4
+    c = make(m + size, "f16", m, n, k, r, a, "mixed", ranks=False)
+    g = torch.Generator(device="cuda").manual_seed(3)
+    by_token = torch.exp2(torch.randint(-6, 7, (m, 1), generator=g, device="cuda").double())
+    # (first . input) is the low-rank value: forward down . x, in the gradient up^T . dy
+    first, second, key, other = ("down", "up", "x", "dy") if forward else ("up", "down", "dy", "x")
+    pool, back = 2.0 ** min(max(size / 2, -10), 11), 2.0 ** min(max(-size, -12), 14)
+    for q, f in ((first, pool), (second, back), (key, by_token * 2.0 ** min(size - np.log2(pool), 7)),
+                 (other, 2.0 ** (max(-size, -12) - 3 if size > 0 else -size // 2 - 8))):
+        c[q] = (c[q].double() * f).half()
+        assert torch.isfinite(c[q]).all()
+    args = (c["down"], c["up"], c["index"], c["scale"])
+
+    def check(have, ref, total, chain):
+        inside = ref.abs() < 65000  # (a result past fp16's largest number is infinite)
+        assert inside.double().mean() > 0.5
+        close(have[inside], ref[inside], total[inside], "f16", chain)
+    if forward:
+        w = wl.random_24_f16(np.random.default_rng(m), 1, k, n)["Wp"]
+        vals, meta = lib.w24_pack_f16(w)
+        vals, meta = torch.from_numpy(vals).cuda(), torch.from_numpy(meta.view(np.int32)).cuda()
+        delta, total = reference(c)
+        base, x, w = c["base"].double(), c["x"].double(), torch.from_numpy(w).cuda().double()
+        check(lib.low_rank_add(c["base"], c["x"], *args), base + delta, base.abs() + total, k + r)
+        check(lib.w24_low_rank_gemm_f16(c["x"], vals, meta, *args), x @ w + delta, x.abs() @ w.abs() + total, k + r)
+    dx, ddown, dup = lib.low_rank_backward(c["dy"], c["x"], *args, base=c["xbase"])
+    ref = reference(c, backward=True)
+    base = c["xbase"].double()
+    check(dx, base + ref[0][0], base.abs() + ref[0][1], n + r)
+    check(ddown, *ref[1], n + m)
+    check(dup, *ref[2], k + m)
+
+
 @pytest.mark.parametrize("dtype", ["f16", "bf16"])
 @pytest.mark.parametrize("m,r,rank", [(60, 8, 8), (60, 24, 13), (200, 8, 8), (200, 24, 13), (200, 128, 100)])
 def test_infinite_low_rank_values_follow_the_formula(lib, gpu, dtype, m, r, rank):
