@@ -206,6 +206,110 @@ def test_slots_past_the_rank_get_zeros_beside_inputs_that_are_not_finite(lib, gp
         assert torch.equal(ddown[keep], ref[1][keep]) and torch.equal(dup[keep], ref[2][keep])
 
 
+TILES = [  # tokens, channels, the tile that the product takes there
+    (150, 256, (32, 32)), (512, 2048, (64, 64)), (1024, 2048, (64, 128)), (1100, 2048, (128, 128)),
+    (4500, 2816, (256, 256))]
+
+
+def _fused(lib, m, n, k, r, a, seed):
+    """A call of the fused product with every tile's tokens mixed over the adapters, and its pieces."""
+    import torch
+    c = make(seed, "f16", m, n, k, r, a, "mixed")
+    w = wl.random_24_f16(np.random.default_rng(seed), 1, k, n)["Wp"]
+    vals, meta = lib.w24_pack_f16(w)
+    vals, meta = torch.from_numpy(vals).cuda(), torch.from_numpy(meta.view(np.int32)).cuda()
+
+    def call(down=None, up=None, index=None, x=None):
+        return lib.w24_low_rank_gemm_f16(c["x"] if x is None else x, vals, meta, c["down"] if down is None else down,
+                                         c["up"] if up is None else up, c["index"] if index is None else index,
+                                         c["scale"], c["ranks"])
+    return c, torch.from_numpy(w).cuda().double(), call
+
+
+@pytest.mark.parametrize("r,a", [(24, 5), (128, 5), (128, 2)])
+@pytest.mark.parametrize("m,n,tile", TILES)
+def test_every_tile_of_the_fused_product(lib, gpu, m, n, tile, r, a):
+    """Each tile of the fused product (with and without loader waves, one and more waves, one and two
+    rounds of 64 slots): its values, and what NaN past the ranks, a broken adapter and
+    an index outside the pool do."""
+    import torch
+    assert lib.tile_choice(1, m, n, 128) == tile
+    c, w, call = _fused(lib, m, n, 128, r, a, m + r)
+    c["ranks"][1] = r
+    out = call()
+    delta, size = reference(c)
+    x = c["x"].double()
+    close(out, x @ w + delta, x.abs() @ w.abs() + size, "f16", 128 + r, r)
+
+    # slots past the ranks
+    down, up = c["down"].clone(), c["up"].clone()
+    for i in range(a):
+        q = int(c["ranks"][i])
+        down[i, q:], up[i, :, q:] = float("nan"), float("inf")
+    assert torch.equal(call(down, up), out)
+
+    # a broken adapter: its own tokens, in the broken channels
+    mine = c["index"] == 1
+    slots = [0, r // 2, r - 1]
+    channels = torch.tensor([0, 7, 31, 32, n // 2 + 5, n - 1], device="cuda")
+    up = c["up"].clone()
+    for i, ch in enumerate(channels.tolist()):
+        up[1, ch, slots[i % 3]] = (float("nan"), float("inf"), float("-inf"))[i % 3]
+    got = call(up=up)
+    expect = torch.zeros(m, n, dtype=torch.bool, device="cuda")
+    expect[:, channels] = mine[:, None].expand(-1, len(channels))
+    assert torch.equal(torch.isfinite(got), ~expect)
+    assert torch.equal(got[~expect], out[~expect])
+    down = c["down"].clone()
+    down[1, r - 1, 3] = float("nan")
+    got = call(down=down)
+    assert torch.isnan(got[mine]).all() and torch.equal(got[~mine], out[~mine])
+
+    # a token whose input is not finite
+    x = c["x"].clone()
+    x[m // 2] = float("nan")
+    got = call(x=x)
+    others = torch.arange(m, device="cuda") != m // 2
+    assert torch.isnan(got[m // 2]).all() and torch.equal(got[others], out[others])
+
+    # indices outside the pool
+    index, none = c["index"].clone(), c["index"].clone()
+    bad = torch.zeros(m, dtype=torch.bool, device="cuda")
+    for i, v in ((0, a), (33, -2), (64, 2 ** 31 - 1), (m - 1, -2 ** 31), (m // 2, 65535)):
+        index[i], none[i], bad[i] = v, -1, True
+    got, ref = call(index=index), call(index=none)
+    assert torch.isnan(got[bad]).all() and torch.equal(got[~bad], ref[~bad])
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("m", [60, 300])
+@pytest.mark.parametrize("r", [24, 128])
+def test_broken_weights_mark_their_channels(lib, gpu, dtype, m, r):
+    """Values of `up` that are not finite, in any slot in use: beside a base, exactly their adapter's tokens
+    in exactly their channels are not finite, and nothing else changes; the same of `down` in dx."""
+    import torch
+    n, k, a = 200, 136, 5
+    c = make(m + r, dtype, m, n, k, r, a, "mixed")
+    c["ranks"][1] = r
+    rest = (c["index"], c["scale"], c["ranks"])
+    mine = c["index"] == 1
+    for key, width, call in (
+            ("up", n, lambda p: lib.low_rank_add(c["base"], c["x"], c["down"], p, *rest)),
+            ("down", k, lambda p: lib.low_rank_backward(c["dy"], c["x"], p, c["up"], *rest, base=c["xbase"])[0])):
+        out = call(c[key])
+        pool = c[key].clone()
+        channels = torch.tensor([0, 7, 31, 64, width - 1], device="cuda")
+        for i, ch in enumerate(channels.tolist()):
+            slot = (0, r // 2, r - 1)[i % 3]
+            at = (1, ch, slot) if key == "up" else (1, slot, ch)
+            pool[at] = (float("nan"), float("inf"), float("-inf"))[i % 3]
+        got = call(pool)
+        expect = torch.zeros(m, width, dtype=torch.bool, device="cuda")
+        expect[:, channels] = mine[:, None].expand(-1, len(channels))
+        assert torch.equal(torch.isfinite(got), ~expect)
+        assert torch.equal(got[~expect], out[~expect])
+
+
 @pytest.mark.parametrize("m", [40, 260])
 def test_index_outside_the_pool_gives_nan_rows(lib, gpu, m):
     import torch
