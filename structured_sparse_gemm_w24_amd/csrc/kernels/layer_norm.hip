@@ -377,23 +377,28 @@ ln_cols_kernel(const T *dy, int64_t lddy, const T *x, int64_t ldx, const float *
         if (c + i < N) pw[c + i] = dw[i], pb[c + i] = db[i];
 }
 
-// Sums the workgroups' slices part[G][2N] in order: 32 columns a workgroup, 32
-// threads a column, each over every 32nd slice, then their sums in order.
+// Sums the workgroups' slices part[G][2N] in order: 32 columns a workgroup (a
+// workgroup in turns: a launch ends before 2^32 threads), 32 threads a column, each
+// over every 32nd slice, then their sums in order.
+constexpr int kParamBlocks = 1 << 20;
 __global__ void __launch_bounds__(1024)
 ln_param_kernel(const float *__restrict__ part, int G, int64_t N, float *__restrict__ dw, float *__restrict__ db) {
     __shared__ float s[32][33];
     const int col = threadIdx.x & 31, lane = threadIdx.x >> 5;
-    const int64_t j = int64_t(blockIdx.x) * 32 + col;
-    float a = 0.0f;
-    if (j < 2 * N)
-        for (int g = lane; g < G; g += 32) a += part[int64_t(g) * 2 * N + j];
-    s[lane][col] = a;
-    __syncthreads();
-    if (lane == 0 && j < 2 * N) {
-        a = 0.0f;
+    for (int64_t j0 = int64_t(blockIdx.x) * 32; j0 < 2 * N; j0 += int64_t(gridDim.x) * 32) {
+        const int64_t j = j0 + col;
+        float a = 0.0f;
+        if (j < 2 * N)
+            for (int g = lane; g < G; g += 32) a += part[int64_t(g) * 2 * N + j];
+        s[lane][col] = a;
+        __syncthreads();
+        if (lane == 0 && j < 2 * N) {
+            a = 0.0f;
 #pragma unroll
-        for (int i = 0; i < 32; ++i) a += s[i][col];
-        (j < N ? dw[j] : db[j - N]) = a;
+            for (int i = 0; i < 32; ++i) a += s[i][col];
+            (j < N ? dw[j] : db[j - N]) = a;
+        }
+        __syncthreads();
     }
 }
 
@@ -502,8 +507,9 @@ hipError_t bwd(const LnBwd &a, hipStream_t st) {
     }
     if constexpr (PARAM) {
         if (e != hipSuccess) return e;
-        hipLaunchKernelGGL(ln_param_kernel, dim3(int((2 * a.N + 31) / 32)), dim3(1024), 0, st, a.part, slices, a.N,
-                           a.dw, a.db);
+        const int64_t groups = (2 * a.N + 31) / 32;
+        hipLaunchKernelGGL(ln_param_kernel, dim3(int(groups < kParamBlocks ? groups : kParamBlocks)), dim3(1024), 0, st,
+                           a.part, slices, a.N, a.dw, a.db);
         e = hipGetLastError();
     }
     return e;

@@ -272,3 +272,21 @@ def test_every_tail_of_a_row(lib, gpu, dtype, n):
     for i in (0, 5):
         one = lib.layer_norm(c["x"][i:i + 1], c["w"], c["b"], residual=c["res"][i:i + 1])
         assert torch.equal(one[0], y[i:i + 1]) and torch.equal(one[2], rstd[i:i + 1])
+
+
+def test_parameter_gradients_of_a_very_long_row(lib, gpu):
+    """A row past 2^26 elements: the column sums' launch stays below 2^32 threads."""
+    import torch
+    m, n = 2, (1 << 26) + 5
+    g = torch.Generator(device="cuda").manual_seed(1)
+    x, dy = (torch.randn(m, n, generator=g, device="cuda", dtype=torch.float16) for _ in range(2))
+    mean = torch.tensor([0.1, -0.2], device="cuda")
+    rstd = torch.tensor([0.9, 1.3], device="cuda")
+    dx, dw, db = lib.layer_norm_backward(dy, x, mean, rstd)
+    at = torch.cat([torch.arange(0, n, 9973, device="cuda"), torch.arange(n - 70, n, device="cuda")])
+    d = dy[:, at].double()
+    xh = (x[:, at].double() - mean.double()[:, None]) * rstd.double()[:, None]
+    # (the difference, the product and m sums in fp32: 2^-24 each)
+    assert ((dw[at].double() - (d * xh).sum(0)).abs() <= E * (m + 8) * (d.abs() * (xh.abs() + 1)).sum(0)).all()
+    assert ((db[at].double() - d.sum(0)).abs() <= E * (m + 8) * d.abs().sum(0)).all()
+    assert torch.isfinite(dx[:, at]).all()
