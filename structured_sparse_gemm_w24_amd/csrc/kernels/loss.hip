@@ -581,9 +581,15 @@ LossPlan loss_plan(int64_t M, int64_t V, int64_t D, bool pack_x, bool pack_w, bo
     if (pack_x || backward) p.x = take(M * p.dp * 2);
     if (pack_w) p.w = take(V * p.dp * 2);
     if (!backward) {
-        // pieces only where w passes the products' 4 GiB
+        // pieces only where w passes the products' 4 GiB, or the tiles (of 512 threads) the
+        // 2^32 threads of a launch
         p.piece = (int64_t(4000) << 20) / (p.dp * 2) / 256 * 256;
         if (p.piece > V) p.piece = V;
+        auto launch_tiles = [&](int64_t n) {
+            const LossTileShape &t = kLossTiles[loss_tile(M, n, false)];
+            return (M + t.bm - 1) / t.bm * ((n + t.bn - 1) / t.bn);
+        };
+        while (launch_tiles(p.piece) >= (int64_t(1) << 23)) p.piece = up(p.piece / 2, 256);
         p.tiles = 0;
         for (int64_t v0 = 0; v0 < V; v0 += p.piece) {
             const int64_t n = V - v0 < p.piece ? V - v0 : p.piece;

@@ -110,6 +110,20 @@ def test_split_sum_over_the_vocabulary(lib, gpu, dtype, m, v, d):
     assert (dx[m // 2] == 0).all()
 
 
+def test_more_tiles_than_one_launch_takes(lib, gpu):
+    """Rows times entries past the 2^32 threads of one launch: the statistics come from two."""
+    import torch
+    m, v, d = 7_990_001, 69_000, 64
+    g = torch.Generator(device="cuda").manual_seed(3)
+    x = torch.randn(m, d, generator=g, device="cuda", dtype=torch.float16)
+    w = (torch.randn(v, d, generator=g, device="cuda") * 0.2).half()
+    t = torch.randint(0, v, (m,), generator=g, device="cuda")
+    loss, lse = lib.linear_cross_entropy(x, w, t)
+    at = torch.cat([torch.arange(0, m, 79_861, device="cuda"), torch.arange(m - 40, m, device="cuda")])
+    check_forward((loss[at], lse[at]), x[at], w, t[at])
+    assert torch.isfinite(loss).all() and torch.isfinite(lse).all()
+
+
 def test_strides(lib, gpu):
     import torch
     x, w, t, dloss = make(1, "f16", 77, 300, 3 * 128)
