@@ -488,8 +488,11 @@ int linear_cross_entropy_forward(int32_t dtype, const void *x, int64_t ldx, cons
  * forward pass's lse: for G[m][v] = dloss[m] (exp(z[m][v] - lse[m]) - [v ==
  * target[m]]), zero in ignored rows whatever their x holds,
  *   dx = G . w  [M][D]  and  dw = G^T . x  [V][D]  (row strides lddx, lddw)
- * in dtype, rounded once from fp32 sums.  The logits are computed again in
- * pieces of the vocabulary; the workspace holds a copy of x and one piece's G
+ * in dtype, rounded once from fp32 sums of products of G, rounded to dtype's
+ * 16 bits, with w and x.  (fp16 holds G no finer than 2^-36 of the largest
+ * finite |dloss|, so that a row that weighs less than about 2^-18 of the
+ * heaviest loses digits of its dx; bf16 has no such limit.)  The logits are
+ * computed again in pieces of the vocabulary; the workspace holds a copy of x and one piece's G
  * (together at most 256 MiB, or the copy and 2048 entries' G), dx's fp32 sums,
  * and a copy of a w that is not read in place.  A target outside [0, V) makes
  * its row of dx, and dw, NaN; a dloss that is not finite, in a row that is not

@@ -336,7 +336,7 @@ def linear_cross_entropy(x, w, target, ignore_index=-100, workspace=None):
 def linear_cross_entropy_backward(dloss, x, w, target, lse, ignore_index=-100, out=None, dw_out=None, workspace=None):
     """Gradient of linear_cross_entropy for dloss float32 [M] (the derivative by each row's loss: 1 / rows for
     their mean) and its lse.  Returns (dx, dw) in x's type; the logits are computed again in pieces of the
-    vocabulary."""
+    vocabulary.  In float16 a row whose |dloss| is below about 2^-18 of the largest loses digits of its dx."""
     torch = _torch()
     dt, m, v, d, ldx, ldw = _head(x, w, target)
     _flat(dloss, torch.float32, (m,), x, "dloss")

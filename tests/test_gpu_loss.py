@@ -187,6 +187,28 @@ def test_a_weight_that_is_not_finite_stays_with_its_row(lib, gpu, dtype, value, 
         assert torch.equal(p, q)
 
 
+def test_row_weights_of_a_wide_range_in_fp16(lib, gpu):
+    """Weights from 1 to 2^-30 in fp16: G's step of 2^-36 of the largest bounds every row, and the rows
+    down to 2^-18 of it keep their digits.  For those: G's rounding and dx's (2^-11 each), and over a row
+    of 500 entries of size 1.5 / 8 steps of at most 2^-37 each, beside a gradient of about 2^-18 times that
+    size: 2^-9 of the row's norm in all."""
+    import torch
+    g = torch.Generator(device="cuda").manual_seed(11)
+    w = (torch.randn(500, 64, generator=g, device="cuda") * 1.5 / 8).half()
+    x = torch.randn(124, 64, generator=g, device="cuda").half()
+    t = torch.randint(0, 500, (124,), generator=g, device="cuda")
+    dloss = torch.exp2(-0.25 * torch.arange(124, device="cuda").float())
+    lse = lib.linear_cross_entropy(x, w, t)[1]
+    # (a common factor that keeps the lightest rows above fp16's smallest step)
+    dloss *= 1024.0
+    got = lib.linear_cross_entropy_backward(dloss, x, w, t, lse)
+    check_backward(got, x, w, t, dloss, lse, "f16")
+    _, _, grad, _ = gradient(x, w, t, dloss, lse)
+    ref, heavy = grad @ w.double(), dloss >= 1024.0 * 2.0 ** -18
+    off = (got[0].double() - ref).norm(dim=1)
+    assert heavy.sum() == 73 and (off[heavy] <= 2.0 ** -9 * ref.norm(dim=1)[heavy]).all()
+
+
 def test_ignored_rows_and_zero_weights(lib, gpu):
     import torch
     x, w, t, dloss = make(4, "f16", 70, 200, 64)
