@@ -370,6 +370,40 @@ def test_low_rank_values_of_any_size(lib, gpu, m, size, forward):
     check(dup, *ref[2], k + m)
 
 
+@pytest.mark.parametrize("m,n,k,r,a,index", [
+    (100, 136, 512, 24, 26, "mixed"), (600, 128, 128, 16, 60, "mixed"), (3000, 64, 64, 8, 40, "runs"),
+    (6200, 256, 136, 16, 2, "runs"), (5000, 1024, 512, 128, 400, "mixed")])
+def test_gradients_of_tokens_of_mixed_sizes(lib, gpu, m, n, k, r, a, index):
+    """Low-rank values from 2^-25 to 2^19 within an adapter's tokens: one and several ranges, adapters dealt
+    over workgroups, and a large pool's one long range; every call twice the same."""
+    import torch
+    c = make(m + a, "f16", m, n, k, r, a, index)
+    g = torch.Generator(device="cuda").manual_seed(4)
+    for key in ("x", "dy"):
+        size = torch.exp2(torch.randint(-18, 12, (m, 1), generator=g, device="cuda").double())
+        c[key] = (c[key].double() * size).half()
+    for key in ("down", "up"):
+        size = torch.exp2(torch.randint(-7, 7, (a, 1, 1), generator=g, device="cuda").double())
+        c[key] = (c[key].double() * size).half()
+    assert all(torch.isfinite(c[q]).all() for q in ("x", "dy", "down", "up"))
+    args = (c["dy"], c["x"], c["down"], c["up"], c["index"], c["scale"], c["ranks"], c["xbase"])
+    got = lib.low_rank_backward(*args)
+    dx, ddown, dup = reference(c, backward=True)
+    base = c["xbase"].double()
+    for have, ref, total, chain in ((got[0], base + dx[0], base.abs() + dx[1], n + r), (got[1], *ddown, n + m),
+                                    (got[2], *dup, k + m)):
+        inside = ref.abs() < 65000
+        assert inside.double().mean() > 0.5
+        close(have[inside], ref[inside], total[inside], "f16", chain)
+    for p, q in zip(got, lib.low_rank_backward(*args)):
+        assert torch.equal(p, q)
+    out = lib.low_rank_add(c["base"], c["x"], *args[2:7])
+    delta, total = reference(c)
+    ref = c["base"].double() + delta
+    inside = ref.abs() < 65000
+    close(out[inside], ref[inside], (c["base"].double().abs() + total)[inside], "f16", k + r)
+
+
 @pytest.mark.parametrize("dtype", ["f16", "bf16"])
 @pytest.mark.parametrize("m,r,rank", [(60, 8, 8), (60, 24, 13), (200, 8, 8), (200, 24, 13), (200, 128, 100)])
 def test_infinite_low_rank_values_follow_the_formula(lib, gpu, dtype, m, r, rank):
