@@ -4,7 +4,9 @@ adapters, the cross entropy of a linear head.
 Same manner as ``_lib``: torch device tensors in and out, one library call on
 torch's current stream, ``SsgError`` on a nonzero status, no fallback.  Rows may
 be strided (a 2-D tensor whose last axis is contiguous); workspaces come from
-torch's caching allocator, whose reuse is ordered by the stream.
+torch's caching allocator, whose reuse is ordered by the stream.  The gradients
+are calls of their own and no autograd functions: results carry no history, also
+where an input requires a gradient.
 """
 
 from __future__ import annotations
@@ -154,7 +156,7 @@ def layer_norm(x, weight=None, bias=None, eps=1e-5, residual=None, out=None, sum
     """y = (s - mean) * rstd * weight + bias over the last axis of x [M, N], where s = x, or
     x + residual rounded to x's type.  Returns (y, mean, rstd), with a residual
     (y, mean, rstd, s); mean and rstd are fp32 [M].  x: float16, bfloat16 or float32;
-    weight and bias [N]: x's type or float32."""
+    weight and bias [N]: both of x's type or both float32."""
     torch = _torch()
     dt = _code(x, "x")
     shape = _matrix(x, "x")

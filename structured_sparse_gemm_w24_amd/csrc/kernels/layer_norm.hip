@@ -11,13 +11,17 @@
 // Bound by memory: forward reads and writes every row once, backward reads dy
 // and x (and dres) once and writes dx once.  A row therefore stays in registers
 // as fp32 between the statistics and the output, held by TPR threads with C
-// 16-byte chunks each; only rows past 16384 16-bit elements (backward 8192) are
-// read again.  The variance is the sum of squared distances from the finished
+// 16-byte chunks each; only rows past 16384 16-bit or 8192 fp32 elements (backward
+// 8192 and 4096) are read again.  The variance is the sum of squared distances from the finished
 // mean, so an offset that is large against the spread costs no digits.
 // Workgroups are persistent over rows: w and b are loaded once, the next turn's
 // rows are fetched while this turn's are reduced, and outputs are streaming
 // stores (without the last two, forward ran 18.7 instead of 16.8 us at
-// 12608 x 768 fp16 with a residual).  The backward pass keeps its column sums
+// 12608 x 768 fp16 with a residual).  At most 768 of them, three a CU: by graph
+// with 256 / 512 / 768 / 1536 / 4096, 12608 x 768 24.4 / 20.2 / 20.7 / 20.4 / 21.9
+// us, without residual 23.2 / 17.7 / 16.1 / 16.1 / 17.5, 3000 x 8192 41.9 / 40.6 /
+// 41.0 / 42.8 / 47.2, 1500 x 3001 fp32 20.0 / 16.6 / 15.2 / 18.1 / 18.2, 2865 x 4183
+// bf16 43 / 31 / 36 / 36 / 45.  The backward pass keeps its column sums
 // for dw and db in registers, adds those of a workgroup's rows through LDS and
 // writes one slice a workgroup; a second launch sums the slices in order.  No
 // atomics: results repeat bit for bit.  Its registers (w, dw, db, x, dy and the
@@ -33,7 +37,10 @@
 // wide 36.2 and 50.7), 2865 x 4183 bf16 31.5 us = 3.0 TB/s and 32.6 us, 4099 x
 // 1537 bf16 without residual 12.4 us = 2.0 TB/s and 19.5 us.  Pieces cut at 16-byte boundaries
 // instead of the row's start were slower (60 us at 2865 x 4183: two part pieces a row), and a
-// row's sums would then depend on its place in the batch.
+// row's sums would then depend on its place in the batch.  fp32: forward 1500 x 3001 with
+// residual 15.0 us = 4.9 TB/s, backward 2000 x 4096 19.7 us = 5.4 TB/s and 3.9.  Rows past the
+// register forms: forward 2000 x 20000 fp16 61 us (three reads of a row), backward 2000 x 12001
+// fp16 52 + 32 + 5 us and 2000 x 8192 fp32 55 + 22 + 5 (dx, the column sums' slices, their sum).
 #include "elem.h"
 #include "launch.h"
 

@@ -26,10 +26,14 @@
 // are multiplied by again in fp32.  In fp16 its steps are then 2^-36 of that factor, so
 // rows that weigh less than about 2^-18 of the heaviest lose digits of their dx; a factor
 // for each row would have to come out of the sum over rows in dw again.
-// Measured on MI355X: forward 8192 x 1024 x 32000 fp16 501 us = 1072 TFLOP/s (the
-// library's product alone 431-448 us); backward 6144 x 1024 x 30001 bf16 1069-1091 us
-// = 1038-1059 TFLOP/s, in two pieces, each G 211-220 us, dx 164, dw 158.  The matrix units are
-// busy 0.57 of the forward and 0.41 / 0.61 / 0.55 of the three: what bounds them is
+// The rounding shows: 6144 x 1024 x 30001 bf16 is 0.0019 of its norm off the 64-bit
+// result, where 32-bit probabilities and one rounding of the outputs give 0.0017; a
+// second 16-bit part of G would run both gradient products again, 640 of 1090 us more.
+// Measured on MI355X, several runs: forward 8192 x 1024 x 32000 fp16 501-522 us = 1029-1072
+// TFLOP/s (the library's product alone 431-448 us); backward 6144 x 1024 x 30001 bf16
+// 1069-1109 us = 1021-1059 TFLOP/s, in two pieces, each G 211-221 us, dx 164-168, dw 158-165.
+// The matrix units are
+// busy 0.57 of the forward and 0.41 / 0.62 / 0.54 of the three: what bounds them is
 // LDS, whose reads and direct writes fill its port, and for G the epilogue (an
 // exponential a logit and 184 MB of G written; a library product of that size, at
 // the 1084 TFLOP/s it reaches at twice the width, takes 175).
@@ -330,8 +334,8 @@ loss_zero_kernel(uint16_t *__restrict__ dst, int64_t ld, int64_t rows, int D) {
 // NaN, is not finite in its own G alone.)  The others: x to contiguous rows of dp
 // columns, zeros past D and in ignored rows, whose G is zero: read as they lie, an
 // infinity or NaN there (padding that nothing has written) would reach all of
-// dw = G^T x as 0 * inf.  The copy costs the call nothing while it takes less
-// than workgroup 0's 8 us (6144 x 1024: 5).
+// dw = G^T x as 0 * inf.  Beside workgroup 0, which takes 8 us alone, the copy costs
+// little: 6144 x 1024 10.6 us in all.
 __global__ void __launch_bounds__(1024)
 loss_prepare_kernel(const float *__restrict__ dloss, const int64_t *__restrict__ target, int64_t ignore, int M,
                     float div, float *__restrict__ out, const uint16_t *__restrict__ x, int64_t ldx,
@@ -434,6 +438,10 @@ long loss_cost(int64_t M, int64_t N, bool trans, LossTile *tile) {
         const long c = rounds * (trans ? s.cost_trans : s.cost);
         if (t == LT_256 || c < best) best = c, *tile = LossTile(t);
     }
+    // Fewer than 96 tiles of 128 x 128 leave most CUs idle: 64 x 64 (by graph, with the cut
+    // at 48 / 96 / 192: 64 such tiles, 512 x 2048 x 1024, forward 19.1 / 16.7 / 16.8 us,
+    // gradient 45 / 40 / 39; 96 tiles, 1024 x 1500 x 1024, 19.4 / 19.5 / 17.8 and 50 / 51 / 48;
+    // the gradient of 2048 x 2048 x 1024, whose products have 128 and 256, 62.6 / 62.7 / 75.9).
     if (tiles(int(M), int(N), 128, 128) < 96) *tile = LT_64;
     return best;
 }

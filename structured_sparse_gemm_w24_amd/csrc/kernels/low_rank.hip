@@ -15,11 +15,14 @@
 // wgrad reads x and dy once; the pools are small beside them, and the products
 // (2 M R (K + N) operations) far below the matrix units' rate.  Measured on
 // MI355X, inputs in rotating buffers (HBM traffic by counter where named):
-//   6144 x 1024 -> 4096 fp16, rank 16, 4 adapters, backward 44.9 us:
-//     both shrinks 15.2 us (62.9 MB read: 4.1 TB/s), expand 6.9 us (25 MB:
-//     3.6 TB/s), wgrad 16.0 us (69 MB: 4.3 TB/s), wgrad_sum 3.9 us
-//   1531 x 768 -> 2312 bf16, rank 32, 8 adapters: shrink 5.6, expand 5.5-7.2 us
-//   32 tokens, 1024 -> 4096, 24 adapters of rank 16 (tokens): 3.5-4.9 us
+//   6144 x 1024 -> 4096 fp16, rank 16, 4 adapters, backward 47 us; medians:
+//     both shrinks 18.0 us (64.8 MB: 3.6 TB/s), expand 8.1 us (26 MB: 3.2 TB/s),
+//     wgrad 18.1 us (72.4 MB: 4.0 TB/s), wgrad_sum 4.1 us (least 15.8, 7.3, 16.4)
+//   4096 x 1024 -> 1024 fp16, rank 128, 4 adapters, backward: 25.2, 15.3, 33.8, 5.5 us;
+//   1755 x 2400 -> 1024, rank 64: 13.9, 10.3, 22.4, 4.1 us.  Bytes would take 5 to 10:
+//     a slice of the pool is fetched, waited for and read before the next one leaves
+//   1531 x 768 -> 2312 bf16, rank 32, 8 adapters: shrink 6.3, expand 8.4 us
+//   32 tokens, 1024 -> 4096, 24 adapters of rank 16 (tokens): 4.6 us
 // The small ones are a chain of a few dependent loads each, not bytes.
 #include "launch.h"
 #include "low_rank.h"
@@ -813,7 +816,25 @@ hipError_t bwd(const LowRankBwd &b, hipStream_t st) {
 
 int64_t low_rank_bytes(int64_t M, int R) { return low_plane(M, R) * 4; }
 
-// Few tokens: one launch on the vector units.
+// Few tokens: one launch on the vector units (in the gradient, dx by token).  The
+// tiled form takes a tile's adapters one after another, each a chain of waits; the
+// tokens' form computes a token's low values again for every 512 channels.  Both, us a
+// call by graph, fp16, K = N, tokens / tiled:
+//   width  adapters  rank    32 tokens    64           128          256          512
+//   1024   32        16      18 / 35      16 / 35      16 / 28      17 / 24      17 / 22
+//   1024   1         128     19 / 21      20 / 22      21 / 22      28 / 22      49 / 22
+//   4096   32        16      16 / 39      16 / 39      18 / 34      25 / 31      39 / 30
+//   4096   32        128     41 / 135     73 / 148     110 / 119    186 / 93     301 / 78
+//   4096   1         16      16 / 19      17 / 19      17 / 18      24 / 18      39 / 19
+//   4096   1         128     29 / 30      46 / 30      86 / 30      161 / 33     309 / 35
+//   4096   32        16, 2:4       22 / 76      25 / 81      31 / 76      47 / 73      67 / 52
+//   4096   1         128, 2:4      42 / 71      59 / 73      103 / 73     184 / 73     333 / 55
+//   4096   32        128, gradient 126 / 204    132 / 219    133 / 194    140 / 174    221 / 231
+//   4096   1         128, gradient  49 / 50      51 / 53      62 / 60      75 / 67      90 / 72
+// 128 is where they meet for many adapters of a high rank and for one of a low rank.
+// It loses from 64 tokens on for one adapter of rank 64 and more at 4096 wide, and
+// above 128 for many of a low rank: how many adapters the tokens have is not known
+// here, and the workspace's size, which follows the form, depends on M and R alone.
 bool low_rank_few(int M) { return M <= 128; }
 
 LowRankPlan low_rank_plan(int adapters, int R, int64_t M, int64_t N, int64_t K) {

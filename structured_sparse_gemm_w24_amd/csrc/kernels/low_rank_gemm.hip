@@ -3,9 +3,9 @@
 // w24_gemm_f16; between the main loop and the epilogue each wave adds its
 // tokens' adapters to the accumulators (low_rank.h), so the sum is rounded
 // once and the adapters cost no second read and write of C.  4096 x 1024 x 4096,
-// rank 64, 12 adapters: 37.6 us (w24_gemm_f16 alone 30; a separate add would read
-// and write 67 MB more, 13 us), after a shrink of 8.  The adapters' 7 us are the
-// tile's end: every workgroup fetches its low values and pool rows at the same
+// rank 64, 12 adapters: 39.3 us, least 37.6 (w24_gemm_f16 alone 30; a separate add
+// would read and write 67 MB more, 13 us), after a shrink of 8.7.  The adapters' 8 us
+// are the tile's end: every workgroup fetches its low values and pool rows at the same
 // time, with no main loop left to hide them.
 #include "gemm_core.h"
 #include "gemm_tiles.h"
