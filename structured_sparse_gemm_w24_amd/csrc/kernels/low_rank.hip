@@ -664,6 +664,7 @@ wgrad_kernel(WgradTask<T> p, WgradTask<T> q, const int32_t *__restrict__ index, 
                 for (int b = 0; b < RB; ++b) {
                     const uint32_t hi = l_at + b * 32, lo = hi + L_STAGE;
                     read_tr(hi, hi + RT * 8, lo, lo + RT * 8, lv[0][b], lv[1][b]);
+                    lv[1][b] = lo_value<T>(lv[1][b]);
                 }
 #pragma unroll
                 for (int part = 0; part < 2; ++part)

@@ -370,6 +370,27 @@ def test_low_rank_values_of_any_size(lib, gpu, m, size, forward):
     check(dup, *ref[2], k + m)
 
 
+@pytest.mark.parametrize("m", [40, 200])
+@pytest.mark.parametrize("r", [8, 24])
+def test_opposite_low_rank_values_cancel_exactly(lib, gpu, m, r):
+    """Two tokens whose low-rank values are 2^15 and -2^15, just past fp16's own range, with the same other
+    side: powers of two throughout, so their gradients' sums are zero to the last bit."""
+    import torch
+    n = k = 64
+    zeros = lambda *s: torch.zeros(*s, dtype=torch.float16, device="cuda")
+    x, dy, down, up = zeros(m, k), zeros(m, n), zeros(1, r, k), zeros(1, n, r)
+    index = torch.full((m,), -1, dtype=torch.int32, device="cuda")
+    index[3] = index[m - 2] = 0
+    down[0, :, 0] = up[0, 0, :] = 2.0 ** 7
+    for value, same, first, second in (("x", "dy", x, dy), ("dy", "x", dy, x)):
+        first[3], first[m - 2], second[3], second[m - 2] = 2.0 ** 8, -2.0 ** 8, 1.0, 1.0
+        _, ddown, dup = lib.low_rank_backward(dy, x, down, up, index)
+        grad = dup if value == "x" else ddown  # sums low . dy, or dlow . x, over both tokens
+        assert (grad == 0).all()
+    out = lib.low_rank_add(None, x, down, up, index)  # (x is 1 here: 2^7 . 2^7 . r of every slot)
+    assert (out[3, 0] == 2.0 ** 14 * r if 2.0 ** 14 * r < 65504 else torch.isinf(out[3, 0])) and (out[3, 1:] == 0).all()
+
+
 @pytest.mark.parametrize("m,n,k,r,a,index", [
     (100, 136, 512, 24, 26, "mixed"), (600, 128, 128, 16, 60, "mixed"), (3000, 64, 64, 8, 40, "runs"),
     (6200, 256, 136, 16, 2, "runs"), (5000, 1024, 512, 128, 400, "mixed")])
