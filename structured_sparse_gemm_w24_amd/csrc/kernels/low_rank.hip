@@ -15,7 +15,7 @@
 // wgrad reads x and dy once; the pools are small beside them, and the products
 // (2 M R (K + N) operations) far below the matrix units' rate.  Measured on
 // MI355X, inputs in rotating buffers (HBM traffic by counter where named):
-//   6144 x 1024 -> 4096 fp16, rank 16, 4 adapters, backward 47 us; medians:
+//   6144 x 1024 -> 4096 fp16, rank 16, 4 adapters, backward 47-52 us; medians:
 //     both shrinks 18.0 us (64.8 MB: 3.6 TB/s), expand 8.1 us (26 MB: 3.2 TB/s),
 //     wgrad 18.1 us (72.4 MB: 4.0 TB/s), wgrad_sum 4.1 us (least 15.8, 7.3, 16.4)
 //   4096 x 1024 -> 1024 fp16, rank 128, 4 adapters, backward: 25.2, 15.3, 33.8, 5.5 us;
