@@ -505,6 +505,85 @@ int linear_cross_entropy_backward(int32_t dtype, const float *dloss, const void 
 int64_t linear_cross_entropy_workspace_bytes(int32_t dtype, int64_t M, int64_t V, int64_t D, int64_t ldx, int64_t ldw,
                                              int32_t backward);
 
+/* ---- Experts: products grouped by expert, microscaled 4-bit weights, and the
+ * gradient norm.  16-byte aligned operands unless a call says otherwise;
+ * nothing is allocated, every call may be captured into a graph.
+ *
+ * offsets int32 [experts + 1] (device): rows offsets[e] .. offsets[e + 1] of the
+ * M rows belong to expert e; an expert may have none.  The device cannot refuse
+ * a call, so offsets outside 0 .. M are clamped to it, and one below an earlier
+ * offset counts as the largest before it.  Output rows of no expert (before
+ * offsets[0], behind offsets[experts]) are left as they are. */
+
+/* out[m] = w[e] . x[m] for the expert e of row m: x [M][K], w [experts][N][K]
+ * contiguous, out [M][N], dtype SSG_DT_F16 or SSG_DT_BF16, fp32 sums, one
+ * rounding.  0 <= M < 2^31, N and K positive multiples of 8 below 2^22, one
+ * weight below 2 GiB, 1 <= experts <= 65535; row strides in multiples of 8, below 2^22. */
+int grouped_gemm(int32_t dtype, const void *x, int64_t ldx, const void *w, const int32_t *offsets, int32_t experts,
+                 void *out, int64_t ldo, int64_t M, int64_t N, int64_t K, void *stream);
+
+/* Its gradients for dy [M][N]: dx[m] = w[e]^T . dy[m] [M][K], and dw [experts][N][K]
+ * contiguous, dw[e] = sum over e's rows of dy[m] x[m]^T (zeros for an expert
+ * without rows).  dx or dw may be null: not computed (then w, or x, may be null
+ * too).  No atomics: results repeat bit for bit. */
+int grouped_gemm_backward(int32_t dtype, const void *dy, int64_t lddy, const void *x, int64_t ldx, const void *w,
+                          const int32_t *offsets, int32_t experts, void *dx, int64_t lddx, void *dw, int64_t M,
+                          int64_t N, int64_t K, void *stream);
+
+/* Microscaled 4-bit rows (MXFP4: E2M1 values, every 32 along K share a scale).
+ * A packed matrix of M rows of K values has, with kp = K rounded up to 128,
+ *   codes  [M][kp / 2]   value 2i in the low half of byte i; a code's low three
+ *                        bits select 0, .5, 1, 1.5, 2, 3, 4, 6, bit 3 is the sign
+ *   scales [M][kp / 32]  2^(byte - 127); 255: the block is NaN
+ * both contiguous.  Codes past K are 0 (their scales any but 255).
+ *
+ * mxfp4_quantize: scale byte max(0, floor(log2 max|x|) + 125) of each block,
+ * code the nearest magnitude to |x| / scale (ties to the even code, past 6: 6).
+ * A block with an infinity or NaN gets byte 255 and codes 0.  x of any dtype,
+ * element-aligned, any row stride >= K. */
+int mxfp4_quantize(int32_t dtype, const void *x, int64_t ldx, uint8_t *codes, uint8_t *scales, int64_t M, int64_t K,
+                   void *stream);
+/* out [M][K] of any dtype: the values, rounded once to it. */
+int mxfp4_dequantize(const uint8_t *codes, const uint8_t *scales, int32_t dtype, void *out, int64_t ldo, int64_t M,
+                     int64_t K, void *stream);
+
+/* out[m][n] = sum_k a[m][k] w[n][k] of packed a (M rows) and w (N rows) of K
+ * values, fp32 sums, rounded once to dtype (any); out element-aligned, any row
+ * stride >= N.  With offsets (else null and experts = 1): w holds experts
+ * matrices of N rows one after another, and row m meets its expert's.
+ * 0 <= M < 2^31, 1 <= N, K < 2^22, one weight's codes below 2 GiB.  NaN blocks
+ * make the rows or columns that they are in NaN. */
+int mxfp4_gemm(const uint8_t *a, const uint8_t *a_scales, const uint8_t *w, const uint8_t *w_scales,
+               const int32_t *offsets, int32_t experts, int32_t dtype, void *out, int64_t ldo, int64_t M, int64_t N,
+               int64_t K, void *stream);
+
+/* mxfp4_gemm of x [M][K] (SSG_DT_F16 or SSG_DT_BF16, element-aligned, row stride
+ * ldx) as mxfp4_quantize packs it, out in x's type.  ws: 16-byte aligned,
+ * mxfp4_linear_workspace_bytes(). */
+int mxfp4_linear(int32_t dtype, const void *x, int64_t ldx, const uint8_t *w, const uint8_t *w_scales,
+                 const int32_t *offsets, int32_t experts, void *out, int64_t ldo, int64_t M, int64_t N, int64_t K,
+                 void *ws, int64_t ws_bytes, void *stream);
+int64_t mxfp4_linear_workspace_bytes(int64_t M, int64_t K);
+
+/* norm[0] = sqrt of the sum of squares of n tensors' elements (fp64 sums), rounded to fp32.
+ * grads, sizes (elements, 0 allowed) and dtypes are host arrays of n entries,
+ * read during the call; tensors are contiguous and element-aligned.  ws:
+ * 16-byte aligned, grad_norm_workspace_bytes(n). */
+int grad_norm(int32_t n, const void *const *grads, const int64_t *sizes, const int32_t *dtypes, float *norm, void *ws,
+              int64_t ws_bytes, void *stream);
+
+/* outs[i] = grads[i] min(1, max_norm / (norm + 1e-6)), the factor rounded to fp32
+ * and the product once to the tensor's type; outs[i] is grads[i] (in place;
+ * not touched where the factor is 1) or a buffer that overlaps no tensor of the
+ * call (refused).  norm_in null: norm is grad_norm's and written to norm[0];
+ * else norm_in[0] (device, e.g. summed over ranks) is the norm, and norm and ws
+ * may be null.  An infinite norm makes the factor 0, a NaN one makes it NaN.
+ * The same element in two entries is refused when it would be scaled twice. */
+int clip_grad_norm(int32_t n, const void *const *grads, void *const *outs, const int64_t *sizes,
+                   const int32_t *dtypes, double max_norm, const float *norm_in, float *norm, void *ws,
+                   int64_t ws_bytes, void *stream);
+int64_t grad_norm_workspace_bytes(int32_t n);
+
 #ifdef __cplusplus
 }
 #endif

@@ -74,4 +74,15 @@ from ._tune import (  # noqa: F401
     low_rank_backward,
     w24_low_rank_gemm_f16,
 )
+from ._expert import (  # noqa: F401
+    clip_grad_norm,
+    grad_norm,
+    grouped_gemm,
+    grouped_gemm_backward,
+    mxfp4_dequantize,
+    mxfp4_gemm,
+    mxfp4_grouped_linear,
+    mxfp4_linear,
+    mxfp4_quantize,
+)
 from . import perf  # noqa: F401

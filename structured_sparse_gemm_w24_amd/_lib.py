@@ -85,6 +85,16 @@ SIGNATURES = {
     "linear_cross_entropy_backward": [_I32, _P, _P, _I64, _P, _I64, _P, _I64, _P, _P, _I64, _P, _I64, _I64, _I64,
                                       _I64, _P, _I64, _P],
     "linear_cross_entropy_workspace_bytes": [_I32, _I64, _I64, _I64, _I64, _I64, _I32],
+    "grouped_gemm": [_I32, _P, _I64, _P, _P, _I32, _P, _I64, _I64, _I64, _I64, _P],
+    "grouped_gemm_backward": [_I32, _P, _I64, _P, _I64, _P, _P, _I32, _P, _I64, _P, _I64, _I64, _I64, _P],
+    "mxfp4_quantize": [_I32, _P, _I64, _P, _P, _I64, _I64, _P],
+    "mxfp4_dequantize": [_P, _P, _I32, _P, _I64, _I64, _I64, _P],
+    "mxfp4_gemm": [_P, _P, _P, _P, _P, _I32, _I32, _P, _I64, _I64, _I64, _I64, _P],
+    "mxfp4_linear": [_I32, _P, _I64, _P, _P, _P, _I32, _P, _I64, _I64, _I64, _I64, _P, _I64, _P],
+    "mxfp4_linear_workspace_bytes": [_I64, _I64],
+    "grad_norm": [_I32, _P, _P, _P, _P, _P, _I64, _P],
+    "clip_grad_norm": [_I32, _P, _P, _P, _P, ct.c_double, _P, _P, _P, _I64, _P],
+    "grad_norm_workspace_bytes": [_I32],
 }
 
 

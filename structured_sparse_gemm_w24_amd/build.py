@@ -39,7 +39,8 @@ CXX_FLAGS = ["-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", "-Wall", "-Wex
 HOST_SOURCES = ["status.cpp", "pack.cpp"]
 HIP_SOURCES = ["api.hip", "kernels/gemm.hip", "kernels/splitk.hip", "kernels/tw_gemm.hip",
                "kernels/tw_gemm_i8.hip", "kernels/transpose.hip", "api_tune.hip", "kernels/layer_norm.hip",
-               "kernels/low_rank.hip", "kernels/low_rank_gemm.hip", "kernels/loss.hip"]
+               "kernels/low_rank.hip", "kernels/low_rank_gemm.hip", "kernels/loss.hip",
+               "api_expert.hip", "kernels/grouped.hip", "kernels/mxfp4.hip", "kernels/grad_norm.hip"]
 
 
 def _obj(src):

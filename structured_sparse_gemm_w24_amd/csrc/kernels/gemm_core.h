@@ -77,14 +77,25 @@
 
 namespace ssg {
 
-// (DENSE_BF16 is used by the linear cross entropy alone.)
-enum Kind { DENSE_F16 = 0, W24_F16 = 1, DENSE_I8 = 2, W24_I8 = 3, DENSE_BF16 = 4 };
+// (DENSE_BF16 is used by the linear cross entropy and the experts' products,
+// MX_F4 by the products of microscaled 4-bit operands.)
+enum Kind { DENSE_F16 = 0, W24_F16 = 1, DENSE_I8 = 2, W24_I8 = 3, DENSE_BF16 = 4, MX_F4 = 5 };
 // EPI_F16: fp16 kinds.  int8 kinds: EPI_I32 raw accumulators; the others
 // compute y = float(acc) * scale[n] (+ bias[n]), each step rounded to nearest
 // even, then store y as fp32, fp16 or saturated int8.  EPI_PART (split K, any
 // kind): the raw accumulators (fp32 or int32) of K-split blockIdx.y go to its
 // [M][N] slice of the workspace passed as C; a second kernel sums the slices.
-enum Epi { EPI_F16 = 0, EPI_I32 = 1, EPI_F32_SCALE = 2, EPI_F16_SCALE = 3, EPI_I8_SCALE = 4, EPI_PART = 5 };
+// EPI_BF16, EPI_F32: the accumulators rounded to bf16, or as they are.
+enum Epi {
+    EPI_F16 = 0,
+    EPI_I32 = 1,
+    EPI_F32_SCALE = 2,
+    EPI_F16_SCALE = 3,
+    EPI_I8_SCALE = 4,
+    EPI_PART = 5,
+    EPI_BF16 = 6,
+    EPI_F32 = 7
+};
 
 template <int KIND>
 struct KindTraits;
@@ -98,6 +109,9 @@ struct KindTraits<DENSE_F16> {
 };
 template <>
 struct KindTraits<DENSE_BF16> : KindTraits<DENSE_F16> {};
+// 4-bit values: a stage is 256 k; both operands bring 8 scale bytes a row (two words), one byte per 32 k.
+template <>
+struct KindTraits<MX_F4> : KindTraits<DENSE_F16> {};
 template <>
 struct KindTraits<W24_F16> {
     static constexpr bool kSparse = true, kI8 = false;
@@ -168,6 +182,24 @@ __device__ __forceinline__ void wait_lgkm_vm_barrier() {
 
 typedef uint32_t u32x8 __attribute__((ext_vector_type(8)));
 
+// Stores the first `room` elements of OB bytes (all 16 / OB, or fewer at a row's end; none
+// below 1) at any element alignment.
+template <int OB, bool NTS>
+__device__ __forceinline__ void store_piece(uint8_t *p, u32x4 v, int room) {
+    typedef u32x4 Any __attribute__((aligned(2)));
+    if (room >= 16 / OB) {
+        if constexpr (NTS) __builtin_nontemporal_store(v, reinterpret_cast<Any *>(p));
+        else *reinterpret_cast<Any *>(p) = v;
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < 16 / OB - 1; ++i) {
+        if (i >= room) break;
+        if constexpr (OB == 4) reinterpret_cast<uint32_t *>(p)[i] = v[i];
+        else reinterpret_cast<uint16_t *>(p)[i] = uint16_t(v[i / 2] >> (16 * (i % 2)));
+    }
+}
+
 // One matrix instruction.  w: the row operand (kept W^T values, or dense W^T
 // for the dense kinds); a: the column operand (activations).  For the sparse
 // kinds a holds 32 bytes; the dense kinds use its low 16 bytes.
@@ -192,6 +224,17 @@ __device__ __forceinline__ void mma(typename AccOf<KIND>::T &acc, u32x4 w, u32x8
         acc = __builtin_amdgcn_mfma_i32_32x32x32_i8(__builtin_bit_cast(intx4, w), __builtin_bit_cast(intx4, lo), acc,
                                                      0, 0, 0);
     }
+}
+
+// The microscaled 4-bit instruction: 32 x 32 x 64, lane (h, r) holds k = 32h .. 32h+31 of its
+// row r, i.e. one block, whose scale is byte OP of its scale word.
+template <int OP>
+__device__ __forceinline__ void mma_f4(floatx16 &acc, u32x4 w, u32x4 a, uint32_t sw, uint32_t sa) {
+    const intx4 wi = __builtin_bit_cast(intx4, w), ai = __builtin_bit_cast(intx4, a);
+    constexpr int kF4 = 4;  // operand format: E2M1
+    acc = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+        __builtin_shufflevector(wi, wi, 0, 1, 2, 3, 0, 1, 2, 3), __builtin_shufflevector(ai, ai, 0, 1, 2, 3, 0, 1, 2, 3),
+        acc, kF4, kF4, OP, int(sw), OP, int(sa));
 }
 
 // Epilogue store of one 16-byte piece; nontemporal stores stream past L2.
@@ -245,7 +288,10 @@ struct Layout {
     // overwrites a block that a stage still in the ring reads.
     static constexpr int MP = KT::kSparse ? CF::MP : 0;
     static constexpr int M_STAGE = MP ? 0 : M_BYTES;
-    static constexpr int STAGE = A_STAGE + W_STAGE + M_STAGE;
+    // MX_F4: the scales of a stage, 8 bytes a row, [BM] then [BN] rows behind the codes; in 256-byte
+    // chunks of 32 rows (waves past the last chunk load it once more, so that all issue alike)
+    static constexpr int S_CHUNKS = KIND == MX_F4 ? (BM + BN) * DK / 32 : 0;
+    static constexpr int STAGE = A_STAGE + W_STAGE + M_STAGE + S_CHUNKS * 256;
     static constexpr int RW = MP * MW;  // words per row in a block
     static constexpr int MBLK = MP * M_BYTES;
     static constexpr int MSLOTS = MP ? 2 + (CF::STAGES - 2 + MP - 1) / MP : 0;
@@ -263,7 +309,8 @@ struct Layout {
     static constexpr int LA = A_STAGE / 1024 / NL;
     static constexpr int LW = W_STAGE / 1024 / NL;
     static constexpr int LM = MCH >= NL ? MCH / NL : (MCH > 0 ? 1 : 0);
-    static constexpr int L = LA + LW + LM;
+    static constexpr int LS = (S_CHUNKS + NL - 1) / NL;
+    static constexpr int L = LA + LW + LM + LS;
     static_assert(LA * NL * 1024 == A_STAGE && LW * NL * 1024 == W_STAGE && MCH * 256 == M_BYTES &&
                       (MCH == 0 || MCH % NL == 0 || NL % MCH == 0),
                   "stage does not split evenly over the waves");
@@ -287,16 +334,25 @@ struct Layout {
 // Extra::kEpilogue -- epilogue() takes the place of the store to C; kTransA /
 // kTransW (dense 16-bit kinds) -- the operand lies the other way round, A as
 // [rows_a][lda] and W as [rows_w][ldw] with k along the rows (zeros past the
-// last one), and is read through transposing LDS reads.  Plain GEMMs have none
-// of them.
+// last one), and is read through transposing LDS reads.  Extra::kPlace --
+// place() finds the workgroup's tile (one of many products of one launch): it
+// moves the operands' pointers to the tile's rows and sets M, the tile's place
+// in N and the number of K stages, or returns false where there is no such
+// tile; A's rows are then lda elements apart, and K may end inside a stage
+// (chunks past it are read as zeros).  Plain GEMMs have none of them.
 struct NoExtra {
-    static constexpr bool kAfter = false, kEpilogue = false, kTransA = false, kTransW = false;
+    static constexpr bool kAfter = false, kEpilogue = false, kTransA = false, kTransW = false, kPlace = false;
 };
 
 template <class Extra>
 __device__ __forceinline__ int lda_of(const Extra &e) {
     if constexpr (Extra::kTransA) return e.lda;
     else return 0;
+}
+template <class Extra>
+__device__ __forceinline__ int64_t a_row_of(const Extra &e, int64_t row) {
+    if constexpr (Extra::kPlace) return e.a_row;
+    else return row;
 }
 template <class Extra>
 __device__ __forceinline__ int ldw_of(const Extra &e) {
@@ -343,8 +399,10 @@ gemm_kernel(const uint8_t *__restrict__ A, const uint8_t *__restrict__ Wv, const
     constexpr int BM = LY::BM, BN = LY::BN, WB = LY::WB, MW = LY::MW;
     constexpr int A_STAGE = LY::A_STAGE, W_STAGE = LY::W_STAGE, STAGE = LY::STAGE;
     constexpr int SA = KT::kI8 ? 1 : 2;  // bytes per element
+    constexpr bool F4 = KIND == MX_F4;
     // LDS-staged epilogue: each wave owns 32 token rows x TN*32 channels per pass
-    constexpr int OB = (EPI == EPI_F16 || EPI == EPI_F16_SCALE) ? 2 : (EPI == EPI_I8_SCALE ? 1 : 4);  // output bytes
+    constexpr int OB = (EPI == EPI_F16 || EPI == EPI_F16_SCALE || EPI == EPI_BF16) ? 2
+                                                                                   : (EPI == EPI_I8_SCALE ? 1 : 4);  // output bytes
     constexpr int EROW = TN * 32 * OB + 16;       // padded LDS row (odd multiple of 16 B)
     constexpr int EWAVE = 32 * EROW;
     constexpr int EPASS = (TM * EWAVE * LY::NW <= CF::STAGES * STAGE) ? TM : 1;
@@ -366,18 +424,27 @@ gemm_kernel(const uint8_t *__restrict__ A, const uint8_t *__restrict__ Wv, const
     const int h = lane >> 5, r = lane & 31;
 
     // ---- tile assignment: XCD-contiguous ranges, GM tile-rows per group
-    const int tiles_m = (M + BM - 1) / BM, tiles_n = (N + BN - 1) / BN;
-    const int b = xcd_remap(blockIdx.x, tiles_m * tiles_n);
-    const int group = b / (GM * tiles_n);
-    const int first_m = group * GM;
-    const int gm = min(tiles_m - first_m, GM);
-    const int in_group = b % (GM * tiles_n);
-    const int tile_m = first_m + in_group % gm;
-    const int tile_n = in_group / gm;
-    const int m0 = tile_m * BM, n0 = tile_n * BN;
+    int b = 0, tile_m = 0, tile_n = 0, m0 = 0, n0 = 0;
+    if constexpr (Extra::kPlace) {
+        const uint8_t *a = A, *w = Wv;
+        void *c = C;
+        if (!extra.template place<CF, BM, BN>(a, w, c, M, N, K, stages, n0)) return;
+        A = a, Wv = w, C = c;
+    } else {
+        const int tiles_m = (M + BM - 1) / BM, tiles_n = (N + BN - 1) / BN;
+        b = xcd_remap(blockIdx.x, tiles_m * tiles_n);
+        const int group = b / (GM * tiles_n);
+        const int first_m = group * GM;
+        const int gm = min(tiles_m - first_m, GM);
+        const int in_group = b % (GM * tiles_n);
+        tile_m = first_m + in_group % gm;
+        tile_n = in_group / gm;
+        m0 = tile_m * BM, n0 = tile_n * BN;
+    }
 
-    const int64_t a_row = int64_t(K) * SA;                  // bytes per A row
-    const int64_t w_row = KT::kSparse ? a_row / 2 : a_row;  // bytes per W row
+    const int64_t k_row = F4 ? int64_t(K) / 2 : int64_t(K) * SA;  // bytes of K values
+    const int64_t a_row = a_row_of(extra, k_row);                 // bytes between A rows
+    const int64_t w_row = KT::kSparse ? k_row / 2 : k_row;        // bytes per W row
     const int64_t m_row = K / 32;                            // meta words per row
     // S = K stages of this workgroup (128 bytes of an A row each): all of them,
     // or, with K split over gridDim.y, split blockIdx.y's equal share.  The
@@ -438,7 +505,9 @@ gemm_kernel(const uint8_t *__restrict__ A, const uint8_t *__restrict__ Wv, const
     // (the host caps A and W below 4 GiB, so every byte count fits 32 bits)
     // (transposed operands end with their last row: a partial last stage reads zeros past it)
     const __amdgpu_buffer_rsrc_t bufA =
-        buffer_of(A, Extra::kTransA ? bytes_a_of(extra) : uint32_t(int64_t(M) * a_row));
+        buffer_of(A, Extra::kTransA  ? bytes_a_of(extra)
+                     : Extra::kPlace ? uint32_t(int64_t(min(M, BM) - 1) * a_row + k_row)
+                                     : uint32_t(int64_t(M) * a_row));
     const __amdgpu_buffer_rsrc_t bufW =
         buffer_of(Wv, Extra::kTransW ? bytes_w_of(extra) : uint32_t(int64_t(N) * w_row));
     const __amdgpu_buffer_rsrc_t bufM = buffer_of(meta_b, KT::kSparse ? uint32_t(int64_t(N) * m_row * 4) : 0u);
@@ -467,10 +536,73 @@ gemm_kernel(const uint8_t *__restrict__ A, const uint8_t *__restrict__ Wv, const
         }
     };
     const bool issuer = LY::NL == LY::NW || wave < LY::NL;  // (with PROD: the loaders)
+    // The last stage of a K that ends inside it (place() launches, whose buffers, a tile's rows of
+    // A and one weight, end below 2 GiB):
+    // chunks past the end are read past the buffer, i.e. as zeros.
+    [[maybe_unused]] auto issue_end = [&](uint8_t *base, int sg) {
+        constexpr uint32_t kNone = 0x80000000u;
+        const int room = int(k_row) - sg * LY::AB;
+#pragma unroll
+        for (int j = 0; j < LY::LA; ++j) {
+            const int byte = (j * LY::NL + wave) * 1024 + lane * 16;
+            const int row = byte / LY::AB, pos = (byte / 16) % (LY::AB / 16);
+            const bool in = swzw<LY::AB>(row, pos) * 16 < room;
+            dma16(bufA, in ? oa[j] + uint32_t(sg * LY::AB) : kNone, base + (j * LY::NL + wave) * 1024);
+        }
+#pragma unroll
+        for (int j = 0; j < LY::LW; ++j) {
+            if constexpr (Extra::kTransW) {
+                dma16(bufW, ow[j] + uint32_t(sg) * uint32_t(ldw_of(extra) * 128), base + A_STAGE + (j * LY::NL + wave) * 1024);
+            } else {
+                const int byte = (j * LY::NL + wave) * 1024 + lane * 16;
+                const int row = byte / WB, pos = (byte / 16) % (WB / 16);
+                const bool in = swzw<WB>(row, pos) * 16 < room;
+                dma16(bufW, in ? ow[j] + uint32_t(sg * WB) : kNone, base + A_STAGE + (j * LY::NL + wave) * 1024);
+            }
+        }
+    };
+    // MX_F4: the scales of a stage, words past the end of K as zeros.
+    [[maybe_unused]] auto issue_scales = [&](uint8_t *base, int sg) {
+        if constexpr (F4) {
+            constexpr int WPR = 2 * LY::DK;  // words a row
+            const int s_row = K / 32;
+            const __amdgpu_buffer_rsrc_t bufSA = buffer_of(extra.sa, uint32_t(min(M, BM) * s_row));
+            const __amdgpu_buffer_rsrc_t bufSW = buffer_of(extra.sw, uint32_t(N * s_row));
+#pragma unroll
+            for (int j = 0; j < LY::LS; ++j) {
+                const int c = min(j * LY::NL + wave, LY::S_CHUNKS - 1);
+                const int word = c * 64 + lane, row = word / WPR;
+                const int at = (sg * WPR + word % WPR) * 4;
+                const bool of_a = c < BM * LY::DK / 32;  // (a chunk is all A's or all W's)
+                const uint32_t line = uint32_t(of_a ? min(m0 + row, M - 1) : min(n0 + row - BM, N - 1));
+                const uint32_t off = at < s_row ? line * uint32_t(s_row) + uint32_t(at) : 0x80000000u;
+                if (of_a) dma4(bufSA, off, base + A_STAGE + W_STAGE + c * 256);
+                else dma4(bufSW, off, base + A_STAGE + W_STAGE + c * 256);
+            }
+        }
+    };
     auto issue = [&](int s) {
         if (!issuer) return;
         uint8_t *base = smem + (s % NB) * STAGE;
         const int sg = ks0 + ((s + rot < S) ? s + rot : s + rot - S);  // global K stage
+        if constexpr (F4) issue_scales(base, sg);
+        if constexpr (Extra::kPlace && !Extra::kTransA) {
+            if ((sg + 1) * LY::AB > int(k_row)) {
+                issue_end(base, sg);
+                return;
+            }
+        }
+        if constexpr (Extra::kPlace && Extra::kTransA) {
+            // rows of a group may reach past 32-bit offsets: each stage has a buffer of its own
+            const int64_t sa = int64_t(sg) * extra.lda * 128, sw = int64_t(sg) * extra.ldw * 128;
+            const __amdgpu_buffer_rsrc_t a = buffer_of(A + sa, uint32_t(min(extra.bytes_a - sa, int64_t(0x7fffffff))));
+            const __amdgpu_buffer_rsrc_t w = buffer_of(Wv + sw, uint32_t(min(extra.bytes_w - sw, int64_t(0x7fffffff))));
+#pragma unroll
+            for (int j = 0; j < LY::LA; ++j) dma16(a, oa[j], base + (j * LY::NL + wave) * 1024);
+#pragma unroll
+            for (int j = 0; j < LY::LW; ++j) dma16(w, ow[j], base + A_STAGE + (j * LY::NL + wave) * 1024);
+            return;
+        }
 #pragma unroll
         for (int j = 0; j < LY::LA; ++j)
             dma16(bufA, oa[j] + (Extra::kTransA ? uint32_t(sg) * uint32_t(lda_of(extra) * 128) : uint32_t(sg * LY::AB)), base + (j * LY::NL + wave) * 1024);
@@ -492,6 +624,7 @@ gemm_kernel(const uint8_t *__restrict__ A, const uint8_t *__restrict__ Wv, const
         u32x4 w[TN];
         uint32_t idx[TN];
         u32x8 a[TM];
+        uint32_t sw[F4 ? TN : 1], sa[F4 ? TM : 1];  // MX_F4: this lane's block's scale in byte 2 (k-step % 2)
     };
     // byte of a [k][column] stage that this lane points at for k-step kk, block column `row`
     [[maybe_unused]] auto tr_at = [&](int row, int kk, int columns) {
@@ -535,17 +668,39 @@ gemm_kernel(const uint8_t *__restrict__ A, const uint8_t *__restrict__ Wv, const
         }
     };
 
+    // MX_F4: one word of scales serves two k-steps.
+    [[maybe_unused]] auto load_scales = [&](int s, int kk, Frag &F, const Frag &before) {
+        if constexpr (F4) {
+            constexpr int WPR = 2 * LY::DK;
+            const uint32_t *b = reinterpret_cast<const uint32_t *>(smem + (s % NB) * STAGE + A_STAGE + W_STAGE) + kk / 2;
+#pragma unroll
+            for (int tn = 0; tn < TN; ++tn)
+                F.sw[tn] = kk % 2 ? before.sw[tn] : b[(BM + wn * TN * 32 + tn * 32 + r) * WPR] >> (8 * h);
+#pragma unroll
+            for (int tm = 0; tm < TM; ++tm)
+                F.sa[tm] = kk % 2 ? before.sa[tm] : b[(wm * TM * 32 + tm * 32 + r) * WPR] >> (8 * h);
+        }
+    };
+
     Acc acc[TN][TM];
 #pragma unroll
     for (int i = 0; i < TN; ++i)
 #pragma unroll
         for (int j = 0; j < TM; ++j) acc[i][j] = Acc{};
 
-    auto mma_frag = [&](const Frag &F) {
+    auto mma_frag = [&](const Frag &F, [[maybe_unused]] int kk) {
 #pragma unroll
         for (int tn = 0; tn < TN; ++tn)
 #pragma unroll
-            for (int tm = 0; tm < TM; ++tm) mma<KIND>(acc[tn][tm], F.w[tn], F.a[tm], F.idx[tn]);
+            for (int tm = 0; tm < TM; ++tm) {
+                if constexpr (F4) {
+                    const u32x4 a = __builtin_shufflevector(F.a[tm], F.a[tm], 0, 1, 2, 3);
+                    if (kk % 2) mma_f4<2>(acc[tn][tm], F.w[tn], a, F.sw[tn], F.sa[tm]);
+                    else mma_f4<0>(acc[tn][tm], F.w[tn], a, F.sw[tn], F.sa[tm]);
+                } else {
+                    mma<KIND>(acc[tn][tm], F.w[tn], F.a[tm], F.idx[tn]);
+                }
+            }
     };
     // Interleave hint: one matrix instruction, then its share of LDS reads.
     constexpr int NMMA = TN * TM;
@@ -593,6 +748,7 @@ gemm_kernel(const uint8_t *__restrict__ A, const uint8_t *__restrict__ Wv, const
     } else {
         Frag F[2];
         load_frag(0, 0, F[0]);
+        if constexpr (F4) load_scales(0, 0, F[0], F[0]);
 
         // One stage; STEADY: the ring still has a stage to fetch (s + NB < S).
         // The next stage's first fragments are read unconditionally: on the last
@@ -604,6 +760,7 @@ gemm_kernel(const uint8_t *__restrict__ A, const uint8_t *__restrict__ Wv, const
                 Frag &nxt = F[(kk + 1) & 1];
                 if (kk + 1 < LY::NI) {
                     load_frag(s, kk + 1, nxt);
+                    if constexpr (F4) load_scales(s, kk + 1, nxt, cur);
                 } else {
                     // stage s is fully in registers; stage s+1 must be complete
                     if constexpr (decltype(steady)::value) {
@@ -613,8 +770,9 @@ gemm_kernel(const uint8_t *__restrict__ A, const uint8_t *__restrict__ Wv, const
                         wait_lgkm_vm_barrier<0>();
                     }
                     load_frag(s + 1, 0, nxt);
+                    if constexpr (F4) load_scales(s + 1, 0, nxt, cur);
                 }
-                mma_frag(cur);
+                mma_frag(cur, kk);
                 interleave();
             }
         };
@@ -639,7 +797,12 @@ gemm_kernel(const uint8_t *__restrict__ A, const uint8_t *__restrict__ Wv, const
         if constexpr (EPI == EPI_F16) {
             o.x = pack_half2_rne(v[4 * q + 0], v[4 * q + 1]);
             o.y = pack_half2_rne(v[4 * q + 2], v[4 * q + 3]);
-        } else if constexpr (EPI == EPI_PART) {
+        } else if constexpr (EPI == EPI_BF16) {
+            typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+            const bf16x4 t = {__bf16(v[4 * q + 0]), __bf16(v[4 * q + 1]), __bf16(v[4 * q + 2]), __bf16(v[4 * q + 3])};
+            const u32x2 u = __builtin_bit_cast(u32x2, t);
+            o.x = u.x, o.y = u.y;
+        } else if constexpr (EPI == EPI_PART || EPI == EPI_F32) {
             // (whole 4-vectors are bit-cast: a bit-cast of a single element of
             // the 16-wide accumulator vector yielded element 0 for every lane)
             using E4 = typename std::conditional<KT::kI8, intx4, floatx4>::type;
@@ -727,7 +890,11 @@ gemm_kernel(const uint8_t *__restrict__ A, const uint8_t *__restrict__ Wv, const
                     const int m = m0 + row_of_wave + (tp + e) * 32 + row;
                     const int n = nw + ch * (16 / OB);
                     const u32x4 v = *reinterpret_cast<const u32x4 *>(ew + e * EWAVE + row * EROW + ch * 16);
-                    if (m < M && n < N) store16<CF::NTS>(Cb + (int64_t(m) * N + n) * OB, v);
+                    if constexpr (Extra::kPlace) {
+                        store_piece<OB, CF::NTS>(Cb + (int64_t(m) * extra.ldc + n) * OB, v, m < M ? N - n : 0);
+                    } else {
+                        if (m < M && n < N) store16<CF::NTS>(Cb + (int64_t(m) * N + n) * OB, v);
+                    }
                 }
             }
         }

@@ -1,0 +1,267 @@
+// Global norm of many tensors and their scaling to a largest norm.
+//
+//   norm = sqrt(sum over all tensors of x^2),   out = x min(1, max_norm / (norm + 1e-6))
+//
+// Bound by memory: every element is read for the norm, read again and written for the
+// scaling.  The tensors' addresses travel in the kernel arguments (a launch takes as
+// many as fit in 4 KiB), so a call copies nothing to the device and captures into a
+// graph.  A launch's tensors are cut into pieces of 16 KiB; each workgroup of a fixed grid
+// takes a run of consecutive pieces, so each writes one partial sum and the sums are added
+// in a fixed order.  Squares and sums are fp64: an fp32 gradient of 1e30 does not overflow,
+// and the order of summation shows in no digit of an fp32 norm.
+#include "elem.h"
+#include "launch.h"
+
+namespace ssg {
+
+namespace {
+
+constexpr int kGrid = 1024;    // workgroups of a launch, at most
+constexpr int kPiece = 16384;  // bytes
+constexpr int kThreads = 256;
+constexpr int kNormTensors = 190, kClipTensors = 136;
+constexpr double kEps = 1e-6;
+
+// size: elements, with the type in the bits above 2^56.
+struct NormTable {
+    const void *grad[kNormTensors];
+    int64_t size[kNormTensors];
+    uint32_t first[kNormTensors + 1];  // first piece of each tensor; at n: all pieces
+    int n;
+};
+struct ClipTable {
+    const void *grad[kClipTensors];
+    void *out[kClipTensors];
+    int64_t size[kClipTensors];
+    uint32_t first[kClipTensors + 1];
+    int n;
+};
+static_assert(sizeof(NormTable) <= 4000 && sizeof(ClipTable) <= 4000, "tables must fit in the kernel arguments");
+
+// The tensor that piece p belongs to.
+template <class Table>
+__device__ __forceinline__ int tensor_of(const Table &t, uint32_t p) {
+    int lo = 0, hi = t.n - 1;
+    while (lo < hi) {  // the last tensor that starts at or before p (empty ones start where the next one does)
+        const int mid = (lo + hi + 1) / 2;
+        if (t.first[mid] <= p) lo = mid;
+        else hi = mid - 1;
+    }
+    return lo;
+}
+
+__device__ __forceinline__ uint32_t run_start(uint32_t pieces, uint32_t b) {
+    return uint32_t(uint64_t(pieces) * b / gridDim.x);
+}
+
+template <class T>
+__device__ __forceinline__ void add_squares(double &sum, typename Elem<T>::Vec v) {
+#pragma unroll
+    for (int i = 0; i < Elem<T>::V; ++i) {
+        const double d = double(float(v[i]));
+        sum = __builtin_fma(d, d, sum);
+    }
+}
+
+// A piece: four 16-byte accesses a thread, kThreads apart.
+template <class T>
+__device__ __forceinline__ void piece_squares(double &sum, const void *p, int64_t at, int64_t n) {
+    constexpr int V = Elem<T>::V, STEP = kThreads * V;
+    const T *x = static_cast<const T *>(p) + at;
+    const int64_t room = n - at;
+    const int c = int(threadIdx.x) * V;
+    typename Elem<T>::Vec v[4];
+    if (room >= 4 * STEP) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = fetch_raw<T, false>(x, c + i * STEP, 4 * STEP);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = load_raw(x, c + i * STEP, room);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) add_squares<T>(sum, v[i]);
+}
+
+template <class T>
+__device__ __forceinline__ void piece_scale(float by, const void *p, void *q, int64_t at, int64_t n) {
+    constexpr int V = Elem<T>::V, STEP = kThreads * V;
+    const T *x = static_cast<const T *>(p) + at;
+    T *y = static_cast<T *>(q) + at;
+    const int64_t room = n - at;
+    const int c = int(threadIdx.x) * V;
+    typename Elem<T>::Vec v[4];
+    if (room >= 4 * STEP) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = fetch_raw<T, false>(x, c + i * STEP, 4 * STEP);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            float f[V];
+            to_float<T>(v[i], f);
+#pragma unroll
+            for (int j = 0; j < V; ++j) f[j] *= by;
+            store_stream<T, false>(y, c + i * STEP, 4 * STEP, f);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = load_raw(x, c + i * STEP, room);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            float f[V];
+            to_float<T>(v[i], f);
+#pragma unroll
+            for (int j = 0; j < V; ++j) f[j] *= by;
+            store_stream<T, true>(y, c + i * STEP, room, f);
+        }
+    }
+}
+
+// Sum over the workgroup; every thread gets it.
+template <int T>
+__device__ __forceinline__ double group_sum(double v, double *red) {
+#pragma unroll
+    for (int d = 32; d > 0; d >>= 1) v += __shfl_xor(v, d, 64);
+    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
+    __syncthreads();
+    v = 0.0;
+#pragma unroll
+    for (int i = 0; i < T / 64; ++i) v += red[i];
+    return v;
+}
+
+__global__ void __launch_bounds__(kThreads)
+norm_squares_kernel(NormTable t, double *__restrict__ part) {
+    __shared__ double red[kThreads / 64];
+    const uint32_t pieces = t.first[t.n];
+    const uint32_t from = run_start(pieces, blockIdx.x), to = run_start(pieces, blockIdx.x + 1);
+    double sum = 0.0;
+    int at = tensor_of(t, from);
+    for (uint32_t p = from; p < to; ++p) {
+        while (t.first[at + 1] <= p) ++at;
+        const int64_t n = t.size[at] & ((int64_t(1) << 56) - 1);
+        const int type = int(t.size[at] >> 56);
+        const int64_t q = p - t.first[at];
+        if (type == DT_F16) piece_squares<_Float16>(sum, t.grad[at], q * (kPiece / 2), n);
+        else if (type == DT_BF16) piece_squares<__bf16>(sum, t.grad[at], q * (kPiece / 2), n);
+        else piece_squares<float>(sum, t.grad[at], q * (kPiece / 4), n);
+    }
+    sum = group_sum<kThreads>(sum, red);
+    if (threadIdx.x == 0) part[blockIdx.x] = sum;
+}
+
+template <int T>
+__device__ __forceinline__ double norm_of(const double *part, int slots, double *red) {
+    double sum = 0.0;
+#pragma unroll 4
+    for (int i = threadIdx.x; i < slots; i += T) sum += part[i];
+    return sqrt(group_sum<T>(sum, red));
+}
+
+__global__ void __launch_bounds__(1024)
+norm_finish_kernel(const double *__restrict__ part, int slots, float *__restrict__ norm) {
+    __shared__ double red[16];
+    const double n = norm_of<1024>(part, slots, red);
+    if (threadIdx.x == 0) norm[0] = float(n);
+}
+
+// Every workgroup adds the partial sums for itself (at most 8 KiB a launch of the first kernel,
+// from L2), which takes less than a launch between.  The pieces go backwards: the last ones
+// read for the norm are the likeliest to be cached.
+__global__ void __launch_bounds__(kThreads)
+clip_kernel(ClipTable t, double max_norm, const float *__restrict__ norm_in, const double *__restrict__ part, int slots,
+            float *__restrict__ norm) {
+    __shared__ double red[kThreads / 64];
+    const double n = norm_in ? double(norm_in[0]) : norm_of<kThreads>(part, slots, red);
+    if (norm && blockIdx.x == 0 && threadIdx.x == 0) norm[0] = float(n);
+    const double c = max_norm / (n + kEps);
+    const float by = c > 1.0 ? 1.0f : float(c);  // (a NaN stays one)
+    const uint32_t pieces = t.first[t.n], b = gridDim.x - 1 - blockIdx.x;
+    const uint32_t from = run_start(pieces, b), to = run_start(pieces, b + 1);
+    if (from >= to) return;
+    int at = tensor_of(t, to - 1);
+    for (uint32_t p = to; p-- > from;) {
+        while (t.first[at] > p) --at;
+        if (by == 1.0f && t.grad[at] == t.out[at]) continue;
+        const int64_t size = t.size[at] & ((int64_t(1) << 56) - 1);
+        const int type = int(t.size[at] >> 56);
+        const int64_t q = p - t.first[at];
+        if (type == DT_F16) piece_scale<_Float16>(by, t.grad[at], t.out[at], q * (kPiece / 2), size);
+        else if (type == DT_BF16) piece_scale<__bf16>(by, t.grad[at], t.out[at], q * (kPiece / 2), size);
+        else piece_scale<float>(by, t.grad[at], t.out[at], q * (kPiece / 4), size);
+    }
+}
+
+// Entries of l from i on, at most Most of them; returns how many entries were looked at.
+template <int Most, class Table, class F>
+int fill(const GradList &l, int i, Table &t, F more) {
+    t.n = 0;
+    uint64_t pieces = 0;
+    int at = i;
+    for (; at < l.n && t.n < Most; ++at) {
+        if (l.sizes[at] == 0) continue;
+        const int64_t bytes = l.sizes[at] * (l.dtypes[at] == DT_F32 ? 4 : 2);
+        const uint64_t here = uint64_t((bytes + kPiece - 1) / kPiece);
+        if (pieces + here >= (uint64_t(1) << 32)) break;
+        t.grad[t.n] = l.grads[at];
+        t.size[t.n] = l.sizes[at] | int64_t(l.dtypes[at]) << 56;
+        t.first[t.n] = uint32_t(pieces);
+        more(t, at);
+        pieces += here;
+        ++t.n;
+    }
+    t.first[t.n] = uint32_t(pieces);
+    return at - i;
+}
+
+hipError_t squares(const GradList &l, double *ws, int &slots, hipStream_t st) {
+    slots = 0;
+    for (int i = 0; i < l.n;) {
+        NormTable t;
+        i += fill<kNormTensors>(l, i, t, [](NormTable &, int) {});
+        if (t.n == 0) continue;
+        const uint32_t pieces = t.first[t.n];
+        const int grid = pieces < uint32_t(kGrid) ? int(pieces) : kGrid;
+        hipLaunchKernelGGL(norm_squares_kernel, dim3(grid), dim3(kThreads), 0, st, t, ws + slots);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+        slots += grid;
+    }
+    return hipSuccess;
+}
+
+hipError_t finish(const double *ws, int slots, float *norm, hipStream_t st) {
+    hipLaunchKernelGGL(norm_finish_kernel, dim3(1), dim3(1024), 0, st, ws, slots, norm);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+// (every launch but the last takes kNormTensors tensors that are not empty)
+int64_t grad_norm_slots(int n) { return (int64_t(n) + kNormTensors - 1) / kNormTensors * kGrid; }
+
+hipError_t launch_grad_norm(const GradList &l, double *ws, float *norm, hipStream_t st) {
+    int slots;
+    const hipError_t e = squares(l, ws, slots, st);
+    return e != hipSuccess ? e : finish(ws, slots, norm, st);
+}
+
+hipError_t launch_clip_grad_norm(const GradList &l, double max_norm, const float *norm_in, double *ws, float *norm,
+                                 hipStream_t st) {
+    int slots = 0;
+    hipError_t e = norm_in ? hipSuccess : squares(l, ws, slots, st);
+    if (e != hipSuccess) return e;
+    bool told = norm_in != nullptr;  // the first scaling launch writes the norm
+    for (int i = 0; i < l.n;) {
+        ClipTable t;
+        i += fill<kClipTensors>(l, i, t, [&](ClipTable &u, int at) { u.out[u.n] = l.outs[at]; });
+        if (t.n == 0) continue;
+        const uint32_t pieces = t.first[t.n];
+        const int grid = pieces < uint32_t(2 * kGrid) ? int(pieces) : 2 * kGrid;
+        hipLaunchKernelGGL(clip_kernel, dim3(grid), dim3(kThreads), 0, st, t, max_norm, norm_in, ws, slots,
+                           told ? nullptr : norm);
+        if ((e = hipGetLastError()) != hipSuccess) return e;
+        told = true;
+    }
+    return told ? hipSuccess : finish(ws, slots, norm, st);
+}
+
+}  // namespace ssg

@@ -163,6 +163,56 @@ LossPlan loss_plan(int64_t M, int64_t V, int64_t D, bool pack_x, bool pack_w, bo
 hipError_t launch_loss_fwd(const Loss &a, const LossPlan &pl, hipStream_t st);
 hipError_t launch_loss_bwd(const Loss &a, const LossPlan &pl, hipStream_t st);
 
+// Products grouped by expert (formulas in grouped.hip).  w [experts][N][K],
+// offsets [experts + 1] on the device.
+struct Grouped {
+    int dtype;  // DT_F16 or DT_BF16
+    const void *x, *w, *dy;
+    const int32_t *offsets;
+    int experts;
+    int64_t ldx, lddy, ldo, lddx;
+    void *out, *dx, *dw;  // backward: dx or dw may be null
+    int64_t M, N, K;
+};
+hipError_t launch_grouped_fwd(const Grouped &a, hipStream_t st);
+hipError_t launch_grouped_bwd(const Grouped &a, hipStream_t st);
+// workgroups of the finest launch of these sizes
+int64_t grouped_blocks(int64_t M, int64_t experts, int64_t N, int64_t K);
+
+// Microscaled 4-bit floating point (formulas in mxfp4.hip).  Packed rows hold kp
+// values, a multiple of 128: kp / 2 code bytes and kp / 32 scale bytes.
+hipError_t launch_mxfp4_quantize(int dtype, const void *x, int64_t ldx, uint8_t *codes, uint8_t *scales, int64_t M,
+                                 int64_t K, hipStream_t st);
+hipError_t launch_mxfp4_dequantize(int dtype, const uint8_t *codes, const uint8_t *scales, void *out, int64_t ldo,
+                                   int64_t M, int64_t K, hipStream_t st);
+struct Mxfp4Gemm {
+    const uint8_t *a, *a_scales, *w, *w_scales;
+    const int32_t *offsets;  // null: one product of all rows
+    int experts;
+    int dtype;  // of out
+    void *out;
+    int64_t ldo, M, N, K;
+};
+hipError_t launch_mxfp4_gemm(const Mxfp4Gemm &g, hipStream_t st);
+// workgroups of the finest launch of these sizes (experts 0: one product)
+int64_t mxfp4_blocks(int64_t M, int64_t experts, int64_t N);
+inline int64_t mxfp4_padded(int64_t K) { return (K + 127) / 128 * 128; }
+
+// Sum of squares over many tensors and their scaling (grad_norm.hip).  ws: fp64
+// partial sums, grad_norm_slots(n) of them.
+struct GradList {
+    int n;
+    const void *const *grads;
+    void *const *outs;  // null: the norm alone
+    const int64_t *sizes;
+    const int32_t *dtypes;
+};
+int64_t grad_norm_slots(int n);
+hipError_t launch_grad_norm(const GradList &l, double *ws, float *norm, hipStream_t st);
+// norm_in: the norm to clip by; null: it is computed, and written to norm
+hipError_t launch_clip_grad_norm(const GradList &l, double max_norm, const float *norm_in, double *ws, float *norm,
+                                 hipStream_t st);
+
 // K stages (one per 128 bytes of an A row) for a kind and K.
 inline int gemm_k_stages(int kind, int K) { return (kind == 2 || kind == 3) ? K / 128 : K / 64; }
 

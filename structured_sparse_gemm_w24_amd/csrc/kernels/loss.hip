@@ -63,7 +63,7 @@ __device__ __forceinline__ void merge(float &m, float &s, float m2, float s2) {
 
 // ---- forward epilogue: a tile's statistics and the targets' logits.
 struct LossStats {
-    static constexpr bool kAfter = false, kEpilogue = true, kTransA = false, kTransW = false;
+    static constexpr bool kAfter = false, kEpilogue = true, kTransA = false, kTransW = false, kPlace = false;
     const int64_t *target;
     float *part;   // [tiles][M][2]
     float *logit;  // [M]
@@ -157,7 +157,7 @@ loss_rows_kernel(const float *__restrict__ part, const float *__restrict__ logit
 // ---- backward epilogue: logits to G [M][ldg], zeros past the last channel.
 template <class T>
 struct LossGrad {
-    static constexpr bool kAfter = false, kEpilogue = true, kTransA = false, kTransW = false;
+    static constexpr bool kAfter = false, kEpilogue = true, kTransA = false, kTransW = false, kPlace = false;
     const int64_t *target;
     int64_t ignore, V, v0;
     const float *dloss, *lse, *scale;  // scale[0] = largest finite |dloss|
@@ -234,7 +234,7 @@ struct LossGrad {
 // w (and, TA, the first operand too) has k along its rows.
 template <class T, bool TA>
 struct LossOut {
-    static constexpr bool kAfter = false, kEpilogue = true, kTransA = TA, kTransW = true;
+    static constexpr bool kAfter = false, kEpilogue = true, kTransA = TA, kTransW = true, kPlace = false;
     int lda, rows_a;  // (TA)
     int ldw, rows_w;
     const float *scale;  // [1]: largest finite |dloss| / kGradScale

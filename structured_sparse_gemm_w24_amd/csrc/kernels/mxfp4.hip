@@ -1,0 +1,234 @@
+// Microscaled 4-bit floating point (E2M1 values, blocks of 32 along K that share a
+// power-of-two scale; the MXFP4 format of the OCP Microscaling specification, v1.0):
+// quantisation, its inverse, and products of packed operands.
+//
+//   scale byte = max(0, floor(log2 max|x|) - 2 + 127), the block's scale 2^(byte - 127);
+//   code = nearest of 0, .5, 1, 1.5, 2, 3, 4, 6 to |x| / scale, ties to the even code,
+//          past 6: 6; bit 3 is the sign.  A block with an infinity or NaN has byte 255 and
+//          stands for NaN.
+//   C[m][n] = sum_k a[m][k] w[n][k], fp32 sums, rounded once.
+//
+// A lane of the scaled matrix instruction (32 x 32 x 64) holds 32 consecutive k of one
+// row, which is one block: its 16 code bytes as they lie in memory, and one scale byte.
+// So packed rows go to LDS as the other kinds' rows do, and the scales, 8 bytes a row and
+// stage, beside them.
+#include "elem.h"
+#include "gemm_core.h"
+#include "gemm_tiles.h"
+#include "group_place.h"
+#include "launch.h"
+
+namespace ssg {
+
+namespace {
+
+__device__ __forceinline__ uint32_t magnitude_bits(float f) { return __builtin_bit_cast(uint32_t, f) & 0x7fffffffu; }
+
+template <int CTRL>
+__device__ __forceinline__ uint32_t dpp(uint32_t v) {
+    return uint32_t(__builtin_amdgcn_update_dpp(int(v), int(v), CTRL, 0xf, 0xf, false));
+}
+
+// Scale byte of the block whose largest magnitude has these bits.
+__device__ __forceinline__ uint32_t scale_byte(uint32_t top) {
+    const uint32_t e = top >> 23;
+    return e == 255 ? 255u : e > 2 ? e - 2 : 0u;
+}
+
+// Eight values to eight codes.  x / scale is exact (a power of two, and what becomes
+// subnormal rounds to code 0 either way); a block that is not finite keeps codes 0.
+__device__ __forceinline__ uint32_t codes_of(const float (&f)[8], uint32_t byte) {
+    if (byte == 255) return 0;
+    const float by = __builtin_bit_cast(float, (254u - byte) << 23);
+    uint32_t c = 0;
+    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, f[0] * by, f[1] * by, 1.0f, 0);
+    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, f[2] * by, f[3] * by, 1.0f, 1);
+    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, f[4] * by, f[5] * by, 1.0f, 2);
+    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, f[6] * by, f[7] * by, 1.0f, 3);
+    return c;
+}
+
+// Eight values from column c on, zeros past the row's end.
+template <class T, bool TAIL>
+__device__ __forceinline__ void load8(const T *row, int64_t c, int64_t n, float (&f)[8]) {
+    constexpr int V = Elem<T>::V;
+#pragma unroll
+    for (int i = 0; i < 8; i += V) {
+        const typename Elem<T>::Vec v = settle<T, TAIL>(fetch_raw<T, TAIL>(row, c + i, n), c + i, n);
+#pragma unroll
+        for (int j = 0; j < V; ++j) f[i + j] = float(v[j]);
+    }
+}
+
+// Eight values a thread, so four threads a block and sixteen a word of four scales.
+template <class T, bool TAIL>
+__global__ void __launch_bounds__(256)
+mx_quantize_kernel(const T *__restrict__ x, int64_t ldx, uint32_t *__restrict__ codes, uint32_t *__restrict__ scales,
+                   int64_t M, int64_t K, int pieces) {  // pieces of a row: a multiple of 16
+    const int64_t all = M * pieces;
+    for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < all; i += int64_t(gridDim.x) * 256) {
+        const int64_t m = i / pieces, c = i % pieces * 8;
+        float f[8];
+        load8<T, TAIL>(x + m * ldx, c, K, f);
+        uint32_t top = 0;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) top = max(top, magnitude_bits(f[j]));
+        top = max(top, dpp<0xb1>(top));  // (quad permutations: lanes ^ 1, ^ 2)
+        top = max(top, dpp<0x4e>(top));
+        const uint32_t byte = scale_byte(top);
+        codes[i] = codes_of(f, byte);
+        uint32_t word = byte << (8 * ((threadIdx.x >> 2) & 3));
+        word |= dpp<0x124>(word);  // (row rotations by 4 and 8: all four quads of the row)
+        word |= dpp<0x128>(word);
+        if ((threadIdx.x & 15) == 0) scales[i >> 4] = word;
+    }
+}
+
+template <class T, bool TAIL>
+__global__ void __launch_bounds__(256)
+mx_dequantize_kernel(const uint32_t *__restrict__ codes, const uint8_t *__restrict__ scales, T *__restrict__ out,
+                     int64_t ldo, int64_t M, int64_t K, int pieces) {
+    const int64_t all = M * pieces;
+    for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < all; i += int64_t(gridDim.x) * 256) {
+        const int64_t m = i / pieces, c = i % pieces * 8;
+        const uint32_t b = scales[i >> 2], v = codes[i];
+        const float s = __builtin_bit_cast(float, b == 0 ? 0x00400000u : b == 255 ? 0x7fc00000u : b << 23);
+        typedef float f2 __attribute__((ext_vector_type(2)));
+        const f2 p0 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(v, 1.0f, 0);
+        const f2 p1 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(v, 1.0f, 1);
+        const f2 p2 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(v, 1.0f, 2);
+        const f2 p3 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(v, 1.0f, 3);
+        const float f[8] = {p0.x * s, p0.y * s, p1.x * s, p1.y * s, p2.x * s, p2.y * s, p3.x * s, p3.y * s};
+        constexpr int V = Elem<T>::V;
+#pragma unroll
+        for (int j = 0; j < 8; j += V) {
+            float g[V];
+#pragma unroll
+            for (int q = 0; q < V; ++q) g[q] = f[j + q];
+            if (c + j < K) store_vec<T, false, TAIL>(out + m * ldo, c + j, K, g);
+        }
+    }
+}
+
+// ---- products
+template <bool GROUPED, int OB>
+struct MxProduct {
+    static constexpr bool kAfter = false, kEpilogue = false, kTransA = false, kTransW = false, kPlace = true;
+    const int32_t *offsets;
+    int groups;
+    const uint8_t *sa, *sw;
+    int64_t a_row, ldc;  // bytes of a packed row; elements between C's rows
+
+    template <class CF, int BM, int BN>
+    __device__ __forceinline__ bool place(const uint8_t *&A, const uint8_t *&W, void *&C, int &M, int N, int K, int &,
+                                          int &n0) {
+        const int tiles_n = (N + BN - 1) / BN;
+        int row, rows;
+        if constexpr (GROUPED) {
+            const group::Tile t = group::find_tile<BM>(offsets, groups, M, tiles_n, CF::GM);
+            if (t.group < 0) return false;
+            row = t.row, rows = t.rows, n0 = t.tile_n * BN;
+            W += int64_t(t.group) * N * a_row;
+            sw += int64_t(t.group) * N * (K / 32);
+        } else {
+            const int tiles_m = (M + BM - 1) / BM;
+            const int b = xcd_remap(blockIdx.x, tiles_m * tiles_n);
+            const int super = b / (CF::GM * tiles_n), gm = min(tiles_m - super * CF::GM, CF::GM);
+            const int in = b % (CF::GM * tiles_n);
+            row = (super * CF::GM + in % gm) * BM, rows = M - row, n0 = in / gm * BN;
+        }
+        A += row * a_row;
+        sa += int64_t(row) * (K / 32);
+        C = static_cast<uint8_t *>(C) + row * ldc * OB;
+        M = rows;
+        return true;
+    }
+};
+
+template <int EPI, class CF, bool GROUPED>
+hipError_t gemm_cfg(const Mxfp4Gemm &g, int K, hipStream_t st) {
+    using LY = Layout<MX_F4, CF>;
+    constexpr int OB = EPI == EPI_F32 ? 4 : 2;
+    const MxProduct<GROUPED, OB> ex{g.offsets, g.experts, g.a_scales, g.w_scales, K / 2, g.ldo};
+    const int64_t tiles_n = (g.N + LY::BN - 1) / LY::BN;
+    const int64_t blocks =
+        GROUPED ? group_tiles(g.M, g.experts, LY::BM, tiles_n) : (g.M + LY::BM - 1) / LY::BM * tiles_n;
+    hipLaunchKernelGGL((gemm_kernel<MX_F4, EPI, CF, MxProduct<GROUPED, OB>>), dim3(unsigned(blocks)), dim3(LY::NT), 0,
+                       st, g.a, g.w, nullptr, nullptr, nullptr, g.out, int(g.M), int(g.N), K, (K + 255) / 256, ex);
+    return hipGetLastError();
+}
+
+using Mx32x128 = Cfg<1, 4, 1, 1, 3, 8, true, false>;
+using Mx64x128 = Cfg<2, 2, 1, 2, 3, 8, true, false>;
+using Mx256x128 = Cfg<2, 2, 4, 2, 2, 8, true, false, 0, true>;
+using Mx128x128 = Cfg<2, 2, 2, 2, 3, 8, true, false, 0, true>;
+
+template <int EPI, bool GROUPED>
+hipError_t gemm_any(const Mxfp4Gemm &g, hipStream_t st) {
+    const int K = int(mxfp4_padded(g.K));
+    const int64_t each = GROUPED ? g.M / g.experts : g.M;
+    if (each <= 32) return gemm_cfg<EPI, Mx32x128, GROUPED>(g, K, st);
+    if (each <= 64) return gemm_cfg<EPI, Mx64x128, GROUPED>(g, K, st);
+    if (each <= 256) return gemm_cfg<EPI, Mx128x128, GROUPED>(g, K, st);
+    return gemm_cfg<EPI, Mx256x128, GROUPED>(g, K, st);
+}
+
+template <int EPI>
+hipError_t gemm_epi(const Mxfp4Gemm &g, hipStream_t st) {
+    return g.offsets ? gemm_any<EPI, true>(g, st) : gemm_any<EPI, false>(g, st);
+}
+
+template <class T>
+hipError_t quantize(const void *x, int64_t ldx, uint8_t *codes, uint8_t *scales, int64_t M, int64_t K,
+                    hipStream_t st) {
+    const int pieces = int(mxfp4_padded(K) / 8);
+    const int64_t blocks = (M * pieces + 255) / 256;
+    const dim3 grid(unsigned(blocks < 16384 ? blocks : 16384));
+    const bool whole = K % Elem<T>::V == 0;
+    auto k = whole ? mx_quantize_kernel<T, false> : mx_quantize_kernel<T, true>;
+    hipLaunchKernelGGL(k, grid, dim3(256), 0, st, static_cast<const T *>(x), ldx, reinterpret_cast<uint32_t *>(codes),
+                       reinterpret_cast<uint32_t *>(scales), M, K, pieces);
+    return hipGetLastError();
+}
+
+template <class T>
+hipError_t dequantize(const uint8_t *codes, const uint8_t *scales, void *out, int64_t ldo, int64_t M, int64_t K,
+                      hipStream_t st) {
+    const int pieces = int(mxfp4_padded(K) / 8);
+    const int64_t blocks = (M * pieces + 255) / 256;
+    const dim3 grid(unsigned(blocks < 16384 ? blocks : 16384));
+    const bool whole = K % Elem<T>::V == 0;
+    auto k = whole ? mx_dequantize_kernel<T, false> : mx_dequantize_kernel<T, true>;
+    hipLaunchKernelGGL(k, grid, dim3(256), 0, st, reinterpret_cast<const uint32_t *>(codes), scales,
+                       static_cast<T *>(out), ldo, M, K, pieces);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+int64_t mxfp4_blocks(int64_t M, int64_t experts, int64_t N) {
+    const int64_t tiles_n = (N + 127) / 128;
+    return experts ? group_tiles(M, experts, 32, tiles_n) : (M + 31) / 32 * tiles_n;
+}
+
+hipError_t launch_mxfp4_quantize(int dtype, const void *x, int64_t ldx, uint8_t *codes, uint8_t *scales, int64_t M,
+                                 int64_t K, hipStream_t st) {
+    if (dtype == DT_F16) return quantize<_Float16>(x, ldx, codes, scales, M, K, st);
+    if (dtype == DT_BF16) return quantize<__bf16>(x, ldx, codes, scales, M, K, st);
+    return quantize<float>(x, ldx, codes, scales, M, K, st);
+}
+
+hipError_t launch_mxfp4_dequantize(int dtype, const uint8_t *codes, const uint8_t *scales, void *out, int64_t ldo,
+                                   int64_t M, int64_t K, hipStream_t st) {
+    if (dtype == DT_F16) return dequantize<_Float16>(codes, scales, out, ldo, M, K, st);
+    if (dtype == DT_BF16) return dequantize<__bf16>(codes, scales, out, ldo, M, K, st);
+    return dequantize<float>(codes, scales, out, ldo, M, K, st);
+}
+
+hipError_t launch_mxfp4_gemm(const Mxfp4Gemm &g, hipStream_t st) {
+    if (g.dtype == DT_F16) return gemm_epi<EPI_F16>(g, st);
+    if (g.dtype == DT_BF16) return gemm_epi<EPI_BF16>(g, st);
+    return gemm_epi<EPI_F32>(g, st);
+}
+
+}  // namespace ssg
