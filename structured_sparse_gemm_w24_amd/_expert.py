@@ -8,7 +8,7 @@ gradients are calls of their own and results carry no history.
 
 from __future__ import annotations
 
-import ctypes as ct
+from array import array
 
 from ._tune import (SSG_DT_BF16, SSG_DT_F16, _check, _code, _codes, _flat, _matrix, _on, _out, _ptr, _rows, _stream,
                     _torch, _workspace, load)
@@ -205,40 +205,55 @@ def _dense(t):
     return True
 
 
+# (a model has hundreds of tensors, and each look at one from Python is 50 to 100 ns: what the checks
+# of a good list need is asked for once, in comprehensions, and a bad one is looked at again)
 def _list(grads, name):
-    """Checks a list of tensors on one device; returns it with the C arrays of addresses, sizes and types."""
+    """Checks a list of tensors on one device; returns it with its sizes, types and their C arrays."""
     torch, codes = _torch(), _codes()
     grads = list(grads)
-    device = None
+    if not grads:
+        raise ValueError(f"{name} is empty")
+    good = all([isinstance(t, torch.Tensor) for t in grads])
+    if good:
+        devices = {t.get_device() for t in grads}
+        types = [codes.get(t.dtype, -1) for t in grads]
+        good = len(devices) == 1 and -1 not in devices and -1 not in types and \
+            all([t.is_contiguous() or _dense(t) for t in grads])
+    if not good:
+        _refuse_list(grads, name)
+    sizes = [t.numel() for t in grads]
+    return (grads, sizes, types, array("Q", [t.data_ptr() for t in grads]), array("q", sizes), array("i", types))
+
+
+def _refuse_list(grads, name):
+    torch, codes = _torch(), _codes()
     for t in grads:
         if not isinstance(t, torch.Tensor) or not t.is_cuda:
             raise TypeError(f"{name} must be torch tensors on a HIP device")
-        if device is None:
-            device = t.device
-        elif t.device != device:
-            raise TypeError(f"{name} must be on one device, got {device} and {t.device}")
+        if t.device != grads[0].device:
+            raise TypeError(f"{name} must be on one device, got {grads[0].device} and {t.device}")
         if t.dtype not in codes:
             raise TypeError(f"{name} of type {t.dtype}, which this call does not take")
         if not _dense(t):
             raise ValueError(f"{name} must each fill one run of memory, got strides {t.stride()} of {tuple(t.shape)}")
-    if not grads:
-        raise ValueError(f"{name} is empty")
-    n = len(grads)
-    return (grads, (ct.c_void_p * n)(*[t.data_ptr() for t in grads]), (ct.c_int64 * n)(*[t.numel() for t in grads]),
-            (ct.c_int32 * n)(*[codes[t.dtype] for t in grads]))
+
+
+def _at(a):
+    """Address of an array's items."""
+    return a.buffer_info()[0]
 
 
 def grad_norm(grads, workspace=None):
     """The 2-norm of all elements of the tensors (float16, bfloat16, float32, mixed) as a float32 scalar
     tensor; squares are summed in 64 bits, in a fixed order."""
     torch = _torch()
-    grads, ptrs, sizes, types = _list(grads, "grads")
+    grads, _, _, ptrs, sizes, types = _list(grads, "grads")
     like = grads[0]
     norm = torch.empty((), dtype=torch.float32, device=like.device)
     lib = load()
     ws = _norm_workspace(lib, len(grads), like, workspace)
     with _on(like):
-        _check(lib.grad_norm(len(grads), ptrs, sizes, types, _ptr(norm), _ptr(ws), ws.numel(), _stream(like)))
+        _check(lib.grad_norm(len(grads), _at(ptrs), _at(sizes), _at(types), _ptr(norm), _ptr(ws), ws.numel(), _stream(like)))
     return norm
 
 
@@ -248,23 +263,25 @@ def clip_grad_norm(grads, max_norm, norm=None, out=None, workspace=None):
     tensors to write, grads themselves for clipping in place (left untouched where nothing is clipped);
     None makes new ones.  Tensors that share elements with one that is written are refused."""
     torch = _torch()
-    grads, ptrs, sizes, types = _list(grads, "grads")
+    given_grads = grads
+    grads, numels, codes, ptrs, sizes, types = _list(grads, "grads")
     like = grads[0]
+    n = len(grads)
     if out is None:
         out = [torch.empty_like(t) for t in grads]
+        outs = array("Q", [t.data_ptr() for t in out])
+    elif out is given_grads:
+        out, outs = grads, ptrs
     else:
         out = list(out)
-        if len(out) != len(grads):
-            raise ValueError(f"{len(out)} outputs for {len(grads)} gradients")
-        for o, t in zip(out, grads):
-            if o is t:
-                continue
-            if not isinstance(o, torch.Tensor) or o.dtype is not t.dtype or o.device != t.device:
-                raise TypeError(f"out must be {t.dtype} tensors on {t.device}, as grads are")
-            if o.shape != t.shape or (o.stride() != t.stride() and not (o.is_contiguous() and t.is_contiguous())):
-                raise ValueError("out must have the shapes and strides of grads")
-    n = len(grads)
-    outs = (ct.c_void_p * n)(*[t.data_ptr() for t in out])
+        if len(out) != n:
+            raise ValueError(f"{len(out)} outputs for {n} gradients")
+        out, onumels, ocodes, outs, _, _ = _list(out, "out")
+        if ocodes != codes or out[0].get_device() != like.get_device():
+            raise TypeError("out must have the types of grads, on their device")
+        if onumels != numels or not all([(o.is_contiguous() and t.is_contiguous()) or
+                                         (o.shape == t.shape and o.stride() == t.stride()) for o, t in zip(out, grads)]):
+            raise ValueError("out must be contiguous with grads' sizes, or have the shapes and strides of grads")
     lib = load()
     ws, given = None, norm
     if given is None:
@@ -275,7 +292,7 @@ def clip_grad_norm(grads, max_norm, norm=None, out=None, workspace=None):
     else:
         _flat(given, torch.float32, given.shape, like, "norm")
     with _on(like):
-        _check(lib.clip_grad_norm(n, ptrs, outs, sizes, types, float(max_norm), _ptr(given),
+        _check(lib.clip_grad_norm(n, _at(ptrs), _at(outs), _at(sizes), _at(types), float(max_norm), _ptr(given),
                                   _ptr(norm) if given is None else None, _ptr(ws), ws.numel() if ws is not None else 0,
                                   _stream(like)))
     return norm, out

@@ -75,7 +75,7 @@ int check_grouped(const char *fn, int32_t dtype, const int32_t *offsets, int32_t
                          fn, (long long)M, (long long)N, (long long)K);
     if (int rc = check_groups(fn, offsets, experts)) return rc;
     // (a launch takes fewer than 2^32 threads, in workgroups of up to 512)
-    if (ssg::grouped_blocks(M, experts, N, K) >= (int64_t(1) << 22))
+    if (ssg::grouped_blocks(M, experts, N, K) >= (int64_t(1) << 23))
         return ssg::fail(SSG_EINVAL, "%s: dimensions too large for one launch", fn);
     return SSG_OK;
 }
@@ -105,7 +105,7 @@ int check_mx_gemm(const char *fn, const uint8_t *w, const uint8_t *w_scales, con
                          (long long)N, (long long)K);
     if (offsets ? (rc = check_groups(fn, offsets, experts)) : experts != 1)
         return rc ? rc : ssg::fail(SSG_EINVAL, "%s: experts=%d without offsets", fn, experts);
-    if (ssg::mxfp4_blocks(M, offsets ? experts : 0, N) >= (int64_t(1) << 22))
+    if (ssg::mxfp4_blocks(M, offsets ? experts : 0, N, K) >= (int64_t(1) << 23))
         return ssg::fail(SSG_EINVAL, "%s: dimensions too large for one launch", fn);
     if (M == 0) return SSG_OK;
     if ((rc = check_any(fn, "out", out, ldo, M, N, dtype))) return rc;

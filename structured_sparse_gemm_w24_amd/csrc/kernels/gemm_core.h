@@ -261,6 +261,13 @@ struct Cfg {
     static constexpr int WM = WM_, WN = WN_, TM = TM_, TN = TN_, STAGES = STAGES_, GM = GM_;
     static constexpr bool NTS = NTS_, ROT = ROT_, PROD = PROD_;
     static constexpr int MP = MP_, NLD = NLD_, DK = DK_;
+    static constexpr bool DEEP = false;
+};
+// Four waves of 128 x 128 on a 256 x 256 tile (or TM x TN blocks each), a whole stage's fragments in
+// registers.
+template <int TM_, int TN_, int GM_, bool NTS_>
+struct CfgDeep : Cfg<2, 2, TM_, TN_, 2, GM_, NTS_, false> {
+    static constexpr bool DEEP = true;
 };
 
 template <int KIND, class CF>
@@ -288,10 +295,18 @@ struct Layout {
     // overwrites a block that a stage still in the ring reads.
     static constexpr int MP = KT::kSparse ? CF::MP : 0;
     static constexpr int M_STAGE = MP ? 0 : M_BYTES;
-    // MX_F4: the scales of a stage, 8 bytes a row, [BM] then [BN] rows behind the codes; in 256-byte
-    // chunks of 32 rows (waves past the last chunk load it once more, so that all issue alike)
-    static constexpr int S_CHUNKS = KIND == MX_F4 ? (BM + BN) * DK / 32 : 0;
-    static constexpr int STAGE = A_STAGE + W_STAGE + M_STAGE + S_CHUNKS * 256;
+    static constexpr int STAGE = A_STAGE + W_STAGE + M_STAGE;
+    // MX_F4: scale blocks, the scales of two stages, 16 bytes a row, A's rows then W's, in a ring of
+    // three behind the stages.  Block c is fetched in two parts with the loads of stages 2c - 1 and 2c.
+    // (Fetched stage by stage they are 8 bytes a row, so as many cache lines as all the codes: 8192^3
+    // on the 256 x 256 tile 310 us, without any scales 279.)  In chunks of 64 rows; waves past a part's
+    // last chunk fetch it once more, so that all issue alike.
+    static constexpr int S_AROWS = (BM + 63) / 64 * 64;
+    static constexpr int S_CHUNKS = KIND == MX_F4 ? S_AROWS / 64 + (BN + 63) / 64 : 0;
+    static constexpr int S_PART = (S_CHUNKS + 1) / 2;
+    static constexpr int S_BLOCK = S_CHUNKS * 1024;
+    static constexpr int S_RING = 3 * S_BLOCK;
+    static_assert(S_CHUNKS == 0 || DK == 1, "scale blocks are of two stages of 256 k");
     static constexpr int RW = MP * MW;  // words per row in a block
     static constexpr int MBLK = MP * M_BYTES;
     static constexpr int MSLOTS = MP ? 2 + (CF::STAGES - 2 + MP - 1) / MP : 0;
@@ -309,7 +324,7 @@ struct Layout {
     static constexpr int LA = A_STAGE / 1024 / NL;
     static constexpr int LW = W_STAGE / 1024 / NL;
     static constexpr int LM = MCH >= NL ? MCH / NL : (MCH > 0 ? 1 : 0);
-    static constexpr int LS = (S_CHUNKS + NL - 1) / NL;
+    static constexpr int LS = (S_PART + NL - 1) / NL;
     static constexpr int L = LA + LW + LM + LS;
     static_assert(LA * NL * 1024 == A_STAGE && LW * NL * 1024 == W_STAGE && MCH * 256 == M_BYTES &&
                       (MCH == 0 || MCH % NL == 0 || NL % MCH == 0),
@@ -407,7 +422,7 @@ gemm_kernel(const uint8_t *__restrict__ A, const uint8_t *__restrict__ Wv, const
     constexpr int EWAVE = 32 * EROW;
     constexpr int EPASS = (TM * EWAVE * LY::NW <= CF::STAGES * STAGE) ? TM : 1;
     constexpr int SMEM_EPI = EPASS * EWAVE * LY::NW;
-    constexpr int SMEM_MAIN = CF::STAGES * STAGE + LY::MRING;
+    constexpr int SMEM_MAIN = CF::STAGES * STAGE + LY::MRING + LY::S_RING;
     constexpr int SMEM = (SMEM_MAIN > SMEM_EPI) ? SMEM_MAIN : SMEM_EPI;
 
     __shared__ __attribute__((aligned(1024))) uint8_t smem[SMEM];
@@ -561,32 +576,33 @@ gemm_kernel(const uint8_t *__restrict__ A, const uint8_t *__restrict__ Wv, const
             }
         }
     };
-    // MX_F4: the scales of a stage, words past the end of K as zeros.
-    [[maybe_unused]] auto issue_scales = [&](uint8_t *base, int sg) {
+    // MX_F4: part t + 1 - 2c of scale block c = ceil(t / 2), with the loads of stage t.  (Past the end of
+    // a row it may bring the next row's scales: load_scales() leaves them out.)
+    [[maybe_unused]] auto issue_scales = [&](int t) {
         if constexpr (F4) {
-            constexpr int WPR = 2 * LY::DK;  // words a row
-            const int s_row = K / 32;
+            const int c = (t + 1) >> 1, part = (t + 1) & 1, s_row = K / 32;
             const __amdgpu_buffer_rsrc_t bufSA = buffer_of(extra.sa, uint32_t(min(M, BM) * s_row));
             const __amdgpu_buffer_rsrc_t bufSW = buffer_of(extra.sw, uint32_t(N * s_row));
+            uint8_t *block = smem + NB * STAGE + c % 3 * LY::S_BLOCK;
 #pragma unroll
             for (int j = 0; j < LY::LS; ++j) {
-                const int c = min(j * LY::NL + wave, LY::S_CHUNKS - 1);
-                const int word = c * 64 + lane, row = word / WPR;
-                const int at = (sg * WPR + word % WPR) * 4;
-                const bool of_a = c < BM * LY::DK / 32;  // (a chunk is all A's or all W's)
-                const uint32_t line = uint32_t(of_a ? min(m0 + row, M - 1) : min(n0 + row - BM, N - 1));
-                const uint32_t off = at < s_row ? line * uint32_t(s_row) + uint32_t(at) : 0x80000000u;
-                if (of_a) dma4(bufSA, off, base + A_STAGE + W_STAGE + c * 256);
-                else dma4(bufSW, off, base + A_STAGE + W_STAGE + c * 256);
+                const int chunk = min(part * LY::S_PART + min(j * LY::NL + wave, LY::S_PART - 1), LY::S_CHUNKS - 1);
+                const int row = chunk * 64 + lane;
+                if (chunk < LY::S_AROWS / 64)  // (uniform)
+                    dma16(bufSA, uint32_t(min(m0 + row, M - 1)) * uint32_t(s_row) + uint32_t(c * 16), block + chunk * 1024);
+                else
+                    dma16(bufSW, uint32_t(min(n0 + row - LY::S_AROWS, N - 1)) * uint32_t(s_row) + uint32_t(c * 16),
+                          block + chunk * 1024);
             }
         }
     };
-    auto issue = [&](int s) {
+    // whole: stage s is known to lie inside K (no branch parts what the scheduler may interleave).
+    auto issue = [&](int s, auto whole) {
         if (!issuer) return;
         uint8_t *base = smem + (s % NB) * STAGE;
         const int sg = ks0 + ((s + rot < S) ? s + rot : s + rot - S);  // global K stage
-        if constexpr (F4) issue_scales(base, sg);
-        if constexpr (Extra::kPlace && !Extra::kTransA) {
+        if constexpr (F4) issue_scales(s);
+        if constexpr (Extra::kPlace && !Extra::kTransA && !decltype(whole)::value) {
             if ((sg + 1) * LY::AB > int(k_row)) {
                 issue_end(base, sg);
                 return;
@@ -668,17 +684,17 @@ gemm_kernel(const uint8_t *__restrict__ A, const uint8_t *__restrict__ Wv, const
         }
     };
 
-    // MX_F4: one word of scales serves two k-steps.
+    // MX_F4: one word of scales serves two k-steps (none past the end of K).
     [[maybe_unused]] auto load_scales = [&](int s, int kk, Frag &F, const Frag &before) {
         if constexpr (F4) {
-            constexpr int WPR = 2 * LY::DK;
-            const uint32_t *b = reinterpret_cast<const uint32_t *>(smem + (s % NB) * STAGE + A_STAGE + W_STAGE) + kk / 2;
+            const uint8_t *b = smem + NB * STAGE + (s >> 1) % 3 * LY::S_BLOCK + (s & 1) * 8 + kk / 2 * 4;
+            const uint32_t live = (s * 2 + kk / 2) * 4 < K / 32 ? 0xffffffffu : 0u;
+            auto word = [&](int row) { return (*reinterpret_cast<const uint32_t *>(b + row * 16) & live) >> (8 * h); };
 #pragma unroll
             for (int tn = 0; tn < TN; ++tn)
-                F.sw[tn] = kk % 2 ? before.sw[tn] : b[(BM + wn * TN * 32 + tn * 32 + r) * WPR] >> (8 * h);
+                F.sw[tn] = kk % 2 ? before.sw[tn] : word(LY::S_AROWS + wn * TN * 32 + tn * 32 + r);
 #pragma unroll
-            for (int tm = 0; tm < TM; ++tm)
-                F.sa[tm] = kk % 2 ? before.sa[tm] : b[(wm * TM * 32 + tm * 32 + r) * WPR] >> (8 * h);
+            for (int tm = 0; tm < TM; ++tm) F.sa[tm] = kk % 2 ? before.sa[tm] : word(wm * TM * 32 + tm * 32 + r);
         }
     };
 
@@ -730,9 +746,10 @@ gemm_kernel(const uint8_t *__restrict__ A, const uint8_t *__restrict__ Wv, const
     if (!PROD || loader) {
         if constexpr (LY::MP > 1)
             for (int t = 1 - LY::MP; t < 0; ++t) issue_meta(t);
+        if constexpr (F4) issue_scales(-1);
 #pragma unroll
         for (int s = 0; s < NB; ++s)
-            if (s < S) issue(s);
+            if (s < S) issue(s, std::false_type{});
     }
     if (NB < S) wait_vm_barrier<(NB - 1) * LY::L>();
     else wait_vm_barrier<0>();
@@ -742,9 +759,55 @@ gemm_kernel(const uint8_t *__restrict__ A, const uint8_t *__restrict__ Wv, const
         int s = 0;
         for (; s + NB < S; ++s) {
             wait_vm_barrier<(NB - 2) * LY::L>();
-            issue(s + NB);
+            issue(s + NB, std::false_type{});
         }
         for (; s < S; ++s) wait_vm_barrier<0>();
+    } else if constexpr (CF::DEEP) {
+        // One wave a SIMD with registers for a whole stage's fragments: they are read a stage's last
+        // k-step ahead of their use (and the last one in the first), so that a stage's buffer is free
+        // again after its first k-step, and the loads into it have a stage and a half to arrive instead
+        // of one.  Two barriers a stage: its reads are done, the next stage is there.
+        static_assert(!PROD && NB == 2 && LY::NL == LY::NW);
+        constexpr int NI = LY::NI;
+        Frag F[NI];
+        auto load = [&](int s, int kk) {
+            load_frag(s, kk, F[kk]);
+            if constexpr (F4) load_scales(s, kk, F[kk], F[kk & ~1]);
+        };
+#pragma unroll
+        for (int kk = 0; kk + 1 < NI; ++kk) load(0, kk);
+        // PHASE 0: stage s + NB is fetched, and whole; 1: fetched; 2: there is none
+        auto stage = [&](int s, auto phase) {
+            constexpr int PHASE = decltype(phase)::value;
+#pragma unroll
+            for (int kk = 0; kk < NI; ++kk) {
+                if (kk == 0) load(s, NI - 1);
+                if (kk == 1 && PHASE < 2) {
+                    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+                    if constexpr (PHASE == 0) issue(s + NB, std::true_type{});
+                    else issue(s + NB, std::false_type{});
+                }
+                if (kk == NI - 1) {
+                    if constexpr (PHASE < 2) wait_vm_barrier<LY::L>();
+                    else wait_vm_barrier<0>();
+#pragma unroll
+                    for (int k = 0; k + 1 < NI; ++k) load(s + 1, k);
+                }
+                mma_frag(F[kk], kk);
+#pragma unroll
+                for (int i = 0; i < TN * TM; ++i) {
+                    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);  // matrix
+                    if (kk == NI - 1) __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);  // LDS reads
+                    else if (kk == 0) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+                    else if (PHASE < 2 && i % 2 == 0) __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);  // loads
+                }
+            }
+        };
+        const int whole = Extra::kPlace && !Extra::kTransA ? int(k_row / LY::AB) : S;
+        int s = 0;
+        for (; s + NB < whole; ++s) stage(s, std::integral_constant<int, 0>{});
+        for (; s + NB < S; ++s) stage(s, std::integral_constant<int, 1>{});
+        for (; s < S; ++s) stage(s, std::integral_constant<int, 2>{});
     } else {
         Frag F[2];
         load_frag(0, 0, F[0]);
@@ -765,7 +828,7 @@ gemm_kernel(const uint8_t *__restrict__ A, const uint8_t *__restrict__ Wv, const
                     // stage s is fully in registers; stage s+1 must be complete
                     if constexpr (decltype(steady)::value) {
                         wait_lgkm_vm_barrier<(NB - 2) * LY::L>();
-                        if constexpr (!PROD) issue(s + NB);  // reuses stage s's buffer
+                        if constexpr (!PROD) issue(s + NB, std::false_type{});  // reuses stage s's buffer
                     } else {
                         wait_lgkm_vm_barrier<0>();
                     }

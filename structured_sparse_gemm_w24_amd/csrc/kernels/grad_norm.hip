@@ -5,9 +5,10 @@
 // Bound by memory: every element is read for the norm, read again and written for the
 // scaling.  The tensors' addresses travel in the kernel arguments (a launch takes as
 // many as fit in 4 KiB), so a call copies nothing to the device and captures into a
-// graph.  A launch's tensors are cut into pieces of 16 KiB; each workgroup of a fixed grid
-// takes a run of consecutive pieces, so each writes one partial sum and the sums are added
-// in a fixed order.  Squares and sums are fp64: an fp32 gradient of 1e30 does not overflow,
+// graph.  A launch's tensors are cut into pieces of 16 KiB, which the workgroups of a grid of
+// fixed size take in turn; each writes one partial sum and the sums are added in a fixed
+// order.  So a launch walks through memory once from its first tensor to its last, and the
+// scaling walks back the same way: what the norm read last (256 MB) may still be cached.  Squares and sums are fp64: an fp32 gradient of 1e30 does not overflow,
 // and the order of summation shows in no digit of an fp32 norm.
 #include "elem.h"
 #include "launch.h"
@@ -48,10 +49,6 @@ __device__ __forceinline__ int tensor_of(const Table &t, uint32_t p) {
         else hi = mid - 1;
     }
     return lo;
-}
-
-__device__ __forceinline__ uint32_t run_start(uint32_t pieces, uint32_t b) {
-    return uint32_t(uint64_t(pieces) * b / gridDim.x);
 }
 
 template <class T>
@@ -132,10 +129,9 @@ __global__ void __launch_bounds__(kThreads)
 norm_squares_kernel(NormTable t, double *__restrict__ part) {
     __shared__ double red[kThreads / 64];
     const uint32_t pieces = t.first[t.n];
-    const uint32_t from = run_start(pieces, blockIdx.x), to = run_start(pieces, blockIdx.x + 1);
     double sum = 0.0;
-    int at = tensor_of(t, from);
-    for (uint32_t p = from; p < to; ++p) {
+    int at = tensor_of(t, blockIdx.x);
+    for (uint32_t p = blockIdx.x; p < pieces; p += gridDim.x) {
         while (t.first[at + 1] <= p) ++at;
         const int64_t n = t.size[at] & ((int64_t(1) << 56) - 1);
         const int type = int(t.size[at] >> 56);
@@ -164,8 +160,7 @@ norm_finish_kernel(const double *__restrict__ part, int slots, float *__restrict
 }
 
 // Every workgroup adds the partial sums for itself (at most 8 KiB a launch of the first kernel,
-// from L2), which takes less than a launch between.  The pieces go backwards: the last ones
-// read for the norm are the likeliest to be cached.
+// from L2), which takes less than a launch between.
 __global__ void __launch_bounds__(kThreads)
 clip_kernel(ClipTable t, double max_norm, const float *__restrict__ norm_in, const double *__restrict__ part, int slots,
             float *__restrict__ norm) {
@@ -174,11 +169,10 @@ clip_kernel(ClipTable t, double max_norm, const float *__restrict__ norm_in, con
     if (norm && blockIdx.x == 0 && threadIdx.x == 0) norm[0] = float(n);
     const double c = max_norm / (n + kEps);
     const float by = c > 1.0 ? 1.0f : float(c);  // (a NaN stays one)
-    const uint32_t pieces = t.first[t.n], b = gridDim.x - 1 - blockIdx.x;
-    const uint32_t from = run_start(pieces, b), to = run_start(pieces, b + 1);
-    if (from >= to) return;
-    int at = tensor_of(t, to - 1);
-    for (uint32_t p = to; p-- > from;) {
+    const uint32_t pieces = t.first[t.n];
+    int at = tensor_of(t, pieces - 1 - blockIdx.x);
+    for (uint32_t back = blockIdx.x; back < pieces; back += gridDim.x) {
+        const uint32_t p = pieces - 1 - back;
         while (t.first[at] > p) --at;
         if (by == 1.0f && t.grad[at] == t.out[at]) continue;
         const int64_t size = t.size[at] & ((int64_t(1) << 56) - 1);
@@ -190,33 +184,48 @@ clip_kernel(ClipTable t, double max_norm, const float *__restrict__ norm_in, con
     }
 }
 
-// Entries of l from i on, at most Most of them; returns how many entries were looked at.
-template <int Most, class Table, class F>
-int fill(const GradList &l, int i, Table &t, F more) {
-    t.n = 0;
-    uint64_t pieces = 0;
-    int at = i;
-    for (; at < l.n && t.n < Most; ++at) {
-        if (l.sizes[at] == 0) continue;
-        const int64_t bytes = l.sizes[at] * (l.dtypes[at] == DT_F32 ? 4 : 2);
-        const uint64_t here = uint64_t((bytes + kPiece - 1) / kPiece);
-        if (pieces + here >= (uint64_t(1) << 32)) break;
-        t.grad[t.n] = l.grads[at];
-        t.size[t.n] = l.sizes[at] | int64_t(l.dtypes[at]) << 56;
-        t.first[t.n] = uint32_t(pieces);
-        more(t, at);
+int64_t pieces_of(const GradList &l, int i) {
+    return (l.sizes[i] * (l.dtypes[i] == DT_F32 ? 4 : 2) + kPiece - 1) / kPiece;
+}
+
+// The end of the entries from i on that go into one table (those before i, backwards: their start).
+template <int Most>
+int table_end(const GradList &l, int i, bool back) {
+    int64_t pieces = 0;
+    for (int n = 0; back ? i > 0 : i < l.n; i += back ? -1 : 1) {
+        const int64_t here = pieces_of(l, back ? i - 1 : i);
+        if (here == 0) continue;
+        if (n == Most || (n > 0 && pieces + here >= (int64_t(1) << 31))) break;
+        ++n;
         pieces += here;
+    }
+    return i;
+}
+
+// Fills a table with the entries [i, end) that are not empty.
+template <class Table, class F>
+void fill(const GradList &l, int i, int end, Table &t, F more) {
+    t.n = 0;
+    uint32_t pieces = 0;
+    for (; i < end; ++i) {
+        if (l.sizes[i] == 0) continue;
+        t.grad[t.n] = l.grads[i];
+        t.size[t.n] = l.sizes[i] | int64_t(l.dtypes[i]) << 56;
+        t.first[t.n] = pieces;
+        more(t, i);
+        pieces += uint32_t(pieces_of(l, i));
         ++t.n;
     }
-    t.first[t.n] = uint32_t(pieces);
-    return at - i;
+    t.first[t.n] = pieces;
 }
 
 hipError_t squares(const GradList &l, double *ws, int &slots, hipStream_t st) {
     slots = 0;
     for (int i = 0; i < l.n;) {
         NormTable t;
-        i += fill<kNormTensors>(l, i, t, [](NormTable &, int) {});
+        const int end = table_end<kNormTensors>(l, i, false);
+        fill(l, i, end, t, [](NormTable &, int) {});
+        i = end;
         if (t.n == 0) continue;
         const uint32_t pieces = t.first[t.n];
         const int grid = pieces < uint32_t(kGrid) ? int(pieces) : kGrid;
@@ -250,9 +259,11 @@ hipError_t launch_clip_grad_norm(const GradList &l, double max_norm, const float
     hipError_t e = norm_in ? hipSuccess : squares(l, ws, slots, st);
     if (e != hipSuccess) return e;
     bool told = norm_in != nullptr;  // the first scaling launch writes the norm
-    for (int i = 0; i < l.n;) {
+    for (int end = l.n; end > 0;) {
         ClipTable t;
-        i += fill<kClipTensors>(l, i, t, [&](ClipTable &u, int at) { u.out[u.n] = l.outs[at]; });
+        const int i = table_end<kClipTensors>(l, end, true);
+        fill(l, i, end, t, [&](ClipTable &u, int at) { u.out[u.n] = l.outs[at]; });
+        end = i;
         if (t.n == 0) continue;
         const uint32_t pieces = t.first[t.n];
         const int grid = pieces < uint32_t(2 * kGrid) ? int(pieces) : 2 * kGrid;

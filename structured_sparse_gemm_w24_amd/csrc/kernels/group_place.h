@@ -12,6 +12,8 @@
 // raised to the largest before it, so groups never overlap and never leave the operands.
 #pragma once
 
+#include <cmath>
+
 #include "common.h"
 
 namespace ssg {
@@ -103,6 +105,44 @@ __device__ __forceinline__ void rows_of(const int32_t *offsets, int groups, int 
 }
 
 }  // namespace group
+
+// A tile's cost in a launch: `per_cu` workgroups share a CU, so `tiles` of them take
+// rounds = tiles / (256 per_cu), each of tile + stages * stage us (the stage times measured with one
+// workgroup on a CU or with a full one), after a start that does not depend on them.  The figures are
+// fitted to launches of random sizes on MI355X (80 for each product of grouped.hip, 110 of mxfp4.hip,
+// all candidates timed); the choice by least cost is 4 to 5 % off the best tile of each in the mean.
+struct TileCost {
+    int bm, bn, per_cu;
+    float start, tile, stage;
+    float us(double tiles, double stages) const {
+        double rounds = tiles / (256.0 * per_cu);
+        if (rounds <= 3.0) rounds = double(int64_t(rounds) + (rounds > double(int64_t(rounds)) ? 1 : 0));
+        else rounds += 0.5;
+        const double share = tiles / 256.0 < 1.0 ? 1.0 : tiles / 256.0 < per_cu ? tiles / 256.0 : per_cu;
+        return float(start + (rounds < 1.0 ? 1.0 : rounds) * (tile + stages * stage * share));
+    }
+};
+
+// Tile rows that M rows in `groups` groups will need about: the host knows no group's length, so half a
+// tile is taken to be empty at the end of every group that an even choice would reach.
+inline double group_tile_rows(int64_t M, int64_t groups, int bm) {
+    if (groups == 1) return double((M + bm - 1) / bm);
+    const double live = double(groups) * (1.0 - std::exp(-double(M) / double(groups)));
+    const double rows = double(M) / bm + 0.5 * live;
+    return rows > live ? rows : live;
+}
+
+// The cheapest of N tiles: tiles(bm, bn) says how many a launch has.
+template <int N, class F>
+int cheapest(const TileCost (&c)[N], double stages, F tiles) {
+    int best = 0;
+    float least = 0.0f;
+    for (int i = 0; i < N; ++i) {
+        const float us = c[i].us(tiles(c[i].bm, c[i].bn), stages);
+        if (i == 0 || us < least) best = i, least = us;
+    }
+    return best;
+}
 
 // Workgroups that any division of M rows into `groups` groups can need.
 inline int64_t group_tiles(int64_t M, int64_t groups, int64_t bm, int64_t tiles_n) {

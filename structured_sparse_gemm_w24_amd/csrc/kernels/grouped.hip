@@ -83,10 +83,29 @@ hipError_t launch_cfg(const void *A, const void *W, void *C, const Extra &ex, in
     return hipGetLastError();
 }
 
-using Cfg32x128 = Cfg<1, 4, 1, 1, 4, 8, true, false>;
+// Tiles: with few of them the smallest, whose loads have waves of their own (a chain of K stages, each
+// waiting for memory: 2000 rows of 48 x 1560 in 8 groups 8.7 us, 64 x 64 without loader waves 10.9,
+// 128 x 128 12.9); dx needs loader waves at every size, as its transposing reads keep the others busy
+// (16384 x 1024 from 4096, 16 experts: 155 us on 192 x 128, 252 on 256 x 256 without).
+using Cfg32x64 = Cfg<1, 2, 1, 1, 4, 8, true, false, 0, true>;
+using Cfg64x64 = Cfg<2, 2, 1, 1, 3, 8, true, false>;
+using Cfg64x64P = Cfg<2, 2, 1, 1, 4, 8, true, false, 0, true>;
 using Cfg64x128 = Cfg<2, 2, 1, 2, 3, 8, true, false>;
-using Cfg128x128 = Cfg<2, 2, 2, 2, 4, 8, true, false, 0, true>;
-using Cfg256x128 = Cfg<2, 2, 4, 2, 3, 8, true, false, 0, true>;
+using Cfg64x128P = Cfg<2, 2, 1, 2, 3, 8, true, false, 0, true>;
+using Cfg128x128 = CfgDeep<2, 2, 8, true>;
+using Cfg128x128P = Cfg<2, 2, 2, 2, 4, 8, true, false, 0, true>;
+using Cfg192x128P = Cfg<2, 2, 3, 2, 4, 8, true, false, 0, true>;
+using Cfg256x128P = Cfg<2, 2, 4, 2, 3, 8, true, false, 0, true>;
+constexpr TileCost kFwdTiles[] = {{32, 64, 3, 4.2f, 0.8f, 0.19f},  {64, 64, 3, 4.1f, 0.2f, 0.30f},
+                                  {64, 128, 2, 3.4f, 1.0f, 0.45f}, {128, 128, 2, 2.1f, 2.8f, 0.55f},
+                                  {192, 128, 1, 0.0f, 5.1f, 0.68f}, {256, 256, 1, 0.0f, 7.2f, 1.33f}};
+constexpr TileCost kDxTiles[] = {{32, 64, 3, 3.7f, 0.7f, 0.22f},   {64, 64, 2, 3.6f, 1.3f, 0.31f},
+                                 {64, 128, 1, 2.4f, 1.1f, 0.46f},  {128, 128, 1, 0.0f, 4.3f, 0.58f},
+                                 {128, 128, 2, 4.6f, 0.9f, 0.77f}, {192, 128, 1, 0.0f, 5.6f, 0.67f},
+                                 {256, 256, 1, 0.0f, 6.7f, 1.75f}};
+constexpr TileCost kDwTiles[] = {{32, 64, 3, 3.1f, 1.2f, 0.21f},   {64, 128, 1, 3.9f, 0.9f, 0.45f},
+                                 {128, 128, 2, 2.2f, 1.8f, 1.01f}, {128, 128, 1, 3.0f, 2.2f, 0.66f},
+                                 {256, 128, 1, 3.6f, 3.6f, 1.04f}, {256, 256, 1, 1.9f, 4.5f, 2.41f}};
 
 template <int KIND, class CF, bool TW>
 hipError_t rows_cfg(const Grouped &a, const void *A, int64_t lda, void *C, int64_t ldc, int N, int K, hipStream_t st) {
@@ -96,13 +115,47 @@ hipError_t rows_cfg(const Grouped &a, const void *A, int64_t lda, void *C, int64
     return launch_cfg<KIND, CF>(A, a.w, C, ex, blocks, int(a.M), N, K, st);
 }
 
+// Entry of kFwdTiles, kDxTiles (TW) and kDwTiles for a product.
+template <bool TW>
+int rows_tile(int64_t M, int64_t experts, int64_t N, int64_t K) {
+    auto count = [&](int bm, int bn) { return group_tile_rows(M, experts, bm) * double((N + bn - 1) / bn); };
+    const double stages = double((K + 63) / 64);
+    if constexpr (TW) return cheapest(kDxTiles, stages, count);
+    else return cheapest(kFwdTiles, stages, count);
+}
+int weights_tile(int64_t M, int64_t experts, int64_t N, int64_t K) {
+    auto count = [&](int bm, int bn) {
+        return double(experts) * double((N + bm - 1) / bm) * double((K + bn - 1) / bn);
+    };
+    const double stages = double(M) / double(experts) / 64.0 + 0.5;
+    return cheapest(kDwTiles, stages < 1.0 ? 1.0 : stages, count);
+}
+
 template <int KIND, bool TW>
 hipError_t rows(const Grouped &a, const void *A, int64_t lda, void *C, int64_t ldc, int N, int K, hipStream_t st) {
-    const int64_t each = a.M / a.experts;
-    if (each <= 32) return rows_cfg<KIND, Cfg32x128, TW>(a, A, lda, C, ldc, N, K, st);
-    if (each <= 64) return rows_cfg<KIND, Cfg64x128, TW>(a, A, lda, C, ldc, N, K, st);
-    if (each <= 256) return rows_cfg<KIND, Cfg128x128, TW>(a, A, lda, C, ldc, N, K, st);
-    return rows_cfg<KIND, CfgBigDense<true>, TW>(a, A, lda, C, ldc, N, K, st);
+#define SSG_TILE(i, CF) \
+    case i: return rows_cfg<KIND, CF, TW>(a, A, lda, C, ldc, N, K, st)
+    if constexpr (TW) {
+        switch (rows_tile<true>(a.M, a.experts, N, K)) {
+            SSG_TILE(0, Cfg32x64);
+            SSG_TILE(1, Cfg64x64P);
+            SSG_TILE(2, Cfg64x128P);
+            SSG_TILE(3, Cfg128x128P);
+            SSG_TILE(4, Cfg128x128);
+            SSG_TILE(5, Cfg192x128P);
+            default: return rows_cfg<KIND, CfgBigDense<true>, TW>(a, A, lda, C, ldc, N, K, st);
+        }
+    } else {
+        switch (rows_tile<false>(a.M, a.experts, N, K)) {
+            SSG_TILE(0, Cfg32x64);
+            SSG_TILE(1, Cfg64x64);
+            SSG_TILE(2, Cfg64x128);
+            SSG_TILE(3, Cfg128x128);
+            SSG_TILE(4, Cfg192x128P);
+            default: return rows_cfg<KIND, CfgBigDense<true>, TW>(a, A, lda, C, ldc, N, K, st);
+        }
+    }
+#undef SSG_TILE
 }
 
 template <int KIND, class CF>
@@ -117,8 +170,14 @@ hipError_t weights_cfg(const Grouped &a, hipStream_t st) {
 
 template <int KIND>
 hipError_t weights(const Grouped &a, hipStream_t st) {
-    if (a.experts * tiles(int(a.N), int(a.K), 128, 128) < 96) return weights_cfg<KIND, CfgT64<true, false>>(a, st);
-    return weights_cfg<KIND, Cfg256x128>(a, st);
+    switch (weights_tile(a.M, a.experts, a.N, a.K)) {
+        case 0: return weights_cfg<KIND, Cfg32x64>(a, st);
+        case 1: return weights_cfg<KIND, Cfg64x128P>(a, st);
+        case 2: return weights_cfg<KIND, Cfg<2, 2, 2, 2, 2, 8, true, false>>(a, st);
+        case 3: return weights_cfg<KIND, Cfg128x128P>(a, st);
+        case 4: return weights_cfg<KIND, Cfg256x128P>(a, st);
+        default: return weights_cfg<KIND, CfgBigDense<true>>(a, st);
+    }
 }
 
 template <int KIND>
@@ -133,10 +192,13 @@ hipError_t backward(const Grouped &a, hipStream_t st) {
 }  // namespace
 
 int64_t grouped_blocks(int64_t M, int64_t experts, int64_t N, int64_t K) {
-    const int64_t side = N > K ? N : K;
-    const int64_t fwd = group_tiles(M, experts, 32, (side + 127) / 128);
-    const int64_t dw = experts * ((N + 63) / 64) * ((K + 63) / 64);
-    return fwd > dw ? fwd : dw;
+    auto of_rows = [&](const TileCost &t, int64_t n) { return group_tiles(M, experts, t.bm, (n + t.bn - 1) / t.bn); };
+    const TileCost &w = kDwTiles[weights_tile(M, experts, N, K)];
+    const int64_t fwd = of_rows(kFwdTiles[rows_tile<false>(M, experts, N, K)], N);
+    const int64_t dx = of_rows(kDxTiles[rows_tile<true>(M, experts, K, N)], K);
+    const int64_t dw = experts * ((N + w.bm - 1) / w.bm) * ((K + w.bn - 1) / w.bn);
+    const int64_t most = fwd > dx ? fwd : dx;
+    return most > dw ? most : dw;
 }
 
 hipError_t launch_grouped_fwd(const Grouped &a, hipStream_t st) {

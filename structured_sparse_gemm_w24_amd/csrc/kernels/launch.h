@@ -176,7 +176,7 @@ struct Grouped {
 };
 hipError_t launch_grouped_fwd(const Grouped &a, hipStream_t st);
 hipError_t launch_grouped_bwd(const Grouped &a, hipStream_t st);
-// workgroups of the finest launch of these sizes
+// workgroups of the largest of the launches of these sizes
 int64_t grouped_blocks(int64_t M, int64_t experts, int64_t N, int64_t K);
 
 // Microscaled 4-bit floating point (formulas in mxfp4.hip).  Packed rows hold kp
@@ -194,8 +194,8 @@ struct Mxfp4Gemm {
     int64_t ldo, M, N, K;
 };
 hipError_t launch_mxfp4_gemm(const Mxfp4Gemm &g, hipStream_t st);
-// workgroups of the finest launch of these sizes (experts 0: one product)
-int64_t mxfp4_blocks(int64_t M, int64_t experts, int64_t N);
+// workgroups of a product (experts 0: of all rows with one weight)
+int64_t mxfp4_blocks(int64_t M, int64_t experts, int64_t N, int64_t K);
 inline int64_t mxfp4_padded(int64_t K) { return (K + 127) / 128 * 128; }
 
 // Sum of squares over many tensors and their scaling (grad_norm.hip).  ws: fp64

@@ -158,19 +158,38 @@ hipError_t gemm_cfg(const Mxfp4Gemm &g, int K, hipStream_t st) {
     return hipGetLastError();
 }
 
-using Mx32x128 = Cfg<1, 4, 1, 1, 3, 8, true, false>;
-using Mx64x128 = Cfg<2, 2, 1, 2, 3, 8, true, false>;
-using Mx256x128 = Cfg<2, 2, 4, 2, 2, 8, true, false, 0, true>;
-using Mx128x128 = Cfg<2, 2, 2, 2, 3, 8, true, false, 0, true>;
+// Tiles: the largest keep a whole stage's fragments in registers (CfgDeep: 8192^3 261 us, the same tile
+// without 313, eight waves of two a SIMD 329); 128 x 128 ones share a CU in pairs, one's epilogue under
+// the other's main loop, which short K likes (6000 x 4096 x 1024 22.3 us, 256 x 256 26.7).
+using Mx32x32 = Cfg<1, 1, 1, 1, 4, 8, true, false, 0, true>;
+using Mx64x64 = CfgDeep<1, 1, 8, true>;
+using Mx64x128 = CfgDeep<1, 2, 8, true>;
+using Mx128x128 = CfgDeep<2, 2, 8, true>;
+using Mx192x256 = CfgDeep<3, 4, 8, true>;
+using Mx256x256 = CfgDeep<4, 4, 4, true>;
+constexpr TileCost kMxTiles[] = {{32, 32, 6, 4.6f, 2.1f, 0.10f},   {64, 64, 4, 3.2f, 2.9f, 0.20f},
+                                 {64, 128, 2, 4.1f, 2.0f, 0.39f},  {128, 128, 2, 1.9f, 4.8f, 0.51f},
+                                 {192, 256, 1, 0.9f, 8.0f, 1.19f}, {256, 256, 1, 0.8f, 9.7f, 1.32f}};
+
+// (experts 0: one product)
+int mx_tile(int64_t M, int64_t experts, int64_t N, int64_t K) {
+    auto count = [&](int bm, int bn) {
+        return group_tile_rows(M, experts ? experts : 1, bm) * double((N + bn - 1) / bn);
+    };
+    return cheapest(kMxTiles, double((K + 255) / 256), count);
+}
 
 template <int EPI, bool GROUPED>
 hipError_t gemm_any(const Mxfp4Gemm &g, hipStream_t st) {
     const int K = int(mxfp4_padded(g.K));
-    const int64_t each = GROUPED ? g.M / g.experts : g.M;
-    if (each <= 32) return gemm_cfg<EPI, Mx32x128, GROUPED>(g, K, st);
-    if (each <= 64) return gemm_cfg<EPI, Mx64x128, GROUPED>(g, K, st);
-    if (each <= 256) return gemm_cfg<EPI, Mx128x128, GROUPED>(g, K, st);
-    return gemm_cfg<EPI, Mx256x128, GROUPED>(g, K, st);
+    switch (mx_tile(g.M, GROUPED ? g.experts : 0, g.N, g.K)) {
+        case 0: return gemm_cfg<EPI, Mx32x32, GROUPED>(g, K, st);
+        case 1: return gemm_cfg<EPI, Mx64x64, GROUPED>(g, K, st);
+        case 2: return gemm_cfg<EPI, Mx64x128, GROUPED>(g, K, st);
+        case 3: return gemm_cfg<EPI, Mx128x128, GROUPED>(g, K, st);
+        case 4: return gemm_cfg<EPI, Mx192x256, GROUPED>(g, K, st);
+        default: return gemm_cfg<EPI, Mx256x256, GROUPED>(g, K, st);
+    }
 }
 
 template <int EPI>
@@ -206,9 +225,10 @@ hipError_t dequantize(const uint8_t *codes, const uint8_t *scales, void *out, in
 
 }  // namespace
 
-int64_t mxfp4_blocks(int64_t M, int64_t experts, int64_t N) {
-    const int64_t tiles_n = (N + 127) / 128;
-    return experts ? group_tiles(M, experts, 32, tiles_n) : (M + 31) / 32 * tiles_n;
+int64_t mxfp4_blocks(int64_t M, int64_t experts, int64_t N, int64_t K) {
+    const TileCost &t = kMxTiles[mx_tile(M, experts, N, K)];
+    const int64_t tiles_n = (N + t.bn - 1) / t.bn;
+    return experts ? group_tiles(M, experts, t.bm, tiles_n) : (M + t.bm - 1) / t.bm * tiles_n;
 }
 
 hipError_t launch_mxfp4_quantize(int dtype, const void *x, int64_t ldx, uint8_t *codes, uint8_t *scales, int64_t M,
