@@ -525,10 +525,12 @@ int grouped_gemm(int32_t dtype, const void *x, int64_t ldx, const void *w, const
 /* Its gradients for dy [M][N]: dx[m] = w[e]^T . dy[m] [M][K], and dw [experts][N][K]
  * contiguous, dw[e] = sum over e's rows of dy[m] x[m]^T (zeros for an expert
  * without rows).  dx or dw may be null: not computed (then w, or x, may be null
- * too).  No atomics: results repeat bit for bit. */
+ * too).  No atomics: results repeat bit for bit.  ws: 16-byte aligned,
+ * grouped_gemm_backward_workspace_bytes() (often 0; not used without dw). */
 int grouped_gemm_backward(int32_t dtype, const void *dy, int64_t lddy, const void *x, int64_t ldx, const void *w,
                           const int32_t *offsets, int32_t experts, void *dx, int64_t lddx, void *dw, int64_t M,
-                          int64_t N, int64_t K, void *stream);
+                          int64_t N, int64_t K, void *ws, int64_t ws_bytes, void *stream);
+int64_t grouped_gemm_backward_workspace_bytes(int32_t experts, int64_t M, int64_t N, int64_t K);
 
 /* Microscaled 4-bit rows (MXFP4: E2M1 values, every 32 along K share a scale).
  * A packed matrix of M rows of K values has, with kp = K rounded up to 128,
@@ -540,7 +542,7 @@ int grouped_gemm_backward(int32_t dtype, const void *dy, int64_t lddy, const voi
  * mxfp4_quantize: scale byte max(0, floor(log2 max|x|) + 125) of each block,
  * code the nearest magnitude to |x| / scale (ties to the even code, past 6: 6).
  * A block with an infinity or NaN gets byte 255 and codes 0.  x of any dtype,
- * element-aligned, any row stride >= K. */
+ * element-aligned, any row stride >= K; 0 <= M < 2^31, 1 <= K < 2^22, fewer than 2^37 values. */
 int mxfp4_quantize(int32_t dtype, const void *x, int64_t ldx, uint8_t *codes, uint8_t *scales, int64_t M, int64_t K,
                    void *stream);
 /* out [M][K] of any dtype: the values, rounded once to it. */

@@ -45,7 +45,7 @@ def grouped_gemm(x, w, offsets, out=None):
     return out
 
 
-def grouped_gemm_backward(dy, x, w, offsets, out=None, dw_out=None, x_grad=True, w_grad=True):
+def grouped_gemm_backward(dy, x, w, offsets, out=None, dw_out=None, x_grad=True, w_grad=True, workspace=None):
     """Gradients of grouped_gemm for dy [M, N]: returns (dx, dw), dx [M, K] (rows of no expert as in
     grouped_gemm) and dw [E, N, K] (zeros for an expert without rows), in x's type; None for one that is
     not asked for."""
@@ -60,11 +60,15 @@ def grouped_gemm_backward(dy, x, w, offsets, out=None, dw_out=None, x_grad=True,
     lddx = k
     if x_grad:
         dx, lddx = _out(out, x, (m, k))
+    lib, ws = load(), None
     if w_grad:
         dw = _torch().empty_like(w) if dw_out is None else _flat(dw_out, x.dtype, (e, n, k), x, "dw_out")
+        need = lib.grouped_gemm_backward_workspace_bytes(e, m, n, k)
+        if need > 0:
+            ws = _workspace(need, x, workspace)
     with _on(x):
-        _check(load().grouped_gemm_backward(dt, _ptr(dy), lddy, _ptr(x), ldx, _ptr(w), _ptr(offsets), e, _ptr(dx), lddx,
-                                            _ptr(dw), m, n, k, _stream(x)))
+        _check(lib.grouped_gemm_backward(dt, _ptr(dy), lddy, _ptr(x), ldx, _ptr(w), _ptr(offsets), e, _ptr(dx), lddx,
+                                         _ptr(dw), m, n, k, _ptr(ws), ws.numel() if ws is not None else 0, _stream(x)))
     return dx, dw
 
 
@@ -90,10 +94,13 @@ def mxfp4_quantize(x, codes_out=None, scales_out=None):
     ldx = _rows(x, x, x.shape, "x")
     kp = _padded(k)
     if codes_out is None:
-        codes_out = torch.empty(m, kp // 2, dtype=torch.uint8, device=x.device)
+        codes_out = x.new_empty((m, kp // 2), dtype=torch.uint8)
+    else:
+        _flat(codes_out, torch.uint8, (m, kp // 2), x, "codes_out")
     if scales_out is None:
-        scales_out = torch.empty(m, kp // BLOCK, dtype=torch.uint8, device=x.device)
-    _packed(codes_out, scales_out, (m,), k, x, "codes_out")
+        scales_out = x.new_empty((m, kp // BLOCK), dtype=torch.uint8)
+    else:
+        _flat(scales_out, torch.uint8, (m, kp // BLOCK), x, "scales_out")
     with _on(x):
         _check(load().mxfp4_quantize(dt, _ptr(x), ldx, _ptr(codes_out), _ptr(scales_out), m, k, _stream(x)))
     return codes_out, scales_out
@@ -110,7 +117,7 @@ def mxfp4_dequantize(codes, scales, k, dtype=None, out=None):
     m = codes.shape[0]
     _packed(codes, scales, (m,), k, codes, "codes")
     if out is None:
-        out, ldo = torch.empty(m, k, dtype=dtype, device=codes.device), k
+        out, ldo = codes.new_empty((m, k), dtype=dtype), k
     else:
         if out.dtype is not dtype:
             raise TypeError(f"out must be {dtype}, got {out.dtype}")
@@ -137,7 +144,7 @@ def mxfp4_gemm(a, a_scales, w, w_scales, k, dtype=None, offsets=None, out=None):
     _packed(a, a_scales, (m,), k, a, "a")
     e, n = _mx_weight(w, w_scales, offsets, k, a)
     if out is None:
-        out, ldo = torch.empty(m, n, dtype=dtype, device=a.device), n
+        out, ldo = a.new_empty((m, n), dtype=dtype), n
     else:
         if out.dtype is not dtype:
             raise TypeError(f"out must be {dtype}, got {out.dtype}")
@@ -208,21 +215,24 @@ def _dense(t):
 # (a model has hundreds of tensors, and each look at one from Python is 50 to 100 ns: what the checks
 # of a good list need is asked for once, in comprehensions, and a bad one is looked at again)
 def _list(grads, name):
-    """Checks a list of tensors on one device; returns it with its sizes, types and their C arrays."""
-    torch, codes = _torch(), _codes()
+    """Checks a list of tensors on one device; returns it, whether all are contiguous, its device, sizes and
+    types, and the C arrays of addresses, sizes and types."""
+    codes = _codes()
     grads = list(grads)
     if not grads:
         raise ValueError(f"{name} is empty")
-    good = all([isinstance(t, torch.Tensor) for t in grads])
-    if good:
+    try:
         devices = {t.get_device() for t in grads}
         types = [codes.get(t.dtype, -1) for t in grads]
-        good = len(devices) == 1 and -1 not in devices and -1 not in types and \
-            all([t.is_contiguous() or _dense(t) for t in grads])
-    if not good:
+        plain = all([t.is_contiguous() for t in grads])
+        sizes = [t.numel() for t in grads]
+        ptrs = array("Q", [t.data_ptr() for t in grads])
+    except AttributeError:  # not all are tensors
         _refuse_list(grads, name)
-    sizes = [t.numel() for t in grads]
-    return (grads, sizes, types, array("Q", [t.data_ptr() for t in grads]), array("q", sizes), array("i", types))
+        raise
+    if len(devices) != 1 or -1 in devices or -1 in types or not (plain or all([_dense(t) for t in grads])):
+        _refuse_list(grads, name)
+    return grads, plain, devices, sizes, types, ptrs, array("q", sizes), array("i", types)
 
 
 def _refuse_list(grads, name):
@@ -247,9 +257,9 @@ def grad_norm(grads, workspace=None):
     """The 2-norm of all elements of the tensors (float16, bfloat16, float32, mixed) as a float32 scalar
     tensor; squares are summed in 64 bits, in a fixed order."""
     torch = _torch()
-    grads, _, _, ptrs, sizes, types = _list(grads, "grads")
+    grads, _, _, _, _, ptrs, sizes, types = _list(grads, "grads")
     like = grads[0]
-    norm = torch.empty((), dtype=torch.float32, device=like.device)
+    norm = like.new_empty((), dtype=torch.float32)
     lib = load()
     ws = _norm_workspace(lib, len(grads), like, workspace)
     with _on(like):
@@ -264,7 +274,7 @@ def clip_grad_norm(grads, max_norm, norm=None, out=None, workspace=None):
     None makes new ones.  Tensors that share elements with one that is written are refused."""
     torch = _torch()
     given_grads = grads
-    grads, numels, codes, ptrs, sizes, types = _list(grads, "grads")
+    grads, plain, devices, numels, codes, ptrs, sizes, types = _list(grads, "grads")
     like = grads[0]
     n = len(grads)
     if out is None:
@@ -276,16 +286,17 @@ def clip_grad_norm(grads, max_norm, norm=None, out=None, workspace=None):
         out = list(out)
         if len(out) != n:
             raise ValueError(f"{len(out)} outputs for {n} gradients")
-        out, onumels, ocodes, outs, _, _ = _list(out, "out")
-        if ocodes != codes or out[0].get_device() != like.get_device():
+        out, oplain, odevices, onumels, ocodes, outs, _, _ = _list(out, "out")
+        if ocodes != codes or odevices != devices:
             raise TypeError("out must have the types of grads, on their device")
-        if onumels != numels or not all([(o.is_contiguous() and t.is_contiguous()) or
-                                         (o.shape == t.shape and o.stride() == t.stride()) for o, t in zip(out, grads)]):
+        if onumels != numels or not (plain and oplain or all([
+                (o.is_contiguous() and t.is_contiguous()) or (o.shape == t.shape and o.stride() == t.stride())
+                for o, t in zip(out, grads)])):
             raise ValueError("out must be contiguous with grads' sizes, or have the shapes and strides of grads")
     lib = load()
     ws, given = None, norm
     if given is None:
-        norm = torch.empty((), dtype=torch.float32, device=like.device)
+        norm = like.new_empty((), dtype=torch.float32)
         ws = _norm_workspace(lib, n, like, workspace)
     elif not isinstance(given, torch.Tensor) or given.numel() != 1:
         raise ValueError("norm must be a tensor of one element")
@@ -302,4 +313,4 @@ def _norm_workspace(lib, n, like, workspace):
     torch = _torch()
     if workspace is not None:
         return _flat(workspace, torch.uint8, workspace.shape, like, "workspace")
-    return torch.empty(lib.grad_norm_workspace_bytes(n), dtype=torch.uint8, device=like.device)
+    return like.new_empty(lib.grad_norm_workspace_bytes(n), dtype=torch.uint8)

@@ -65,10 +65,15 @@ int check_groups(const char *fn, const int32_t *offsets, int32_t experts) {
     return SSG_OK;
 }
 
+bool grouped_dims(int64_t M, int64_t N, int64_t K) {
+    return M >= 0 && fits_int(M) && N >= 8 && K >= 8 && N % 8 == 0 && K % 8 == 0 && N < kSide && K < kSide &&
+           N * K * 2 < kGiB2;
+}
+
 int check_grouped(const char *fn, int32_t dtype, const int32_t *offsets, int32_t experts, int64_t M, int64_t N,
                   int64_t K) {
     if (!half_type(dtype)) return ssg::fail(SSG_EINVAL, "%s: dtype %d must be fp16 or bf16", fn, dtype);
-    if (M < 0 || !fits_int(M) || N < 8 || K < 8 || N % 8 || K % 8 || N >= kSide || K >= kSide || N * K * 2 >= kGiB2)
+    if (!grouped_dims(M, N, K))
         return ssg::fail(SSG_EINVAL,
                          "%s: M=%lld N=%lld K=%lld (need 0 <= M < 2^31, N and K positive multiples of 8 below 2^22, a "
                          "weight below 2 GiB)",
@@ -80,12 +85,15 @@ int check_grouped(const char *fn, int32_t dtype, const int32_t *offsets, int32_t
     return SSG_OK;
 }
 
-bool mx_dims(int64_t M, int64_t K) { return M >= 0 && fits_int(M) && K >= 1 && K < kSide; }
+// (the element kernels: eight values a thread, four pieces each for so many, 2^32 threads a launch)
+bool mx_dims(int64_t M, int64_t K) {
+    return M >= 0 && fits_int(M) && K >= 1 && K < kSide && M * (ssg::mxfp4_padded(K) / 8) < (int64_t(1) << 34) - 1024;
+}
 
 int check_mx(const char *fn, int64_t M, int64_t K) {
     if (!mx_dims(M, K))
-        return ssg::fail(SSG_EINVAL, "%s: M=%lld K=%lld (need 0 <= M < 2^31, 1 <= K < 2^22)", fn, (long long)M,
-                         (long long)K);
+        return ssg::fail(SSG_EINVAL, "%s: M=%lld K=%lld (need 0 <= M < 2^31, 1 <= K < 2^22, below 2^37 values)", fn,
+                         (long long)M, (long long)K);
     return SSG_OK;
 }
 
@@ -130,9 +138,14 @@ SSG_API int grouped_gemm(int32_t dtype, const void *x, int64_t ldx, const void *
     return launched(ssg::launch_grouped_fwd(a, hipStream_t(stream)), fn);
 }
 
+SSG_API int64_t grouped_gemm_backward_workspace_bytes(int32_t experts, int64_t M, int64_t N, int64_t K) {
+    if (experts < 1 || experts > 65535 || !grouped_dims(M, N, K)) return 0;
+    return ssg::grouped_slices_bytes(M, experts, N, K);
+}
+
 SSG_API int grouped_gemm_backward(int32_t dtype, const void *dy, int64_t lddy, const void *x, int64_t ldx,
                                   const void *w, const int32_t *offsets, int32_t experts, void *dx, int64_t lddx,
-                                  void *dw, int64_t M, int64_t N, int64_t K, void *stream) {
+                                  void *dw, int64_t M, int64_t N, int64_t K, void *ws, int64_t ws_bytes, void *stream) {
     const char *fn = "grouped_gemm_backward";
     int rc = check_grouped(fn, dtype, offsets, experts, M, N, K);
     if (rc) return rc;
@@ -141,12 +154,14 @@ SSG_API int grouped_gemm_backward(int32_t dtype, const void *dy, int64_t lddy, c
         if (dx && ((rc = check_rows(fn, "dx", dx, lddx, K)) || (rc = check_rows(fn, "w", w, K, K)))) return rc;
         if (dw && (rc = check_rows(fn, "x", x, ldx, K))) return rc;
     }
-    if (dw && (rc = check_rows(fn, "dw", dw, K, K))) return rc;
+    if (dw && ((rc = check_rows(fn, "dw", dw, K, K)) ||
+               (rc = check_ws(fn, ws, ws_bytes, grouped_gemm_backward_workspace_bytes(experts, M, N, K)))))
+        return rc;
     if (!dw && (!dx || M == 0)) return ok();
     if ((rc = check_device())) return rc;
     ssg::Grouped a{};
     a.dtype = dtype, a.x = x, a.w = w, a.dy = dy, a.offsets = offsets, a.experts = experts;
-    a.ldx = ldx, a.lddy = lddy, a.dx = dx, a.lddx = lddx, a.dw = dw, a.M = M, a.N = N, a.K = K;
+    a.ldx = ldx, a.lddy = lddy, a.dx = dx, a.lddx = lddx, a.dw = dw, a.ws = ws, a.M = M, a.N = N, a.K = K;
     return launched(ssg::launch_grouped_bwd(a, hipStream_t(stream)), fn);
 }
 

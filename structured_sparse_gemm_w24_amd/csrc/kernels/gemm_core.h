@@ -184,11 +184,11 @@ typedef uint32_t u32x8 __attribute__((ext_vector_type(8)));
 
 // Stores the first `room` elements of OB bytes (all 16 / OB, or fewer at a row's end; none
 // below 1) at any element alignment.
-template <int OB, bool NTS>
-__device__ __forceinline__ void store_piece(uint8_t *p, u32x4 v, int room) {
+template <int OB>
+__device__ __forceinline__ void store_piece(uint8_t *p, u32x4 v, int room, bool stream) {
     typedef u32x4 Any __attribute__((aligned(2)));
     if (room >= 16 / OB) {
-        if constexpr (NTS) __builtin_nontemporal_store(v, reinterpret_cast<Any *>(p));
+        if (stream) __builtin_nontemporal_store(v, reinterpret_cast<Any *>(p));
         else *reinterpret_cast<Any *>(p) = v;
         return;
     }
@@ -954,7 +954,7 @@ gemm_kernel(const uint8_t *__restrict__ A, const uint8_t *__restrict__ Wv, const
                     const int n = nw + ch * (16 / OB);
                     const u32x4 v = *reinterpret_cast<const u32x4 *>(ew + e * EWAVE + row * EROW + ch * 16);
                     if constexpr (Extra::kPlace) {
-                        store_piece<OB, CF::NTS>(Cb + (int64_t(m) * extra.ldc + n) * OB, v, m < M ? N - n : 0);
+                        store_piece<OB>(Cb + (int64_t(m) * extra.ldc + n) * OB, v, m < M ? N - n : 0, CF::NTS && extra.stream);
                     } else {
                         if (m < M && n < N) store16<CF::NTS>(Cb + (int64_t(m) * N + n) * OB, v);
                     }

@@ -8,7 +8,10 @@
 // workgroup's tile (group_place.h).  dx reads w[e] as it lies, summed along its
 // rows, and dw both dy and x, through transposing LDS reads; a group's last rows
 // end its buffer, so that the rows of the next expert never enter a sum.  dw's
-// groups have K loops of different lengths in one launch.
+// groups have K loops of different lengths in one launch; with few tiles of many rows
+// each group's rows are split over several workgroups, whose fp32 sums a second launch
+// adds in order.
+#include "elem.h"
 #include "gemm_core.h"
 #include "gemm_tiles.h"
 #include "group_place.h"
@@ -21,7 +24,7 @@ namespace {
 // forward (TW false) and dx (TW true): tiles of a group's rows.
 template <bool TW>
 struct GroupRows {
-    static constexpr bool kAfter = false, kEpilogue = false, kTransA = false, kTransW = TW, kPlace = true;
+    static constexpr bool kAfter = false, kEpilogue = false, kTransA = false, kTransW = TW, kPlace = true, stream = true;
     const int32_t *offsets;
     int groups;
     int64_t a_row, ldc, w_bytes;  // bytes between A's rows, elements between C's, bytes of a weight
@@ -41,11 +44,13 @@ struct GroupRows {
     }
 };
 
-// dw: every tile of every expert; M and N are the weight's sides.
+// dw: every tile of every expert; M and N are the weight's sides.  splits > 1: the launch repeats for
+// each share of a group's K stages and writes its sums, fp32, to slices of all experts' weights.
+template <int OB>
 struct GroupWeights {
-    static constexpr bool kAfter = false, kEpilogue = false, kTransA = true, kTransW = true, kPlace = true;
+    static constexpr bool kAfter = false, kEpilogue = false, kTransA = true, kTransW = true, kPlace = true, stream = true;
     const int32_t *offsets;
-    int groups, rows;
+    int groups, rows, splits;
     int64_t a_row, ldc;  // (a_row: unused)
     int lda, ldw;
     int rows_a, rows_w;        // (unused: the stages' buffers take bytes_a and bytes_w)
@@ -56,27 +61,49 @@ struct GroupWeights {
                                           int &stages, int &n0) {
         const int tiles_n = (N + BN - 1) / BN, each = (M + BM - 1) / BM * tiles_n;
         // (every expert's tiles are spread over the XCDs: a popular expert is no XCD's alone)
-        const int g = blockIdx.x / each, j = xcd_remap(blockIdx.x % each, each);
+        const int share = blockIdx.x / (each * groups), tile = blockIdx.x - share * (each * groups);
+        const int g = tile / each, j = xcd_remap(tile % each, each);
         int lo, hi;
         group::rows_of(offsets, groups, rows, g, lo, hi);
+        const int all = (hi - lo + 63) / 64, per = (all + splits - 1) / splits, from = min(share * per, all);
+        stages = min(per, all - from);
+        lo += from * 64;
         const int m0 = j / tiles_n * BM;
         n0 = j % tiles_n * BN;
         A += (int64_t(lo) * lda + m0) * 2;
         W += int64_t(lo) * ldw * 2;
-        C = static_cast<uint16_t *>(C) + (int64_t(g) * M + m0) * ldc;
+        C = static_cast<uint8_t *>(C) + ((int64_t(share) * groups + g) * M + m0) * ldc * OB;
         bytes_a = (int64_t(hi - lo - 1) * lda + M - m0) * 2;
         bytes_w = (int64_t(hi - lo - 1) * ldw + N) * 2;
         M -= m0;
-        stages = (hi - lo + 63) / 64;
         return true;
     }
 };
 
-template <int KIND, class CF, class Extra>
+// Sums the splits' slices in order: eight weights a thread.
+template <class T>
+__global__ void __launch_bounds__(256)
+group_sum_kernel(const float *__restrict__ part, int splits, int64_t size, T *__restrict__ out) {
+    const int64_t i = (int64_t(blockIdx.x) * 256 + threadIdx.x) * 8;
+    if (i >= size) return;
+    float v[8] = {};
+#pragma unroll 4
+    for (int s = 0; s < splits; ++s) {
+        const floatx4 a = *reinterpret_cast<const floatx4 *>(part + s * size + i);
+        const floatx4 b = *reinterpret_cast<const floatx4 *>(part + s * size + i + 4);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[j] += a[j], v[4 + j] += b[j];
+    }
+    typename Elem<T>::Vec t;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) t[j] = T(v[j]);
+    __builtin_nontemporal_store(__builtin_bit_cast(u32x4, t), reinterpret_cast<u32x4 *>(out + i));
+}
+
+template <int KIND, class CF, class Extra, int EPI = KIND == DENSE_F16 ? EPI_F16 : EPI_BF16>
 hipError_t launch_cfg(const void *A, const void *W, void *C, const Extra &ex, int64_t blocks, int M, int N, int K,
                       hipStream_t st) {
     using LY = Layout<KIND, CF>;
-    constexpr int EPI = KIND == DENSE_F16 ? EPI_F16 : EPI_BF16;
     hipLaunchKernelGGL((gemm_kernel<KIND, EPI, CF, Extra>), dim3(unsigned(blocks)), dim3(LY::NT), 0, st,
                        static_cast<const uint8_t *>(A), static_cast<const uint8_t *>(W), nullptr, nullptr, nullptr, C,
                        M, N, K, (K + 63) / 64, ex);
@@ -123,12 +150,28 @@ int rows_tile(int64_t M, int64_t experts, int64_t N, int64_t K) {
     if constexpr (TW) return cheapest(kDxTiles, stages, count);
     else return cheapest(kFwdTiles, stages, count);
 }
-int weights_tile(int64_t M, int64_t experts, int64_t N, int64_t K) {
-    auto count = [&](int bm, int bn) {
-        return double(experts) * double((N + bm - 1) / bm) * double((K + bn - 1) / bn);
-    };
-    const double stages = double(M) / double(experts) / 64.0 + 0.5;
-    return cheapest(kDwTiles, stages < 1.0 ? 1.0 : stages, count);
+// dw's tile and splits: the least of the tiles' cost, with each group's stages in up to 32 shares of
+// four at least, and for more than one share the second launch and the slices' way through memory
+// (16384 rows of one expert, 1024 x 1024: 113 us in one share; below 256 MiB of slices).
+struct WeightsPlan {
+    int tile, splits;
+};
+WeightsPlan weights_plan(int64_t M, int64_t experts, int64_t N, int64_t K) {
+    const double even = double(M) / double(experts) / 64.0 + 0.5, stages = even < 1.0 ? 1.0 : even;
+    const double slice = double(experts) * double(N) * double(K) * 4.0;
+    WeightsPlan best{0, 1};
+    float least = 0.0f;
+    for (int p = 1; p <= 32; p *= 2) {
+        if (p > 1 && (stages < 4.0 * p || slice * p > double(1 << 28))) break;
+        auto count = [&](int bm, int bn) {
+            return double(p) * double(experts) * double((N + bm - 1) / bm) * double((K + bn - 1) / bn);
+        };
+        const int t = cheapest(kDwTiles, stages / p, count);
+        float us = kDwTiles[t].us(count(kDwTiles[t].bm, kDwTiles[t].bn), stages / p);
+        if (p > 1) us += 4.0f + float(slice * (2 * p + 0.5) / 5.0e6);
+        if (p == 1 || us < least) best = {t, p}, least = us;
+    }
+    return best;
 }
 
 template <int KIND, bool TW>
@@ -158,26 +201,41 @@ hipError_t rows(const Grouped &a, const void *A, int64_t lda, void *C, int64_t l
 #undef SSG_TILE
 }
 
-template <int KIND, class CF>
-hipError_t weights_cfg(const Grouped &a, hipStream_t st) {
+template <int KIND, class CF, bool SPLIT>
+hipError_t weights_cfg(const Grouped &a, int splits, hipStream_t st) {
     using LY = Layout<KIND, CF>;
-    GroupWeights ex{};
-    ex.offsets = a.offsets, ex.groups = a.experts, ex.rows = int(a.M), ex.ldc = a.K;
+    GroupWeights<SPLIT ? 4 : 2> ex{};
+    ex.offsets = a.offsets, ex.groups = a.experts, ex.rows = int(a.M), ex.splits = splits, ex.ldc = a.K;
     ex.lda = int(a.lddy), ex.ldw = int(a.ldx);
-    const int64_t blocks = a.experts * ((a.N + LY::BM - 1) / LY::BM) * ((a.K + LY::BN - 1) / LY::BN);
-    return launch_cfg<KIND, CF>(a.dy, a.x, a.dw, ex, blocks, int(a.N), int(a.K), 0, st);
+    const int64_t blocks = splits * a.experts * ((a.N + LY::BM - 1) / LY::BM) * ((a.K + LY::BN - 1) / LY::BN);
+    if constexpr (SPLIT)
+        return launch_cfg<KIND, CF, GroupWeights<4>, EPI_F32>(a.dy, a.x, a.ws, ex, blocks, int(a.N), int(a.K), 0, st);
+    else return launch_cfg<KIND, CF>(a.dy, a.x, a.dw, ex, blocks, int(a.N), int(a.K), 0, st);
+}
+
+template <int KIND, bool SPLIT>
+hipError_t weights_any(const Grouped &a, const WeightsPlan &pl, hipStream_t st) {
+    switch (pl.tile) {
+        case 0: return weights_cfg<KIND, Cfg32x64, SPLIT>(a, pl.splits, st);
+        case 1: return weights_cfg<KIND, Cfg64x128P, SPLIT>(a, pl.splits, st);
+        case 2: return weights_cfg<KIND, Cfg<2, 2, 2, 2, 2, 8, true, false>, SPLIT>(a, pl.splits, st);
+        case 3: return weights_cfg<KIND, Cfg128x128P, SPLIT>(a, pl.splits, st);
+        case 4: return weights_cfg<KIND, Cfg256x128P, SPLIT>(a, pl.splits, st);
+        default: return weights_cfg<KIND, CfgBigDense<true>, SPLIT>(a, pl.splits, st);
+    }
 }
 
 template <int KIND>
 hipError_t weights(const Grouped &a, hipStream_t st) {
-    switch (weights_tile(a.M, a.experts, a.N, a.K)) {
-        case 0: return weights_cfg<KIND, Cfg32x64>(a, st);
-        case 1: return weights_cfg<KIND, Cfg64x128P>(a, st);
-        case 2: return weights_cfg<KIND, Cfg<2, 2, 2, 2, 2, 8, true, false>>(a, st);
-        case 3: return weights_cfg<KIND, Cfg128x128P>(a, st);
-        case 4: return weights_cfg<KIND, Cfg256x128P>(a, st);
-        default: return weights_cfg<KIND, CfgBigDense<true>>(a, st);
-    }
+    const WeightsPlan pl = weights_plan(a.M, a.experts, a.N, a.K);
+    if (pl.splits == 1) return weights_any<KIND, false>(a, pl, st);
+    hipError_t e = weights_any<KIND, true>(a, pl, st);
+    if (e != hipSuccess) return e;
+    using T = typename std::conditional<KIND == DENSE_F16, _Float16, __bf16>::type;
+    const int64_t size = a.experts * a.N * a.K;  // (a multiple of 8)
+    hipLaunchKernelGGL(group_sum_kernel<T>, dim3(unsigned((size / 8 + 255) / 256)), dim3(256), 0, st,
+                       static_cast<const float *>(a.ws), pl.splits, size, static_cast<T *>(a.dw));
+    return hipGetLastError();
 }
 
 template <int KIND>
@@ -193,12 +251,18 @@ hipError_t backward(const Grouped &a, hipStream_t st) {
 
 int64_t grouped_blocks(int64_t M, int64_t experts, int64_t N, int64_t K) {
     auto of_rows = [&](const TileCost &t, int64_t n) { return group_tiles(M, experts, t.bm, (n + t.bn - 1) / t.bn); };
-    const TileCost &w = kDwTiles[weights_tile(M, experts, N, K)];
+    const WeightsPlan pl = weights_plan(M, experts, N, K);
+    const TileCost &w = kDwTiles[pl.tile];
     const int64_t fwd = of_rows(kFwdTiles[rows_tile<false>(M, experts, N, K)], N);
     const int64_t dx = of_rows(kDxTiles[rows_tile<true>(M, experts, K, N)], K);
-    const int64_t dw = experts * ((N + w.bm - 1) / w.bm) * ((K + w.bn - 1) / w.bn);
+    const int64_t dw = pl.splits * experts * ((N + w.bm - 1) / w.bm) * ((K + w.bn - 1) / w.bn);
     const int64_t most = fwd > dx ? fwd : dx;
     return most > dw ? most : dw;
+}
+
+int64_t grouped_slices_bytes(int64_t M, int64_t experts, int64_t N, int64_t K) {
+    const int splits = weights_plan(M, experts, N, K).splits;
+    return splits > 1 ? splits * experts * N * K * 4 : 0;
 }
 
 hipError_t launch_grouped_fwd(const Grouped &a, hipStream_t st) {

@@ -172,10 +172,13 @@ struct Grouped {
     int experts;
     int64_t ldx, lddy, ldo, lddx;
     void *out, *dx, *dw;  // backward: dx or dw may be null
+    void *ws;             // dw: grouped_slices_bytes()
     int64_t M, N, K;
 };
 hipError_t launch_grouped_fwd(const Grouped &a, hipStream_t st);
 hipError_t launch_grouped_bwd(const Grouped &a, hipStream_t st);
+// fp32 slices of dw's split sums (0: not split)
+int64_t grouped_slices_bytes(int64_t M, int64_t experts, int64_t N, int64_t K);
 // workgroups of the largest of the launches of these sizes
 int64_t grouped_blocks(int64_t M, int64_t experts, int64_t N, int64_t K);
 

@@ -48,28 +48,48 @@ __device__ __forceinline__ uint32_t codes_of(const float (&f)[8], uint32_t byte)
     return c;
 }
 
-// Eight values from column c on, zeros past the row's end.
-template <class T, bool TAIL>
-__device__ __forceinline__ void load8(const T *row, int64_t c, int64_t n, float (&f)[8]) {
-    constexpr int V = Elem<T>::V;
-#pragma unroll
-    for (int i = 0; i < 8; i += V) {
-        const typename Elem<T>::Vec v = settle<T, TAIL>(fetch_raw<T, TAIL>(row, c + i, n), c + i, n);
-#pragma unroll
-        for (int j = 0; j < V; ++j) f[i + j] = float(v[j]);
-    }
+// The piece `at` behind the first one of a workgroup, which is piece c0 of row m0 (a 64-bit division
+// for each piece was a third of the time: 8192 x 4096 fp16 18.8 us).
+struct Place {
+    int64_t m;
+    int c;
+};
+__device__ __forceinline__ Place piece_at(int64_t m0, uint32_t c0, uint32_t at, uint32_t pieces) {
+    const uint32_t c = c0 + at, q = c / pieces;
+    return {m0 + q, int(c - q * pieces) * 8};
 }
 
-// Eight values a thread, so four threads a block and sixteen a word of four scales.
-template <class T, bool TAIL>
+// Pieces of eight values: four threads share a block, sixteen a word of four scales.  Each thread takes
+// U of them, 256 apart, and has all their loads under way before the first is used.
+template <class T, bool TAIL, int U>
 __global__ void __launch_bounds__(256)
 mx_quantize_kernel(const T *__restrict__ x, int64_t ldx, uint32_t *__restrict__ codes, uint32_t *__restrict__ scales,
                    int64_t M, int64_t K, int pieces) {  // pieces of a row: a multiple of 16
-    const int64_t all = M * pieces;
-    for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < all; i += int64_t(gridDim.x) * 256) {
-        const int64_t m = i / pieces, c = i % pieces * 8;
+    constexpr int V = Elem<T>::V;
+    const int64_t all = M * pieces, first = int64_t(blockIdx.x) * (256 * U), m0 = first / pieces;
+    const uint32_t c0 = uint32_t(first - m0 * pieces);
+    typename Elem<T>::Vec v[U][8 / V];
+    int64_t col[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const int at = u * 256 + threadIdx.x;
+        if (first + at >= all) break;
+        const Place p = piece_at(m0, c0, uint32_t(at), uint32_t(pieces));
+        col[u] = p.c;
+#pragma unroll
+        for (int j = 0; j < 8 / V; ++j) v[u][j] = fetch_raw<T, TAIL>(x + p.m * ldx, p.c + j * V, K);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const int64_t i = first + u * 256 + threadIdx.x;
+        if (i >= all) return;  // (a row's pieces are a multiple of 16: whole groups of lanes leave)
         float f[8];
-        load8<T, TAIL>(x + m * ldx, c, K, f);
+#pragma unroll
+        for (int j = 0; j < 8 / V; ++j) {
+            const typename Elem<T>::Vec w = settle<T, TAIL>(v[u][j], col[u] + j * V, K);
+#pragma unroll
+            for (int q = 0; q < V; ++q) f[j * V + q] = float(w[q]);
+        }
         uint32_t top = 0;
 #pragma unroll
         for (int j = 0; j < 8; ++j) top = max(top, magnitude_bits(f[j]));
@@ -84,14 +104,26 @@ mx_quantize_kernel(const T *__restrict__ x, int64_t ldx, uint32_t *__restrict__ 
     }
 }
 
-template <class T, bool TAIL>
+template <class T, bool TAIL, int U>
 __global__ void __launch_bounds__(256)
 mx_dequantize_kernel(const uint32_t *__restrict__ codes, const uint8_t *__restrict__ scales, T *__restrict__ out,
                      int64_t ldo, int64_t M, int64_t K, int pieces) {
-    const int64_t all = M * pieces;
-    for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < all; i += int64_t(gridDim.x) * 256) {
-        const int64_t m = i / pieces, c = i % pieces * 8;
-        const uint32_t b = scales[i >> 2], v = codes[i];
+    const int64_t all = M * pieces, first = int64_t(blockIdx.x) * (256 * U), m0 = first / pieces;
+    const uint32_t c0 = uint32_t(first - m0 * pieces);
+    uint32_t word[U], byte[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const int64_t i = first + u * 256 + threadIdx.x;
+        if (i >= all) break;
+        byte[u] = scales[i >> 2], word[u] = codes[i];
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const int at = u * 256 + threadIdx.x;
+        if (first + at >= all) return;
+        const Place p = piece_at(m0, c0, uint32_t(at), uint32_t(pieces));
+        const int64_t m = p.m, c = p.c;
+        const uint32_t b = byte[u], v = word[u];
         const float s = __builtin_bit_cast(float, b == 0 ? 0x00400000u : b == 255 ? 0x7fc00000u : b << 23);
         typedef float f2 __attribute__((ext_vector_type(2)));
         const f2 p0 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(v, 1.0f, 0);
@@ -118,6 +150,10 @@ struct MxProduct {
     int groups;
     const uint8_t *sa, *sw;
     int64_t a_row, ldc;  // bytes of a packed row; elements between C's rows
+    // C's rows at any 2 or 4 bytes leave parts of cache lines in every piece, which nontemporal stores
+    // send to memory one by one (7648 x 3001 x 533 26.6 us, cached stores 22.9; but 3008 wide, 18.9 and
+    // 21.6, and 16079 x 1388 x 2757, whose rows are 8 bytes off, 47.1 and 53.5)
+    bool stream;
 
     template <class CF, int BM, int BN>
     __device__ __forceinline__ bool place(const uint8_t *&A, const uint8_t *&W, void *&C, int &M, int N, int K, int &,
@@ -149,7 +185,7 @@ template <int EPI, class CF, bool GROUPED>
 hipError_t gemm_cfg(const Mxfp4Gemm &g, int K, hipStream_t st) {
     using LY = Layout<MX_F4, CF>;
     constexpr int OB = EPI == EPI_F32 ? 4 : 2;
-    const MxProduct<GROUPED, OB> ex{g.offsets, g.experts, g.a_scales, g.w_scales, K / 2, g.ldo};
+    const MxProduct<GROUPED, OB> ex{g.offsets, g.experts, g.a_scales, g.w_scales, K / 2, g.ldo, g.ldo * OB % 8 == 0 && reinterpret_cast<uintptr_t>(g.out) % 8 == 0};
     const int64_t tiles_n = (g.N + LY::BN - 1) / LY::BN;
     const int64_t blocks =
         GROUPED ? group_tiles(g.M, g.experts, LY::BM, tiles_n) : (g.M + LY::BM - 1) / LY::BM * tiles_n;
@@ -197,16 +233,19 @@ hipError_t gemm_epi(const Mxfp4Gemm &g, hipStream_t st) {
     return g.offsets ? gemm_any<EPI, true>(g, st) : gemm_any<EPI, false>(g, st);
 }
 
+// Pieces a thread: four once that still leaves eight workgroups a CU.
+bool many_pieces(int64_t all) { return all >= int64_t(4 * 256) * 8 * 256; }
+
 template <class T>
 hipError_t quantize(const void *x, int64_t ldx, uint8_t *codes, uint8_t *scales, int64_t M, int64_t K,
                     hipStream_t st) {
     const int pieces = int(mxfp4_padded(K) / 8);
-    const int64_t blocks = (M * pieces + 255) / 256;
-    const dim3 grid(unsigned(blocks < 16384 ? blocks : 16384));
-    const bool whole = K % Elem<T>::V == 0;
-    auto k = whole ? mx_quantize_kernel<T, false> : mx_quantize_kernel<T, true>;
-    hipLaunchKernelGGL(k, grid, dim3(256), 0, st, static_cast<const T *>(x), ldx, reinterpret_cast<uint32_t *>(codes),
-                       reinterpret_cast<uint32_t *>(scales), M, K, pieces);
+    const bool whole = K % Elem<T>::V == 0, many = many_pieces(M * pieces);
+    const int64_t each = many ? 1024 : 256;
+    auto k = whole ? (many ? mx_quantize_kernel<T, false, 4> : mx_quantize_kernel<T, false, 1>)
+                   : (many ? mx_quantize_kernel<T, true, 4> : mx_quantize_kernel<T, true, 1>);
+    hipLaunchKernelGGL(k, dim3(unsigned((M * pieces + each - 1) / each)), dim3(256), 0, st, static_cast<const T *>(x),
+                       ldx, reinterpret_cast<uint32_t *>(codes), reinterpret_cast<uint32_t *>(scales), M, K, pieces);
     return hipGetLastError();
 }
 
@@ -214,12 +253,12 @@ template <class T>
 hipError_t dequantize(const uint8_t *codes, const uint8_t *scales, void *out, int64_t ldo, int64_t M, int64_t K,
                       hipStream_t st) {
     const int pieces = int(mxfp4_padded(K) / 8);
-    const int64_t blocks = (M * pieces + 255) / 256;
-    const dim3 grid(unsigned(blocks < 16384 ? blocks : 16384));
-    const bool whole = K % Elem<T>::V == 0;
-    auto k = whole ? mx_dequantize_kernel<T, false> : mx_dequantize_kernel<T, true>;
-    hipLaunchKernelGGL(k, grid, dim3(256), 0, st, reinterpret_cast<const uint32_t *>(codes), scales,
-                       static_cast<T *>(out), ldo, M, K, pieces);
+    const bool whole = K % Elem<T>::V == 0, many = many_pieces(M * pieces);
+    const int64_t each = many ? 1024 : 256;
+    auto k = whole ? (many ? mx_dequantize_kernel<T, false, 4> : mx_dequantize_kernel<T, false, 1>)
+                   : (many ? mx_dequantize_kernel<T, true, 4> : mx_dequantize_kernel<T, true, 1>);
+    hipLaunchKernelGGL(k, dim3(unsigned((M * pieces + each - 1) / each)), dim3(256), 0, st,
+                       reinterpret_cast<const uint32_t *>(codes), scales, static_cast<T *>(out), ldo, M, K, pieces);
     return hipGetLastError();
 }
 

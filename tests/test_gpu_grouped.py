@@ -174,3 +174,24 @@ def test_no_rows(lib, gpu):
     dx, dw = lib.grouped_gemm_backward(dy[:0].cuda(), x[:0].cuda(), w.cuda(), offsets,
                                        dw_out=torch.ones(2, 64, 72, dtype=torch.float16, device="cuda"))
     assert dx.shape == (0, 72) and not bool(dw.any())
+
+
+@pytest.mark.parametrize("lengths,n,k", [([9000], 64, 136), ([0, 3000, 1, 5000], 72, 80), ([20000, 300], 128, 256)])
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+def test_weight_gradient_of_many_rows(lib, gpu, lengths, n, k, dt):
+    """Few tiles, long sums: the rows are split and the slices added."""
+    import torch
+    m, e = sum(lengths), len(lengths)
+    need = lib.load().grouped_gemm_backward_workspace_bytes(e, m, n, k)
+    assert need > 0 and need % (e * n * k * 4) == 0
+    x, dy, w, offsets = _case(lengths, 0, 0, n, k, dt, 7)
+    args = [t.cuda() for t in (dy, x, w, offsets)]
+    _, dw = lib.grouped_gemm_backward(*args, x_grad=False)
+    o = offsets.tolist()
+    for i in range(e):
+        _close(dw[i], dy[o[i]:o[i + 1]].double().t(), x[o[i]:o[i + 1]].double(), dt)
+    again = lib.grouped_gemm_backward(*args, x_grad=False, workspace=torch.full((need,), 255, dtype=torch.uint8,
+                                                                               device="cuda"))[1]
+    assert torch.equal(dw, again)
+    with pytest.raises(lib.SsgError, match="needed"):
+        lib.grouped_gemm_backward(*args, workspace=torch.empty(need - 16, dtype=torch.uint8, device="cuda"))
