@@ -8,8 +8,9 @@ and the update:
     t  -> layer_norm -> y -> fc1 (2:4 + adapters) -> gelu -> fc2 (2:4 + adapters) -> o
     s = t + o -> layer_norm -> z -> cross entropy against the vocabulary `head`
 
-and back.  The targets come from a teacher whose adapters differ, so the loss has
-somewhere to go.  Afterwards every adapter serves single tokens of many requests.
+and back, with the gradients of all parameters clipped together.  The targets come
+from a teacher whose adapters differ, so the loss has somewhere to go.  Afterwards
+every adapter serves single tokens of many requests.
 
     python examples/tune_adapters.py [--steps 60]
 """
@@ -84,7 +85,7 @@ class Block:
         return [self.a1.down, self.a1.up, self.a2.down, self.a2.up, *self.norms]
 
 
-def tune(steps=60, tokens=512, seed=0, lr=3e-3, loss_scale=1024.0, verbose=True):
+def tune(steps=60, tokens=512, seed=0, lr=3e-3, loss_scale=1024.0, verbose=True, max_norm=1.0):
     """Returns the mean loss of every step, and the tuned block."""
     g = torch.Generator().manual_seed(seed)
     weights = sparse_weight(g, D, F), sparse_weight(g, F, D)
@@ -106,7 +107,9 @@ def tune(steps=60, tokens=512, seed=0, lr=3e-3, loss_scale=1024.0, verbose=True)
         z, saved = block.forward(t, index)
         loss, lse = ssg.linear_cross_entropy(z, head, target)
         dz, _ = ssg.linear_cross_entropy_backward(dloss, z, head, target, lse)
-        for p, grad, (m1, m2) in zip(block.parameters(), block.backward(dz, saved, index), moments):
+        grads = block.backward(dz, saved, index)
+        ssg.clip_grad_norm(grads, max_norm * loss_scale, out=grads)
+        for p, grad, (m1, m2) in zip(block.parameters(), grads, moments):
             grad = grad.float() / loss_scale
             m1.mul_(0.9).add_(grad, alpha=0.1)
             m2.mul_(0.99).addcmul_(grad, grad, value=0.01)
