@@ -54,9 +54,10 @@ struct Tile {
     int group, row, rows, tile_n;  // group < 0: none; row: its first row, rows: of the group from there on
 };
 
-// The workgroup's tile of BM rows (and of tiles_n columns), GM tile rows of a group at a time.
+// The `block`-th tile of BM rows (and of tiles_n columns), GM tile rows of a group at a time.
 template <int BM>
-__device__ __forceinline__ Tile find_tile(const int32_t *offsets, int groups, int rows, int tiles_n, int GM) {
+__device__ __forceinline__ Tile find_tile(int block, const int32_t *offsets, int groups, int rows, int tiles_n,
+                                          int GM) {
     const int first = clamped(offsets[0], rows);
     int reached = first, total = 0, lo, hi, sum = 0, count = 0;
     for (int g0 = 0; g0 < groups; g0 += 64) {
@@ -66,8 +67,8 @@ __device__ __forceinline__ Tile find_tile(const int32_t *offsets, int groups, in
         total = __builtin_amdgcn_readlane(sum, 63);
     }
     Tile t{-1, 0, 0, 0};
-    if (int(blockIdx.x) >= total * tiles_n) return t;
-    const int b = xcd_remap(blockIdx.x, total * tiles_n);
+    if (block >= total * tiles_n) return t;
+    const int b = xcd_remap(block, total * tiles_n);
     int g0 = 0;
     if (groups > 64) {
         reached = first, total = 0;

@@ -31,9 +31,9 @@ struct GroupRows {
     int ldw, rows_w;              // (TW)
 
     template <class CF, int BM, int BN>
-    __device__ __forceinline__ bool place(const uint8_t *&A, const uint8_t *&W, void *&C, int &M, int N, int, int &,
-                                          int &n0) const {
-        const group::Tile t = group::find_tile<BM>(offsets, groups, M, (N + BN - 1) / BN, CF::GM);
+    __device__ __forceinline__ bool place(int block, const uint8_t *&A, const uint8_t *&W, void *&C, int &M, int N,
+                                          int, int &, int &n0) const {
+        const group::Tile t = group::find_tile<BM>(block, offsets, groups, M, (N + BN - 1) / BN, CF::GM);
         if (t.group < 0) return false;
         A += t.row * a_row;
         W += t.group * w_bytes;
@@ -57,11 +57,11 @@ struct GroupWeights {
     int64_t bytes_a, bytes_w;  // of the group's rows, from the tile's first column on
 
     template <class CF, int BM, int BN>
-    __device__ __forceinline__ bool place(const uint8_t *&A, const uint8_t *&W, void *&C, int &M, int N, int,
-                                          int &stages, int &n0) {
+    __device__ __forceinline__ bool place(int block, const uint8_t *&A, const uint8_t *&W, void *&C, int &M, int N,
+                                          int, int &stages, int &n0) {
         const int tiles_n = (N + BN - 1) / BN, each = (M + BM - 1) / BM * tiles_n;
         // (every expert's tiles are spread over the XCDs: a popular expert is no XCD's alone)
-        const int share = blockIdx.x / (each * groups), tile = blockIdx.x - share * (each * groups);
+        const int share = block / (each * groups), tile = block - share * (each * groups);
         const int g = tile / each, j = xcd_remap(tile % each, each);
         int lo, hi;
         group::rows_of(offsets, groups, rows, g, lo, hi);
@@ -174,6 +174,34 @@ WeightsPlan weights_plan(int64_t M, int64_t experts, int64_t N, int64_t K) {
     return best;
 }
 
+// The tile of a launch of both, or -1: two launches.  A tile of the joint launch costs what it does in
+// either; together they take nine tenths of the longest tile or of the CUs' share, whichever is more.
+constexpr struct {
+    TileCost dx, dw;
+} kBothTiles[] = {{kDxTiles[0], kDwTiles[0]}, {kDxTiles[2], kDwTiles[1]}, {kDxTiles[3], kDwTiles[3]}};
+int both_tile(int64_t M, int64_t experts, int64_t N, int64_t K) {
+    const WeightsPlan pl = weights_plan(M, experts, N, K);
+    if (pl.splits > 1) return -1;
+    const double sx = double((N + 63) / 64), even = double(M) / double(experts) / 64.0 + 0.5, sw = even < 1.0 ? 1.0 : even;
+    auto count_x = [&](int bm, int bn) { return group_tile_rows(M, experts, bm) * double((K + bn - 1) / bn); };
+    auto count_w = [&](int bm, int bn) {
+        return double(experts) * double((N + bm - 1) / bm) * double((K + bn - 1) / bn);
+    };
+    auto us = [&](const TileCost &t, double stages, auto count) { return t.us(count(t.bm, t.bn), stages); };
+    float least = us(kDxTiles[rows_tile<true>(M, experts, K, N)], sx, count_x) + us(kDwTiles[pl.tile], sw, count_w);
+    int best = -1;
+    for (int i = 0; i < 3; ++i) {
+        const TileCost &x = kBothTiles[i].dx, &w = kBothTiles[i].dw;
+        const double total = (count_x(x.bm, x.bn) * (x.tile / x.per_cu + sx * x.stage) +
+                              count_w(w.bm, w.bn) * (w.tile / w.per_cu + sw * w.stage)) / 256.0;
+        double longest = x.tile + sx * x.stage;
+        if (w.tile + sw * w.stage > longest) longest = w.tile + sw * w.stage;
+        const float t = 5.0f + 0.9f * float(total > longest ? total : longest);
+        if (t < least) best = i, least = t;
+    }
+    return best;
+}
+
 template <int KIND, bool TW>
 hipError_t rows(const Grouped &a, const void *A, int64_t lda, void *C, int64_t ldc, int N, int K, hipStream_t st) {
 #define SSG_TILE(i, CF) \
@@ -238,8 +266,48 @@ hipError_t weights(const Grouped &a, hipStream_t st) {
     return hipGetLastError();
 }
 
+// dx and dw in one launch: the first `first` workgroups are dx's tiles, the others dw's.  Small calls
+// are two chains of latencies, which then run side by side, and one launch (1531 rows of 6 experts,
+// 776 x 1000: 22.0 us in two launches, 17.9 in one; 307 rows of one, 176 x 2736: 12.5 and 7.1); the large
+// ones are faster apart, each on its own tile (16384 rows of 16, 4096 x 1024: 343 and 353).  Over 100 calls
+// of random sizes two launches take 1.37 times the better of both, and both_tile()'s choice 1.014.
+template <int KIND, class CF>
+__global__ void __launch_bounds__(CF::WM *CF::WN * 64 * (CF::PROD ? 2 : 1))
+group_both_kernel(const uint8_t *__restrict__ dy, const uint8_t *__restrict__ x, const uint8_t *__restrict__ w, void *dx,
+                  void *dw, int M, int N, int K, int first, GroupRows<true> of_rows, GroupWeights<2> of_weights) {
+    constexpr int EPI = KIND == DENSE_F16 ? EPI_F16 : EPI_BF16;
+    __shared__ __attribute__((aligned(1024))) uint8_t smem[Slabs<KIND, EPI, CF>::SMEM];
+    if (int(blockIdx.x) < first)
+        gemm_tile<KIND, EPI, CF>(dy, w, dx, M, K, N, (N + 63) / 64, of_rows, smem, blockIdx.x);
+    else gemm_tile<KIND, EPI, CF>(dy, x, dw, N, K, 0, 0, of_weights, smem, blockIdx.x - first);
+}
+
+template <int KIND, class CF>
+hipError_t both_cfg(const Grouped &a, hipStream_t st) {
+    using LY = Layout<KIND, CF>;
+    const int N = int(a.N), K = int(a.K);
+    const GroupRows<true> r{a.offsets, a.experts, a.lddy * 2, a.lddx, a.N * a.K * 2, K, N};
+    GroupWeights<2> ex{};
+    ex.offsets = a.offsets, ex.groups = a.experts, ex.rows = int(a.M), ex.splits = 1, ex.ldc = a.K;
+    ex.lda = int(a.lddy), ex.ldw = int(a.ldx);
+    const int64_t first = (group_tiles(a.M, a.experts, LY::BM, (K + LY::BN - 1) / LY::BN) + 7) / 8 * 8;
+    const int64_t more = a.experts * int64_t((N + LY::BM - 1) / LY::BM) * ((K + LY::BN - 1) / LY::BN);
+    hipLaunchKernelGGL((group_both_kernel<KIND, CF>), dim3(unsigned(first + more)), dim3(LY::NT), 0, st,
+                       static_cast<const uint8_t *>(a.dy), static_cast<const uint8_t *>(a.x),
+                       static_cast<const uint8_t *>(a.w), a.dx, a.dw, int(a.M), N, K, int(first), r, ex);
+    return hipGetLastError();
+}
+
 template <int KIND>
 hipError_t backward(const Grouped &a, hipStream_t st) {
+    if (a.dx && a.dw && a.M > 0) {
+        switch (both_tile(a.M, a.experts, a.N, a.K)) {
+            case 0: return both_cfg<KIND, Cfg32x64>(a, st);
+            case 1: return both_cfg<KIND, Cfg64x128P>(a, st);
+            case 2: return both_cfg<KIND, Cfg128x128P>(a, st);
+            default: break;
+        }
+    }
     if (a.dx && a.M > 0) {
         const hipError_t e = rows<KIND, true>(a, a.dy, a.lddy, a.dx, a.lddx, int(a.K), int(a.N), st);
         if (e != hipSuccess) return e;
@@ -255,7 +323,13 @@ int64_t grouped_blocks(int64_t M, int64_t experts, int64_t N, int64_t K) {
     const TileCost &w = kDwTiles[pl.tile];
     const int64_t fwd = of_rows(kFwdTiles[rows_tile<false>(M, experts, N, K)], N);
     const int64_t dx = of_rows(kDxTiles[rows_tile<true>(M, experts, K, N)], K);
-    const int64_t dw = pl.splits * experts * ((N + w.bm - 1) / w.bm) * ((K + w.bn - 1) / w.bn);
+    int64_t dw = pl.splits * experts * ((N + w.bm - 1) / w.bm) * ((K + w.bn - 1) / w.bn);
+    const int both = both_tile(M, experts, N, K);
+    if (both >= 0) {  // (dx and dw of its tile in one launch)
+        const TileCost &t = kBothTiles[both].dx;
+        const int64_t all = of_rows(t, K) + 8 + experts * ((N + t.bm - 1) / t.bm) * ((K + t.bn - 1) / t.bn);
+        if (all > dw) dw = all;
+    }
     const int64_t most = fwd > dx ? fwd : dx;
     return most > dw ? most : dw;
 }

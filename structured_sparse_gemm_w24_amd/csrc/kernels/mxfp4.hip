@@ -156,19 +156,19 @@ struct MxProduct {
     bool stream;
 
     template <class CF, int BM, int BN>
-    __device__ __forceinline__ bool place(const uint8_t *&A, const uint8_t *&W, void *&C, int &M, int N, int K, int &,
-                                          int &n0) {
+    __device__ __forceinline__ bool place(int block, const uint8_t *&A, const uint8_t *&W, void *&C, int &M, int N,
+                                          int K, int &, int &n0) {
         const int tiles_n = (N + BN - 1) / BN;
         int row, rows;
         if constexpr (GROUPED) {
-            const group::Tile t = group::find_tile<BM>(offsets, groups, M, tiles_n, CF::GM);
+            const group::Tile t = group::find_tile<BM>(block, offsets, groups, M, tiles_n, CF::GM);
             if (t.group < 0) return false;
             row = t.row, rows = t.rows, n0 = t.tile_n * BN;
             W += int64_t(t.group) * N * a_row;
             sw += int64_t(t.group) * N * (K / 32);
         } else {
             const int tiles_m = (M + BM - 1) / BM;
-            const int b = xcd_remap(blockIdx.x, tiles_m * tiles_n);
+            const int b = xcd_remap(block, tiles_m * tiles_n);
             const int super = b / (CF::GM * tiles_n), gm = min(tiles_m - super * CF::GM, CF::GM);
             const int in = b % (CF::GM * tiles_n);
             row = (super * CF::GM + in % gm) * BM, rows = M - row, n0 = in / gm * BN;
