@@ -542,7 +542,7 @@ int64_t grouped_gemm_backward_workspace_bytes(int32_t experts, int64_t M, int64_
  * mxfp4_quantize: scale byte max(0, floor(log2 max|x|) + 125) of each block,
  * code the nearest magnitude to |x| / scale (ties to the even code, past 6: 6).
  * A block with an infinity or NaN gets byte 255 and codes 0.  x of any dtype,
- * element-aligned, any row stride >= K; 0 <= M < 2^31, 1 <= K < 2^22, fewer than 2^37 values. */
+ * element-aligned, any row stride >= K; 0 <= M < 2^31, 1 <= K < 2^22, fewer than 2^36 values. */
 int mxfp4_quantize(int32_t dtype, const void *x, int64_t ldx, uint8_t *codes, uint8_t *scales, int64_t M, int64_t K,
                    void *stream);
 /* out [M][K] of any dtype: the values, rounded once to it. */

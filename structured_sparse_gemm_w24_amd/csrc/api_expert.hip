@@ -85,14 +85,14 @@ int check_grouped(const char *fn, int32_t dtype, const int32_t *offsets, int32_t
     return SSG_OK;
 }
 
-// (the element kernels: eight values a thread, four pieces each for so many, 2^32 threads a launch)
+// (the element kernels: two pieces of eight values a thread, 2^32 threads a launch)
 bool mx_dims(int64_t M, int64_t K) {
-    return M >= 0 && fits_int(M) && K >= 1 && K < kSide && M * (ssg::mxfp4_padded(K) / 8) < (int64_t(1) << 34) - 1024;
+    return M >= 0 && fits_int(M) && K >= 1 && K < kSide && M * (ssg::mxfp4_padded(K) / 8) < (int64_t(1) << 33) - 512;
 }
 
 int check_mx(const char *fn, int64_t M, int64_t K) {
     if (!mx_dims(M, K))
-        return ssg::fail(SSG_EINVAL, "%s: M=%lld K=%lld (need 0 <= M < 2^31, 1 <= K < 2^22, below 2^37 values)", fn,
+        return ssg::fail(SSG_EINVAL, "%s: M=%lld K=%lld (need 0 <= M < 2^31, 1 <= K < 2^22, below 2^36 values)", fn,
                          (long long)M, (long long)K);
     return SSG_OK;
 }

@@ -92,16 +92,27 @@ __device__ __forceinline__ Tile find_tile(int block, const int32_t *offsets, int
     return t;
 }
 
-// Group g's rows [lo, hi).
-__device__ __forceinline__ void rows_of(const int32_t *offsets, int groups, int rows, int g, int &lo, int &hi) {
+// The k-th group (sorted: the k-th longest of its 64, ties in their order): its number and its rows
+// [lo, hi).
+__device__ __forceinline__ int nth_group(const int32_t *offsets, int groups, int rows, int k, bool sorted, int &lo,
+                                         int &hi) {
     int reached = clamped(offsets[0], rows), l, h;
     for (int g0 = 0;; g0 += 64) {
         span(offsets, groups, rows, g0, reached, l, h);
-        if (g < g0 + 64) {
-            lo = __builtin_amdgcn_readlane(l, g - g0);
-            hi = __builtin_amdgcn_readlane(h, g - g0);
-            return;
+        if (k >= g0 + 64) continue;
+        int at = k - g0;
+        if (sorted) {
+            const int lane = threadIdx.x & 63, len = h - l, n = min(groups - g0, 64);
+            int before = 0;  // groups that come before this lane's
+            for (int j = 0; j < n; ++j) {
+                const int other = __builtin_amdgcn_readlane(len, j);
+                before += other > len || (other == len && j < lane) ? 1 : 0;
+            }
+            at = __builtin_ctzll(__ballot(before == k - g0 && lane < n));
         }
+        lo = __builtin_amdgcn_readlane(l, at);
+        hi = __builtin_amdgcn_readlane(h, at);
+        return g0 + at;
     }
 }
 

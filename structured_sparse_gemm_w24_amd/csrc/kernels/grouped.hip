@@ -51,6 +51,7 @@ struct GroupWeights {
     static constexpr bool kAfter = false, kEpilogue = false, kTransA = true, kTransW = true, kPlace = true, stream = true;
     const int32_t *offsets;
     int groups, rows, splits;
+    bool sorted;
     int64_t a_row, ldc;  // (a_row: unused)
     int lda, ldw;
     int rows_a, rows_w;        // (unused: the stages' buffers take bytes_a and bytes_w)
@@ -62,9 +63,9 @@ struct GroupWeights {
         const int tiles_n = (N + BN - 1) / BN, each = (M + BM - 1) / BM * tiles_n;
         // (every expert's tiles are spread over the XCDs: a popular expert is no XCD's alone)
         const int share = block / (each * groups), tile = block - share * (each * groups);
-        const int g = tile / each, j = xcd_remap(tile % each, each);
+        const int j = xcd_remap(tile % each, each);
         int lo, hi;
-        group::rows_of(offsets, groups, rows, g, lo, hi);
+        const int g = group::nth_group(offsets, groups, rows, tile / each, sorted, lo, hi);
         const int all = (hi - lo + 63) / 64, per = (all + splits - 1) / splits, from = min(share * per, all);
         stages = min(per, all - from);
         lo += from * 64;
@@ -229,11 +230,17 @@ hipError_t rows(const Grouped &a, const void *A, int64_t lda, void *C, int64_t l
 #undef SSG_TILE
 }
 
+// Whether dw's longest groups go first, so that no long sum is the last to start (16384 rows of 64 experts,
+// 1024 x 1024, dw 79.9 us in their own order, 74.6 sorted; 8192 of 8, 2048 x 2048, 95.2 and 90.1); with short
+// sums finding the order costs more than it gives (64 rows of 32, 1024 x 2048, 29.1 and 36.4).
+bool long_sums(const Grouped &a) { return a.M >= 128 * int64_t(a.experts); }
+
 template <int KIND, class CF, bool SPLIT>
 hipError_t weights_cfg(const Grouped &a, int splits, hipStream_t st) {
     using LY = Layout<KIND, CF>;
     GroupWeights<SPLIT ? 4 : 2> ex{};
     ex.offsets = a.offsets, ex.groups = a.experts, ex.rows = int(a.M), ex.splits = splits, ex.ldc = a.K;
+    ex.sorted = long_sums(a);
     ex.lda = int(a.lddy), ex.ldw = int(a.ldx);
     const int64_t blocks = splits * a.experts * ((a.N + LY::BM - 1) / LY::BM) * ((a.K + LY::BN - 1) / LY::BN);
     if constexpr (SPLIT)
@@ -289,6 +296,7 @@ hipError_t both_cfg(const Grouped &a, hipStream_t st) {
     const GroupRows<true> r{a.offsets, a.experts, a.lddy * 2, a.lddx, a.N * a.K * 2, K, N};
     GroupWeights<2> ex{};
     ex.offsets = a.offsets, ex.groups = a.experts, ex.rows = int(a.M), ex.splits = 1, ex.ldc = a.K;
+    ex.sorted = long_sums(a);
     ex.lda = int(a.lddy), ex.ldw = int(a.ldx);
     const int64_t first = (group_tiles(a.M, a.experts, LY::BM, (K + LY::BN - 1) / LY::BN) + 7) / 8 * 8;
     const int64_t more = a.experts * int64_t((N + LY::BM - 1) / LY::BM) * ((K + LY::BN - 1) / LY::BN);
