@@ -24,7 +24,8 @@
     // `wave` is a wave's index within its group.
     constexpr bool PROD = CF::PROD;
     const bool loader = PROD && (tid >> 6) >= LY::NW;
-    const int wave = loader ? (tid >> 6) - LY::NW : tid >> 6;
+    // (DEEP: known to be uniform, so that where a load goes in LDS is a scalar)
+    const int wave = CF::DEEP ? __builtin_amdgcn_readfirstlane(tid >> 6) : loader ? (tid >> 6) - LY::NW : tid >> 6;
     const int wm = wave % WM, wn = wave / WM;
     const int h = lane >> 5, r = lane & 31;
 
@@ -209,6 +210,15 @@
             for (int j = 0; j < LY::LW; ++j) dma16(w, ow[j], base + A_STAGE + (j * LY::NL + wave) * 1024);
             return;
         }
+        if constexpr (CF::DEEP && decltype(whole)::value && !Extra::kTransW) {
+            // (the stage in the scalar offset)
+#pragma unroll
+            for (int j = 0; j < LY::LA; ++j) dma16s(bufA, oa[j], uint32_t(sg * LY::AB), base + (j * LY::NL + wave) * 1024);
+#pragma unroll
+            for (int j = 0; j < LY::LW; ++j)
+                dma16s(bufW, ow[j], uint32_t(sg * WB), base + A_STAGE + (j * LY::NL + wave) * 1024);
+            return;
+        }
 #pragma unroll
         for (int j = 0; j < LY::LA; ++j)
             dma16(bufA, oa[j] + (Extra::kTransA ? uint32_t(sg) * uint32_t(lda_of(extra) * 128) : uint32_t(sg * LY::AB)), base + (j * LY::NL + wave) * 1024);
@@ -275,10 +285,10 @@
     };
 
     // MX_F4: one word of scales serves two k-steps (none past the end of K).
-    [[maybe_unused]] auto load_scales = [&](int s, int kk, Frag &F, const Frag &before) {
+    [[maybe_unused]] auto load_scales = [&](int s, int kk, Frag &F, const Frag &before, auto whole) {
         if constexpr (F4) {
             const uint8_t *b = smem + NB * STAGE + (s >> 1) % 3 * LY::S_BLOCK + (s & 1) * 8 + kk / 2 * 4;
-            const uint32_t live = (s * 2 + kk / 2) * 4 < K / 32 ? 0xffffffffu : 0u;
+            const uint32_t live = decltype(whole)::value || (s * 2 + kk / 2) * 4 < K / 32 ? 0xffffffffu : 0u;
             auto word = [&](int row) { return (*reinterpret_cast<const uint32_t *>(b + row * 16) & live) >> (8 * h); };
 #pragma unroll
             for (int tn = 0; tn < TN; ++tn)
@@ -360,18 +370,44 @@
         static_assert(!PROD && NB == 2 && LY::NL == LY::NW);
         constexpr int NI = LY::NI;
         Frag F[NI];
-        auto load = [&](int s, int kk) {
-            load_frag(s, kk, F[kk]);
-            if constexpr (F4) load_scales(s, kk, F[kk], F[kk & ~1]);
+        // Where this lane's chunks lie in a stage.  Of the swizzle of a row r + 32 t only bit 2, t % 2,
+        // depends on t, and in k-step kk it is that of k-step kk ^ 2 of t's neighbour: four places an
+        // operand and constant distances from them serve all its rows (each place found by itself is
+        // two of the three vector instructions beside every matrix instruction of a stage).
+        int at_a[NI], at_w[NI];
+        constexpr bool PLACES = !Extra::kTransW;
+        if constexpr (PLACES) {
+            static_assert(NI == 4 && LY::AB == 128 && WB == 128);
+#pragma unroll
+            for (int kk = 0; kk < NI; ++kk) {
+                const int ra = wm * TM * 32 + r, rw = wn * TN * 32 + r;
+                at_a[kk] = ra * 128 + swz128(ra, 2 * kk + h) * 16;
+                at_w[kk] = A_STAGE + rw * 128 + swz128(rw, 2 * kk + h) * 16;
+            }
+        }
+        auto load = [&](int s, int kk, auto whole) {
+            if constexpr (PLACES) {
+                const uint8_t *b = smem + (s & 1) * STAGE;
+#pragma unroll
+                for (int tn = 0; tn < TN; ++tn) F[kk].w[tn] = lds16(b + at_w[kk ^ (tn & 1) * 2] + tn * 4096);
+#pragma unroll
+                for (int tm = 0; tm < TM; ++tm) {
+                    const u32x4 lo = lds16(b + at_a[kk ^ (tm & 1) * 2] + tm * 4096);
+                    F[kk].a[tm] = __builtin_shufflevector(lo, lo, 0, 1, 2, 3, 0, 1, 2, 3);
+                }
+            } else {
+                load_frag(s, kk, F[kk]);
+            }
+            if constexpr (F4) load_scales(s, kk, F[kk], F[kk & ~1], whole);
         };
 #pragma unroll
-        for (int kk = 0; kk + 1 < NI; ++kk) load(0, kk);
+        for (int kk = 0; kk + 1 < NI; ++kk) load(0, kk, std::false_type{});
         // PHASE 0: stage s + NB is fetched, and whole; 1: fetched; 2: there is none
         auto stage = [&](int s, auto phase) {
             constexpr int PHASE = decltype(phase)::value;
 #pragma unroll
             for (int kk = 0; kk < NI; ++kk) {
-                if (kk == 0) load(s, NI - 1);
+                if (kk == 0) load(s, NI - 1, std::integral_constant<bool, PHASE == 0>{});
                 if (kk == 1 && PHASE < 2) {
                     asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
                     if constexpr (PHASE == 0) issue(s + NB, std::true_type{});
@@ -381,7 +417,7 @@
                     if constexpr (PHASE < 2) wait_vm_barrier<LY::L>();
                     else wait_vm_barrier<0>();
 #pragma unroll
-                    for (int k = 0; k + 1 < NI; ++k) load(s + 1, k);
+                    for (int k = 0; k + 1 < NI; ++k) load(s + 1, k, std::integral_constant<bool, PHASE == 0>{});
                 }
                 mma_frag(F[kk], kk);
 #pragma unroll
@@ -401,7 +437,7 @@
     } else {
         Frag F[2];
         load_frag(0, 0, F[0]);
-        if constexpr (F4) load_scales(0, 0, F[0], F[0]);
+        if constexpr (F4) load_scales(0, 0, F[0], F[0], std::false_type{});
 
         // One stage; STEADY: the ring still has a stage to fetch (s + NB < S).
         // The next stage's first fragments are read unconditionally: on the last
@@ -413,7 +449,7 @@
                 Frag &nxt = F[(kk + 1) & 1];
                 if (kk + 1 < LY::NI) {
                     load_frag(s, kk + 1, nxt);
-                    if constexpr (F4) load_scales(s, kk + 1, nxt, cur);
+                    if constexpr (F4) load_scales(s, kk + 1, nxt, cur, std::false_type{});
                 } else {
                     // stage s is fully in registers; stage s+1 must be complete
                     if constexpr (decltype(steady)::value) {
@@ -423,7 +459,7 @@
                         wait_lgkm_vm_barrier<0>();
                     }
                     load_frag(s + 1, 0, nxt);
-                    if constexpr (F4) load_scales(s + 1, 0, nxt, cur);
+                    if constexpr (F4) load_scales(s + 1, 0, nxt, cur, std::false_type{});
                 }
                 mma_frag(cur, kk);
                 interleave();
