@@ -230,6 +230,16 @@ __device__ __forceinline__ void mma(typename AccOf<KIND>::T &acc, u32x4 w, u32x8
     }
 }
 
+// What place() found, as scalars: the same in every lane, but computed in vector registers it makes each
+// load loop over the lanes' buffer descriptors (dx of grouped.hip, 16384 x 1024 from 4096, 256 x 256 tiles,
+// 241 us).
+__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+__device__ __forceinline__ const uint8_t *uniform(const uint8_t *p) {
+    const uint64_t v = reinterpret_cast<uint64_t>(p);
+    const uint64_t lo = uint32_t(uniform(int(uint32_t(v)))), hi = uint32_t(uniform(int(uint32_t(v >> 32))));
+    return reinterpret_cast<const uint8_t *>(hi << 32 | lo);
+}
+
 // The microscaled 4-bit instruction: 32 x 32 x 64, lane (h, r) holds k = 32h .. 32h+31 of its
 // row r, i.e. one block, whose scale is byte OP of its scale word.
 template <int OP>

@@ -35,7 +35,8 @@
         const uint8_t *a = A, *w = Wv;
         void *c = C;
         if (!extra.template place<CF, BM, BN>(block, a, w, c, M, N, K, stages, n0)) return;
-        A = a, Wv = w, C = c;
+        A = uniform(a), Wv = uniform(w), C = c;
+        M = uniform(M);
     } else {
         const int tiles_m = (M + BM - 1) / BM, tiles_n = (N + BN - 1) / BN;
         b = xcd_remap(block, tiles_m * tiles_n);
@@ -112,7 +113,7 @@
     // (transposed operands end with their last row: a partial last stage reads zeros past it)
     const __amdgpu_buffer_rsrc_t bufA =
         buffer_of(A, Extra::kTransA  ? bytes_a_of(extra)
-                     : Extra::kPlace ? uint32_t(int64_t(min(M, BM) - 1) * a_row + k_row)
+                     : Extra::kPlace ? uint32_t(uniform(int(int64_t(min(M, BM) - 1) * a_row + k_row)))
                                      : uint32_t(int64_t(M) * a_row));
     const __amdgpu_buffer_rsrc_t bufW =
         buffer_of(Wv, Extra::kTransW ? bytes_w_of(extra) : uint32_t(int64_t(N) * w_row));
@@ -202,21 +203,23 @@
         if constexpr (Extra::kPlace && Extra::kTransA) {
             // rows of a group may reach past 32-bit offsets: each stage has a buffer of its own
             const int64_t sa = int64_t(sg) * extra.lda * 128, sw = int64_t(sg) * extra.ldw * 128;
-            const __amdgpu_buffer_rsrc_t a = buffer_of(A + sa, uint32_t(min(extra.bytes_a - sa, int64_t(0x7fffffff))));
-            const __amdgpu_buffer_rsrc_t w = buffer_of(Wv + sw, uint32_t(min(extra.bytes_w - sw, int64_t(0x7fffffff))));
+            auto room = [](int64_t bytes) { return uint32_t(uniform(int(min(bytes, int64_t(0x7fffffff))))); };
+            const __amdgpu_buffer_rsrc_t a = buffer_of(uniform(A + sa), room(extra.bytes_a - sa));
+            const __amdgpu_buffer_rsrc_t w = buffer_of(uniform(Wv + sw), room(extra.bytes_w - sw));
 #pragma unroll
             for (int j = 0; j < LY::LA; ++j) dma16(a, oa[j], base + (j * LY::NL + wave) * 1024);
 #pragma unroll
             for (int j = 0; j < LY::LW; ++j) dma16(w, ow[j], base + A_STAGE + (j * LY::NL + wave) * 1024);
             return;
         }
-        if constexpr (CF::DEEP && decltype(whole)::value && !Extra::kTransW) {
+        if constexpr (CF::DEEP && decltype(whole)::value) {
             // (the stage in the scalar offset)
+            const uint32_t more_w = Extra::kTransW ? uint32_t(sg) * uint32_t(ldw_of(extra) * 128) : uint32_t(sg * WB);
 #pragma unroll
             for (int j = 0; j < LY::LA; ++j) dma16s(bufA, oa[j], uint32_t(sg * LY::AB), base + (j * LY::NL + wave) * 1024);
 #pragma unroll
             for (int j = 0; j < LY::LW; ++j)
-                dma16s(bufW, ow[j], uint32_t(sg * WB), base + A_STAGE + (j * LY::NL + wave) * 1024);
+                dma16s(bufW, ow[j], more_w, base + A_STAGE + (j * LY::NL + wave) * 1024);
             return;
         }
 #pragma unroll
@@ -373,30 +376,37 @@
         // Where this lane's chunks lie in a stage.  Of the swizzle of a row r + 32 t only bit 2, t % 2,
         // depends on t, and in k-step kk it is that of k-step kk ^ 2 of t's neighbour: four places an
         // operand and constant distances from them serve all its rows (each place found by itself is
-        // two of the three vector instructions beside every matrix instruction of a stage).
-        int at_a[NI], at_w[NI];
-        constexpr bool PLACES = !Extra::kTransW;
-        if constexpr (PLACES) {
-            static_assert(NI == 4 && LY::AB == 128 && WB == 128);
+        // two of the three vector instructions beside every matrix instruction of a stage).  A transposed
+        // operand has a place for each t, and its k-steps at constant distances.
+        static_assert(NI == 4 && LY::AB == 128 && WB == 128);
+        int at_a[Extra::kTransA ? TM : NI], at_w[Extra::kTransW ? TN : NI];
+        auto place_t = [&](int row, int columns) {
+            const int k = 8 * h + ((lane & 15) >> 2), col = row - (r & 15) + 4 * (lane & 3);
+            return k * (columns * 2) + swzk(k, col >> 3, columns / 8) * 16 + (col & 7) * 2;
+        };
 #pragma unroll
-            for (int kk = 0; kk < NI; ++kk) {
-                const int ra = wm * TM * 32 + r, rw = wn * TN * 32 + r;
-                at_a[kk] = ra * 128 + swz128(ra, 2 * kk + h) * 16;
-                at_w[kk] = A_STAGE + rw * 128 + swz128(rw, 2 * kk + h) * 16;
-            }
+        for (int t = 0; t < (Extra::kTransA ? TM : NI); ++t) {
+            const int row = wm * TM * 32 + r;
+            at_a[t] = Extra::kTransA ? place_t(row + t * 32, BM) : row * 128 + swz128(row, 2 * t + h) * 16;
+        }
+#pragma unroll
+        for (int t = 0; t < (Extra::kTransW ? TN : NI); ++t) {
+            const int row = wn * TN * 32 + r;
+            at_w[t] = A_STAGE + (Extra::kTransW ? place_t(row + t * 32, BN) : row * 128 + swz128(row, 2 * t + h) * 16);
         }
         auto load = [&](int s, int kk, auto whole) {
-            if constexpr (PLACES) {
-                const uint8_t *b = smem + (s & 1) * STAGE;
+            const uint8_t *b = smem + (s & 1) * STAGE;
 #pragma unroll
-                for (int tn = 0; tn < TN; ++tn) F[kk].w[tn] = lds16(b + at_w[kk ^ (tn & 1) * 2] + tn * 4096);
+            for (int tn = 0; tn < TN; ++tn) {
+                if constexpr (Extra::kTransW) F[kk].w[tn] = lds_tr8(b + at_w[tn] + kk * (32 * BN), BN * 2);
+                else F[kk].w[tn] = lds16(b + at_w[kk ^ (tn & 1) * 2] + tn * 4096);
+            }
 #pragma unroll
-                for (int tm = 0; tm < TM; ++tm) {
-                    const u32x4 lo = lds16(b + at_a[kk ^ (tm & 1) * 2] + tm * 4096);
-                    F[kk].a[tm] = __builtin_shufflevector(lo, lo, 0, 1, 2, 3, 0, 1, 2, 3);
-                }
-            } else {
-                load_frag(s, kk, F[kk]);
+            for (int tm = 0; tm < TM; ++tm) {
+                u32x4 lo;
+                if constexpr (Extra::kTransA) lo = lds_tr8(b + at_a[tm] + kk * (32 * BM), BM * 2);
+                else lo = lds16(b + at_a[kk ^ (tm & 1) * 2] + tm * 4096);
+                F[kk].a[tm] = __builtin_shufflevector(lo, lo, 0, 1, 2, 3, 0, 1, 2, 3);
             }
             if constexpr (F4) load_scales(s, kk, F[kk], F[kk & ~1], whole);
         };

@@ -112,9 +112,11 @@ hipError_t launch_cfg(const void *A, const void *W, void *C, const Extra &ex, in
 }
 
 // Tiles: with few of them the smallest, whose loads have waves of their own (a chain of K stages, each
-// waiting for memory: 2000 rows of 48 x 1560 in 8 groups 8.7 us, 64 x 64 without loader waves 10.9,
-// 128 x 128 12.9); dx needs loader waves at every size, as its transposing reads keep the others busy
-// (16384 x 1024 from 4096, 16 experts: 155 us on 192 x 128, 252 on 256 x 256 without).
+// waiting for memory: 2324 rows of 8 groups, 72 x 1560, 8.7 us, 64 x 64 without loader waves 10.9,
+// 64 x 128 12.9); the forward's largest keep a stage's fragments in registers (16384 rows of 16, 4096 x
+// 1024 141 us, with eight waves instead 145; 8192 of 8, 2048 x 2048, 192 x 256 77, 256 x 256 95); dx needs
+// loader waves at nearly every size, as its transposing reads keep the others busy (8192 rows of 8, 2048 x
+// 2048: 87 us on 192 x 128 with, 123 on 192 x 256 without).
 using Cfg32x64 = Cfg<1, 2, 1, 1, 4, 8, true, false, 0, true>;
 using Cfg64x64 = Cfg<2, 2, 1, 1, 3, 8, true, false>;
 using Cfg64x64P = Cfg<2, 2, 1, 1, 4, 8, true, false, 0, true>;
@@ -124,9 +126,12 @@ using Cfg128x128 = CfgDeep<2, 2, 8, true>;
 using Cfg128x128P = Cfg<2, 2, 2, 2, 4, 8, true, false, 0, true>;
 using Cfg192x128P = Cfg<2, 2, 3, 2, 4, 8, true, false, 0, true>;
 using Cfg256x128P = Cfg<2, 2, 4, 2, 3, 8, true, false, 0, true>;
-constexpr TileCost kFwdTiles[] = {{32, 64, 3, 4.2f, 0.8f, 0.19f},  {64, 64, 3, 4.1f, 0.2f, 0.30f},
-                                  {64, 128, 2, 3.4f, 1.0f, 0.45f}, {128, 128, 2, 2.1f, 2.8f, 0.55f},
-                                  {192, 128, 1, 0.0f, 5.1f, 0.68f}, {256, 256, 1, 0.0f, 7.2f, 1.33f}};
+using Cfg192x256 = CfgDeep<3, 4, 4, true>;
+using Cfg256x256 = CfgDeep<4, 4, 4, true>;
+constexpr TileCost kFwdTiles[] = {{32, 64, 3, 3.9f, 0.8f, 0.19f},  {64, 64, 3, 4.7f, 0.1f, 0.29f},
+                                  {64, 128, 2, 4.5f, 0.6f, 0.45f}, {128, 128, 2, 2.9f, 1.9f, 0.59f},
+                                  {192, 128, 1, 0.1f, 4.8f, 0.70f}, {192, 256, 1, 0.7f, 6.6f, 1.07f},
+                                  {256, 256, 1, 2.4f, 6.6f, 1.25f}};
 constexpr TileCost kDxTiles[] = {{32, 64, 3, 3.7f, 0.7f, 0.22f},   {64, 64, 2, 3.6f, 1.3f, 0.31f},
                                  {64, 128, 1, 2.4f, 1.1f, 0.46f},  {128, 128, 1, 0.0f, 4.3f, 0.58f},
                                  {128, 128, 2, 4.6f, 0.9f, 0.77f}, {192, 128, 1, 0.0f, 5.6f, 0.67f},
@@ -224,7 +229,8 @@ hipError_t rows(const Grouped &a, const void *A, int64_t lda, void *C, int64_t l
             SSG_TILE(2, Cfg64x128);
             SSG_TILE(3, Cfg128x128);
             SSG_TILE(4, Cfg192x128P);
-            default: return rows_cfg<KIND, CfgBigDense<true>, TW>(a, A, lda, C, ldc, N, K, st);
+            SSG_TILE(5, Cfg192x256);
+            default: return rows_cfg<KIND, Cfg256x256, TW>(a, A, lda, C, ldc, N, K, st);
         }
     }
 #undef SSG_TILE

@@ -205,9 +205,9 @@ using Mx64x128 = CfgDeep<1, 2, 8, true>;
 using Mx128x128 = CfgDeep<2, 2, 8, true>;
 using Mx192x256 = CfgDeep<3, 4, 8, true>;
 using Mx256x256 = CfgDeep<4, 4, 4, true>;
-constexpr TileCost kMxTiles[] = {{32, 32, 6, 4.6f, 2.1f, 0.10f},   {64, 64, 4, 3.2f, 2.9f, 0.20f},
-                                 {64, 128, 2, 4.1f, 2.0f, 0.39f},  {128, 128, 2, 1.9f, 4.8f, 0.51f},
-                                 {192, 256, 1, 0.9f, 8.0f, 1.19f}, {256, 256, 1, 0.8f, 9.7f, 1.32f}};
+constexpr TileCost kMxTiles[] = {{32, 32, 6, 4.5f, 2.2f, 0.10f},   {64, 64, 4, 4.3f, 1.7f, 0.21f},
+                                 {64, 128, 2, 3.7f, 2.2f, 0.36f},  {128, 128, 2, 3.6f, 3.2f, 0.49f},
+                                 {192, 256, 1, 1.4f, 7.5f, 1.13f}, {256, 256, 1, 2.3f, 8.8f, 1.31f}};
 
 // (experts 0: one product)
 int mx_tile(int64_t M, int64_t experts, int64_t N, int64_t K) {
