@@ -192,8 +192,13 @@ template <int OB>
 __device__ __forceinline__ void store_piece(uint8_t *p, u32x4 v, int room, bool stream) {
     typedef u32x4 Any __attribute__((aligned(2)));
     if (room >= 16 / OB) {
-        if (stream) __builtin_nontemporal_store(v, reinterpret_cast<Any *>(p));
-        else *reinterpret_cast<Any *>(p) = v;
+        if (stream) {
+            asm volatile("" ::: "memory");  // (else the compiler makes one plain store of the two)
+            __builtin_nontemporal_store(v, reinterpret_cast<Any *>(p));
+            asm volatile("" ::: "memory");
+        } else {
+            *reinterpret_cast<Any *>(p) = v;
+        }
         return;
     }
 #pragma unroll

@@ -24,11 +24,12 @@ namespace {
 // forward (TW false) and dx (TW true): tiles of a group's rows.
 template <bool TW>
 struct GroupRows {
-    static constexpr bool kAfter = false, kEpilogue = false, kTransA = false, kTransW = TW, kPlace = true, stream = true;
+    static constexpr bool kAfter = false, kEpilogue = false, kTransA = false, kTransW = TW, kPlace = true;
     const int32_t *offsets;
     int groups;
     int64_t a_row, ldc, w_bytes;  // bytes between A's rows, elements between C's, bytes of a weight
     int ldw, rows_w;              // (TW)
+    bool stream;                  // stores past the L2: large outputs
 
     template <class CF, int BM, int BN>
     __device__ __forceinline__ bool place(int block, const uint8_t *&A, const uint8_t *&W, void *&C, int &M, int N,
@@ -66,6 +67,16 @@ struct GroupWeights {
         const int j = xcd_remap(tile % each, each);
         int lo, hi;
         const int g = group::nth_group(offsets, groups, rows, tile / each, sorted, lo, hi);
+        if (lo == hi && splits == 1) {
+            // an expert without rows: its zeros as one run, a share for each of its workgroups (as tiles,
+            // rows of any width leave parts of cache lines: 58 experts, mostly empty, 872 x 2936 118 us)
+            const int64_t pieces = int64_t(M) * N * OB / 16, n = (pieces + each - 1) / each;
+            const int64_t first = (tile % each) * n, last = min(first + n, pieces);
+            u32x4 *const out = static_cast<u32x4 *>(C) + g * pieces;
+            for (int64_t i = first + threadIdx.x; i < last; i += blockDim.x)
+                __builtin_nontemporal_store(u32x4{0, 0, 0, 0}, out + i);
+            return false;
+        }
         const int all = (hi - lo + 63) / 64, per = (all + splits - 1) / splits, from = min(share * per, all);
         stages = min(per, all - from);
         lo += from * 64;
@@ -143,7 +154,7 @@ constexpr TileCost kDwTiles[] = {{32, 64, 3, 3.1f, 1.2f, 0.21f},   {64, 128, 1, 
 template <int KIND, class CF, bool TW>
 hipError_t rows_cfg(const Grouped &a, const void *A, int64_t lda, void *C, int64_t ldc, int N, int K, hipStream_t st) {
     using LY = Layout<KIND, CF>;
-    GroupRows<TW> ex{a.offsets, a.experts, lda * 2, ldc, int64_t(N) * K * 2, N, K};
+    const GroupRows<TW> ex{a.offsets, a.experts, lda * 2, ldc, int64_t(N) * K * 2, N, K, streams(a.M * N * 2)};
     const int64_t blocks = group_tiles(a.M, a.experts, LY::BM, (N + LY::BN - 1) / LY::BN);
     return launch_cfg<KIND, CF>(A, a.w, C, ex, blocks, int(a.M), N, K, st);
 }
@@ -299,7 +310,7 @@ template <int KIND, class CF>
 hipError_t both_cfg(const Grouped &a, hipStream_t st) {
     using LY = Layout<KIND, CF>;
     const int N = int(a.N), K = int(a.K);
-    const GroupRows<true> r{a.offsets, a.experts, a.lddy * 2, a.lddx, a.N * a.K * 2, K, N};
+    const GroupRows<true> r{a.offsets, a.experts, a.lddy * 2, a.lddx, a.N * a.K * 2, K, N, streams(a.M * K * 2)};
     GroupWeights<2> ex{};
     ex.offsets = a.offsets, ex.groups = a.experts, ex.rows = int(a.M), ex.splits = 1, ex.ldc = a.K;
     ex.sorted = long_sums(a);

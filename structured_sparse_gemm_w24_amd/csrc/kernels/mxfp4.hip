@@ -152,9 +152,9 @@ struct MxProduct {
     int groups;
     const uint8_t *sa, *sw;
     int64_t a_row, ldc;  // bytes of a packed row; elements between C's rows
-    // C's rows at any 2 or 4 bytes leave parts of cache lines in every piece, which nontemporal stores
-    // send to memory one by one (7648 x 3001 x 533 26.6 us, cached stores 22.9; but 3008 wide, 18.9 and
-    // 21.6, and 16079 x 1388 x 2757, whose rows are 8 bytes off, 47.1 and 53.5)
+    // Stores past the L2: large outputs whose rows are whole 64 bytes (others leave parts of cache lines in
+    // every piece, which then go to memory one by one: 7648 x 3000 x 533 25.4 us, cached 23.2; but 16384 x
+    // 4096 x 1024 61.6 and 65.3)
     bool stream;
 
     template <class CF, int BM, int BN>
@@ -187,7 +187,9 @@ template <int EPI, class CF, bool GROUPED>
 hipError_t gemm_cfg(const Mxfp4Gemm &g, int K, hipStream_t st) {
     using LY = Layout<MX_F4, CF>;
     constexpr int OB = EPI == EPI_F32 ? 4 : 2;
-    const MxProduct<GROUPED, OB> ex{g.offsets, g.experts, g.a_scales, g.w_scales, K / 2, g.ldo, g.ldo * OB % 8 == 0 && reinterpret_cast<uintptr_t>(g.out) % 8 == 0};
+    const bool whole = g.ldo * OB % 64 == 0 && reinterpret_cast<uintptr_t>(g.out) % 64 == 0;
+    const MxProduct<GROUPED, OB> ex{g.offsets, g.experts, g.a_scales, g.w_scales, K / 2, g.ldo,
+                                    whole && streams(g.M * g.N * OB)};
     const int64_t tiles_n = (g.N + LY::BN - 1) / LY::BN;
     const int64_t blocks =
         GROUPED ? group_tiles(g.M, g.experts, LY::BM, tiles_n) : (g.M + LY::BM - 1) / LY::BM * tiles_n;
