@@ -506,18 +506,18 @@ int64_t linear_cross_entropy_workspace_bytes(int32_t dtype, int64_t M, int64_t V
                                              int32_t backward);
 
 /* ---- Experts: products grouped by expert, microscaled 4-bit weights, and the
- * gradient norm.  16-byte aligned operands unless a call says otherwise;
- * nothing is allocated, every call may be captured into a graph.
+ * gradient norm.  16-byte aligned operands (scales 4-byte) unless a call says
+ * otherwise; nothing is allocated, every call may be captured into a graph.
  *
  * offsets int32 [experts + 1] (device): rows offsets[e] .. offsets[e + 1] of the
  * M rows belong to expert e; an expert may have none.  The device cannot refuse
  * a call, so offsets outside 0 .. M are clamped to it, and one below an earlier
  * offset counts as the largest before it.  Output rows of no expert (before
- * offsets[0], behind offsets[experts]) are left as they are. */
+ * offsets[0], behind offsets[experts]) are left as they are.  No output overlaps an input. */
 
 /* out[m] = w[e] . x[m] for the expert e of row m: x [M][K], w [experts][N][K]
  * contiguous, out [M][N], dtype SSG_DT_F16 or SSG_DT_BF16, fp32 sums, one
- * rounding.  0 <= M < 2^31, N and K positive multiples of 8 below 2^22, one
+ * rounding.  0 <= M < 2^29, N and K positive multiples of 8 below 2^22, one
  * weight below 2 GiB, 1 <= experts <= 65535; row strides in multiples of 8, below 2^22. */
 int grouped_gemm(int32_t dtype, const void *x, int64_t ldx, const void *w, const int32_t *offsets, int32_t experts,
                  void *out, int64_t ldo, int64_t M, int64_t N, int64_t K, void *stream);
@@ -542,7 +542,7 @@ int64_t grouped_gemm_backward_workspace_bytes(int32_t experts, int64_t M, int64_
  * mxfp4_quantize: scale byte max(0, floor(log2 max|x|) + 125) of each block,
  * code the nearest magnitude to |x| / scale (ties to the even code, past 6: 6).
  * A block with an infinity or NaN gets byte 255 and codes 0.  x of any dtype,
- * element-aligned, any row stride >= K; 0 <= M < 2^31, 1 <= K < 2^22, fewer than 2^36 values. */
+ * element-aligned, any row stride >= K; 0 <= M < 2^29, 1 <= K < 2^22, M kp < 2^36. */
 int mxfp4_quantize(int32_t dtype, const void *x, int64_t ldx, uint8_t *codes, uint8_t *scales, int64_t M, int64_t K,
                    void *stream);
 /* out [M][K] of any dtype: the values, rounded once to it. */
@@ -553,7 +553,7 @@ int mxfp4_dequantize(const uint8_t *codes, const uint8_t *scales, int32_t dtype,
  * values, fp32 sums, rounded once to dtype (any); out element-aligned, any row
  * stride >= N.  With offsets (else null and experts = 1): w holds experts
  * matrices of N rows one after another, and row m meets its expert's.
- * 0 <= M < 2^31, 1 <= N, K < 2^22, one weight's codes below 2 GiB.  NaN blocks
+ * 0 <= M < 2^29, 1 <= N, K < 2^22, one weight's codes below 2 GiB.  NaN blocks
  * make the rows or columns that they are in NaN. */
 int mxfp4_gemm(const uint8_t *a, const uint8_t *a_scales, const uint8_t *w, const uint8_t *w_scales,
                const int32_t *offsets, int32_t experts, int32_t dtype, void *out, int64_t ldo, int64_t M, int64_t N,
@@ -569,8 +569,8 @@ int64_t mxfp4_linear_workspace_bytes(int64_t M, int64_t K);
 
 /* norm[0] = sqrt of the sum of squares of n tensors' elements (fp64 sums), rounded to fp32.
  * grads, sizes (elements, 0 allowed) and dtypes are host arrays of n entries,
- * read during the call; tensors are contiguous and element-aligned.  ws:
- * 16-byte aligned, grad_norm_workspace_bytes(n). */
+ * read during the call; tensors are contiguous and element-aligned, up to 2^20
+ * of them and 16 TiB.  ws: 16-byte aligned, grad_norm_workspace_bytes(n). */
 int grad_norm(int32_t n, const void *const *grads, const int64_t *sizes, const int32_t *dtypes, float *norm, void *ws,
               int64_t ws_bytes, void *stream);
 
@@ -578,8 +578,8 @@ int grad_norm(int32_t n, const void *const *grads, const int64_t *sizes, const i
  * and the product once to the tensor's type; outs[i] is grads[i] (in place;
  * not touched where the factor is 1) or a buffer that overlaps no tensor of the
  * call (refused).  norm_in null: norm is grad_norm's and written to norm[0];
- * else norm_in[0] (device, e.g. summed over ranks) is the norm, and norm and ws
- * may be null.  An infinite norm makes the factor 0, a NaN one makes it NaN.
+ * else norm_in[0] (device, e.g. summed over ranks, in no output) is the norm, and
+ * norm and ws may be null.  An infinite norm makes the factor 0, a NaN one makes it NaN.
  * The same element in two entries is refused when it would be scaled twice. */
 int clip_grad_norm(int32_t n, const void *const *grads, void *const *outs, const int64_t *sizes,
                    const int32_t *dtypes, double max_norm, const float *norm_in, float *norm, void *ws,

@@ -17,8 +17,9 @@ using ssg::check_device;
 using ssg::fits_int;
 using ssg::launched;
 
-// A tile's 256 rows stay below 2 GiB: the kernels' offsets are of 32 bits.
-constexpr int64_t kSide = int64_t(1) << 22, kGiB2 = int64_t(1) << 31;
+// A tile's 256 rows stay below 2 GiB (the kernels' offsets are of 32 bits), and the products' rows below
+// 2^29 (so are their tile counts, and stages of 64 rows below 2^24).
+constexpr int64_t kSide = int64_t(1) << 22, kGiB2 = int64_t(1) << 31, kRows = int64_t(1) << 29;
 
 int ok() {
     ssg::clear_error();
@@ -66,33 +67,34 @@ int check_groups(const char *fn, const int32_t *offsets, int32_t experts) {
 }
 
 bool grouped_dims(int64_t M, int64_t N, int64_t K) {
-    return M >= 0 && fits_int(M) && N >= 8 && K >= 8 && N % 8 == 0 && K % 8 == 0 && N < kSide && K < kSide &&
+    return M >= 0 && M < kRows && N >= 8 && K >= 8 && N % 8 == 0 && K % 8 == 0 && N < kSide && K < kSide &&
            N * K * 2 < kGiB2;
 }
 
 int check_grouped(const char *fn, int32_t dtype, const int32_t *offsets, int32_t experts, int64_t M, int64_t N,
-                  int64_t K) {
+                  int64_t K, bool backward) {
     if (!half_type(dtype)) return ssg::fail(SSG_EINVAL, "%s: dtype %d must be fp16 or bf16", fn, dtype);
     if (!grouped_dims(M, N, K))
         return ssg::fail(SSG_EINVAL,
-                         "%s: M=%lld N=%lld K=%lld (need 0 <= M < 2^31, N and K positive multiples of 8 below 2^22, a "
+                         "%s: M=%lld N=%lld K=%lld (need 0 <= M < 2^29, N and K positive multiples of 8 below 2^22, a "
                          "weight below 2 GiB)",
                          fn, (long long)M, (long long)N, (long long)K);
     if (int rc = check_groups(fn, offsets, experts)) return rc;
     // (a launch takes fewer than 2^32 threads, in workgroups of up to 512)
-    if (ssg::grouped_blocks(M, experts, N, K) >= (int64_t(1) << 23))
+    if (ssg::grouped_blocks(M, experts, N, K, backward) >= (int64_t(1) << 23))
         return ssg::fail(SSG_EINVAL, "%s: dimensions too large for one launch", fn);
     return SSG_OK;
 }
 
-// (the element kernels: two pieces of eight values a thread, 2^32 threads a launch)
+// (the element kernels: two pieces of eight values a thread, 2^32 threads a launch; padded rows have 16
+// pieces or more, so M stays below 2^29 as well)
 bool mx_dims(int64_t M, int64_t K) {
     return M >= 0 && fits_int(M) && K >= 1 && K < kSide && M * (ssg::mxfp4_padded(K) / 8) < (int64_t(1) << 33) - 512;
 }
 
 int check_mx(const char *fn, int64_t M, int64_t K) {
     if (!mx_dims(M, K))
-        return ssg::fail(SSG_EINVAL, "%s: M=%lld K=%lld (need 0 <= M < 2^31, 1 <= K < 2^22, below 2^36 values)", fn,
+        return ssg::fail(SSG_EINVAL, "%s: M=%lld K=%lld (need 0 <= M < 2^29, 1 <= K < 2^22, below 2^36 padded values)", fn,
                          (long long)M, (long long)K);
     return SSG_OK;
 }
@@ -126,7 +128,7 @@ int check_mx_gemm(const char *fn, const uint8_t *w, const uint8_t *w_scales, con
 SSG_API int grouped_gemm(int32_t dtype, const void *x, int64_t ldx, const void *w, const int32_t *offsets,
                          int32_t experts, void *out, int64_t ldo, int64_t M, int64_t N, int64_t K, void *stream) {
     const char *fn = "grouped_gemm";
-    int rc = check_grouped(fn, dtype, offsets, experts, M, N, K);
+    int rc = check_grouped(fn, dtype, offsets, experts, M, N, K, false);
     if (rc) return rc;
     if (M == 0) return ok();
     if ((rc = check_rows(fn, "x", x, ldx, K)) || (rc = check_rows(fn, "w", w, K, K)) ||
@@ -147,7 +149,7 @@ SSG_API int grouped_gemm_backward(int32_t dtype, const void *dy, int64_t lddy, c
                                   const void *w, const int32_t *offsets, int32_t experts, void *dx, int64_t lddx,
                                   void *dw, int64_t M, int64_t N, int64_t K, void *ws, int64_t ws_bytes, void *stream) {
     const char *fn = "grouped_gemm_backward";
-    int rc = check_grouped(fn, dtype, offsets, experts, M, N, K);
+    int rc = check_grouped(fn, dtype, offsets, experts, M, N, K, true);
     if (rc) return rc;
     if (M > 0) {
         if ((rc = check_rows(fn, "dy", dy, lddy, N))) return rc;
@@ -232,8 +234,10 @@ SSG_API int mxfp4_linear(int32_t dtype, const void *x, int64_t ldx, const uint8_
 // ---------------------------------------------------------------- gradient norm
 namespace {
 
+// (up to 2^20 tensors and 2^44 bytes: piece and slot numbers stay below 2^31)
 int check_list(const char *fn, int32_t n, const void *const *grads, const int64_t *sizes, const int32_t *dtypes) {
-    if (n < 0) return ssg::fail(SSG_EINVAL, "%s: n=%d tensors", fn, n);
+    if (n < 0 || n > (1 << 20)) return ssg::fail(SSG_EINVAL, "%s: n=%d tensors (need 0 <= n <= 2^20)", fn, n);
+    int64_t bytes = 0;
     if (n > 0 && (!grads || !sizes || !dtypes)) return ssg::fail(SSG_EINVAL, "%s: null list", fn);
     for (int i = 0; i < n; ++i) {
         if (!known(dtypes[i])) return ssg::fail(SSG_EINVAL, "%s: unknown dtype %d of tensor %d", fn, dtypes[i], i);
@@ -242,6 +246,8 @@ int check_list(const char *fn, int32_t n, const void *const *grads, const int64_
                              (long long)sizes[i]);
         if (sizes[i] > 0 && (!grads[i] || !aligned_to(grads[i], elem_bytes(dtypes[i]))))
             return ssg::fail(SSG_EINVAL, "%s: tensor %d null or not aligned to its elements", fn, i);
+        if ((bytes += sizes[i] * elem_bytes(dtypes[i])) > int64_t(1) << 44)
+            return ssg::fail(SSG_EINVAL, "%s: tensors of more than 16 TiB", fn);
     }
     return SSG_OK;
 }
@@ -253,12 +259,12 @@ struct Span {
 };
 
 // What is written must be no one else's: spans in address order, a written one overlaps no other
-// (an in-place tensor is one span).
+// (an in-place tensor is one span) and not the norm that every workgroup reads.
 int check_overlap(const char *fn, int32_t n, const void *const *grads, void *const *outs, const int64_t *sizes,
-                  const int32_t *dtypes) {
+                  const int32_t *dtypes, const float *norm_in) {
     std::vector<Span> spans;
     try {
-        spans.reserve(size_t(n) * 2);
+        spans.reserve(size_t(n) * 2 + 1);
     } catch (const std::bad_alloc &) {
         return ssg::fail(SSG_ENOSPC, "%s: no host memory for %d tensors", fn, n);
     }
@@ -271,11 +277,16 @@ int check_overlap(const char *fn, int32_t n, const void *const *grads, void *con
         spans.push_back({to, to + bytes, i, true});
         if (in != to) spans.push_back({in, in + bytes, i, false});
     }
+    if (norm_in) {
+        const uintptr_t at = reinterpret_cast<uintptr_t>(norm_in);
+        spans.push_back({at, at + sizeof(float), -1, false});
+    }
     std::sort(spans.begin(), spans.end(), [](const Span &a, const Span &b) { return a.from < b.from; });
     uintptr_t any = 0, written = 0;  // furthest end so far, of all spans and of the written ones
     for (const Span &s : spans) {
         if (s.from < written || (s.written && s.from < any))
-            return ssg::fail(SSG_EINVAL, "%s: tensor %d overlaps another input or output", fn, s.tensor);
+            return s.tensor < 0 ? ssg::fail(SSG_EINVAL, "%s: norm_in overlaps an output", fn)
+                                : ssg::fail(SSG_EINVAL, "%s: tensor %d overlaps another input or output", fn, s.tensor);
         any = std::max(any, s.to);
         if (s.written) written = std::max(written, s.to);
     }
@@ -305,7 +316,7 @@ SSG_API int clip_grad_norm(int32_t n, const void *const *grads, void *const *out
     if (rc) return rc;
     if (!(max_norm >= 0.0)) return ssg::fail(SSG_EINVAL, "%s: max_norm=%g must be 0 or more", fn, max_norm);
     if (n > 0 && !outs) return ssg::fail(SSG_EINVAL, "%s: null list", fn);
-    if ((rc = check_overlap(fn, n, grads, outs, sizes, dtypes))) return rc;
+    if ((rc = check_overlap(fn, n, grads, outs, sizes, dtypes, norm_in))) return rc;
     if (!norm_in) {
         if (!norm || !aligned_to(norm, 4)) return ssg::fail(SSG_EINVAL, "%s: norm null or misaligned", fn);
         if ((rc = check_ws(fn, ws, ws_bytes, grad_norm_workspace_bytes(n)))) return rc;

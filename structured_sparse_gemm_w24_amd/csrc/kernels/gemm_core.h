@@ -236,8 +236,7 @@ __device__ __forceinline__ void mma(typename AccOf<KIND>::T &acc, u32x4 w, u32x8
 }
 
 // What place() found, as scalars: the same in every lane, but computed in vector registers it makes each
-// load loop over the lanes' buffer descriptors (dx of grouped.hip, 16384 x 1024 from 4096, 256 x 256 tiles,
-// 241 us).
+// load loop over the lanes' buffer descriptors.
 __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
 __device__ __forceinline__ const uint8_t *uniform(const uint8_t *p) {
     const uint64_t v = reinterpret_cast<uint64_t>(p);
@@ -283,7 +282,7 @@ struct Cfg {
     static constexpr bool DEEP = false;
 };
 // Four waves of 128 x 128 on a 256 x 256 tile (or TM x TN blocks each), a whole stage's fragments in
-// registers.
+// registers, so that a stage's buffer is free after the first quarter of its matrix instructions.
 template <int TM_, int TN_, int GM_, bool NTS_>
 struct CfgDeep : Cfg<2, 2, TM_, TN_, 2, GM_, NTS_, false> {
     static constexpr bool DEEP = true;

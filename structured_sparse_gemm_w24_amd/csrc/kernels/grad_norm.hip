@@ -8,8 +8,9 @@
 // graph.  A launch's tensors are cut into pieces of 16 KiB, which the workgroups of a grid of
 // fixed size take in turn; each writes one partial sum and the sums are added in a fixed
 // order.  So a launch walks through memory once from its first tensor to its last, and the
-// scaling walks back the same way: what the norm read last (256 MB) may still be cached.  Squares and sums are fp64: an fp32 gradient of 1e30 does not overflow,
-// and the order of summation shows in no digit of an fp32 norm.
+// scaling walks back the same way: what the norm read last (256 MB) may still be cached.  Squares and
+// sums are fp64: an fp32 gradient of 1e30 does not overflow, and the order of summation shows in no
+// digit of an fp32 norm.
 #include "elem.h"
 #include "launch.h"
 
@@ -191,13 +192,10 @@ int64_t pieces_of(const GradList &l, int i) {
 // The end of the entries from i on that go into one table (those before i, backwards: their start).
 template <int Most>
 int table_end(const GradList &l, int i, bool back) {
-    int64_t pieces = 0;
     for (int n = 0; back ? i > 0 : i < l.n; i += back ? -1 : 1) {
-        const int64_t here = pieces_of(l, back ? i - 1 : i);
-        if (here == 0) continue;
-        if (n == Most || (n > 0 && pieces + here >= (int64_t(1) << 31))) break;
+        if (l.sizes[back ? i - 1 : i] == 0) continue;
+        if (n == Most) break;
         ++n;
-        pieces += here;
     }
     return i;
 }

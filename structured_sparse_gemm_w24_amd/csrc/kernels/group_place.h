@@ -135,14 +135,19 @@ struct TileCost {
     }
 };
 
-// Tile rows that M rows in `groups` groups will need about: the host knows no group's length, so half a
-// tile is taken to be empty at the end of every group that an even choice would reach.
-inline double group_tile_rows(int64_t M, int64_t groups, int bm) {
-    if (groups == 1) return double((M + bm - 1) / bm);
-    const double live = double(groups) * (1.0 - std::exp(-double(M) / double(groups)));
-    const double rows = double(M) / bm + 0.5 * live;
-    return rows > live ? rows : live;
-}
+// M rows in `groups` groups, whose lengths the host does not know: how many an even choice would reach,
+// and the tile rows that they will need about, with half a tile empty at the end of each.
+struct GroupRowsGuess {
+    int64_t M, groups;
+    double live;
+    GroupRowsGuess(int64_t M_, int64_t groups_)
+        : M(M_), groups(groups_), live(double(groups_) * (1.0 - std::exp(-double(M_) / double(groups_)))) {}
+    double tiles(int bm) const {
+        if (groups == 1) return double((M + bm - 1) / bm);
+        const double rows = double(M) / bm + 0.5 * live;
+        return rows > live ? rows : live;
+    }
+};
 
 // The cheapest of N tiles: tiles(bm, bn) says how many a launch has.
 template <int N, class F>

@@ -162,7 +162,8 @@ hipError_t rows_cfg(const Grouped &a, const void *A, int64_t lda, void *C, int64
 // Entry of kFwdTiles, kDxTiles (TW) and kDwTiles for a product.
 template <bool TW>
 int rows_tile(int64_t M, int64_t experts, int64_t N, int64_t K) {
-    auto count = [&](int bm, int bn) { return group_tile_rows(M, experts, bm) * double((N + bn - 1) / bn); };
+    const GroupRowsGuess guess(M, experts);
+    auto count = [&](int bm, int bn) { return guess.tiles(bm) * double((N + bn - 1) / bn); };
     const double stages = double((K + 63) / 64);
     if constexpr (TW) return cheapest(kDxTiles, stages, count);
     else return cheapest(kFwdTiles, stages, count);
@@ -196,11 +197,11 @@ WeightsPlan weights_plan(int64_t M, int64_t experts, int64_t N, int64_t K) {
 constexpr struct {
     TileCost dx, dw;
 } kBothTiles[] = {{kDxTiles[0], kDwTiles[0]}, {kDxTiles[2], kDwTiles[1]}, {kDxTiles[3], kDwTiles[3]}};
-int both_tile(int64_t M, int64_t experts, int64_t N, int64_t K) {
-    const WeightsPlan pl = weights_plan(M, experts, N, K);
+int both_tile(const WeightsPlan &pl, int64_t M, int64_t experts, int64_t N, int64_t K) {
     if (pl.splits > 1) return -1;
     const double sx = double((N + 63) / 64), even = double(M) / double(experts) / 64.0 + 0.5, sw = even < 1.0 ? 1.0 : even;
-    auto count_x = [&](int bm, int bn) { return group_tile_rows(M, experts, bm) * double((K + bn - 1) / bn); };
+    const GroupRowsGuess guess(M, experts);
+    auto count_x = [&](int bm, int bn) { return guess.tiles(bm) * double((K + bn - 1) / bn); };
     auto count_w = [&](int bm, int bn) {
         return double(experts) * double((N + bm - 1) / bm) * double((K + bn - 1) / bn);
     };
@@ -278,8 +279,7 @@ hipError_t weights_any(const Grouped &a, const WeightsPlan &pl, hipStream_t st) 
 }
 
 template <int KIND>
-hipError_t weights(const Grouped &a, hipStream_t st) {
-    const WeightsPlan pl = weights_plan(a.M, a.experts, a.N, a.K);
+hipError_t weights(const Grouped &a, const WeightsPlan &pl, hipStream_t st) {
     if (pl.splits == 1) return weights_any<KIND, false>(a, pl, st);
     hipError_t e = weights_any<KIND, true>(a, pl, st);
     if (e != hipSuccess) return e;
@@ -325,8 +325,9 @@ hipError_t both_cfg(const Grouped &a, hipStream_t st) {
 
 template <int KIND>
 hipError_t backward(const Grouped &a, hipStream_t st) {
+    const WeightsPlan pl = weights_plan(a.M, a.experts, a.N, a.K);
     if (a.dx && a.dw && a.M > 0) {
-        switch (both_tile(a.M, a.experts, a.N, a.K)) {
+        switch (both_tile(pl, a.M, a.experts, a.N, a.K)) {
             case 0: return both_cfg<KIND, Cfg32x64>(a, st);
             case 1: return both_cfg<KIND, Cfg64x128P>(a, st);
             case 2: return both_cfg<KIND, Cfg128x128P>(a, st);
@@ -337,26 +338,28 @@ hipError_t backward(const Grouped &a, hipStream_t st) {
         const hipError_t e = rows<KIND, true>(a, a.dy, a.lddy, a.dx, a.lddx, int(a.K), int(a.N), st);
         if (e != hipSuccess) return e;
     }
-    return a.dw ? weights<KIND>(a, st) : hipSuccess;
+    return a.dw ? weights<KIND>(a, pl, st) : hipSuccess;
 }
 
 }  // namespace
 
-int64_t grouped_blocks(int64_t M, int64_t experts, int64_t N, int64_t K) {
+int64_t grouped_blocks(int64_t M, int64_t experts, int64_t N, int64_t K, bool backward) {
     auto of_rows = [&](const TileCost &t, int64_t n) { return group_tiles(M, experts, t.bm, (n + t.bn - 1) / t.bn); };
+    auto of_weights = [&](const TileCost &t) {
+        return experts * ((N + t.bm - 1) / t.bm) * ((K + t.bn - 1) / t.bn);
+    };
+    if (!backward) return of_rows(kFwdTiles[rows_tile<false>(M, experts, N, K)], N);
     const WeightsPlan pl = weights_plan(M, experts, N, K);
-    const TileCost &w = kDwTiles[pl.tile];
-    const int64_t fwd = of_rows(kFwdTiles[rows_tile<false>(M, experts, N, K)], N);
+    const int both = both_tile(pl, M, experts, N, K);
     const int64_t dx = of_rows(kDxTiles[rows_tile<true>(M, experts, K, N)], K);
-    int64_t dw = pl.splits * experts * ((N + w.bm - 1) / w.bm) * ((K + w.bn - 1) / w.bn);
-    const int both = both_tile(M, experts, N, K);
-    if (both >= 0) {  // (dx and dw of its tile in one launch)
+    int64_t most = pl.splits * of_weights(kDwTiles[pl.tile]);
+    if (dx > most) most = dx;
+    if (both >= 0) {
         const TileCost &t = kBothTiles[both].dx;
-        const int64_t all = of_rows(t, K) + 8 + experts * ((N + t.bm - 1) / t.bm) * ((K + t.bn - 1) / t.bn);
-        if (all > dw) dw = all;
+        const int64_t all = of_rows(t, K) + 8 + of_weights(t);
+        if (all > most) most = all;
     }
-    const int64_t most = fwd > dx ? fwd : dx;
-    return most > dw ? most : dw;
+    return most;
 }
 
 int64_t grouped_slices_bytes(int64_t M, int64_t experts, int64_t N, int64_t K) {

@@ -179,8 +179,8 @@ hipError_t launch_grouped_fwd(const Grouped &a, hipStream_t st);
 hipError_t launch_grouped_bwd(const Grouped &a, hipStream_t st);
 // fp32 slices of dw's split sums (0: not split)
 int64_t grouped_slices_bytes(int64_t M, int64_t experts, int64_t N, int64_t K);
-// workgroups of the largest of the launches of these sizes
-int64_t grouped_blocks(int64_t M, int64_t experts, int64_t N, int64_t K);
+// workgroups of the forward launch, or of the largest of the backward ones
+int64_t grouped_blocks(int64_t M, int64_t experts, int64_t N, int64_t K, bool backward);
 
 // Microscaled 4-bit floating point (formulas in mxfp4.hip).  Packed rows hold kp
 // values, a multiple of 128: kp / 2 code bytes and kp / 32 scale bytes.

@@ -213,9 +213,8 @@ constexpr TileCost kMxTiles[] = {{32, 32, 6, 4.5f, 2.2f, 0.10f},   {64, 64, 4, 4
 
 // (experts 0: one product)
 int mx_tile(int64_t M, int64_t experts, int64_t N, int64_t K) {
-    auto count = [&](int bm, int bn) {
-        return group_tile_rows(M, experts ? experts : 1, bm) * double((N + bn - 1) / bn);
-    };
+    const GroupRowsGuess guess(M, experts ? experts : 1);
+    auto count = [&](int bm, int bn) { return guess.tiles(bm) * double((N + bn - 1) / bn); };
     return cheapest(kMxTiles, double((K + 255) / 256), count);
 }
 

@@ -71,7 +71,7 @@ def _clip(r, grads=(4096,), sizes=(8,), types=(F16,), outs=None, most=1.0, norm_
     (lambda r: _fwd(r, k=4), "multiples of 8"),
     (lambda r: _fwd(r, n=1 << 22), "2^22"),
     (lambda r: _fwd(r, n=1 << 16, k=1 << 15, ldx=1 << 15, ldo=1 << 16), "2 GiB"),
-    (lambda r: _fwd(r, m=1 << 31), "2^31"),
+    (lambda r: _fwd(r, m=1 << 29), "2^29"),
     (lambda r: _fwd(r, experts=0), "experts=0"),
     (lambda r: _fwd(r, experts=65536), "experts=65536"),
     (lambda r: _fwd(r, offsets=None), "offsets"),
@@ -83,7 +83,7 @@ def _clip(r, grads=(4096,), sizes=(8,), types=(F16,), outs=None, most=1.0, norm_
     (lambda r: _fwd(r, x=24), "16-byte aligned"),
     (lambda r: _fwd(r, w=None), "w null"),
     (lambda r: _fwd(r, out=None), "out null"),
-    (lambda r: _fwd(r, m=(1 << 31) - 1, n=1 << 20, ldo=1 << 20), "too large"),
+    (lambda r: _fwd(r, m=(1 << 29) - 1, n=1 << 20, ldo=1 << 20), "too large"),
     (lambda r: _bwd(r, dy=None), "dy null"),
     (lambda r: _bwd(r, lddy=60), "row stride"),
     (lambda r: _bwd(r, w=None), "w null"),
@@ -105,6 +105,9 @@ def _clip(r, grads=(4096,), sizes=(8,), types=(F16,), outs=None, most=1.0, norm_
     (lambda r: _dequant(r, ldo=64), "row stride"),
     (lambda r: _gemm(r, dtype=5), "unknown dtype"),
     (lambda r: _gemm(r, n=0), "N=0"),
+    (lambda r: _gemm(r, m=1 << 29), "2^29"),
+    (lambda r: _gemm(r, m=(1 << 29) - 64, n=1 << 21, k=128, ldo=1 << 21), "too large"),
+    (lambda r: _quant(r, m=(1 << 31) - 1, k=1000, ldx=1000), "2^36"),
     (lambda r: _gemm(r, experts=2), "without offsets"),
     (lambda r: _gemm(r, offsets=16, experts=0), "experts=0"),
     (lambda r: _gemm(r, a=None), "codes of a"),
@@ -134,6 +137,9 @@ def _clip(r, grads=(4096,), sizes=(8,), types=(F16,), outs=None, most=1.0, norm_
     (lambda r: _clip(r, grads=(4096, 8192), outs=(12288, 12296), sizes=(8, 8), types=(F16, F16)), "overlaps"),
     (lambda r: _clip(r, norm=None), "norm null"),
     (lambda r: _clip(r, norm_in=18), "norm_in"),
+    (lambda r: _clip(r, norm_in=4108), "norm_in overlaps"),
+    (lambda r: _norm(r, grads=(4096,) * 5, sizes=((1 << 40) - 1,) * 5, types=(F32,) * 5), "16 TiB"),
+    (lambda r: r.grad_norm((1 << 20) + 1, _p(16), _p(16), _p(16), _p(16), _p(16), 1 << 30, None), "2^20"),
 ])
 def test_refused_on_host(lib, call, msg):
     raw = lib.load()
@@ -164,7 +170,7 @@ def test_workspace_sizes(lib):
     assert raw.grouped_gemm_backward_workspace_bytes(0, 16384, 4096, 1024) == 0
     assert raw.grouped_gemm_backward_workspace_bytes(2, 100, 60, 64) == 0
     for e in (1, 2, 7, 64):
-        for m in (0, 1, 100, 5000, 100000, (1 << 31) - 1):
+        for m in (0, 1, 100, 5000, 100000, (1 << 29) - 1):
             for n, k in ((8, 8), (64, 720), (1024, 1024), (8192, 4096)):
                 w = raw.grouped_gemm_backward_workspace_bytes(e, m, n, k)
                 assert w % (e * n * k * 4) == 0 and w <= 256 << 20
