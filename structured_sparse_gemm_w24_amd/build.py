@@ -40,7 +40,7 @@ HOST_SOURCES = ["status.cpp", "pack.cpp"]
 HIP_SOURCES = ["api.hip", "kernels/gemm.hip", "kernels/splitk.hip", "kernels/tw_gemm.hip",
                "kernels/tw_gemm_i8.hip", "kernels/transpose.hip", "api_tune.hip", "kernels/layer_norm.hip",
                "kernels/low_rank.hip", "kernels/low_rank_gemm.hip", "kernels/loss.hip",
-               "api_expert.hip", "kernels/grouped.hip", "kernels/mxfp4.hip", "kernels/grad_norm.hip"]
+               "api_expert.hip", "kernels/grouped.hip", "kernels/mxfp4.hip", "kernels/mxfp4_few.hip", "kernels/grad_norm.hip"]
 
 
 def _obj(src):

@@ -224,6 +224,11 @@ SSG_API int mxfp4_linear(int32_t dtype, const void *x, int64_t ldx, const uint8_
     if ((rc = check_any(fn, "x", x, ldx, M, K, dtype)) ||
         (rc = check_ws(fn, ws, ws_bytes, mxfp4_linear_workspace_bytes(M, K))) || (rc = check_device()))
         return rc;
+    if (ssg::mxfp4_few_kind(M, offsets ? experts : 0, N, K) >= 0) {
+        const ssg::Mxfp4Gemm g{static_cast<const uint8_t *>(x), nullptr, w, w_scales, offsets, experts, dtype, out, ldo, M,
+                               N, K};
+        return launched(ssg::launch_mxfp4_few(g, dtype, ldx, hipStream_t(stream)), fn);
+    }
     uint8_t *codes = static_cast<uint8_t *>(ws), *scales = codes + M * (ssg::mxfp4_padded(K) / 2);
     const hipError_t e = ssg::launch_mxfp4_quantize(dtype, x, ldx, codes, scales, M, K, hipStream_t(stream));
     if (e != hipSuccess) return launched(e, fn);

@@ -197,6 +197,10 @@ struct Mxfp4Gemm {
     int64_t ldo, M, N, K;
 };
 hipError_t launch_mxfp4_gemm(const Mxfp4Gemm &g, hipStream_t st);
+// The same for few rows, in one launch with the quantisation: a is x [M][K] of x_dtype with row stride
+// ldx, or (x_dtype -1) packed.  The kind says which tile, below 0: the product is not for it.
+hipError_t launch_mxfp4_few(const Mxfp4Gemm &g, int x_dtype, int64_t ldx, hipStream_t st);
+int mxfp4_few_kind(int64_t M, int64_t experts, int64_t N, int64_t K);
 // workgroups of a product (experts 0: of all rows with one weight)
 int64_t mxfp4_blocks(int64_t M, int64_t experts, int64_t N, int64_t K);
 inline int64_t mxfp4_padded(int64_t K) { return (K + 127) / 128 * 128; }

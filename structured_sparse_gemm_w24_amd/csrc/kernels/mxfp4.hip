@@ -17,36 +17,11 @@
 #include "gemm_tiles.h"
 #include "group_place.h"
 #include "launch.h"
+#include "mx_codes.h"
 
 namespace ssg {
 
 namespace {
-
-__device__ __forceinline__ uint32_t magnitude_bits(float f) { return __builtin_bit_cast(uint32_t, f) & 0x7fffffffu; }
-
-template <int CTRL>
-__device__ __forceinline__ uint32_t dpp(uint32_t v) {
-    return uint32_t(__builtin_amdgcn_update_dpp(int(v), int(v), CTRL, 0xf, 0xf, false));
-}
-
-// Scale byte of the block whose largest magnitude has these bits.
-__device__ __forceinline__ uint32_t scale_byte(uint32_t top) {
-    const uint32_t e = top >> 23;
-    return e == 255 ? 255u : e > 2 ? e - 2 : 0u;
-}
-
-// Eight values to eight codes.  x / scale is exact (a power of two, and what becomes
-// subnormal rounds to code 0 either way); a block that is not finite keeps codes 0.
-__device__ __forceinline__ uint32_t codes_of(const float (&f)[8], uint32_t byte) {
-    if (byte == 255) return 0;
-    const float by = __builtin_bit_cast(float, (254u - byte) << 23);
-    uint32_t c = 0;
-    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, f[0] * by, f[1] * by, 1.0f, 0);
-    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, f[2] * by, f[3] * by, 1.0f, 1);
-    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, f[4] * by, f[5] * by, 1.0f, 2);
-    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, f[6] * by, f[7] * by, 1.0f, 3);
-    return c;
-}
 
 // The piece `at` behind the first one of a workgroup, which is piece c0 of row m0 (one 64-bit division a
 // workgroup).
@@ -85,20 +60,17 @@ mx_quantize_kernel(const T *__restrict__ x, int64_t ldx, uint32_t *__restrict__ 
     for (int u = 0; u < U; ++u) {
         const int64_t i = first + u * 256 + threadIdx.x;
         if (i >= all) return;  // (a row's pieces are a multiple of 16: whole groups of lanes leave)
-        float f[8];
+        Top<T> most;
 #pragma unroll
         for (int j = 0; j < 8 / V; ++j) {
-            const typename Elem<T>::Vec w = settle<T, TAIL>(v[u][j], col[u] + j * V, K);
-#pragma unroll
-            for (int q = 0; q < V; ++q) f[j * V + q] = float(w[q]);
+            v[u][j] = settle<T, TAIL>(v[u][j], col[u] + j * V, K);
+            most.add(v[u][j]);
         }
-        uint32_t top = 0;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) top = max(top, magnitude_bits(f[j]));
+        uint32_t top = most.bits();
         top = max(top, dpp<0xb1>(top));  // (quad permutations: lanes ^ 1, ^ 2)
         top = max(top, dpp<0x4e>(top));
         const uint32_t byte = scale_byte(top);
-        codes[i] = codes_of(f, byte);
+        codes[i] = codes_of<T>(v[u], byte);
         uint32_t word = byte << (8 * ((threadIdx.x >> 2) & 3));
         word |= dpp<0x124>(word);  // (row rotations by 4 and 8: all four quads of the row)
         word |= dpp<0x128>(word);
@@ -126,7 +98,7 @@ mx_dequantize_kernel(const uint32_t *__restrict__ codes, const uint8_t *__restri
         const Place p = piece_at(m0, c0, uint32_t(at), uint32_t(pieces));
         const int64_t m = p.m, c = p.c;
         const uint32_t b = byte[u], v = word[u];
-        const float s = __builtin_bit_cast(float, b == 0 ? 0x00400000u : b == 255 ? 0x7fc00000u : b << 23);
+        const float s = b == 255 ? __builtin_nanf("") : scale_of(b);
         typedef float f2 __attribute__((ext_vector_type(2)));
         const f2 p0 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(v, 1.0f, 0);
         const f2 p1 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(v, 1.0f, 1);
@@ -260,10 +232,48 @@ hipError_t dequantize(const uint8_t *codes, const uint8_t *scales, void *out, in
 
 }  // namespace
 
+// One launch for few rows (mxfp4_few.hip): its tiles of 32 rows, and what one costs in us for each unit of
+// 256 k of a wave's, for a unit of a CU's share of all tiles, and for eight of a CU's waves.
+struct FewCost {
+    int bn, waves;
+    float start, unit, load, waves8;
+};
+// with up to 8 rows a tile, and with more
+constexpr FewCost kFewTiles[2][3] = {
+    {{32, 4, 2.8f, 0.85f, 0.21f, 0.70f}, {32, 8, 2.4f, 1.05f, 0.20f, 1.35f}, {64, 4, 2.65f, 1.25f, 0.44f, 0.80f}},
+    {{32, 4, 2.8f, 2.20f, 0.35f, 0.70f}, {32, 8, 2.4f, 2.60f, 0.41f, 1.35f}, {64, 4, 2.65f, 2.75f, 0.48f, 0.80f}}};
+
+// The choice between one launch and two (quantisation and product: 1.76 times the product's estimate less
+// 4.6) by least estimate, fitted as TileCost's: over 220 random calls of 1 to 362 rows the choice takes
+// 1.02 times the best of all four, two launches 1.29.  A packed operand goes the same way, so that the
+// product of quantised rows is the same bit for bit.  (Past the fit, and with more than 2000 units of full
+// tiles, always two: 334 rows of 22 experts, 7040 x 500, 16.2 us and 29.5.)
+int mxfp4_few_kind(int64_t M, int64_t experts, int64_t N, int64_t K) {
+    if (M > 512) return -1;
+    const GroupRowsGuess guess(M, experts ? experts : 1);
+    const double tiles = guess.tiles(32), units = double((K + 255) / 256);
+    const bool full = double(M) > 8.0 * tiles;
+    auto columns = [&](int bn) { return double((N + bn - 1) / bn); };
+    if (full && tiles * columns(32) * units > 2000.0) return -1;
+    const TileCost &two = kMxTiles[mx_tile(M, experts, N, K)];
+    double least = 1.76 * two.us(guess.tiles(two.bm) * columns(two.bn), units) - 4.6;
+    int best = -1;
+    for (int i = 0; i < 3; ++i) {
+        const FewCost &c = kFewTiles[full][i];
+        const double all = tiles * columns(c.bn), each = double((int64_t(units) + c.waves - 1) / c.waves);
+        const double us = c.start + (experts ? 0.45 : 0.0) + each * c.unit + all * units / 256.0 * c.load +
+                          all * c.waves / 2048.0 * c.waves8;
+        if (us < least) best = i, least = us;
+    }
+    return best;
+}
+
 int64_t mxfp4_blocks(int64_t M, int64_t experts, int64_t N, int64_t K) {
+    const int few = mxfp4_few_kind(M, experts, N, K);
     const TileCost &t = kMxTiles[mx_tile(M, experts, N, K)];
-    const int64_t tiles_n = (N + t.bn - 1) / t.bn;
-    return experts ? group_tiles(M, experts, t.bm, tiles_n) : (M + t.bm - 1) / t.bm * tiles_n;
+    const int bm = few < 0 ? t.bm : 32, bn = few < 0 ? t.bn : kFewTiles[0][few].bn;
+    const int64_t tiles_n = (N + bn - 1) / bn;
+    return experts ? group_tiles(M, experts, bm, tiles_n) : (M + bm - 1) / bm * tiles_n;
 }
 
 hipError_t launch_mxfp4_quantize(int dtype, const void *x, int64_t ldx, uint8_t *codes, uint8_t *scales, int64_t M,
@@ -281,6 +291,7 @@ hipError_t launch_mxfp4_dequantize(int dtype, const uint8_t *codes, const uint8_
 }
 
 hipError_t launch_mxfp4_gemm(const Mxfp4Gemm &g, hipStream_t st) {
+    if (mxfp4_few_kind(g.M, g.offsets ? g.experts : 0, g.N, g.K) >= 0) return launch_mxfp4_few(g, -1, 0, st);
     if (g.dtype == DT_F16) return gemm_epi<EPI_F16>(g, st);
     if (g.dtype == DT_BF16) return gemm_epi<EPI_BF16>(g, st);
     return gemm_epi<EPI_F32>(g, st);

@@ -109,6 +109,36 @@ def test_quantize_extremes(lib, gpu):
     assert np.isnan(back[6:9]).all() and np.array_equal(back, ref_values(*want, 32), equal_nan=True)
 
 
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+def test_quantize_every_16_bit_value(lib, gpu, dt):
+    """Each bit pattern, in blocks of its neighbours, of values up to 2^5 times as large and beside its
+    ties: quantised in a call of its own and inside a product of few rows and of many."""
+    import torch
+    bits = torch.arange(65536, dtype=torch.int32).to(torch.int16)
+    near = bits.view(_dt(dt)).view(2048, 32)
+    g = torch.Generator().manual_seed(7)
+    finite = near.flatten()[torch.isfinite(near.flatten())]
+    spread = finite[torch.randint(0, len(finite), (4096, 32), generator=g)].double()
+    top = spread[:, :1].abs()
+    spread = (top * 2.0 ** torch.randint(-5, 1, (4096, 32), generator=g) * (1 + torch.rand(4096, 32, generator=g) / 2))
+    ties = top * torch.tensor([0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0, 4.0] * 4) / 4
+    x = torch.cat([near, spread.to(_dt(dt)), ties.to(_dt(dt))])
+    codes, scales = lib.mxfp4_quantize(x.cuda())
+    want = ref_quantize(x.double().numpy())
+    assert np.array_equal(_cpu(scales), want[1]) and np.array_equal(_cpu(codes), want[0])
+    # a product with 1 at one place of each block gives that value back
+    eye = torch.zeros(32, 32)
+    eye.fill_diagonal_(1.0)
+    w = lib.mxfp4_quantize(eye.cuda())
+    values = torch.from_numpy(ref_values(*want, 32)).to(_dt(dt))
+    values[values.isnan().any(1)] = float("nan")
+    for at in list(range(0, len(x), 512)) + [None]:
+        part = x if at is None else x[at:at + 31]
+        got = lib.mxfp4_linear(part.cuda(), *w).cpu()
+        assert torch.equal(got.isnan(), values[at:at + 31].isnan() if at is not None else values.isnan())
+        assert torch.equal(got.nan_to_num(), (values if at is None else values[at:at + 31]).nan_to_num())
+
+
 def test_dequantize_every_code_and_scale(lib, gpu):
     import torch
     codes = torch.arange(256, dtype=torch.int32).to(torch.uint8).view(1, 256).repeat(256, 1)
@@ -173,6 +203,25 @@ def test_linear(lib, gpu, m, n, k, dt):
         assert keep.any()
         got, a = got[:, :].cpu()[np.flatnonzero(keep)], a[keep]
     _close(got, a, w, dt)
+
+
+# rows that share a tile of 32 in every way that it takes them, K of one and of many units of 256 values,
+# whole, half and odd
+@pytest.mark.parametrize("m", [1, 2, 3, 8, 9, 32, 33, 70])
+@pytest.mark.parametrize("n,k", [(1, 3), (33, 128), (70, 385), (40, 1030), (96, 2500), (130, 5001), (31, 8320)])
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+def test_few_rows(lib, gpu, m, n, k, dt):
+    import torch
+    wide = _random(m, k + 5, "f32", m + n).clamp(-8, 8).to(_dt(dt)).cuda()
+    x = wide[:, 3:3 + k]  # (rows at any element)
+    codes, scales = _weight(n, k, n + m)
+    out = torch.full((m, n + 3), 5.0, dtype=_dt(dt), device="cuda")
+    lib.mxfp4_linear(x, codes.cuda(), scales.cuda(), out=out[:, 1:1 + n])
+    packed = lib.mxfp4_quantize(x)
+    assert torch.equal(out[:, 1:1 + n], lib.mxfp4_gemm(*packed, codes.cuda(), scales.cuda(), k, _dt(dt)))
+    assert bool((out[:, 0] == 5).all()) and bool((out[:, 1 + n:] == 5).all())
+    a = ref_values(*ref_quantize(_cpu(x.double())), k)
+    _close(out[:, 1:1 + n], a, ref_values(codes.numpy(), scales.numpy(), k), dt)
 
 
 @pytest.mark.parametrize("m,n,k", [(3, 70, 200), (40, 65, 513), (200, 131, 129), (600, 300, 256)])
