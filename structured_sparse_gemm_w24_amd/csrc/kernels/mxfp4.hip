@@ -35,8 +35,8 @@ __device__ __forceinline__ Place piece_at(int64_t m0, uint32_t c0, uint32_t at, 
 }
 
 // Pieces of eight values: four threads share a block, sixteen a word of four scales.  Each thread takes
-// two, 256 apart, and has both loads under way before the first is used (8192 x 4096 bf16 17.8 us = 4.8
-// TB/s, a kernel that only reads and writes as much 16.3; one piece a thread 19.5, four 20.1).
+// two, 256 apart, and has both loads under way before the first is used (8192 x 4096 fp16 16.5 us = 5.1
+// TB/s, and 13.8 back; converted by way of fp32 bf16 took 17.8, one piece a thread 19.5, four 20.1).
 constexpr int U = 2;
 template <class T, bool TAIL>
 __global__ void __launch_bounds__(256)
@@ -244,8 +244,9 @@ constexpr FewCost kFewTiles[2][3] = {
     {{32, 4, 2.8f, 2.20f, 0.35f, 0.70f}, {32, 8, 2.4f, 2.60f, 0.41f, 1.35f}, {64, 4, 2.65f, 2.75f, 0.48f, 0.80f}}};
 
 // The choice between one launch and two (quantisation and product: 1.76 times the product's estimate less
-// 4.6) by least estimate, fitted as TileCost's: over 220 random calls of 1 to 362 rows the choice takes
-// 1.02 times the best of all four, two launches 1.29.  A packed operand goes the same way, so that the
+// 4.6) by least estimate, fitted as TileCost's: over 220 random calls of 1 to 362 rows, in graphs, the
+// choice takes 1.02 times the best of all four, two launches 1.29.  (Here with 1 us more for the second
+// launch, which costs the host 4: 32 rows of 32 experts, 2048 x 1024, 10.6 us and 11.2 in a graph.)  A packed operand goes the same way, so that the
 // product of quantised rows is the same bit for bit.  (Past the fit, and with more than 2000 units of full
 // tiles, always two: 334 rows of 22 experts, 7040 x 500, 16.2 us and 29.5.)
 int mxfp4_few_kind(int64_t M, int64_t experts, int64_t N, int64_t K) {
@@ -256,7 +257,7 @@ int mxfp4_few_kind(int64_t M, int64_t experts, int64_t N, int64_t K) {
     auto columns = [&](int bn) { return double((N + bn - 1) / bn); };
     if (full && tiles * columns(32) * units > 2000.0) return -1;
     const TileCost &two = kMxTiles[mx_tile(M, experts, N, K)];
-    double least = 1.76 * two.us(guess.tiles(two.bm) * columns(two.bn), units) - 4.6;
+    double least = 1.76 * two.us(guess.tiles(two.bm) * columns(two.bn), units) - 3.6;
     int best = -1;
     for (int i = 0; i < 3; ++i) {
         const FewCost &c = kFewTiles[full][i];
