@@ -246,7 +246,7 @@ constexpr FewCost kFewTiles[2][3] = {
 // The choice between one launch and two (quantisation and product: 1.76 times the product's estimate less
 // 4.6) by least estimate, fitted as TileCost's: over 220 random calls of 1 to 362 rows, in graphs, the
 // choice takes 1.02 times the best of all four, two launches 1.29.  (Here with 1 us more for the second
-// launch, which costs the host 4: 32 rows of 32 experts, 2048 x 1024, 10.6 us and 11.2 in a graph.)  A packed operand goes the same way, so that the
+// launch, which costs the host 4: 32 rows of 32 experts, 2048 x 1024, 9.4 us a call and 12.7.)  A packed operand goes the same way, so that the
 // product of quantised rows is the same bit for bit.  (Past the fit, and with more than 2000 units of full
 // tiles, always two: 334 rows of 22 experts, 7040 x 500, 16.2 us and 29.5.)
 int mxfp4_few_kind(int64_t M, int64_t experts, int64_t N, int64_t K) {
