@@ -161,7 +161,7 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const void *base, ui
 __device__ __forceinline__ void dma16(__amdgpu_buffer_rsrc_t r, uint32_t off, uint8_t *wave_base) {
     __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_ptr_t)wave_base, 16, off, 0, 0, 0);
 }
-// (the same at `off` + `more`, the latter uniform)
+// (the same at `off` + `more`, the latter uniform; only `off` is checked against the buffer's size)
 __device__ __forceinline__ void dma16s(__amdgpu_buffer_rsrc_t r, uint32_t off, uint32_t more, uint8_t *wave_base) {
     __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_ptr_t)wave_base, 16, off, more, 0, 0);
 }

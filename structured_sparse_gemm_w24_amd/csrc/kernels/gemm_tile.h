@@ -213,13 +213,17 @@
             return;
         }
         if constexpr (CF::DEEP && decltype(whole)::value) {
-            // (the stage in the scalar offset)
-            const uint32_t more_w = Extra::kTransW ? uint32_t(sg) * uint32_t(ldw_of(extra) * 128) : uint32_t(sg * WB);
+            // The stage in the scalar offset, which the buffer's range check leaves out: only for operands
+            // whose rows a whole stage never leaves.  (A transposed W is read past its last row's end where
+            // the tile is wider, and the check has to see all of the offset.)
 #pragma unroll
             for (int j = 0; j < LY::LA; ++j) dma16s(bufA, oa[j], uint32_t(sg * LY::AB), base + (j * LY::NL + wave) * 1024);
 #pragma unroll
-            for (int j = 0; j < LY::LW; ++j)
-                dma16s(bufW, ow[j], more_w, base + A_STAGE + (j * LY::NL + wave) * 1024);
+            for (int j = 0; j < LY::LW; ++j) {
+                uint8_t *const to = base + A_STAGE + (j * LY::NL + wave) * 1024;
+                if constexpr (Extra::kTransW) dma16(bufW, ow[j] + uint32_t(sg) * uint32_t(ldw_of(extra) * 128), to);
+                else dma16s(bufW, ow[j], uint32_t(sg * WB), to);
+            }
             return;
         }
 #pragma unroll
