@@ -575,11 +575,14 @@ int grad_norm(int32_t n, const void *const *grads, const int64_t *sizes, const i
               int64_t ws_bytes, void *stream);
 
 /* outs[i] = grads[i] min(1, max_norm / (norm + 1e-6)), the factor rounded to fp32
- * and the product once to the tensor's type; outs[i] is grads[i] (in place;
- * not touched where the factor is 1) or a buffer that overlaps no tensor of the
- * call (refused).  norm_in null: norm is grad_norm's and written to norm[0];
+ * (below 2^-126, that of a huge norm, it is fp64's), the product to fp32 and then to
+ * the tensor's type; outs[i] is grads[i] (in place; not touched where the factor is 1)
+ * or a buffer that overlaps no tensor of the call (refused).  norm_in null: the
+ * gradients are clipped by the square root of their fp64 sum of squares, also where
+ * that passes fp32, and grad_norm's result (then infinite) is written to norm[0];
  * else norm_in[0] (device, e.g. summed over ranks, in no output) is the norm, and
- * norm and ws may be null.  An infinite norm makes the factor 0, a NaN one makes it NaN.
+ * norm and ws may be null.  An infinite norm (an infinite gradient, or norm_in) makes
+ * the factor 0, whatever max_norm is, a NaN one makes it NaN.
  * The same element in two entries is refused when it would be scaled twice. */
 int clip_grad_norm(int32_t n, const void *const *grads, void *const *outs, const int64_t *sizes,
                    const int32_t *dtypes, double max_norm, const float *norm_in, float *norm, void *ws,

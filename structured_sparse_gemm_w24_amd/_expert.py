@@ -269,7 +269,8 @@ def grad_norm(grads, workspace=None):
 
 def clip_grad_norm(grads, max_norm, norm=None, out=None, workspace=None):
     """Every gradient times min(1, max_norm / (norm + 1e-6)): returns (norm, clipped).  norm: grad_norm of
-    the list, or a float32 scalar tensor to clip by instead (one that was reduced over ranks).  out: the
+    the list, or a float32 scalar tensor to clip by instead (one that was reduced over ranks); an infinite one
+    makes the factor 0.  (The list's own norm clips in 64 bits, also where float32 holds it as infinite.)  out: the
     tensors to write, grads themselves for clipping in place (left untouched where nothing is clipped);
     None makes new ones.  Tensors that share elements with one that is written are refused."""
     torch = _torch()

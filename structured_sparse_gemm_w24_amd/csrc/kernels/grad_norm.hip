@@ -12,6 +12,9 @@
 // sums are fp64: an fp32 gradient of 1e30 does not overflow, and the order of summation shows in no
 // digit of an fp32 norm.  290 tensors of 120 M values (720 MB to read, read again and write): 205 us in five
 // launches, 5.2 TB/s of what a copy of that size takes 209 for.
+#include <cfloat>
+#include <cmath>
+
 #include "elem.h"
 #include "launch.h"
 
@@ -81,8 +84,9 @@ __device__ __forceinline__ void piece_squares(double &sum, const void *p, int64_
     for (int i = 0; i < 4; ++i) add_squares<T>(sum, v[i]);
 }
 
-template <class T>
-__device__ __forceinline__ void piece_scale(float by, const void *p, void *q, int64_t at, int64_t n) {
+// F: the factor's type.  The product is rounded to fp32 and then to T.
+template <class T, class F>
+__device__ __forceinline__ void piece_scale(F by, const void *p, void *q, int64_t at, int64_t n) {
     constexpr int V = Elem<T>::V, STEP = kThreads * V;
     const T *x = static_cast<const T *>(p) + at;
     T *y = static_cast<T *>(q) + at;
@@ -97,7 +101,7 @@ __device__ __forceinline__ void piece_scale(float by, const void *p, void *q, in
             float f[V];
             to_float<T>(v[i], f);
 #pragma unroll
-            for (int j = 0; j < V; ++j) f[j] *= by;
+            for (int j = 0; j < V; ++j) f[j] = float(F(f[j]) * by);
             store_stream<T, false>(y, c + i * STEP, 4 * STEP, f);
         }
     } else {
@@ -108,7 +112,7 @@ __device__ __forceinline__ void piece_scale(float by, const void *p, void *q, in
             float f[V];
             to_float<T>(v[i], f);
 #pragma unroll
-            for (int j = 0; j < V; ++j) f[j] *= by;
+            for (int j = 0; j < V; ++j) f[j] = float(F(f[j]) * by);
             store_stream<T, true>(y, c + i * STEP, room, f);
         }
     }
@@ -170,20 +174,16 @@ norm_finish_kernel(const double *__restrict__ part, int slots, float *__restrict
 // of every launch, which is quadratic in the tensors (12000 of 100 KB, in a graph, 1.55 ms so and 3.86; 950 of them
 // 119 us and 127; 290 of 800 KB 136 and 137).
 constexpr int kOwnSlots = kThreads;
-__global__ void __launch_bounds__(kThreads)
-clip_kernel(ClipTable t, double max_norm, const float *__restrict__ norm_in, const double *__restrict__ part, int slots,
-            float *__restrict__ norm) {
-    __shared__ double red[kThreads / 64];
-    const double n = norm_in ? double(norm_in[0]) : sqrt(sum_of<kThreads>(part, slots, red));
-    if (norm && blockIdx.x == 0 && threadIdx.x == 0) norm[0] = float(n);
-    const double c = max_norm / (n + kEps);
-    const float by = c > 1.0 ? 1.0f : float(c);  // (a NaN stays one)
+
+// Pieces from the last to the first.
+template <class F>
+__device__ __forceinline__ void scale_all(const ClipTable &t, F by) {
     const uint32_t pieces = t.first[t.n];
     int at = tensor_of(t, pieces - 1 - blockIdx.x);
     for (uint32_t back = blockIdx.x; back < pieces; back += gridDim.x) {
         const uint32_t p = pieces - 1 - back;
         while (t.first[at] > p) --at;
-        if (by == 1.0f && t.grad[at] == t.out[at]) continue;
+        if (by == F(1) && t.grad[at] == t.out[at]) continue;
         const int64_t size = t.size[at] & ((int64_t(1) << 56) - 1);
         const int type = int(t.size[at] >> 56);
         const int64_t q = p - t.first[at];
@@ -191,6 +191,20 @@ clip_kernel(ClipTable t, double max_norm, const float *__restrict__ norm_in, con
         else if (type == DT_BF16) piece_scale<__bf16>(by, t.grad[at], t.out[at], q * (kPiece / 2), size);
         else piece_scale<float>(by, t.grad[at], t.out[at], q * (kPiece / 4), size);
     }
+}
+
+// The factor is rounded to fp32 once, but below the normal fp32 values (norms near and past fp32's largest),
+// where that would cost its digits, stays fp64.
+__global__ void __launch_bounds__(kThreads)
+clip_kernel(ClipTable t, double max_norm, const float *__restrict__ norm_in, const double *__restrict__ part, int slots,
+            float *__restrict__ norm) {
+    __shared__ double red[kThreads / 64];
+    const double n = norm_in ? double(norm_in[0]) : sqrt(sum_of<kThreads>(part, slots, red));
+    if (norm && blockIdx.x == 0 && threadIdx.x == 0) norm[0] = float(n);
+    // (an infinite norm: 0, whatever max_norm is; a NaN stays one)
+    const double c = n == double(INFINITY) ? 0.0 : max_norm / (n + kEps);
+    if (c > 0.0 && c < double(FLT_MIN)) scale_all(t, c);
+    else scale_all(t, c > 1.0 ? 1.0f : float(c));
 }
 
 int64_t pieces_of(const GradList &l, int i) {

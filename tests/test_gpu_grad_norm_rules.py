@@ -1,10 +1,54 @@
-"""What the gradient norm and clipping promise beyond ordinary values: one norm from both calls, long lists."""
+"""What the gradient norm and clipping promise beyond ordinary values: a norm past fp32, one norm from
+both calls, long lists."""
 
 import pytest
 
 pytestmark = pytest.mark.gpu
 
 INF = float("inf")
+
+
+@pytest.mark.parametrize("dt", ["float32", "bfloat16"])
+@pytest.mark.parametrize("most", [1.0, 1e-6, 1e30, INF])
+def test_a_norm_past_fp32(lib, gpu, dt, most):
+    """The call that sums the squares clips by its 64-bit norm, also where norm[0] is infinite; an infinite
+    norm that is given makes the factor 0.  Roundings: the product to fp32, then to the type."""
+    import torch
+    t = torch.full((5000,), 3e38).to(getattr(torch, dt))
+    small = torch.tensor([1.0, -2.0]).to(t.dtype)
+    want = float(t[0].double()) * 5000 ** 0.5
+    by = min(1.0, most / (want + 1e-6))
+    g = [t.cuda(), small.cuda()]
+    norm, outs = lib.clip_grad_norm(g, most)
+    told = lib.grad_norm(g)
+    assert norm.item() == INF and told.item() == INF
+    fi = torch.finfo(t.dtype)
+    for a, have in zip((t, small), outs):
+        exact = a.double() * by
+        bound = exact.abs() * ((fi.eps / 2 if dt == "bfloat16" else 0) + 2.0 ** -23 + 1e-11)
+        bound = bound + fi.smallest_normal * fi.eps
+        assert bool(((have.cpu().double() - exact).abs() <= bound).all())
+    for have in lib.clip_grad_norm(g, most, norm=told)[1]:
+        assert not bool(have.any()) and not bool(have.isnan().any())
+    g[0][17] = INF  # (infinite times zero)
+    norm, (a, b) = lib.clip_grad_norm(g, most)
+    assert norm.item() == INF and a.isnan().nonzero().flatten().tolist() == [17]
+    assert not bool(a.nan_to_num().any()) and not bool(b.any())
+
+
+@pytest.mark.parametrize("top,most", [(3e38, 1.0), (3e38, 1e-3), (1e38, 1e-6), (1e30, 1e-12)])
+def test_factors_below_the_normal_fp32_values(lib, gpu, top, most):
+    """The factor keeps its digits below 2^-126: roundings of the factor (2^-24 where fp32 holds it) and of the
+    product (2^-24, or half of the smallest value)."""
+    import torch
+    t = torch.tensor([top, -top / 4, 1.0])
+    want = float(t.double().norm())
+    assert want < 3.4e38
+    norm, (out,) = lib.clip_grad_norm([t.cuda()], most)
+    by = most / (want + 1e-6)
+    bound = t.double().abs() * by * (2.0 ** -23 + 1e-11) + 2.0 ** -150
+    assert abs(norm.item() - want) <= 2.0 ** -24 * want * (1 + 1e-9)
+    assert bool(((out.cpu().double() - t.double() * by).abs() <= bound).all())
 
 
 def test_both_calls_add_in_one_order(lib, gpu):
