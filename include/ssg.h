@@ -513,7 +513,9 @@ int64_t linear_cross_entropy_workspace_bytes(int32_t dtype, int64_t M, int64_t V
  * M rows belong to expert e; an expert may have none.  The device cannot refuse
  * a call, so offsets outside 0 .. M are clamped to it, and one below an earlier
  * offset counts as the largest before it.  Output rows of no expert (before
- * offsets[0], behind offsets[experts]) are left as they are.  No output overlaps an input. */
+ * offsets[0], behind offsets[experts]) are left as they are.  An output or a
+ * workspace that overlaps an input or another output is refused (rows of one
+ * buffer beside each other, as column slices are, do not overlap). */
 
 /* out[m] = w[e] . x[m] for the expert e of row m: x [M][K], w [experts][N][K]
  * contiguous, out [M][N], dtype SSG_DT_F16 or SSG_DT_BF16, fp32 sums, one

@@ -3,7 +3,8 @@ gradients, microscaled 4-bit (MXFP4) operands, the global gradient norm and clip
 
 Same manner as ``_tune``: torch device tensors in and out, one library call on torch's
 current stream, ``SsgError`` on a nonzero status, no fallback; rows may be strided, the
-gradients are calls of their own and results carry no history.
+gradients are calls of their own and results carry no history.  An output or a workspace
+that overlaps an input is refused.
 """
 
 from __future__ import annotations

@@ -4,7 +4,9 @@
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
+#include <initializer_list>
 #include <new>
+#include <numeric>
 #include <vector>
 
 #include "device.h"
@@ -122,6 +124,50 @@ int check_mx_gemm(const char *fn, const uint8_t *w, const uint8_t *w_scales, con
     return check_packed(fn, "w", w, w_scales);
 }
 
+// Memory that a call reads or writes: rows of `width` bytes, `step` apart (a run of memory: one row).
+struct Area {
+    const char *name;
+    const void *p;
+    int64_t rows, step, width;
+};
+Area run(const char *name, const void *p, int64_t bytes) { return {name, p, 1, bytes, bytes}; }
+Area matrix(const char *name, const void *p, int64_t rows, int64_t ld, int64_t n, int bytes) {
+    return {name, p, rows, ld * bytes, n * bytes};
+}
+
+// Rows of one buffer beside each other (column slices, every other row) share no byte: they lie apart by
+// their place in the common divisor of both steps.
+bool meet(const Area &a, const Area &b) {
+    if (!a.p || !b.p || a.rows < 1 || b.rows < 1 || a.width < 1 || b.width < 1) return false;
+    const uintptr_t pa = reinterpret_cast<uintptr_t>(a.p), pb = reinterpret_cast<uintptr_t>(b.p);
+    if (pa + uintptr_t((a.rows - 1) * a.step + a.width) <= pb || pb + uintptr_t((b.rows - 1) * b.step + b.width) <= pa)
+        return false;
+    if (a.rows == 1 && b.rows == 1) return true;
+    const int64_t g = a.rows == 1 ? b.step : b.rows == 1 ? a.step : std::gcd(a.step, b.step);
+    const int64_t off = pb >= pa ? int64_t((pb - pa) % uintptr_t(g)) : g - 1 - int64_t((pa - pb - 1) % uintptr_t(g));
+    return off < a.width || off + b.width > g;
+}
+
+// Nothing that is written may share a byte with anything else of the call.
+int check_apart(const char *fn, std::initializer_list<Area> written, std::initializer_list<Area> read) {
+    for (const Area *w = written.begin(); w != written.end(); ++w) {
+        for (const Area *o = w + 1; o != written.end(); ++o)
+            if (meet(*w, *o)) return ssg::fail(SSG_EINVAL, "%s: %s overlaps %s", fn, w->name, o->name);
+        for (const Area &r : read)
+            if (meet(*w, r)) return ssg::fail(SSG_EINVAL, "%s: %s overlaps %s", fn, w->name, r.name);
+    }
+    return SSG_OK;
+}
+Area offsets_area(const int32_t *offsets, int32_t experts) {
+    return run("offsets", offsets, 4 * (int64_t(experts) + 1));
+}
+Area codes_area(const char *name, const uint8_t *p, int64_t rows, int64_t K) {
+    return run(name, p, rows * (ssg::mxfp4_padded(K) / 2));
+}
+Area scales_area(const char *name, const uint8_t *p, int64_t rows, int64_t K) {
+    return run(name, p, rows * (ssg::mxfp4_padded(K) / 32));
+}
+
 }  // namespace
 
 // ------------------------------------------------------------ grouped products
@@ -132,7 +178,11 @@ SSG_API int grouped_gemm(int32_t dtype, const void *x, int64_t ldx, const void *
     if (rc) return rc;
     if (M == 0) return ok();
     if ((rc = check_rows(fn, "x", x, ldx, K)) || (rc = check_rows(fn, "w", w, K, K)) ||
-        (rc = check_rows(fn, "out", out, ldo, N)) || (rc = check_device()))
+        (rc = check_rows(fn, "out", out, ldo, N)) ||
+        (rc = check_apart(fn, {matrix("out", out, M, ldo, N, 2)},
+                          {matrix("x", x, M, ldx, K, 2), run("w", w, experts * N * K * 2),
+                           offsets_area(offsets, experts)})) ||
+        (rc = check_device()))
         return rc;
     ssg::Grouped a{};
     a.dtype = dtype, a.x = x, a.w = w, a.offsets = offsets, a.experts = experts, a.ldx = ldx, a.out = out, a.ldo = ldo;
@@ -160,7 +210,12 @@ SSG_API int grouped_gemm_backward(int32_t dtype, const void *dy, int64_t lddy, c
                (rc = check_ws(fn, ws, ws_bytes, grouped_gemm_backward_workspace_bytes(experts, M, N, K)))))
         return rc;
     if (!dw && (!dx || M == 0)) return ok();
-    if ((rc = check_device())) return rc;
+    const int64_t pool = experts * N * K * 2, slices = dw ? grouped_gemm_backward_workspace_bytes(experts, M, N, K) : 0;
+    if ((rc = check_apart(fn, {matrix("dx", dx, M, lddx, K, 2), run("dw", dw, pool), run("the workspace", ws, slices)},
+                          {matrix("dy", dy, M, lddy, N, 2), matrix("x", dw ? x : nullptr, M, ldx, K, 2),
+                           run("w", dx ? w : nullptr, pool), offsets_area(offsets, experts)})) ||
+        (rc = check_device()))
+        return rc;
     ssg::Grouped a{};
     a.dtype = dtype, a.x = x, a.w = w, a.dy = dy, a.offsets = offsets, a.experts = experts;
     a.ldx = ldx, a.lddy = lddy, a.dx = dx, a.lddx = lddx, a.dw = dw, a.ws = ws, a.M = M, a.N = N, a.K = K;
@@ -176,6 +231,8 @@ SSG_API int mxfp4_quantize(int32_t dtype, const void *x, int64_t ldx, uint8_t *c
     if (rc) return rc;
     if (M == 0) return ok();
     if ((rc = check_any(fn, "x", x, ldx, M, K, dtype)) || (rc = check_packed(fn, "the output", codes, scales)) ||
+        (rc = check_apart(fn, {codes_area("codes", codes, M, K), scales_area("scales", scales, M, K)},
+                          {matrix("x", x, M, ldx, K, elem_bytes(dtype))})) ||
         (rc = check_device()))
         return rc;
     return launched(ssg::launch_mxfp4_quantize(dtype, x, ldx, codes, scales, M, K, hipStream_t(stream)), fn);
@@ -189,6 +246,8 @@ SSG_API int mxfp4_dequantize(const uint8_t *codes, const uint8_t *scales, int32_
     if (rc) return rc;
     if (M == 0) return ok();
     if ((rc = check_any(fn, "out", out, ldo, M, K, dtype)) || (rc = check_packed(fn, "the input", codes, scales)) ||
+        (rc = check_apart(fn, {matrix("out", out, M, ldo, K, elem_bytes(dtype))},
+                          {codes_area("codes", codes, M, K), scales_area("scales", scales, M, K)})) ||
         (rc = check_device()))
         return rc;
     return launched(ssg::launch_mxfp4_dequantize(dtype, codes, scales, out, ldo, M, K, hipStream_t(stream)), fn);
@@ -202,7 +261,13 @@ SSG_API int mxfp4_gemm(const uint8_t *a, const uint8_t *a_scales, const uint8_t 
     int rc = check_mx_gemm(fn, w, w_scales, offsets, experts, dtype, out, ldo, M, N, K);
     if (rc) return rc;
     if (M == 0) return ok();
-    if ((rc = check_packed(fn, "a", a, a_scales)) || (rc = check_device())) return rc;
+    if ((rc = check_packed(fn, "a", a, a_scales)) ||
+        (rc = check_apart(fn, {matrix("out", out, M, ldo, N, elem_bytes(dtype))},
+                          {codes_area("a", a, M, K), scales_area("a's scales", a_scales, M, K),
+                           codes_area("w", w, experts * N, K), scales_area("w's scales", w_scales, experts * N, K),
+                           offsets_area(offsets, experts)})) ||
+        (rc = check_device()))
+        return rc;
     const ssg::Mxfp4Gemm g{a, a_scales, w, w_scales, offsets, experts, dtype, out, ldo, M, N, K};
     return launched(ssg::launch_mxfp4_gemm(g, hipStream_t(stream)), fn);
 }
@@ -222,7 +287,11 @@ SSG_API int mxfp4_linear(int32_t dtype, const void *x, int64_t ldx, const uint8_
     if (rc) return rc;
     if (M == 0) return ok();
     if ((rc = check_any(fn, "x", x, ldx, M, K, dtype)) ||
-        (rc = check_ws(fn, ws, ws_bytes, mxfp4_linear_workspace_bytes(M, K))) || (rc = check_device()))
+        (rc = check_ws(fn, ws, ws_bytes, mxfp4_linear_workspace_bytes(M, K))) ||
+        (rc = check_apart(fn, {matrix("out", out, M, ldo, N, 2), run("the workspace", ws, mxfp4_linear_workspace_bytes(M, K))},
+                          {matrix("x", x, M, ldx, K, 2), codes_area("w", w, experts * N, K),
+                           scales_area("w's scales", w_scales, experts * N, K), offsets_area(offsets, experts)})) ||
+        (rc = check_device()))
         return rc;
     if (ssg::mxfp4_few_kind(M, offsets ? experts : 0, N, K) >= 0) {
         const ssg::Mxfp4Gemm g{static_cast<const uint8_t *>(x), nullptr, w, w_scales, offsets, experts, dtype, out, ldo, M,
