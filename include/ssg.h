@@ -569,6 +569,13 @@ int mxfp4_linear(int32_t dtype, const void *x, int64_t ldx, const uint8_t *w, co
                  void *ws, int64_t ws_bytes, void *stream);
 int64_t mxfp4_linear_workspace_bytes(int64_t M, int64_t K);
 
+/* Which kernel a product runs on, as an entry of the library's table of tiles for
+ * that product (a host query, for tests and tuning).  product 0: grouped_gemm; 1 and
+ * 2: dx, and dw (+ 256 times its splits), in launches of their own; 3: dx and dw in
+ * one launch, -1 where they are not; 4: mxfp4_gemm and mxfp4_linear (experts 0: without
+ * offsets), 16 + entry for the kernels of few rows.  -2: no such product. */
+int32_t ssg_expert_tile(int32_t product, int32_t experts, int64_t M, int64_t N, int64_t K);
+
 /* norm[0] = sqrt of the sum of squares of n tensors' elements (fp64 sums), rounded to fp32.
  * grads, sizes (elements, 0 allowed) and dtypes are host arrays of n entries,
  * read during the call; tensors are contiguous and element-aligned, up to 2^20

@@ -76,6 +76,7 @@ from ._tune import (  # noqa: F401
 )
 from ._expert import (  # noqa: F401
     clip_grad_norm,
+    expert_tile,
     grad_norm,
     grouped_gemm,
     grouped_gemm_backward,

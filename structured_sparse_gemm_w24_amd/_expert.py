@@ -73,6 +73,12 @@ def grouped_gemm_backward(dy, x, w, offsets, out=None, dw_out=None, x_grad=True,
     return dx, dw
 
 
+def expert_tile(product, experts, m, n, k):
+    """The entry of the library's table of tiles that a product of expert layers runs on (ssg_expert_tile in
+    ssg.h: 0 grouped_gemm, 1 dx, 2 dw, 3 dx and dw in one launch, 4 the 4-bit products)."""
+    return int(load().ssg_expert_tile(product, experts, m, n, k))
+
+
 # ------------------------------------------------------------ microscaled 4 bit
 def _padded(k):
     return -(-k // PAD) * PAD

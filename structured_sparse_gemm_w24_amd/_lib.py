@@ -88,6 +88,7 @@ SIGNATURES = {
     "grouped_gemm": [_I32, _P, _I64, _P, _P, _I32, _P, _I64, _I64, _I64, _I64, _P],
     "grouped_gemm_backward": [_I32, _P, _I64, _P, _I64, _P, _P, _I32, _P, _I64, _P, _I64, _I64, _I64, _P, _I64, _P],
     "grouped_gemm_backward_workspace_bytes": [_I32, _I64, _I64, _I64],
+    "ssg_expert_tile": [_I32, _I32, _I64, _I64, _I64],
     "mxfp4_quantize": [_I32, _P, _I64, _P, _P, _I64, _I64, _P],
     "mxfp4_dequantize": [_P, _P, _I32, _P, _I64, _I64, _I64, _P],
     "mxfp4_gemm": [_P, _P, _P, _P, _P, _I32, _I32, _P, _I64, _I64, _I64, _I64, _P],

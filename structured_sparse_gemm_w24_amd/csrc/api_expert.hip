@@ -222,6 +222,14 @@ SSG_API int grouped_gemm_backward(int32_t dtype, const void *dy, int64_t lddy, c
     return launched(ssg::launch_grouped_bwd(a, hipStream_t(stream)), fn);
 }
 
+SSG_API int32_t ssg_expert_tile(int32_t product, int32_t experts, int64_t M, int64_t N, int64_t K) {
+    if (product < 0 || product > 4 || M < 1 || experts < (product == 4 ? 0 : 1) || experts > 65535) return -2;
+    if (product < 4) return grouped_dims(M, N, K) ? ssg::grouped_tile(product, M, experts, N, K) : -2;
+    if (!mx_dims(M, K) || N < 1 || N >= kSide) return -2;
+    const int few = ssg::mxfp4_few_kind(M, experts, N, K);
+    return few >= 0 ? 16 + few : ssg::mxfp4_tile(M, experts, N, K);
+}
+
 // ------------------------------------------------------------ microscaled 4 bit
 SSG_API int mxfp4_quantize(int32_t dtype, const void *x, int64_t ldx, uint8_t *codes, uint8_t *scales, int64_t M,
                            int64_t K, void *stream) {

@@ -365,6 +365,13 @@ int64_t grouped_blocks(int64_t M, int64_t experts, int64_t N, int64_t K, bool ba
     return most;
 }
 
+int grouped_tile(int product, int64_t M, int64_t experts, int64_t N, int64_t K) {
+    if (product == 0) return rows_tile<false>(M, experts, N, K);
+    if (product == 1) return rows_tile<true>(M, experts, K, N);
+    const WeightsPlan pl = weights_plan(M, experts, N, K);
+    return product == 2 ? pl.tile + 256 * pl.splits : both_tile(pl, M, experts, N, K);
+}
+
 int64_t grouped_slices_bytes(int64_t M, int64_t experts, int64_t N, int64_t K) {
     const int splits = weights_plan(M, experts, N, K).splits;
     return splits > 1 ? splits * experts * N * K * 4 : 0;

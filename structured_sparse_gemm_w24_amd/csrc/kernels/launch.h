@@ -181,6 +181,9 @@ hipError_t launch_grouped_bwd(const Grouped &a, hipStream_t st);
 int64_t grouped_slices_bytes(int64_t M, int64_t experts, int64_t N, int64_t K);
 // workgroups of the forward launch, or of the largest of the backward ones
 int64_t grouped_blocks(int64_t M, int64_t experts, int64_t N, int64_t K, bool backward);
+// Entry of the product's table of tiles: 0 forward, 1 dx and 2 dw in launches of their own (dw: + 256 splits),
+// 3 both in one (-1: they are not).
+int grouped_tile(int product, int64_t M, int64_t experts, int64_t N, int64_t K);
 
 // Microscaled 4-bit floating point (formulas in mxfp4.hip).  Packed rows hold kp
 // values, a multiple of 128: kp / 2 code bytes and kp / 32 scale bytes.
@@ -201,6 +204,8 @@ hipError_t launch_mxfp4_gemm(const Mxfp4Gemm &g, hipStream_t st);
 // ldx, or (x_dtype -1) packed.  The kind says which tile, below 0: the product is not for it.
 hipError_t launch_mxfp4_few(const Mxfp4Gemm &g, int x_dtype, int64_t ldx, hipStream_t st);
 int mxfp4_few_kind(int64_t M, int64_t experts, int64_t N, int64_t K);
+// Entry of the table of tiles where mxfp4_few_kind() is below 0.
+int mxfp4_tile(int64_t M, int64_t experts, int64_t N, int64_t K);
 // workgroups of a product (experts 0: of all rows with one weight)
 int64_t mxfp4_blocks(int64_t M, int64_t experts, int64_t N, int64_t K);
 inline int64_t mxfp4_padded(int64_t K) { return (K + 127) / 128 * 128; }

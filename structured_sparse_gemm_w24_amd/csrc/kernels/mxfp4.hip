@@ -269,6 +269,8 @@ int mxfp4_few_kind(int64_t M, int64_t experts, int64_t N, int64_t K) {
     return best;
 }
 
+int mxfp4_tile(int64_t M, int64_t experts, int64_t N, int64_t K) { return mx_tile(M, experts, N, K); }
+
 int64_t mxfp4_blocks(int64_t M, int64_t experts, int64_t N, int64_t K) {
     const int few = mxfp4_few_kind(M, experts, N, K);
     const TileCost &t = kMxTiles[mx_tile(M, experts, N, K)];
