@@ -193,8 +193,9 @@ template <class T, class O, bool GROUPED, int NB, int NW>
 hipError_t few_cfg(const Few &p, hipStream_t st) {
     const int64_t tiles_n = (p.N + 32 * NB - 1) / (32 * NB);
     const int64_t blocks = GROUPED ? group_tiles(p.M, p.groups, 32, tiles_n) : (p.M + 31) / 32 * tiles_n;
-    auto k = p.K % 8 == 0 ? few_rows_kernel<T, O, GROUPED, NB, NW, false> : few_rows_kernel<T, O, GROUPED, NB, NW, true>;
-    if constexpr (sizeof(T) == 1) k = few_rows_kernel<T, O, GROUPED, NB, NW, false>;
+    auto k = few_rows_kernel<T, O, GROUPED, NB, NW, false>;
+    if constexpr (sizeof(T) > 1)
+        if (p.K % 8) k = few_rows_kernel<T, O, GROUPED, NB, NW, true>;
     hipLaunchKernelGGL(k, dim3(unsigned(blocks)), dim3(NW * 64), 0, st, p);
     return hipGetLastError();
 }

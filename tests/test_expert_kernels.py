@@ -45,3 +45,17 @@ def test_loads_that_may_pass_the_end_have_their_whole_offset_checked(tmp_path):
         assert moved <= {first} and {r for r, _ in loads} > {first}, name
         checked += bool(moved)
     assert checked == 2  # fp16 and bf16 of the tile that moves A's stage to the scalar offset
+
+
+def test_kernels_of_few_rows(tmp_path):
+    """Every compiled kernel is one that a call reaches (packed operands are whole pieces, K is their padded one),
+    none spills, none has packed fp32 arithmetic."""
+    asm = _assembly("mxfp4_few.hip", tmp_path)
+    names = [name for name, _ in _bodies(asm)]
+    packed = [n for n in names if "few_rows_kernelIh" in n]
+    assert len(packed) == 3 * 2 * 3  # output types, grouped or not, tiles
+    assert len(names) - len(packed) == 2 * 2 * 3 * 2  # and whole rows or not
+    for d in re.findall(r"^\s*\.amdhsa_kernel (\S+)\n(.*?)\.end_amdhsa_kernel", asm, re.M | re.S):
+        value = lambda key: int(re.search(r"\.amdhsa_" + key + r"\s+(\d+)", d[1]).group(1))
+        assert value("private_segment_fixed_size") == 0 and value("group_segment_fixed_size") <= 160 * 1024, d[0]
+    assert not re.search(r"^\s*v_pk_(fma|mul|add)_f32", asm, re.M)
