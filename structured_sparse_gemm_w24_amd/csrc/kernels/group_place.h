@@ -149,12 +149,12 @@ struct GroupRowsGuess {
     }
 };
 
-// The cheapest of N tiles: tiles(bm, bn) says how many a launch has.
+// The cheapest of N tiles (or of the first `some`): tiles(bm, bn) says how many a launch has.
 template <int N, class F>
-int cheapest(const TileCost (&c)[N], double stages, F tiles) {
+int cheapest(const TileCost (&c)[N], double stages, F tiles, int some = N) {
     int best = 0;
     float least = 0.0f;
-    for (int i = 0; i < N; ++i) {
+    for (int i = 0; i < some; ++i) {
         const float us = c[i].us(tiles(c[i].bm, c[i].bn), stages);
         if (i == 0 || us < least) best = i, least = us;
     }

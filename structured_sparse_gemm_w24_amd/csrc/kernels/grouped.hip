@@ -173,7 +173,8 @@ int rows_tile(int64_t M, int64_t experts, int64_t N, int64_t K) {
 }
 // dw's tile and splits: the least of the tiles' cost, with each group's stages in up to 32 shares of
 // four at least, and for more than one share the second launch and the slices' way through memory
-// (16384 rows of one expert, 1024 x 1024: 113 us in one share; below 256 MiB of slices).
+// (16384 rows of one expert, 1024 x 1024: 113 us in one share; below 256 MiB of slices).  Shares are for few
+// tiles: the largest is never the cheapest with more than one (of 5 million random calls), and not compiled for it.
 struct WeightsPlan {
     int tile, splits;
 };
@@ -187,7 +188,7 @@ WeightsPlan weights_plan(int64_t M, int64_t experts, int64_t N, int64_t K) {
         auto count = [&](int bm, int bn) {
             return double(p) * double(experts) * double((N + bm - 1) / bm) * double((K + bn - 1) / bn);
         };
-        const int t = cheapest(kDwTiles, stages / p, count);
+        const int t = cheapest(kDwTiles, stages / p, count, p > 1 ? 5 : 6);
         float us = kDwTiles[t].us(count(kDwTiles[t].bm, kDwTiles[t].bn), stages / p);
         if (p > 1) us += 4.0f + float(slice * (2 * p + 0.5) / 5.0e6);
         if (p == 1 || us < least) best = {t, p}, least = us;
@@ -277,8 +278,10 @@ hipError_t weights_any(const Grouped &a, const WeightsPlan &pl, hipStream_t st) 
         case 2: return weights_cfg<KIND, Cfg<2, 2, 2, 2, 2, 8, true, false>, SPLIT>(a, pl.splits, st);
         case 3: return weights_cfg<KIND, Cfg128x128P, SPLIT>(a, pl.splits, st);
         case 4: return weights_cfg<KIND, Cfg256x128P, SPLIT>(a, pl.splits, st);
-        default: return weights_cfg<KIND, CfgBigDense<true>, SPLIT>(a, pl.splits, st);
+        default: break;
     }
+    if constexpr (SPLIT) return hipErrorInvalidValue;
+    else return weights_cfg<KIND, CfgBigDense<true>, false>(a, 1, st);
 }
 
 template <int KIND>
