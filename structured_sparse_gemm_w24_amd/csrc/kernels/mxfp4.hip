@@ -244,10 +244,13 @@ constexpr FewCost kFewTiles[2][3] = {
     {{32, 4, 2.8f, 2.20f, 0.35f, 0.70f}, {32, 8, 2.4f, 2.60f, 0.41f, 1.35f}, {64, 4, 2.65f, 2.75f, 0.48f, 0.80f}}};
 
 // The choice between one launch and two (quantisation and product: 1.76 times the product's estimate less
-// 4.6) by least estimate, fitted as TileCost's: over 220 random calls of 1 to 362 rows, in graphs, the
-// choice takes 1.02 times the best of all four, two launches 1.29.  (Here with 1 us more for the second
-// launch, which costs the host 4: 32 rows of 32 experts, 2048 x 1024, 9.4 us a call and 12.7.)  A packed operand goes the same way, so that the
-// product of quantised rows is the same bit for bit.  (Past the fit, and with more than 2000 units of full
+// 4.6) by least estimate, fitted as TileCost's to launches in graphs.  Up to 16 units, where the estimates of
+// both are close, two count 1 us more: the second launch costs the host 3 us (32 rows of 32 experts, 2048 x 1024,
+// a call 13.1 us, in one launch 10.5; in a graph 10.9 and 10.5).  Past that one launch may be far off its
+// estimate (157 x 288 x 6100 27.3 us, two 13.3).  Over 224 random calls of 1 to 362 rows the choice takes in
+// graphs 1.019 times the best of all four, called 1.022 times; without the microsecond 1.021 and 1.032, with it
+// for any K 1.028 and 1.030, always two launches 1.33 and 1.26.  A packed operand goes the same way, so that
+// the product of quantised rows is the same bit for bit.  (Past the fit, and with more than 2000 units of full
 // tiles, always two: 334 rows of 22 experts, 7040 x 500, 16.2 us and 29.5.)
 int mxfp4_few_kind(int64_t M, int64_t experts, int64_t N, int64_t K) {
     if (M > 512) return -1;
@@ -257,7 +260,7 @@ int mxfp4_few_kind(int64_t M, int64_t experts, int64_t N, int64_t K) {
     auto columns = [&](int bn) { return double((N + bn - 1) / bn); };
     if (full && tiles * columns(32) * units > 2000.0) return -1;
     const TileCost &two = kMxTiles[mx_tile(M, experts, N, K)];
-    double least = 1.76 * two.us(guess.tiles(two.bm) * columns(two.bn), units) - 3.6;
+    double least = 1.76 * two.us(guess.tiles(two.bm) * columns(two.bn), units) - (units <= 16.0 ? 3.6 : 4.6);
     int best = -1;
     for (int i = 0; i < 3; ++i) {
         const FewCost &c = kFewTiles[full][i];

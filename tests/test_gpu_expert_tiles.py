@@ -57,6 +57,12 @@ def test_shapes_run_on_their_tiles_and_reach_all(lib):
         assert lib.expert_tile(*bad) == -2
 
 
+@pytest.mark.parametrize("m,n,k", [(157, 288, 6100), (193, 120, 5304), (12, 352, 7724)])
+def test_long_sums_are_not_taken_by_the_few_rows_kernels_for_the_host_s_sake(lib, m, n, k):
+    """One launch takes up to twice the time of two on the device there (27.3 us and 13.3 for the first)."""
+    assert 0 <= lib.expert_tile(MX, 0, m, n, k) < 16
+
+
 def _dt(name):
     import torch
     return {"f16": torch.float16, "bf16": torch.bfloat16, "f32": torch.float32}[name]
