@@ -132,7 +132,7 @@ struct Area {
 };
 Area run(const char *name, const void *p, int64_t bytes) { return {name, p, 1, bytes, bytes}; }
 Area matrix(const char *name, const void *p, int64_t rows, int64_t ld, int64_t n, int bytes) {
-    return {name, p, rows, ld * bytes, n * bytes};
+    return {name, p, rows, rows > 1 ? ld * bytes : n * bytes, n * bytes};  // (one row: of any stride)
 }
 
 // Rows of one buffer beside each other (column slices, every other row) share no byte: they lie apart by

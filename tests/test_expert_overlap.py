@@ -24,8 +24,8 @@ def _bwd(r, dy=1 << 20, lddy=N, x=2 << 20, w=3 << 20, offsets=4 << 20, dx=5 << 2
                                    _p(ws), 1 << 29, None)
 
 
-def _quant(r, x=1 << 20, ldx=100, codes=2 << 20, scales=3 << 20):
-    return r.mxfp4_quantize(F16, _p(x), ldx, _p(codes), _p(scales), M, 100, None)
+def _quant(r, x=1 << 20, ldx=100, codes=2 << 20, scales=3 << 20, dtype=F16, m=M):
+    return r.mxfp4_quantize(dtype, _p(x), ldx, _p(codes), _p(scales), m, 100, None)
 
 
 def _dequant(r, codes=1 << 20, scales=2 << 20, out=3 << 20, ldo=100):
@@ -92,6 +92,7 @@ APART = [
     lambda r: _fwd(r, ldo=128, offsets=4 * MB + 128),              # behind a row, before the next
     lambda r: _bwd(r, dw=None, x=5 * MB),                          # (x is not read)
     lambda r: _bwd(r, dx=None, w=6 * MB),                          # (nor w)
+    lambda r: _quant(r, dtype=F32, m=1, ldx=1 << 61),              # one row, of any stride
 ]
 
 
