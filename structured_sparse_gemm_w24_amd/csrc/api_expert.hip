@@ -375,6 +375,20 @@ int check_overlap(const char *fn, int32_t n, const void *const *grads, void *con
     return SSG_OK;
 }
 
+// The norm that is written and the workspace lie apart from each other and from every tensor.
+int check_norm_apart(const char *fn, int32_t n, const void *const *grads, const void *const *outs, const int64_t *sizes,
+                     const int32_t *dtypes, const float *norm, const void *ws) {
+    const Area of_norm = run("norm", norm, sizeof(float)), of_ws = run("the workspace", ws, ssg::grad_norm_slots(n) * 8);
+    if (int rc = check_apart(fn, {of_norm, of_ws}, {})) return rc;
+    for (int i = 0; i < n; ++i) {
+        const int64_t bytes = sizes[i] * elem_bytes(dtypes[i]);
+        for (const Area &a : {run("a tensor", grads[i], bytes), run("an output", outs ? outs[i] : nullptr, bytes)})
+            for (const Area &w : {of_norm, of_ws})
+                if (meet(w, a)) return ssg::fail(SSG_EINVAL, "%s: %s overlaps %s (entry %d)", fn, w.name, a.name, i);
+    }
+    return SSG_OK;
+}
+
 }  // namespace
 
 SSG_API int64_t grad_norm_workspace_bytes(int32_t n) { return n > 0 ? ssg::grad_norm_slots(n) * 8 : 0; }
@@ -385,7 +399,9 @@ SSG_API int grad_norm(int32_t n, const void *const *grads, const int64_t *sizes,
     int rc = check_list(fn, n, grads, sizes, dtypes);
     if (rc) return rc;
     if (!norm || !aligned_to(norm, 4)) return ssg::fail(SSG_EINVAL, "%s: norm null or misaligned", fn);
-    if ((rc = check_ws(fn, ws, ws_bytes, grad_norm_workspace_bytes(n))) || (rc = check_device())) return rc;
+    if ((rc = check_ws(fn, ws, ws_bytes, grad_norm_workspace_bytes(n))) ||
+        (rc = check_norm_apart(fn, n, grads, nullptr, sizes, dtypes, norm, n > 0 ? ws : nullptr)) || (rc = check_device()))
+        return rc;
     const ssg::GradList l{n, grads, nullptr, sizes, dtypes};
     return launched(ssg::launch_grad_norm(l, static_cast<double *>(ws), norm, hipStream_t(stream)), fn);
 }
@@ -401,7 +417,9 @@ SSG_API int clip_grad_norm(int32_t n, const void *const *grads, void *const *out
     if ((rc = check_overlap(fn, n, grads, outs, sizes, dtypes, norm_in))) return rc;
     if (!norm_in) {
         if (!norm || !aligned_to(norm, 4)) return ssg::fail(SSG_EINVAL, "%s: norm null or misaligned", fn);
-        if ((rc = check_ws(fn, ws, ws_bytes, grad_norm_workspace_bytes(n)))) return rc;
+        if ((rc = check_ws(fn, ws, ws_bytes, grad_norm_workspace_bytes(n))) ||
+            (rc = check_norm_apart(fn, n, grads, outs, sizes, dtypes, norm, n > 0 ? ws : nullptr)))
+            return rc;
     } else if (!aligned_to(norm_in, 4)) {
         return ssg::fail(SSG_EINVAL, "%s: norm_in misaligned", fn);
     }

@@ -41,6 +41,18 @@ def _linear(r, x=1 << 20, ldx=100, w=2 << 20, sw=3 << 20, offsets=4 << 20, out=5
                           None)
 
 
+def _norm(r, grads=(1 << 20,), norm=2 << 20, ws=3 << 20):
+    n = len(grads)
+    return r.grad_norm(n, (ct.c_void_p * n)(*grads), (ct.c_int64 * n)(*[8] * n), (ct.c_int32 * n)(*[F32] * n),
+                       _p(norm), _p(ws), 1 << 20, None)
+
+
+def _clip(r, grads=(1 << 20,), outs=(4 << 20,), norm=2 << 20, ws=3 << 20, norm_in=None):
+    n = len(grads)
+    return r.clip_grad_norm(n, (ct.c_void_p * n)(*grads), (ct.c_void_p * n)(*outs), (ct.c_int64 * n)(*[8] * n),
+                            (ct.c_int32 * n)(*[F32] * n), 1.0, _p(norm_in), _p(norm), _p(ws), 1 << 20, None)
+
+
 MB = 1 << 20
 ROW = 2 * N
 REFUSED = [
@@ -70,6 +82,12 @@ REFUSED = [
     (lambda r: _linear(r, out=MB + 2), "out overlaps x"),
     (lambda r: _linear(r, ws=MB), "workspace overlaps x"),
     (lambda r: _linear(r, ws=5 * MB), "out overlaps the workspace"),
+    (lambda r: _norm(r, norm=MB + 28), "norm overlaps a tensor (entry 0)"),
+    (lambda r: _norm(r, grads=(MB, 3 * MB + 64)), "workspace overlaps a tensor (entry 1)"),
+    (lambda r: _norm(r, norm=3 * MB + 8), "norm overlaps the workspace"),
+    (lambda r: _clip(r, norm=4 * MB), "norm overlaps an output"),
+    (lambda r: _clip(r, norm=MB + 4), "norm overlaps a tensor"),
+    (lambda r: _clip(r, ws=4 * MB - 32), "workspace overlaps an output"),
 ]
 
 
@@ -93,6 +111,9 @@ APART = [
     lambda r: _bwd(r, dw=None, x=5 * MB),                          # (x is not read)
     lambda r: _bwd(r, dx=None, w=6 * MB),                          # (nor w)
     lambda r: _quant(r, dtype=F32, m=1, ldx=1 << 61),              # one row, of any stride
+    lambda r: _norm(r, norm=MB + 32),
+    lambda r: _clip(r, norm=MB + 32),
+    lambda r: _clip(r, norm=4 * MB, ws=MB, norm_in=5 * MB),        # (neither is used)
 ]
 
 
