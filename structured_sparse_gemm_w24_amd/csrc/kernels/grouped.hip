@@ -12,7 +12,8 @@
 // each group's rows are split over several workgroups, whose fp32 sums a second launch
 // adds in order.
 //
-// Measured: 16384 rows of 16 experts, 4096 x 1024, forward fp16 151 us (910 TFLOP/s), gradients bf16 315 (870);
+// Measured: 16384 rows of 16 experts, 4096 x 1024, forward fp16 151 to 162 us by card (850 to 910 TFLOP/s),
+// gradients bf16 315 (870); with all rows at one of many experts dw is slow (16384 of 64, 1024 x 1024, 374 us, even 73);
 // bound by the start and end of loops of 16 stages, the gradients by their transposing LDS reads.
 #include "elem.h"
 #include "gemm_core.h"
@@ -127,10 +128,10 @@ hipError_t launch_cfg(const void *A, const void *W, void *C, const Extra &ex, in
 
 // Tiles: with few of them the smallest, whose loads have waves of their own (a chain of K stages, each
 // waiting for memory: 2324 rows of 8 groups, 72 x 1560, 8.7 us, 64 x 64 without loader waves 10.9,
-// 64 x 128 12.9); the forward's largest keep a stage's fragments in registers (16384 rows of 16, 4096 x
-// 1024 141 us, with eight waves instead 145; 8192 of 8, 2048 x 2048, 192 x 256 77, 256 x 256 95); dx needs
-// loader waves at nearly every size, as its transposing reads keep the others busy (8192 rows of 8, 2048 x
-// 2048: 87 us on 192 x 128 with, 123 on 192 x 256 without).
+// 64 x 128 12.9); the forward's largest keep a stage's fragments in registers (side by side in a sweep of
+// tiles on one card: 16384 rows of 16, 4096 x 1024, 141 us, with eight waves instead 145; 8192 of 8, 2048 x
+// 2048, 192 x 256 77, 256 x 256 95); dx needs loader waves at nearly every size, as its transposing reads keep
+// the others busy (8192 rows of 8, 2048 x 2048: 87 us on 192 x 128 with, 123 on 192 x 256 without).
 using Cfg32x64 = Cfg<1, 2, 1, 1, 4, 8, true, false, 0, true>;
 using Cfg64x64 = Cfg<2, 2, 1, 1, 3, 8, true, false>;
 using Cfg64x64P = Cfg<2, 2, 1, 1, 4, 8, true, false, 0, true>;
